@@ -13,12 +13,20 @@ The entry points mirror include/mamba2_scan.h:
     bwd_full(h_history, h_s2, saved, d_context, W_A, W_B, W_C) -> dict(dW_*, d_h_history, d_h_s2)
     fwd_blend(...) -> (context, h_enriched, saved);  bwd_blend(...) -> dict(...)
     saved_bytes(B, K, SH2, D), workspace_bytes(B, K, SH2, D)
+
+The selective layer (include/mamba2_layer.h; module `layer`):
+    conv_fwd, conv_bwd, conv_step  -- short causal depthwise convolution with SiLU
+    ssm_fwd, ssm_bwd, ssm_step     -- selective state space scan
+    grad_norm, clip_grads          -- global gradient norm over many tensors, and clipping
 """
 from __future__ import annotations
 
 import ctypes
 import os
 import re
+
+from . import layer
+from .layer import clip_grads, conv_bwd, conv_fwd, conv_step, grad_norm, ssm_bwd, ssm_fwd, ssm_step  # noqa: F401
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libmamba2scan.so")
@@ -87,7 +95,7 @@ def lib():
                 f"{LIB_PATH} is missing: build it with `python -m bwd_mamba2_scan_amd.build` "
                 "(there is no fallback implementation)")
         handle = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in _SIGNATURES.items():
+        for name, (res, args) in (*_SIGNATURES.items(), *layer.SIGNATURES.items()):
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args

@@ -4,13 +4,16 @@
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import subprocess
 import sys
+import tempfile
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
-SRC = os.path.join(PKG_DIR, "csrc", "mamba2_scan.hip")
+CSRC = os.path.join(PKG_DIR, "csrc")
+SOURCES = ("mamba2_scan.hip", "conv.hip", "grad_clip.hip", "ssm.hip", "ssm_bwd.hip")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libmamba2scan.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
@@ -21,7 +24,6 @@ HIPCC_FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-Wall",
     # Keep the compiler from emitting packed fp32 (v_pk_*_f32) instructions.
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -35,10 +37,7 @@ def hipcc() -> str:
     return path if os.path.exists(path) else "hipcc"
 
 
-def build(verbose: bool = False) -> str:
-    """Compile the library; returns its path.  Raises on compiler failure."""
-    tmp = f"{LIB_PATH}.tmp{os.getpid()}"
-    cmd = [hipcc(), *HIPCC_FLAGS, SRC, "-o", tmp]
+def _run(cmd: list[str], verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     proc = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
@@ -46,12 +45,27 @@ def build(verbose: bool = False) -> str:
     noise = "'-packed-fp32-ops' is not a recognized feature"
     out = "\n".join(ln for ln in proc.stdout.splitlines() if noise not in ln)
     if proc.returncode != 0:
-        if os.path.exists(tmp):
-            os.unlink(tmp)
         raise RuntimeError(f"hipcc failed ({proc.returncode}):\n{out}")
     if out.strip() and verbose:
         print(out, flush=True)
-    os.replace(tmp, LIB_PATH)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile the library; returns its path.  Raises on compiler failure."""
+    with tempfile.TemporaryDirectory(prefix="mamba2scan_build_") as tmp:
+        objects = [os.path.join(tmp, src + ".o") for src in SOURCES]
+        jobs = [[hipcc(), *HIPCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+                for src, obj in zip(SOURCES, objects)]
+        with concurrent.futures.ThreadPoolExecutor(max_workers=len(jobs)) as pool:
+            for done in [pool.submit(_run, cmd, verbose) for cmd in jobs]:
+                done.result()
+        out = f"{LIB_PATH}.tmp{os.getpid()}"
+        try:
+            _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objects, "-o", out], verbose)
+            os.replace(out, LIB_PATH)
+        finally:
+            if os.path.exists(out):
+                os.unlink(out)
     return LIB_PATH
 
 

@@ -1,0 +1,444 @@
+// Selective state space scan for gfx950: the forward over prompts and the
+// single-token form.
+//
+// ssm_fwd_kernel: a work-group owns one head (or 64 of its columns), its NW
+// waves 16 columns each, and walks the tokens in steps of 64.  A wave keeps
+// its columns of the state, S [states][16], in registers in fp32 as a matrix
+// result; result order makes that register file directly the operand of
+// S^T C.  Per step:
+//   scores   W[t][s] = (C_t . B_s) 2^(c_t - c_s) d_s (s <= t): the ten 16 x 16
+//            tiles on and below the diagonal, dealt to the waves, to LDS
+//   y        2^c_t (C_t . S) + W x + D x, 64 x 16 per wave
+//   S        2^c_end S + B^T (2^(c_end - c_s) d_s x_s)
+// B, C, x of the next step are loaded while this one is computed.
+//
+// Long sequences with few heads are cut into segments that run in parallel:
+// a summary pass (ssm_summary_kernel: each segment's own contribution to
+// the state), the carry across segments (ssm_carry_kernel), and the forward from
+// the states so found.
+#include "ssm_common.h"
+
+namespace {
+
+using namespace ssm;
+
+// Tile i of the ten with s <= t: row tile (t) and column tile (s).
+__device__ __forceinline__ void lower_tile(int i, int* ti, int* si) {
+  *ti = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3;
+  *si = i - (*ti * (*ti + 1)) / 2;
+}
+
+template <class T, int NB, int NW>
+struct FwdLds {
+  static constexpr int kN = NB * 32;          // states, padded
+  static constexpr int kP = NW * 16;          // columns of the head in this work-group
+  static constexpr int ldn = stride_of<T>(kN);
+  static constexpr int ldp = stride_of<T>(kP);
+  static constexpr int ldw = stride_of<T>(kTok);
+  alignas(16) T b[kTok * ldn];
+  alignas(16) T c[kTok * ldn];
+  alignas(16) T x[kTok * ldp];
+  alignas(16) T w[kTok * ldw];
+  alignas(16) Decays dc;
+};
+
+template <class T, int NB, int NW>
+__global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(SsmArgs a, Walk w) {
+  typedef FwdLds<T, NB, NW> L;
+  __shared__ L s;
+  constexpr int kThreads = NW * 64;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, l15 = lane & 15, g = lane >> 4;
+  const int work = xcd_contiguous(blockIdx.x, gridDim.x);
+  const int per = a.heads * a.slices;
+  const int unit = work / per;
+  const int h = work % per / a.slices;
+  const int slice = work % a.slices;
+  const Unit u = locate(a.q, unit, a.seg);
+  if (!u.live) return;
+  const bool packed = a.q.offsets != nullptr;
+  const int p0 = slice * L::kP;                          // first column of the work-group
+  const int cols = min(a.width - p0, L::kP);
+  const int col = p0 + wave * 16 + l15;                  // this lane's column
+  const bool live = col < a.width;
+  const long head = static_cast<long>(a.states) * a.width;
+
+  const T* xp = seq_ptr<const T>(a.x, u.seq, u.row0, packed) + h * a.width + p0;
+  const T* bp = seq_ptr<const T>(a.B, u.seq, u.row0, packed) + h / a.ratio * a.states;
+  const T* cp = seq_ptr<const T>(a.C, u.seq, u.row0, packed) + h / a.ratio * a.states;
+  T* yp = seq_ptr<T>(a.y, u.seq, u.row0, packed) + h * a.width + p0;
+  const void* dtp = a.dt_bf16 ? static_cast<const void*>(seq_ptr<const bf16>(a.dt, u.seq, u.row0, packed))
+                              : static_cast<const void*>(seq_ptr<const float>(a.dt, u.seq, u.row0, packed));
+  const float A = a.A[h], bias = a.bias != nullptr ? a.bias[h] : 0.0f, D = a.D != nullptr ? a.D[h] : 0.0f;
+
+  v4f st[2 * NB];
+  {
+    const float* from = u.index == 0
+                            ? (a.initial == nullptr ? nullptr : a.initial + (static_cast<long>(u.seq) * a.heads + h) * head)
+                            : w.seg_state + (static_cast<long>(unit) * a.heads + h) * head;
+    load_state<NB>(st, from, a.width, a.states, col, live);
+  }
+  // tiles above the diagonal that a 32-wide product step touches stay zero
+  for (int i = tid; i < kTok * L::ldw; i += kThreads) s.w[i] = static_cast<T>(0.0f);
+
+  const int end = min(u.t0 + a.seg, u.len);
+  Tile<T, kTok, L::kN, kThreads> tb, tc;
+  Tile<T, kTok, L::kP, kThreads> tx;
+  float raw = 0.0f;
+  const auto fetch = [&](int t) {
+    const int rows = end - t;
+    tb.load(bp + t * a.B.row_stride, a.B.row_stride, rows, a.states, tid);
+    tc.load(cp + t * a.C.row_stride, a.C.row_stride, rows, a.states, tid);
+    tx.load(xp + t * a.x.row_stride, a.x.row_stride, rows, cols, tid);
+    if (wave == 0 && lane < rows) raw = raw_step(a, a.dt, dtp, t + lane, h);
+  };
+  if (u.t0 < end) fetch(u.t0);
+  for (int t = u.t0; t < end; t += kTok) {
+    const int rows = min(end - t, kTok);
+    __syncthreads();  // the last step's readers are done
+    tb.store(s.b, L::ldn, tid);
+    tc.store(s.c, L::ldn, tid);
+    tx.store(s.x, L::ldp, tid);
+    if (wave == 0) make_decays(s.dc, lane < rows ? step_of(a, raw, bias) : 0.0f, A);
+    __syncthreads();
+    if (t + kTok < end) fetch(t + kTok);
+
+    // scores, transposed as a result: lane has t = l15, s = 4 g + i
+    for (int i = wave; i < 10; i += NW) {
+      int ti, si;
+      lower_tile(i, &ti, &si);
+      v4f acc = {0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < NB; ++k)
+        mma(acc, frag_row(s.b, L::ldn, si * 16, k * 32), frag_row(s.c, L::ldn, ti * 16, k * 32));
+      const int tt = ti * 16 + l15, ss = si * 16 + 4 * g;
+      const float ch = s.dc.hi[tt], cl = s.dc.lo[tt];
+      T out[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float e = exp2_of((ch - s.dc.hi[ss + j]) + (cl - s.dc.lo[ss + j]));
+        // the scores become an operand: 8 bits with bf16, as x has
+        out[j] = static_cast<T>(ss + j <= tt ? acc[j] * e * s.dc.d[ss + j] : 0.0f);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s.w[tt * L::ldw + ss + j] = out[j];
+    }
+    // y from the state before the step.  The state as an operand keeps 8 bits
+    // with bf16, like the y it goes into; the state itself stays fp32.
+    v4f y[4];
+    {
+      Frag<T> sf[NB];
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = st[2 * k + (j >> 2)][j & 3];
+        sf[k] = frag_of<T>(v, nullptr);
+      }
+#pragma unroll
+      for (int ti = 0; ti < 4; ++ti) {
+        y[ti] = v4f{0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < NB; ++k) mma(y[ti], frag_row_result(s.c, L::ldn, ti * 16, k * 32), sf[k]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[ti][j] *= s.dc.from[ti * 16 + 4 * g + j];
+      }
+    }
+    __syncthreads();
+    Frag<T> xf[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) xf[k] = frag_col(s.x, L::ldp, k * 32, wave * 16);
+#pragma unroll
+    for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+      for (int k = 0; k <= ti / 2; ++k) mma(y[ti], frag_row(s.w, L::ldw, ti * 16, k * 32), xf[k]);
+    advance_state<T, NB>(st, s.dc.total, s.dc.to, s.b, L::ldn, xf);
+    // D x, then y through this wave's own columns of the x tile to rows of 16 bytes
+#pragma unroll
+    for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        T* e = s.x + (ti * 16 + 4 * g + j) * L::ldp + wave * 16 + l15;
+        *e = static_cast<T>(fmaf(D, static_cast<float>(*e), y[ti][j]));
+      }
+    constexpr int kVec = Vec<T>::n, kPerRow = 16 / kVec;
+#pragma unroll
+    for (int i = 0; i < kTok * kPerRow / 64; ++i) {
+      const int r = (lane + i * 64) / kPerRow, c = wave * 16 + (lane + i * 64) % kPerRow * kVec;
+      if (r < rows && c < cols)
+        *reinterpret_cast<typename Vec<T>::type*>(yp + (t + r) * a.y.row_stride + c) =
+            *reinterpret_cast<const typename Vec<T>::type*>(s.x + r * L::ldp + c);
+    }
+  }
+  if (a.final_state != nullptr && u.t0 + static_cast<long>(a.seg) >= u.len)
+    save_state<NB>(st, a.final_state + (static_cast<long>(u.seq) * a.heads + h) * head, a.width, a.states, col, live);
+}
+
+template <class T, int NB, int NW>
+__global__ __launch_bounds__(NW * 64) void ssm_summary_kernel(SsmArgs a, Walk w) {
+  __shared__ WalkLds<T, NB, NW> s;
+  walk<T, NB, NW, false>(a, w, s);
+}
+
+__global__ __launch_bounds__(256) void ssm_carry_kernel(SsmArgs a, Walk w) { carry(a, w, blockIdx.z); }
+
+// ------------------------------------------------------------- single token
+// A work-group per sequence and head; a thread holds four neighbouring
+// columns and walks the state's rows, so a row is read and written as 16-byte
+// accesses and y needs no sum across the lanes of a row.
+constexpr int kStepThreads = 256;
+
+struct StepArgs {
+  SsmArgs a;
+  const float* state;
+  float* new_state;
+};
+
+template <class T>
+__global__ __launch_bounds__(kStepThreads) void ssm_step_kernel(StepArgs sa) {
+  const SsmArgs& a = sa.a;
+  __shared__ float lds[kStepThreads * 4];
+  __shared__ float sb[kMaxDim], sc[kMaxDim];
+  const int h = blockIdx.x, seq = blockIdx.y, tid = threadIdx.x;
+  const int quads = a.width / 4;
+  const int rows = kStepThreads / quads;  // state rows per pass
+  const int q = tid % quads, r0 = tid / quads;
+  const long base = (static_cast<long>(seq) * a.heads + h) * a.states * a.width;
+  constexpr int kAhead = 8;
+  v4f s[kAhead];
+  const bool live = r0 < rows;
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    const int n = r0 + j * rows;
+    if (live && n < a.states) s[j] = *reinterpret_cast<const v4f*>(sa.state + base + static_cast<long>(n) * a.width + 4 * q);
+  }
+  const int gr = h / a.ratio * a.states;
+  if (tid < a.states) sb[tid] = static_cast<float>((static_cast<const T*>(a.B.data) + seq * a.B.batch_stride)[gr + tid]);
+  else if (tid >= kMaxDim && tid - kMaxDim < a.states)
+    sc[tid - kMaxDim] = static_cast<float>((static_cast<const T*>(a.C.data) + seq * a.C.batch_stride)[gr + tid - kMaxDim]);
+  const long di = seq * a.dt.batch_stride + h;
+  const float raw = a.dt_bf16 ? static_cast<float>(static_cast<const bf16*>(a.dt.data)[di])
+                              : static_cast<const float*>(a.dt.data)[di];
+  const float d = step_of(a, raw, a.bias != nullptr ? a.bias[h] : 0.0f);
+  const float decay = exp2_of(static_cast<double>(d) * static_cast<double>(a.A[h]) * 1.4426950408889634074);
+  const T* xp = static_cast<const T*>(a.x.data) + seq * a.x.batch_stride + h * a.width + 4 * q;
+  float x[4], xd[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = static_cast<float>(xp[i]);
+    xd[i] = x[i] * d;
+  }
+  __syncthreads();
+  v4f y = {0, 0, 0, 0};
+  for (int j0 = 0; j0 * rows < a.states; j0 += kAhead) {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int n = r0 + (j0 + j) * rows;
+      if (live && n < a.states) {
+        const long at = base + static_cast<long>(n) * a.width + 4 * q;
+        v4f v = j0 == 0 ? s[j] : *reinterpret_cast<const v4f*>(sa.state + at);
+        const float b = sb[n], c = sc[n];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i] = fmaf(decay, v[i], b * xd[i]);
+          y[i] = fmaf(c, v[i], y[i]);
+        }
+        *reinterpret_cast<v4f*>(sa.new_state + at) = v;
+      }
+    }
+  }
+  if (live) *reinterpret_cast<v4f*>(&lds[(r0 * quads + q) * 4]) = y;
+  __syncthreads();
+  if (tid < a.width) {
+    float v = 0.0f;
+    for (int r = 0; r < rows; ++r) v += lds[r * a.width + tid];
+    const float xv = static_cast<float>((static_cast<const T*>(a.x.data) + seq * a.x.batch_stride)[h * a.width + tid]);
+    if (a.D != nullptr) v = fmaf(a.D[h], xv, v);
+    (static_cast<T*>(a.y.data) + seq * a.y.batch_stride)[h * a.width + tid] = static_cast<T>(v);
+  }
+}
+
+// --------------------------------------------------------------------- host
+template <class T, int NB, int NW>
+int launch_fwd(const SsmArgs& a, const Walk& w, bool segments, unsigned blocks, hipStream_t s) {
+  if (segments) {
+    ssm_summary_kernel<T, NB, NW><<<blocks, NW * 64, 0, s>>>(a, w);
+    if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
+    const unsigned quads = static_cast<unsigned>((a.states * a.width + 1023) / 1024);
+    ssm_carry_kernel<<<dim3(quads, a.heads, a.q.batch), 256, 0, s>>>(a, w);
+    if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
+  }
+  ssm_fwd_kernel<T, NB, NW><<<blocks, NW * 64, 0, s>>>(a, w);
+  return launch_status();
+}
+
+template <class T, int NB>
+int launch_fwd_width(const SsmArgs& a, const Walk& w, bool segments, unsigned blocks, int nw,
+                     hipStream_t s) {
+  switch (nw) {
+    case 1: return launch_fwd<T, NB, 1>(a, w, segments, blocks, s);
+    case 2: return launch_fwd<T, NB, 2>(a, w, segments, blocks, s);
+    default: return launch_fwd<T, NB, 4>(a, w, segments, blocks, s);
+  }
+}
+
+template <class T>
+int launch_fwd_states(const SsmArgs& a, const Walk& w, bool segments, unsigned blocks, int nw,
+                     hipStream_t s) {
+  if (a.states <= 32) return launch_fwd_width<T, 1>(a, w, segments, blocks, nw, s);
+  if (a.states <= 64) return launch_fwd_width<T, 2>(a, w, segments, blocks, nw, s);
+  return launch_fwd_width<T, 4>(a, w, segments, blocks, nw, s);
+}
+
+}  // namespace
+
+namespace ssm {
+
+int check_dims(const mamba2_seqs& q, const mamba2_ssm_dims& d) {
+  if (!type_ok(d.type) || !type_ok(d.dt_type)) return MAMBA2_SCAN_EUNSUPPORTED;
+  const int st = check_seqs(q);
+  if (st != MAMBA2_SCAN_OK) return st;
+  if (d.heads < 1 || d.groups < 1 || d.width < 1 || d.states < 1 || d.heads % d.groups != 0) return MAMBA2_SCAN_EBADDIM;
+  if (d.width % 8 != 0 || d.states % 8 != 0 || d.width > kMaxDim || d.states > kMaxDim || d.heads > 65535 ||
+      q.batch > 65535)
+    return MAMBA2_SCAN_EUNSUPPORTED;
+  return MAMBA2_SCAN_OK;
+}
+
+// Rows that are accessed in 16-byte vectors.
+int check_vec_rows(const mamba2_rows& r, const mamba2_seqs& q, long long width, size_t elem) {
+  const int st = check_rows(r, q, width, elem);
+  if (st != MAMBA2_SCAN_OK || q.length == 0) return st;
+  const long long n = 8;
+  if (!aligned_to(r.data, 16)) return MAMBA2_SCAN_EALIGN;
+  if ((q.length > 1 && r.row_stride % n != 0) || (q.offsets == nullptr && q.batch > 1 && r.batch_stride % n != 0))
+    return MAMBA2_SCAN_EALIGN;
+  return MAMBA2_SCAN_OK;
+}
+
+int waves_of(int width) { return width <= 16 ? 1 : width <= 32 ? 2 : 4; }
+
+// Tokens per segment.  A work-group walks its tokens one step after another,
+// so short of kCUs * 4 work-groups the tokens are cut into segments; each
+// costs a second reading of x and B and a state, so no more than needed.
+int segment_tokens(const mamba2_seqs& q, const mamba2_ssm_dims& d) {
+  const long slices = (d.width + waves_of(d.width) * 16 - 1) / (waves_of(d.width) * 16);
+  const long lanes = static_cast<long>(d.heads) * slices * (q.offsets != nullptr ? 1 : q.batch);
+  const long want = (kCUs * 4 + lanes - 1) / lanes;  // segments, over all rows of a packed call
+  long seg = (q.length + want - 1) / want;
+  if (want <= 2 && q.offsets == nullptr) seg = q.length;  // enough sequences and heads
+  seg = (seg + kTok - 1) / kTok * kTok;
+  return static_cast<int>(seg < 2 * kTok ? 2 * kTok : seg);
+}
+
+}  // namespace ssm
+
+extern "C" {
+
+size_t mamba2_ssm_fwd_workspace_bytes(mamba2_seqs q, mamba2_ssm_dims d) {
+  if (check_dims(q, d) != MAMBA2_SCAN_OK) return 0;
+  const int seg = segment_tokens(q, d);
+  if (q.length <= seg) return 0;
+  const size_t n = static_cast<size_t>(unit_count(q, seg)) * d.heads * (static_cast<size_t>(d.states) * d.width + 1);
+  return (n * sizeof(float) + 15) / 16 * 16;
+}
+
+int mamba2_ssm_fwd(mamba2_seqs q, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows dt, const float* A, mamba2_rows B,
+                   mamba2_rows C, const float* D, const float* dt_bias, const float* initial_state, mamba2_rows y,
+                   float* final_state, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_dims(q, d);
+  if (st != MAMBA2_SCAN_OK) return st;
+  const size_t e = type_size(d.type);
+  const long long xw = static_cast<long long>(d.heads) * d.width, bw = static_cast<long long>(d.groups) * d.states;
+  if (A == nullptr) return MAMBA2_SCAN_ENULL;
+  if ((st = check_vec_rows(x, q, xw, e)) != MAMBA2_SCAN_OK || (st = check_vec_rows(B, q, bw, e)) != MAMBA2_SCAN_OK ||
+      (st = check_vec_rows(C, q, bw, e)) != MAMBA2_SCAN_OK || (st = check_vec_rows(y, q, xw, e)) != MAMBA2_SCAN_OK ||
+      (st = check_rows(dt, q, d.heads, type_size(d.dt_type))) != MAMBA2_SCAN_OK)
+    return st;
+  if (!aligned_to(A, 4) || !aligned_to(D, 4) || !aligned_to(dt_bias, 4) || !aligned_to(initial_state, 16) ||
+      !aligned_to(final_state, 16))
+    return MAMBA2_SCAN_EALIGN;
+  const size_t need = mamba2_ssm_fwd_workspace_bytes(q, d);
+  if (need > 0) {
+    if (workspace == nullptr) return MAMBA2_SCAN_ENULL;
+    if (workspace_bytes < need) return MAMBA2_SCAN_ESIZE;
+    if (!aligned_to(workspace, 16)) return MAMBA2_SCAN_EALIGN;
+  }
+  if (q.length == 0 && final_state == nullptr) return MAMBA2_SCAN_OK;
+  SsmArgs a = {};
+  a.q = q;
+  a.x = x;
+  a.dt = dt;
+  a.B = B;
+  a.C = C;
+  a.y = y;
+  a.A = A;
+  a.D = D;
+  a.bias = dt_bias;
+  a.initial = initial_state;
+  a.final_state = final_state;
+  a.heads = d.heads;
+  a.width = d.width;
+  a.ratio = d.heads / d.groups;
+  a.states = d.states;
+  a.softplus = d.softplus;
+  a.dt_bf16 = d.dt_type == MAMBA2_BF16;
+  const int nw = waves_of(d.width);
+  a.slices = (d.width + nw * 16 - 1) / (nw * 16);
+  a.seg = segment_tokens(q, d);
+  a.units = static_cast<int>(unit_count(q, a.seg));
+  Walk w = {};
+  w.v = x;
+  w.m = B;
+  w.first = initial_state;
+  w.seg_state = static_cast<float*>(workspace);
+  w.seg_decay = need > 0 ? w.seg_state + static_cast<size_t>(a.units) * d.heads * d.states * d.width : nullptr;
+  const long long blocks = static_cast<long long>(a.units) * a.heads * a.slices;
+  if (blocks > 2147483647LL) return MAMBA2_SCAN_EBADDIM;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const unsigned n = static_cast<unsigned>(blocks);
+  return d.type == MAMBA2_BF16 ? launch_fwd_states<bf16>(a, w, need > 0, n, nw, s)
+                               : launch_fwd_states<float>(a, w, need > 0, n, nw, s);
+}
+
+int mamba2_ssm_step(int batch, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows dt, const float* A, mamba2_rows B,
+                    mamba2_rows C, const float* D, const float* dt_bias, const float* state, mamba2_rows y,
+                    float* new_state, void* stream) {
+  const mamba2_seqs q = {batch, 1, nullptr};
+  int st = check_dims(q, d);
+  if (st != MAMBA2_SCAN_OK) return st;
+  const size_t e = type_size(d.type);
+  const long long xw = static_cast<long long>(d.heads) * d.width, bw = static_cast<long long>(d.groups) * d.states;
+  if (A == nullptr || state == nullptr || new_state == nullptr) return MAMBA2_SCAN_ENULL;
+  if ((st = check_rows(x, q, xw, e)) != MAMBA2_SCAN_OK || (st = check_rows(B, q, bw, e)) != MAMBA2_SCAN_OK ||
+      (st = check_rows(C, q, bw, e)) != MAMBA2_SCAN_OK || (st = check_rows(y, q, xw, e)) != MAMBA2_SCAN_OK ||
+      (st = check_rows(dt, q, d.heads, type_size(d.dt_type))) != MAMBA2_SCAN_OK)
+    return st;
+  if (!aligned_to(A, 4) || !aligned_to(D, 4) || !aligned_to(dt_bias, 4) || !aligned_to(state, 16) ||
+      !aligned_to(new_state, 16))
+    return MAMBA2_SCAN_EALIGN;
+  StepArgs sa = {};
+  SsmArgs& a = sa.a;
+  a.x = x;
+  a.dt = dt;
+  a.B = B;
+  a.C = C;
+  a.y = y;
+  a.A = A;
+  a.D = D;
+  a.bias = dt_bias;
+  a.heads = d.heads;
+  a.width = d.width;
+  a.ratio = d.heads / d.groups;
+  a.states = d.states;
+  a.softplus = d.softplus;
+  a.dt_bf16 = d.dt_type == MAMBA2_BF16;
+  sa.state = state;
+  sa.new_state = new_state;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const dim3 grid(d.heads, batch);
+  if (d.type == MAMBA2_BF16) ssm_step_kernel<bf16><<<grid, kStepThreads, 0, s>>>(sa);
+  else ssm_step_kernel<float><<<grid, kStepThreads, 0, s>>>(sa);
+  return launch_status();
+}
+
+}  // extern "C"

@@ -1,0 +1,693 @@
+// Backward of the selective state space scan for gfx950.
+//
+// With G_t the gradient of the state S_t (G_t = C_t d_y_t^T + e^(d A)_{t+1} G_{t+1}):
+//   d_x_t = d_t G_t^T B_t + D d_y_t          d_B_t = sum_heads G_t (d_t x_t)
+//   d_C_t = sum_heads S_t d_y_t              d_S_0 = e^(d A)_1 G_1
+//   d_d_t = x_t . (G_t^T B_t) + A m_t        d_A = sum_t d_t m_t,  m_t = <G_t, e^(d A)_t S_{t-1}>
+// where m_t is the gradient of token t's log decay: everything that flows
+// from before t to t or behind it.
+//
+// Two passes.  The walk (ssm_walk_kernel) recomputes the state forward and its
+// gradient in reverse, side by side, and writes both at every step of 64
+// tokens.  ssm_bwd_kernel then takes all steps in parallel: a work-group owns
+// the 64 tokens of one step and a run of the heads that share B and C, so d_B
+// and d_C are summed over heads in registers, in a fixed order.  Each of its
+// four waves owns 16 rows of every output.  In a step, per head, with
+// E[t][s] = 2^(c_t - c_s) (s <= t), V = (G B)^T and U = S^T-side products:
+//   P = (C B^T) o E,  Q = (d_y x^T) o E o d
+//   d_x = d o (P^T d_y + 2^(c_end-c) o (B G))        + D d_y
+//   d_B = Q^T C + 2^(c_end-c) d o (x G^T)
+//   d_C = Q B   + 2^c o (d_y S^T)
+// m_t is a sum of terms that are all of its own kind: pairs s < t <= t' of
+// P o d_y x^T, the step's starting state into rows at or behind t, rows before t
+// into what follows the step, and the starting state through the whole step.
+// Nothing is obtained as a difference of larger sums.
+#include "ssm_common.h"
+
+namespace {
+
+using namespace ssm;
+
+struct BwdArgs {
+  SsmArgs a;
+  mamba2_rows d_y, d_x, d_dt, d_B, d_C;
+  const float* keep_s;     // [steps][heads][states][width]
+  const float* keep_g;
+  float* part;             // [steps][heads][4]: d_A, d_D, d_dt_bias of the step
+  float* part_b;           // [splits][rows][groups][states]: d_B of a run of heads
+  float* part_c;
+  long rows;
+  int steps;
+  int groups;
+  int splits;              // runs of heads per group
+  int run;                 // heads per run
+};
+
+template <class T, int NB, int NW>
+__global__ __launch_bounds__(NW * 64) void ssm_walk_kernel(SsmArgs a, Walk f, Walk r) {
+  __shared__ WalkLds<T, NB, NW> s;
+  walk<T, NB, NW, true>(a, blockIdx.y == 0 ? f : r, s);
+}
+template <class T, int NB, int NW>
+__global__ __launch_bounds__(NW * 64) void ssm_walk_summary_kernel(SsmArgs a, Walk f, Walk r) {
+  __shared__ WalkLds<T, NB, NW> s;
+  walk<T, NB, NW, false>(a, blockIdx.y == 0 ? f : r, s);
+}
+__global__ __launch_bounds__(256) void ssm_walk_carry_kernel(SsmArgs a, Walk f, Walk r) {
+  if (blockIdx.z & 1) carry(a, r, blockIdx.z >> 1);
+  else carry(a, f, blockIdx.z >> 1);
+}
+
+constexpr int kBwdThreads = 256;
+
+template <class T, int NB, int PT>
+struct BwdLds {
+  static constexpr int kN = NB * 32;
+  static constexpr int kP = PT * 16 < 32 ? 32 : PT * 16;  // a product over the columns takes 32 at a time
+  static constexpr int kTerms = sizeof(T) == 2 ? 2 : 1;
+  static constexpr int ldn = stride_of<T>(kN);
+  static constexpr int ldp = stride_of<T>(kP);
+  alignas(16) T b[kTok * ldn];
+  alignas(16) T c[kTok * ldn];
+  alignas(16) T x[kTok * ldp];
+  alignas(16) T dy[kTok * ldp];
+  alignas(16) T st[kTerms][kN * ldp];  // the starting state, then the gradient behind the step, in two terms
+  alignas(16) Decays dc;
+  float inner[4][kTok];   // m_t: pairs within the step, per wave's columns
+  float after[kTok];      // starting state into row t
+  float before[kTok];     // row t into what follows (without d)
+  float direct[kTok];     // x . P^T d_y
+  float whole[4];         // starting state through the step, per wave
+  float skip[4];          // sum d_y . x, per wave
+};
+
+// A [states][width] fp32 matrix slice in registers, then LDS in one or two terms.
+template <class T, int NB, int PT>
+struct StateTile {
+  typedef BwdLds<T, NB, PT> L;
+  static constexpr int kQuads = L::kP / 4;
+  static constexpr int kN = L::kN * kQuads / kBwdThreads;
+  v4f v[kN];
+  __device__ __forceinline__ void load(const float* p, int width, int states, int cols) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int e = threadIdx.x + i * kBwdThreads, r = e / kQuads, c = e % kQuads * 4;
+      v[i] = (r < states && c < cols) ? *reinterpret_cast<const v4f*>(p + static_cast<long>(r) * width + c)
+                                      : v4f{0, 0, 0, 0};
+    }
+  }
+  __device__ __forceinline__ void store(L& s) const {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int e = threadIdx.x + i * kBwdThreads, r = e / kQuads, c = e % kQuads * 4;
+      if constexpr (sizeof(T) == 2) {
+        v4bf hi, lo;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          hi[j] = static_cast<bf16>(v[i][j]);
+          lo[j] = static_cast<bf16>(v[i][j] - static_cast<float>(hi[j]));
+        }
+        *reinterpret_cast<v4bf*>(&s.st[0][r * L::ldp + c]) = hi;
+        *reinterpret_cast<v4bf*>(&s.st[L::kTerms - 1][r * L::ldp + c]) = lo;
+      } else {
+        *reinterpret_cast<v4f*>(&s.st[0][r * L::ldp + c]) = v[i];
+      }
+    }
+  }
+};
+
+// Two result tiles stacked along k as one operand.
+template <class T>
+__device__ __forceinline__ Frag<T> frag_tiles(const v4f& a, const v4f& b) {
+  const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  return frag_of<T>(v, nullptr);
+}
+
+template <class T, int NB, int PT>
+__global__ __launch_bounds__(kBwdThreads, 1) void ssm_bwd_kernel(BwdArgs ba) {
+  typedef BwdLds<T, NB, PT> L;
+  __shared__ L s;
+  const SsmArgs& a = ba.a;
+  constexpr int kKp = L::kP / 32;   // 32-wide product steps over the columns
+  constexpr int kPt = L::kP / 16;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, l15 = lane & 15, g = lane >> 4;
+  const int work = xcd_contiguous(blockIdx.x, gridDim.x);
+  const int split = work % ba.splits;
+  const int gr = work / ba.splits % ba.groups;
+  const int step = work / ba.splits / ba.groups;
+  const Unit u = locate(a.q, step, kTok);
+  if (u.t0 >= u.len) return;  // (the reduction skips these steps too)
+  const bool packed = a.q.offsets != nullptr;
+  const int rows = min(u.len - u.t0, kTok);
+  const int h0 = gr * a.ratio + split * ba.run;
+  const int h1 = min(h0 + ba.run, (gr + 1) * a.ratio);
+  const long head = static_cast<long>(a.states) * a.width;
+  const int row = wave * 16;                // this wave's rows
+  const int slices = (a.width + L::kP - 1) / L::kP;
+
+  const T* xp = seq_ptr<const T>(a.x, u.seq, u.row0, packed) + u.t0 * a.x.row_stride;
+  const T* gp = seq_ptr<const T>(ba.d_y, u.seq, u.row0, packed) + u.t0 * ba.d_y.row_stride;
+  T* op = seq_ptr<T>(ba.d_x, u.seq, u.row0, packed) + u.t0 * ba.d_x.row_stride;
+  const void* dtp = a.dt_bf16 ? static_cast<const void*>(seq_ptr<const bf16>(a.dt, u.seq, u.row0, packed))
+                              : static_cast<const void*>(seq_ptr<const float>(a.dt, u.seq, u.row0, packed));
+  {
+    Tile<T, kTok, L::kN, kBwdThreads> tb, tc;
+    tb.load(seq_ptr<const T>(a.B, u.seq, u.row0, packed) + u.t0 * a.B.row_stride + gr * a.states, a.B.row_stride,
+            rows, a.states, tid);
+    tc.load(seq_ptr<const T>(a.C, u.seq, u.row0, packed) + u.t0 * a.C.row_stride + gr * a.states, a.C.row_stride,
+            rows, a.states, tid);
+    tb.store(s.b, L::ldn, tid);
+    tc.store(s.c, L::ldn, tid);
+    s.inner[wave][lane] = 0.0f;  // rows before a wave's columns stay zero
+  }
+  v4f db[2 * NB], dcc[2 * NB];
+#pragma unroll
+  for (int n = 0; n < 2 * NB; ++n) db[n] = dcc[n] = v4f{0, 0, 0, 0};
+  v4f cb[4];  // (C B^T)[t][s], column s = row + l15, rows t = 16 ti + 4 g + i
+  __syncthreads();
+#pragma unroll
+  for (int ti = 0; ti < 4; ++ti) {
+    cb[ti] = v4f{0, 0, 0, 0};
+    if (ti >= wave) {
+#pragma unroll
+      for (int k = 0; k < NB; ++k) mma(cb[ti], frag_row(s.c, L::ldn, ti * 16, k * 32), frag_row(s.b, L::ldn, row, k * 32));
+    }
+  }
+
+  for (int h = h0; h < h1; ++h) {
+    const float A = a.A[h], bias = a.bias != nullptr ? a.bias[h] : 0.0f, D = a.D != nullptr ? a.D[h] : 0.0f;
+    float raw = 0.0f;
+    if (wave == 0 && lane < rows) raw = raw_step(a, a.dt, dtp, u.t0 + lane, h);
+    for (int slice = 0; slice < slices; ++slice) {
+      const int p0 = slice * L::kP, cols = min(a.width - p0, L::kP);
+      const long state_at = (static_cast<long>(step) * a.heads + h) * head + p0;
+      StateTile<T, NB, PT> ts, tg;
+      Tile<T, kTok, L::kP, kBwdThreads> tx, ty;
+      ts.load(ba.keep_s + state_at, a.width, a.states, cols);
+      tx.load(xp + h * a.width + p0, a.x.row_stride, rows, cols, tid);
+      ty.load(gp + h * a.width + p0, ba.d_y.row_stride, rows, cols, tid);
+      __syncthreads();  // the last round's readers are done
+      ts.store(s);
+      tx.store(s.x, L::ldp, tid);
+      ty.store(s.dy, L::ldp, tid);
+      if (wave == 0 && slice == 0) make_decays(s.dc, lane < rows ? step_of(a, raw, bias) : 0.0f, A);
+      __syncthreads();
+      tg.load(ba.keep_g + state_at, a.width, a.states, cols);
+
+      // ---- within the step, columns s of this wave
+      v4f dx[kPt];
+#pragma unroll
+      for (int p = 0; p < kPt; ++p) dx[p] = v4f{0, 0, 0, 0};
+      {
+        const int sc = row + l15;
+        const float ch = s.dc.hi[sc], cl = s.dc.lo[sc], d = s.dc.d[sc];
+        v4f pw[4], qw[4];
+        float direct = 0.0f, skip = 0.0f, behind = 0.0f;
+#pragma unroll
+        for (int ti = 3; ti >= 0; --ti) {
+          pw[ti] = qw[ti] = v4f{0, 0, 0, 0};
+          if (ti < wave) continue;
+          v4f yx = {0, 0, 0, 0};
+#pragma unroll
+          for (int k = 0; k < kKp; ++k) mma(yx, frag_row(s.dy, L::ldp, ti * 16, k * 32), frag_row(s.x, L::ldp, row, k * 32));
+          float pair[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = ti * 16 + 4 * g + i;
+            const float e = t >= sc ? exp2_of((s.dc.hi[t] - ch) + (s.dc.lo[t] - cl)) : 0.0f;
+            pw[ti][i] = cb[ti][i] * e;
+            qw[ti][i] = yx[i] * e * d;
+            const float m = pw[ti][i] * yx[i];
+            direct += m;
+            pair[i] = t > sc ? m : 0.0f;
+            if (t == sc) skip += yx[i];
+          }
+          // sum of the column's pairs at rows >= t: in the lane, over the lane
+          // groups behind, and over the tiles behind
+          pair[2] += pair[3];
+          pair[1] += pair[2];
+          pair[0] += pair[1];
+          const float d1 = __shfl_down(pair[0], 16), d2 = __shfl_down(pair[0], 32), d3 = __shfl_down(pair[0], 48);
+          const float rest = behind + (g < 3 ? d1 : 0.0f) + (g < 2 ? d2 : 0.0f) + (g < 1 ? d3 : 0.0f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = ti * 16 + 4 * g + i;
+            const float v = sum16(sc < t ? (pair[i] + rest) * d : 0.0f);
+            if (l15 == 0) s.inner[wave][t] = slice == 0 ? v : s.inner[wave][t] + v;
+          }
+          float all = pair[0];
+          all += __shfl_xor(all, 16);
+          behind += all + __shfl_xor(all, 32);
+        }
+        direct += __shfl_xor(direct, 16);
+        direct += __shfl_xor(direct, 32);
+        if (g == 0) s.direct[sc] = slice == 0 ? direct : s.direct[sc] + direct;
+        skip = sum64(skip);
+        if (lane == 0) s.skip[wave] = slice == 0 ? skip : s.skip[wave] + skip;
+        // The products' own operands keep 8 bits with bf16, as their results do.
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (2 * k + 1 < wave) continue;
+          const Frag<T> pf = frag_tiles<T>(pw[2 * k], pw[2 * k + 1]), qf = frag_tiles<T>(qw[2 * k], qw[2 * k + 1]);
+#pragma unroll
+          for (int p = 0; p < kPt; ++p) mma(dx[p], pf, frag_col_result(s.dy, L::ldp, k * 32, p * 16));
+#pragma unroll
+          for (int n = 0; n < 2 * NB; ++n) mma(db[n], qf, frag_col_result(s.c, L::ldn, k * 32, n * 16));
+        }
+      }
+      // ---- within the step, rows t of this wave
+      {
+        const int t = row + l15;
+        const float ch = s.dc.hi[t], cl = s.dc.lo[t];
+        v4f qw[4];
+#pragma unroll
+        for (int si = 0; si < 4; ++si) {
+          qw[si] = v4f{0, 0, 0, 0};
+          if (si > wave) continue;
+          v4f yx = {0, 0, 0, 0};
+#pragma unroll
+          for (int k = 0; k < kKp; ++k) mma(yx, frag_row(s.x, L::ldp, si * 16, k * 32), frag_row(s.dy, L::ldp, row, k * 32));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int sc = si * 16 + 4 * g + i;
+            const float e = t >= sc ? exp2_of((ch - s.dc.hi[sc]) + (cl - s.dc.lo[sc])) : 0.0f;
+            qw[si][i] = yx[i] * e * s.dc.d[sc];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (2 * k > wave) continue;
+          const Frag<T> qf = frag_tiles<T>(qw[2 * k], qw[2 * k + 1]);
+#pragma unroll
+          for (int n = 0; n < 2 * NB; ++n) mma(dcc[n], qf, frag_col_result(s.b, L::ldn, k * 32, n * 16));
+        }
+      }
+      // ---- the starting state into this wave's rows
+      {
+        Frag<T> yf[kKp];
+#pragma unroll
+        for (int k = 0; k < kKp; ++k) yf[k] = frag_row(s.dy, L::ldp, row, k * 32);
+        float from[4], r[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) from[i] = s.dc.from[row + 4 * g + i];
+#pragma unroll
+        for (int n = 0; n < 2 * NB; ++n) {
+          v4f o = {0, 0, 0, 0};
+#pragma unroll
+          for (int k = 0; k < kKp; ++k)
+#pragma unroll
+            for (int z = 0; z < L::kTerms; ++z) mma(o, yf[k], frag_row(s.st[z], L::ldp, n * 16, k * 32));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o[i] *= from[i];
+            r[i] = fmaf(static_cast<float>(s.c[(row + 4 * g + i) * L::ldn + n * 16 + l15]), o[i], r[i]);
+            dcc[n][i] += o[i];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float v = sum16(r[i]);
+          const int t = row + 4 * g + i;
+          if (l15 == 0) s.after[t] = slice == 0 ? v : s.after[t] + v;
+        }
+      }
+      __syncthreads();  // the starting state's readers are done
+      {
+        float w = 0.0f;
+#pragma unroll
+        for (int i = 0; i < StateTile<T, NB, PT>::kN; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w = fmaf(ts.v[i][j], tg.v[i][j], w);
+        w = sum64(w);
+        if (lane == 0) s.whole[wave] = slice == 0 ? w : s.whole[wave] + w;
+        tg.store(s);
+      }
+      __syncthreads();
+      // ---- this wave's rows into what follows the step
+      {
+        float left[4], to[4], q[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          left[i] = s.dc.left[row + 4 * g + i];
+          to[i] = s.dc.to[row + 4 * g + i];
+        }
+        Frag<T> bf[NB];
+#pragma unroll
+        for (int k = 0; k < NB; ++k) bf[k] = frag_row(s.b, L::ldn, row, k * 32);
+#pragma unroll
+        for (int p = 0; p < kPt; ++p) {
+          v4f o = {0, 0, 0, 0};
+#pragma unroll
+          for (int k = 0; k < NB; ++k)
+#pragma unroll
+            for (int z = 0; z < L::kTerms; ++z) mma(o, bf[k], frag_col(s.st[z], L::ldp, k * 32, p * 16));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o[i] *= left[i];
+            q[i] = fmaf(static_cast<float>(s.x[(row + 4 * g + i) * L::ldp + p * 16 + l15]), o[i], q[i]);
+            dx[p][i] += o[i];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float v = sum16(q[i]);
+          const int t = row + 4 * g + i;
+          if (l15 == 0) s.before[t] = slice == 0 ? v : s.before[t] + v;
+        }
+        Frag<T> xf[kKp];
+#pragma unroll
+        for (int k = 0; k < kKp; ++k) xf[k] = frag_row(s.x, L::ldp, row, k * 32);
+#pragma unroll
+        for (int n = 0; n < 2 * NB; ++n) {
+          v4f o = {0, 0, 0, 0};
+#pragma unroll
+          for (int k = 0; k < kKp; ++k) mma(o, xf[k], frag_row(s.st[0], L::ldp, n * 16, k * 32));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) db[n][i] = fmaf(to[i], o[i], db[n][i]);
+        }
+      }
+      // d_x through this wave's own rows of the x tile to rows of 16 bytes
+#pragma unroll
+      for (int p = 0; p < kPt; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = row + 4 * g + i, at = t * L::ldp + p * 16 + l15;
+          s.x[at] = static_cast<T>(fmaf(D, static_cast<float>(s.dy[at]), s.dc.d[t] * dx[p][i]));
+        }
+      constexpr int kVec = Vec<T>::n, kPerRow = L::kP / kVec;
+#pragma unroll
+      for (int i = 0; i < 16 * kPerRow / 64; ++i) {
+        const int r = row + (lane + i * 64) / kPerRow, c = (lane + i * 64) % kPerRow * kVec;
+        if (r < rows && c < cols)
+          *reinterpret_cast<typename Vec<T>::type*>(op + r * ba.d_x.row_stride + h * a.width + p0 + c) =
+              *reinterpret_cast<const typename Vec<T>::type*>(s.x + r * L::ldp + c);
+      }
+    }
+    __syncthreads();
+    // ---- the step sizes' gradients: wave 0, a token per lane
+    if (wave == 0) {
+      const float d = s.dc.d[lane];
+      const float after = __shfl(scan64(__shfl(s.after[lane], 63 - lane)), 63 - lane);
+      const float q = d * s.before[lane];
+      float upto = __shfl_up(scan64(q), 1);
+      if (lane == 0) upto = 0.0f;
+      const float whole = ((s.whole[0] + s.whole[1]) + (s.whole[2] + s.whole[3])) * s.dc.total;
+      const float inner = (s.inner[0][lane] + s.inner[1][lane]) + (s.inner[2][lane] + s.inner[3][lane]);
+      const float m = inner + after + upto + whole;
+      float dd = s.direct[lane] + s.before[lane] + A * m;
+      if (a.softplus) dd *= 1.0f / (1.0f + expf(-(raw + bias)));
+      float dA = d * m;
+      if (lane < rows) {
+        const long i = (u.t0 + lane) * ba.d_dt.row_stride + h;
+        if (a.dt_bf16) seq_ptr<bf16>(ba.d_dt, u.seq, u.row0, packed)[i] = static_cast<bf16>(dd);
+        else seq_ptr<float>(ba.d_dt, u.seq, u.row0, packed)[i] = dd;
+      } else {
+        dd = dA = 0.0f;
+      }
+      dA = sum64(dA);
+      dd = sum64(dd);
+      if (lane == 0) {
+        float* p = ba.part + (static_cast<long>(step) * a.heads + h) * 4;
+        p[0] = dA;
+        p[1] = (s.skip[0] + s.skip[1]) + (s.skip[2] + s.skip[3]);
+        p[2] = dd;
+      }
+    }
+  }
+
+  // ---- d_B and d_C, through this wave's own rows of the b and c tiles
+  __syncthreads();
+  if (ba.splits > 1) {
+    const long r0 = (packed ? u.row0 : static_cast<long>(u.seq) * a.q.length) + u.t0;
+    const long at = (split * ba.rows + r0) * ba.groups + gr;
+#pragma unroll
+    for (int n = 0; n < 2 * NB; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = row + 4 * g + i, c = n * 16 + l15;
+        if (t < rows && c < a.states) {
+          const long e = (at + static_cast<long>(t) * ba.groups) * a.states + c;
+          ba.part_b[e] = db[n][i];
+          ba.part_c[e] = dcc[n][i];
+        }
+      }
+    return;
+  }
+#pragma unroll
+  for (int n = 0; n < 2 * NB; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = (row + 4 * g + i) * L::ldn + n * 16 + l15;
+      s.b[at] = static_cast<T>(db[n][i]);
+      s.c[at] = static_cast<T>(dcc[n][i]);
+    }
+  T* bp = seq_ptr<T>(ba.d_B, u.seq, u.row0, packed) + u.t0 * ba.d_B.row_stride + gr * a.states;
+  T* cp = seq_ptr<T>(ba.d_C, u.seq, u.row0, packed) + u.t0 * ba.d_C.row_stride + gr * a.states;
+  constexpr int kVec = Vec<T>::n, kPerRow = L::kN / kVec;
+#pragma unroll
+  for (int i = 0; i < 16 * kPerRow / 64; ++i) {
+    const int r = row + (lane + i * 64) / kPerRow, c = (lane + i * 64) % kPerRow * kVec;
+    if (r < rows && c < a.states) {
+      *reinterpret_cast<typename Vec<T>::type*>(bp + r * ba.d_B.row_stride + c) =
+          *reinterpret_cast<const typename Vec<T>::type*>(s.b + r * L::ldn + c);
+      *reinterpret_cast<typename Vec<T>::type*>(cp + r * ba.d_C.row_stride + c) =
+          *reinterpret_cast<const typename Vec<T>::type*>(s.c + r * L::ldn + c);
+    }
+  }
+}
+
+// Sums the runs of heads: a block per step, four elements per thread.
+template <class T>
+__global__ __launch_bounds__(256) void ssm_bwd_join_kernel(BwdArgs ba) {
+  const SsmArgs& a = ba.a;
+  const Unit u = locate(a.q, blockIdx.x, kTok);
+  if (u.t0 >= u.len) return;
+  const bool packed = a.q.offsets != nullptr;
+  const int rows = min(u.len - u.t0, kTok), wide = ba.groups * a.states, quads = wide / 4;
+  const long r0 = (packed ? u.row0 : static_cast<long>(u.seq) * a.q.length) + u.t0;
+  const float* part = blockIdx.y == 0 ? ba.part_b : ba.part_c;
+  const mamba2_rows& out = blockIdx.y == 0 ? ba.d_B : ba.d_C;
+  T* op = seq_ptr<T>(out, u.seq, u.row0, packed) + u.t0 * out.row_stride;
+  for (int e = threadIdx.x; e < rows * quads; e += 256) {
+    const int r = e / quads, c = e % quads * 4;
+    v4f v = {0, 0, 0, 0};
+    for (int k = 0; k < ba.splits; ++k)
+      v += *reinterpret_cast<const v4f*>(part + (k * ba.rows + r0 + r) * wide + c);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) op[r * out.row_stride + c + j] = static_cast<T>(v[j]);
+  }
+}
+
+// Sums the steps' parts of d_A, d_D, d_dt_bias: a block per head.
+__global__ __launch_bounds__(256) void ssm_bwd_heads_kernel(BwdArgs ba, float* d_A, float* d_D, float* d_bias) {
+  __shared__ float lds[3][4];
+  const SsmArgs& a = ba.a;
+  const int h = blockIdx.x;
+  float v[3] = {0, 0, 0};
+  for (int i = threadIdx.x; i < ba.steps; i += 256) {
+    const Unit u = locate(a.q, i, kTok);
+    if (u.t0 >= u.len) continue;
+    const float* p = ba.part + (static_cast<long>(i) * a.heads + h) * 4;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) v[k] += p[k];
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    v[k] = sum64(v[k]);
+    if ((threadIdx.x & 63) == 0) lds[k][threadIdx.x >> 6] = v[k];
+  }
+  __syncthreads();
+  if (threadIdx.x < 3) {
+    const int k = threadIdx.x;
+    float* out = k == 0 ? d_A : k == 1 ? d_D : d_bias;
+    if (out != nullptr) out[h] = (lds[k][0] + lds[k][1]) + (lds[k][2] + lds[k][3]);
+  }
+}
+
+// --------------------------------------------------------------------- host
+struct Plan {
+  int seg, units, steps, slices, nw;
+  int splits, run;
+  long rows;
+  bool segments;
+  size_t keep, seg_state, seg_decay, part, part_bc, total;  // floats
+};
+
+size_t pad4(size_t n) { return (n + 3) / 4 * 4; }
+
+int make_plan(const mamba2_seqs& q, const mamba2_ssm_dims& d, Plan* p) {
+  const int st = check_dims(q, d);
+  if (st != MAMBA2_SCAN_OK) return st;
+  const size_t head = static_cast<size_t>(d.states) * d.width;
+  p->nw = waves_of(d.width);
+  p->slices = (d.width + p->nw * 16 - 1) / (p->nw * 16);
+  p->seg = segment_tokens(q, d);
+  p->units = static_cast<int>(unit_count(q, p->seg));
+  p->steps = static_cast<int>(unit_count(q, kTok));
+  p->segments = q.length > p->seg;
+  p->rows = static_cast<long>(q.length) * (q.offsets != nullptr ? 1 : q.batch);
+  // heads that share B and C stay together as long as the work-groups fill the chip
+  const int ratio = d.heads / d.groups;
+  const long groups = static_cast<long>(p->steps) * d.groups;
+  long splits = (2 * kCUs + groups - 1) / groups;
+  if (splits > ratio) splits = ratio;
+  p->run = static_cast<int>((ratio + splits - 1) / splits);
+  p->splits = (ratio + p->run - 1) / p->run;
+  p->keep = pad4(static_cast<size_t>(p->steps) * d.heads * head);
+  p->seg_state = p->segments ? pad4(static_cast<size_t>(p->units) * d.heads * head) : 0;
+  p->seg_decay = p->segments ? pad4(static_cast<size_t>(p->units) * d.heads) : 0;
+  p->part = pad4(static_cast<size_t>(p->steps) * d.heads * 4);
+  p->part_bc = p->splits > 1 ? pad4(static_cast<size_t>(p->splits) * p->rows * d.groups * d.states) : 0;
+  p->total = 2 * (p->keep + p->seg_state + p->seg_decay + p->part_bc) + p->part;
+  return MAMBA2_SCAN_OK;
+}
+
+struct Call {
+  BwdArgs ba;
+  Walk f, r;
+  Plan p;
+  float *d_A, *d_D, *d_bias;
+  hipStream_t s;
+};
+
+template <class T, int NB, int NW>
+int launch_bwd(const Call& c) {
+  const SsmArgs& a = c.ba.a;
+  const dim3 grid(static_cast<unsigned>(static_cast<long>(c.p.units) * a.heads * c.p.slices), 2);
+  if (c.p.segments) {
+    ssm_walk_summary_kernel<T, NB, NW><<<grid, NW * 64, 0, c.s>>>(a, c.f, c.r);
+    if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
+    const unsigned quads = static_cast<unsigned>((a.states * a.width + 1023) / 1024);
+    ssm_walk_carry_kernel<<<dim3(quads, a.heads, 2 * a.q.batch), 256, 0, c.s>>>(a, c.f, c.r);
+    if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
+  }
+  ssm_walk_kernel<T, NB, NW><<<grid, NW * 64, 0, c.s>>>(a, c.f, c.r);
+  if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
+  const unsigned blocks = static_cast<unsigned>(static_cast<long>(c.p.steps) * c.ba.groups * c.p.splits);
+  ssm_bwd_kernel<T, NB, NW><<<blocks, kBwdThreads, 0, c.s>>>(c.ba);
+  if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
+  if (c.p.splits > 1) {
+    ssm_bwd_join_kernel<T><<<dim3(c.p.steps, 2), 256, 0, c.s>>>(c.ba);
+    if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
+  }
+  ssm_bwd_heads_kernel<<<a.heads, 256, 0, c.s>>>(c.ba, c.d_A, c.d_D, c.d_bias);
+  return launch_status();
+}
+
+template <class T, int NB>
+int launch_bwd_width(const Call& c) {
+  switch (c.p.nw) {
+    case 1: return launch_bwd<T, NB, 1>(c);
+    case 2: return launch_bwd<T, NB, 2>(c);
+    default: return launch_bwd<T, NB, 4>(c);
+  }
+}
+
+template <class T>
+int launch_bwd_states(const Call& c) {
+  if (c.ba.a.states <= 32) return launch_bwd_width<T, 1>(c);
+  if (c.ba.a.states <= 64) return launch_bwd_width<T, 2>(c);
+  return launch_bwd_width<T, 4>(c);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mamba2_ssm_bwd_workspace_bytes(mamba2_seqs q, mamba2_ssm_dims d) {
+  Plan p;
+  if (make_plan(q, d, &p) != MAMBA2_SCAN_OK) return 0;
+  return p.total * sizeof(float);
+}
+
+int mamba2_ssm_bwd(mamba2_seqs q, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows dt, const float* A, mamba2_rows B,
+                   mamba2_rows C, const float* D, const float* dt_bias, const float* initial_state, mamba2_rows d_y,
+                   const float* d_final_state, mamba2_rows d_x, mamba2_rows d_dt, float* d_A, mamba2_rows d_B,
+                   mamba2_rows d_C, float* d_D, float* d_dt_bias, float* d_initial_state, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  Call c = {};
+  int st = make_plan(q, d, &c.p);
+  if (st != MAMBA2_SCAN_OK) return st;
+  const size_t e = type_size(d.type), de = type_size(d.dt_type);
+  const long long xw = static_cast<long long>(d.heads) * d.width, bw = static_cast<long long>(d.groups) * d.states;
+  if (A == nullptr || d_A == nullptr || workspace == nullptr) return MAMBA2_SCAN_ENULL;
+  const mamba2_rows* wide[4] = {&x, &d_y, &d_x, nullptr};
+  for (int i = 0; wide[i] != nullptr; ++i)
+    if ((st = check_vec_rows(*wide[i], q, xw, e)) != MAMBA2_SCAN_OK) return st;
+  const mamba2_rows* shared[5] = {&B, &C, &d_B, &d_C, nullptr};
+  for (int i = 0; shared[i] != nullptr; ++i)
+    if ((st = check_vec_rows(*shared[i], q, bw, e)) != MAMBA2_SCAN_OK) return st;
+  if ((st = check_rows(dt, q, d.heads, de)) != MAMBA2_SCAN_OK ||
+      (st = check_rows(d_dt, q, d.heads, de)) != MAMBA2_SCAN_OK)
+    return st;
+  if (workspace_bytes < c.p.total * sizeof(float)) return MAMBA2_SCAN_ESIZE;
+  if (!aligned_to(A, 4) || !aligned_to(D, 4) || !aligned_to(dt_bias, 4) || !aligned_to(initial_state, 16) ||
+      !aligned_to(d_final_state, 16) || !aligned_to(d_initial_state, 16) || !aligned_to(workspace, 16) ||
+      !aligned_to(d_A, 4) || !aligned_to(d_D, 4) || !aligned_to(d_dt_bias, 4))
+    return MAMBA2_SCAN_EALIGN;
+  if (static_cast<long long>(c.p.units) * d.heads * c.p.slices > 2147483647LL ||
+      static_cast<long long>(c.p.steps) * d.groups * c.p.splits > 2147483647LL || q.batch > 32767)
+    return MAMBA2_SCAN_EBADDIM;
+
+  SsmArgs& a = c.ba.a;
+  a.q = q;
+  a.x = x;
+  a.dt = dt;
+  a.B = B;
+  a.C = C;
+  a.A = A;
+  a.D = D;
+  a.bias = dt_bias;
+  a.heads = d.heads;
+  a.width = d.width;
+  a.ratio = d.heads / d.groups;
+  a.states = d.states;
+  a.softplus = d.softplus;
+  a.dt_bf16 = d.dt_type == MAMBA2_BF16;
+  a.slices = c.p.slices;
+  a.seg = c.p.seg;
+  a.units = c.p.units;
+
+  float* w = static_cast<float*>(workspace);
+  const auto take = [&w](size_t n) {
+    float* p = n > 0 ? w : nullptr;
+    w += n;
+    return p;
+  };
+  c.f.v = x;
+  c.f.m = B;
+  c.f.first = initial_state;
+  c.f.keep = take(c.p.keep);
+  c.f.seg_state = take(c.p.seg_state);
+  c.f.seg_decay = take(c.p.seg_decay);
+  c.r.v = d_y;
+  c.r.m = C;
+  c.r.first = d_final_state;
+  c.r.last = d_initial_state;
+  c.r.keep = take(c.p.keep);
+  c.r.seg_state = take(c.p.seg_state);
+  c.r.seg_decay = take(c.p.seg_decay);
+  c.r.rev = 1;
+  c.ba.part_b = take(c.p.part_bc);
+  c.ba.part_c = take(c.p.part_bc);
+  c.ba.part = take(c.p.part);
+  c.ba.d_y = d_y;
+  c.ba.d_x = d_x;
+  c.ba.d_dt = d_dt;
+  c.ba.d_B = d_B;
+  c.ba.d_C = d_C;
+  c.ba.keep_s = c.f.keep;
+  c.ba.keep_g = c.r.keep;
+  c.ba.rows = c.p.rows;
+  c.ba.steps = c.p.steps;
+  c.ba.groups = d.groups;
+  c.ba.splits = c.p.splits;
+  c.ba.run = c.p.run;
+  c.d_A = d_A;
+  c.d_D = d_D;
+  c.d_bias = d_dt_bias;
+  c.s = static_cast<hipStream_t>(stream);
+  return d.type == MAMBA2_BF16 ? launch_bwd_states<bf16>(c) : launch_bwd_states<float>(c);
+}
+
+}  // extern "C"

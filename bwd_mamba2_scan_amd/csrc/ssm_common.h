@@ -1,0 +1,480 @@
+// Shared by the selective scan's kernels: matrix fragments of both element
+// types, LDS tiles, the per-chunk decay arrays, and the call's arguments.
+//
+// The scan is computed in chunks.  With l_t = d_t A log2(e) and c_t the sum of
+// l over the chunk up to t, and S the state before the chunk,
+//   y_t   = 2^c_t S^T C_t + sum_{s <= t} (C_t . B_s) 2^(c_t - c_s) d_s x_s
+//   S_end = 2^c_end S + sum_s 2^(c_end - c_s) d_s B_s x_s^T
+// so everything but the elementwise decays is a matrix product.
+#pragma once
+
+#include "layer_common.h"
+
+namespace ssm {
+
+using namespace layer;
+
+constexpr int kTok = 64;        // tokens per step of a kernel: one lane each in the decay scan
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMaxDim = 128;    // largest width and number of states
+
+struct SsmArgs {
+  mamba2_seqs q;
+  mamba2_rows x, dt, B, C, y;
+  const float* A;
+  const float* D;
+  const float* bias;
+  const float* initial;    // [batch][heads][states][width]
+  float* final_state;
+  int heads, width, ratio, states;
+  int slices;              // work-groups per head: slices of its width
+  int softplus, dt_bf16;
+  int seg;                 // tokens per segment (a multiple of kTok)
+  int units;
+};
+
+// A 16 x 32 (or 32 x 16) matrix operand: lane l holds row (column) l & 15 and
+// eight of the 32 k positions.  Which position of the sum sits in which slot
+// does not matter as long as both operands agree, so there are two orders:
+//   natural: slot j of lane group g = l >> 4 is k = 8 g + j
+//   result:  slot j is k = 4 g + j (j < 4) and 16 + 4 g + j - 4: the order in
+//            which two stacked 16 x 16 results hold their rows, so a result
+//            becomes an operand without leaving its lane.
+template <class T>
+struct Frag;
+template <>
+struct Frag<bf16> {
+  v8bf v;
+};
+template <>
+struct Frag<float> {
+  v4f v[2];
+};
+
+// acc[m][n] += sum_k a[m][k] b[k][n]; lane l gets column l & 15, rows 4 g + i.
+// bf16: one matrix instruction over the 32 k positions.  fp32: eight over 4.
+__device__ __forceinline__ void mma(v4f& acc, const Frag<bf16>& a, const Frag<bf16>& b) {
+  acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, acc, 0, 0, 0);
+}
+__device__ __forceinline__ void mma(v4f& acc, const Frag<float>& a, const Frag<float>& b) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[h][j], b.v[h][j], acc, 0, 0, 0);
+}
+
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+
+// LDS row stride of `n` columns: 16 bytes of padding spread neighbouring rows
+// over the banks and keep them 16-byte aligned.
+template <class T>
+constexpr int stride_of(int n) {
+  return n + 16 / static_cast<int>(sizeof(T));
+}
+
+// Operand whose row (column) index is an LDS row, k along the row: natural order.
+__device__ __forceinline__ Frag<bf16> frag_row(const bf16* p, int ld, int row, int k0) {
+  const int l = threadIdx.x & 63;
+  return {*reinterpret_cast<const v8bf*>(p + (row + (l & 15)) * ld + k0 + 8 * (l >> 4))};
+}
+__device__ __forceinline__ Frag<float> frag_row(const float* p, int ld, int row, int k0) {
+  const int l = threadIdx.x & 63;
+  const v4f* r = reinterpret_cast<const v4f*>(p + (row + (l & 15)) * ld + k0 + 8 * (l >> 4));
+  return {{r[0], r[1]}};
+}
+// The same in result order.
+__device__ __forceinline__ Frag<bf16> frag_row_result(const bf16* p, int ld, int row, int k0) {
+  const int l = threadIdx.x & 63;
+  const bf16* r = p + (row + (l & 15)) * ld + k0 + 4 * (l >> 4);
+  const v4bf a = *reinterpret_cast<const v4bf*>(r);
+  const v4bf b = *reinterpret_cast<const v4bf*>(r + 16);
+  return {__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7)};
+}
+__device__ __forceinline__ Frag<float> frag_row_result(const float* p, int ld, int row, int k0) {
+  const int l = threadIdx.x & 63;
+  const float* r = p + (row + (l & 15)) * ld + k0 + 4 * (l >> 4);
+  return {{*reinterpret_cast<const v4f*>(r), *reinterpret_cast<const v4f*>(r + 16)}};
+}
+// Operand whose k runs over LDS rows and whose row (column) index is an LDS
+// column: natural order.  bf16: the transposing LDS read hands lane i of 16
+// lanes column i of the 4 x 16 block whose rows the lanes address in fours.
+__device__ __forceinline__ v4s read_tr(const bf16* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (__attribute__((address_space(3))) v4s*)(const_cast<bf16*>(p)));
+}
+__device__ __forceinline__ Frag<bf16> frag_col(const bf16* p, int ld, int k0, int col) {
+  const int l = threadIdx.x & 63;
+  const bf16* r = p + (k0 + 8 * (l >> 4) + ((l & 15) >> 2)) * ld + col + 4 * (l & 3);
+  const v4s a = read_tr(r), b = read_tr(r + 4 * ld);
+  typedef short v8s __attribute__((ext_vector_type(8)));
+  const v8s v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  return {__builtin_bit_cast(v8bf, v)};
+}
+__device__ __forceinline__ Frag<float> frag_col(const float* p, int ld, int k0, int col) {
+  const int l = threadIdx.x & 63;
+  const float* r = p + (k0 + 8 * (l >> 4)) * ld + col + (l & 15);
+  Frag<float> f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f.v[j >> 2][j & 3] = r[j * ld];
+  return f;
+}
+
+// The same in result order.
+__device__ __forceinline__ Frag<bf16> frag_col_result(const bf16* p, int ld, int k0, int col) {
+  const int l = threadIdx.x & 63;
+  const bf16* r = p + (k0 + 4 * (l >> 4) + ((l & 15) >> 2)) * ld + col + 4 * (l & 3);
+  const v4s a = read_tr(r), b = read_tr(r + 16 * ld);
+  typedef short v8s __attribute__((ext_vector_type(8)));
+  const v8s v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  return {__builtin_bit_cast(v8bf, v)};
+}
+__device__ __forceinline__ Frag<float> frag_col_result(const float* p, int ld, int k0, int col) {
+  const int l = threadIdx.x & 63;
+  const float* r = p + (k0 + 4 * (l >> 4)) * ld + col + (l & 15);
+  Frag<float> f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f.v[j >> 2][j & 3] = r[((j >> 2) * 16 + (j & 3)) * ld];
+  return f;
+}
+
+// Eight fp32 values as an operand.  bf16 keeps 8 of their bits; the remainder
+// rounded the same way (`rest`) brings a product to 16.
+template <class T>
+__device__ __forceinline__ Frag<T> frag_of(const float (&v)[8], Frag<T>* rest);
+template <>
+__device__ __forceinline__ Frag<bf16> frag_of<bf16>(const float (&v)[8], Frag<bf16>* rest) {
+  Frag<bf16> f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f.v[j] = static_cast<bf16>(v[j]);
+  if (rest != nullptr) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rest->v[j] = static_cast<bf16>(v[j] - static_cast<float>(f.v[j]));
+  }
+  return f;
+}
+template <>
+__device__ __forceinline__ Frag<float> frag_of<float>(const float (&v)[8], Frag<float>*) {
+  return {{{v[0], v[1], v[2], v[3]}, {v[4], v[5], v[6], v[7]}}};
+}
+__device__ __forceinline__ float frag_get(const Frag<bf16>& f, int j) { return static_cast<float>(f.v[j]); }
+__device__ __forceinline__ float frag_get(const Frag<float>& f, int j) { return f.v[j >> 2][j & 3]; }
+
+// ------------------------------------------------------------------- tiles
+// A tile of R rows (tokens) by C columns of a token-major tensor, moved by
+// THREADS threads in 16-byte vectors: loads() issues the global loads,
+// stores() puts them into LDS.  Rows from `rows` on and columns from `cols`
+// on are zero.
+template <class T, int R, int C, int THREADS>
+struct Tile {
+  static constexpr int kVec = Vec<T>::n;
+  static constexpr int kPerRow = C / kVec;
+  static constexpr int kN = (R * kPerRow + THREADS - 1) / THREADS;
+  typename Vec<T>::type v[kN];
+
+  __device__ __forceinline__ void load(const T* p, long stride, int rows, int cols, int tid) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int e = tid + i * THREADS;
+      const int r = e / kPerRow, c = e % kPerRow * kVec;
+      if (r < rows && c < cols) {
+        v[i] = *reinterpret_cast<const typename Vec<T>::type*>(p + r * stride + c);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) v[i][j] = static_cast<T>(0.0f);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* lds, int ld, int tid) const {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int e = tid + i * THREADS;
+      const int r = e / kPerRow, c = e % kPerRow * kVec;
+      if (R * kPerRow % THREADS == 0 || r < R) *reinterpret_cast<typename Vec<T>::type*>(lds + r * ld + c) = v[i];
+    }
+  }
+};
+
+// ------------------------------------------------------------------ decays
+// v + the lane's DPP neighbour, where the DPP control reaches one (else v).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v) {
+  const long b = __builtin_bit_cast(long, v);
+  const int lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, ROWS, 0xf, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, ROWS, 0xf, false);
+  return v + __builtin_bit_cast(double, (static_cast<long>(hi) << 32) | static_cast<unsigned>(lo));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+  const int n = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false);
+  return v + __builtin_bit_cast(float, n);
+}
+// The sum over each 16 lanes, in all of them.
+__device__ __forceinline__ float sum16(float v) {
+  v = dpp_add<0x128, 0xf>(v);  // row_ror:8
+  v = dpp_add<0x124, 0xf>(v);  // row_ror:4
+  v = dpp_add<0x122, 0xf>(v);  // row_ror:2
+  return dpp_add<0x121, 0xf>(v);
+}
+__device__ __forceinline__ float sum64(float v) {
+  v = sum16(v);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+// Inclusive prefix sum over the 64 lanes.
+template <class F>
+__device__ __forceinline__ F scan64(F v) {
+  v = dpp_add<0x111, 0xf>(v);  // row_shr:1
+  v = dpp_add<0x112, 0xf>(v);  // row_shr:2
+  v = dpp_add<0x114, 0xf>(v);  // row_shr:4
+  v = dpp_add<0x118, 0xf>(v);  // row_shr:8
+  v = dpp_add<0x142, 0xa>(v);  // row_bcast:15 into rows 1 and 3
+  v = dpp_add<0x143, 0xc>(v);  // row_bcast:31 into rows 2 and 3
+  return v;
+}
+
+__device__ __forceinline__ float exp2_of(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// 2^v for a 64-bit v: the whole part is an exact scaling, so the result has
+// fp32's full precision however large |v| is.
+__device__ __forceinline__ float exp2_of(double v) {
+  const double r = rint(v);
+  return exp2_of(static_cast<float>(v - r)) * exp2_of(static_cast<float>(r));
+}
+
+__device__ __forceinline__ float raw_step(const SsmArgs& a, const mamba2_rows& r, const void* base, int t, int h) {
+  const long i = t * r.row_stride + h;
+  return a.dt_bf16 ? static_cast<float>(static_cast<const bf16*>(base)[i]) : static_cast<const float*>(base)[i];
+}
+// softplus(v) = log(1 + e^v), whole for large v and to full precision for
+// very negative ones.
+__device__ __forceinline__ float step_of(const SsmArgs& a, float raw, float bias) {
+  const float v = raw + bias;
+  if (!a.softplus) return v;
+  return v > 20.0f ? v : log1pf(expf(v));
+}
+
+// The decays of a step of kTok tokens.  Sums of log2 decays are formed in 64
+// bits and kept as two floats: a difference of two of them is needed to
+// about 1e-7, and they reach into the thousands.
+struct Decays {
+  float hi[kTok], lo[kTok];   // c_t
+  float d[kTok];              // d_t; 0 behind the last token
+  float from[kTok];           // 2^c_t
+  float left[kTok];           // 2^(c_end - c_t)
+  float to[kTok];             // 2^(c_end - c_t) d_t
+  float total;                // 2^c_end
+  double end;                 // c_end
+};
+
+// One wave; lane t has token t.  A token whose decay underflows any fp32
+// (2^-1100) is held there, so that later differences keep their bits.
+__device__ __forceinline__ void make_decays(Decays& dc, float d, float A) {
+  const int t = threadIdx.x & 63;
+  const double l = fmax(static_cast<double>(d) * static_cast<double>(A) * 1.4426950408889634074, -1100.0);
+  const double c = scan64(l);
+  const double end = __shfl(c, 63);
+  const float hi = static_cast<float>(c);
+  dc.hi[t] = hi;
+  dc.lo[t] = static_cast<float>(c - hi);
+  dc.d[t] = d;
+  dc.from[t] = exp2_of(c);
+  const float left = exp2_of(end - c);
+  dc.left[t] = left;
+  dc.to[t] = left * d;
+  if (t == 63) {
+    dc.total = exp2_of(c);
+    dc.end = c;
+  }
+}
+
+// Dispatch is round-robin over the 8 XCDs: gives each XCD a contiguous range
+// of the work, so that the heads that share B and C share an L2.
+__device__ __forceinline__ int xcd_contiguous(int block, int total) {
+  const int xcd = block & 7, k = block >> 3, q = total >> 3, r = total & 7;
+  return xcd * q + min(xcd, r) + k;
+}
+
+// ------------------------------------------------------------------- walk
+// One pass of a state over the tokens: forward,
+//   S <- 2^c_end S + sum_s 2^(c_end - c_s) d_s B_s x_s^T      per step,
+// or in reverse, for the gradient G of the state,
+//   G <- 2^c_end G + sum_t 2^c_t C_t d_y_t^T.
+struct Walk {
+  mamba2_rows v, m;        // x and B, or d_y and C
+  const float* first;      // the state the pass starts from, per sequence (NULL: 0)
+  float* last;             // where it ends, per sequence (NULL: not kept)
+  float* seg_state;        // [units][heads][states][width]: the state each segment starts from
+  float* seg_decay;        // [units][heads]: each segment's decay
+  float* keep;             // [steps][heads][states][width]: the state each step starts from
+  int rev;
+};
+
+template <int NB>
+__device__ __forceinline__ void load_state(v4f (&st)[2 * NB], const float* p, int width, int states, int col,
+                                           bool live) {
+  const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int n = 0; n < 2 * NB; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = n * 16 + 4 * g + i;
+      st[n][i] = (p != nullptr && live && r < states) ? p[static_cast<long>(r) * width + col] : 0.0f;
+    }
+}
+template <int NB>
+__device__ __forceinline__ void save_state(const v4f (&st)[2 * NB], float* p, int width, int states, int col,
+                                           bool live) {
+  const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int n = 0; n < 2 * NB; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = n * 16 + 4 * g + i;
+      if (live && r < states) p[static_cast<long>(r) * width + col] = st[n][i];
+    }
+}
+
+// S = total S + M^T (coef_s v_s) for a wave's 16 columns; vf holds v.  With
+// bf16 the scaled v is kept in two terms: M is exact, so the state's sums
+// carry 16 bits of each product instead of 8.
+template <class T, int NB>
+__device__ __forceinline__ void advance_state(v4f (&st)[2 * NB], float total, const float* coef, const T* m, int ldn,
+                                              const Frag<T> (&vf)[2]) {
+  const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int n = 0; n < 2 * NB; ++n) st[n] *= total;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = frag_get(vf[k], j) * coef[k * 32 + 8 * g + j];
+    Frag<T> lo;
+    const Frag<T> hi = frag_of<T>(v, &lo);
+#pragma unroll
+    for (int n = 0; n < 2 * NB; ++n) {
+      const Frag<T> mf = frag_col(m, ldn, k * 32, n * 16);
+      mma(st[n], mf, hi);
+      if constexpr (sizeof(T) == 2) mma(st[n], mf, lo);
+    }
+  }
+}
+
+template <class T, int NB, int NW>
+struct WalkLds {
+  static constexpr int ldn = stride_of<T>(NB * 32);
+  static constexpr int ldp = stride_of<T>(NW * 16);
+  alignas(16) T m[kTok * ldn];
+  alignas(16) T v[kTok * ldp];
+  alignas(16) Decays dc;
+};
+
+// KEEP false: the summary of a segment that another follows, from a zero
+// state, into that segment's place.  KEEP true: the walk itself, from the
+// states the carry left, writing every step's starting state.
+template <class T, int NB, int NW, bool KEEP>
+__device__ __forceinline__ void walk(const SsmArgs& a, const Walk& w, WalkLds<T, NB, NW>& s) {
+  typedef WalkLds<T, NB, NW> L;
+  constexpr int kThreads = NW * 64;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int work = xcd_contiguous(blockIdx.x, gridDim.x);
+  const int per = a.heads * a.slices;
+  const int unit = work / per;
+  const int h = work % per / a.slices;
+  const int slice = work % a.slices;
+  const Unit u = locate(a.q, unit, a.seg);
+  if (!u.live) return;
+  const bool first = w.rev ? u.t0 + static_cast<long>(a.seg) >= u.len : u.index == 0;
+  const bool last = w.rev ? u.index == 0 : u.t0 + static_cast<long>(a.seg) >= u.len;
+  if (!KEEP && last) return;
+  const bool packed = a.q.offsets != nullptr;
+  const int p0 = slice * NW * 16;
+  const int cols = min(a.width - p0, NW * 16);
+  const int col = p0 + wave * 16 + (lane & 15);
+  const bool live = col < a.width;
+  const long head = static_cast<long>(a.states) * a.width;
+  const T* vp = seq_ptr<const T>(w.v, u.seq, u.row0, packed) + h * a.width + p0;
+  const T* mp = seq_ptr<const T>(w.m, u.seq, u.row0, packed) + h / a.ratio * a.states;
+  const void* dtp = a.dt_bf16 ? static_cast<const void*>(seq_ptr<const bf16>(a.dt, u.seq, u.row0, packed))
+                              : static_cast<const void*>(seq_ptr<const float>(a.dt, u.seq, u.row0, packed));
+  const float A = a.A[h], bias = a.bias != nullptr ? a.bias[h] : 0.0f;
+  const long at = static_cast<long>(unit) * a.heads + h;
+  const long of_seq = (static_cast<long>(u.seq) * a.heads + h) * head;
+  v4f st[2 * NB];
+  {
+    const float* from = nullptr;
+    if (KEEP) from = first ? (w.first == nullptr ? nullptr : w.first + of_seq) : w.seg_state + at * head;
+    load_state<NB>(st, from, a.width, a.states, col, live);
+  }
+  double decay = 0.0;
+  Tile<T, kTok, NB * 32, kThreads> tm;
+  Tile<T, kTok, NW * 16, kThreads> tv;
+  float raw = 0.0f;
+  const int end = min(u.t0 + a.seg, u.len);
+  const int steps = (end - u.t0 + kTok - 1) / kTok;
+  const auto token = [&](int i) { return u.t0 + (w.rev ? steps - 1 - i : i) * kTok; };
+  const auto fetch = [&](int t) {
+    const int rows = end - t;
+    tm.load(mp + t * w.m.row_stride, w.m.row_stride, rows, a.states, tid);
+    tv.load(vp + t * w.v.row_stride, w.v.row_stride, rows, cols, tid);
+    if (wave == 0 && lane < rows) raw = raw_step(a, a.dt, dtp, t + lane, h);
+  };
+  if (steps > 0) fetch(token(0));
+  for (int i = 0; i < steps; ++i) {
+    const int t = token(i);
+    __syncthreads();
+    tm.store(s.m, L::ldn, tid);
+    tv.store(s.v, L::ldp, tid);
+    if (wave == 0) make_decays(s.dc, lane < end - t ? step_of(a, raw, bias) : 0.0f, A);
+    __syncthreads();
+    if (i + 1 < steps) fetch(token(i + 1));
+    if (KEEP) {
+      const long step = static_cast<long>(unit_base(a.q, u.seq, kTok)) + t / kTok;
+      save_state<NB>(st, w.keep + (step * a.heads + h) * head, a.width, a.states, col, live);
+    }
+    Frag<T> vf[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) vf[k] = frag_col(s.v, L::ldp, k * 32, wave * 16);
+    advance_state<T, NB>(st, s.dc.total, w.rev ? s.dc.from : s.dc.to, s.m, L::ldn, vf);
+    if (!KEEP) decay += s.dc.end;
+  }
+  if (KEEP) {
+    if (last && w.last != nullptr) save_state<NB>(st, w.last + of_seq, a.width, a.states, col, live);
+  } else {
+    const long next = at + (w.rev ? -a.heads : a.heads);
+    save_state<NB>(st, w.seg_state + next * head, a.width, a.states, col, live);
+    if (tid == 0 && slice == 0) w.seg_decay[at] = exp2_of(decay);
+  }
+}
+
+// Carry: turns the segments' own contributions into the state each segment
+// starts from.  One thread per four elements of a sequence's head.
+__device__ __forceinline__ void carry(const SsmArgs& a, const Walk& w, int seq) {
+  const long head = static_cast<long>(a.states) * a.width;
+  const long e = (static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x) * 4;
+  if (e >= head) return;
+  const int h = blockIdx.y;
+  long row0;
+  int len;
+  seq_rows(a.q, seq, &row0, &len);
+  const int n = units_of(len, a.seg);
+  const long base = unit_base(a.q, seq, a.seg);
+  v4f run = {0, 0, 0, 0};
+  if (w.first != nullptr)
+    run = *reinterpret_cast<const v4f*>(w.first + (static_cast<long>(seq) * a.heads + h) * head + e);
+  const int d = w.rev ? -1 : 1;
+  for (int i = w.rev ? n - 2 : 1; i >= 0 && i < n; i += d) {
+    const long at = (base + i) * a.heads + h;
+    v4f* p = reinterpret_cast<v4f*>(w.seg_state + at * head + e);
+    run = run * w.seg_decay[at - d * a.heads] + *p;
+    *p = run;
+  }
+}
+
+// Host side, in ssm.hip.
+int check_dims(const mamba2_seqs& q, const mamba2_ssm_dims& d);
+int check_vec_rows(const mamba2_rows& r, const mamba2_seqs& q, long long width, size_t elem);
+int waves_of(int width);
+int segment_tokens(const mamba2_seqs& q, const mamba2_ssm_dims& d);
+
+}  // namespace ssm

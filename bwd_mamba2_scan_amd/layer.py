@@ -1,0 +1,563 @@
+"""Python binding of the selective layer's operators (include/mamba2_layer.h).
+
+    conv_fwd(x, weight, bias)                  -> (y, final_state)
+    conv_bwd(x, weight, d_y, bias)             -> dict(d_x, d_weight, d_bias[, d_initial_state])
+    conv_step(x, weight, state, bias)          -> y; the state moves on in place
+    ssm_fwd(x, dt, A, B, C, D=, dt_bias=)      -> (y, final_state)
+    ssm_bwd(x, dt, A, B, C, d_y, ...)          -> dict(d_x, d_dt, d_A, d_B, d_C[, d_D, d_dt_bias, d_initial_state])
+    ssm_step(x, dt, A, B, C, state, ...)       -> y; the state moves on in place
+    grad_norm(grads)                           -> norm
+    clip_grads(grads, max_norm)                -> norm; the gradients are scaled in place
+
+Token-major tensors are [batch, length, ...] or, with `offsets`, packed as
+[rows, ...] with sequence s in rows offsets[s] .. offsets[s + 1] - 1.  Only
+their inner dimensions need be contiguous, so slices of a wider projection go
+in as they are.  Work runs on `stream` (default: the current stream of the
+tensors' device); outputs and workspaces that a call allocates belong to it.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+_F32, _BF16 = 0, 1
+
+_c_int, _c_size, _c_vp, _c_ll = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_longlong
+
+
+class Seqs(ctypes.Structure):
+    """mamba2_seqs"""
+    _fields_ = [("batch", _c_int), ("length", _c_int), ("offsets", _c_vp)]
+
+
+class Rows(ctypes.Structure):
+    """mamba2_rows"""
+    _fields_ = [("data", _c_vp), ("batch_stride", _c_ll), ("row_stride", _c_ll)]
+
+
+class SsmDims(ctypes.Structure):
+    """mamba2_ssm_dims"""
+    _fields_ = [(n, _c_int) for n in ("type", "dt_type", "heads", "width", "groups", "states", "softplus")]
+
+
+class Grad(ctypes.Structure):
+    """mamba2_grad"""
+    _fields_ = [("grad", _c_vp), ("out", _c_vp), ("numel", _c_ll), ("type", _c_int)]
+
+
+SIGNATURES = {
+    "mamba2_conv_fwd": (_c_int, [_c_int, Seqs, _c_int, _c_int, _c_int, Rows, _c_vp, _c_vp, _c_vp, Rows, _c_vp, _c_vp]),
+    "mamba2_conv_bwd_workspace_bytes": (_c_size, [Seqs, _c_int, _c_int]),
+    "mamba2_conv_bwd": (_c_int, [_c_int, Seqs, _c_int, _c_int, _c_int, Rows, _c_vp, _c_vp, _c_vp, Rows, _c_vp, Rows,
+                                 _c_vp, _c_vp, _c_vp, _c_vp, _c_size, _c_vp]),
+    "mamba2_conv_step": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, Rows, _c_vp, _c_vp, _c_vp, Rows, _c_vp,
+                                  _c_vp]),
+    "mamba2_ssm_fwd_workspace_bytes": (_c_size, [Seqs, SsmDims]),
+    "mamba2_ssm_fwd": (_c_int, [Seqs, SsmDims, Rows, Rows, _c_vp, Rows, Rows, _c_vp, _c_vp, _c_vp, Rows, _c_vp, _c_vp,
+                                _c_size, _c_vp]),
+    "mamba2_ssm_bwd_workspace_bytes": (_c_size, [Seqs, SsmDims]),
+    "mamba2_ssm_bwd": (_c_int, [Seqs, SsmDims, Rows, Rows, _c_vp, Rows, Rows, _c_vp, _c_vp, _c_vp, Rows, _c_vp, Rows,
+                                Rows, _c_vp, Rows, Rows, _c_vp, _c_vp, _c_vp, _c_vp, _c_size, _c_vp]),
+    "mamba2_ssm_step": (_c_int, [_c_int, SsmDims, Rows, Rows, _c_vp, Rows, Rows, _c_vp, _c_vp, _c_vp, Rows, _c_vp,
+                                 _c_vp]),
+    "mamba2_grad_workspace_bytes": (_c_size, [_c_vp, _c_int]),
+    "mamba2_grad_norm": (_c_int, [_c_vp, _c_int, _c_vp, _c_vp, _c_size, _c_vp]),
+    "mamba2_clip_grads": (_c_int, [_c_vp, _c_int, ctypes.c_float, _c_vp, _c_vp, _c_size, _c_vp]),
+}
+
+
+def _pkg():
+    import bwd_mamba2_scan_amd as m2
+    return m2
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+class _On:
+    """The tensors' device and the stream of a call, made current for its allocations and launches."""
+
+    def __init__(self, dev, stream):
+        torch = _torch()
+        self._guards = []
+        if torch.cuda.current_device() != dev.index:
+            self._guards.append(torch.cuda.device(dev))
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+            self._guards.append(torch.cuda.stream(stream))
+        self._dev = dev
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+        return _torch().cuda.current_stream(self._dev).cuda_stream
+
+    def __exit__(self, *exc):
+        for g in reversed(self._guards):
+            g.__exit__(*exc)
+        return False
+
+
+def _type(t, name):
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return _BF16
+    if t.dtype == torch.float32:
+        return _F32
+    raise TypeError(f"{name} must be float32 or bfloat16 (got {t.dtype})")
+
+
+def _gpu(t, name, dev=None):
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _dense(t, name, shape, dtype, dev):
+    """A contiguous tensor, or None."""
+    if t is None:
+        return None
+    _gpu(t, name, dev)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, name, lead, inner, dtype, dev):
+    """A token-major tensor: contiguous inner dimensions, free outer strides."""
+    _gpu(t, name, dev)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if tuple(t.shape) != lead + inner:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {lead + inner}")
+    strides = t.stride()
+    want = 1
+    for size, stride in zip(reversed(inner), reversed(strides)):
+        if size != 1 and stride != want:
+            raise ValueError(f"{name}: the inner dimensions {inner} must be contiguous (strides {strides})")
+        want *= size
+    if len(lead) == 2:
+        return Rows(t.data_ptr(), strides[0], strides[1])
+    return Rows(t.data_ptr(), 0, strides[0])
+
+
+def _seqs(x, offsets, inner_dims, dev):
+    """(mamba2_seqs, the leading shape, the number of sequences)"""
+    torch = _torch()
+    if offsets is None:
+        if x.dim() != 2 + inner_dims:
+            raise ValueError(f"x must have {2 + inner_dims} dimensions (got {x.dim()}); packed rows need offsets")
+        batch, length = int(x.shape[0]), int(x.shape[1])
+        return Seqs(batch, length, None), (batch, length), batch
+    if x.dim() != 1 + inner_dims:
+        raise ValueError(f"with offsets x must have {1 + inner_dims} dimensions (got {x.dim()})")
+    _gpu(offsets, "offsets", dev)
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous int32 vector of at least two elements")
+    batch = offsets.numel() - 1
+    return Seqs(batch, int(x.shape[0]), offsets.data_ptr()), (int(x.shape[0]),), batch
+
+
+def _span(t):
+    """(first byte, byte behind the last, (row stride, column window) of a row slice or None)"""
+    e = t.element_size()
+    lo = t.data_ptr()
+    hi = lo + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * e
+    return lo, hi
+
+
+def _apart(outs, ins):
+    """Refuses outputs that a caller gave and that overlap an input or one another.
+
+    Slices of one wide row-major tensor interleave without overlapping: equal
+    row strides and disjoint windows within the row are told apart.
+    """
+    outs = [(n, t) for n, t in outs if t is not None and t.numel()]
+    if not outs:
+        return
+    every = outs + [(n, t) for n, t in ins if t is not None and t.numel()]
+    for i, (n, t) in enumerate(outs):
+        lo, hi = _span(t)
+        for m, o in every[i + 1:]:
+            a, b = _span(o)
+            if hi <= a or b <= lo:
+                continue
+            if not _interleaved(t, o):
+                raise ValueError(f"{n} overlaps {m}")
+
+
+def _interleaved(t, o):
+    def window(v):  # (row stride in bytes, width of a row in bytes)
+        sizes, strides = list(v.shape), list(v.stride())
+        width = 1
+        while sizes and (sizes[-1] == 1 or strides[-1] == width):
+            width *= sizes.pop()
+            strides.pop()
+        return [s * v.element_size() for n, s in zip(sizes, strides) if n > 1], width * v.element_size()
+
+    (st, wt), (so, wo) = window(t), window(o)
+    if not st or not so or st[-1] != so[-1] or any(s % st[-1] for s in st + so):
+        return False
+    row = st[-1]
+    at, ao = t.data_ptr() % row, o.data_ptr() % row
+    gap = (ao - at) % row
+    return wt <= gap and gap + wo <= row
+
+
+def _empty(shape, dtype, dev):
+    return _torch().empty(shape, dtype=dtype, device=dev)
+
+
+# -------------------------------------------------------------- convolution
+def _conv_dims(x, weight, dev):
+    if weight.dim() != 2:
+        raise ValueError("weight must be [channels, taps]")
+    channels, taps = (int(v) for v in weight.shape)
+    w = _dense(weight, "weight", (channels, taps), _torch().float32, dev)
+    return channels, taps, w
+
+
+def conv_fwd(x, weight, bias=None, *, silu=True, initial_state=None, offsets=None, want_final_state=False, y=None,
+             final_state=None, stream=None):
+    """Short causal depthwise convolution: y_t = f(bias + sum_k weight[:, k] x_{t-W+1+k}), f = SiLU or the identity.
+
+    x [batch, length, channels] (or [rows, channels] with offsets), float32 or
+    bfloat16; weight [channels, W], W = 2, 3 or 4, and bias [channels],
+    float32.  initial_state [batch, W - 1, channels] holds the inputs before
+    the first token (default: zeros).  Returns (y, the last W - 1 inputs, or
+    None unless want_final_state or final_state is given).
+    """
+    m2 = _pkg()
+    torch = _torch()
+    _gpu(x, "x")
+    dev = x.device
+    typ = _type(x, "x")
+    seqs, lead, batch = _seqs(x, offsets, 1, dev)
+    channels, taps, w = _conv_dims(x, weight, dev)
+    rx = _rows(x, "x", lead, (channels,), x.dtype, dev)
+    b = _dense(bias, "bias", (channels,), torch.float32, dev)
+    s0 = _dense(initial_state, "initial_state", (batch, taps - 1, channels), x.dtype, dev)
+    _apart((("y", y), ("final_state", final_state)),
+           (("x", x), ("weight", weight), ("bias", bias), ("initial_state", initial_state)))
+    with _On(dev, stream) as s:
+        if y is None:
+            y = _empty(lead + (channels,), x.dtype, dev)
+        if final_state is None and want_final_state:
+            final_state = _empty((batch, taps - 1, channels), x.dtype, dev)
+        st = m2.lib().mamba2_conv_fwd(typ, seqs, channels, taps, int(bool(silu)), rx, w, b, s0,
+                                      _rows(y, "y", lead, (channels,), x.dtype, dev),
+                                      _dense(final_state, "final_state", (batch, taps - 1, channels), x.dtype, dev), s)
+    m2._raise(st, "mamba2_conv_fwd")
+    return y, final_state
+
+
+def conv_bwd(x, weight, d_y, bias=None, *, silu=True, initial_state=None, d_final_state=None, offsets=None, out=None,
+             workspace=None, stream=None):
+    """Gradients of conv_fwd for dL/dy = d_y (and dL/dfinal_state): dict with d_x, d_weight, d_bias (None without
+    bias) and d_initial_state (None without initial_state).  `out` may hold some of these tensors.
+    """
+    m2 = _pkg()
+    torch = _torch()
+    _gpu(x, "x")
+    dev = x.device
+    typ = _type(x, "x")
+    seqs, lead, batch = _seqs(x, offsets, 1, dev)
+    channels, taps, w = _conv_dims(x, weight, dev)
+    rx = _rows(x, "x", lead, (channels,), x.dtype, dev)
+    rg = _rows(d_y, "d_y", lead, (channels,), x.dtype, dev)
+    b = _dense(bias, "bias", (channels,), torch.float32, dev)
+    tail = (batch, taps - 1, channels)
+    s0 = _dense(initial_state, "initial_state", tail, x.dtype, dev)
+    sf = _dense(d_final_state, "d_final_state", tail, x.dtype, dev)
+    res = dict(out or {})
+    _apart(tuple(res.items()) + (("workspace", workspace),),
+           (("x", x), ("weight", weight), ("bias", bias), ("d_y", d_y), ("initial_state", initial_state),
+            ("d_final_state", d_final_state)))
+    with _On(dev, stream) as s:
+        if res.get("d_x") is None:
+            res["d_x"] = _empty(lead + (channels,), x.dtype, dev)
+        if res.get("d_weight") is None:
+            res["d_weight"] = _empty((channels, taps), torch.float32, dev)
+        for name, given, shape, dtype in (("d_bias", bias, (channels,), torch.float32),
+                                          ("d_initial_state", initial_state, tail, x.dtype)):
+            if given is None:
+                res[name] = None
+            elif res.get(name) is None:
+                res[name] = _empty(shape, dtype, dev)
+        workspace, nbytes = _workspace(workspace, m2.lib().mamba2_conv_bwd_workspace_bytes(seqs, channels, taps), dev)
+        st = m2.lib().mamba2_conv_bwd(
+            typ, seqs, channels, taps, int(bool(silu)), rx, w, b, s0, rg, sf,
+            _rows(res["d_x"], "d_x", lead, (channels,), x.dtype, dev),
+            _dense(res["d_weight"], "d_weight", (channels, taps), torch.float32, dev),
+            _dense(res["d_bias"], "d_bias", (channels,), torch.float32, dev),
+            _dense(res["d_initial_state"], "d_initial_state", tail, x.dtype, dev), _ptr(workspace), nbytes, s)
+    m2._raise(st, "mamba2_conv_bwd")
+    return res
+
+
+def _workspace(workspace, need, dev):
+    """The given workspace or a new one; (tensor or None, bytes)."""
+    torch = _torch()
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = torch.empty(-(-need // 4), dtype=torch.float32, device=dev)
+    _gpu(workspace, "workspace", dev)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def conv_step(x, weight, state, bias=None, *, silu=True, new_state=None, y=None, stream=None):
+    """One token of each sequence: x [batch, channels] -> y; state [batch, W - 1, channels] moves on in place, or
+    into new_state where that is given.
+    """
+    m2 = _pkg()
+    torch = _torch()
+    _gpu(x, "x")
+    dev = x.device
+    typ = _type(x, "x")
+    channels, taps, w = _conv_dims(x, weight, dev)
+    batch = int(x.shape[0])
+    rx = _rows(x.unsqueeze(1) if x.dim() == 2 else x, "x", (batch, 1), (channels,), x.dtype, dev)
+    tail = (batch, taps - 1, channels)
+    s0 = _dense(state, "state", tail, x.dtype, dev)
+    if s0 is None:
+        raise TypeError("state must be a torch.Tensor")
+    b = _dense(bias, "bias", (channels,), torch.float32, dev)
+    if y is not None or new_state is not None:
+        _apart((("y", y), ("new_state", None if new_state is state else new_state)),
+               (("x", x), ("weight", weight), ("bias", bias), ("state", state)))
+    s1 = s0 if new_state is None else _dense(new_state, "new_state", tail, x.dtype, dev)
+    with _On(dev, stream) as s:
+        if y is None:
+            y = _empty((batch, channels), x.dtype, dev)
+        st = m2.lib().mamba2_conv_step(typ, batch, channels, taps, int(bool(silu)), rx, w, b, s0,
+                                       _rows(y.unsqueeze(1), "y", (batch, 1), (channels,), x.dtype, dev), s1, s)
+    m2._raise(st, "mamba2_conv_step")
+    return y
+
+
+# ---------------------------------------------------------------------- scan
+def _ssm_dims(x, dt, B, softplus):
+    if B.dim() != x.dim():
+        raise ValueError("B and C must be [..., groups, states] beside x [..., heads, width]")
+    heads, width = int(x.shape[-2]), int(x.shape[-1])
+    groups, states = int(B.shape[-2]), int(B.shape[-1])
+    return SsmDims(_type(x, "x"), _type(dt, "dt"), heads, width, groups, states, int(bool(softplus)))
+
+
+def _ssm_inputs(x, dt, A, B, C, D, dt_bias, lead, d, dev):
+    f32 = _torch().float32
+    inner, shared = (d.heads, d.width), (d.groups, d.states)
+    vec = (d.heads,)
+    if A is None:
+        raise TypeError("A must be a torch.Tensor")
+    return (_rows(x, "x", lead, inner, x.dtype, dev), _rows(dt, "dt", lead, vec, dt.dtype, dev),
+            _dense(A, "A", vec, f32, dev), _rows(B, "B", lead, shared, x.dtype, dev),
+            _rows(C, "C", lead, shared, x.dtype, dev), _dense(D, "D", vec, f32, dev),
+            _dense(dt_bias, "dt_bias", vec, f32, dev))
+
+
+def ssm_fwd(x, dt, A, B, C, *, D=None, dt_bias=None, softplus=True, initial_state=None, offsets=None,
+            want_final_state=False, y=None, final_state=None, workspace=None, stream=None):
+    """Selective state space scan: S_t = exp(d_t A) S_{t-1} + d_t B_t x_t^T, y_t = S_t^T C_t + D x_t, with
+    d_t = softplus(dt_t + dt_bias) (or dt_t + dt_bias).
+
+    x [batch, length, heads, width], dt [batch, length, heads],
+    B, C [batch, length, groups, states] (with offsets: no batch axis), float32
+    or bfloat16 (x, B, C alike); A, D, dt_bias [heads] float32; heads / groups
+    neighbouring heads share a B and C.  initial_state [batch, heads, states,
+    width] float32 (default: zeros).  Returns (y, the final state, or None
+    unless want_final_state or final_state is given).
+    """
+    m2 = _pkg()
+    torch = _torch()
+    _gpu(x, "x")
+    dev = x.device
+    seqs, lead, batch = _seqs(x, offsets, 2, dev)
+    d = _ssm_dims(x, dt, B, softplus)
+    px, pdt, pA, pB, pC, pD, pbias = _ssm_inputs(x, dt, A, B, C, D, dt_bias, lead, d, dev)
+    shape = (batch, d.heads, d.states, d.width)
+    s0 = _dense(initial_state, "initial_state", shape, torch.float32, dev)
+    _apart((("y", y), ("final_state", final_state), ("workspace", workspace)),
+           (("x", x), ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("dt_bias", dt_bias),
+            ("initial_state", initial_state)))
+    with _On(dev, stream) as s:
+        if y is None:
+            y = _empty(lead + (d.heads, d.width), x.dtype, dev)
+        if final_state is None and want_final_state:
+            final_state = _empty(shape, torch.float32, dev)
+        workspace, nbytes = _workspace(workspace, m2.lib().mamba2_ssm_fwd_workspace_bytes(seqs, d), dev)
+        st = m2.lib().mamba2_ssm_fwd(seqs, d, px, pdt, pA, pB, pC, pD, pbias, s0,
+                                     _rows(y, "y", lead, (d.heads, d.width), x.dtype, dev),
+                                     _dense(final_state, "final_state", shape, torch.float32, dev), _ptr(workspace),
+                                     nbytes, s)
+    m2._raise(st, "mamba2_ssm_fwd")
+    return y, final_state
+
+
+def ssm_bwd(x, dt, A, B, C, d_y, *, D=None, dt_bias=None, softplus=True, initial_state=None, d_final_state=None,
+            offsets=None, out=None, workspace=None, stream=None):
+    """Gradients of ssm_fwd for dL/dy = d_y (and dL/dfinal_state): dict with d_x, d_dt, d_A, d_B, d_C, and d_D,
+    d_dt_bias, d_initial_state (each None where the forward had no such input).  `out` may hold some of them.
+    """
+    m2 = _pkg()
+    torch = _torch()
+    _gpu(x, "x")
+    dev = x.device
+    f32 = torch.float32
+    seqs, lead, batch = _seqs(x, offsets, 2, dev)
+    d = _ssm_dims(x, dt, B, softplus)
+    px, pdt, pA, pB, pC, pD, pbias = _ssm_inputs(x, dt, A, B, C, D, dt_bias, lead, d, dev)
+    inner, shared, vec = (d.heads, d.width), (d.groups, d.states), (d.heads,)
+    shape = (batch, d.heads, d.states, d.width)
+    pg = _rows(d_y, "d_y", lead, inner, x.dtype, dev)
+    s0 = _dense(initial_state, "initial_state", shape, f32, dev)
+    sf = _dense(d_final_state, "d_final_state", shape, f32, dev)
+    res = dict(out or {})
+    _apart(tuple(res.items()) + (("workspace", workspace),),
+           (("x", x), ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("dt_bias", dt_bias), ("d_y", d_y),
+            ("initial_state", initial_state), ("d_final_state", d_final_state)))
+    specs = {"d_x": (lead + inner, x.dtype, True), "d_dt": (lead + vec, dt.dtype, True), "d_A": (vec, f32, True),
+             "d_B": (lead + shared, x.dtype, True), "d_C": (lead + shared, x.dtype, True),
+             "d_D": (vec, f32, D is not None), "d_dt_bias": (vec, f32, dt_bias is not None),
+             "d_initial_state": (shape, f32, initial_state is not None)}
+    with _On(dev, stream) as s:
+        for name, (size, dtype, wanted) in specs.items():
+            if not wanted:
+                res[name] = None
+            elif res.get(name) is None:
+                res[name] = _empty(size, dtype, dev)
+        workspace, nbytes = _workspace(workspace, m2.lib().mamba2_ssm_bwd_workspace_bytes(seqs, d), dev)
+        st = m2.lib().mamba2_ssm_bwd(
+            seqs, d, px, pdt, pA, pB, pC, pD, pbias, s0, pg, sf, _rows(res["d_x"], "d_x", lead, inner, x.dtype, dev),
+            _rows(res["d_dt"], "d_dt", lead, vec, dt.dtype, dev), _dense(res["d_A"], "d_A", vec, f32, dev),
+            _rows(res["d_B"], "d_B", lead, shared, x.dtype, dev),
+            _rows(res["d_C"], "d_C", lead, shared, x.dtype, dev), _dense(res["d_D"], "d_D", vec, f32, dev),
+            _dense(res["d_dt_bias"], "d_dt_bias", vec, f32, dev),
+            _dense(res["d_initial_state"], "d_initial_state", shape, f32, dev), _ptr(workspace), nbytes, s)
+    m2._raise(st, "mamba2_ssm_bwd")
+    return res
+
+
+def ssm_step(x, dt, A, B, C, state, *, D=None, dt_bias=None, softplus=True, new_state=None, y=None, stream=None):
+    """One token of each sequence: x [batch, heads, width], dt [batch, heads], B, C [batch, groups, states] -> y.
+
+    state [batch, heads, states, width] float32 moves on in place, or into
+    new_state where that is given.
+    """
+    m2 = _pkg()
+    torch = _torch()
+    _gpu(x, "x")
+    if x.dim() != 3:
+        raise ValueError("x must be [batch, heads, width]")
+    dev = x.device
+    batch = int(x.shape[0])
+    d = _ssm_dims(x, dt, B, softplus)
+    px, pdt, pA, pB, pC, pD, pbias = _ssm_inputs(x, dt, A, B, C, D, dt_bias, (batch,), d, dev)
+    shape = (batch, d.heads, d.states, d.width)
+    s0 = _dense(state, "state", shape, torch.float32, dev)
+    if s0 is None:
+        raise TypeError("state must be a torch.Tensor")
+    if y is not None or new_state is not None:
+        _apart((("y", y), ("new_state", None if new_state is state else new_state)),
+               (("x", x), ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("dt_bias", dt_bias), ("state", state)))
+    s1 = s0 if new_state is None else _dense(new_state, "new_state", shape, torch.float32, dev)
+    with _On(dev, stream) as s:
+        if y is None:
+            y = _empty((batch, d.heads, d.width), x.dtype, dev)
+        py = _rows(y, "y", (batch,), (d.heads, d.width), x.dtype, dev)
+        for r in (px, pdt, pB, pC, py):  # one token per sequence: the rows are the sequences
+            r.batch_stride = r.row_stride
+        st = m2.lib().mamba2_ssm_step(batch, d, px, pdt, pA, pB, pC, pD, pbias, s0, py, s1, s)
+    m2._raise(st, "mamba2_ssm_step")
+    return y
+
+
+# ----------------------------------------------------------------- gradients
+def _grad_table(grads, out):
+    grads = list(grads)
+    if not grads:
+        raise ValueError("no gradients")
+    _gpu(grads[0], "grads[0]")
+    dev = grads[0].device
+    outs = grads if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError(f"{len(outs)} outputs for {len(grads)} gradients")
+    table = (Grad * len(grads))()
+    spans = []
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        _gpu(g, f"grads[{i}]", dev)
+        typ = _type(g, f"grads[{i}]")
+        if not g.is_contiguous():
+            raise ValueError(f"grads[{i}] must be contiguous")
+        p, n = g.data_ptr(), g.numel()
+        q = p
+        if n:
+            spans.append((p, p + n * g.element_size(), i))
+        if o is not g:
+            _gpu(o, f"out[{i}]", dev)
+            if o.dtype != g.dtype or o.shape != g.shape or not o.is_contiguous():
+                raise ValueError(f"out[{i}] must be contiguous, of the gradient's type and shape")
+            q = o.data_ptr()
+            if n and q != p:
+                spans.append((q, q + n * g.element_size(), i))
+        e = table[i]
+        e.grad, e.out, e.numel, e.type = p, q, n, typ
+    spans.sort()
+    for (_, end, i), (start, _, j) in zip(spans, spans[1:]):
+        if start < end:
+            raise ValueError(f"the tensors of entries {i} and {j} overlap")
+    return table, len(grads), dev
+
+
+def grad_norm(grads, *, norm=None, workspace=None, stream=None):
+    """The global 2-norm of a list of float32 / bfloat16 tensors, as a float32 tensor without dimensions."""
+    return _grads(grads, None, None, norm, workspace, stream)
+
+
+def clip_grads(grads, max_norm, *, out=None, norm=None, workspace=None, stream=None):
+    """Scales the gradients by min(1, max_norm / (norm + 1e-6)), norm their global 2-norm, and returns the norm.
+
+    In place, or into the tensors of `out`.  Nothing waits for the GPU.
+    """
+    max_norm = float(max_norm)
+    if math.isnan(max_norm) or max_norm < 0:
+        raise ValueError(f"max_norm must not be negative (got {max_norm})")
+    return _grads(grads, max_norm, out, norm, workspace, stream)
+
+
+def _grads(grads, max_norm, out, norm, workspace, stream):
+    m2 = _pkg()
+    torch = _torch()
+    table, count, dev = _grad_table(grads, out)
+    with _On(dev, stream) as s:
+        if norm is None:
+            norm = _empty((), torch.float32, dev)
+        _gpu(norm, "norm", dev)
+        if norm.dtype != torch.float32 or norm.numel() != 1:
+            raise ValueError("norm must be one float32")
+        lib = m2.lib()
+        p = ctypes.addressof(table)
+        workspace, nbytes = _workspace(workspace, lib.mamba2_grad_workspace_bytes(p, count), dev)
+        if max_norm is None:
+            st = lib.mamba2_grad_norm(p, count, norm.data_ptr(), _ptr(workspace), nbytes, s)
+        else:
+            st = lib.mamba2_clip_grads(p, count, max_norm, norm.data_ptr(), _ptr(workspace), nbytes, s)
+    m2._raise(st, "mamba2_grad_norm" if max_norm is None else "mamba2_clip_grads")
+    return norm
