@@ -43,9 +43,9 @@ ESCRATCH = -7
 
 
 class Mamba2ScanError(RuntimeError):
-    def __init__(self, status: int, where: str):
+    def __init__(self, status: int, where: str, text: str | None = None):
         self.status = status
-        super().__init__(f"{where}: {strerror(status)} (status {status})")
+        super().__init__(f"{where}: {strerror(status) if text is None else text} (status {status})")
 
 
 _lib = None

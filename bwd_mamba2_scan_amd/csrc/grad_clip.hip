@@ -11,6 +11,10 @@
 // The number of blocks is held near kBlocks so that those partials stay few.
 // The second pass walks the pieces backwards: what the first pass read last
 // is still in the 256 MB cache.
+#include <stdlib.h>
+
+#include <algorithm>
+
 #include "layer_common.h"
 
 namespace {
@@ -178,6 +182,35 @@ int check_grads(const mamba2_grad* g, int count, bool clip, Sizes* out) {
   return MAMBA2_SCAN_OK;
 }
 
+struct Span {
+  uintptr_t lo, hi;
+};
+
+// Does any gradient or output overlap another?  The second pass writes while
+// the first one's other tensors are still to be scaled, so each must be apart.
+int check_apart(const mamba2_grad* g, int count) {
+  const size_t most = 2 * static_cast<size_t>(count);
+  Span few[256];
+  Span* spans = few;
+  if (most > 256) {
+    spans = static_cast<Span*>(malloc(most * sizeof(Span)));
+    if (spans == nullptr) return MAMBA2_SCAN_EHIP;
+  }
+  size_t n = 0;
+  for (int i = 0; i < count; ++i) {
+    if (g[i].numel == 0) continue;
+    const size_t bytes = static_cast<size_t>(g[i].numel) * type_size(g[i].type);
+    const uintptr_t p = reinterpret_cast<uintptr_t>(g[i].grad), o = reinterpret_cast<uintptr_t>(g[i].out);
+    spans[n++] = {p, p + bytes};
+    if (o != p) spans[n++] = {o, o + bytes};
+  }
+  std::sort(spans, spans + n, [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  bool apart = true;
+  for (size_t i = 1; i < n; ++i) apart = apart && spans[i - 1].hi <= spans[i].lo;
+  if (spans != few) free(spans);
+  return apart ? MAMBA2_SCAN_OK : MAMBA2_SCAN_EOVERLAP;
+}
+
 // Calls f(table, first block of the table) for each table of the list.
 template <class F>
 int for_tables(const mamba2_grad* g, int count, const Sizes& sz, F f) {
@@ -246,6 +279,7 @@ int mamba2_clip_grads(const mamba2_grad* grads, int count, float max_norm, float
   if (!(max_norm >= 0.0f)) return MAMBA2_SCAN_EBADDIM;
   int st = check_call(grads, count, true, norm, workspace, workspace_bytes, &sz);
   if (st != MAMBA2_SCAN_OK) return st;
+  if ((st = check_apart(grads, count)) != MAMBA2_SCAN_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if ((st = run_squares(grads, count, sz, workspace, s)) != MAMBA2_SCAN_OK) return st;
   const double* partial = static_cast<const double*>(workspace);

@@ -39,7 +39,7 @@ struct FwdLds {
   alignas(16) T c[kTok * ldn];
   alignas(16) T x[kTok * ldp];
   alignas(16) T w[kTok * ldw];
-  alignas(16) Decays dc;
+  alignas(16) Decays dc[2];
 };
 
 template <class T, int NB, int NW>
@@ -58,49 +58,73 @@ __global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(SsmArgs a, Walk w) {
   const bool packed = a.q.offsets != nullptr;
   const int p0 = slice * L::kP;                          // first column of the work-group
   const int cols = min(a.width - p0, L::kP);
-  const int col = p0 + wave * 16 + l15;                  // this lane's column
-  const bool live = col < a.width;
+  const int quad = wave * 16 + 4 * g;                    // this lane's four columns of y
   const long head = static_cast<long>(a.states) * a.width;
+  const long of_seq = (static_cast<long>(u.seq) * a.heads + h) * head;
 
   const T* xp = seq_ptr<const T>(a.x, u.seq, u.row0, packed) + h * a.width + p0;
   const T* bp = seq_ptr<const T>(a.B, u.seq, u.row0, packed) + h / a.ratio * a.states;
   const T* cp = seq_ptr<const T>(a.C, u.seq, u.row0, packed) + h / a.ratio * a.states;
   T* yp = seq_ptr<T>(a.y, u.seq, u.row0, packed) + h * a.width + p0;
-  const void* dtp = a.dt_bf16 ? static_cast<const void*>(seq_ptr<const bf16>(a.dt, u.seq, u.row0, packed))
-                              : static_cast<const void*>(seq_ptr<const float>(a.dt, u.seq, u.row0, packed));
   const float A = a.A[h], bias = a.bias != nullptr ? a.bias[h] : 0.0f, D = a.D != nullptr ? a.D[h] : 0.0f;
 
-  v4f st[2 * NB];
-  {
-    const float* from = u.index == 0
-                            ? (a.initial == nullptr ? nullptr : a.initial + (static_cast<long>(u.seq) * a.heads + h) * head)
-                            : w.seg_state + (static_cast<long>(unit) * a.heads + h) * head;
-    load_state<NB>(st, from, a.width, a.states, col, live);
-  }
+  State<NB, true> st;
+  st.init(a.width, p0, wave);
+  st.load(u.index == 0 ? (a.initial == nullptr ? nullptr : a.initial + of_seq)
+                       : w.seg_state + (static_cast<long>(unit) * a.heads + h) * head,
+          a.width, a.states);
   // tiles above the diagonal that a 32-wide product step touches stay zero
   for (int i = tid; i < kTok * L::ldw; i += kThreads) s.w[i] = static_cast<T>(0.0f);
 
   const int end = min(u.t0 + a.seg, u.len);
   Tile<T, kTok, L::kN, kThreads> tb, tc;
   Tile<T, kTok, L::kP, kThreads> tx;
-  float raw = 0.0f;
+  tb.init(a.B.row_stride, a.states, tid);
+  tc.init(a.C.row_stride, a.states, tid);
+  tx.init(a.x.row_stride, cols, tid);
   const auto fetch = [&](int t) {
-    const int rows = end - t;
-    tb.load(bp + t * a.B.row_stride, a.B.row_stride, rows, a.states, tid);
-    tc.load(cp + t * a.C.row_stride, a.C.row_stride, rows, a.states, tid);
-    tx.load(xp + t * a.x.row_stride, a.x.row_stride, rows, cols, tid);
-    if (wave == 0 && lane < rows) raw = raw_step(a, a.dt, dtp, t + lane, h);
-  };
-  if (u.t0 < end) fetch(u.t0);
-  for (int t = u.t0; t < end; t += kTok) {
     const int rows = min(end - t, kTok);
+    tb.load(rows_rsrc(bp + t * a.B.row_stride, a.B.row_stride, rows, a.states));
+    tc.load(rows_rsrc(cp + t * a.C.row_stride, a.C.row_stride, rows, a.states));
+    tx.load(rows_rsrc(xp + t * a.x.row_stride, a.x.row_stride, rows, cols));
+  };
+  // The last wave, which has the fewest score tiles, prepares the next step's
+  // decays; the raw step sizes are loaded a step before that.
+  const bool decays = wave == NW - 1;
+  float raw = 0.0f;
+  const auto fetch_raw = [&](int t) { raw = load_raw(a, step_rsrc(a, u, packed, t, min(end - t, kTok)), h); };
+  const auto prepare = [&](Decays& dc, int t) {
+    make_decays(dc, lane < end - t ? step_of(a, raw, bias) : 0.0f, A);
+  };
+  if (u.t0 < end) {
+    fetch(u.t0);
+    if (decays) {
+      fetch_raw(u.t0);
+      prepare(s.dc[0], u.t0);
+      if (u.t0 + kTok < end) fetch_raw(u.t0 + kTok);
+    }
+  }
+  unsigned yoff[4];
+#pragma unroll
+  for (int ti = 0; ti < 4; ++ti)
+    yoff[ti] = quad < cols
+                   ? static_cast<unsigned>(((ti * 16 + l15) * static_cast<int>(a.y.row_stride) + quad) * sizeof(T))
+                   : kOutside;
+  int turn = 0;
+  for (int t = u.t0; t < end; t += kTok, turn ^= 1) {
+    const Decays& dc = s.dc[turn];
     __syncthreads();  // the last step's readers are done
     tb.store(s.b, L::ldn, tid);
     tc.store(s.c, L::ldn, tid);
     tx.store(s.x, L::ldp, tid);
-    if (wave == 0) make_decays(s.dc, lane < rows ? step_of(a, raw, bias) : 0.0f, A);
     __syncthreads();
-    if (t + kTok < end) fetch(t + kTok);
+    if (t + kTok < end) {
+      fetch(t + kTok);
+      if (decays) {
+        prepare(s.dc[turn ^ 1], t + kTok);
+        if (t + 2 * kTok < end) fetch_raw(t + 2 * kTok);
+      }
+    }
 
     // scores, transposed as a result: lane has t = l15, s = 4 g + i
     for (int i = wave; i < 10; i += NW) {
@@ -111,19 +135,22 @@ __global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(SsmArgs a, Walk w) {
       for (int k = 0; k < NB; ++k)
         mma(acc, frag_row(s.b, L::ldn, si * 16, k * 32), frag_row(s.c, L::ldn, ti * 16, k * 32));
       const int tt = ti * 16 + l15, ss = si * 16 + 4 * g;
-      const float ch = s.dc.hi[tt], cl = s.dc.lo[tt];
-      T out[4];
+      const float ch = dc.hi[tt], cl = dc.lo[tt];
+      const v4f hi = *reinterpret_cast<const v4f*>(&dc.hi[ss]), lo = *reinterpret_cast<const v4f*>(&dc.lo[ss]);
+      const v4f d = *reinterpret_cast<const v4f*>(&dc.d[ss]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float e = exp2_of((ch - s.dc.hi[ss + j]) + (cl - s.dc.lo[ss + j]));
-        // the scores become an operand: 8 bits with bf16, as x has
-        out[j] = static_cast<T>(ss + j <= tt ? acc[j] * e * s.dc.d[ss + j] : 0.0f);
+      for (int j = 0; j < 4; ++j) acc[j] *= exp2_of((ch - hi[j]) + (cl - lo[j])) * d[j];
+      if (ti == si) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (ss + j > tt) acc[j] = 0.0f;
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s.w[tt * L::ldw + ss + j] = out[j];
+      // the scores become an operand: 8 bits with bf16, as x has
+      quad_put(&s.w[tt * L::ldw + ss], acc);
     }
-    // y from the state before the step.  The state as an operand keeps 8 bits
-    // with bf16, like the y it goes into; the state itself stays fp32.
+    // y transposed (lane: t = l15, columns 4 g + i), from the state before the
+    // step.  The state as an operand keeps 8 bits with bf16, like the y it
+    // goes into; the state itself stays fp32.
     v4f y[4];
     {
       Frag<T> sf[NB];
@@ -131,48 +158,36 @@ __global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(SsmArgs a, Walk w) {
       for (int k = 0; k < NB; ++k) {
         float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = st[2 * k + (j >> 2)][j & 3];
-        sf[k] = frag_of<T>(v, nullptr);
+        for (int j = 0; j < 8; ++j) v[j] = st.st[2 * k + (j >> 2)][j & 3];
+        sf[k] = frag_of<T>(v);
       }
 #pragma unroll
       for (int ti = 0; ti < 4; ++ti) {
         y[ti] = v4f{0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < NB; ++k) mma(y[ti], frag_row_result(s.c, L::ldn, ti * 16, k * 32), sf[k]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[ti][j] *= s.dc.from[ti * 16 + 4 * g + j];
+        for (int k = 0; k < NB; ++k) mma(y[ti], sf[k], frag_row_result(s.c, L::ldn, ti * 16, k * 32));
+        y[ti] *= dc.from[ti * 16 + l15];
       }
     }
-    __syncthreads();
     Frag<T> xf[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) xf[k] = frag_col(s.x, L::ldp, k * 32, wave * 16);
+    st.template advance<T>(dc.total, dc.to, s.b, L::ldn, xf);
+    __syncthreads();
+    const Rsrc ry = rows_rsrc(yp + t * a.y.row_stride, a.y.row_stride, min(end - t, kTok), cols);
 #pragma unroll
-    for (int ti = 0; ti < 4; ++ti)
+    for (int ti = 0; ti < 4; ++ti) {
 #pragma unroll
-      for (int k = 0; k <= ti / 2; ++k) mma(y[ti], frag_row(s.w, L::ldw, ti * 16, k * 32), xf[k]);
-    advance_state<T, NB>(st, s.dc.total, s.dc.to, s.b, L::ldn, xf);
-    // D x, then y through this wave's own columns of the x tile to rows of 16 bytes
-#pragma unroll
-    for (int ti = 0; ti < 4; ++ti)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        T* e = s.x + (ti * 16 + 4 * g + j) * L::ldp + wave * 16 + l15;
-        *e = static_cast<T>(fmaf(D, static_cast<float>(*e), y[ti][j]));
-      }
-    constexpr int kVec = Vec<T>::n, kPerRow = 16 / kVec;
-#pragma unroll
-    for (int i = 0; i < kTok * kPerRow / 64; ++i) {
-      const int r = (lane + i * 64) / kPerRow, c = wave * 16 + (lane + i * 64) % kPerRow * kVec;
-      if (r < rows && c < cols)
-        *reinterpret_cast<typename Vec<T>::type*>(yp + (t + r) * a.y.row_stride + c) =
-            *reinterpret_cast<const typename Vec<T>::type*>(s.x + r * L::ldp + c);
+      for (int k = 0; k <= ti / 2; ++k) mma(y[ti], xf[k], frag_row(s.w, L::ldw, ti * 16, k * 32));
+      y[ti] += D * quad_get(&s.x[(ti * 16 + l15) * L::ldp + quad]);
+      Quad<T>::store(ry, yoff[ti], y[ti]);
     }
   }
   if (a.final_state != nullptr && u.t0 + static_cast<long>(a.seg) >= u.len)
-    save_state<NB>(st, a.final_state + (static_cast<long>(u.seq) * a.heads + h) * head, a.width, a.states, col, live);
+    st.save(a.final_state + of_seq, a.width, a.states);
 }
 
+// Summary pass of the segments; see walk().
 template <class T, int NB, int NW>
 __global__ __launch_bounds__(NW * 64) void ssm_summary_kernel(SsmArgs a, Walk w) {
   __shared__ WalkLds<T, NB, NW> s;
@@ -310,9 +325,19 @@ int check_vec_rows(const mamba2_rows& r, const mamba2_seqs& q, long long width, 
   if (st != MAMBA2_SCAN_OK || q.length == 0) return st;
   const long long n = 8;
   if (!aligned_to(r.data, 16)) return MAMBA2_SCAN_EALIGN;
+  // a step's 64 rows are addressed with 31-bit offsets
+  (void)elem;
+  if (q.length > 1 && r.row_stride > (1LL << 29) / (kTok + 1)) return MAMBA2_SCAN_EUNSUPPORTED;
   if ((q.length > 1 && r.row_stride % n != 0) || (q.offsets == nullptr && q.batch > 1 && r.batch_stride % n != 0))
     return MAMBA2_SCAN_EALIGN;
   return MAMBA2_SCAN_OK;
+}
+
+// dt: any stride that the same offsets reach.
+int check_step_rows(const mamba2_rows& r, const mamba2_seqs& q, const mamba2_ssm_dims& d) {
+  const int st = check_rows(r, q, d.heads, type_size(d.dt_type));
+  if (st != MAMBA2_SCAN_OK) return st;
+  return q.length > 1 && r.row_stride > (1LL << 29) / (kTok + 1) ? MAMBA2_SCAN_EUNSUPPORTED : MAMBA2_SCAN_OK;
 }
 
 int waves_of(int width) { return width <= 16 ? 1 : width <= 32 ? 2 : 4; }
@@ -334,6 +359,20 @@ int segment_tokens(const mamba2_seqs& q, const mamba2_ssm_dims& d) {
 
 extern "C" {
 
+const char* mamba2_layer_strerror(int status) {
+  switch (status) {
+    case MAMBA2_SCAN_OK: return "success";
+    case MAMBA2_SCAN_EBADDIM: return "invalid dimension or stride (sizes positive, strides not shorter than a row)";
+    case MAMBA2_SCAN_EUNSUPPORTED: return "unsupported type or size (taps 2-4; width and states multiples of 8 up to 128)";
+    case MAMBA2_SCAN_ENULL: return "a required pointer is NULL";
+    case MAMBA2_SCAN_ESIZE: return "workspace is smaller than required";
+    case MAMBA2_SCAN_EALIGN: return "a pointer or stride is not aligned as required (the scan: 16 bytes, strides 8 elements)";
+    case MAMBA2_SCAN_EHIP: return "HIP runtime error while enqueuing a kernel";
+    case MAMBA2_SCAN_EOVERLAP: return "tensors that must be apart overlap";
+    default: return "unknown status";
+  }
+}
+
 size_t mamba2_ssm_fwd_workspace_bytes(mamba2_seqs q, mamba2_ssm_dims d) {
   if (check_dims(q, d) != MAMBA2_SCAN_OK) return 0;
   const int seg = segment_tokens(q, d);
@@ -352,7 +391,7 @@ int mamba2_ssm_fwd(mamba2_seqs q, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows 
   if (A == nullptr) return MAMBA2_SCAN_ENULL;
   if ((st = check_vec_rows(x, q, xw, e)) != MAMBA2_SCAN_OK || (st = check_vec_rows(B, q, bw, e)) != MAMBA2_SCAN_OK ||
       (st = check_vec_rows(C, q, bw, e)) != MAMBA2_SCAN_OK || (st = check_vec_rows(y, q, xw, e)) != MAMBA2_SCAN_OK ||
-      (st = check_rows(dt, q, d.heads, type_size(d.dt_type))) != MAMBA2_SCAN_OK)
+      (st = check_step_rows(dt, q, d)) != MAMBA2_SCAN_OK)
     return st;
   if (!aligned_to(A, 4) || !aligned_to(D, 4) || !aligned_to(dt_bias, 4) || !aligned_to(initial_state, 16) ||
       !aligned_to(final_state, 16))

@@ -43,19 +43,22 @@ struct BwdArgs {
   int run;                 // heads per run
 };
 
+struct Walks {  // forward, reverse: side by side in one launch
+  Walk w[2];
+};
+
 template <class T, int NB, int NW>
-__global__ __launch_bounds__(NW * 64) void ssm_walk_kernel(SsmArgs a, Walk f, Walk r) {
+__global__ __launch_bounds__(NW * 64) void ssm_walk_kernel(SsmArgs a, Walks ws) {
   __shared__ WalkLds<T, NB, NW> s;
-  walk<T, NB, NW, true>(a, blockIdx.y == 0 ? f : r, s);
+  walk<T, NB, NW, true>(a, ws.w[blockIdx.y], s);
 }
 template <class T, int NB, int NW>
-__global__ __launch_bounds__(NW * 64) void ssm_walk_summary_kernel(SsmArgs a, Walk f, Walk r) {
+__global__ __launch_bounds__(NW * 64) void ssm_walk_summary_kernel(SsmArgs a, Walks ws) {
   __shared__ WalkLds<T, NB, NW> s;
-  walk<T, NB, NW, false>(a, blockIdx.y == 0 ? f : r, s);
+  walk<T, NB, NW, false>(a, ws.w[blockIdx.y], s);
 }
-__global__ __launch_bounds__(256) void ssm_walk_carry_kernel(SsmArgs a, Walk f, Walk r) {
-  if (blockIdx.z & 1) carry(a, r, blockIdx.z >> 1);
-  else carry(a, f, blockIdx.z >> 1);
+__global__ __launch_bounds__(256) void ssm_walk_carry_kernel(SsmArgs a, Walks ws) {
+  carry(a, ws.w[blockIdx.z & 1], blockIdx.z >> 1);
 }
 
 constexpr int kBwdThreads = 256;
@@ -65,52 +68,58 @@ struct BwdLds {
   static constexpr int kN = NB * 32;
   static constexpr int kP = PT * 16 < 32 ? 32 : PT * 16;  // a product over the columns takes 32 at a time
   static constexpr int kTerms = sizeof(T) == 2 ? 2 : 1;
+  static constexpr int kRows = kN < 64 ? kN : 64;         // state rows staged at a time
   static constexpr int ldn = stride_of<T>(kN);
   static constexpr int ldp = stride_of<T>(kP);
   alignas(16) T b[kTok * ldn];
   alignas(16) T c[kTok * ldn];
   alignas(16) T x[kTok * ldp];
   alignas(16) T dy[kTok * ldp];
-  alignas(16) T st[kTerms][kN * ldp];  // the starting state, then the gradient behind the step, in two terms
-  alignas(16) Decays dc;
-  float inner[4][kTok];   // m_t: pairs within the step, per wave's columns
-  float after[kTok];      // starting state into row t
-  float before[kTok];     // row t into what follows (without d)
-  float direct[kTok];     // x . P^T d_y
-  float whole[4];         // starting state through the step, per wave
-  float skip[4];          // sum d_y . x, per wave
+  alignas(16) T st[kTerms][kRows * ldp];  // rows of the starting state, then of the gradient behind the step
+  alignas(16) Decays dc[3];  // of the head before (its gradients are put together), this one and the next
+  float slope[3][kTok];      // d d_t / d dt_t
+  struct Sums {              // of a head and the one before
+    float inner[4][kTok];    // m_t: pairs within the step, per wave's columns
+    float after[kTok];       // starting state into row t
+    float before[kTok];      // row t into what follows (without d)
+    float direct[kTok];      // x . P^T d_y
+    float whole[4];          // starting state through the step, per wave
+    float skip[4];           // sum d_y . x, per wave
+  } sums[2];
 };
 
-// A [states][width] fp32 matrix slice in registers, then LDS in one or two terms.
+// Rows of a [states][width] fp32 matrix slice in registers, then LDS, where a
+// bf16 product finds them in two terms (16 bits; the third would cost a
+// product and LDS space, and only the sums over thousands of tokens that
+// d_A and d_dt_bias are would show it).
 template <class T, int NB, int PT>
 struct StateTile {
   typedef BwdLds<T, NB, PT> L;
   static constexpr int kQuads = L::kP / 4;
-  static constexpr int kN = L::kN * kQuads / kBwdThreads;
+  static constexpr int kN = L::kRows * kQuads / kBwdThreads;
+  static constexpr int kStep = kBwdThreads / kQuads;  // rows between a thread's quads
   v4f v[kN];
-  __device__ __forceinline__ void load(const float* p, int width, int states, int cols) {
+  __device__ __forceinline__ static unsigned offset(int width, int cols) {
+    const int r = threadIdx.x / kQuads, c = threadIdx.x % kQuads * 4;
+    return c < cols ? static_cast<unsigned>((r * width + c) * 4) : kOutside;
+  }
+  __device__ __forceinline__ void load(Rsrc rs, unsigned off, int width, int phase) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int e = threadIdx.x + i * kBwdThreads, r = e / kQuads, c = e % kQuads * 4;
-      v[i] = (r < states && c < cols) ? *reinterpret_cast<const v4f*>(p + static_cast<long>(r) * width + c)
-                                      : v4f{0, 0, 0, 0};
-    }
+    for (int i = 0; i < kN; ++i)
+      v[i] = __builtin_bit_cast(
+          v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, off + (phase * L::kRows + i * kStep) * width * 4, 0, 0));
   }
   __device__ __forceinline__ void store(L& s) const {
+    const int at = threadIdx.x / kQuads * L::ldp + threadIdx.x % kQuads * 4;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int e = threadIdx.x + i * kBwdThreads, r = e / kQuads, c = e % kQuads * 4;
-      if constexpr (sizeof(T) == 2) {
-        v4bf hi, lo;
+      T* p = &s.st[0][at + i * kStep * L::ldp];
+      quad_put(p, v[i]);
+      if constexpr (L::kTerms == 2) {
+        v4f rest;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          hi[j] = static_cast<bf16>(v[i][j]);
-          lo[j] = static_cast<bf16>(v[i][j] - static_cast<float>(hi[j]));
-        }
-        *reinterpret_cast<v4bf*>(&s.st[0][r * L::ldp + c]) = hi;
-        *reinterpret_cast<v4bf*>(&s.st[L::kTerms - 1][r * L::ldp + c]) = lo;
-      } else {
-        *reinterpret_cast<v4f*>(&s.st[0][r * L::ldp + c]) = v[i];
+        for (int j = 0; j < 4; ++j) rest[j] = v[i][j] - static_cast<float>(static_cast<bf16>(v[i][j]));
+        quad_put(p + L::kRows * L::ldp, rest);
       }
     }
   }
@@ -120,50 +129,124 @@ struct StateTile {
 template <class T>
 __device__ __forceinline__ Frag<T> frag_tiles(const v4f& a, const v4f& b) {
   const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-  return frag_of<T>(v, nullptr);
+  return frag_of<T>(v);
 }
 
+// The sum over the four lanes with the same l & 15.
+__device__ __forceinline__ float sum_groups(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+// Results lie so that a lane has one row (token) and four neighbouring
+// columns: a row's factor is one value, and results go out as they are.
 template <class T, int NB, int PT>
-__global__ __launch_bounds__(kBwdThreads, 1) void ssm_bwd_kernel(BwdArgs ba) {
+__global__ __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_kernel(BwdArgs ba) {
   typedef BwdLds<T, NB, PT> L;
+  typedef StateTile<T, NB, PT> ST;
   __shared__ L s;
   const SsmArgs& a = ba.a;
   constexpr int kKp = L::kP / 32;   // 32-wide product steps over the columns
   constexpr int kPt = L::kP / 16;
+  constexpr int kPhases = L::kN / L::kRows;
+  constexpr int kNt = L::kRows / 16;  // 16-row tiles of the state per phase
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, l15 = lane & 15, g = lane >> 4;
   const int work = xcd_contiguous(blockIdx.x, gridDim.x);
   const int split = work % ba.splits;
   const int gr = work / ba.splits % ba.groups;
   const int step = work / ba.splits / ba.groups;
   const Unit u = locate(a.q, step, kTok);
-  if (u.t0 >= u.len) return;  // (the reduction skips these steps too)
+  if (u.t0 >= u.len) return;  // (the reductions skip these steps too)
   const bool packed = a.q.offsets != nullptr;
   const int rows = min(u.len - u.t0, kTok);
   const int h0 = gr * a.ratio + split * ba.run;
   const int h1 = min(h0 + ba.run, (gr + 1) * a.ratio);
   const long head = static_cast<long>(a.states) * a.width;
   const int row = wave * 16;                // this wave's rows
+  const int mine = row + l15;               // this lane's row
   const int slices = (a.width + L::kP - 1) / L::kP;
 
   const T* xp = seq_ptr<const T>(a.x, u.seq, u.row0, packed) + u.t0 * a.x.row_stride;
   const T* gp = seq_ptr<const T>(ba.d_y, u.seq, u.row0, packed) + u.t0 * ba.d_y.row_stride;
   T* op = seq_ptr<T>(ba.d_x, u.seq, u.row0, packed) + u.t0 * ba.d_x.row_stride;
-  const void* dtp = a.dt_bf16 ? static_cast<const void*>(seq_ptr<const bf16>(a.dt, u.seq, u.row0, packed))
-                              : static_cast<const void*>(seq_ptr<const float>(a.dt, u.seq, u.row0, packed));
+  const Rsrc rdt = step_rsrc(a, u, packed, u.t0, rows);
   {
     Tile<T, kTok, L::kN, kBwdThreads> tb, tc;
-    tb.load(seq_ptr<const T>(a.B, u.seq, u.row0, packed) + u.t0 * a.B.row_stride + gr * a.states, a.B.row_stride,
-            rows, a.states, tid);
-    tc.load(seq_ptr<const T>(a.C, u.seq, u.row0, packed) + u.t0 * a.C.row_stride + gr * a.states, a.C.row_stride,
-            rows, a.states, tid);
+    tb.init(a.B.row_stride, a.states, tid);
+    tc.init(a.C.row_stride, a.states, tid);
+    tb.load(rows_rsrc(seq_ptr<const T>(a.B, u.seq, u.row0, packed) + u.t0 * a.B.row_stride + gr * a.states,
+                      a.B.row_stride, rows, a.states));
+    tc.load(rows_rsrc(seq_ptr<const T>(a.C, u.seq, u.row0, packed) + u.t0 * a.C.row_stride + gr * a.states,
+                      a.C.row_stride, rows, a.states));
     tb.store(s.b, L::ldn, tid);
     tc.store(s.c, L::ldn, tid);
-    s.inner[wave][lane] = 0.0f;  // rows before a wave's columns stay zero
+    s.sums[0].inner[wave][lane] = s.sums[1].inner[wave][lane] = 0.0f;  // rows before a wave's columns stay zero
+  }
+
+  Tile<T, kTok, L::kP, kBwdThreads> tx, ty;
+  ST ts, tg;
+  const auto fetch_rows = [&](int h, int p0) {
+    const int cols = min(a.width - p0, L::kP);
+    tx.init(a.x.row_stride, cols, tid);
+    ty.init(ba.d_y.row_stride, cols, tid);
+    tx.load(rows_rsrc(xp + h * a.width + p0, a.x.row_stride, rows, cols));
+    ty.load(rows_rsrc(gp + h * a.width + p0, ba.d_y.row_stride, rows, cols));
+  };
+  const auto fetch_state = [&](ST& t, const float* keep, int h, int p0, int phase) {
+    const float* p = keep + (static_cast<long>(step) * a.heads + h) * head + p0;
+    t.load(make_rsrc(p, static_cast<unsigned>((head - p0) * 4)), ST::offset(a.width, min(a.width - p0, L::kP)),
+           a.width, phase);
+  };
+  // The last wave prepares the next head's decays while the others multiply.
+  const bool decays = wave == 3;
+  float raw = 0.0f;
+  const auto prepare = [&](int h, int k) {
+    const float bias = a.bias != nullptr ? a.bias[h] : 0.0f;
+    make_decays(s.dc[k], lane < rows ? step_of(a, raw, bias) : 0.0f, a.A[h]);
+    s.slope[k][lane] = a.softplus ? __builtin_amdgcn_rcpf(1.0f + expf(-(raw + bias))) : 1.0f;
+  };
+  // The step sizes' gradients of a head whose sums are complete: a token per lane.
+  const auto finish = [&](int h, int k, int par) {
+    const auto& sum = s.sums[par];
+    const Decays& dc = s.dc[k];
+    const float A = a.A[h], d = dc.d[lane];
+    const float after = __shfl(scan64(__shfl(sum.after[lane], 63 - lane)), 63 - lane);
+    float upto = __shfl_up(scan64(d * sum.before[lane]), 1);
+    if (lane == 0) upto = 0.0f;
+    const float whole = ((sum.whole[0] + sum.whole[1]) + (sum.whole[2] + sum.whole[3])) * dc.total;
+    const float inner = (sum.inner[0][lane] + sum.inner[1][lane]) + (sum.inner[2][lane] + sum.inner[3][lane]);
+    const float m = inner + after + upto + whole;
+    float dd = (sum.direct[lane] + sum.before[lane] + A * m) * s.slope[k][lane];
+    float dA = d * m;
+    if (lane < rows) {
+      const long i = (u.t0 + lane) * ba.d_dt.row_stride + h;
+      if (a.dt_bf16) seq_ptr<bf16>(ba.d_dt, u.seq, u.row0, packed)[i] = static_cast<bf16>(dd);
+      else seq_ptr<float>(ba.d_dt, u.seq, u.row0, packed)[i] = dd;
+    } else {
+      dd = dA = 0.0f;
+    }
+    dA = sum64(dA);
+    dd = sum64(dd);
+    if (lane == 0) {
+      float* p = ba.part + (static_cast<long>(step) * a.heads + h) * 4;
+      p[0] = dA;
+      p[1] = (sum.skip[0] + sum.skip[1]) + (sum.skip[2] + sum.skip[3]);
+      p[2] = dd;
+    }
+  };
+
+  fetch_rows(h0, 0);
+  fetch_state(ts, ba.keep_s, h0, 0, 0);
+  fetch_state(tg, ba.keep_g, h0, 0, 0);
+  if (decays) {
+    raw = load_raw(a, rdt, h0);
+    prepare(h0, 0);
+    if (h0 + 1 < h1) raw = load_raw(a, rdt, h0 + 1);
   }
   v4f db[2 * NB], dcc[2 * NB];
 #pragma unroll
   for (int n = 0; n < 2 * NB; ++n) db[n] = dcc[n] = v4f{0, 0, 0, 0};
-  v4f cb[4];  // (C B^T)[t][s], column s = row + l15, rows t = 16 ti + 4 g + i
+  v4f cb[4];  // (C B^T)[t][s], column s = mine, rows t = 16 ti + 4 g + i
   __syncthreads();
 #pragma unroll
   for (int ti = 0; ti < 4; ++ti) {
@@ -174,285 +257,248 @@ __global__ __launch_bounds__(kBwdThreads, 1) void ssm_bwd_kernel(BwdArgs ba) {
     }
   }
 
+  int cur = 0, par = 0;
   for (int h = h0; h < h1; ++h) {
-    const float A = a.A[h], bias = a.bias != nullptr ? a.bias[h] : 0.0f, D = a.D != nullptr ? a.D[h] : 0.0f;
-    float raw = 0.0f;
-    if (wave == 0 && lane < rows) raw = raw_step(a, a.dt, dtp, u.t0 + lane, h);
+    const float D = a.D != nullptr ? a.D[h] : 0.0f;
+    const int next = cur == 2 ? 0 : cur + 1, last = cur == 0 ? 2 : cur - 1;
+    const Decays& dc = s.dc[cur];
+    auto& sum = s.sums[par];
     for (int slice = 0; slice < slices; ++slice) {
       const int p0 = slice * L::kP, cols = min(a.width - p0, L::kP);
-      const long state_at = (static_cast<long>(step) * a.heads + h) * head + p0;
-      StateTile<T, NB, PT> ts, tg;
-      Tile<T, kTok, L::kP, kBwdThreads> tx, ty;
-      ts.load(ba.keep_s + state_at, a.width, a.states, cols);
-      tx.load(xp + h * a.width + p0, a.x.row_stride, rows, cols, tid);
-      ty.load(gp + h * a.width + p0, ba.d_y.row_stride, rows, cols, tid);
-      __syncthreads();  // the last round's readers are done
-      ts.store(s);
-      tx.store(s.x, L::ldp, tid);
-      ty.store(s.dy, L::ldp, tid);
-      if (wave == 0 && slice == 0) make_decays(s.dc, lane < rows ? step_of(a, raw, bias) : 0.0f, A);
-      __syncthreads();
-      tg.load(ba.keep_g + state_at, a.width, a.states, cols);
-
-      // ---- within the step, columns s of this wave
+      const bool more = slice + 1 < slices || h + 1 < h1;  // a round follows this one, of:
+      const int hn = slice + 1 < slices ? h : h + 1, pn = slice + 1 < slices ? p0 + L::kP : 0;
       v4f dx[kPt];
+      float whole = 0.0f, after = 0.0f, before = 0.0f;
 #pragma unroll
-      for (int p = 0; p < kPt; ++p) dx[p] = v4f{0, 0, 0, 0};
-      {
-        const int sc = row + l15;
-        const float ch = s.dc.hi[sc], cl = s.dc.lo[sc], d = s.dc.d[sc];
-        v4f pw[4], qw[4];
-        float direct = 0.0f, skip = 0.0f, behind = 0.0f;
+      for (int ph = 0; ph < kPhases; ++ph) {
 #pragma unroll
-        for (int ti = 3; ti >= 0; --ti) {
-          pw[ti] = qw[ti] = v4f{0, 0, 0, 0};
-          if (ti < wave) continue;
-          v4f yx = {0, 0, 0, 0};
+        for (int i = 0; i < ST::kN; ++i)
 #pragma unroll
-          for (int k = 0; k < kKp; ++k) mma(yx, frag_row(s.dy, L::ldp, ti * 16, k * 32), frag_row(s.x, L::ldp, row, k * 32));
-          float pair[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int t = ti * 16 + 4 * g + i;
-            const float e = t >= sc ? exp2_of((s.dc.hi[t] - ch) + (s.dc.lo[t] - cl)) : 0.0f;
-            pw[ti][i] = cb[ti][i] * e;
-            qw[ti][i] = yx[i] * e * d;
-            const float m = pw[ti][i] * yx[i];
-            direct += m;
-            pair[i] = t > sc ? m : 0.0f;
-            if (t == sc) skip += yx[i];
+          for (int j = 0; j < 4; ++j) whole = fmaf(ts.v[i][j], tg.v[i][j], whole);
+        __syncthreads();  // the readers of what is overwritten are done
+        if (ph == 0) {
+          tx.store(s.x, L::ldp, tid);
+          ty.store(s.dy, L::ldp, tid);
+        }
+        ts.store(s);
+        __syncthreads();
+        if (ph + 1 < kPhases) fetch_state(ts, ba.keep_s, h, p0, ph + 1);
+        else if (more) {
+          fetch_rows(hn, pn);
+          fetch_state(ts, ba.keep_s, hn, pn, 0);
+        }
+        if (ph == 0) {
+          if (slice == 0) {
+            if (wave == 0 && h > h0) finish(h - 1, last, par ^ 1);
+            if (decays && h + 1 < h1) {
+              prepare(h + 1, next);
+              if (h + 2 < h1) raw = load_raw(a, rdt, h + 2);
+            }
           }
-          // sum of the column's pairs at rows >= t: in the lane, over the lane
-          // groups behind, and over the tiles behind
-          pair[2] += pair[3];
-          pair[1] += pair[2];
-          pair[0] += pair[1];
-          const float d1 = __shfl_down(pair[0], 16), d2 = __shfl_down(pair[0], 32), d3 = __shfl_down(pair[0], 48);
-          const float rest = behind + (g < 3 ? d1 : 0.0f) + (g < 2 ? d2 : 0.0f) + (g < 1 ? d3 : 0.0f);
+          // ---- within the step, column s = mine
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int t = ti * 16 + 4 * g + i;
-            const float v = sum16(sc < t ? (pair[i] + rest) * d : 0.0f);
-            if (l15 == 0) s.inner[wave][t] = slice == 0 ? v : s.inner[wave][t] + v;
+          for (int p = 0; p < kPt; ++p) dx[p] = v4f{0, 0, 0, 0};
+          {
+            const float ch = dc.hi[mine], cl = dc.lo[mine], d = dc.d[mine];
+            v4f pw[4], qw[4];
+            float direct = 0.0f, skip = 0.0f, behind = 0.0f;
+#pragma unroll
+            for (int ti = 3; ti >= 0; --ti) {
+              pw[ti] = qw[ti] = v4f{0, 0, 0, 0};
+              if (ti < wave) continue;
+              v4f yx = {0, 0, 0, 0};
+#pragma unroll
+              for (int k = 0; k < kKp; ++k)
+                mma(yx, frag_row(s.dy, L::ldp, ti * 16, k * 32), frag_row(s.x, L::ldp, row, k * 32));
+              const int t0 = ti * 16 + 4 * g;
+              const v4f hi = *reinterpret_cast<const v4f*>(&dc.hi[t0]), lo = *reinterpret_cast<const v4f*>(&dc.lo[t0]);
+              v4f pair;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float e = exp2_of((hi[i] - ch) + (lo[i] - cl));
+                if (ti == wave) e = t0 + i >= mine ? e : 0.0f;
+                pw[ti][i] = cb[ti][i] * e;
+                qw[ti][i] = yx[i] * (e * d);
+                pair[i] = pw[ti][i] * yx[i];
+                direct += pair[i];
+                if (ti == wave) {
+                  if (t0 + i == mine) skip = yx[i];
+                  pair[i] = t0 + i > mine ? pair[i] : 0.0f;
+                }
+              }
+              // the column's pairs at rows >= t: in the lane, over the lane
+              // groups behind, and over the tiles behind
+              pair[2] += pair[3];
+              pair[1] += pair[2];
+              pair[0] += pair[1];
+              const float d1 = __shfl_down(pair[0], 16), d2 = __shfl_down(pair[0], 32), d3 = __shfl_down(pair[0], 48);
+              const float rest = behind + (g < 3 ? d1 : 0.0f) + (g < 2 ? d2 : 0.0f) + (g < 1 ? d3 : 0.0f);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float v = (pair[i] + rest) * d;
+                if (ti == wave) v = mine < t0 + i ? v : 0.0f;
+                v = sum16(v);
+                if (l15 == 0) sum.inner[wave][t0 + i] = slice == 0 ? v : sum.inner[wave][t0 + i] + v;
+              }
+              behind += sum_groups(pair[0]);
+            }
+            direct = sum_groups(direct);
+            if (g == 0) sum.direct[mine] = slice == 0 ? direct : sum.direct[mine] + direct;
+            skip = sum64(skip);
+            if (lane == 0) sum.skip[wave] = slice == 0 ? skip : sum.skip[wave] + skip;
+            // The products' own operands keep 8 bits with bf16, as their results do.
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              if (2 * k + 1 < wave) continue;
+              const Frag<T> pf = frag_tiles<T>(pw[2 * k], pw[2 * k + 1]), qf = frag_tiles<T>(qw[2 * k], qw[2 * k + 1]);
+#pragma unroll
+              for (int p = 0; p < kPt; ++p) mma(dx[p], frag_col_result(s.dy, L::ldp, k * 32, p * 16), pf);
+#pragma unroll
+              for (int n = 0; n < 2 * NB; ++n) mma(db[n], frag_col_result(s.c, L::ldn, k * 32, n * 16), qf);
+            }
           }
-          float all = pair[0];
-          all += __shfl_xor(all, 16);
-          behind += all + __shfl_xor(all, 32);
-        }
-        direct += __shfl_xor(direct, 16);
-        direct += __shfl_xor(direct, 32);
-        if (g == 0) s.direct[sc] = slice == 0 ? direct : s.direct[sc] + direct;
-        skip = sum64(skip);
-        if (lane == 0) s.skip[wave] = slice == 0 ? skip : s.skip[wave] + skip;
-        // The products' own operands keep 8 bits with bf16, as their results do.
+          // ---- within the step, row t = mine
+          {
+            const float ch = dc.hi[mine], cl = dc.lo[mine];
+            v4f qw[4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          if (2 * k + 1 < wave) continue;
-          const Frag<T> pf = frag_tiles<T>(pw[2 * k], pw[2 * k + 1]), qf = frag_tiles<T>(qw[2 * k], qw[2 * k + 1]);
+            for (int si = 0; si < 4; ++si) {
+              qw[si] = v4f{0, 0, 0, 0};
+              if (si > wave) continue;
+              v4f yx = {0, 0, 0, 0};
 #pragma unroll
-          for (int p = 0; p < kPt; ++p) mma(dx[p], pf, frag_col_result(s.dy, L::ldp, k * 32, p * 16));
+              for (int k = 0; k < kKp; ++k)
+                mma(yx, frag_row(s.x, L::ldp, si * 16, k * 32), frag_row(s.dy, L::ldp, row, k * 32));
+              const int s0 = si * 16 + 4 * g;
+              const v4f hi = *reinterpret_cast<const v4f*>(&dc.hi[s0]), lo = *reinterpret_cast<const v4f*>(&dc.lo[s0]);
+              const v4f d = *reinterpret_cast<const v4f*>(&dc.d[s0]);
 #pragma unroll
-          for (int n = 0; n < 2 * NB; ++n) mma(db[n], qf, frag_col_result(s.c, L::ldn, k * 32, n * 16));
-        }
-      }
-      // ---- within the step, rows t of this wave
-      {
-        const int t = row + l15;
-        const float ch = s.dc.hi[t], cl = s.dc.lo[t];
-        v4f qw[4];
+              for (int i = 0; i < 4; ++i) {
+                float e = exp2_of((ch - hi[i]) + (cl - lo[i])) * d[i];
+                if (si == wave) e = mine >= s0 + i ? e : 0.0f;
+                qw[si][i] = yx[i] * e;
+              }
+            }
 #pragma unroll
-        for (int si = 0; si < 4; ++si) {
-          qw[si] = v4f{0, 0, 0, 0};
-          if (si > wave) continue;
-          v4f yx = {0, 0, 0, 0};
+            for (int k = 0; k < 2; ++k) {
+              if (2 * k > wave) continue;
+              const Frag<T> qf = frag_tiles<T>(qw[2 * k], qw[2 * k + 1]);
 #pragma unroll
-          for (int k = 0; k < kKp; ++k) mma(yx, frag_row(s.x, L::ldp, si * 16, k * 32), frag_row(s.dy, L::ldp, row, k * 32));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int sc = si * 16 + 4 * g + i;
-            const float e = t >= sc ? exp2_of((ch - s.dc.hi[sc]) + (cl - s.dc.lo[sc])) : 0.0f;
-            qw[si][i] = yx[i] * e * s.dc.d[sc];
+              for (int n = 0; n < 2 * NB; ++n) mma(dcc[n], frag_col_result(s.b, L::ldn, k * 32, n * 16), qf);
+            }
           }
         }
+        // ---- the starting state into this lane's row
+        {
+          Frag<T> yf[kKp];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          if (2 * k > wave) continue;
-          const Frag<T> qf = frag_tiles<T>(qw[2 * k], qw[2 * k + 1]);
+          for (int k = 0; k < kKp; ++k) yf[k] = frag_row(s.dy, L::ldp, row, k * 32);
+          const float from = dc.from[mine];
 #pragma unroll
-          for (int n = 0; n < 2 * NB; ++n) mma(dcc[n], qf, frag_col_result(s.b, L::ldn, k * 32, n * 16));
-        }
-      }
-      // ---- the starting state into this wave's rows
-      {
-        Frag<T> yf[kKp];
+          for (int n = 0; n < kNt; ++n) {
+            v4f o = {0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < kKp; ++k) yf[k] = frag_row(s.dy, L::ldp, row, k * 32);
-        float from[4], r[4] = {0, 0, 0, 0};
+            for (int k = 0; k < kKp; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) from[i] = s.dc.from[row + 4 * g + i];
-#pragma unroll
-        for (int n = 0; n < 2 * NB; ++n) {
-          v4f o = {0, 0, 0, 0};
-#pragma unroll
-          for (int k = 0; k < kKp; ++k)
-#pragma unroll
-            for (int z = 0; z < L::kTerms; ++z) mma(o, yf[k], frag_row(s.st[z], L::ldp, n * 16, k * 32));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            o[i] *= from[i];
-            r[i] = fmaf(static_cast<float>(s.c[(row + 4 * g + i) * L::ldn + n * 16 + l15]), o[i], r[i]);
-            dcc[n][i] += o[i];
+              for (int z = 0; z < L::kTerms; ++z) mma(o, frag_row(s.st[z], L::ldp, n * 16, k * 32), yf[k]);
+            const int nt = ph * kNt + n;
+            const v4f c = quad_get(&s.c[mine * L::ldn + nt * 16 + 4 * g]);
+            o *= from;
+            dcc[nt] += o;
+            o *= c;
+            after += (o[0] + o[1]) + (o[2] + o[3]);
           }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float v = sum16(r[i]);
-          const int t = row + 4 * g + i;
-          if (l15 == 0) s.after[t] = slice == 0 ? v : s.after[t] + v;
-        }
-      }
-      __syncthreads();  // the starting state's readers are done
-      {
-        float w = 0.0f;
-#pragma unroll
-        for (int i = 0; i < StateTile<T, NB, PT>::kN; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w = fmaf(ts.v[i][j], tg.v[i][j], w);
-        w = sum64(w);
-        if (lane == 0) s.whole[wave] = slice == 0 ? w : s.whole[wave] + w;
+        __syncthreads();  // the starting state's readers are done
         tg.store(s);
-      }
-      __syncthreads();
-      // ---- this wave's rows into what follows the step
-      {
-        float left[4], to[4], q[4] = {0, 0, 0, 0};
+        __syncthreads();
+        if (ph + 1 < kPhases) fetch_state(tg, ba.keep_g, h, p0, ph + 1);
+        else if (more) fetch_state(tg, ba.keep_g, hn, pn, 0);
+        // ---- this lane's row into what follows the step
+        {
+          const float left = dc.left[mine], to = dc.to[mine];
+          Frag<T> bf[L::kRows / 32];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          left[i] = s.dc.left[row + 4 * g + i];
-          to[i] = s.dc.to[row + 4 * g + i];
-        }
-        Frag<T> bf[NB];
+          for (int k = 0; k < L::kRows / 32; ++k) bf[k] = frag_row(s.b, L::ldn, row, ph * L::kRows + k * 32);
 #pragma unroll
-        for (int k = 0; k < NB; ++k) bf[k] = frag_row(s.b, L::ldn, row, k * 32);
+          for (int p = 0; p < kPt; ++p) {
+            v4f o = {0, 0, 0, 0};
 #pragma unroll
-        for (int p = 0; p < kPt; ++p) {
-          v4f o = {0, 0, 0, 0};
+            for (int k = 0; k < L::kRows / 32; ++k)
 #pragma unroll
-          for (int k = 0; k < NB; ++k)
+              for (int z = 0; z < L::kTerms; ++z) mma(o, frag_col(s.st[z], L::ldp, k * 32, p * 16), bf[k]);
+            const v4f x = quad_get(&s.x[mine * L::ldp + p * 16 + 4 * g]);
+            o *= left;
+            dx[p] += o;
+            o *= x;
+            before += (o[0] + o[1]) + (o[2] + o[3]);
+          }
+          Frag<T> xf[kKp];
 #pragma unroll
-            for (int z = 0; z < L::kTerms; ++z) mma(o, bf[k], frag_col(s.st[z], L::ldp, k * 32, p * 16));
+          for (int k = 0; k < kKp; ++k) xf[k] = frag_row(s.x, L::ldp, row, k * 32);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            o[i] *= left[i];
-            q[i] = fmaf(static_cast<float>(s.x[(row + 4 * g + i) * L::ldp + p * 16 + l15]), o[i], q[i]);
-            dx[p][i] += o[i];
+          for (int n = 0; n < kNt; ++n) {
+            v4f o = {0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < kKp; ++k) mma(o, frag_row(s.st[0], L::ldp, n * 16, k * 32), xf[k]);
+            db[ph * kNt + n] += to * o;
           }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float v = sum16(q[i]);
-          const int t = row + 4 * g + i;
-          if (l15 == 0) s.before[t] = slice == 0 ? v : s.before[t] + v;
-        }
-        Frag<T> xf[kKp];
-#pragma unroll
-        for (int k = 0; k < kKp; ++k) xf[k] = frag_row(s.x, L::ldp, row, k * 32);
-#pragma unroll
-        for (int n = 0; n < 2 * NB; ++n) {
-          v4f o = {0, 0, 0, 0};
-#pragma unroll
-          for (int k = 0; k < kKp; ++k) mma(o, xf[k], frag_row(s.st[0], L::ldp, n * 16, k * 32));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) db[n][i] = fmaf(to[i], o[i], db[n][i]);
-        }
       }
-      // d_x through this wave's own rows of the x tile to rows of 16 bytes
+      after = sum_groups(after);
+      before = sum_groups(before);
+      whole = sum64(whole);
+      if (g == 0) {
+        sum.after[mine] = slice == 0 ? after : sum.after[mine] + after;
+        sum.before[mine] = slice == 0 ? before : sum.before[mine] + before;
+      }
+      if (lane == 0) sum.whole[wave] = slice == 0 ? whole : sum.whole[wave] + whole;
+      const Rsrc ro = rows_rsrc(op + h * a.width + p0, ba.d_x.row_stride, rows, cols);
+      const float d = dc.d[mine];
 #pragma unroll
-      for (int p = 0; p < kPt; ++p)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = row + 4 * g + i, at = t * L::ldp + p * 16 + l15;
-          s.x[at] = static_cast<T>(fmaf(D, static_cast<float>(s.dy[at]), s.dc.d[t] * dx[p][i]));
-        }
-      constexpr int kVec = Vec<T>::n, kPerRow = L::kP / kVec;
-#pragma unroll
-      for (int i = 0; i < 16 * kPerRow / 64; ++i) {
-        const int r = row + (lane + i * 64) / kPerRow, c = (lane + i * 64) % kPerRow * kVec;
-        if (r < rows && c < cols)
-          *reinterpret_cast<typename Vec<T>::type*>(op + r * ba.d_x.row_stride + h * a.width + p0 + c) =
-              *reinterpret_cast<const typename Vec<T>::type*>(s.x + r * L::ldp + c);
+      for (int p = 0; p < kPt; ++p) {
+        const int c = p * 16 + 4 * g;
+        const v4f v = d * dx[p] + D * quad_get(&s.dy[mine * L::ldp + c]);
+        Quad<T>::store(ro, c < cols ? static_cast<unsigned>((mine * static_cast<int>(ba.d_x.row_stride) + c) * sizeof(T))
+                                    : kOutside, v);
       }
     }
-    __syncthreads();
-    // ---- the step sizes' gradients: wave 0, a token per lane
-    if (wave == 0) {
-      const float d = s.dc.d[lane];
-      const float after = __shfl(scan64(__shfl(s.after[lane], 63 - lane)), 63 - lane);
-      const float q = d * s.before[lane];
-      float upto = __shfl_up(scan64(q), 1);
-      if (lane == 0) upto = 0.0f;
-      const float whole = ((s.whole[0] + s.whole[1]) + (s.whole[2] + s.whole[3])) * s.dc.total;
-      const float inner = (s.inner[0][lane] + s.inner[1][lane]) + (s.inner[2][lane] + s.inner[3][lane]);
-      const float m = inner + after + upto + whole;
-      float dd = s.direct[lane] + s.before[lane] + A * m;
-      if (a.softplus) dd *= 1.0f / (1.0f + expf(-(raw + bias)));
-      float dA = d * m;
-      if (lane < rows) {
-        const long i = (u.t0 + lane) * ba.d_dt.row_stride + h;
-        if (a.dt_bf16) seq_ptr<bf16>(ba.d_dt, u.seq, u.row0, packed)[i] = static_cast<bf16>(dd);
-        else seq_ptr<float>(ba.d_dt, u.seq, u.row0, packed)[i] = dd;
-      } else {
-        dd = dA = 0.0f;
-      }
-      dA = sum64(dA);
-      dd = sum64(dd);
-      if (lane == 0) {
-        float* p = ba.part + (static_cast<long>(step) * a.heads + h) * 4;
-        p[0] = dA;
-        p[1] = (s.skip[0] + s.skip[1]) + (s.skip[2] + s.skip[3]);
-        p[2] = dd;
-      }
+    if (h + 1 == h1) {
+      __syncthreads();
+      if (wave == 0) finish(h, cur, par);
     }
+    cur = next;
+    par ^= 1;
   }
 
-  // ---- d_B and d_C, through this wave's own rows of the b and c tiles
-  __syncthreads();
+  // ---- d_B and d_C
   if (ba.splits > 1) {
     const long r0 = (packed ? u.row0 : static_cast<long>(u.seq) * a.q.length) + u.t0;
-    const long at = (split * ba.rows + r0) * ba.groups + gr;
+    const long at = ((split * ba.rows + r0) * ba.groups + gr) * a.states;
+    const int stride = ba.groups * a.states;
+    const Rsrc rb = rows_rsrc(ba.part_b + at, stride, rows, a.states);
+    const Rsrc rc = rows_rsrc(ba.part_c + at, stride, rows, a.states);
 #pragma unroll
-    for (int n = 0; n < 2 * NB; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = row + 4 * g + i, c = n * 16 + l15;
-        if (t < rows && c < a.states) {
-          const long e = (at + static_cast<long>(t) * ba.groups) * a.states + c;
-          ba.part_b[e] = db[n][i];
-          ba.part_c[e] = dcc[n][i];
-        }
-      }
+    for (int n = 0; n < 2 * NB; ++n) {
+      const int c = n * 16 + 4 * g;
+      const unsigned off = c < a.states ? static_cast<unsigned>((mine * stride + c) * 4) : kOutside;
+      Quad<float>::store(rb, off, db[n]);
+      Quad<float>::store(rc, off, dcc[n]);
+    }
     return;
   }
+  const Rsrc rb = rows_rsrc(seq_ptr<T>(ba.d_B, u.seq, u.row0, packed) + u.t0 * ba.d_B.row_stride + gr * a.states,
+                            ba.d_B.row_stride, rows, a.states);
+  const Rsrc rc = rows_rsrc(seq_ptr<T>(ba.d_C, u.seq, u.row0, packed) + u.t0 * ba.d_C.row_stride + gr * a.states,
+                            ba.d_C.row_stride, rows, a.states);
 #pragma unroll
-  for (int n = 0; n < 2 * NB; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int at = (row + 4 * g + i) * L::ldn + n * 16 + l15;
-      s.b[at] = static_cast<T>(db[n][i]);
-      s.c[at] = static_cast<T>(dcc[n][i]);
-    }
-  T* bp = seq_ptr<T>(ba.d_B, u.seq, u.row0, packed) + u.t0 * ba.d_B.row_stride + gr * a.states;
-  T* cp = seq_ptr<T>(ba.d_C, u.seq, u.row0, packed) + u.t0 * ba.d_C.row_stride + gr * a.states;
-  constexpr int kVec = Vec<T>::n, kPerRow = L::kN / kVec;
-#pragma unroll
-  for (int i = 0; i < 16 * kPerRow / 64; ++i) {
-    const int r = row + (lane + i * 64) / kPerRow, c = (lane + i * 64) % kPerRow * kVec;
-    if (r < rows && c < a.states) {
-      *reinterpret_cast<typename Vec<T>::type*>(bp + r * ba.d_B.row_stride + c) =
-          *reinterpret_cast<const typename Vec<T>::type*>(s.b + r * L::ldn + c);
-      *reinterpret_cast<typename Vec<T>::type*>(cp + r * ba.d_C.row_stride + c) =
-          *reinterpret_cast<const typename Vec<T>::type*>(s.c + r * L::ldn + c);
-    }
+  for (int n = 0; n < 2 * NB; ++n) {
+    const int c = n * 16 + 4 * g;
+    const bool in = c < a.states;
+    Quad<T>::store(rb, in ? static_cast<unsigned>((mine * static_cast<int>(ba.d_B.row_stride) + c) * sizeof(T)) : kOutside,
+                   db[n]);
+    Quad<T>::store(rc, in ? static_cast<unsigned>((mine * static_cast<int>(ba.d_C.row_stride) + c) * sizeof(T)) : kOutside,
+                   dcc[n]);
   }
 }
 
@@ -544,7 +590,7 @@ int make_plan(const mamba2_seqs& q, const mamba2_ssm_dims& d, Plan* p) {
 
 struct Call {
   BwdArgs ba;
-  Walk f, r;
+  Walks w;
   Plan p;
   float *d_A, *d_D, *d_bias;
   hipStream_t s;
@@ -555,13 +601,13 @@ int launch_bwd(const Call& c) {
   const SsmArgs& a = c.ba.a;
   const dim3 grid(static_cast<unsigned>(static_cast<long>(c.p.units) * a.heads * c.p.slices), 2);
   if (c.p.segments) {
-    ssm_walk_summary_kernel<T, NB, NW><<<grid, NW * 64, 0, c.s>>>(a, c.f, c.r);
+    ssm_walk_summary_kernel<T, NB, NW><<<grid, NW * 64, 0, c.s>>>(a, c.w);
     if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
     const unsigned quads = static_cast<unsigned>((a.states * a.width + 1023) / 1024);
-    ssm_walk_carry_kernel<<<dim3(quads, a.heads, 2 * a.q.batch), 256, 0, c.s>>>(a, c.f, c.r);
+    ssm_walk_carry_kernel<<<dim3(quads, a.heads, 2 * a.q.batch), 256, 0, c.s>>>(a, c.w);
     if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
   }
-  ssm_walk_kernel<T, NB, NW><<<grid, NW * 64, 0, c.s>>>(a, c.f, c.r);
+  ssm_walk_kernel<T, NB, NW><<<grid, NW * 64, 0, c.s>>>(a, c.w);
   if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
   const unsigned blocks = static_cast<unsigned>(static_cast<long>(c.p.steps) * c.ba.groups * c.p.splits);
   ssm_bwd_kernel<T, NB, NW><<<blocks, kBwdThreads, 0, c.s>>>(c.ba);
@@ -608,7 +654,7 @@ int mamba2_ssm_bwd(mamba2_seqs q, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows 
   Call c = {};
   int st = make_plan(q, d, &c.p);
   if (st != MAMBA2_SCAN_OK) return st;
-  const size_t e = type_size(d.type), de = type_size(d.dt_type);
+  const size_t e = type_size(d.type);
   const long long xw = static_cast<long long>(d.heads) * d.width, bw = static_cast<long long>(d.groups) * d.states;
   if (A == nullptr || d_A == nullptr || workspace == nullptr) return MAMBA2_SCAN_ENULL;
   const mamba2_rows* wide[4] = {&x, &d_y, &d_x, nullptr};
@@ -617,8 +663,7 @@ int mamba2_ssm_bwd(mamba2_seqs q, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows 
   const mamba2_rows* shared[5] = {&B, &C, &d_B, &d_C, nullptr};
   for (int i = 0; shared[i] != nullptr; ++i)
     if ((st = check_vec_rows(*shared[i], q, bw, e)) != MAMBA2_SCAN_OK) return st;
-  if ((st = check_rows(dt, q, d.heads, de)) != MAMBA2_SCAN_OK ||
-      (st = check_rows(d_dt, q, d.heads, de)) != MAMBA2_SCAN_OK)
+  if ((st = check_step_rows(dt, q, d)) != MAMBA2_SCAN_OK || (st = check_step_rows(d_dt, q, d)) != MAMBA2_SCAN_OK)
     return st;
   if (workspace_bytes < c.p.total * sizeof(float)) return MAMBA2_SCAN_ESIZE;
   if (!aligned_to(A, 4) || !aligned_to(D, 4) || !aligned_to(dt_bias, 4) || !aligned_to(initial_state, 16) ||
@@ -654,20 +699,21 @@ int mamba2_ssm_bwd(mamba2_seqs q, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows 
     w += n;
     return p;
   };
-  c.f.v = x;
-  c.f.m = B;
-  c.f.first = initial_state;
-  c.f.keep = take(c.p.keep);
-  c.f.seg_state = take(c.p.seg_state);
-  c.f.seg_decay = take(c.p.seg_decay);
-  c.r.v = d_y;
-  c.r.m = C;
-  c.r.first = d_final_state;
-  c.r.last = d_initial_state;
-  c.r.keep = take(c.p.keep);
-  c.r.seg_state = take(c.p.seg_state);
-  c.r.seg_decay = take(c.p.seg_decay);
-  c.r.rev = 1;
+  Walk &f = c.w.w[0], &r = c.w.w[1];
+  f.v = x;
+  f.m = B;
+  f.first = initial_state;
+  f.keep = take(c.p.keep);
+  f.seg_state = take(c.p.seg_state);
+  f.seg_decay = take(c.p.seg_decay);
+  r.v = d_y;
+  r.m = C;
+  r.first = d_final_state;
+  r.last = d_initial_state;
+  r.keep = take(c.p.keep);
+  r.seg_state = take(c.p.seg_state);
+  r.seg_decay = take(c.p.seg_decay);
+  r.rev = 1;
   c.ba.part_b = take(c.p.part_bc);
   c.ba.part_c = take(c.p.part_bc);
   c.ba.part = take(c.p.part);
@@ -676,8 +722,8 @@ int mamba2_ssm_bwd(mamba2_seqs q, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows 
   c.ba.d_dt = d_dt;
   c.ba.d_B = d_B;
   c.ba.d_C = d_C;
-  c.ba.keep_s = c.f.keep;
-  c.ba.keep_g = c.r.keep;
+  c.ba.keep_s = f.keep;
+  c.ba.keep_g = r.keep;
   c.ba.rows = c.p.rows;
   c.ba.steps = c.p.steps;
   c.ba.groups = d.groups;

@@ -138,62 +138,121 @@ __device__ __forceinline__ Frag<float> frag_col_result(const float* p, int ld, i
   return f;
 }
 
-// Eight fp32 values as an operand.  bf16 keeps 8 of their bits; the remainder
-// rounded the same way (`rest`) brings a product to 16.
-template <class T>
-__device__ __forceinline__ Frag<T> frag_of(const float (&v)[8], Frag<T>* rest);
-template <>
-__device__ __forceinline__ Frag<bf16> frag_of<bf16>(const float (&v)[8], Frag<bf16>* rest) {
-  Frag<bf16> f;
+// Eight fp32 values as an operand in TERMS parts that add up to it: with bf16
+// each part holds 8 more bits (3 parts: all 24), fp32 needs one.
+template <class T, int TERMS>
+struct Split {
+  Frag<T> f[TERMS];
+};
+template <class T, int TERMS>
+__device__ __forceinline__ Split<T, TERMS> split_of(const float (&v)[8]) {
+  Split<T, TERMS> s;
+  if constexpr (sizeof(T) == 4) {
+    s.f[0] = {{{v[0], v[1], v[2], v[3]}, {v[4], v[5], v[6], v[7]}}};
+  } else {
+    float r[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) f.v[j] = static_cast<bf16>(v[j]);
-  if (rest != nullptr) {
+    for (int j = 0; j < 8; ++j) r[j] = v[j];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) rest->v[j] = static_cast<bf16>(v[j] - static_cast<float>(f.v[j]));
+    for (int t = 0; t < TERMS; ++t)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s.f[t].v[j] = static_cast<bf16>(r[j]);
+        if (t + 1 < TERMS) r[j] -= static_cast<float>(s.f[t].v[j]);
+      }
   }
-  return f;
+  return s;
 }
-template <>
-__device__ __forceinline__ Frag<float> frag_of<float>(const float (&v)[8], Frag<float>*) {
-  return {{{v[0], v[1], v[2], v[3]}, {v[4], v[5], v[6], v[7]}}};
+template <class T>
+__device__ __forceinline__ Frag<T> frag_of(const float (&v)[8]) {
+  return split_of<T, 1>(v).f[0];
 }
 __device__ __forceinline__ float frag_get(const Frag<bf16>& f, int j) { return static_cast<float>(f.v[j]); }
 __device__ __forceinline__ float frag_get(const Frag<float>& f, int j) { return f.v[j >> 2][j & 3]; }
+template <class T>
+constexpr int kExact = sizeof(T) == 2 ? 3 : 1;  // parts that hold an fp32 value whole
 
 // ------------------------------------------------------------------- tiles
-// A tile of R rows (tokens) by C columns of a token-major tensor, moved by
-// THREADS threads in 16-byte vectors: loads() issues the global loads,
-// stores() puts them into LDS.  Rows from `rows` on and columns from `cols`
-// on are zero.
+// Tiles are moved through buffer resources that end with the last valid row:
+// loads behind it give zero and stores are dropped, so a step's ragged end
+// needs no branches.  A column outside the tensor gets an offset outside any
+// resource.  Offsets within a step's 64 rows fit 31 bits (check_vec_rows).
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+constexpr unsigned kOutside = 0x80000000u;
+
+__device__ __forceinline__ Rsrc make_rsrc(const void* p, unsigned bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
+}
+// `rows` rows of `width` elements, `stride` elements apart.
+template <class T>
+__device__ __forceinline__ Rsrc rows_rsrc(const T* p, long stride, int rows, int width) {
+  return make_rsrc(p, rows > 0 ? static_cast<unsigned>(((rows - 1) * stride + width) * sizeof(T)) : 0u);
+}
+
+// R rows (tokens) by C columns of a token-major tensor, moved by THREADS
+// threads in 16-byte vectors; `cols` of the columns exist.
 template <class T, int R, int C, int THREADS>
 struct Tile {
   static constexpr int kVec = Vec<T>::n;
   static constexpr int kPerRow = C / kVec;
   static constexpr int kN = (R * kPerRow + THREADS - 1) / THREADS;
-  typename Vec<T>::type v[kN];
+  v4i v[kN];
+  unsigned off[kN];
 
-  __device__ __forceinline__ void load(const T* p, long stride, int rows, int cols, int tid) {
+  __device__ __forceinline__ void init(long stride, int cols, int tid) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int e = tid + i * THREADS;
-      const int r = e / kPerRow, c = e % kPerRow * kVec;
-      if (r < rows && c < cols) {
-        v[i] = *reinterpret_cast<const typename Vec<T>::type*>(p + r * stride + c);
-      } else {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) v[i][j] = static_cast<T>(0.0f);
-      }
+      const int e = tid + i * THREADS, r = e / kPerRow, c = e % kPerRow * kVec;
+      off[i] = (c < cols && r < R) ? static_cast<unsigned>((r * static_cast<int>(stride) + c) * sizeof(T)) : kOutside;
     }
+  }
+  __device__ __forceinline__ void load(Rsrc rs) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, off[i], 0, 0);
   }
   __device__ __forceinline__ void store(T* lds, int ld, int tid) const {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int e = tid + i * THREADS;
-      const int r = e / kPerRow, c = e % kPerRow * kVec;
-      if (R * kPerRow % THREADS == 0 || r < R) *reinterpret_cast<typename Vec<T>::type*>(lds + r * ld + c) = v[i];
+      const int e = tid + i * THREADS, r = e / kPerRow, c = e % kPerRow * kVec;
+      if (R * kPerRow % THREADS == 0 || r < R) *reinterpret_cast<v4i*>(lds + r * ld + c) = v[i];
     }
   }
 };
+
+// Four consecutive elements of type T.
+template <class T>
+struct Quad;
+template <>
+struct Quad<bf16> {
+  typedef v4bf type;
+  static __device__ __forceinline__ void store(Rsrc rs, unsigned off, v4f v) {
+    v4bf r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = static_cast<bf16>(v[i]);
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2i, r), rs, off, 0, 0);
+  }
+};
+template <>
+struct Quad<float> {
+  typedef v4f type;
+  static __device__ __forceinline__ void store(Rsrc rs, unsigned off, v4f v) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, v), rs, off, 0, 0);
+  }
+};
+template <class T>
+__device__ __forceinline__ v4f quad_get(const T* p) {
+  const typename Quad<T>::type r = *reinterpret_cast<const typename Quad<T>::type*>(p);
+  return v4f{static_cast<float>(r[0]), static_cast<float>(r[1]), static_cast<float>(r[2]), static_cast<float>(r[3])};
+}
+template <class T>
+__device__ __forceinline__ void quad_put(T* p, v4f v) {
+  typename Quad<T>::type r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = static_cast<T>(v[i]);
+  *reinterpret_cast<typename Quad<T>::type*>(p) = r;
+}
 
 // ------------------------------------------------------------------ decays
 // v + the lane's DPP neighbour, where the DPP control reaches one (else v).
@@ -242,16 +301,36 @@ __device__ __forceinline__ float exp2_of(double v) {
   return exp2_of(static_cast<float>(v - r)) * exp2_of(static_cast<float>(r));
 }
 
-__device__ __forceinline__ float raw_step(const SsmArgs& a, const mamba2_rows& r, const void* base, int t, int h) {
-  const long i = t * r.row_stride + h;
-  return a.dt_bf16 ? static_cast<float>(static_cast<const bf16*>(base)[i]) : static_cast<const float*>(base)[i];
+// The raw step sizes of a step's tokens; token behind the last give zero.
+__device__ __forceinline__ Rsrc step_rsrc(const SsmArgs& a, const Unit& u, bool packed, int t, int rows) {
+  if (a.dt_bf16) return rows_rsrc(seq_ptr<const bf16>(a.dt, u.seq, u.row0, packed) + t * a.dt.row_stride,
+                                  a.dt.row_stride, rows, a.heads);
+  return rows_rsrc(seq_ptr<const float>(a.dt, u.seq, u.row0, packed) + t * a.dt.row_stride, a.dt.row_stride, rows,
+                   a.heads);
 }
-// softplus(v) = log(1 + e^v), whole for large v and to full precision for
-// very negative ones.
+__device__ __forceinline__ float load_raw(const SsmArgs& a, Rsrc rs, int h) {
+  const int e = static_cast<int>(threadIdx.x & 63) * static_cast<int>(a.dt.row_stride) + h;
+  if (a.dt_bf16)
+    return __builtin_bit_cast(float, static_cast<unsigned>(
+               static_cast<unsigned short>(__builtin_amdgcn_raw_buffer_load_b16(rs, e * 2, 0, 0))) << 16);
+  return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, e * 4, 0, 0));
+}
+// softplus(v) = log(1 + e^v) to fp32's last bits.  e^v: the product with
+// log2(e) in two terms.  log(1 + t): log(w) t / (w - 1) with w = 1 + t rounded
+// cancels that rounding (Kahan); below 2^-6, where w - 1 keeps few bits of t,
+// the series.
 __device__ __forceinline__ float step_of(const SsmArgs& a, float raw, float bias) {
   const float v = raw + bias;
   if (!a.softplus) return v;
-  return v > 20.0f ? v : log1pf(expf(v));
+  const float p = v * kLog2e;
+  const float rest = fmaf(v, 1.925963033500e-8f, fmaf(v, kLog2e, -p));  // log2(e) - kLog2e, and p's rounding
+  float t = exp2_of(p);
+  t = fmaf(t, 0.69314718056f * rest, t);
+  const float w = 1.0f + t;
+  const float kahan = __builtin_amdgcn_logf(w) * 0.69314718056f * (t * __builtin_amdgcn_rcpf(w - 1.0f));
+  const float series = t * fmaf(t, fmaf(t, fmaf(t, -0.25f, 0.33333333f), -0.5f), 1.0f);
+  const float s = t < 0.015625f ? series : kahan;
+  return v > 20.0f ? v : v < -80.0f ? expf(v) : s;
 }
 
 // The decays of a step of kTok tokens.  Sums of log2 decays are formed in 64
@@ -310,55 +389,87 @@ struct Walk {
   int rev;
 };
 
-template <int NB>
-__device__ __forceinline__ void load_state(v4f (&st)[2 * NB], const float* p, int width, int states, int col,
-                                           bool live) {
-  const int g = (threadIdx.x & 63) >> 4;
-#pragma unroll
-  for (int n = 0; n < 2 * NB; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = n * 16 + 4 * g + i;
-      st[n][i] = (p != nullptr && live && r < states) ? p[static_cast<long>(r) * width + col] : 0.0f;
-    }
-}
-template <int NB>
-__device__ __forceinline__ void save_state(const v4f (&st)[2 * NB], float* p, int width, int states, int col,
-                                           bool live) {
-  const int g = (threadIdx.x & 63) >> 4;
-#pragma unroll
-  for (int n = 0; n < 2 * NB; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = n * 16 + 4 * g + i;
-      if (live && r < states) p[static_cast<long>(r) * width + col] = st[n][i];
-    }
-}
+// A wave's 16 columns of a state [states][width], as fp32 results.  COLS true:
+// lane l has column l & 15, rows 4 g + i (the order an operand needs); false:
+// lane l has row l & 15 of each 16, columns 4 g + i (16-byte accesses).
+template <int NB, bool COLS>
+struct State {
+  v4f st[2 * NB];
+  unsigned off;    // bytes, of the lane's first element; kOutside for a column that does not exist
 
-// S = total S + M^T (coef_s v_s) for a wave's 16 columns; vf holds v.  With
-// bf16 the scaled v is kept in two terms: M is exact, so the state's sums
-// carry 16 bits of each product instead of 8.
-template <class T, int NB>
-__device__ __forceinline__ void advance_state(v4f (&st)[2 * NB], float total, const float* coef, const T* m, int ldn,
-                                              const Frag<T> (&vf)[2]) {
-  const int g = (threadIdx.x & 63) >> 4;
+  __device__ __forceinline__ void init(int width, int col0, int wave) {
+    const int l = threadIdx.x & 63, l15 = l & 15, g = l >> 4;
+    const int c = col0 + wave * 16 + (COLS ? l15 : 4 * g), r = COLS ? 4 * g : l15;
+    off = c < width ? static_cast<unsigned>((r * width + c) * 4) : kOutside;
+  }
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-  for (int n = 0; n < 2 * NB; ++n) st[n] *= total;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = frag_get(vf[k], j) * coef[k * 32 + 8 * g + j];
-    Frag<T> lo;
-    const Frag<T> hi = frag_of<T>(v, &lo);
+    for (int n = 0; n < 2 * NB; ++n) st[n] = v4f{0, 0, 0, 0};
+  }
+  static __device__ __forceinline__ Rsrc rsrc(const float* p, int width, int states) {
+    return make_rsrc(p, static_cast<unsigned>(states * width * 4));
+  }
+  __device__ __forceinline__ void load(const float* p, int width, int states) {
+    if (p == nullptr) {
+      zero();
+      return;
+    }
+    const Rsrc rs = rsrc(p, width, states);
 #pragma unroll
     for (int n = 0; n < 2 * NB; ++n) {
-      const Frag<T> mf = frag_col(m, ldn, k * 32, n * 16);
-      mma(st[n], mf, hi);
-      if constexpr (sizeof(T) == 2) mma(st[n], mf, lo);
+      const unsigned o = off + n * 64 * width;
+      if constexpr (COLS) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          st[n][i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, o + i * 4 * width, 0, 0));
+      } else {
+        st[n] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0));
+      }
     }
   }
-}
+  __device__ __forceinline__ void save(float* p, int width, int states) const {
+    const Rsrc rs = rsrc(p, width, states);
+#pragma unroll
+    for (int n = 0; n < 2 * NB; ++n) {
+      const unsigned o = off + n * 64 * width;
+      if constexpr (COLS) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(st[n][i]), rs, o + i * 4 * width, 0, 0);
+      } else {
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, st[n]), rs, o, 0, 0);
+      }
+    }
+  }
+  // S = total S + M^T (coef_s v_s); vf holds v.  With bf16 the scaled v goes
+  // in whole, in three parts: M is exact, so the state keeps fp32's precision.
+  template <class T>
+  __device__ __forceinline__ void advance(float total, const float* coef, const T* m, int ldn,
+                                          const Frag<T> (&vf)[2]) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int n = 0; n < 2 * NB; ++n) st[n] *= total;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float v[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const v4f c = *reinterpret_cast<const v4f*>(coef + k * 32 + 8 * g + 4 * h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[4 * h + j] = frag_get(vf[k], 4 * h + j) * c[j];
+      }
+      const auto parts = split_of<T, kExact<T>>(v);
+#pragma unroll
+      for (int n = 0; n < 2 * NB; ++n) {
+        const Frag<T> mf = frag_col(m, ldn, k * 32, n * 16);
+#pragma unroll
+        for (int z = 0; z < kExact<T>; ++z) {
+          if constexpr (COLS) mma(st[n], mf, parts.f[z]); else mma(st[n], parts.f[z], mf);
+        }
+      }
+    }
+  }
+};
 
 template <class T, int NB, int NW>
 struct WalkLds {
@@ -366,7 +477,7 @@ struct WalkLds {
   static constexpr int ldp = stride_of<T>(NW * 16);
   alignas(16) T m[kTok * ldn];
   alignas(16) T v[kTok * ldp];
-  alignas(16) Decays dc;
+  alignas(16) Decays dc[2];
 };
 
 // KEEP false: the summary of a segment that another follows, from a zero
@@ -390,59 +501,78 @@ __device__ __forceinline__ void walk(const SsmArgs& a, const Walk& w, WalkLds<T,
   const bool packed = a.q.offsets != nullptr;
   const int p0 = slice * NW * 16;
   const int cols = min(a.width - p0, NW * 16);
-  const int col = p0 + wave * 16 + (lane & 15);
-  const bool live = col < a.width;
   const long head = static_cast<long>(a.states) * a.width;
   const T* vp = seq_ptr<const T>(w.v, u.seq, u.row0, packed) + h * a.width + p0;
   const T* mp = seq_ptr<const T>(w.m, u.seq, u.row0, packed) + h / a.ratio * a.states;
-  const void* dtp = a.dt_bf16 ? static_cast<const void*>(seq_ptr<const bf16>(a.dt, u.seq, u.row0, packed))
-                              : static_cast<const void*>(seq_ptr<const float>(a.dt, u.seq, u.row0, packed));
   const float A = a.A[h], bias = a.bias != nullptr ? a.bias[h] : 0.0f;
   const long at = static_cast<long>(unit) * a.heads + h;
   const long of_seq = (static_cast<long>(u.seq) * a.heads + h) * head;
-  v4f st[2 * NB];
-  {
-    const float* from = nullptr;
-    if (KEEP) from = first ? (w.first == nullptr ? nullptr : w.first + of_seq) : w.seg_state + at * head;
-    load_state<NB>(st, from, a.width, a.states, col, live);
+  State<NB, false> st;
+  st.init(a.width, p0, wave);
+  if (KEEP) {
+    const float* from = first ? (w.first == nullptr ? nullptr : w.first + of_seq) : w.seg_state + at * head;
+    st.load(from, a.width, a.states);
+  } else {
+    st.zero();
   }
   double decay = 0.0;
   Tile<T, kTok, NB * 32, kThreads> tm;
   Tile<T, kTok, NW * 16, kThreads> tv;
-  float raw = 0.0f;
+  tm.init(w.m.row_stride, a.states, tid);
+  tv.init(w.v.row_stride, cols, tid);
   const int end = min(u.t0 + a.seg, u.len);
   const int steps = (end - u.t0 + kTok - 1) / kTok;
   const auto token = [&](int i) { return u.t0 + (w.rev ? steps - 1 - i : i) * kTok; };
   const auto fetch = [&](int t) {
-    const int rows = end - t;
-    tm.load(mp + t * w.m.row_stride, w.m.row_stride, rows, a.states, tid);
-    tv.load(vp + t * w.v.row_stride, w.v.row_stride, rows, cols, tid);
-    if (wave == 0 && lane < rows) raw = raw_step(a, a.dt, dtp, t + lane, h);
+    const int rows = min(end - t, kTok);
+    tm.load(rows_rsrc(mp + t * w.m.row_stride, w.m.row_stride, rows, a.states));
+    tv.load(rows_rsrc(vp + t * w.v.row_stride, w.v.row_stride, rows, cols));
   };
-  if (steps > 0) fetch(token(0));
+  // The last wave prepares the next step's decays while the others multiply;
+  // the raw step sizes are loaded a step before that.
+  const bool decays = wave == NW - 1;
+  float raw = 0.0f;
+  const auto fetch_raw = [&](int t) { raw = load_raw(a, step_rsrc(a, u, packed, t, min(end - t, kTok)), h); };
+  const auto prepare = [&](Decays& dc, int t) {
+    make_decays(dc, lane < end - t ? step_of(a, raw, bias) : 0.0f, A);
+  };
+  if (steps > 0) {
+    fetch(token(0));
+    if (decays) {
+      fetch_raw(token(0));
+      prepare(s.dc[0], token(0));
+      if (steps > 1) fetch_raw(token(1));
+    }
+  }
   for (int i = 0; i < steps; ++i) {
     const int t = token(i);
+    const Decays& dc = s.dc[i & 1];
     __syncthreads();
     tm.store(s.m, L::ldn, tid);
     tv.store(s.v, L::ldp, tid);
-    if (wave == 0) make_decays(s.dc, lane < end - t ? step_of(a, raw, bias) : 0.0f, A);
     __syncthreads();
-    if (i + 1 < steps) fetch(token(i + 1));
+    if (i + 1 < steps) {
+      fetch(token(i + 1));
+      if (decays) {
+        prepare(s.dc[(i + 1) & 1], token(i + 1));
+        if (i + 2 < steps) fetch_raw(token(i + 2));
+      }
+    }
     if (KEEP) {
       const long step = static_cast<long>(unit_base(a.q, u.seq, kTok)) + t / kTok;
-      save_state<NB>(st, w.keep + (step * a.heads + h) * head, a.width, a.states, col, live);
+      st.save(w.keep + (step * a.heads + h) * head, a.width, a.states);
     }
     Frag<T> vf[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) vf[k] = frag_col(s.v, L::ldp, k * 32, wave * 16);
-    advance_state<T, NB>(st, s.dc.total, w.rev ? s.dc.from : s.dc.to, s.m, L::ldn, vf);
-    if (!KEEP) decay += s.dc.end;
+    st.template advance<T>(dc.total, w.rev ? dc.from : dc.to, s.m, L::ldn, vf);
+    if (!KEEP) decay += dc.end;
   }
   if (KEEP) {
-    if (last && w.last != nullptr) save_state<NB>(st, w.last + of_seq, a.width, a.states, col, live);
+    if (last && w.last != nullptr) st.save(w.last + of_seq, a.width, a.states);
   } else {
     const long next = at + (w.rev ? -a.heads : a.heads);
-    save_state<NB>(st, w.seg_state + next * head, a.width, a.states, col, live);
+    st.save(w.seg_state + next * head, a.width, a.states);
     if (tid == 0 && slice == 0) w.seg_decay[at] = exp2_of(decay);
   }
 }
@@ -463,17 +593,34 @@ __device__ __forceinline__ void carry(const SsmArgs& a, const Walk& w, int seq) 
   if (w.first != nullptr)
     run = *reinterpret_cast<const v4f*>(w.first + (static_cast<long>(seq) * a.heads + h) * head + e);
   const int d = w.rev ? -1 : 1;
-  for (int i = w.rev ? n - 2 : 1; i >= 0 && i < n; i += d) {
-    const long at = (base + i) * a.heads + h;
-    v4f* p = reinterpret_cast<v4f*>(w.seg_state + at * head + e);
-    run = run * w.seg_decay[at - d * a.heads] + *p;
-    *p = run;
+  constexpr int kAhead = 8;  // segments whose states are in flight together
+  for (int i = w.rev ? n - 2 : 1; i >= 0 && i < n; i += d * kAhead) {
+    v4f own[kAhead];
+    float decay[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = i + d * j;
+      if (k >= 0 && k < n) {
+        const long at = (base + k) * a.heads + h;
+        own[j] = *reinterpret_cast<const v4f*>(w.seg_state + at * head + e);
+        decay[j] = w.seg_decay[at - d * a.heads];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = i + d * j;
+      if (k >= 0 && k < n) {
+        run = run * decay[j] + own[j];
+        *reinterpret_cast<v4f*>(w.seg_state + ((base + k) * a.heads + h) * head + e) = run;
+      }
+    }
   }
 }
 
 // Host side, in ssm.hip.
 int check_dims(const mamba2_seqs& q, const mamba2_ssm_dims& d);
 int check_vec_rows(const mamba2_rows& r, const mamba2_seqs& q, long long width, size_t elem);
+int check_step_rows(const mamba2_rows& r, const mamba2_seqs& q, const mamba2_ssm_dims& d);
 int waves_of(int width);
 int segment_tokens(const mamba2_seqs& q, const mamba2_ssm_dims& d);
 

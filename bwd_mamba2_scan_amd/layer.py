@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 _F32, _BF16 = 0, 1
 
@@ -40,12 +41,8 @@ class SsmDims(ctypes.Structure):
     _fields_ = [(n, _c_int) for n in ("type", "dt_type", "heads", "width", "groups", "states", "softplus")]
 
 
-class Grad(ctypes.Structure):
-    """mamba2_grad"""
-    _fields_ = [("grad", _c_vp), ("out", _c_vp), ("numel", _c_ll), ("type", _c_int)]
-
-
 SIGNATURES = {
+    "mamba2_layer_strerror": (ctypes.c_char_p, [_c_int]),
     "mamba2_conv_fwd": (_c_int, [_c_int, Seqs, _c_int, _c_int, _c_int, Rows, _c_vp, _c_vp, _c_vp, Rows, _c_vp, _c_vp]),
     "mamba2_conv_bwd_workspace_bytes": (_c_size, [Seqs, _c_int, _c_int]),
     "mamba2_conv_bwd": (_c_int, [_c_int, Seqs, _c_int, _c_int, _c_int, Rows, _c_vp, _c_vp, _c_vp, Rows, _c_vp, Rows,
@@ -66,38 +63,48 @@ SIGNATURES = {
 }
 
 
-def _pkg():
-    import bwd_mamba2_scan_amd as m2
-    return m2
+# torch, the loaded library and the element types, looked up once, by the first
+# call (importing this package imports no torch).
+torch = lib = _TYPES = None
 
 
-def _torch():
-    import torch
-    return torch
+def _load():
+    global torch, lib, _TYPES
+    import torch as t
+    from . import lib as load
+
+    lib = load()
+    _TYPES = {t.float32: _F32, t.bfloat16: _BF16}
+    torch = t
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _raise(status, where):
+    if status != 0:
+        from . import Mamba2ScanError
+        raise Mamba2ScanError(status, where, lib.mamba2_layer_strerror(status).decode())
 
 
 class _On:
     """The tensors' device and the stream of a call, made current for its allocations and launches."""
 
+    __slots__ = ("_dev", "_stream", "_guards")
+
     def __init__(self, dev, stream):
-        torch = _torch()
-        self._guards = []
-        if torch.cuda.current_device() != dev.index:
-            self._guards.append(torch.cuda.device(dev))
-        if stream is not None:
-            if stream.device != dev:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-            self._guards.append(torch.cuda.stream(stream))
-        self._dev = dev
+        self._dev, self._stream, self._guards = dev, stream, ()
 
     def __enter__(self):
-        for g in self._guards:
-            g.__enter__()
-        return _torch().cuda.current_stream(self._dev).cuda_stream
+        index = self._dev.index
+        if torch.cuda.current_device() != index:
+            self._push(torch.cuda.device(index))
+        if self._stream is not None:
+            if self._stream.device != self._dev:
+                raise ValueError(f"stream is on {self._stream.device}, the tensors on {self._dev}")
+            self._push(torch.cuda.stream(self._stream))
+        return torch._C._cuda_getCurrentRawStream(index)
+
+    def _push(self, guard):
+        guard.__enter__()
+        self._guards += (guard,)
 
     def __exit__(self, *exc):
         for g in reversed(self._guards):
@@ -105,32 +112,38 @@ class _On:
         return False
 
 
+def _start(x):
+    """(device, element type code) of a call's first tensor."""
+    if torch is None:
+        _load()
+    _gpu(x, "x")
+    return x.device, _type(x, "x")
+
+
 def _type(t, name):
-    torch = _torch()
-    if t.dtype == torch.bfloat16:
-        return _BF16
-    if t.dtype == torch.float32:
-        return _F32
-    raise TypeError(f"{name} must be float32 or bfloat16 (got {t.dtype})")
+    typ = _TYPES.get(t.dtype)
+    if typ is None:
+        raise TypeError(f"{name} must be float32 or bfloat16 (got {t.dtype})")
+    return typ
 
 
 def _gpu(t, name, dev=None):
-    if not isinstance(t, _torch().Tensor):
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
-    if dev is not None and t.device != dev:
+    if dev is not None and t.get_device() != dev.index:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
 
 def _dense(t, name, shape, dtype, dev):
-    """A contiguous tensor, or None."""
+    """The address of a contiguous tensor, or None."""
     if t is None:
         return None
     _gpu(t, name, dev)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -140,12 +153,16 @@ def _dense(t, name, shape, dtype, dev):
 def _rows(t, name, lead, inner, dtype, dev):
     """A token-major tensor: contiguous inner dimensions, free outer strides."""
     _gpu(t, name, dev)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if tuple(t.shape) != lead + inner:
+    if t.shape != lead + inner:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {lead + inner}")
-    strides = t.stride()
     want = 1
+    if t.is_contiguous():
+        for size in inner:
+            want *= size
+        return Rows(t.data_ptr(), want * lead[-1], want)
+    strides = t.stride()
     for size, stride in zip(reversed(inner), reversed(strides)):
         if size != 1 and stride != want:
             raise ValueError(f"{name}: the inner dimensions {inner} must be contiguous (strides {strides})")
@@ -155,13 +172,18 @@ def _rows(t, name, lead, inner, dtype, dev):
     return Rows(t.data_ptr(), 0, strides[0])
 
 
+def _token(rows):
+    """The rows of a tensor without a token axis: its first axis counts the sequences."""
+    rows.batch_stride, rows.row_stride = rows.row_stride, 0
+    return rows
+
+
 def _seqs(x, offsets, inner_dims, dev):
     """(mamba2_seqs, the leading shape, the number of sequences)"""
-    torch = _torch()
     if offsets is None:
         if x.dim() != 2 + inner_dims:
             raise ValueError(f"x must have {2 + inner_dims} dimensions (got {x.dim()}); packed rows need offsets")
-        batch, length = int(x.shape[0]), int(x.shape[1])
+        batch, length = x.shape[:2]
         return Seqs(batch, length, None), (batch, length), batch
     if x.dim() != 1 + inner_dims:
         raise ValueError(f"with offsets x must have {1 + inner_dims} dimensions (got {x.dim()})")
@@ -169,15 +191,15 @@ def _seqs(x, offsets, inner_dims, dev):
     if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous int32 vector of at least two elements")
     batch = offsets.numel() - 1
-    return Seqs(batch, int(x.shape[0]), offsets.data_ptr()), (int(x.shape[0]),), batch
+    return Seqs(batch, x.shape[0], offsets.data_ptr()), (x.shape[0],), batch
 
 
 def _span(t):
-    """(first byte, byte behind the last, (row stride, column window) of a row slice or None)"""
-    e = t.element_size()
+    """First byte and byte behind the last of a tensor."""
     lo = t.data_ptr()
-    hi = lo + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * e
-    return lo, hi
+    if t.is_contiguous():
+        return lo, lo + t.nbytes
+    return lo, lo + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
 
 
 def _apart(outs, ins):
@@ -201,7 +223,7 @@ def _apart(outs, ins):
 
 
 def _interleaved(t, o):
-    def window(v):  # (row stride in bytes, width of a row in bytes)
+    def window(v):  # row strides in bytes, outermost first, and the bytes of a row's window
         sizes, strides = list(v.shape), list(v.stride())
         width = 1
         while sizes and (sizes[-1] == 1 or strides[-1] == width):
@@ -213,21 +235,25 @@ def _interleaved(t, o):
     if not st or not so or st[-1] != so[-1] or any(s % st[-1] for s in st + so):
         return False
     row = st[-1]
-    at, ao = t.data_ptr() % row, o.data_ptr() % row
-    gap = (ao - at) % row
+    gap = (o.data_ptr() - t.data_ptr()) % row
     return wt <= gap and gap + wo <= row
 
 
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _empty(shape, dtype, dev):
-    return _torch().empty(shape, dtype=dtype, device=dev)
+    return torch.empty(shape, dtype=dtype, device=dev)
 
 
 # -------------------------------------------------------------- convolution
 def _conv_dims(x, weight, dev):
+    _gpu(weight, "weight", dev)
     if weight.dim() != 2:
         raise ValueError("weight must be [channels, taps]")
-    channels, taps = (int(v) for v in weight.shape)
-    w = _dense(weight, "weight", (channels, taps), _torch().float32, dev)
+    channels, taps = weight.shape
+    w = _dense(weight, "weight", (channels, taps), torch.float32, dev)
     return channels, taps, w
 
 
@@ -241,11 +267,7 @@ def conv_fwd(x, weight, bias=None, *, silu=True, initial_state=None, offsets=Non
     the first token (default: zeros).  Returns (y, the last W - 1 inputs, or
     None unless want_final_state or final_state is given).
     """
-    m2 = _pkg()
-    torch = _torch()
-    _gpu(x, "x")
-    dev = x.device
-    typ = _type(x, "x")
+    dev, typ = _start(x)
     seqs, lead, batch = _seqs(x, offsets, 1, dev)
     channels, taps, w = _conv_dims(x, weight, dev)
     rx = _rows(x, "x", lead, (channels,), x.dtype, dev)
@@ -258,10 +280,10 @@ def conv_fwd(x, weight, bias=None, *, silu=True, initial_state=None, offsets=Non
             y = _empty(lead + (channels,), x.dtype, dev)
         if final_state is None and want_final_state:
             final_state = _empty((batch, taps - 1, channels), x.dtype, dev)
-        st = m2.lib().mamba2_conv_fwd(typ, seqs, channels, taps, int(bool(silu)), rx, w, b, s0,
+        st = lib.mamba2_conv_fwd(typ, seqs, channels, taps, bool(silu), rx, w, b, s0,
                                       _rows(y, "y", lead, (channels,), x.dtype, dev),
                                       _dense(final_state, "final_state", (batch, taps - 1, channels), x.dtype, dev), s)
-    m2._raise(st, "mamba2_conv_fwd")
+    _raise(st, "mamba2_conv_fwd")
     return y, final_state
 
 
@@ -270,11 +292,7 @@ def conv_bwd(x, weight, d_y, bias=None, *, silu=True, initial_state=None, d_fina
     """Gradients of conv_fwd for dL/dy = d_y (and dL/dfinal_state): dict with d_x, d_weight, d_bias (None without
     bias) and d_initial_state (None without initial_state).  `out` may hold some of these tensors.
     """
-    m2 = _pkg()
-    torch = _torch()
-    _gpu(x, "x")
-    dev = x.device
-    typ = _type(x, "x")
+    dev, typ = _start(x)
     seqs, lead, batch = _seqs(x, offsets, 1, dev)
     channels, taps, w = _conv_dims(x, weight, dev)
     rx = _rows(x, "x", lead, (channels,), x.dtype, dev)
@@ -298,20 +316,19 @@ def conv_bwd(x, weight, d_y, bias=None, *, silu=True, initial_state=None, d_fina
                 res[name] = None
             elif res.get(name) is None:
                 res[name] = _empty(shape, dtype, dev)
-        workspace, nbytes = _workspace(workspace, m2.lib().mamba2_conv_bwd_workspace_bytes(seqs, channels, taps), dev)
-        st = m2.lib().mamba2_conv_bwd(
-            typ, seqs, channels, taps, int(bool(silu)), rx, w, b, s0, rg, sf,
+        workspace, nbytes = _workspace(workspace, lib.mamba2_conv_bwd_workspace_bytes(seqs, channels, taps), dev)
+        st = lib.mamba2_conv_bwd(
+            typ, seqs, channels, taps, bool(silu), rx, w, b, s0, rg, sf,
             _rows(res["d_x"], "d_x", lead, (channels,), x.dtype, dev),
             _dense(res["d_weight"], "d_weight", (channels, taps), torch.float32, dev),
             _dense(res["d_bias"], "d_bias", (channels,), torch.float32, dev),
             _dense(res["d_initial_state"], "d_initial_state", tail, x.dtype, dev), _ptr(workspace), nbytes, s)
-    m2._raise(st, "mamba2_conv_bwd")
+    _raise(st, "mamba2_conv_bwd")
     return res
 
 
 def _workspace(workspace, need, dev):
     """The given workspace or a new one; (tensor or None, bytes)."""
-    torch = _torch()
     if workspace is None:
         if need == 0:
             return None, 0
@@ -326,14 +343,10 @@ def conv_step(x, weight, state, bias=None, *, silu=True, new_state=None, y=None,
     """One token of each sequence: x [batch, channels] -> y; state [batch, W - 1, channels] moves on in place, or
     into new_state where that is given.
     """
-    m2 = _pkg()
-    torch = _torch()
-    _gpu(x, "x")
-    dev = x.device
-    typ = _type(x, "x")
+    dev, typ = _start(x)
     channels, taps, w = _conv_dims(x, weight, dev)
-    batch = int(x.shape[0])
-    rx = _rows(x.unsqueeze(1) if x.dim() == 2 else x, "x", (batch, 1), (channels,), x.dtype, dev)
+    batch = x.shape[0]
+    rx = _token(_rows(x, "x", (batch,), (channels,), x.dtype, dev))
     tail = (batch, taps - 1, channels)
     s0 = _dense(state, "state", tail, x.dtype, dev)
     if s0 is None:
@@ -346,23 +359,23 @@ def conv_step(x, weight, state, bias=None, *, silu=True, new_state=None, y=None,
     with _On(dev, stream) as s:
         if y is None:
             y = _empty((batch, channels), x.dtype, dev)
-        st = m2.lib().mamba2_conv_step(typ, batch, channels, taps, int(bool(silu)), rx, w, b, s0,
-                                       _rows(y.unsqueeze(1), "y", (batch, 1), (channels,), x.dtype, dev), s1, s)
-    m2._raise(st, "mamba2_conv_step")
+        st = lib.mamba2_conv_step(typ, batch, channels, taps, bool(silu), rx, w, b, s0,
+                                       _token(_rows(y, "y", (batch,), (channels,), x.dtype, dev)), s1, s)
+    _raise(st, "mamba2_conv_step")
     return y
 
 
 # ---------------------------------------------------------------------- scan
-def _ssm_dims(x, dt, B, softplus):
+def _ssm_dims(typ, x, dt, B, softplus):
+    _gpu(dt, "dt")
+    _gpu(B, "B")
     if B.dim() != x.dim():
         raise ValueError("B and C must be [..., groups, states] beside x [..., heads, width]")
-    heads, width = int(x.shape[-2]), int(x.shape[-1])
-    groups, states = int(B.shape[-2]), int(B.shape[-1])
-    return SsmDims(_type(x, "x"), _type(dt, "dt"), heads, width, groups, states, int(bool(softplus)))
+    return SsmDims(typ, _type(dt, "dt"), *x.shape[-2:], *B.shape[-2:], bool(softplus))
 
 
 def _ssm_inputs(x, dt, A, B, C, D, dt_bias, lead, d, dev):
-    f32 = _torch().float32
+    f32 = torch.float32
     inner, shared = (d.heads, d.width), (d.groups, d.states)
     vec = (d.heads,)
     if A is None:
@@ -385,12 +398,9 @@ def ssm_fwd(x, dt, A, B, C, *, D=None, dt_bias=None, softplus=True, initial_stat
     width] float32 (default: zeros).  Returns (y, the final state, or None
     unless want_final_state or final_state is given).
     """
-    m2 = _pkg()
-    torch = _torch()
-    _gpu(x, "x")
-    dev = x.device
+    dev, typ = _start(x)
     seqs, lead, batch = _seqs(x, offsets, 2, dev)
-    d = _ssm_dims(x, dt, B, softplus)
+    d = _ssm_dims(typ, x, dt, B, softplus)
     px, pdt, pA, pB, pC, pD, pbias = _ssm_inputs(x, dt, A, B, C, D, dt_bias, lead, d, dev)
     shape = (batch, d.heads, d.states, d.width)
     s0 = _dense(initial_state, "initial_state", shape, torch.float32, dev)
@@ -402,12 +412,12 @@ def ssm_fwd(x, dt, A, B, C, *, D=None, dt_bias=None, softplus=True, initial_stat
             y = _empty(lead + (d.heads, d.width), x.dtype, dev)
         if final_state is None and want_final_state:
             final_state = _empty(shape, torch.float32, dev)
-        workspace, nbytes = _workspace(workspace, m2.lib().mamba2_ssm_fwd_workspace_bytes(seqs, d), dev)
-        st = m2.lib().mamba2_ssm_fwd(seqs, d, px, pdt, pA, pB, pC, pD, pbias, s0,
+        workspace, nbytes = _workspace(workspace, lib.mamba2_ssm_fwd_workspace_bytes(seqs, d), dev)
+        st = lib.mamba2_ssm_fwd(seqs, d, px, pdt, pA, pB, pC, pD, pbias, s0,
                                      _rows(y, "y", lead, (d.heads, d.width), x.dtype, dev),
                                      _dense(final_state, "final_state", shape, torch.float32, dev), _ptr(workspace),
                                      nbytes, s)
-    m2._raise(st, "mamba2_ssm_fwd")
+    _raise(st, "mamba2_ssm_fwd")
     return y, final_state
 
 
@@ -416,13 +426,10 @@ def ssm_bwd(x, dt, A, B, C, d_y, *, D=None, dt_bias=None, softplus=True, initial
     """Gradients of ssm_fwd for dL/dy = d_y (and dL/dfinal_state): dict with d_x, d_dt, d_A, d_B, d_C, and d_D,
     d_dt_bias, d_initial_state (each None where the forward had no such input).  `out` may hold some of them.
     """
-    m2 = _pkg()
-    torch = _torch()
-    _gpu(x, "x")
-    dev = x.device
+    dev, typ = _start(x)
     f32 = torch.float32
     seqs, lead, batch = _seqs(x, offsets, 2, dev)
-    d = _ssm_dims(x, dt, B, softplus)
+    d = _ssm_dims(typ, x, dt, B, softplus)
     px, pdt, pA, pB, pC, pD, pbias = _ssm_inputs(x, dt, A, B, C, D, dt_bias, lead, d, dev)
     inner, shared, vec = (d.heads, d.width), (d.groups, d.states), (d.heads,)
     shape = (batch, d.heads, d.states, d.width)
@@ -443,15 +450,15 @@ def ssm_bwd(x, dt, A, B, C, d_y, *, D=None, dt_bias=None, softplus=True, initial
                 res[name] = None
             elif res.get(name) is None:
                 res[name] = _empty(size, dtype, dev)
-        workspace, nbytes = _workspace(workspace, m2.lib().mamba2_ssm_bwd_workspace_bytes(seqs, d), dev)
-        st = m2.lib().mamba2_ssm_bwd(
+        workspace, nbytes = _workspace(workspace, lib.mamba2_ssm_bwd_workspace_bytes(seqs, d), dev)
+        st = lib.mamba2_ssm_bwd(
             seqs, d, px, pdt, pA, pB, pC, pD, pbias, s0, pg, sf, _rows(res["d_x"], "d_x", lead, inner, x.dtype, dev),
             _rows(res["d_dt"], "d_dt", lead, vec, dt.dtype, dev), _dense(res["d_A"], "d_A", vec, f32, dev),
             _rows(res["d_B"], "d_B", lead, shared, x.dtype, dev),
             _rows(res["d_C"], "d_C", lead, shared, x.dtype, dev), _dense(res["d_D"], "d_D", vec, f32, dev),
             _dense(res["d_dt_bias"], "d_dt_bias", vec, f32, dev),
             _dense(res["d_initial_state"], "d_initial_state", shape, f32, dev), _ptr(workspace), nbytes, s)
-    m2._raise(st, "mamba2_ssm_bwd")
+    _raise(st, "mamba2_ssm_bwd")
     return res
 
 
@@ -461,14 +468,11 @@ def ssm_step(x, dt, A, B, C, state, *, D=None, dt_bias=None, softplus=True, new_
     state [batch, heads, states, width] float32 moves on in place, or into
     new_state where that is given.
     """
-    m2 = _pkg()
-    torch = _torch()
-    _gpu(x, "x")
+    dev, typ = _start(x)
     if x.dim() != 3:
         raise ValueError("x must be [batch, heads, width]")
-    dev = x.device
-    batch = int(x.shape[0])
-    d = _ssm_dims(x, dt, B, softplus)
+    batch = x.shape[0]
+    d = _ssm_dims(typ, x, dt, B, softplus)
     px, pdt, pA, pB, pC, pD, pbias = _ssm_inputs(x, dt, A, B, C, D, dt_bias, (batch,), d, dev)
     shape = (batch, d.heads, d.states, d.width)
     s0 = _dense(state, "state", shape, torch.float32, dev)
@@ -482,48 +486,46 @@ def ssm_step(x, dt, A, B, C, state, *, D=None, dt_bias=None, softplus=True, new_
         if y is None:
             y = _empty((batch, d.heads, d.width), x.dtype, dev)
         py = _rows(y, "y", (batch,), (d.heads, d.width), x.dtype, dev)
-        for r in (px, pdt, pB, pC, py):  # one token per sequence: the rows are the sequences
-            r.batch_stride = r.row_stride
-        st = m2.lib().mamba2_ssm_step(batch, d, px, pdt, pA, pB, pC, pD, pbias, s0, py, s1, s)
-    m2._raise(st, "mamba2_ssm_step")
+        for r in (px, pdt, pB, pC, py):
+            _token(r)
+        st = lib.mamba2_ssm_step(batch, d, px, pdt, pA, pB, pC, pD, pbias, s0, py, s1, s)
+    _raise(st, "mamba2_ssm_step")
     return y
 
 
 # ----------------------------------------------------------------- gradients
 def _grad_table(grads, out):
+    """(the mamba2_grad table as bytes, its length, the device)"""
+    if torch is None:
+        _load()
     grads = list(grads)
     if not grads:
         raise ValueError("no gradients")
-    _gpu(grads[0], "grads[0]")
-    dev = grads[0].device
     outs = grads if out is None else list(out)
     if len(outs) != len(grads):
         raise ValueError(f"{len(outs)} outputs for {len(grads)} gradients")
-    table = (Grad * len(grads))()
-    spans = []
-    for i, (g, o) in enumerate(zip(grads, outs)):
-        _gpu(g, f"grads[{i}]", dev)
-        typ = _type(g, f"grads[{i}]")
+    _gpu(grads[0], "grads[0]")
+    index = grads[0].get_device()
+    fields = []
+    for i, g in enumerate(grads):
+        if not isinstance(g, torch.Tensor) or g.get_device() != index:
+            _gpu(g, f"grads[{i}]", grads[0].device)
+        typ = _TYPES.get(g.dtype)
+        if typ is None:
+            _type(g, f"grads[{i}]")
         if not g.is_contiguous():
             raise ValueError(f"grads[{i}] must be contiguous")
-        p, n = g.data_ptr(), g.numel()
-        q = p
-        if n:
-            spans.append((p, p + n * g.element_size(), i))
-        if o is not g:
-            _gpu(o, f"out[{i}]", dev)
-            if o.dtype != g.dtype or o.shape != g.shape or not o.is_contiguous():
-                raise ValueError(f"out[{i}] must be contiguous, of the gradient's type and shape")
-            q = o.data_ptr()
-            if n and q != p:
-                spans.append((q, q + n * g.element_size(), i))
-        e = table[i]
-        e.grad, e.out, e.numel, e.type = p, q, n, typ
-    spans.sort()
-    for (_, end, i), (start, _, j) in zip(spans, spans[1:]):
-        if start < end:
-            raise ValueError(f"the tensors of entries {i} and {j} overlap")
-    return table, len(grads), dev
+        p = g.data_ptr()
+        o = outs[i]
+        if o is g:
+            fields += (p, p, g.numel(), typ)
+            continue
+        if not isinstance(o, torch.Tensor) or o.get_device() != index:
+            _gpu(o, f"out[{i}]", grads[0].device)
+        if o.dtype is not g.dtype or o.shape != g.shape or not o.is_contiguous():
+            raise ValueError(f"out[{i}] must be contiguous, of the gradient's type and shape")
+        fields += (p, o.data_ptr(), g.numel(), typ)
+    return struct.pack("=" + "QQqq" * len(grads), *fields), len(grads), grads[0].device
 
 
 def grad_norm(grads, *, norm=None, workspace=None, stream=None):
@@ -543,8 +545,6 @@ def clip_grads(grads, max_norm, *, out=None, norm=None, workspace=None, stream=N
 
 
 def _grads(grads, max_norm, out, norm, workspace, stream):
-    m2 = _pkg()
-    torch = _torch()
     table, count, dev = _grad_table(grads, out)
     with _On(dev, stream) as s:
         if norm is None:
@@ -552,12 +552,10 @@ def _grads(grads, max_norm, out, norm, workspace, stream):
         _gpu(norm, "norm", dev)
         if norm.dtype != torch.float32 or norm.numel() != 1:
             raise ValueError("norm must be one float32")
-        lib = m2.lib()
-        p = ctypes.addressof(table)
-        workspace, nbytes = _workspace(workspace, lib.mamba2_grad_workspace_bytes(p, count), dev)
+        workspace, nbytes = _workspace(workspace, lib.mamba2_grad_workspace_bytes(table, count), dev)
         if max_norm is None:
-            st = lib.mamba2_grad_norm(p, count, norm.data_ptr(), _ptr(workspace), nbytes, s)
+            st = lib.mamba2_grad_norm(table, count, norm.data_ptr(), _ptr(workspace), nbytes, s)
         else:
-            st = lib.mamba2_clip_grads(p, count, max_norm, norm.data_ptr(), _ptr(workspace), nbytes, s)
-    m2._raise(st, "mamba2_grad_norm" if max_norm is None else "mamba2_clip_grads")
+            st = lib.mamba2_clip_grads(table, count, max_norm, norm.data_ptr(), _ptr(workspace), nbytes, s)
+    _raise(st, "mamba2_grad_norm" if max_norm is None else "mamba2_clip_grads")
     return norm

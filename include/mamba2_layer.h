@@ -34,6 +34,10 @@
 extern "C" {
 #endif
 
+/* A status beside those of mamba2_scan.h, and every status in this header's terms. */
+#define MAMBA2_SCAN_EOVERLAP     -8 /* tensors that must be apart overlap     */
+const char* mamba2_layer_strerror(int status);
+
 #define MAMBA2_F32  0
 #define MAMBA2_BF16 1
 
@@ -203,7 +207,8 @@ int mamba2_grad_norm(const mamba2_grad* grads, int count, float* norm,
  * *norm as above, and out = grad * min(1, max_norm / (norm + 1e-6)) for every
  * tensor.  max_norm >= 0 (infinity clips nothing).  A NaN among the gradients
  * makes every output NaN; an infinite one makes the factor 0.  The tensors
- * may not overlap one another; out overlaps grad only by being it.
+ * may not overlap one another; out overlaps grad only by being it
+ * (MAMBA2_SCAN_EOVERLAP otherwise).
  */
 int mamba2_clip_grads(const mamba2_grad* grads, int count, float max_norm,
                       float* norm, void* workspace, size_t workspace_bytes,
