@@ -43,11 +43,11 @@ struct FwdLds {
 };
 
 template <class T, int NB, int NW>
-__global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(SsmArgs a, Walk w) {
+__global__ __launch_bounds__(NW * 64, 2) void ssm_fwd_kernel(SsmArgs a, Walk w) {
   typedef FwdLds<T, NB, NW> L;
   __shared__ L s;
   constexpr int kThreads = NW * 64;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, l15 = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
   const int work = xcd_contiguous(blockIdx.x, gridDim.x);
   const int per = a.heads * a.slices;
   const int unit = work / per;
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(SsmArgs a, Walk w) {
       if (ti == si) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (ss + j > tt) acc[j] = 0.0f;
+          if (4 * g + j > l15) acc[j] = 0.0f;
       }
       // the scores become an operand: 8 bits with bf16, as x has
       quad_put(&s.w[tt * L::ldw + ss], acc);
@@ -189,7 +189,7 @@ __global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(SsmArgs a, Walk w) {
 
 // Summary pass of the segments; see walk().
 template <class T, int NB, int NW>
-__global__ __launch_bounds__(NW * 64) void ssm_summary_kernel(SsmArgs a, Walk w) {
+__global__ __launch_bounds__(NW * 64, 2) void ssm_summary_kernel(SsmArgs a, Walk w) {
   __shared__ WalkLds<T, NB, NW> s;
   walk<T, NB, NW, false>(a, w, s);
 }

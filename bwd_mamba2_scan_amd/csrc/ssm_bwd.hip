@@ -11,9 +11,8 @@
 // gradient in reverse, side by side, and writes both at every step of 64
 // tokens.  ssm_bwd_kernel then takes all steps in parallel: a work-group owns
 // the 64 tokens of one step and a run of the heads that share B and C, so d_B
-// and d_C are summed over heads in registers, in a fixed order.  Each of its
-// four waves owns 16 rows of every output.  In a step, per head, with
-// E[t][s] = 2^(c_t - c_s) (s <= t), V = (G B)^T and U = S^T-side products:
+// and d_C are summed over heads in registers, in a fixed order.  In a step,
+// per head, with E[t][s] = 2^(c_t - c_s) (s <= t):
 //   P = (C B^T) o E,  Q = (d_y x^T) o E o d
 //   d_x = d o (P^T d_y + 2^(c_end-c) o (B G))        + D d_y
 //   d_B = Q^T C + 2^(c_end-c) d o (x G^T)
@@ -48,12 +47,12 @@ struct Walks {  // forward, reverse: side by side in one launch
 };
 
 template <class T, int NB, int NW>
-__global__ __launch_bounds__(NW * 64) void ssm_walk_kernel(SsmArgs a, Walks ws) {
+__global__ __launch_bounds__(NW * 64, 2) void ssm_walk_kernel(SsmArgs a, Walks ws) {
   __shared__ WalkLds<T, NB, NW> s;
   walk<T, NB, NW, true>(a, ws.w[blockIdx.y], s);
 }
 template <class T, int NB, int NW>
-__global__ __launch_bounds__(NW * 64) void ssm_walk_summary_kernel(SsmArgs a, Walks ws) {
+__global__ __launch_bounds__(NW * 64, 2) void ssm_walk_summary_kernel(SsmArgs a, Walks ws) {
   __shared__ WalkLds<T, NB, NW> s;
   walk<T, NB, NW, false>(a, ws.w[blockIdx.y], s);
 }
@@ -61,21 +60,21 @@ __global__ __launch_bounds__(256) void ssm_walk_carry_kernel(SsmArgs a, Walks ws
   carry(a, ws.w[blockIdx.z & 1], blockIdx.z >> 1);
 }
 
-constexpr int kBwdThreads = 256;
+constexpr int kBwdThreads = 512;
 
 template <class T, int NB, int PT>
 struct BwdLds {
   static constexpr int kN = NB * 32;
   static constexpr int kP = PT * 16 < 32 ? 32 : PT * 16;  // a product over the columns takes 32 at a time
   static constexpr int kTerms = sizeof(T) == 2 ? 2 : 1;
-  static constexpr int kRows = kN < 64 ? kN : 64;         // state rows staged at a time
+  static constexpr int kRows = sizeof(T) == 2 || kN < 64 ? kN : 64;  // state rows staged at a time
   static constexpr int ldn = stride_of<T>(kN);
   static constexpr int ldp = stride_of<T>(kP);
   alignas(16) T b[kTok * ldn];
   alignas(16) T c[kTok * ldn];
   alignas(16) T x[kTok * ldp];
   alignas(16) T dy[kTok * ldp];
-  alignas(16) T st[kTerms][kRows * ldp];  // rows of the starting state, then of the gradient behind the step
+  alignas(16) T st[2][kTerms][kRows * ldp];  // rows of the starting state and of the gradient behind the step
   alignas(16) Decays dc[3];  // of the head before (its gradients are put together), this one and the next
   float slope[3][kTok];      // d d_t / d dt_t
   struct Sums {              // of a head and the one before
@@ -83,25 +82,25 @@ struct BwdLds {
     float after[kTok];       // starting state into row t
     float before[kTok];      // row t into what follows (without d)
     float direct[kTok];      // x . P^T d_y
-    float whole[4];          // starting state through the step, per wave
+    float whole[8];          // starting state through the step, per wave
     float skip[4];           // sum d_y . x, per wave
   } sums[2];
 };
 
 // Rows of a [states][width] fp32 matrix slice in registers, then LDS, where a
-// bf16 product finds them in two terms (16 bits; the third would cost a
-// product and LDS space, and only the sums over thousands of tokens that
-// d_A and d_dt_bias are would show it).
+// bf16 product finds them in two terms (16 bits; a third would not fit, and
+// only the sums over thousands of tokens that d_A and d_dt_bias are show it).
 template <class T, int NB, int PT>
 struct StateTile {
   typedef BwdLds<T, NB, PT> L;
   static constexpr int kQuads = L::kP / 4;
-  static constexpr int kN = L::kRows * kQuads / kBwdThreads;
+  static constexpr int kAll = L::kRows * kQuads;
+  static constexpr int kN = (kAll + kBwdThreads - 1) / kBwdThreads;
   static constexpr int kStep = kBwdThreads / kQuads;  // rows between a thread's quads
   v4f v[kN];
   __device__ __forceinline__ static unsigned offset(int width, int cols) {
     const int r = threadIdx.x / kQuads, c = threadIdx.x % kQuads * 4;
-    return c < cols ? static_cast<unsigned>((r * width + c) * 4) : kOutside;
+    return c < cols && r < L::kRows ? static_cast<unsigned>((r * width + c) * 4) : kOutside;
   }
   __device__ __forceinline__ void load(Rsrc rs, unsigned off, int width, int phase) {
 #pragma unroll
@@ -109,11 +108,12 @@ struct StateTile {
       v[i] = __builtin_bit_cast(
           v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, off + (phase * L::kRows + i * kStep) * width * 4, 0, 0));
   }
-  __device__ __forceinline__ void store(L& s) const {
+  __device__ __forceinline__ void store(T (&st)[L::kTerms][L::kRows * L::ldp]) const {
+    if (kAll < kBwdThreads && threadIdx.x >= kAll) return;
     const int at = threadIdx.x / kQuads * L::ldp + threadIdx.x % kQuads * 4;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      T* p = &s.st[0][at + i * kStep * L::ldp];
+      T* p = &st[0][at + i * kStep * L::ldp];
       quad_put(p, v[i]);
       if constexpr (L::kTerms == 2) {
         v4f rest;
@@ -132,16 +132,21 @@ __device__ __forceinline__ Frag<T> frag_tiles(const v4f& a, const v4f& b) {
   return frag_of<T>(v);
 }
 
-// The sum over the four lanes with the same l & 15.
-__device__ __forceinline__ float sum_groups(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
+// A quad of columns from column c of a result's row: stored where it exists.
+template <class T>
+__device__ __forceinline__ void put_quad(Rsrc rs, int row_off, int c, int cols, v4f v) {
+  Quad<T>::store(rs, c < cols ? static_cast<unsigned>((row_off + c) * static_cast<int>(sizeof(T))) : kOutside, v);
 }
 
+// Eight waves: the first four own 16 rows each of d_x and d_B (rows s), the
+// others 16 rows each of d_C (rows t), so that they work on the gradient
+// behind the step and on the starting state at the same time.  Wave w of the
+// one kind and of the other share a SIMD; their shares of the triangle, 4 - w
+// and w + 1 tiles, add up to the same for all.
 // Results lie so that a lane has one row (token) and four neighbouring
 // columns: a row's factor is one value, and results go out as they are.
 template <class T, int NB, int PT>
-__global__ __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_kernel(BwdArgs ba) {
+__global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
   typedef BwdLds<T, NB, PT> L;
   typedef StateTile<T, NB, PT> ST;
   __shared__ L s;
@@ -150,7 +155,9 @@ __global__ __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
   constexpr int kPt = L::kP / 16;
   constexpr int kPhases = L::kN / L::kRows;
   constexpr int kNt = L::kRows / 16;  // 16-row tiles of the state per phase
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, l15 = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, id = wave_id(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
+  const bool for_x = id < 4;
+  const int wave = id & 3;
   const int work = xcd_contiguous(blockIdx.x, gridDim.x);
   const int split = work % ba.splits;
   const int gr = work / ba.splits % ba.groups;
@@ -180,7 +187,7 @@ __global__ __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
                       a.C.row_stride, rows, a.states));
     tb.store(s.b, L::ldn, tid);
     tc.store(s.c, L::ldn, tid);
-    s.sums[0].inner[wave][lane] = s.sums[1].inner[wave][lane] = 0.0f;  // rows before a wave's columns stay zero
+    s.sums[id >> 2].inner[wave][lane] = 0.0f;  // rows before a wave's columns stay zero
   }
 
   Tile<T, kTok, L::kP, kBwdThreads> tx, ty;
@@ -192,13 +199,15 @@ __global__ __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
     tx.load(rows_rsrc(xp + h * a.width + p0, a.x.row_stride, rows, cols));
     ty.load(rows_rsrc(gp + h * a.width + p0, ba.d_y.row_stride, rows, cols));
   };
-  const auto fetch_state = [&](ST& t, const float* keep, int h, int p0, int phase) {
-    const float* p = keep + (static_cast<long>(step) * a.heads + h) * head + p0;
-    t.load(make_rsrc(p, static_cast<unsigned>((head - p0) * 4)), ST::offset(a.width, min(a.width - p0, L::kP)),
-           a.width, phase);
+  const auto fetch_states = [&](int h, int p0, int phase) {
+    const long at = (static_cast<long>(step) * a.heads + h) * head + p0;
+    const unsigned bytes = static_cast<unsigned>((head - p0) * 4), off = ST::offset(a.width, min(a.width - p0, L::kP));
+    ts.load(make_rsrc(ba.keep_s + at, bytes), off, a.width, phase);
+    tg.load(make_rsrc(ba.keep_g + at, bytes), off, a.width, phase);
   };
-  // The last wave prepares the next head's decays while the others multiply.
-  const bool decays = wave == 3;
+  // Two of the waves with less to multiply prepare the next head's decays
+  // and put the last head's gradients together meanwhile.
+  const bool decays = id == 5, finishes = id == 4;
   float raw = 0.0f;
   const auto prepare = [&](int h, int k) {
     const float bias = a.bias != nullptr ? a.bias[h] : 0.0f;
@@ -210,10 +219,11 @@ __global__ __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
     const auto& sum = s.sums[par];
     const Decays& dc = s.dc[k];
     const float A = a.A[h], d = dc.d[lane];
-    const float after = __shfl(scan64(__shfl(sum.after[lane], 63 - lane)), 63 - lane);
+    const float after = __shfl(scan64(sum.after[63 - lane]), 63 - lane);
     float upto = __shfl_up(scan64(d * sum.before[lane]), 1);
     if (lane == 0) upto = 0.0f;
-    const float whole = ((sum.whole[0] + sum.whole[1]) + (sum.whole[2] + sum.whole[3])) * dc.total;
+    const float whole = (((sum.whole[0] + sum.whole[1]) + (sum.whole[2] + sum.whole[3])) +
+                         ((sum.whole[4] + sum.whole[5]) + (sum.whole[6] + sum.whole[7]))) * dc.total;
     const float inner = (sum.inner[0][lane] + sum.inner[1][lane]) + (sum.inner[2][lane] + sum.inner[3][lane]);
     const float m = inner + after + upto + whole;
     float dd = (sum.direct[lane] + sum.before[lane] + A * m) * s.slope[k][lane];
@@ -236,22 +246,21 @@ __global__ __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
   };
 
   fetch_rows(h0, 0);
-  fetch_state(ts, ba.keep_s, h0, 0, 0);
-  fetch_state(tg, ba.keep_g, h0, 0, 0);
+  fetch_states(h0, 0, 0);
   if (decays) {
     raw = load_raw(a, rdt, h0);
     prepare(h0, 0);
     if (h0 + 1 < h1) raw = load_raw(a, rdt, h0 + 1);
   }
-  v4f db[2 * NB], dcc[2 * NB];
+  v4f acc[2 * NB];  // d_B or d_C
 #pragma unroll
-  for (int n = 0; n < 2 * NB; ++n) db[n] = dcc[n] = v4f{0, 0, 0, 0};
+  for (int n = 0; n < 2 * NB; ++n) acc[n] = v4f{0, 0, 0, 0};
   v4f cb[4];  // (C B^T)[t][s], column s = mine, rows t = 16 ti + 4 g + i
   __syncthreads();
 #pragma unroll
   for (int ti = 0; ti < 4; ++ti) {
     cb[ti] = v4f{0, 0, 0, 0};
-    if (ti >= wave) {
+    if (for_x && ti >= wave) {
 #pragma unroll
       for (int k = 0; k < NB; ++k) mma(cb[ti], frag_row(s.c, L::ldn, ti * 16, k * 32), frag_row(s.b, L::ldn, row, k * 32));
     }
@@ -268,37 +277,38 @@ __global__ __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
       const bool more = slice + 1 < slices || h + 1 < h1;  // a round follows this one, of:
       const int hn = slice + 1 < slices ? h : h + 1, pn = slice + 1 < slices ? p0 + L::kP : 0;
       v4f dx[kPt];
-      float whole = 0.0f, after = 0.0f, before = 0.0f;
+      float whole = 0.0f, edge = 0.0f;  // edge: x . (what follows), or C . (starting state)
 #pragma unroll
+      for (int p = 0; p < kPt; ++p) dx[p] = v4f{0, 0, 0, 0};
       for (int ph = 0; ph < kPhases; ++ph) {
 #pragma unroll
         for (int i = 0; i < ST::kN; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) whole = fmaf(ts.v[i][j], tg.v[i][j], whole);
-        __syncthreads();  // the readers of what is overwritten are done
+        __syncthreads();  // the last round's readers are done
         if (ph == 0) {
           tx.store(s.x, L::ldp, tid);
           ty.store(s.dy, L::ldp, tid);
         }
-        ts.store(s);
+        ts.store(s.st[0]);
+        tg.store(s.st[1]);
         __syncthreads();
-        if (ph + 1 < kPhases) fetch_state(ts, ba.keep_s, h, p0, ph + 1);
-        else if (more) {
+        if (ph + 1 < kPhases) {
+          fetch_states(h, p0, ph + 1);
+        } else if (more) {
           fetch_rows(hn, pn);
-          fetch_state(ts, ba.keep_s, hn, pn, 0);
+          fetch_states(hn, pn, 0);
         }
-        if (ph == 0) {
-          if (slice == 0) {
-            if (wave == 0 && h > h0) finish(h - 1, last, par ^ 1);
-            if (decays && h + 1 < h1) {
-              prepare(h + 1, next);
-              if (h + 2 < h1) raw = load_raw(a, rdt, h + 2);
-            }
+        if (ph == 0 && slice == 0) {
+          if (finishes && h > h0) finish(h - 1, last, par ^ 1);
+          if (decays && h + 1 < h1) {
+            prepare(h + 1, next);
+            if (h + 2 < h1) raw = load_raw(a, rdt, h + 2);
           }
-          // ---- within the step, column s = mine
-#pragma unroll
-          for (int p = 0; p < kPt; ++p) dx[p] = v4f{0, 0, 0, 0};
-          {
+        }
+        if (for_x) {
+          if (ph == 0) {
+            // ---- within the step, column s = mine
             const float ch = dc.hi[mine], cl = dc.lo[mine], d = dc.d[mine];
             v4f pw[4], qw[4];
             float direct = 0.0f, skip = 0.0f, behind = 0.0f;
@@ -316,14 +326,14 @@ __global__ __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 float e = exp2_of((hi[i] - ch) + (lo[i] - cl));
-                if (ti == wave) e = t0 + i >= mine ? e : 0.0f;
+                if (ti == wave) e = 4 * g + i >= l15 ? e : 0.0f;
                 pw[ti][i] = cb[ti][i] * e;
                 qw[ti][i] = yx[i] * (e * d);
                 pair[i] = pw[ti][i] * yx[i];
                 direct += pair[i];
                 if (ti == wave) {
-                  if (t0 + i == mine) skip = yx[i];
-                  pair[i] = t0 + i > mine ? pair[i] : 0.0f;
+                  if (4 * g + i == l15) skip = yx[i];
+                  pair[i] = 4 * g + i > l15 ? pair[i] : 0.0f;
                 }
               }
               // the column's pairs at rows >= t: in the lane, over the lane
@@ -331,16 +341,21 @@ __global__ __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
               pair[2] += pair[3];
               pair[1] += pair[2];
               pair[0] += pair[1];
-              const float d1 = __shfl_down(pair[0], 16), d2 = __shfl_down(pair[0], 32), d3 = __shfl_down(pair[0], 48);
-              const float rest = behind + (g < 3 ? d1 : 0.0f) + (g < 2 ? d2 : 0.0f) + (g < 1 ? d3 : 0.0f);
+              const Pair two = swap16(pair[0]);          // groups 0 and 1, or 2 and 3
+              const Pair all = swap32(two.a + two.b);    // the first two, the last two
+              const float rest = behind + ((g & 1) == 0 ? two.b : 0.0f) + (g < 2 ? all.b : 0.0f);
+              v4f v;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                float v = (pair[i] + rest) * d;
-                if (ti == wave) v = mine < t0 + i ? v : 0.0f;
-                v = sum16(v);
-                if (l15 == 0) sum.inner[wave][t0 + i] = slice == 0 ? v : sum.inner[wave][t0 + i] + v;
+                v[i] = (pair[i] + rest) * d;
+                if (ti == wave) v[i] = l15 < 4 * g + i ? v[i] : 0.0f;
+                v[i] = sum16(v[i]);
               }
-              behind += sum_groups(pair[0]);
+              if (l15 == 0) {
+                v4f* o = reinterpret_cast<v4f*>(&sum.inner[wave][t0]);
+                *o = slice == 0 ? v : *o + v;
+              }
+              behind += all.a + all.b;
             }
             direct = sum_groups(direct);
             if (g == 0) sum.direct[mine] = slice == 0 ? direct : sum.direct[mine] + direct;
@@ -354,11 +369,42 @@ __global__ __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
 #pragma unroll
               for (int p = 0; p < kPt; ++p) mma(dx[p], frag_col_result(s.dy, L::ldp, k * 32, p * 16), pf);
 #pragma unroll
-              for (int n = 0; n < 2 * NB; ++n) mma(db[n], frag_col_result(s.c, L::ldn, k * 32, n * 16), qf);
+              for (int n = 0; n < 2 * NB; ++n) mma(acc[n], frag_col_result(s.c, L::ldn, k * 32, n * 16), qf);
             }
           }
-          // ---- within the step, row t = mine
-          {
+          // ---- this lane's row into what follows the step
+          const float left = dc.left[mine], to = dc.to[mine];
+          Frag<T> bf[L::kRows / 32];
+#pragma unroll
+          for (int k = 0; k < L::kRows / 32; ++k) bf[k] = frag_row(s.b, L::ldn, row, ph * L::kRows + k * 32);
+#pragma unroll
+          for (int p = 0; p < kPt; ++p) {
+            v4f o = {0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < L::kRows / 32; ++k)
+#pragma unroll
+              for (int z = 0; z < L::kTerms; ++z) mma(o, frag_col(s.st[1][z], L::ldp, k * 32, p * 16), bf[k]);
+            const v4f x = quad_get(&s.x[mine * L::ldp + p * 16 + 4 * g]);
+            o *= left;
+            dx[p] += o;
+            o *= x;
+            edge += (o[0] + o[1]) + (o[2] + o[3]);
+          }
+          Frag<T> xf[kKp];
+#pragma unroll
+          for (int k = 0; k < kKp; ++k) xf[k] = frag_row(s.x, L::ldp, row, k * 32);
+#pragma unroll
+          for (int n = 0; n < kNt; ++n) {
+            v4f o = {0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < kKp; ++k) mma(o, frag_row(s.st[1][0], L::ldp, n * 16, k * 32), xf[k]);
+#pragma unroll
+            for (int q = 0; q < kPhases; ++q)
+              if (q == ph) acc[q * kNt + n] += to * o;
+          }
+        } else {
+          if (ph == 0) {
+            // ---- within the step, row t = mine
             const float ch = dc.hi[mine], cl = dc.lo[mine];
             v4f qw[4];
 #pragma unroll
@@ -375,7 +421,7 @@ __global__ __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 float e = exp2_of((ch - hi[i]) + (cl - lo[i])) * d[i];
-                if (si == wave) e = mine >= s0 + i ? e : 0.0f;
+                if (si == wave) e = l15 >= 4 * g + i ? e : 0.0f;
                 qw[si][i] = yx[i] * e;
               }
             }
@@ -384,12 +430,10 @@ __global__ __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
               if (2 * k > wave) continue;
               const Frag<T> qf = frag_tiles<T>(qw[2 * k], qw[2 * k + 1]);
 #pragma unroll
-              for (int n = 0; n < 2 * NB; ++n) mma(dcc[n], frag_col_result(s.b, L::ldn, k * 32, n * 16), qf);
+              for (int n = 0; n < 2 * NB; ++n) mma(acc[n], frag_col_result(s.b, L::ldn, k * 32, n * 16), qf);
             }
           }
-        }
-        // ---- the starting state into this lane's row
-        {
+          // ---- the starting state into this lane's row
           Frag<T> yf[kKp];
 #pragma unroll
           for (int k = 0; k < kKp; ++k) yf[k] = frag_row(s.dy, L::ldp, row, k * 32);
@@ -400,106 +444,57 @@ __global__ __launch_bounds__(kBwdThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
 #pragma unroll
             for (int k = 0; k < kKp; ++k)
 #pragma unroll
-              for (int z = 0; z < L::kTerms; ++z) mma(o, frag_row(s.st[z], L::ldp, n * 16, k * 32), yf[k]);
-            const int nt = ph * kNt + n;
-            const v4f c = quad_get(&s.c[mine * L::ldn + nt * 16 + 4 * g]);
+              for (int z = 0; z < L::kTerms; ++z) mma(o, frag_row(s.st[0][z], L::ldp, n * 16, k * 32), yf[k]);
+            const v4f c = quad_get(&s.c[mine * L::ldn + ph * L::kRows + n * 16 + 4 * g]);
             o *= from;
-            dcc[nt] += o;
+#pragma unroll
+            for (int q = 0; q < kPhases; ++q)
+              if (q == ph) acc[q * kNt + n] += o;
             o *= c;
-            after += (o[0] + o[1]) + (o[2] + o[3]);
-          }
-        }
-        __syncthreads();  // the starting state's readers are done
-        tg.store(s);
-        __syncthreads();
-        if (ph + 1 < kPhases) fetch_state(tg, ba.keep_g, h, p0, ph + 1);
-        else if (more) fetch_state(tg, ba.keep_g, hn, pn, 0);
-        // ---- this lane's row into what follows the step
-        {
-          const float left = dc.left[mine], to = dc.to[mine];
-          Frag<T> bf[L::kRows / 32];
-#pragma unroll
-          for (int k = 0; k < L::kRows / 32; ++k) bf[k] = frag_row(s.b, L::ldn, row, ph * L::kRows + k * 32);
-#pragma unroll
-          for (int p = 0; p < kPt; ++p) {
-            v4f o = {0, 0, 0, 0};
-#pragma unroll
-            for (int k = 0; k < L::kRows / 32; ++k)
-#pragma unroll
-              for (int z = 0; z < L::kTerms; ++z) mma(o, frag_col(s.st[z], L::ldp, k * 32, p * 16), bf[k]);
-            const v4f x = quad_get(&s.x[mine * L::ldp + p * 16 + 4 * g]);
-            o *= left;
-            dx[p] += o;
-            o *= x;
-            before += (o[0] + o[1]) + (o[2] + o[3]);
-          }
-          Frag<T> xf[kKp];
-#pragma unroll
-          for (int k = 0; k < kKp; ++k) xf[k] = frag_row(s.x, L::ldp, row, k * 32);
-#pragma unroll
-          for (int n = 0; n < kNt; ++n) {
-            v4f o = {0, 0, 0, 0};
-#pragma unroll
-            for (int k = 0; k < kKp; ++k) mma(o, frag_row(s.st[0], L::ldp, n * 16, k * 32), xf[k]);
-            db[ph * kNt + n] += to * o;
+            edge += (o[0] + o[1]) + (o[2] + o[3]);
           }
         }
       }
-      after = sum_groups(after);
-      before = sum_groups(before);
+      edge = sum_groups(edge);
       whole = sum64(whole);
-      if (g == 0) {
-        sum.after[mine] = slice == 0 ? after : sum.after[mine] + after;
-        sum.before[mine] = slice == 0 ? before : sum.before[mine] + before;
-      }
-      if (lane == 0) sum.whole[wave] = slice == 0 ? whole : sum.whole[wave] + whole;
-      const Rsrc ro = rows_rsrc(op + h * a.width + p0, ba.d_x.row_stride, rows, cols);
-      const float d = dc.d[mine];
+      float* edges = for_x ? sum.before : sum.after;
+      if (g == 0) edges[mine] = slice == 0 ? edge : edges[mine] + edge;
+      if (lane == 0) sum.whole[id] = slice == 0 ? whole : sum.whole[id] + whole;
+      if (for_x) {
+        const Rsrc ro = rows_rsrc(op + h * a.width + p0, ba.d_x.row_stride, rows, cols);
+        const int at = mine * static_cast<int>(ba.d_x.row_stride);
+        const float d = dc.d[mine];
 #pragma unroll
-      for (int p = 0; p < kPt; ++p) {
-        const int c = p * 16 + 4 * g;
-        const v4f v = d * dx[p] + D * quad_get(&s.dy[mine * L::ldp + c]);
-        Quad<T>::store(ro, c < cols ? static_cast<unsigned>((mine * static_cast<int>(ba.d_x.row_stride) + c) * sizeof(T))
-                                    : kOutside, v);
+        for (int p = 0; p < kPt; ++p) {
+          const int c = p * 16 + 4 * g;
+          put_quad<T>(ro, at, c, cols, d * dx[p] + D * quad_get(&s.dy[mine * L::ldp + c]));
+        }
       }
     }
     if (h + 1 == h1) {
       __syncthreads();
-      if (wave == 0) finish(h, cur, par);
+      if (finishes) finish(h, cur, par);
     }
     cur = next;
     par ^= 1;
   }
 
-  // ---- d_B and d_C
+  // ---- d_B or d_C
   if (ba.splits > 1) {
     const long r0 = (packed ? u.row0 : static_cast<long>(u.seq) * a.q.length) + u.t0;
     const long at = ((split * ba.rows + r0) * ba.groups + gr) * a.states;
     const int stride = ba.groups * a.states;
-    const Rsrc rb = rows_rsrc(ba.part_b + at, stride, rows, a.states);
-    const Rsrc rc = rows_rsrc(ba.part_c + at, stride, rows, a.states);
+    const Rsrc rs = rows_rsrc((for_x ? ba.part_b : ba.part_c) + at, stride, rows, a.states);
 #pragma unroll
-    for (int n = 0; n < 2 * NB; ++n) {
-      const int c = n * 16 + 4 * g;
-      const unsigned off = c < a.states ? static_cast<unsigned>((mine * stride + c) * 4) : kOutside;
-      Quad<float>::store(rb, off, db[n]);
-      Quad<float>::store(rc, off, dcc[n]);
-    }
+    for (int n = 0; n < 2 * NB; ++n) put_quad<float>(rs, mine * stride, n * 16 + 4 * g, a.states, acc[n]);
     return;
   }
-  const Rsrc rb = rows_rsrc(seq_ptr<T>(ba.d_B, u.seq, u.row0, packed) + u.t0 * ba.d_B.row_stride + gr * a.states,
-                            ba.d_B.row_stride, rows, a.states);
-  const Rsrc rc = rows_rsrc(seq_ptr<T>(ba.d_C, u.seq, u.row0, packed) + u.t0 * ba.d_C.row_stride + gr * a.states,
-                            ba.d_C.row_stride, rows, a.states);
+  const mamba2_rows& out = for_x ? ba.d_B : ba.d_C;
+  const Rsrc rs = rows_rsrc(seq_ptr<T>(out, u.seq, u.row0, packed) + u.t0 * out.row_stride + gr * a.states,
+                            out.row_stride, rows, a.states);
 #pragma unroll
-  for (int n = 0; n < 2 * NB; ++n) {
-    const int c = n * 16 + 4 * g;
-    const bool in = c < a.states;
-    Quad<T>::store(rb, in ? static_cast<unsigned>((mine * static_cast<int>(ba.d_B.row_stride) + c) * sizeof(T)) : kOutside,
-                   db[n]);
-    Quad<T>::store(rc, in ? static_cast<unsigned>((mine * static_cast<int>(ba.d_C.row_stride) + c) * sizeof(T)) : kOutside,
-                   dcc[n]);
-  }
+  for (int n = 0; n < 2 * NB; ++n)
+    put_quad<T>(rs, mine * static_cast<int>(out.row_stride), n * 16 + 4 * g, a.states, acc[n]);
 }
 
 // Sums the runs of heads: a block per step, four elements per thread.

@@ -275,11 +275,29 @@ __device__ __forceinline__ float sum16(float v) {
   v = dpp_add<0x122, 0xf>(v);  // row_ror:2
   return dpp_add<0x121, 0xf>(v);
 }
-__device__ __forceinline__ float sum64(float v) {
-  v = sum16(v);
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
+// A value of this lane's 16 and of the three other 16s.  permlane16_swap
+// hands back (rows 0, 0, 2, 2) and (rows 1, 1, 3, 3) of a register swapped
+// with itself, permlane32_swap the lower and the upper half.
+struct Pair {
+  float a, b;
+};
+__device__ __forceinline__ Pair swap16(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return {__uint_as_float(r[0]), __uint_as_float(r[1])};
 }
+__device__ __forceinline__ Pair swap32(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return {__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+// The sum over the four lanes with the same l & 15.
+__device__ __forceinline__ float sum_groups(float v) {
+  const Pair p = swap16(v);
+  const Pair q = swap32(p.a + p.b);
+  return q.a + q.b;
+}
+__device__ __forceinline__ float sum64(float v) { return sum_groups(sum16(v)); }
+// The wave's number, known to be the same in all its lanes.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 // Inclusive prefix sum over the 64 lanes.
 template <class F>
 __device__ __forceinline__ F scan64(F v) {
@@ -352,7 +370,10 @@ __device__ __forceinline__ void make_decays(Decays& dc, float d, float A) {
   const int t = threadIdx.x & 63;
   const double l = fmax(static_cast<double>(d) * static_cast<double>(A) * 1.4426950408889634074, -1100.0);
   const double c = scan64(l);
-  const double end = __shfl(c, 63);
+  const long cbits = __builtin_bit_cast(long, c);
+  const double end = __builtin_bit_cast(
+      double, (static_cast<long>(__builtin_amdgcn_readlane(static_cast<int>(cbits >> 32), 63)) << 32) |
+                  static_cast<unsigned>(__builtin_amdgcn_readlane(static_cast<int>(cbits), 63)));
   const float hi = static_cast<float>(c);
   dc.hi[t] = hi;
   dc.lo[t] = static_cast<float>(c - hi);
@@ -487,7 +508,7 @@ template <class T, int NB, int NW, bool KEEP>
 __device__ __forceinline__ void walk(const SsmArgs& a, const Walk& w, WalkLds<T, NB, NW>& s) {
   typedef WalkLds<T, NB, NW> L;
   constexpr int kThreads = NW * 64;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63;
   const int work = xcd_contiguous(blockIdx.x, gridDim.x);
   const int per = a.heads * a.slices;
   const int unit = work / per;
