@@ -9,7 +9,8 @@
 // streamed tensors: bound by HBM.  A lane owns 16 bytes of channels and walks
 // a run of tokens with the last W - 1 inputs (and W pre-activation gradients)
 // in registers, so x and d_y are read once but for the W - 1 tokens where runs
-// meet.  Eight tokens' loads are issued before the first is used.
+// meet.  The next tokens' loads are in flight while the
+// last ones are computed.
 #include "layer_common.h"
 
 namespace {
@@ -17,7 +18,8 @@ namespace {
 using namespace layer;
 
 constexpr int kLanes = 64;      // lanes over channels
-constexpr int kAhead = 8;       // tokens whose loads are in flight together
+constexpr int kAhead = 8;       // tokens that are loaded while as many are computed
+constexpr int kBwdAhead = 4;    // the same in the backward, which loads two tensors
 constexpr int kBwdWaves = 4;    // waves of a backward work-group, along the tokens
 constexpr int kMaxTaps = 4;
 
@@ -51,10 +53,12 @@ __device__ __forceinline__ float sigmoid_of(float v) {
 
 template <int V, int W>
 __device__ __forceinline__ void load_weights(const ConvArgs& a, int c0, float (&w)[W][V], float (&b)[V]) {
+  // a lane's V * W weights lie in a row
+  const float* p = a.weight + static_cast<long>(c0) * W;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
 #pragma unroll
-    for (int k = 0; k < W; ++k) w[k][i] = a.weight[static_cast<long>(c0 + i) * W + k];
+    for (int k = 0; k < W; ++k) w[k][i] = p[i * W + k];
     b[i] = a.bias != nullptr ? a.bias[c0 + i] : 0.0f;
   }
 }
@@ -70,6 +74,66 @@ __device__ __forceinline__ void load_input(const ConvArgs& a, const T* xs, int s
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = 0.0f;
+  }
+}
+
+// V elements as they lie in memory, loaded through a buffer resource that
+// starts at a run's first row: the lane's channel is one offset register, the
+// token a scalar one, so a row costs one instruction.
+template <class T, int V>
+struct Raw {
+  typedef typename Vec<T>::type vec;
+  vec v;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, int lane_off, int row_off) {
+    v = __builtin_bit_cast(vec, __builtin_amdgcn_raw_buffer_load_b128(rs, lane_off, row_off, 0));
+  }
+  __device__ __forceinline__ float get(int i) const { return static_cast<float>(v[i]); }
+};
+template <>
+struct Raw<float, 1> {
+  float v;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, int lane_off, int row_off) {
+    v = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, lane_off, row_off, 0));
+  }
+  __device__ __forceinline__ float get(int) const { return v; }
+};
+template <>
+struct Raw<bf16, 1> {
+  unsigned short v;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, int lane_off, int row_off) {
+    v = static_cast<unsigned short>(__builtin_amdgcn_raw_buffer_load_b16(rs, lane_off, row_off, 0));
+  }
+  __device__ __forceinline__ float get(int) const { return __uint_as_float(static_cast<unsigned>(v) << 16); }
+};
+// The rows of a run are only ever addressed inside the tensor, so the
+// resource needs no end.
+template <class T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t run_rsrc(const T* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(static_cast<const void*>(p)), 0, 0x7fffffff, 0x00020000);
+}
+template <class T, int V>
+__device__ __forceinline__ void put(__amdgpu_buffer_rsrc_t rs, int lane_off, int row_off, const float (&v)[V]) {
+  if constexpr (V == 1) {
+    const T t = static_cast<T>(v[0]);
+    if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, t), rs, lane_off, row_off, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(t), rs, lane_off, row_off, 0);
+  } else {
+    typename Vec<T>::type r;
+#pragma unroll
+    for (int i = 0; i < V; ++i) r[i] = static_cast<T>(v[i]);
+    typedef int v4i __attribute__((ext_vector_type(4)));
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, r), rs, lane_off, row_off, 0);
+  }
+}
+
+// The window of the last W inputs moves on by one token.
+template <class T, int V, int W>
+__device__ __forceinline__ void shift(float (&win)[W][V], const Raw<T, V>& next) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) win[k][i] = win[k + 1][i];
+    win[W - 1][i] = next.get(i);
   }
 }
 
@@ -99,36 +163,42 @@ __global__ __launch_bounds__(kLanes) void conv_fwd_kernel(ConvArgs a) {
   }
   const Unit u = locate(a.q, unit, a.run);
   if (u.t0 >= u.len) return;
-  float w[W][V], b[V], win[W][V];
-  load_weights<V, W>(a, c0, w, b);
   const T* xs = seq_ptr<const T>(a.x, u.seq, u.row0, packed);
-  T* ys = seq_ptr<T>(a.y, u.seq, u.row0, packed) + c0;
-#pragma unroll
-  for (int j = 0; j < W - 1; ++j) load_input<T, V, W>(a, xs, u.seq, u.t0 - (W - 1) + j, c0, win[j + 1]);
-  xs += c0;
-  const int end = min(u.t0 + a.run, u.len);
-  for (int t = u.t0; t < end; t += kAhead) {
-    float next[kAhead][V];
+  const int rows = min(a.run, u.len - u.t0);
+  const auto rx = run_rsrc(xs + u.t0 * a.x.row_stride);
+  const auto ry = run_rsrc(seq_ptr<T>(a.y, u.seq, u.row0, packed) + u.t0 * a.y.row_stride);
+  const int lane_off = c0 * static_cast<int>(sizeof(T));
+  const int sx = static_cast<int>(a.x.row_stride * sizeof(T)), sy = static_cast<int>(a.y.row_stride * sizeof(T));
+  Raw<T, V> now[kAhead], next[kAhead];
+  const auto fetch = [&](Raw<T, V> (&r)[kAhead], int t) {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
-      if (t + j < end) load_vec<T, V>(xs + (t + j) * a.x.row_stride, next[j]);
+      if (t + j < rows) r[j].load(rx, lane_off, (t + j) * sx);
+  };
+  fetch(now, 0);
+  float w[W][V], b[V], win[W][V];
+  load_weights<V, W>(a, c0, w, b);
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) load_input<T, V, W>(a, xs, u.seq, u.t0 - (W - 1) + j, c0, win[j + 1]);
+  for (int t = 0; t < rows; t += kAhead) {
+    if (t + kAhead < rows) fetch(next, t + kAhead);
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      if (t + j < end) {
+      if (t + j < rows) {
         float y[V];
+        shift<T, V, W>(win, now[j]);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-#pragma unroll
-          for (int k = 0; k < W - 1; ++k) win[k][i] = win[k + 1][i];
-          win[W - 1][i] = next[j][i];
           float s = b[i];
 #pragma unroll
           for (int k = 0; k < W; ++k) s = fmaf(w[k][i], win[k][i], s);
           y[i] = SILU ? s * sigmoid_of<T>(s) : s;
         }
-        store_vec<T, V>(ys + (t + j) * a.y.row_stride, y);
+        put<T, V>(ry, lane_off, (t + j) * sy, y);
       }
     }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) now[j] = next[j];
   }
 }
 
@@ -156,7 +226,7 @@ template <class T, int V, int W, bool SILU>
 __global__ __launch_bounds__(kLanes * kBwdWaves) void conv_bwd_kernel(ConvArgs a) {
   __shared__ float lds[kBwdWaves][kLanes * V];
   const int lane = threadIdx.x % kLanes;
-  const int wave = threadIdx.x / kLanes;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
   const int cb = blockIdx.x % a.cblocks;
   const int unit = blockIdx.x / a.cblocks;
   const int c0 = (cb * kLanes + lane) * V;
@@ -220,77 +290,86 @@ __global__ __launch_bounds__(kLanes * kBwdWaves) void conv_bwd_kernel(ConvArgs a
   const Unit u = locate(a.q, unit, a.run * kBwdWaves);
   const int first = u.t0 + wave * a.run;
   if (live && first < u.len) {
+    const T* xs = seq_ptr<const T>(a.x, u.seq, u.row0, packed);
+    const int rows = min(a.run, u.len - first);              // the weights' gradients take these tokens,
+    const int last = min(rows + W - 1, u.len - first);       // d_x the W - 1 behind them too
+    const auto rx = run_rsrc(xs + first * a.x.row_stride);
+    const auto rg = run_rsrc(seq_ptr<const T>(a.d_y, u.seq, u.row0, packed) + first * a.d_y.row_stride);
+    const auto ro = run_rsrc(seq_ptr<T>(a.d_x, u.seq, u.row0, packed) + first * a.d_x.row_stride);
+    const int lane_off = c0 * static_cast<int>(sizeof(T));
+    const int sx = static_cast<int>(a.x.row_stride * sizeof(T)), sg = static_cast<int>(a.d_y.row_stride * sizeof(T)),
+              so = static_cast<int>(a.d_x.row_stride * sizeof(T));
+    Raw<T, V> nx[kBwdAhead], ng[kBwdAhead], mx[kBwdAhead], mg[kBwdAhead];
+    const auto fetch = [&](Raw<T, V> (&x)[kBwdAhead], Raw<T, V> (&gr)[kBwdAhead], int t) {
+#pragma unroll
+      for (int j = 0; j < kBwdAhead; ++j) {
+        if (t + j < last) {
+          x[j].load(rx, lane_off, (t + j) * sx);
+          gr[j].load(rg, lane_off, (t + j) * sg);
+        }
+      }
+    };
+    fetch(nx, ng, 0);
     float w[W][V], b[V], win[W][V], dpw[W][V];
     load_weights<V, W>(a, c0, w, b);
-    const T* xs = seq_ptr<const T>(a.x, u.seq, u.row0, packed);
-    const T* gs = seq_ptr<const T>(a.d_y, u.seq, u.row0, packed) + c0;
-    T* os = seq_ptr<T>(a.d_x, u.seq, u.row0, packed) + c0;
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) load_input<T, V, W>(a, xs, u.seq, first - (W - 1) + j, c0, win[j + 1]);
 #pragma unroll
     for (int k = 0; k < W; ++k)
 #pragma unroll
       for (int i = 0; i < V; ++i) dpw[k][i] = 0.0f;
-    xs += c0;
-    const int end = min(first + a.run, u.len);   // weights' gradients: tokens first .. end - 1
-    const int last = min(end + W - 1, u.len);    // dp needed: tokens first .. last - 1
-    for (int t = first; t < end + W - 1; t += kAhead) {
-      float nx[kAhead][V], ng[kAhead][V];
+    for (int t = 0; t < rows + W - 1; t += kBwdAhead) {
+      fetch(mx, mg, t + kBwdAhead);
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        if (t + j < last) {
-          load_vec<T, V>(xs + (t + j) * a.x.row_stride, nx[j]);
-          load_vec<T, V>(gs + (t + j) * a.d_y.row_stride, ng[j]);
+      for (int j = 0; j < kBwdAhead; ++j) {
+        const int tt = t + j;
+        if (tt < rows + W - 1) {
+          float dp[V];
+          if (tt < last) {
+            float dy[V];
+            shift<T, V, W>(win, nx[j]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) dy[i] = ng[j].get(i);
+            pre_grad<T, V, W, SILU>(w, b, win, dy, dp);
+          } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) dp[i] = 0.0f;
+          }
+          if (tt < rows) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              db[i] += dp[i];
+#pragma unroll
+              for (int k = 0; k < W; ++k) dw[k][i] = fmaf(dp[i], win[k][i], dw[k][i]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < V; ++i) {  // dpw[k] = dp of token tt - k
+#pragma unroll
+            for (int k = W - 1; k > 0; --k) dpw[k][i] = dpw[k - 1][i];
+            dpw[0][i] = dp[i];
+          }
+          const int o = tt - (W - 1);
+          if (o >= 0 && a.d_x.data != nullptr) {
+            float v[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = 0.0f;
+            const int f = first + o - u.len + (W - 1);
+            if (a.d_final != nullptr && f >= 0)
+              load_vec<T, V>(static_cast<const T*>(a.d_final) +
+                                 (static_cast<long>(u.seq) * (W - 1) + f) * a.channels + c0, v);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+              for (int k = 0; k < W; ++k) v[i] = fmaf(w[k][i], dpw[k][i], v[i]);
+            put<T, V>(ro, lane_off, o * so, v);
+          }
         }
       }
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int tt = t + j;
-        if (tt >= end + W - 1) break;
-        float dp[V];
-        if (tt < last) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-#pragma unroll
-            for (int k = 0; k < W - 1; ++k) win[k][i] = win[k + 1][i];
-            win[W - 1][i] = nx[j][i];
-          }
-          pre_grad<T, V, W, SILU>(w, b, win, ng[j], dp);
-        } else {
-#pragma unroll
-          for (int i = 0; i < V; ++i) dp[i] = 0.0f;
-        }
-        if (tt < end) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            db[i] += dp[i];
-#pragma unroll
-            for (int k = 0; k < W; ++k) dw[k][i] = fmaf(dp[i], win[k][i], dw[k][i]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {  // dpw[k] = dp of token tt - k
-#pragma unroll
-          for (int k = W - 1; k > 0; --k) dpw[k][i] = dpw[k - 1][i];
-          dpw[0][i] = dp[i];
-        }
-        const int o = tt - (W - 1);
-        if (o >= first && a.d_x.data != nullptr) {
-          float v[V];
-          const int f = o - u.len + (W - 1);
-          if (a.d_final != nullptr && f >= 0) {
-            load_vec<T, V>(static_cast<const T*>(a.d_final) +
-                               (static_cast<long>(u.seq) * (W - 1) + f) * a.channels + c0, v);
-          } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = 0.0f;
-          }
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int k = 0; k < W; ++k) v[i] = fmaf(w[k][i], dpw[k][i], v[i]);
-          store_vec<T, V>(os + o * a.d_x.row_stride, v);
-        }
+      for (int j = 0; j < kBwdAhead; ++j) {
+        nx[j] = mx[j];
+        ng[j] = mg[j];
       }
     }
   }
@@ -404,10 +483,13 @@ int check_conv(int type, const mamba2_seqs& q, int channels, int taps) {
   if (!type_ok(type)) return MAMBA2_SCAN_EUNSUPPORTED;
   const int st = check_seqs(q);
   if (st != MAMBA2_SCAN_OK) return st;
-  if (channels < 1 || channels > (1 << 24)) return MAMBA2_SCAN_EBADDIM;
+  if (channels < 1 || channels > (1 << 22)) return MAMBA2_SCAN_EBADDIM;
   if (taps < 2 || taps > kMaxTaps) return MAMBA2_SCAN_EUNSUPPORTED;
   return MAMBA2_SCAN_OK;
 }
+
+// A run's rows are addressed with 31-bit offsets from its first.
+bool strides_ok(const mamba2_rows& r) { return r.row_stride <= (1 << 22); }
 
 long long total_rows(const mamba2_seqs& q) {
   return static_cast<long long>(q.length) * (q.offsets != nullptr ? 1 : q.batch);
@@ -448,6 +530,7 @@ int mamba2_conv_fwd(int type, mamba2_seqs q, int channels, int taps, int silu, m
   if ((st = check_rows(y, q, channels, e)) != MAMBA2_SCAN_OK) return st;
   if (!aligned_to(weight, 4) || !aligned_to(bias, 4) || !aligned_to(initial_state, e) || !aligned_to(final_state, e))
     return MAMBA2_SCAN_EALIGN;
+  if (!strides_ok(x) || !strides_ok(y)) return MAMBA2_SCAN_EUNSUPPORTED;
   const bool vec = channels % (16 / static_cast<int>(e)) == 0 && rows_vec(x, e) && rows_vec(y, e) &&
                    state_vec(initial_state) && state_vec(final_state);
   ConvArgs a = {};
@@ -497,6 +580,7 @@ int mamba2_conv_bwd(int type, mamba2_seqs q, int channels, int taps, int silu, m
   if (!aligned_to(weight, 4) || !aligned_to(bias, 4) || !aligned_to(d_weight, 4) || !aligned_to(d_bias, 4) ||
       !aligned_to(initial_state, e) || !aligned_to(d_final_state, e) || !aligned_to(d_initial_state, e))
     return MAMBA2_SCAN_EALIGN;
+  if (!strides_ok(x) || !strides_ok(d_y) || (d_x.data != nullptr && !strides_ok(d_x))) return MAMBA2_SCAN_EUNSUPPORTED;
   const bool vec = channels % (16 / static_cast<int>(e)) == 0 && rows_vec(x, e) && rows_vec(d_y, e) &&
                    (d_x.data == nullptr || rows_vec(d_x, e)) && state_vec(initial_state) && state_vec(d_final_state) &&
                    state_vec(d_initial_state);

@@ -76,7 +76,7 @@ typedef struct {
  * from initial_state [batch][taps - 1][channels] (oldest first, x's type), or
  * is 0 when that is NULL.  final_state (the same layout; NULL skips it) gets
  * the last taps - 1 inputs, which start the next piece of the sequence.
- *   channels >= 1, taps 2, 3 or 4; weight [channels][taps], bias [channels]
+ *   1 <= channels <= 2^22, row strides up to 2^22 elements, taps 2, 3 or 4; weight [channels][taps], bias [channels]
  *   or NULL.  Pointers are aligned to their elements; rows that are 16-byte
  *   aligned with channels * size a multiple of 16 take wide loads.
  */
@@ -127,7 +127,8 @@ int mamba2_conv_step(int type, int batch, int channels, int taps, int silu,
  * was; so a padded batch marks its padding, x, B and C there being finite.
  *   1 <= groups, heads a multiple of groups; width and states multiples of 8,
  *   8 .. 128.  x, B, C, y and the states are 16-byte aligned, with row and
- *   batch strides that are multiples of 8 elements; dt has any stride.
+ *   batch strides that are multiples of 8 elements; dt has any stride.  Row
+ *   strides are at most 2^29 / 65 elements.
  *   A <= 0 is meant; growing states (A > 0) are computed as long as the decay
  *   over 128 tokens stays finite.
  */
