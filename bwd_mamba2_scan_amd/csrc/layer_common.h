@@ -99,6 +99,8 @@ __device__ __forceinline__ void seq_rows(const mamba2_seqs& q, int s, long* row0
   *len = max(clamp_row(q.offsets[s + 1], q.length) - b, 0);
 }
 
+// Called by whole waves.  A packed call's sequence is found with one load per
+// lane once 64 candidates are left (a search step costs a trip to the cache).
 __device__ __forceinline__ Unit locate(const mamba2_seqs& q, int unit, int run) {
   Unit u;
   if (q.offsets == nullptr) {
@@ -107,14 +109,24 @@ __device__ __forceinline__ Unit locate(const mamba2_seqs& q, int unit, int run) 
     u.index = unit - u.seq * per;
   } else {
     int lo = 0, hi = q.batch;  // the last s with unit_base(s) <= unit
-    while (hi - lo > 1) {
+    while (hi - lo > 64) {
       const int mid = (lo + hi) >> 1;
       if (unit_base(q, mid, run) <= unit) lo = mid; else hi = mid;
     }
-    u.seq = lo;
-    u.index = unit - unit_base(q, lo, run);
+    const int s = lo + static_cast<int>(threadIdx.x & 63);
+    const bool before = s < hi && unit_base(q, s, run) <= unit;
+    const unsigned long long m = __ballot(before);
+    u.seq = lo + (m == 0 ? 0 : 63 - __builtin_clzll(m));
+    u.index = unit - unit_base(q, u.seq, run);
   }
-  seq_rows(q, u.seq, &u.row0, &u.len);
+  long row0;
+  int len;
+  seq_rows(q, u.seq, &row0, &len);
+  // known to be the same in all lanes
+  u.seq = __builtin_amdgcn_readfirstlane(u.seq);
+  u.index = __builtin_amdgcn_readfirstlane(u.index);
+  u.row0 = __builtin_amdgcn_readfirstlane(static_cast<int>(row0));
+  u.len = __builtin_amdgcn_readfirstlane(len);
   const long t = static_cast<long>(u.index) * run;
   u.live = u.index >= 0 && t < max(u.len, 1);
   u.t0 = u.live ? static_cast<int>(t) : u.len;

@@ -163,11 +163,14 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
   const int gr = work / ba.splits % ba.groups;
   const int step = work / ba.splits / ba.groups;
   const Unit u = locate(a.q, step, kTok);
-  if (u.t0 >= u.len) return;  // (the reductions skip these steps too)
   const bool packed = a.q.offsets != nullptr;
   const int rows = min(u.len - u.t0, kTok);
   const int h0 = gr * a.ratio + split * ba.run;
   const int h1 = min(h0 + ba.run, (gr + 1) * a.ratio);
+  if (rows <= 0) {  // a step without tokens adds nothing
+    for (int i = tid; i < (h1 - h0) * 4; i += kBwdThreads) ba.part[(static_cast<long>(step) * a.heads + h0) * 4 + i] = 0.0f;
+    return;
+  }
   const long head = static_cast<long>(a.states) * a.width;
   const int row = wave * 16;                // this wave's rows
   const int mine = row + l15;               // this lane's row
@@ -526,8 +529,6 @@ __global__ __launch_bounds__(256) void ssm_bwd_heads_kernel(BwdArgs ba, float* d
   const int h = blockIdx.x;
   float v[3] = {0, 0, 0};
   for (int i = threadIdx.x; i < ba.steps; i += 256) {
-    const Unit u = locate(a.q, i, kTok);
-    if (u.t0 >= u.len) continue;
     const float* p = ba.part + (static_cast<long>(i) * a.heads + h) * 4;
 #pragma unroll
     for (int k = 0; k < 3; ++k) v[k] += p[k];
