@@ -343,14 +343,17 @@ int check_step_rows(const mamba2_rows& r, const mamba2_seqs& q, const mamba2_ssm
 int waves_of(int width) { return width <= 16 ? 1 : width <= 32 ? 2 : 4; }
 
 // Tokens per segment.  A work-group walks its tokens one step after another,
-// so short of kCUs * 4 work-groups the tokens are cut into segments; each
-// costs a second reading of x and B and a state, so no more than needed.
+// so short of kWork work-groups the tokens are cut into segments.  Each costs
+// a second reading of x and B and a state, and all of them two launches, so
+// no more than needed, and none where a few steps do.
 int segment_tokens(const mamba2_seqs& q, const mamba2_ssm_dims& d) {
+  constexpr long kWork = kCUs * 4;
+  constexpr int kFewSteps = 10;
   const long slices = (d.width + waves_of(d.width) * 16 - 1) / (waves_of(d.width) * 16);
   const long lanes = static_cast<long>(d.heads) * slices * (q.offsets != nullptr ? 1 : q.batch);
-  const long want = (kCUs * 4 + lanes - 1) / lanes;  // segments, over all rows of a packed call
+  const long want = (kWork + lanes - 1) / lanes;  // segments, over all rows of a packed call
   long seg = (q.length + want - 1) / want;
-  if (want <= 2 && q.offsets == nullptr) seg = q.length;  // enough sequences and heads
+  if (q.length <= kFewSteps * kTok || (want <= 2 && q.offsets == nullptr)) seg = q.length;
   seg = (seg + kTok - 1) / kTok * kTok;
   return static_cast<int>(seg < 2 * kTok ? 2 * kTok : seg);
 }

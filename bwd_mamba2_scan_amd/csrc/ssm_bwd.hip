@@ -245,6 +245,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
       p[0] = dA;
       p[1] = (sum.skip[0] + sum.skip[1]) + (sum.skip[2] + sum.skip[3]);
       p[2] = dd;
+      p[3] = 0.0f;
     }
   };
 
@@ -500,36 +501,40 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
     put_quad<T>(rs, mine * static_cast<int>(out.row_stride), n * 16 + 4 * g, a.states, acc[n]);
 }
 
-// Sums the runs of heads: a block per step, four elements per thread.
+// What is left to add up, in a fixed order: the first blocks take a step's
+// rows of d_B and d_C each (over the runs of heads, where there are several),
+// the last ones a head's d_A, d_D and d_dt_bias (over the steps).
 template <class T>
-__global__ __launch_bounds__(256) void ssm_bwd_join_kernel(BwdArgs ba) {
+__global__ __launch_bounds__(256) void ssm_bwd_sums_kernel(BwdArgs ba, int joins, float* d_A, float* d_D,
+                                                           float* d_bias) {
   const SsmArgs& a = ba.a;
-  const Unit u = locate(a.q, blockIdx.x, kTok);
-  if (u.t0 >= u.len) return;
-  const bool packed = a.q.offsets != nullptr;
-  const int rows = min(u.len - u.t0, kTok), wide = ba.groups * a.states, quads = wide / 4;
-  const long r0 = (packed ? u.row0 : static_cast<long>(u.seq) * a.q.length) + u.t0;
-  const float* part = blockIdx.y == 0 ? ba.part_b : ba.part_c;
-  const mamba2_rows& out = blockIdx.y == 0 ? ba.d_B : ba.d_C;
-  T* op = seq_ptr<T>(out, u.seq, u.row0, packed) + u.t0 * out.row_stride;
-  for (int e = threadIdx.x; e < rows * quads; e += 256) {
-    const int r = e / quads, c = e % quads * 4;
-    v4f v = {0, 0, 0, 0};
-    for (int k = 0; k < ba.splits; ++k)
-      v += *reinterpret_cast<const v4f*>(part + (k * ba.rows + r0 + r) * wide + c);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) op[r * out.row_stride + c + j] = static_cast<T>(v[j]);
+  const int block = blockIdx.x;
+  if (block < joins) {
+    const Unit u = locate(a.q, block >> 1, kTok);
+    if (u.t0 >= u.len) return;
+    const bool packed = a.q.offsets != nullptr;
+    const int rows = min(u.len - u.t0, kTok), wide = ba.groups * a.states, quads = wide / 4;
+    const long r0 = (packed ? u.row0 : static_cast<long>(u.seq) * a.q.length) + u.t0;
+    const float* part = (block & 1) == 0 ? ba.part_b : ba.part_c;
+    const mamba2_rows& out = (block & 1) == 0 ? ba.d_B : ba.d_C;
+    T* op = seq_ptr<T>(out, u.seq, u.row0, packed) + u.t0 * out.row_stride;
+    const long next = ba.rows * wide;
+    for (int e = threadIdx.x; e < rows * quads; e += 256) {
+      const int r = e / quads, c = e % quads * 4;
+      const float* p = part + (r0 + r) * wide + c;
+      v4f v = *reinterpret_cast<const v4f*>(p);
+#pragma unroll 4
+      for (int k = 1; k < ba.splits; ++k) v += *reinterpret_cast<const v4f*>(p + k * next);
+      quad_put(op + r * out.row_stride + c, v);
+    }
+    return;
   }
-}
-
-// Sums the steps' parts of d_A, d_D, d_dt_bias: a block per head.
-__global__ __launch_bounds__(256) void ssm_bwd_heads_kernel(BwdArgs ba, float* d_A, float* d_D, float* d_bias) {
   __shared__ float lds[3][4];
-  const SsmArgs& a = ba.a;
-  const int h = blockIdx.x;
+  const int h = block - joins;
   float v[3] = {0, 0, 0};
+#pragma unroll 4
   for (int i = threadIdx.x; i < ba.steps; i += 256) {
-    const float* p = ba.part + (static_cast<long>(i) * a.heads + h) * 4;
+    const v4f p = *reinterpret_cast<const v4f*>(ba.part + (static_cast<long>(i) * a.heads + h) * 4);
 #pragma unroll
     for (int k = 0; k < 3; ++k) v[k] += p[k];
   }
@@ -608,11 +613,8 @@ int launch_bwd(const Call& c) {
   const unsigned blocks = static_cast<unsigned>(static_cast<long>(c.p.steps) * c.ba.groups * c.p.splits);
   ssm_bwd_kernel<T, NB, NW><<<blocks, kBwdThreads, 0, c.s>>>(c.ba);
   if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
-  if (c.p.splits > 1) {
-    ssm_bwd_join_kernel<T><<<dim3(c.p.steps, 2), 256, 0, c.s>>>(c.ba);
-    if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
-  }
-  ssm_bwd_heads_kernel<<<a.heads, 256, 0, c.s>>>(c.ba, c.d_A, c.d_D, c.d_bias);
+  const int joins = c.p.splits > 1 ? 2 * c.p.steps : 0;
+  ssm_bwd_sums_kernel<T><<<joins + a.heads, 256, 0, c.s>>>(c.ba, joins, c.d_A, c.d_D, c.d_bias);
   return launch_status();
 }
 

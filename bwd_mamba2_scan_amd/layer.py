@@ -130,9 +130,11 @@ def _type(t, name):
 def _gpu(t, name, dev=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if dev is not None and t.get_device() == dev.index:
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
-    if dev is not None and t.get_device() != dev.index:
+    if dev is not None:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
 
@@ -243,8 +245,25 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _empty(shape, dtype, dev):
-    return torch.empty(shape, dtype=dtype, device=dev)
+def _new_rows(t, name, lead, inner, dtype, dev):
+    """(a token-major output, its mamba2_rows): the given tensor, or a new one."""
+    if t is not None:
+        return t, _rows(t, name, lead, inner, dtype, dev)
+    t = torch.empty(lead + inner, dtype=dtype, device=dev)
+    width = 1
+    for n in inner:
+        width *= n
+    return t, Rows(t.data_ptr(), width * lead[-1], width)
+
+
+def _new_dense(t, name, shape, dtype, dev, wanted=True):
+    """(a contiguous output or None, its address): the given tensor, or a new one where it is wanted."""
+    if t is not None:
+        return t, _dense(t, name, shape, dtype, dev)
+    if not wanted:
+        return None, None
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    return t, t.data_ptr()
 
 
 # -------------------------------------------------------------- convolution
@@ -276,13 +295,10 @@ def conv_fwd(x, weight, bias=None, *, silu=True, initial_state=None, offsets=Non
     _apart((("y", y), ("final_state", final_state)),
            (("x", x), ("weight", weight), ("bias", bias), ("initial_state", initial_state)))
     with _On(dev, stream) as s:
-        if y is None:
-            y = _empty(lead + (channels,), x.dtype, dev)
-        if final_state is None and want_final_state:
-            final_state = _empty((batch, taps - 1, channels), x.dtype, dev)
-        st = lib.mamba2_conv_fwd(typ, seqs, channels, taps, bool(silu), rx, w, b, s0,
-                                      _rows(y, "y", lead, (channels,), x.dtype, dev),
-                                      _dense(final_state, "final_state", (batch, taps - 1, channels), x.dtype, dev), s)
+        y, ry = _new_rows(y, "y", lead, (channels,), x.dtype, dev)
+        final_state, s1 = _new_dense(final_state, "final_state", (batch, taps - 1, channels), x.dtype, dev,
+                                     want_final_state)
+        st = lib.mamba2_conv_fwd(typ, seqs, channels, taps, bool(silu), rx, w, b, s0, ry, s1, s)
     _raise(st, "mamba2_conv_fwd")
     return y, final_state
 
@@ -306,23 +322,16 @@ def conv_bwd(x, weight, d_y, bias=None, *, silu=True, initial_state=None, d_fina
            (("x", x), ("weight", weight), ("bias", bias), ("d_y", d_y), ("initial_state", initial_state),
             ("d_final_state", d_final_state)))
     with _On(dev, stream) as s:
-        if res.get("d_x") is None:
-            res["d_x"] = _empty(lead + (channels,), x.dtype, dev)
-        if res.get("d_weight") is None:
-            res["d_weight"] = _empty((channels, taps), torch.float32, dev)
-        for name, given, shape, dtype in (("d_bias", bias, (channels,), torch.float32),
-                                          ("d_initial_state", initial_state, tail, x.dtype)):
-            if given is None:
-                res[name] = None
-            elif res.get(name) is None:
-                res[name] = _empty(shape, dtype, dev)
+        get = res.get
+        res["d_x"], rx1 = _new_rows(get("d_x"), "d_x", lead, (channels,), x.dtype, dev)
+        res["d_weight"], w1 = _new_dense(get("d_weight"), "d_weight", (channels, taps), torch.float32, dev)
+        res["d_bias"], b1 = (_new_dense(get("d_bias"), "d_bias", (channels,), torch.float32, dev)
+                             if bias is not None else (None, None))
+        res["d_initial_state"], s1 = (_new_dense(get("d_initial_state"), "d_initial_state", tail, x.dtype, dev)
+                                      if initial_state is not None else (None, None))
         workspace, nbytes = _workspace(workspace, lib.mamba2_conv_bwd_workspace_bytes(seqs, channels, taps), dev)
-        st = lib.mamba2_conv_bwd(
-            typ, seqs, channels, taps, bool(silu), rx, w, b, s0, rg, sf,
-            _rows(res["d_x"], "d_x", lead, (channels,), x.dtype, dev),
-            _dense(res["d_weight"], "d_weight", (channels, taps), torch.float32, dev),
-            _dense(res["d_bias"], "d_bias", (channels,), torch.float32, dev),
-            _dense(res["d_initial_state"], "d_initial_state", tail, x.dtype, dev), _ptr(workspace), nbytes, s)
+        st = lib.mamba2_conv_bwd(typ, seqs, channels, taps, bool(silu), rx, w, b, s0, rg, sf, rx1, w1, b1, s1,
+                                 _ptr(workspace), nbytes, s)
     _raise(st, "mamba2_conv_bwd")
     return res
 
@@ -357,10 +366,8 @@ def conv_step(x, weight, state, bias=None, *, silu=True, new_state=None, y=None,
                (("x", x), ("weight", weight), ("bias", bias), ("state", state)))
     s1 = s0 if new_state is None else _dense(new_state, "new_state", tail, x.dtype, dev)
     with _On(dev, stream) as s:
-        if y is None:
-            y = _empty((batch, channels), x.dtype, dev)
-        st = lib.mamba2_conv_step(typ, batch, channels, taps, bool(silu), rx, w, b, s0,
-                                       _token(_rows(y, "y", (batch,), (channels,), x.dtype, dev)), s1, s)
+        y, ry = _new_rows(y, "y", (batch,), (channels,), x.dtype, dev)
+        st = lib.mamba2_conv_step(typ, batch, channels, taps, bool(silu), rx, w, b, s0, _token(ry), s1, s)
     _raise(st, "mamba2_conv_step")
     return y
 
@@ -408,15 +415,10 @@ def ssm_fwd(x, dt, A, B, C, *, D=None, dt_bias=None, softplus=True, initial_stat
            (("x", x), ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("dt_bias", dt_bias),
             ("initial_state", initial_state)))
     with _On(dev, stream) as s:
-        if y is None:
-            y = _empty(lead + (d.heads, d.width), x.dtype, dev)
-        if final_state is None and want_final_state:
-            final_state = _empty(shape, torch.float32, dev)
+        y, py = _new_rows(y, "y", lead, (d.heads, d.width), x.dtype, dev)
+        final_state, s1 = _new_dense(final_state, "final_state", shape, torch.float32, dev, want_final_state)
         workspace, nbytes = _workspace(workspace, lib.mamba2_ssm_fwd_workspace_bytes(seqs, d), dev)
-        st = lib.mamba2_ssm_fwd(seqs, d, px, pdt, pA, pB, pC, pD, pbias, s0,
-                                     _rows(y, "y", lead, (d.heads, d.width), x.dtype, dev),
-                                     _dense(final_state, "final_state", shape, torch.float32, dev), _ptr(workspace),
-                                     nbytes, s)
+        st = lib.mamba2_ssm_fwd(seqs, d, px, pdt, pA, pB, pC, pD, pbias, s0, py, s1, _ptr(workspace), nbytes, s)
     _raise(st, "mamba2_ssm_fwd")
     return y, final_state
 
@@ -440,24 +442,21 @@ def ssm_bwd(x, dt, A, B, C, d_y, *, D=None, dt_bias=None, softplus=True, initial
     _apart(tuple(res.items()) + (("workspace", workspace),),
            (("x", x), ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("dt_bias", dt_bias), ("d_y", d_y),
             ("initial_state", initial_state), ("d_final_state", d_final_state)))
-    specs = {"d_x": (lead + inner, x.dtype, True), "d_dt": (lead + vec, dt.dtype, True), "d_A": (vec, f32, True),
-             "d_B": (lead + shared, x.dtype, True), "d_C": (lead + shared, x.dtype, True),
-             "d_D": (vec, f32, D is not None), "d_dt_bias": (vec, f32, dt_bias is not None),
-             "d_initial_state": (shape, f32, initial_state is not None)}
     with _On(dev, stream) as s:
-        for name, (size, dtype, wanted) in specs.items():
-            if not wanted:
-                res[name] = None
-            elif res.get(name) is None:
-                res[name] = _empty(size, dtype, dev)
+        ptr = {}
+        for name, size, dtype in (("d_x", inner, x.dtype), ("d_dt", vec, dt.dtype), ("d_B", shared, x.dtype),
+                                  ("d_C", shared, x.dtype)):
+            res[name], ptr[name] = _new_rows(res.get(name), name, lead, size, dtype, dev)
+        for name, given, size in (("d_A", A, vec), ("d_D", D, vec), ("d_dt_bias", dt_bias, vec),
+                                  ("d_initial_state", initial_state, shape)):
+            if given is None:
+                res[name] = ptr[name] = None
+            else:
+                res[name], ptr[name] = _new_dense(res.get(name), name, size, f32, dev)
         workspace, nbytes = _workspace(workspace, lib.mamba2_ssm_bwd_workspace_bytes(seqs, d), dev)
-        st = lib.mamba2_ssm_bwd(
-            seqs, d, px, pdt, pA, pB, pC, pD, pbias, s0, pg, sf, _rows(res["d_x"], "d_x", lead, inner, x.dtype, dev),
-            _rows(res["d_dt"], "d_dt", lead, vec, dt.dtype, dev), _dense(res["d_A"], "d_A", vec, f32, dev),
-            _rows(res["d_B"], "d_B", lead, shared, x.dtype, dev),
-            _rows(res["d_C"], "d_C", lead, shared, x.dtype, dev), _dense(res["d_D"], "d_D", vec, f32, dev),
-            _dense(res["d_dt_bias"], "d_dt_bias", vec, f32, dev),
-            _dense(res["d_initial_state"], "d_initial_state", shape, f32, dev), _ptr(workspace), nbytes, s)
+        st = lib.mamba2_ssm_bwd(seqs, d, px, pdt, pA, pB, pC, pD, pbias, s0, pg, sf, ptr["d_x"], ptr["d_dt"],
+                                ptr["d_A"], ptr["d_B"], ptr["d_C"], ptr["d_D"], ptr["d_dt_bias"],
+                                ptr["d_initial_state"], _ptr(workspace), nbytes, s)
     _raise(st, "mamba2_ssm_bwd")
     return res
 
@@ -483,9 +482,7 @@ def ssm_step(x, dt, A, B, C, state, *, D=None, dt_bias=None, softplus=True, new_
                (("x", x), ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("dt_bias", dt_bias), ("state", state)))
     s1 = s0 if new_state is None else _dense(new_state, "new_state", shape, torch.float32, dev)
     with _On(dev, stream) as s:
-        if y is None:
-            y = _empty((batch, d.heads, d.width), x.dtype, dev)
-        py = _rows(y, "y", (batch,), (d.heads, d.width), x.dtype, dev)
+        y, py = _new_rows(y, "y", (batch,), (d.heads, d.width), x.dtype, dev)
         for r in (px, pdt, pB, pC, py):
             _token(r)
         st = lib.mamba2_ssm_step(batch, d, px, pdt, pA, pB, pC, pD, pbias, s0, py, s1, s)
@@ -548,7 +545,7 @@ def _grads(grads, max_norm, out, norm, workspace, stream):
     table, count, dev = _grad_table(grads, out)
     with _On(dev, stream) as s:
         if norm is None:
-            norm = _empty((), torch.float32, dev)
+            norm = torch.empty((), dtype=torch.float32, device=dev)
         _gpu(norm, "norm", dev)
         if norm.dtype != torch.float32 or norm.numel() != 1:
             raise ValueError("norm must be one float32")
