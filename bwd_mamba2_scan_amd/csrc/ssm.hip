@@ -43,7 +43,7 @@ struct FwdLds {
 };
 
 template <class T, int NB, int NW>
-__global__ __launch_bounds__(NW * 64, 2) void ssm_fwd_kernel(SsmArgs a, Walk w) {
+__global__ __launch_bounds__(NW * 64, sizeof(T) == 2 ? 2 : NB == 4 ? 1 : 2) void ssm_fwd_kernel(SsmArgs a, Walk w) {
   typedef FwdLds<T, NB, NW> L;
   __shared__ L s;
   constexpr int kThreads = NW * 64;
@@ -104,12 +104,9 @@ __global__ __launch_bounds__(NW * 64, 2) void ssm_fwd_kernel(SsmArgs a, Walk w) 
       if (u.t0 + kTok < end) fetch_raw(u.t0 + kTok);
     }
   }
-  unsigned yoff[4];
-#pragma unroll
-  for (int ti = 0; ti < 4; ++ti)
-    yoff[ti] = quad < cols
-                   ? static_cast<unsigned>(((ti * 16 + l15) * static_cast<int>(a.y.row_stride) + quad) * sizeof(T))
-                   : kOutside;
+  const int y16 = static_cast<int>(16 * a.y.row_stride * sizeof(T));  // sixteen rows of y
+  const unsigned yoff =
+      quad < cols ? static_cast<unsigned>((l15 * static_cast<int>(a.y.row_stride) + quad) * sizeof(T)) : kOutside;
   int turn = 0;
   for (int t = u.t0; t < end; t += kTok, turn ^= 1) {
     const Decays& dc = s.dc[turn];
@@ -127,26 +124,28 @@ __global__ __launch_bounds__(NW * 64, 2) void ssm_fwd_kernel(SsmArgs a, Walk w) 
     }
 
     // scores, transposed as a result: lane has t = l15, s = 4 g + i
-    for (int i = wave; i < 10; i += NW) {
+#pragma unroll
+    for (int i0 = 0; i0 < 10; i0 += NW) {
+      if (i0 + wave >= 10) continue;
       int ti, si;
-      lower_tile(i, &ti, &si);
-      v4f acc = {0, 0, 0, 0};
+      lower_tile(i0 + wave, &ti, &si);
+      v4f w = {0, 0, 0, 0};
 #pragma unroll
       for (int k = 0; k < NB; ++k)
-        mma(acc, frag_row(s.b, L::ldn, si * 16, k * 32), frag_row(s.c, L::ldn, ti * 16, k * 32));
+        mma(w, frag_row(s.b, L::ldn, si * 16, k * 32), frag_row(s.c, L::ldn, ti * 16, k * 32));
       const int tt = ti * 16 + l15, ss = si * 16 + 4 * g;
       const float ch = dc.hi[tt], cl = dc.lo[tt];
       const v4f hi = *reinterpret_cast<const v4f*>(&dc.hi[ss]), lo = *reinterpret_cast<const v4f*>(&dc.lo[ss]);
       const v4f d = *reinterpret_cast<const v4f*>(&dc.d[ss]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] *= exp2_of((ch - hi[j]) + (cl - lo[j])) * d[j];
+      for (int j = 0; j < 4; ++j) w[j] *= exp2_of((ch - hi[j]) + (cl - lo[j])) * d[j];
       if (ti == si) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (4 * g + j > l15) acc[j] = 0.0f;
+          if (4 * g + j > l15) w[j] = 0.0f;
       }
       // the scores become an operand: 8 bits with bf16, as x has
-      quad_put(&s.w[tt * L::ldw + ss], acc);
+      quad_put(&s.w[tt * L::ldw + ss], w);
     }
     // y transposed (lane: t = l15, columns 4 g + i), from the state before the
     // step.  The state as an operand keeps 8 bits with bf16, like the y it
@@ -162,12 +161,13 @@ __global__ __launch_bounds__(NW * 64, 2) void ssm_fwd_kernel(SsmArgs a, Walk w) 
         sf[k] = frag_of<T>(v);
       }
 #pragma unroll
-      for (int ti = 0; ti < 4; ++ti) {
-        y[ti] = v4f{0, 0, 0, 0};
+      for (int ti = 0; ti < 4; ++ti) y[ti] = v4f{0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < NB; ++k) mma(y[ti], sf[k], frag_row_result(s.c, L::ldn, ti * 16, k * 32));
-        y[ti] *= dc.from[ti * 16 + l15];
-      }
+      for (int k = 0; k < NB; ++k)
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti) mma(y[ti], sf[k], frag_row_result(s.c, L::ldn, ti * 16, k * 32));
+#pragma unroll
+      for (int ti = 0; ti < 4; ++ti) y[ti] *= dc.from[ti * 16 + l15];
     }
     Frag<T> xf[2];
 #pragma unroll
@@ -176,11 +176,13 @@ __global__ __launch_bounds__(NW * 64, 2) void ssm_fwd_kernel(SsmArgs a, Walk w) 
     __syncthreads();
     const Rsrc ry = rows_rsrc(yp + t * a.y.row_stride, a.y.row_stride, min(end - t, kTok), cols);
 #pragma unroll
-    for (int ti = 0; ti < 4; ++ti) {
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int k = 0; k <= ti / 2; ++k) mma(y[ti], xf[k], frag_row(s.w, L::ldw, ti * 16, k * 32));
+      for (int ti = 2 * k; ti < 4; ++ti) mma(y[ti], xf[k], frag_row(s.w, L::ldw, ti * 16, k * 32));
+#pragma unroll
+    for (int ti = 0; ti < 4; ++ti) {
       y[ti] += D * quad_get(&s.x[(ti * 16 + l15) * L::ldp + quad]);
-      Quad<T>::store(ry, yoff[ti], y[ti]);
+      Quad<T>::store(ry, yoff + ti * y16, y[ti]);
     }
   }
   if (a.final_state != nullptr && u.t0 + static_cast<long>(a.seg) >= u.len)
@@ -343,17 +345,22 @@ int check_step_rows(const mamba2_rows& r, const mamba2_seqs& q, const mamba2_ssm
 int waves_of(int width) { return width <= 16 ? 1 : width <= 32 ? 2 : 4; }
 
 // Tokens per segment.  A work-group walks its tokens one step after another,
-// so short of kWork work-groups the tokens are cut into segments.  Each costs
-// a second reading of x and B and a state, and all of them two launches, so
-// no more than needed, and none where a few steps do.
+// so short of one or two rounds of work-groups the tokens are cut into
+// segments.  Each costs a second reading of x and B and a state, and all of
+// them two launches, so no more than needed, and none where a few steps do.
+// A CU holds two work-groups with up to 128 states (LDS) and three with up to 64
+// (registers); one work-group more than the rounds hold costs a round (24 heads,
+// 64 states: 1032 work-groups 109 us, 768 89 us).  Packed sequences come in unequal units
+// and take half as many again.
 int segment_tokens(const mamba2_seqs& q, const mamba2_ssm_dims& d) {
-  constexpr long kWork = kCUs * 4;
   constexpr int kFewSteps = 10;
+  const bool packed = q.offsets != nullptr;
+  const long work = static_cast<long>(kCUs) * (d.states > 64 ? 2 : 3) * (packed ? 3 : 2) / 2;
   const long slices = (d.width + waves_of(d.width) * 16 - 1) / (waves_of(d.width) * 16);
-  const long lanes = static_cast<long>(d.heads) * slices * (q.offsets != nullptr ? 1 : q.batch);
-  const long want = (kWork + lanes - 1) / lanes;  // segments, over all rows of a packed call
+  const long lanes = static_cast<long>(d.heads) * slices * (packed ? 1 : q.batch);
+  const long want = work / lanes > 1 ? work / lanes : 1;  // segments, over all rows of a packed call
   long seg = (q.length + want - 1) / want;
-  if (q.length <= kFewSteps * kTok || (want <= 2 && q.offsets == nullptr)) seg = q.length;
+  if (q.length <= kFewSteps * kTok) seg = q.length;
   seg = (seg + kTok - 1) / kTok * kTok;
   return static_cast<int>(seg < 2 * kTok ? 2 * kTok : seg);
 }

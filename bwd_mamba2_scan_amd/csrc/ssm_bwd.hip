@@ -68,14 +68,16 @@ struct BwdLds {
   static constexpr int kP = PT * 16 < 32 ? 32 : PT * 16;  // a product over the columns takes 32 at a time
   static constexpr int kTerms = sizeof(T) == 2 ? 2 : 1;
   static constexpr int kRows = sizeof(T) == 2 || kN < 64 ? kN : 64;  // state rows staged at a time
-  static constexpr int ldn = stride_of<T>(kN);
+  // b and c are read by rows and, in fours of neighbouring ones, by columns:
+  // 32 bytes of padding put four rows of 128 bf16 into different banks
+  static constexpr int ldn = stride_of<T>(kN) + (sizeof(T) == 2 && kN == 128 ? 8 : 0);
   static constexpr int ldp = stride_of<T>(kP);
   alignas(16) T b[kTok * ldn];
   alignas(16) T c[kTok * ldn];
   alignas(16) T x[kTok * ldp];
   alignas(16) T dy[kTok * ldp];
   alignas(16) T st[2][kTerms][kRows * ldp];  // rows of the starting state and of the gradient behind the step
-  alignas(16) Decays dc[3];  // of the head before (its gradients are put together), this one and the next
+  alignas(16) DecaysOf<true> dc[3];  // of the head before (its gradients are put together), this one and the next
   float slope[3][kTok];      // d d_t / d dt_t
   struct Sums {              // of a head and the one before
     float inner[4][kTok];    // m_t: pairs within the step, per wave's columns
@@ -114,12 +116,13 @@ struct StateTile {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       T* p = &st[0][at + i * kStep * L::ldp];
-      quad_put(p, v[i]);
       if constexpr (L::kTerms == 2) {
-        v4f rest;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) rest[j] = v[i][j] - static_cast<float>(static_cast<bf16>(v[i][j]));
-        quad_put(p + L::kRows * L::ldp, rest);
+        const unsigned a = pack_bf16(v[i][0], v[i][1]), b = pack_bf16(v[i][2], v[i][3]);
+        *reinterpret_cast<v2u*>(p) = v2u{a, b};
+        quad_put(p + L::kRows * L::ldp,
+                 v4f{v[i][0] - low_of(a), v[i][1] - high_of(a), v[i][2] - low_of(b), v[i][3] - high_of(b)});
+      } else {
+        quad_put(p, v[i]);
       }
     }
   }
@@ -155,6 +158,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
   constexpr int kPt = L::kP / 16;
   constexpr int kPhases = L::kN / L::kRows;
   constexpr int kNt = L::kRows / 16;  // 16-row tiles of the state per phase
+  constexpr int kSide = kNt < 4 ? kNt : 4;
   const int tid = threadIdx.x, id = wave_id(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
   const bool for_x = id < 4;
   const int wave = id & 3;
@@ -220,7 +224,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
   // The step sizes' gradients of a head whose sums are complete: a token per lane.
   const auto finish = [&](int h, int k, int par) {
     const auto& sum = s.sums[par];
-    const Decays& dc = s.dc[k];
+    const DecaysOf<true>& dc = s.dc[k];
     const float A = a.A[h], d = dc.d[lane];
     const float after = __shfl(scan64(sum.after[63 - lane]), 63 - lane);
     float upto = __shfl_up(scan64(d * sum.before[lane]), 1);
@@ -274,7 +278,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
   for (int h = h0; h < h1; ++h) {
     const float D = a.D != nullptr ? a.D[h] : 0.0f;
     const int next = cur == 2 ? 0 : cur + 1, last = cur == 0 ? 2 : cur - 1;
-    const Decays& dc = s.dc[cur];
+    const DecaysOf<true>& dc = s.dc[cur];
     auto& sum = s.sums[par];
     for (int slice = 0; slice < slices; ++slice) {
       const int p0 = slice * L::kP, cols = min(a.width - p0, L::kP);
@@ -381,30 +385,39 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
           Frag<T> bf[L::kRows / 32];
 #pragma unroll
           for (int k = 0; k < L::kRows / 32; ++k) bf[k] = frag_row(s.b, L::ldn, row, ph * L::kRows + k * 32);
+          v4f o[4];  // four tiles at a time: a product waits for the last one on the same tile
+#pragma unroll
+          for (int p = 0; p < kPt; ++p) o[p] = v4f{0, 0, 0, 0};
+#pragma unroll
+          for (int k = 0; k < L::kRows / 32; ++k)
+#pragma unroll
+            for (int z = 0; z < L::kTerms; ++z)
+#pragma unroll
+              for (int p = 0; p < kPt; ++p) mma(o[p], frag_col(s.st[1][z], L::ldp, k * 32, p * 16), bf[k]);
 #pragma unroll
           for (int p = 0; p < kPt; ++p) {
-            v4f o = {0, 0, 0, 0};
-#pragma unroll
-            for (int k = 0; k < L::kRows / 32; ++k)
-#pragma unroll
-              for (int z = 0; z < L::kTerms; ++z) mma(o, frag_col(s.st[1][z], L::ldp, k * 32, p * 16), bf[k]);
             const v4f x = quad_get(&s.x[mine * L::ldp + p * 16 + 4 * g]);
-            o *= left;
-            dx[p] += o;
-            o *= x;
-            edge += (o[0] + o[1]) + (o[2] + o[3]);
+            o[p] *= left;
+            dx[p] += o[p];
+            o[p] *= x;
+            edge += (o[p][0] + o[p][1]) + (o[p][2] + o[p][3]);
           }
           Frag<T> xf[kKp];
 #pragma unroll
           for (int k = 0; k < kKp; ++k) xf[k] = frag_row(s.x, L::ldp, row, k * 32);
 #pragma unroll
-          for (int n = 0; n < kNt; ++n) {
-            v4f o = {0, 0, 0, 0};
+          for (int n0 = 0; n0 < kNt; n0 += kSide) {
 #pragma unroll
-            for (int k = 0; k < kKp; ++k) mma(o, frag_row(s.st[1][0], L::ldp, n * 16, k * 32), xf[k]);
+            for (int n = 0; n < kSide; ++n) o[n] = v4f{0, 0, 0, 0};
 #pragma unroll
-            for (int q = 0; q < kPhases; ++q)
-              if (q == ph) acc[q * kNt + n] += to * o;
+            for (int k = 0; k < kKp; ++k)
+#pragma unroll
+              for (int n = 0; n < kSide; ++n) mma(o[n], frag_row(s.st[1][0], L::ldp, (n0 + n) * 16, k * 32), xf[k]);
+#pragma unroll
+            for (int n = 0; n < kSide; ++n)
+#pragma unroll
+              for (int q = 0; q < kPhases; ++q)
+                if (q == ph) acc[q * kNt + n0 + n] += to * o[n];
           }
         } else {
           if (ph == 0) {
@@ -443,19 +456,26 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
           for (int k = 0; k < kKp; ++k) yf[k] = frag_row(s.dy, L::ldp, row, k * 32);
           const float from = dc.from[mine];
 #pragma unroll
-          for (int n = 0; n < kNt; ++n) {
-            v4f o = {0, 0, 0, 0};
+          for (int n0 = 0; n0 < kNt; n0 += kSide) {
+            v4f o[kSide];
+#pragma unroll
+            for (int n = 0; n < kSide; ++n) o[n] = v4f{0, 0, 0, 0};
 #pragma unroll
             for (int k = 0; k < kKp; ++k)
 #pragma unroll
-              for (int z = 0; z < L::kTerms; ++z) mma(o, frag_row(s.st[0][z], L::ldp, n * 16, k * 32), yf[k]);
-            const v4f c = quad_get(&s.c[mine * L::ldn + ph * L::kRows + n * 16 + 4 * g]);
-            o *= from;
+              for (int z = 0; z < L::kTerms; ++z)
 #pragma unroll
-            for (int q = 0; q < kPhases; ++q)
-              if (q == ph) acc[q * kNt + n] += o;
-            o *= c;
-            edge += (o[0] + o[1]) + (o[2] + o[3]);
+                for (int n = 0; n < kSide; ++n) mma(o[n], frag_row(s.st[0][z], L::ldp, (n0 + n) * 16, k * 32), yf[k]);
+#pragma unroll
+            for (int n = 0; n < kSide; ++n) {
+              const v4f c = quad_get(&s.c[mine * L::ldn + ph * L::kRows + (n0 + n) * 16 + 4 * g]);
+              o[n] *= from;
+#pragma unroll
+              for (int q = 0; q < kPhases; ++q)
+                if (q == ph) acc[q * kNt + n0 + n] += o[n];
+              o[n] *= c;
+              edge += (o[n][0] + o[n][1]) + (o[n][2] + o[n][3]);
+            }
           }
         }
       }

@@ -103,13 +103,15 @@ __device__ __forceinline__ v4s read_tr(const bf16* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
       (__attribute__((address_space(3))) v4s*)(const_cast<bf16*>(p)));
 }
-__device__ __forceinline__ Frag<bf16> frag_col(const bf16* p, int ld, int k0, int col) {
-  const int l = threadIdx.x & 63;
-  const bf16* r = p + (k0 + 8 * (l >> 4) + ((l & 15) >> 2)) * ld + col + 4 * (l & 3);
-  const v4s a = read_tr(r), b = read_tr(r + 4 * ld);
+__device__ __forceinline__ Frag<bf16> frag_join(v4s a, v4s b) {
   typedef short v8s __attribute__((ext_vector_type(8)));
   const v8s v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   return {__builtin_bit_cast(v8bf, v)};
+}
+__device__ __forceinline__ Frag<bf16> frag_col(const bf16* p, int ld, int k0, int col) {
+  const int l = threadIdx.x & 63;
+  const bf16* r = p + (k0 + 8 * (l >> 4) + ((l & 15) >> 2)) * ld + col + 4 * (l & 3);
+  return frag_join(read_tr(r), read_tr(r + 4 * ld));
 }
 __device__ __forceinline__ Frag<float> frag_col(const float* p, int ld, int k0, int col) {
   const int l = threadIdx.x & 63;
@@ -119,15 +121,11 @@ __device__ __forceinline__ Frag<float> frag_col(const float* p, int ld, int k0, 
   for (int j = 0; j < 8; ++j) f.v[j >> 2][j & 3] = r[j * ld];
   return f;
 }
-
 // The same in result order.
 __device__ __forceinline__ Frag<bf16> frag_col_result(const bf16* p, int ld, int k0, int col) {
   const int l = threadIdx.x & 63;
   const bf16* r = p + (k0 + 4 * (l >> 4) + ((l & 15) >> 2)) * ld + col + 4 * (l & 3);
-  const v4s a = read_tr(r), b = read_tr(r + 16 * ld);
-  typedef short v8s __attribute__((ext_vector_type(8)));
-  const v8s v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-  return {__builtin_bit_cast(v8bf, v)};
+  return frag_join(read_tr(r), read_tr(r + 16 * ld));
 }
 __device__ __forceinline__ Frag<float> frag_col_result(const float* p, int ld, int k0, int col) {
   const int l = threadIdx.x & 63;
@@ -144,22 +142,34 @@ template <class T, int TERMS>
 struct Split {
   Frag<T> f[TERMS];
 };
+// Two floats rounded to bf16 in one word, and the floats of such a word.
+__device__ __forceinline__ unsigned pack_bf16(float a, float b) {
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(unsigned, __builtin_convertvector((v2f){a, b}, v2bf));
+}
+__device__ __forceinline__ float low_of(unsigned w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high_of(unsigned w) { return __uint_as_float(w & 0xffff0000u); }
+
 template <class T, int TERMS>
 __device__ __forceinline__ Split<T, TERMS> split_of(const float (&v)[8]) {
   Split<T, TERMS> s;
   if constexpr (sizeof(T) == 4) {
     s.f[0] = {{{v[0], v[1], v[2], v[3]}, {v[4], v[5], v[6], v[7]}}};
   } else {
-    float r[8];
+    v4u w[TERMS];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = v[j];
+    for (int j = 0; j < 4; ++j) {
+      float a = v[2 * j], b = v[2 * j + 1];
 #pragma unroll
-    for (int t = 0; t < TERMS; ++t)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        s.f[t].v[j] = static_cast<bf16>(r[j]);
-        if (t + 1 < TERMS) r[j] -= static_cast<float>(s.f[t].v[j]);
+      for (int t = 0; t < TERMS; ++t) {
+        const unsigned p = pack_bf16(a, b);
+        w[t][j] = p;
+        a -= low_of(p);
+        b -= high_of(p);
       }
+    }
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t) s.f[t].v = __builtin_bit_cast(v8bf, w[t]);
   }
   return s;
 }
@@ -228,9 +238,7 @@ template <>
 struct Quad<bf16> {
   typedef v4bf type;
   static __device__ __forceinline__ void store(Rsrc rs, unsigned off, v4f v) {
-    v4bf r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = static_cast<bf16>(v[i]);
+    const v2u r = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
     __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2i, r), rs, off, 0, 0);
   }
 };
@@ -246,12 +254,9 @@ __device__ __forceinline__ v4f quad_get(const T* p) {
   const typename Quad<T>::type r = *reinterpret_cast<const typename Quad<T>::type*>(p);
   return v4f{static_cast<float>(r[0]), static_cast<float>(r[1]), static_cast<float>(r[2]), static_cast<float>(r[3])};
 }
-template <class T>
-__device__ __forceinline__ void quad_put(T* p, v4f v) {
-  typename Quad<T>::type r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = static_cast<T>(v[i]);
-  *reinterpret_cast<typename Quad<T>::type*>(p) = r;
+__device__ __forceinline__ void quad_put(float* p, v4f v) { *reinterpret_cast<v4f*>(p) = v; }
+__device__ __forceinline__ void quad_put(bf16* p, v4f v) {
+  *reinterpret_cast<v2u*>(p) = v2u{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
 }
 
 // ------------------------------------------------------------------ decays
@@ -354,19 +359,22 @@ __device__ __forceinline__ float step_of(const SsmArgs& a, float raw, float bias
 // The decays of a step of kTok tokens.  Sums of log2 decays are formed in 64
 // bits and kept as two floats: a difference of two of them is needed to
 // about 1e-7, and they reach into the thousands.
-struct Decays {
+template <bool LEFT>
+struct DecaysOf {
   float hi[kTok], lo[kTok];   // c_t
   float d[kTok];              // d_t; 0 behind the last token
   float from[kTok];           // 2^c_t
-  float left[kTok];           // 2^(c_end - c_t)
   float to[kTok];             // 2^(c_end - c_t) d_t
+  float left[LEFT ? kTok : 4];  // 2^(c_end - c_t), where the backward needs it
   float total;                // 2^c_end
   double end;                 // c_end
 };
+typedef DecaysOf<false> Decays;
 
 // One wave; lane t has token t.  A token whose decay underflows any fp32
 // (2^-1100) is held there, so that later differences keep their bits.
-__device__ __forceinline__ void make_decays(Decays& dc, float d, float A) {
+template <bool LEFT>
+__device__ __forceinline__ void make_decays(DecaysOf<LEFT>& dc, float d, float A) {
   const int t = threadIdx.x & 63;
   const double l = fmax(static_cast<double>(d) * static_cast<double>(A) * 1.4426950408889634074, -1100.0);
   const double c = scan64(l);
@@ -380,7 +388,7 @@ __device__ __forceinline__ void make_decays(Decays& dc, float d, float A) {
   dc.d[t] = d;
   dc.from[t] = exp2_of(c);
   const float left = exp2_of(end - c);
-  dc.left[t] = left;
+  if (LEFT) dc.left[LEFT ? t : 0] = left;
   dc.to[t] = left * d;
   if (t == 63) {
     dc.total = exp2_of(c);
@@ -473,20 +481,24 @@ struct State {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       float v[8];
+      const v4f* c = reinterpret_cast<const v4f*>(coef + k * 32 + 8 * g);
+      const v4f c0 = c[0], c1 = c[1];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const v4f c = *reinterpret_cast<const v4f*>(coef + k * 32 + 8 * g + 4 * h);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[4 * h + j] = frag_get(vf[k], 4 * h + j) * c[j];
-      }
+      for (int j = 0; j < 8; ++j) v[j] = frag_get(vf[k], j) * (j < 4 ? c0[j & 3] : c1[j & 3]);
       const auto parts = split_of<T, kExact<T>>(v);
+      // four tiles at a time: a product waits for the last one on the same tile
+      constexpr int kTiles = 2 * NB < 4 ? 2 * NB : 4;
 #pragma unroll
-      for (int n = 0; n < 2 * NB; ++n) {
-        const Frag<T> mf = frag_col(m, ldn, k * 32, n * 16);
+      for (int n = 0; n < 2 * NB; n += kTiles) {
+        Frag<T> mf[kTiles];
 #pragma unroll
-        for (int z = 0; z < kExact<T>; ++z) {
-          if constexpr (COLS) mma(st[n], mf, parts.f[z]); else mma(st[n], parts.f[z], mf);
-        }
+        for (int i = 0; i < kTiles; ++i) mf[i] = frag_col(m, ldn, k * 32, (n + i) * 16);
+#pragma unroll
+        for (int z = 0; z < kExact<T>; ++z)
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i) {
+            if constexpr (COLS) mma(st[n + i], mf[i], parts.f[z]); else mma(st[n + i], parts.f[z], mf[i]);
+          }
       }
     }
   }
