@@ -30,7 +30,7 @@ using namespace ssm;
 struct BwdArgs {
   SsmArgs a;
   mamba2_rows d_y, d_x, d_dt, d_B, d_C;
-  const float* keep_s;     // [steps][heads][states][width]
+  const float* keep_s;     // the walk's kept states
   const float* keep_g;
   float* part;             // [steps][heads][4]: d_A, d_D, d_dt_bias of the step
   float* part_b;           // [splits][rows][groups][states]: d_B of a run of heads
@@ -95,27 +95,31 @@ struct BwdLds {
 template <class T, int NB, int PT>
 struct StateTile {
   typedef BwdLds<T, NB, PT> L;
-  static constexpr int kQuads = L::kP / 4;
-  static constexpr int kAll = L::kRows * kQuads;
-  static constexpr int kN = (kAll + kBwdThreads - 1) / kBwdThreads;
-  static constexpr int kStep = kBwdThreads / kQuads;  // rows between a thread's quads
+  static constexpr int kTiles = L::kRows / 16;                // of a strip of 16 columns
+  static constexpr int kAll = kTiles * (L::kP / 16);          // a tile per wave and turn
+  static constexpr int kWaves = kBwdThreads / 64;
+  static constexpr int kN = (kAll + kWaves - 1) / kWaves;
   v4f v[kN];
-  __device__ __forceinline__ static unsigned offset(int width, int cols) {
-    const int r = threadIdx.x / kQuads, c = threadIdx.x % kQuads * 4;
-    return c < cols && r < L::kRows ? static_cast<unsigned>((r * width + c) * 4) : kOutside;
-  }
-  __device__ __forceinline__ void load(Rsrc rs, unsigned off, int width, int phase) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i)
-      v[i] = __builtin_bit_cast(
-          v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, off + (phase * L::kRows + i * kStep) * width * 4, 0, 0));
-  }
-  __device__ __forceinline__ void store(T (&st)[L::kTerms][L::kRows * L::ldp]) const {
-    if (kAll < kBwdThreads && threadIdx.x >= kAll) return;
-    const int at = threadIdx.x / kQuads * L::ldp + threadIdx.x % kQuads * 4;
+  // From strip0 and tile0 on; what the state does not have is zero.
+  __device__ __forceinline__ void load(const float* kept, int width, int states, int strip0, int tile0) {
+    const int strips = tiles_of(width), tiles = tiles_of(states), lane = threadIdx.x & 63;
+    const Rsrc rs = make_rsrc(kept, static_cast<unsigned>(strips * tiles * kKeptTile * 4));
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      T* p = &st[0][at + i * kStep * L::ldp];
+      const int t = wave_id() + i * kWaves, strip = strip0 + t / kTiles, tile = tile0 + t % kTiles;
+      const bool in = t < kAll && strip < strips && tile < tiles;
+      v[i] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(
+                                         rs, (in ? (strip * tiles + tile) * kKeptTile * 4u : kOutside) + lane * 16, 0,
+                                         kNonTemporal));
+    }
+  }
+  __device__ __forceinline__ void store(T (&st)[L::kTerms][L::kRows * L::ldp]) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int t = wave_id() + i * kWaves;
+      if (kAll % kWaves != 0 && t >= kAll) continue;
+      T* p = &st[0][(t % kTiles * 16 + (lane & 15)) * L::ldp + t / kTiles * 16 + 4 * (lane >> 4)];
       if constexpr (L::kTerms == 2) {
         const unsigned a = pack_bf16(v[i][0], v[i][1]), b = pack_bf16(v[i][2], v[i][3]);
         *reinterpret_cast<v2u*>(p) = v2u{a, b};
@@ -175,7 +179,6 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
     for (int i = tid; i < (h1 - h0) * 4; i += kBwdThreads) ba.part[(static_cast<long>(step) * a.heads + h0) * 4 + i] = 0.0f;
     return;
   }
-  const long head = static_cast<long>(a.states) * a.width;
   const int row = wave * 16;                // this wave's rows
   const int mine = row + l15;               // this lane's row
   const int slices = (a.width + L::kP - 1) / L::kP;
@@ -207,10 +210,9 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
     ty.load(rows_rsrc(gp + h * a.width + p0, ba.d_y.row_stride, rows, cols));
   };
   const auto fetch_states = [&](int h, int p0, int phase) {
-    const long at = (static_cast<long>(step) * a.heads + h) * head + p0;
-    const unsigned bytes = static_cast<unsigned>((head - p0) * 4), off = ST::offset(a.width, min(a.width - p0, L::kP));
-    ts.load(make_rsrc(ba.keep_s + at, bytes), off, a.width, phase);
-    tg.load(make_rsrc(ba.keep_g + at, bytes), off, a.width, phase);
+    const long at = (static_cast<long>(step) * a.heads + h) * kept_size(a.width, a.states);
+    ts.load(ba.keep_s + at, a.width, a.states, p0 / 16, phase * ST::kTiles);
+    tg.load(ba.keep_g + at, a.width, a.states, p0 / 16, phase * ST::kTiles);
   };
   // Two of the waves with less to multiply prepare the next head's decays
   // and put the last head's gradients together meanwhile.
@@ -600,7 +602,7 @@ int make_plan(const mamba2_seqs& q, const mamba2_ssm_dims& d, Plan* p) {
   if (splits > ratio) splits = ratio;
   p->run = static_cast<int>((ratio + splits - 1) / splits);
   p->splits = (ratio + p->run - 1) / p->run;
-  p->keep = pad4(static_cast<size_t>(p->steps) * d.heads * head);
+  p->keep = static_cast<size_t>(p->steps) * d.heads * kept_size(d.width, d.states);
   p->seg_state = p->segments ? pad4(static_cast<size_t>(p->units) * d.heads * head) : 0;
   p->seg_decay = p->segments ? pad4(static_cast<size_t>(p->units) * d.heads) : 0;
   p->part = pad4(static_cast<size_t>(p->steps) * d.heads * 4);

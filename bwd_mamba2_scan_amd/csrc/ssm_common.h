@@ -414,7 +414,7 @@ struct Walk {
   float* last;             // where it ends, per sequence (NULL: not kept)
   float* seg_state;        // [units][heads][states][width]: the state each segment starts from
   float* seg_decay;        // [units][heads]: each segment's decay
-  float* keep;             // [steps][heads][states][width]: the state each step starts from
+  float* keep;             // the state each step starts from; see kept_at
   int rev;
 };
 
@@ -503,6 +503,17 @@ struct State {
     }
   }
 };
+
+// The kept states lie as a wave holds them, so that they are written and read
+// a kilobyte at a time: [steps][heads][width / 16][states / 16] tiles (counts
+// rounded up) of [64 lanes][4], lane l with row l & 15 and columns 4 (l >> 4) ..
+// of its tile.  What a tile has beyond the state is zero.
+constexpr int kKeptTile = 256;  // floats
+constexpr int kNonTemporal = 2; // read and written once: past the lines that the heads share (188 against 173 us)
+__host__ __device__ inline int tiles_of(int n) { return (n + 15) / 16; }
+__host__ __device__ inline long kept_size(int width, int states) {
+  return static_cast<long>(tiles_of(width)) * tiles_of(states) * kKeptTile;
+}
 
 template <class T, int NB, int NW>
 struct WalkLds {
@@ -593,7 +604,14 @@ __device__ __forceinline__ void walk(const SsmArgs& a, const Walk& w, WalkLds<T,
     }
     if (KEEP) {
       const long step = static_cast<long>(unit_base(a.q, u.seq, kTok)) + t / kTok;
-      st.save(w.keep + (step * a.heads + h) * head, a.width, a.states);
+      const int strip = slice * NW + wave, tiles = tiles_of(a.states);
+      const Rsrc rs = make_rsrc(w.keep + (step * a.heads + h) * kept_size(a.width, a.states) +
+                                    static_cast<long>(strip) * tiles * kKeptTile,
+                                strip < tiles_of(a.width) ? tiles * kKeptTile * 4u : 0u);
+#pragma unroll
+      for (int n = 0; n < 2 * NB; ++n)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, st.st[n]), rs, (n * 64 + lane) * 16, 0,
+                                               kNonTemporal);
     }
     Frag<T> vf[2];
 #pragma unroll
