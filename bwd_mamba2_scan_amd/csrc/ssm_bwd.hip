@@ -139,6 +139,15 @@ __device__ __forceinline__ Frag<T> frag_tiles(const v4f& a, const v4f& b) {
   return frag_of<T>(v);
 }
 
+// The lane's number, as if it could change: what is computed from it stays in
+// its round.  Kept across rounds, the addresses would cost more registers than
+// there are (and a spilled register's reload waits for the loads in flight).
+__device__ __forceinline__ int lane_anew() {
+  int l = threadIdx.x & 63;
+  asm volatile("" : "+v"(l));
+  return l;
+}
+
 // A quad of columns from column c of a result's row: stored where it exists.
 template <class T>
 __device__ __forceinline__ void put_quad(Rsrc rs, int row_off, int c, int cols, v4f v) {
@@ -219,12 +228,14 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
   const bool decays = id == 5, finishes = id == 4;
   float raw = 0.0f;
   const auto prepare = [&](int h, int k) {
+    const int lane = lane_anew();
     const float bias = a.bias != nullptr ? a.bias[h] : 0.0f;
     make_decays(s.dc[k], lane < rows ? step_of(a, raw, bias) : 0.0f, a.A[h]);
     s.slope[k][lane] = a.softplus ? __builtin_amdgcn_rcpf(1.0f + expf(-(raw + bias))) : 1.0f;
   };
   // The step sizes' gradients of a head whose sums are complete: a token per lane.
   const auto finish = [&](int h, int k, int par) {
+    const int lane = lane_anew();
     const auto& sum = s.sums[par];
     const DecaysOf<true>& dc = s.dc[k];
     const float A = a.A[h], d = dc.d[lane];
@@ -284,6 +295,8 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
     auto& sum = s.sums[par];
     for (int slice = 0; slice < slices; ++slice) {
       const int p0 = slice * L::kP, cols = min(a.width - p0, L::kP);
+      const int ln = lane_anew();
+      const int l15 = ln & 15, g = ln >> 4, mine = row + l15;
       const bool more = slice + 1 < slices || h + 1 < h1;  // a round follows this one, of:
       const int hn = slice + 1 < slices ? h : h + 1, pn = slice + 1 < slices ? p0 + L::kP : 0;
       v4f dx[kPt];
@@ -329,7 +342,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
               v4f yx = {0, 0, 0, 0};
 #pragma unroll
               for (int k = 0; k < kKp; ++k)
-                mma(yx, frag_row(s.dy, L::ldp, ti * 16, k * 32), frag_row(s.x, L::ldp, row, k * 32));
+                mma(yx, frag_row(s.dy, L::ldp, ti * 16, k * 32, ln), frag_row(s.x, L::ldp, row, k * 32, ln));
               const int t0 = ti * 16 + 4 * g;
               const v4f hi = *reinterpret_cast<const v4f*>(&dc.hi[t0]), lo = *reinterpret_cast<const v4f*>(&dc.lo[t0]);
               v4f pair;
@@ -377,16 +390,16 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
               if (2 * k + 1 < wave) continue;
               const Frag<T> pf = frag_tiles<T>(pw[2 * k], pw[2 * k + 1]), qf = frag_tiles<T>(qw[2 * k], qw[2 * k + 1]);
 #pragma unroll
-              for (int p = 0; p < kPt; ++p) mma(dx[p], frag_col_result(s.dy, L::ldp, k * 32, p * 16), pf);
+              for (int p = 0; p < kPt; ++p) mma(dx[p], frag_col_result(s.dy, L::ldp, k * 32, p * 16, ln), pf);
 #pragma unroll
-              for (int n = 0; n < 2 * NB; ++n) mma(acc[n], frag_col_result(s.c, L::ldn, k * 32, n * 16), qf);
+              for (int n = 0; n < 2 * NB; ++n) mma(acc[n], frag_col_result(s.c, L::ldn, k * 32, n * 16, ln), qf);
             }
           }
           // ---- this lane's row into what follows the step
           const float left = dc.left[mine], to = dc.to[mine];
           Frag<T> bf[L::kRows / 32];
 #pragma unroll
-          for (int k = 0; k < L::kRows / 32; ++k) bf[k] = frag_row(s.b, L::ldn, row, ph * L::kRows + k * 32);
+          for (int k = 0; k < L::kRows / 32; ++k) bf[k] = frag_row(s.b, L::ldn, row, ph * L::kRows + k * 32, ln);
           v4f o[4];  // four tiles at a time: a product waits for the last one on the same tile
 #pragma unroll
           for (int p = 0; p < kPt; ++p) o[p] = v4f{0, 0, 0, 0};
@@ -395,7 +408,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
 #pragma unroll
             for (int z = 0; z < L::kTerms; ++z)
 #pragma unroll
-              for (int p = 0; p < kPt; ++p) mma(o[p], frag_col(s.st[1][z], L::ldp, k * 32, p * 16), bf[k]);
+              for (int p = 0; p < kPt; ++p) mma(o[p], frag_col(s.st[1][z], L::ldp, k * 32, p * 16, ln), bf[k]);
 #pragma unroll
           for (int p = 0; p < kPt; ++p) {
             const v4f x = quad_get(&s.x[mine * L::ldp + p * 16 + 4 * g]);
@@ -406,7 +419,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
           }
           Frag<T> xf[kKp];
 #pragma unroll
-          for (int k = 0; k < kKp; ++k) xf[k] = frag_row(s.x, L::ldp, row, k * 32);
+          for (int k = 0; k < kKp; ++k) xf[k] = frag_row(s.x, L::ldp, row, k * 32, ln);
 #pragma unroll
           for (int n0 = 0; n0 < kNt; n0 += kSide) {
 #pragma unroll
@@ -414,7 +427,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
 #pragma unroll
             for (int k = 0; k < kKp; ++k)
 #pragma unroll
-              for (int n = 0; n < kSide; ++n) mma(o[n], frag_row(s.st[1][0], L::ldp, (n0 + n) * 16, k * 32), xf[k]);
+              for (int n = 0; n < kSide; ++n) mma(o[n], frag_row(s.st[1][0], L::ldp, (n0 + n) * 16, k * 32, ln), xf[k]);
 #pragma unroll
             for (int n = 0; n < kSide; ++n)
 #pragma unroll
@@ -433,7 +446,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
               v4f yx = {0, 0, 0, 0};
 #pragma unroll
               for (int k = 0; k < kKp; ++k)
-                mma(yx, frag_row(s.x, L::ldp, si * 16, k * 32), frag_row(s.dy, L::ldp, row, k * 32));
+                mma(yx, frag_row(s.x, L::ldp, si * 16, k * 32, ln), frag_row(s.dy, L::ldp, row, k * 32, ln));
               const int s0 = si * 16 + 4 * g;
               const v4f hi = *reinterpret_cast<const v4f*>(&dc.hi[s0]), lo = *reinterpret_cast<const v4f*>(&dc.lo[s0]);
               const v4f d = *reinterpret_cast<const v4f*>(&dc.d[s0]);
@@ -449,13 +462,13 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
               if (2 * k > wave) continue;
               const Frag<T> qf = frag_tiles<T>(qw[2 * k], qw[2 * k + 1]);
 #pragma unroll
-              for (int n = 0; n < 2 * NB; ++n) mma(acc[n], frag_col_result(s.b, L::ldn, k * 32, n * 16), qf);
+              for (int n = 0; n < 2 * NB; ++n) mma(acc[n], frag_col_result(s.b, L::ldn, k * 32, n * 16, ln), qf);
             }
           }
           // ---- the starting state into this lane's row
           Frag<T> yf[kKp];
 #pragma unroll
-          for (int k = 0; k < kKp; ++k) yf[k] = frag_row(s.dy, L::ldp, row, k * 32);
+          for (int k = 0; k < kKp; ++k) yf[k] = frag_row(s.dy, L::ldp, row, k * 32, ln);
           const float from = dc.from[mine];
 #pragma unroll
           for (int n0 = 0; n0 < kNt; n0 += kSide) {
@@ -467,7 +480,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
 #pragma unroll
               for (int z = 0; z < L::kTerms; ++z)
 #pragma unroll
-                for (int n = 0; n < kSide; ++n) mma(o[n], frag_row(s.st[0][z], L::ldp, (n0 + n) * 16, k * 32), yf[k]);
+                for (int n = 0; n < kSide; ++n) mma(o[n], frag_row(s.st[0][z], L::ldp, (n0 + n) * 16, k * 32, ln), yf[k]);
 #pragma unroll
             for (int n = 0; n < kSide; ++n) {
               const v4f c = quad_get(&s.c[mine * L::ldn + ph * L::kRows + (n0 + n) * 16 + 4 * g]);

@@ -74,25 +74,25 @@ constexpr int stride_of(int n) {
 }
 
 // Operand whose row (column) index is an LDS row, k along the row: natural order.
-__device__ __forceinline__ Frag<bf16> frag_row(const bf16* p, int ld, int row, int k0) {
-  const int l = threadIdx.x & 63;
+__device__ __forceinline__ Frag<bf16> frag_row(const bf16* p, int ld, int row, int k0,
+                                               int l = threadIdx.x & 63) {
   return {*reinterpret_cast<const v8bf*>(p + (row + (l & 15)) * ld + k0 + 8 * (l >> 4))};
 }
-__device__ __forceinline__ Frag<float> frag_row(const float* p, int ld, int row, int k0) {
-  const int l = threadIdx.x & 63;
+__device__ __forceinline__ Frag<float> frag_row(const float* p, int ld, int row, int k0,
+                                               int l = threadIdx.x & 63) {
   const v4f* r = reinterpret_cast<const v4f*>(p + (row + (l & 15)) * ld + k0 + 8 * (l >> 4));
   return {{r[0], r[1]}};
 }
 // The same in result order.
-__device__ __forceinline__ Frag<bf16> frag_row_result(const bf16* p, int ld, int row, int k0) {
-  const int l = threadIdx.x & 63;
+__device__ __forceinline__ Frag<bf16> frag_row_result(const bf16* p, int ld, int row, int k0,
+                                               int l = threadIdx.x & 63) {
   const bf16* r = p + (row + (l & 15)) * ld + k0 + 4 * (l >> 4);
   const v4bf a = *reinterpret_cast<const v4bf*>(r);
   const v4bf b = *reinterpret_cast<const v4bf*>(r + 16);
   return {__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7)};
 }
-__device__ __forceinline__ Frag<float> frag_row_result(const float* p, int ld, int row, int k0) {
-  const int l = threadIdx.x & 63;
+__device__ __forceinline__ Frag<float> frag_row_result(const float* p, int ld, int row, int k0,
+                                               int l = threadIdx.x & 63) {
   const float* r = p + (row + (l & 15)) * ld + k0 + 4 * (l >> 4);
   return {{*reinterpret_cast<const v4f*>(r), *reinterpret_cast<const v4f*>(r + 16)}};
 }
@@ -108,13 +108,13 @@ __device__ __forceinline__ Frag<bf16> frag_join(v4s a, v4s b) {
   const v8s v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   return {__builtin_bit_cast(v8bf, v)};
 }
-__device__ __forceinline__ Frag<bf16> frag_col(const bf16* p, int ld, int k0, int col) {
-  const int l = threadIdx.x & 63;
+__device__ __forceinline__ Frag<bf16> frag_col(const bf16* p, int ld, int k0, int col,
+                                               int l = threadIdx.x & 63) {
   const bf16* r = p + (k0 + 8 * (l >> 4) + ((l & 15) >> 2)) * ld + col + 4 * (l & 3);
   return frag_join(read_tr(r), read_tr(r + 4 * ld));
 }
-__device__ __forceinline__ Frag<float> frag_col(const float* p, int ld, int k0, int col) {
-  const int l = threadIdx.x & 63;
+__device__ __forceinline__ Frag<float> frag_col(const float* p, int ld, int k0, int col,
+                                               int l = threadIdx.x & 63) {
   const float* r = p + (k0 + 8 * (l >> 4)) * ld + col + (l & 15);
   Frag<float> f;
 #pragma unroll
@@ -122,13 +122,13 @@ __device__ __forceinline__ Frag<float> frag_col(const float* p, int ld, int k0, 
   return f;
 }
 // The same in result order.
-__device__ __forceinline__ Frag<bf16> frag_col_result(const bf16* p, int ld, int k0, int col) {
-  const int l = threadIdx.x & 63;
+__device__ __forceinline__ Frag<bf16> frag_col_result(const bf16* p, int ld, int k0, int col,
+                                               int l = threadIdx.x & 63) {
   const bf16* r = p + (k0 + 4 * (l >> 4) + ((l & 15) >> 2)) * ld + col + 4 * (l & 3);
   return frag_join(read_tr(r), read_tr(r + 16 * ld));
 }
-__device__ __forceinline__ Frag<float> frag_col_result(const float* p, int ld, int k0, int col) {
-  const int l = threadIdx.x & 63;
+__device__ __forceinline__ Frag<float> frag_col_result(const float* p, int ld, int k0, int col,
+                                               int l = threadIdx.x & 63) {
   const float* r = p + (k0 + 4 * (l >> 4)) * ld + col + (l & 15);
   Frag<float> f;
 #pragma unroll
