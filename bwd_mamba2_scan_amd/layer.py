@@ -94,7 +94,7 @@ class _On:
 
     def __enter__(self):
         index = self._dev.index
-        if torch.cuda.current_device() != index:
+        if torch._C._cuda_getDevice() != index:
             self._push(torch.cuda.device(index))
         if self._stream is not None:
             if self._stream.device != self._dev:
@@ -201,6 +201,8 @@ def _span(t):
     lo = t.data_ptr()
     if t.is_contiguous():
         return lo, lo + t.nbytes
+    if t.numel() == 0:
+        return lo, lo
     return lo, lo + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
 
 
@@ -210,17 +212,20 @@ def _apart(outs, ins):
     Slices of one wide row-major tensor interleave without overlapping: equal
     row strides and disjoint windows within the row are told apart.
     """
-    outs = [(n, t) for n, t in outs if t is not None and t.numel()]
-    if not outs:
-        return
-    every = outs + [(n, t) for n, t in ins if t is not None and t.numel()]
     for i, (n, t) in enumerate(outs):
+        if t is None:
+            continue
         lo, hi = _span(t)
-        for m, o in every[i + 1:]:
-            a, b = _span(o)
-            if hi <= a or b <= lo:
+        if lo == hi:
+            continue
+        for m, o in (*outs[i + 1:], *ins):
+            if o is None:
                 continue
-            if not _interleaved(t, o):
+            a = o.data_ptr()
+            if hi <= a:
+                continue
+            a, b = _span(o)
+            if b > lo and a != b and not _interleaved(t, o):
                 raise ValueError(f"{n} overlaps {m}")
 
 
