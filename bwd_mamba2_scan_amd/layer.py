@@ -250,11 +250,11 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _new_rows(t, name, lead, inner, dtype, dev):
-    """(a token-major output, its mamba2_rows): the given tensor, or a new one."""
+def _new_rows(t, name, lead, inner, like, dev):
+    """(a token-major output of a tensor's type, its mamba2_rows): the given tensor, or a new one."""
     if t is not None:
-        return t, _rows(t, name, lead, inner, dtype, dev)
-    t = torch.empty(lead + inner, dtype=dtype, device=dev)
+        return t, _rows(t, name, lead, inner, like.dtype, dev)
+    t = like.new_empty(lead + inner)
     width = 1
     for n in inner:
         width *= n
@@ -300,7 +300,7 @@ def conv_fwd(x, weight, bias=None, *, silu=True, initial_state=None, offsets=Non
     _apart((("y", y), ("final_state", final_state)),
            (("x", x), ("weight", weight), ("bias", bias), ("initial_state", initial_state)))
     with _On(dev, stream) as s:
-        y, ry = _new_rows(y, "y", lead, (channels,), x.dtype, dev)
+        y, ry = _new_rows(y, "y", lead, (channels,), x, dev)
         final_state, s1 = _new_dense(final_state, "final_state", (batch, taps - 1, channels), x.dtype, dev,
                                      want_final_state)
         st = lib.mamba2_conv_fwd(typ, seqs, channels, taps, bool(silu), rx, w, b, s0, ry, s1, s)
@@ -328,7 +328,7 @@ def conv_bwd(x, weight, d_y, bias=None, *, silu=True, initial_state=None, d_fina
             ("d_final_state", d_final_state)))
     with _On(dev, stream) as s:
         get = res.get
-        res["d_x"], rx1 = _new_rows(get("d_x"), "d_x", lead, (channels,), x.dtype, dev)
+        res["d_x"], rx1 = _new_rows(get("d_x"), "d_x", lead, (channels,), x, dev)
         res["d_weight"], w1 = _new_dense(get("d_weight"), "d_weight", (channels, taps), torch.float32, dev)
         res["d_bias"], b1 = (_new_dense(get("d_bias"), "d_bias", (channels,), torch.float32, dev)
                              if bias is not None else (None, None))
@@ -367,11 +367,10 @@ def conv_step(x, weight, state, bias=None, *, silu=True, new_state=None, y=None,
         raise TypeError("state must be a torch.Tensor")
     b = _dense(bias, "bias", (channels,), torch.float32, dev)
     if y is not None or new_state is not None:
-        _apart((("y", y), ("new_state", None if new_state is state else new_state)),
-               (("x", x), ("weight", weight), ("bias", bias), ("state", state)))
+        _apart((("y", y), ("new_state", None if new_state is state else new_state)), (("x", x), ("state", state)))
     s1 = s0 if new_state is None else _dense(new_state, "new_state", tail, x.dtype, dev)
     with _On(dev, stream) as s:
-        y, ry = _new_rows(y, "y", (batch,), (channels,), x.dtype, dev)
+        y, ry = _new_rows(y, "y", (batch,), (channels,), x, dev)
         st = lib.mamba2_conv_step(typ, batch, channels, taps, bool(silu), rx, w, b, s0, _token(ry), s1, s)
     _raise(st, "mamba2_conv_step")
     return y
@@ -420,7 +419,7 @@ def ssm_fwd(x, dt, A, B, C, *, D=None, dt_bias=None, softplus=True, initial_stat
            (("x", x), ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("dt_bias", dt_bias),
             ("initial_state", initial_state)))
     with _On(dev, stream) as s:
-        y, py = _new_rows(y, "y", lead, (d.heads, d.width), x.dtype, dev)
+        y, py = _new_rows(y, "y", lead, (d.heads, d.width), x, dev)
         final_state, s1 = _new_dense(final_state, "final_state", shape, torch.float32, dev, want_final_state)
         workspace, nbytes = _workspace(workspace, lib.mamba2_ssm_fwd_workspace_bytes(seqs, d), dev)
         st = lib.mamba2_ssm_fwd(seqs, d, px, pdt, pA, pB, pC, pD, pbias, s0, py, s1, _ptr(workspace), nbytes, s)
@@ -449,9 +448,8 @@ def ssm_bwd(x, dt, A, B, C, d_y, *, D=None, dt_bias=None, softplus=True, initial
             ("initial_state", initial_state), ("d_final_state", d_final_state)))
     with _On(dev, stream) as s:
         ptr = {}
-        for name, size, dtype in (("d_x", inner, x.dtype), ("d_dt", vec, dt.dtype), ("d_B", shared, x.dtype),
-                                  ("d_C", shared, x.dtype)):
-            res[name], ptr[name] = _new_rows(res.get(name), name, lead, size, dtype, dev)
+        for name, size, like in (("d_x", inner, x), ("d_dt", vec, dt), ("d_B", shared, x), ("d_C", shared, x)):
+            res[name], ptr[name] = _new_rows(res.get(name), name, lead, size, like, dev)
         for name, given, size in (("d_A", A, vec), ("d_D", D, vec), ("d_dt_bias", dt_bias, vec),
                                   ("d_initial_state", initial_state, shape)):
             if given is None:
@@ -483,11 +481,10 @@ def ssm_step(x, dt, A, B, C, state, *, D=None, dt_bias=None, softplus=True, new_
     if s0 is None:
         raise TypeError("state must be a torch.Tensor")
     if y is not None or new_state is not None:
-        _apart((("y", y), ("new_state", None if new_state is state else new_state)),
-               (("x", x), ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("dt_bias", dt_bias), ("state", state)))
+        _apart((("y", y), ("new_state", None if new_state is state else new_state)), (("x", x), ("state", state)))
     s1 = s0 if new_state is None else _dense(new_state, "new_state", shape, torch.float32, dev)
     with _On(dev, stream) as s:
-        y, py = _new_rows(y, "y", (batch,), (d.heads, d.width), x.dtype, dev)
+        y, py = _new_rows(y, "y", (batch,), (d.heads, d.width), x, dev)
         for r in (px, pdt, pB, pC, py):
             _token(r)
         st = lib.mamba2_ssm_step(batch, d, px, pdt, pA, pB, pC, pD, pbias, s0, py, s1, s)
