@@ -111,18 +111,25 @@ template <class T>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t run_rsrc(const T* p) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(static_cast<const void*>(p)), 0, 0x7fffffff, 0x00020000);
 }
+// A store's row goes into the lane's offset, not into a scalar one: a 16-byte
+// store that takes a scalar offset reads its data registers late, the compiler
+// counts on it not to, and an instruction right behind that writes them changed
+// the first 8 bytes that lanes 12 .. 15 of every 16 stored, now and then, when
+// the memory was busy.  Without one the compiler keeps the distance.  One
+// addition per row, which no measurement shows.
 template <class T, int V>
 __device__ __forceinline__ void put(__amdgpu_buffer_rsrc_t rs, int lane_off, int row_off, const float (&v)[V]) {
+  const int off = lane_off + row_off;
   if constexpr (V == 1) {
     const T t = static_cast<T>(v[0]);
-    if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, t), rs, lane_off, row_off, 0);
-    else __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(t), rs, lane_off, row_off, 0);
+    if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, t), rs, off, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(t), rs, off, 0, 0);
   } else {
     typename Vec<T>::type r;
 #pragma unroll
     for (int i = 0; i < V; ++i) r[i] = static_cast<T>(v[i]);
     typedef int v4i __attribute__((ext_vector_type(4)));
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, r), rs, lane_off, row_off, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, r), rs, off, 0, 0);
   }
 }
 

@@ -64,8 +64,8 @@ def check(p, y, final, g, spans, silu):
             if got is not None:
                 within(got, e[name], 16 * U * s[name] + rel * noise[name] + half_step(typ) * e[name].abs(), f"{name} {row}")
         d_weight, d_bias = d_weight + e["d_weight"], d_bias + e["d_bias"]
-        wsize = wsize + s["d_weight"] + rel / U * noise["d_weight"] / 1
-        bsize = bsize + s["d_bias"] + rel / U * noise["d_bias"] / 1
+        wsize = wsize + s["d_weight"] + rel / U * noise["d_weight"]
+        bsize = bsize + s["d_bias"] + rel / U * noise["d_bias"]
         tokens += x.shape[0]
     if g is not None:
         # sums over the tokens: at most 32 + units of them one after another, in fp32
@@ -185,6 +185,42 @@ def test_refusals_of_the_binding():
     with pytest.raises(m2.Mamba2ScanError) as e:
         m2.conv_fwd(p["x"][:1].expand(2, 9, 16), p["weight"])
     assert e.value.status == m2.EBADDIM
+
+
+@pytest.mark.parametrize("typ,batch,L,channels", [("bf16", 4, 4096, 4096), ("f32", 2, 8191, 2056)])
+def test_long_runs_under_load(typ, batch, L, channels):
+    """Enough tokens that a wave walks the longest runs and the memory is busy: every value of several calls,
+    against the formulas in 64 bits."""
+    taps = 4
+    g = torch.Generator(DEV).manual_seed(11)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    x, d_y = r(batch, L, channels).to(TYPES[typ]), r(batch, L, channels).to(TYPES[typ])
+    weight, bias = r(channels, taps), r(channels)
+    print("long conv", typ, batch, L, channels, flush=True)
+    calls = [(m2.conv_fwd(x, weight, bias), m2.conv_bwd(x, weight, d_y, bias)) for _ in range(3)]
+    for row in range(batch):
+        xs = torch.nn.functional.pad(x[row].double(), (0, 0, taps - 1, 0))
+        w = weight.double()
+        terms = [w[:, k] * xs[k:k + L] for k in range(taps)]
+        pre = bias.double() + sum(terms)
+        slack = _slack(TYPES[typ], bias.double().abs() + sum(t.abs() for t in terms))
+        del terms
+        sig = torch.sigmoid(pre)
+        want = pre * sig
+        for (y, _), _g in calls:
+            assert bool(((y[row].double() - want).abs() <= slack + half_step(TYPES[typ]) * want.abs()).all()), row
+        # d pre is off by at most d_y times the slack (the slope's slope is below 1) and a dozen roundings
+        dp = torch.nn.functional.pad(d_y[row].double() * sig * (1 + pre * (1 - sig)), (0, 0, 0, taps - 1))
+        off = torch.nn.functional.pad(d_y[row].double().abs() * (slack + 16 * U), (0, 0, 0, taps - 1))
+        want = sum(w[:, k] * dp[taps - 1 - k:taps - 1 - k + L] for k in range(taps))
+        size = sum(w[:, k].abs() * dp[taps - 1 - k:taps - 1 - k + L].abs() for k in range(taps))
+        room = sum(w[:, k].abs() * off[taps - 1 - k:taps - 1 - k + L] for k in range(taps))
+        room = room + 16 * U * size + half_step(TYPES[typ]) * want.abs()
+        for _f, grads in calls:
+            assert bool(((grads["d_x"][row].double() - want).abs() <= room).all()), row
+    for _f, grads in calls:
+        for k in ("d_weight", "d_bias"):
+            assert torch.equal(grads[k], calls[0][1][k]), k
 
 
 def test_no_tokens():
