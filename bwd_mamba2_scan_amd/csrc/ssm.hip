@@ -70,9 +70,7 @@ __global__ __launch_bounds__(NW * 64, sizeof(T) == 2 ? 2 : NB == 4 ? 1 : 2) void
 
   State<NB, true> st;
   st.init(a.width, p0, wave);
-  st.load(u.index == 0 ? (a.initial == nullptr ? nullptr : a.initial + of_seq)
-                       : w.seg_state + (static_cast<long>(unit) * a.heads + h) * head,
-          a.width, a.states);
+  start_state(st, a, w, u, unit, h);
   // tiles above the diagonal that a 32-wide product step touches stay zero
   for (int i = tid; i < kTok * L::ldw; i += kThreads) s.w[i] = static_cast<T>(0.0f);
 
@@ -280,9 +278,11 @@ int launch_fwd(const SsmArgs& a, const Walk& w, bool segments, unsigned blocks, 
   if (segments) {
     ssm_summary_kernel<T, NB, NW><<<blocks, NW * 64, 0, s>>>(a, w);
     if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
-    const unsigned quads = static_cast<unsigned>((a.states * a.width + 1023) / 1024);
-    ssm_carry_kernel<<<dim3(quads, a.heads, a.q.batch), 256, 0, s>>>(a, w);
-    if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
+    if (!a.fold) {
+      const unsigned quads = static_cast<unsigned>((a.states * a.width + 1023) / 1024);
+      ssm_carry_kernel<<<dim3(quads, a.heads, a.q.batch), 256, 0, s>>>(a, w);
+      if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
+    }
   }
   ssm_fwd_kernel<T, NB, NW><<<blocks, NW * 64, 0, s>>>(a, w);
   return launch_status();
@@ -365,6 +365,15 @@ int segment_tokens(const mamba2_seqs& q, const mamba2_ssm_dims& d) {
   return static_cast<int>(seg < 2 * kTok ? 2 * kTok : seg);
 }
 
+// Few segments add up the states before them themselves: i of them read
+// i (i - 1) / 2 states where the carry pass reads and writes 2 (i - 1) in a
+// launch of its own (4 segments: 3 us more in the pass behind, 7 us less before
+// it).  How a packed call's rows are shared out is not known here; with
+// several sequences each is taken to have a part of them.
+int fold_segments(const mamba2_seqs& q, int seg) {
+  return units_of(q.length, seg) <= 8 * (q.offsets != nullptr ? min(q.batch, 3) : 1);
+}
+
 }  // namespace ssm
 
 extern "C" {
@@ -435,6 +444,7 @@ int mamba2_ssm_fwd(mamba2_seqs q, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows 
   a.slices = (d.width + nw * 16 - 1) / (nw * 16);
   a.seg = segment_tokens(q, d);
   a.units = static_cast<int>(unit_count(q, a.seg));
+  a.fold = fold_segments(q, a.seg);
   Walk w = {};
   w.v = x;
   w.m = B;

@@ -639,9 +639,11 @@ int launch_bwd(const Call& c) {
   if (c.p.segments) {
     ssm_walk_summary_kernel<T, NB, NW><<<grid, NW * 64, 0, c.s>>>(a, c.w);
     if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
-    const unsigned quads = static_cast<unsigned>((a.states * a.width + 1023) / 1024);
-    ssm_walk_carry_kernel<<<dim3(quads, a.heads, 2 * a.q.batch), 256, 0, c.s>>>(a, c.w);
-    if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
+    if (!a.fold) {
+      const unsigned quads = static_cast<unsigned>((a.states * a.width + 1023) / 1024);
+      ssm_walk_carry_kernel<<<dim3(quads, a.heads, 2 * a.q.batch), 256, 0, c.s>>>(a, c.w);
+      if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
+    }
   }
   ssm_walk_kernel<T, NB, NW><<<grid, NW * 64, 0, c.s>>>(a, c.w);
   if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
@@ -725,6 +727,7 @@ int mamba2_ssm_bwd(mamba2_seqs q, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows 
   a.slices = c.p.slices;
   a.seg = c.p.seg;
   a.units = c.p.units;
+  a.fold = fold_segments(q, a.seg);
 
   float* w = static_cast<float*>(workspace);
   const auto take = [&w](size_t n) {

@@ -31,6 +31,7 @@ struct SsmArgs {
   int softplus, dt_bf16;
   int seg;                 // tokens per segment (a multiple of kTok)
   int units;
+  int fold;                // a segment adds up the states before it itself; no carry pass
 };
 
 // A 16 x 32 (or 32 x 16) matrix operand: lane l holds row (column) l & 15 and
@@ -524,6 +525,32 @@ struct WalkLds {
   alignas(16) Decays dc[2];
 };
 
+// The state a segment starts from: the sequence's first one, brought through
+// the segments before it (in the pass's direction), whose own contributions
+// lie in the place of the segment behind each.  With few segments every one
+// does that itself; the carry pass leaves the sum in their places otherwise.
+template <int NB, bool COLS>
+__device__ __forceinline__ void start_state(State<NB, COLS>& st, const SsmArgs& a, const Walk& w, const Unit& u, int unit,
+                                            int h) {
+  const long head = static_cast<long>(a.states) * a.width;
+  const int d = w.rev ? -1 : 1;
+  const int before = w.rev ? units_of(u.len, a.seg) - 1 - u.index : u.index;
+  if (before > 0 && !a.fold) {
+    st.load(w.seg_state + (static_cast<long>(unit) * a.heads + h) * head, a.width, a.states);
+    return;
+  }
+  st.load(w.first == nullptr ? nullptr : w.first + (static_cast<long>(u.seq) * a.heads + h) * head, a.width, a.states);
+  for (int i = before - 1; i >= 0; --i) {
+    const long at = (static_cast<long>(unit) - d * i) * a.heads + h;
+    State<NB, COLS> own;
+    own.off = st.off;
+    own.load(w.seg_state + at * head, a.width, a.states);
+    const float decay = w.seg_decay[at - d * a.heads];
+#pragma unroll
+    for (int n = 0; n < 2 * NB; ++n) st.st[n] = st.st[n] * decay + own.st[n];
+  }
+}
+
 // KEEP false: the summary of a segment that another follows, from a zero
 // state, into that segment's place.  KEEP true: the walk itself, from the
 // states the carry left, writing every step's starting state.
@@ -539,7 +566,6 @@ __device__ __forceinline__ void walk(const SsmArgs& a, const Walk& w, WalkLds<T,
   const int slice = work % a.slices;
   const Unit u = locate(a.q, unit, a.seg);
   if (!u.live) return;
-  const bool first = w.rev ? u.t0 + static_cast<long>(a.seg) >= u.len : u.index == 0;
   const bool last = w.rev ? u.index == 0 : u.t0 + static_cast<long>(a.seg) >= u.len;
   if (!KEEP && last) return;
   const bool packed = a.q.offsets != nullptr;
@@ -554,8 +580,7 @@ __device__ __forceinline__ void walk(const SsmArgs& a, const Walk& w, WalkLds<T,
   State<NB, false> st;
   st.init(a.width, p0, wave);
   if (KEEP) {
-    const float* from = first ? (w.first == nullptr ? nullptr : w.first + of_seq) : w.seg_state + at * head;
-    st.load(from, a.width, a.states);
+    start_state(st, a, w, u, unit, h);
   } else {
     st.zero();
   }
@@ -674,5 +699,6 @@ int check_vec_rows(const mamba2_rows& r, const mamba2_seqs& q, long long width, 
 int check_step_rows(const mamba2_rows& r, const mamba2_seqs& q, const mamba2_ssm_dims& d);
 int waves_of(int width);
 int segment_tokens(const mamba2_seqs& q, const mamba2_ssm_dims& d);
+int fold_segments(const mamba2_seqs& q, int seg);
 
 }  // namespace ssm
