@@ -67,6 +67,7 @@ struct BwdLds {
   static constexpr int kN = NB * 32;
   static constexpr int kP = PT * 16 < 32 ? 32 : PT * 16;  // a product over the columns takes 32 at a time
   static constexpr int kTerms = sizeof(T) == 2 ? 2 : 1;
+  static constexpr int kQ = sizeof(T) == 2 ? 2 : 1;
   static constexpr int kRows = sizeof(T) == 2 || kN < 64 ? kN : 64;  // state rows staged at a time
   // b and c are read by rows and, in fours of neighbouring ones, by columns:
   // 32 bytes of padding put four rows of 128 bf16 into different banks
@@ -133,10 +134,10 @@ struct StateTile {
 };
 
 // Two result tiles stacked along k as one operand.
-template <class T>
-__device__ __forceinline__ Frag<T> frag_tiles(const v4f& a, const v4f& b) {
+template <class T, int TERMS>
+__device__ __forceinline__ Split<T, TERMS> split_tiles(const v4f& a, const v4f& b) {
   const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-  return frag_of<T>(v);
+  return split_of<T, TERMS>(v);
 }
 
 // The lane's number, as if it could change: what is computed from it stays in
@@ -171,6 +172,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
   constexpr int kPt = L::kP / 16;
   constexpr int kPhases = L::kN / L::kRows;
   constexpr int kNt = L::kRows / 16;  // 16-row tiles of the state per phase
+  constexpr int kBatch = 2 * NB < 4 ? 2 * NB : 4;
   constexpr int kSide = kNt < 4 ? kNt : 4;
   const int tid = threadIdx.x, id = wave_id(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
   const bool for_x = id < 4;
@@ -388,18 +390,29 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               if (2 * k + 1 < wave) continue;
-              const Frag<T> pf = frag_tiles<T>(pw[2 * k], pw[2 * k + 1]), qf = frag_tiles<T>(qw[2 * k], qw[2 * k + 1]);
+              const Frag<T> pf = split_tiles<T, 1>(pw[2 * k], pw[2 * k + 1]).f[0];
+              const auto qf = split_tiles<T, L::kQ>(qw[2 * k], qw[2 * k + 1]);
 #pragma unroll
               for (int p = 0; p < kPt; ++p) mma(dx[p], frag_col_result(s.dy, L::ldp, k * 32, p * 16, ln), pf);
 #pragma unroll
-              for (int n = 0; n < 2 * NB; ++n) mma(acc[n], frag_col_result(s.c, L::ldn, k * 32, n * 16, ln), qf);
+              for (int n0 = 0; n0 < 2 * NB; n0 += kBatch) {
+                Frag<T> cf[kBatch];
+#pragma unroll
+                for (int n = 0; n < kBatch; ++n) cf[n] = frag_col_result(s.c, L::ldn, k * 32, (n0 + n) * 16, ln);
+#pragma unroll
+                for (int z = 0; z < L::kQ; ++z)
+#pragma unroll
+                  for (int n = 0; n < kBatch; ++n) mma(acc[n0 + n], cf[n], qf.f[z]);
+              }
             }
           }
           // ---- this lane's row into what follows the step
-          const float left = dc.left[mine], to = dc.to[mine];
+          const float to = dc.to[mine];
+          const float left = kFlips<T> && (l15 & 1) != 0 ? -dc.left[mine] : dc.left[mine];
           Frag<T> bf[L::kRows / 32];
 #pragma unroll
-          for (int k = 0; k < L::kRows / 32; ++k) bf[k] = frag_row(s.b, L::ldn, row, ph * L::kRows + k * 32, ln);
+          for (int k = 0; k < L::kRows / 32; ++k) 
+            bf[k] = flip_odd(frag_row(s.b, L::ldn, row, ph * L::kRows + k * 32, ln), l15);
           v4f o[4];  // four tiles at a time: a product waits for the last one on the same tile
 #pragma unroll
           for (int p = 0; p < kPt; ++p) o[p] = v4f{0, 0, 0, 0};
@@ -460,16 +473,24 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               if (2 * k > wave) continue;
-              const Frag<T> qf = frag_tiles<T>(qw[2 * k], qw[2 * k + 1]);
+              const auto qf = split_tiles<T, L::kQ>(qw[2 * k], qw[2 * k + 1]);
 #pragma unroll
-              for (int n = 0; n < 2 * NB; ++n) mma(acc[n], frag_col_result(s.b, L::ldn, k * 32, n * 16, ln), qf);
+              for (int n0 = 0; n0 < 2 * NB; n0 += kBatch) {
+                Frag<T> cf[kBatch];
+#pragma unroll
+                for (int n = 0; n < kBatch; ++n) cf[n] = frag_col_result(s.b, L::ldn, k * 32, (n0 + n) * 16, ln);
+#pragma unroll
+                for (int z = 0; z < L::kQ; ++z)
+#pragma unroll
+                  for (int n = 0; n < kBatch; ++n) mma(acc[n0 + n], cf[n], qf.f[z]);
+              }
             }
           }
           // ---- the starting state into this lane's row
           Frag<T> yf[kKp];
 #pragma unroll
-          for (int k = 0; k < kKp; ++k) yf[k] = frag_row(s.dy, L::ldp, row, k * 32, ln);
-          const float from = dc.from[mine];
+          for (int k = 0; k < kKp; ++k) yf[k] = flip_odd(frag_row(s.dy, L::ldp, row, k * 32, ln), l15);
+          const float from = kFlips<T> && (l15 & 1) != 0 ? -dc.from[mine] : dc.from[mine];
 #pragma unroll
           for (int n0 = 0; n0 < kNt; n0 += kSide) {
             v4f o[kSide];
