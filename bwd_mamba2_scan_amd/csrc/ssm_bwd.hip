@@ -62,12 +62,36 @@ __global__ __launch_bounds__(256) void ssm_walk_carry_kernel(SsmArgs a, Walks ws
 
 constexpr int kBwdThreads = 512;
 
+// A state in LDS.  bf16: strips of 16 columns, each with its rows one after
+// the other (32 bytes a row), so that a tile is written, and an operand read by
+// rows or by columns, from neighbouring banks without padding; three parts of
+// both states fit that way.  fp32: rows of LD.
+template <class T, int ROWS, int COLS, int LD>
+struct StateLds {
+  static constexpr bool kStrips = sizeof(T) == 2;
+  static constexpr int kSize = ROWS * (kStrips ? COLS : LD);
+  static __device__ __forceinline__ int at(int row, int col) {
+    return kStrips ? (col >> 4) * (ROWS * 16) + row * 16 + (col & 15) : row * LD + col;
+  }
+  static __device__ __forceinline__ Frag<T> by_row(const T* p, int row, int k0, int l) {
+    if constexpr (kStrips)
+      return {*reinterpret_cast<const v8bf*>(p + (k0 >> 4) * (ROWS * 16) + (l >> 5) * (ROWS * 16) +
+                                             (row + (l & 15)) * 16 + (l >> 4 & 1) * 8)};
+    else
+      return frag_row(p, LD, row, k0, l);
+  }
+  static __device__ __forceinline__ Frag<T> by_col(const T* p, int k0, int col, int l) {
+    if constexpr (kStrips) return frag_col(p + (col >> 4) * (ROWS * 16), 16, k0, 0, l);
+    else return frag_col(p, LD, k0, col, l);
+  }
+};
+
 template <class T, int NB, int PT>
 struct BwdLds {
   static constexpr int kN = NB * 32;
   static constexpr int kP = PT * 16 < 32 ? 32 : PT * 16;  // a product over the columns takes 32 at a time
-  static constexpr int kTerms = sizeof(T) == 2 ? 2 : 1;
-  static constexpr int kQ = sizeof(T) == 2 ? 2 : 1;
+  static constexpr int kTerms = sizeof(T) == 2 ? 3 : 1;
+  static constexpr int kQ = sizeof(T) == 2 ? 2 : 1;  // parts of Q: with one, its rounding shows in d_B and d_C (2.4e-3 against 1.7e-3)
   static constexpr int kRows = sizeof(T) == 2 || kN < 64 ? kN : 64;  // state rows staged at a time
   // b and c are read by rows and, in fours of neighbouring ones, by columns:
   // 32 bytes of padding put four rows of 128 bf16 into different banks
@@ -77,7 +101,8 @@ struct BwdLds {
   alignas(16) T c[kTok * ldn];
   alignas(16) T x[kTok * ldp];
   alignas(16) T dy[kTok * ldp];
-  alignas(16) T st[2][kTerms][kRows * ldp];  // rows of the starting state and of the gradient behind the step
+  typedef StateLds<T, kRows, kP, ldp> State;
+  alignas(16) T st[2][kTerms][State::kSize];  // rows of the starting state and of the gradient behind the step
   alignas(16) DecaysOf<true> dc[3];  // of the head before (its gradients are put together), this one and the next
   float slope[3][kTok];      // d d_t / d dt_t
   struct Sums {              // of a head and the one before
@@ -91,8 +116,10 @@ struct BwdLds {
 };
 
 // Rows of a [states][width] fp32 matrix slice in registers, then LDS, where a
-// bf16 product finds them in two terms (16 bits; a third would not fit, and
-// only the sums over thousands of tokens that d_A and d_dt_bias are show it).
+// bf16 product finds them whole, in three parts.  d_x and d_C would do with
+// two, but d_A and d_dt_bias, fp32 sums of terms of both signs, show the third:
+// 2e-7 of them against 7e-7, and 1.5e-6 over short sequences (for 40 of 287 us
+// at 4 x 4096 tokens, 32 heads of 64 columns, 128 states).
 template <class T, int NB, int PT>
 struct StateTile {
   typedef BwdLds<T, NB, PT> L;
@@ -114,20 +141,23 @@ struct StateTile {
                                          kNonTemporal));
     }
   }
-  __device__ __forceinline__ void store(T (&st)[L::kTerms][L::kRows * L::ldp]) const {
+  __device__ __forceinline__ void store(T (&st)[L::kTerms][L::State::kSize]) const {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int t = wave_id() + i * kWaves;
       if (kAll % kWaves != 0 && t >= kAll) continue;
-      T* p = &st[0][(t % kTiles * 16 + (lane & 15)) * L::ldp + t / kTiles * 16 + 4 * (lane >> 4)];
-      if constexpr (L::kTerms == 2) {
-        const unsigned a = pack_bf16(v[i][0], v[i][1]), b = pack_bf16(v[i][2], v[i][3]);
-        *reinterpret_cast<v2u*>(p) = v2u{a, b};
-        quad_put(p + L::kRows * L::ldp,
-                 v4f{v[i][0] - low_of(a), v[i][1] - high_of(a), v[i][2] - low_of(b), v[i][3] - high_of(b)});
-      } else {
-        quad_put(p, v[i]);
+      T* p = &st[0][L::State::at(t % kTiles * 16 + (lane & 15), t / kTiles * 16 + 4 * (lane >> 4))];
+      v4f r = v[i];
+#pragma unroll
+      for (int z = 0; z < L::kTerms; ++z) {
+        if constexpr (L::kTerms > 1) {
+          const unsigned a = pack_bf16(r[0], r[1]), b = pack_bf16(r[2], r[3]);
+          *reinterpret_cast<v2u*>(p + z * L::State::kSize) = v2u{a, b};
+          r = v4f{r[0] - low_of(a), r[1] - high_of(a), r[2] - low_of(b), r[3] - high_of(b)};
+        } else {
+          quad_put(p, r);
+        }
       }
     }
   }
@@ -386,7 +416,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
             if (g == 0) sum.direct[mine] = slice == 0 ? direct : sum.direct[mine] + direct;
             skip = sum64(skip);
             if (lane == 0) sum.skip[wave] = slice == 0 ? skip : sum.skip[wave] + skip;
-            // The products' own operands keep 8 bits with bf16, as their results do.
+            // P goes in with 8 bits, as d_x comes out: one term among the three of d_x.
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               if (2 * k + 1 < wave) continue;
@@ -411,7 +441,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
           const float left = kFlips<T> && (l15 & 1) != 0 ? -dc.left[mine] : dc.left[mine];
           Frag<T> bf[L::kRows / 32];
 #pragma unroll
-          for (int k = 0; k < L::kRows / 32; ++k) 
+          for (int k = 0; k < L::kRows / 32; ++k)
             bf[k] = flip_odd(frag_row(s.b, L::ldn, row, ph * L::kRows + k * 32, ln), l15);
           v4f o[4];  // four tiles at a time: a product waits for the last one on the same tile
 #pragma unroll
@@ -421,7 +451,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
 #pragma unroll
             for (int z = 0; z < L::kTerms; ++z)
 #pragma unroll
-              for (int p = 0; p < kPt; ++p) mma(o[p], frag_col(s.st[1][z], L::ldp, k * 32, p * 16, ln), bf[k]);
+              for (int p = 0; p < kPt; ++p) mma(o[p], L::State::by_col(s.st[1][z], k * 32, p * 16, ln), bf[k]);
 #pragma unroll
           for (int p = 0; p < kPt; ++p) {
             const v4f x = quad_get(&s.x[mine * L::ldp + p * 16 + 4 * g]);
@@ -440,7 +470,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
 #pragma unroll
             for (int k = 0; k < kKp; ++k)
 #pragma unroll
-              for (int n = 0; n < kSide; ++n) mma(o[n], frag_row(s.st[1][0], L::ldp, (n0 + n) * 16, k * 32, ln), xf[k]);
+              for (int n = 0; n < kSide; ++n) mma(o[n], L::State::by_row(s.st[1][0], (n0 + n) * 16, k * 32, ln), xf[k]);
 #pragma unroll
             for (int n = 0; n < kSide; ++n)
 #pragma unroll
@@ -501,7 +531,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
 #pragma unroll
               for (int z = 0; z < L::kTerms; ++z)
 #pragma unroll
-                for (int n = 0; n < kSide; ++n) mma(o[n], frag_row(s.st[0][z], L::ldp, (n0 + n) * 16, k * 32, ln), yf[k]);
+                for (int n = 0; n < kSide; ++n) mma(o[n], L::State::by_row(s.st[0][z], (n0 + n) * 16, k * 32, ln), yf[k]);
 #pragma unroll
             for (int n = 0; n < kSide; ++n) {
               const v4f c = quad_get(&s.c[mine * L::ldn + ph * L::kRows + (n0 + n) * 16 + 4 * g]);
