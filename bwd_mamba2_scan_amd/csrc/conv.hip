@@ -6,11 +6,15 @@
 //   d_x_u = sum_k w[k] dp_{u+W-1-k},  d_w[k] = sum_t dp_t x_{t-W+1+k},  d_bias = sum_t dp_t
 //
 // A few operations per element against two (forward) or three (backward)
-// streamed tensors: bound by HBM.  A lane owns 16 bytes of channels and walks
-// a run of tokens with the last W - 1 inputs (and W pre-activation gradients)
-// in registers, so x and d_y are read once but for the W - 1 tokens where runs
-// meet.  The next tokens' loads are in flight while the
-// last ones are computed.
+// streamed tensors: bound by HBM, the backward nearly as much by arithmetic.
+// A lane owns 16 bytes of channels and walks a run of tokens with the last
+// W - 1 inputs (and W pre-activation gradients) in registers, so x and d_y are
+// read once but for the W - 1 tokens where runs meet.  The next tokens' loads
+// are in flight while the last ones are computed.
+// At 4 x 4096 tokens of 4352 bf16 channels, 4 taps: forward 55 us, 285 MB at
+// 5.2 TB/s, what a large copy reaches; backward 114 us, 428 MB at 3.8 TB/s: its
+// loop is 290 vector instructions a token and wave, 16 of them exponentials and
+// reciprocals, or 88 us of the vector units.
 #include "layer_common.h"
 
 namespace {
@@ -144,6 +148,9 @@ __device__ __forceinline__ void shift(float (&win)[W][V], const Raw<T, V>& next)
   }
 }
 
+// Bound by HBM in long calls and by the number of waves in short ones (9
+// prompts of 5515 tokens, 2304 channels: 16 us).  A lane has a run's whole
+// window, so no LDS and no exchange between lanes are needed.
 // Blocks 0 .. units * cblocks - 1 each compute a run of tokens; the blocks
 // behind them copy the sequences' last W - 1 inputs to final_state.
 template <class T, int V, int W, bool SILU>
@@ -227,8 +234,12 @@ __device__ __forceinline__ void pre_grad(const float (&w)[W][V], const float (&b
   }
 }
 
-// A work-group's waves take neighbouring runs of one unit; the blocks behind
-// the units compute d_initial_state.
+// A work-group's waves take neighbouring runs of one unit, and their sums of
+// the weights' gradients meet in LDS, so that a unit leaves one partial per
+// channel and tap; the blocks behind the units compute d_initial_state.  The
+// pre-activation is recomputed from x: a saved one would be another tensor to
+// read.  W - 1 tokens behind the run are loaded and differentiated again, 3 in
+// 32.
 template <class T, int V, int W, bool SILU>
 __global__ __launch_bounds__(kLanes * kBwdWaves, 2) void conv_bwd_kernel(ConvArgs a) {
   __shared__ float lds[kBwdWaves][kLanes * V];
@@ -400,7 +411,8 @@ __global__ __launch_bounds__(kLanes * kBwdWaves, 2) void conv_bwd_kernel(ConvArg
   }
 }
 
-// Sums the units' partials of one (tap or bias, channel) in a fixed order:
+// 4.5 us for 128 units of 4352 channels and 5 sums each (11 MB), most of it the
+// launch.  Sums the units' partials of one (tap or bias, channel) in a fixed order:
 // lanes over channels, four waves over the units.
 __global__ __launch_bounds__(256) void conv_reduce_kernel(const float* partial, int units, int channels, int taps,
                                                           float* d_weight, float* d_bias) {
@@ -426,6 +438,8 @@ __global__ __launch_bounds__(256) void conv_reduce_kernel(const float* partial, 
   }
 }
 
+// One token: bound by the launch (16 sequences of 2304 channels, 0.6 MB: 3 us).
+// The window is read before it is written, so new_state may be state itself.
 template <class T, int V, int W, bool SILU>
 __global__ __launch_bounds__(kLanes) void conv_step_kernel(ConvArgs a) {
   const int c0 = (blockIdx.x * kLanes + threadIdx.x) * V;

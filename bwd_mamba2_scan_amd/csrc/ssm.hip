@@ -15,7 +15,13 @@
 // Long sequences with few heads are cut into segments that run in parallel:
 // a summary pass (ssm_summary_kernel: each segment's own contribution to
 // the state), the carry across segments (ssm_carry_kernel), and the forward from
-// the states so found.
+// the states so found.  Few segments carry by themselves (start_state).
+//
+// Measured at 4 x 4096 tokens, 32 heads of 64 columns, one group of 128 states,
+// bf16: summary 43 us, forward 87 us.  The bytes (164 MB) would take 32 us and
+// the products 17 us at this card's rates; what bounds both kernels is LDS,
+// whose pipes are busy 60 % of the forward's time, and the two barriers of a
+// step, which two work-groups on a CU hide for each other (matrix cores: 24 %).
 #include "ssm_common.h"
 
 namespace {
@@ -187,7 +193,8 @@ __global__ __launch_bounds__(NW * 64, sizeof(T) == 2 ? 2 : NB == 4 ? 1 : 2) void
     st.save(a.final_state + of_seq, a.width, a.states);
 }
 
-// Summary pass of the segments; see walk().
+// Summary pass of the segments; see walk().  43 us where the forward takes 87:
+// it reads x and B (52 MB) and has no scores to compute.
 template <class T, int NB, int NW>
 __global__ __launch_bounds__(NW * 64, 2) void ssm_summary_kernel(SsmArgs a, Walk w) {
   __shared__ WalkLds<T, NB, NW> s;
@@ -199,7 +206,9 @@ __global__ __launch_bounds__(256) void ssm_carry_kernel(SsmArgs a, Walk w) { car
 // ------------------------------------------------------------- single token
 // A work-group per sequence and head; a thread holds four neighbouring
 // columns and walks the state's rows, so a row is read and written as 16-byte
-// accesses and y needs no sum across the lanes of a row.
+// accesses and y needs no sum across the lanes of a row.  Bound by HBM, the
+// fp32 state read and written once: 256 sequences of 32 heads, 128 x 64, 539 MB
+// in 97 us, 5.6 TB/s.  Two sequences of 24 heads take 4 us, a launch's time.
 constexpr int kStepThreads = 256;
 
 struct StepArgs {
@@ -327,8 +336,7 @@ int check_vec_rows(const mamba2_rows& r, const mamba2_seqs& q, long long width, 
   if (st != MAMBA2_SCAN_OK || q.length == 0) return st;
   const long long n = 8;
   if (!aligned_to(r.data, 16)) return MAMBA2_SCAN_EALIGN;
-  // a step's 64 rows are addressed with 31-bit offsets
-  (void)elem;
+  // a step's 64 rows of either type are addressed with 31-bit offsets
   if (q.length > 1 && r.row_stride > (1LL << 29) / (kTok + 1)) return MAMBA2_SCAN_EUNSUPPORTED;
   if ((q.length > 1 && r.row_stride % n != 0) || (q.offsets == nullptr && q.batch > 1 && r.batch_stride % n != 0))
     return MAMBA2_SCAN_EALIGN;

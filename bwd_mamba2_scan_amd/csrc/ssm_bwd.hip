@@ -42,6 +42,8 @@ struct BwdArgs {
   int run;                 // heads per run
 };
 
+// The walk is bound by HBM: it writes the kept states, 537 MB, and reads 187 MB in
+// 125 us, 5.8 TB/s.  Its summaries take 58 us.
 struct Walks {  // forward, reverse: side by side in one launch
   Walk w[2];
 };
@@ -185,6 +187,12 @@ __device__ __forceinline__ void put_quad(Rsrc rs, int row_off, int c, int cols, 
   Quad<T>::store(rs, c < cols ? static_cast<unsigned>((row_off + c) * static_cast<int>(sizeof(T))) : kOutside, v);
 }
 
+// At 4 x 4096 tokens, 32 heads of 64 columns, 128 states, bf16: 287 us for 681 MB
+// read (the kept states 537 MB, in fp32) and 102 MB written.  The products would
+// take 73 us and the bytes 154 us; LDS is busy 43 % of the time, the matrix
+// cores 15 %, and half of the waves' time is waiting: for a head's states, which
+// are loaded one head ahead (the registers hold no more), and at the two barriers
+// of a head.  The staging alone, without the products, takes 188 us.
 // Eight waves: the first four own 16 rows each of d_x and d_B (rows s), the
 // others 16 rows each of d_C (rows t), so that they work on the gradient
 // behind the step and on the starting state at the same time.  Wave w of the
@@ -587,7 +595,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
     put_quad<T>(rs, mine * static_cast<int>(out.row_stride), n * 16 + 4 * g, a.states, acc[n]);
 }
 
-// What is left to add up, in a fixed order: the first blocks take a step's
+// 11 us at the size above (33 MB).  What is left to add up, in a fixed order: the first blocks take a step's
 // rows of d_B and d_C each (over the runs of heads, where there are several),
 // the last ones a head's d_A, d_D and d_dt_bias (over the steps).
 template <class T>

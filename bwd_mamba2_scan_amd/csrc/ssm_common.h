@@ -1,8 +1,8 @@
 // Shared by the selective scan's kernels: matrix fragments of both element
-// types, LDS tiles, the per-chunk decay arrays, and the call's arguments.
+// types, LDS tiles, the decays of a step, and the call's arguments.
 //
-// The scan is computed in chunks.  With l_t = d_t A log2(e) and c_t the sum of
-// l over the chunk up to t, and S the state before the chunk,
+// The scan is computed in steps of 64 tokens.  With l_t = d_t A log2(e) and c_t the sum of
+// l over the step up to t, and S the state before the step,
 //   y_t   = 2^c_t S^T C_t + sum_{s <= t} (C_t . B_s) 2^(c_t - c_s) d_s x_s
 //   S_end = 2^c_end S + sum_s 2^(c_end - c_s) d_s B_s x_s^T
 // so everything but the elementwise decays is a matrix product.
@@ -674,6 +674,7 @@ __device__ __forceinline__ void walk(const SsmArgs& a, const Walk& w, WalkLds<T,
   }
 }
 
+// 8 us for 43 segments of 24 heads of 64 x 64, the chain's length (18 MB).
 // Carry: turns the segments' own contributions into the state each segment
 // starts from.  One thread per four elements of a sequence's head.
 __device__ __forceinline__ void carry(const SsmArgs& a, const Walk& w, int seq) {

@@ -9,8 +9,8 @@ argument of an exponential (up to 128 before the result is zero, in steps of u)
 and 64 for everything of fixed length (softplus, exp, scalings).  bf16 results
 add half a step of the result; and where the kernels round an operand of a
 product to bf16 (scores, the state as an operand) that is ub per term, twice
-for the state's way through a score.  The states and sums kept in two bf16
-terms are within 2^-16.  A term below fp32's smallest normal number, 2^-126, may
+for the state's way through a score.  An operand in two bf16 parts is within
+2^-16, one in three is whole.  A term below fp32's smallest normal number, 2^-126, may
 become zero: up to 2^16 such terms in a sum, each times a factor of the inputs'
 size (below 2^10), are within 2^-100, which fp32's arithmetic cannot tell from
 zero beside anything larger.
