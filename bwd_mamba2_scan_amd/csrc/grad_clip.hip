@@ -202,15 +202,18 @@ struct Span {
 
 // Does any gradient or output overlap another?  The second pass writes while
 // the first one's other tensors are still to be scaled, so each must be apart.
-int check_apart(const mamba2_grad* g, int count) {
-  const size_t most = 2 * static_cast<size_t>(count);
+int check_apart(const mamba2_grad* g, int count, const float* norm, const void* workspace, size_t workspace_bytes) {
+  const size_t most = 2 * static_cast<size_t>(count) + 2;
   Span few[256];
   Span* spans = few;
   if (most > 256) {
     spans = static_cast<Span*>(malloc(most * sizeof(Span)));
     if (spans == nullptr) return MAMBA2_SCAN_EHIP;
   }
-  size_t n = 0;
+  const uintptr_t pn = reinterpret_cast<uintptr_t>(norm), pw = reinterpret_cast<uintptr_t>(workspace);
+  spans[0] = {pn, pn + sizeof(float)};
+  spans[1] = {pw, pw + workspace_bytes};
+  size_t n = 2;
   for (int i = 0; i < count; ++i) {
     if (g[i].numel == 0) continue;
     const size_t bytes = static_cast<size_t>(g[i].numel) * type_size(g[i].type);
@@ -293,7 +296,7 @@ int mamba2_clip_grads(const mamba2_grad* grads, int count, float max_norm, float
   if (!(max_norm >= 0.0f)) return MAMBA2_SCAN_EBADDIM;
   int st = check_call(grads, count, true, norm, workspace, workspace_bytes, &sz);
   if (st != MAMBA2_SCAN_OK) return st;
-  if ((st = check_apart(grads, count)) != MAMBA2_SCAN_OK) return st;
+  if ((st = check_apart(grads, count, norm, workspace, workspace_bytes)) != MAMBA2_SCAN_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if ((st = run_squares(grads, count, sz, workspace, s)) != MAMBA2_SCAN_OK) return st;
   const double* partial = static_cast<const double*>(workspace);

@@ -229,6 +229,13 @@ def _apart(outs, ins):
                 raise ValueError(f"{n} overlaps {m}")
 
 
+def _other(new_state, state):
+    """new_state where it is not the state's own memory, which moves on in place."""
+    if new_state is None or (new_state.data_ptr() == state.data_ptr() and new_state.shape == state.shape):
+        return None
+    return new_state
+
+
 def _interleaved(t, o):
     def window(v):  # row strides in bytes, outermost first, and the bytes of a row's window
         sizes, strides = list(v.shape), list(v.stride())
@@ -367,7 +374,8 @@ def conv_step(x, weight, state, bias=None, *, silu=True, new_state=None, y=None,
         raise TypeError("state must be a torch.Tensor")
     b = _dense(bias, "bias", (channels,), torch.float32, dev)
     if y is not None or new_state is not None:
-        _apart((("y", y), ("new_state", None if new_state is state else new_state)), (("x", x), ("state", state)))
+        _apart((("y", y), ("new_state", _other(new_state, state))),
+               (("x", x), ("weight", weight), ("bias", bias), ("state", state)))
     s1 = s0 if new_state is None else _dense(new_state, "new_state", tail, x.dtype, dev)
     with _On(dev, stream) as s:
         y, ry = _new_rows(y, "y", (batch,), (channels,), x, dev)
@@ -481,7 +489,8 @@ def ssm_step(x, dt, A, B, C, state, *, D=None, dt_bias=None, softplus=True, new_
     if s0 is None:
         raise TypeError("state must be a torch.Tensor")
     if y is not None or new_state is not None:
-        _apart((("y", y), ("new_state", None if new_state is state else new_state)), (("x", x), ("state", state)))
+        _apart((("y", y), ("new_state", _other(new_state, state))),
+               (("x", x), ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("dt_bias", dt_bias), ("state", state)))
     s1 = s0 if new_state is None else _dense(new_state, "new_state", shape, torch.float32, dev)
     with _On(dev, stream) as s:
         y, py = _new_rows(y, "y", (batch,), (d.heads, d.width), x, dev)

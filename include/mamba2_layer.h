@@ -129,6 +129,9 @@ int mamba2_conv_step(int type, int batch, int channels, int taps, int silu,
  *   8 .. 128.  x, B, C, y and the states are 16-byte aligned, with row and
  *   batch strides that are multiples of 8 elements; dt has any stride.  Row
  *   strides are at most 2^29 / 65 elements.
+ *   A value of x, B, C, dt or d_y that is not finite may reach every token of
+ * its own sequence from the start of its step of 64 tokens on (gradients: up
+ * to the end of it and before), but no other sequence.
  *   A <= 0 is meant; growing states (A > 0) are computed as long as the decay
  *   over 128 tokens stays finite.
  */
@@ -208,8 +211,8 @@ int mamba2_grad_norm(const mamba2_grad* grads, int count, float* norm,
  * *norm as above, and out = grad * min(1, max_norm / (norm + 1e-6)) for every
  * tensor.  max_norm >= 0 (infinity clips nothing).  A NaN among the gradients
  * makes every output NaN; an infinite one makes the factor 0.  The tensors
- * may not overlap one another; out overlaps grad only by being it
- * (MAMBA2_SCAN_EOVERLAP otherwise).
+ * may not overlap one another, norm or the workspace; out overlaps grad only
+ * by being it (MAMBA2_SCAN_EOVERLAP otherwise).
  */
 int mamba2_clip_grads(const mamba2_grad* grads, int count, float max_norm,
                       float* norm, void* workspace, size_t workspace_bytes,

@@ -1,6 +1,8 @@
 """The causal convolution's kernels against the float64 oracle, on an MI355X."""
 from __future__ import annotations
 
+import math
+
 import pytest
 import torch
 
@@ -157,6 +159,25 @@ def test_pieces_and_tokens_continue_a_sequence(typ, channels, taps):
     check(p, y, state, None, range(batch), True)
 
 
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+def test_values_that_are_not_finite_reach_their_window_alone(typ):
+    p = to(_inputs(8, (60,), 2, 24, 4, typ, True, True), DEV)
+    off = torch.tensor([2, 31, 58], dtype=torch.int32, device=DEV)
+    run = lambda x: (m2.conv_fwd(x, p["weight"], p["bias"], initial_state=p["state"], offsets=off, y=torch.zeros_like(x))[0],
+                     m2.conv_bwd(x, p["weight"], p["d_y"], p["bias"], initial_state=p["state"], offsets=off,
+                                 out=dict(d_x=torch.zeros_like(x)))["d_x"])
+    y0, g0 = run(p["x"])
+    x = p["x"].clone()
+    x[29] = math.nan                 # two tokens before the first sequence's end
+    x[:2] = x[58:] = math.inf        # rows of no sequence
+    y, g = run(x)
+    rows = torch.arange(60, device=DEV)
+    hit = (rows >= 29) & (rows < 31)                        # y of the token and the ones behind
+    assert torch.equal(y[~hit], y0[~hit]) and bool(torch.isnan(y[hit]).all())
+    hit = (rows >= 26) & (rows < 31)                        # d_x of the inputs of those pre-activations
+    assert torch.equal(g[~hit], g0[~hit]) and bool(torch.isnan(g[hit]).all())
+
+
 def test_parts_of_the_backward():
     p = to(_inputs(5, (1, 30), 1, 16, 4, "f32", True, True), DEV)
     whole = m2.conv_bwd(p["x"], p["weight"], p["d_y"], p["bias"], initial_state=p["state"])
@@ -173,6 +194,13 @@ def test_refusals_of_the_binding():
         m2.conv_fwd(p["x"], p["weight"], y=p["x"])
     with pytest.raises(ValueError, match="overlaps"):
         m2.conv_step(p["x"][:, 0], p["weight"], p["state"], y=p["state"][:, 0])
+    flat = p["weight"].view(-1).view(torch.bfloat16)[:32].view(2, 16)
+    with pytest.raises(ValueError, match="y overlaps weight"):
+        m2.conv_step(p["x"][:, 0].contiguous(), p["weight"], p["state"], y=flat)
+    one, two = p["state"].clone(), p["state"].clone()       # the state's own memory under another name
+    m2.conv_step(p["x"][:, 0], p["weight"], one)
+    m2.conv_step(p["x"][:, 0], p["weight"], two, new_state=two.view(2, 3, 16))
+    assert torch.equal(one, two)
     with pytest.raises(TypeError):
         m2.conv_fwd(p["x"], p["weight"].bfloat16())
     with pytest.raises(TypeError):

@@ -175,7 +175,7 @@ def test_grad_calls_refuse(L):
     need = L.mamba2_grad_workspace_bytes(t, 2)
     assert need > 0
 
-    def clip(t, n=2, max_norm=1.0, norm=P, ws=P, nb=need):
+    def clip(t, n=2, max_norm=1.0, norm=P + (1 << 20), ws=P + (1 << 21), nb=need):
         return L.mamba2_clip_grads(t, n, max_norm, norm, ws, nb, None)
 
     assert clip(t, n=0) == m2.EBADDIM and clip(None) == m2.ENULL
@@ -193,6 +193,8 @@ def test_grad_calls_refuse(L):
     assert clip(_table((P, P + 8, 4, 0)), n=1) == EOVERLAP
     many = _table(*((P + 64 * i, P + 64 * i, 16, 0) for i in range(300)), (P + 5, P + 5, 1, 1))
     assert clip(many, n=301) in (m2.EALIGN, EOVERLAP)
+    # the norm or the workspace in a gradient
+    assert clip(t, norm=P + 396) == EOVERLAP and clip(t, ws=P + 384) == EOVERLAP and clip(t, norm=P + 4096) == EOVERLAP
     assert L.mamba2_grad_norm(t, 2, None, P, need, None) == m2.ENULL
     assert L.mamba2_grad_workspace_bytes(_table((P, P, 4, 9)), 1) == 0
 

@@ -302,6 +302,38 @@ def test_extreme_decays(what):
     check_grads(p, g, range(1), exact, bound)
 
 
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+def test_values_that_are_not_finite_stay_in_their_sequence(typ):
+    """NaN and infinities in one sequence: the others, and the steps before, come out bit for bit as without them."""
+    H, P, G, N = 4, 24, 2, 40
+    offsets = [3, 70, 400, 431]
+    p = scan_inputs(9, (440,), 3, H, P, G, N, typ, typ)
+    off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+
+    def run(q):
+        d = to(q, DEV)
+        y, final = m2.ssm_fwd(*_args(d), initial_state=d["state"], want_final_state=True, offsets=off, **_kw(d, True))
+        g = m2.ssm_bwd(*_args(d), d["d_y"], initial_state=d["state"], d_final_state=d["d_final"], offsets=off, **_kw(d, True))
+        return y, final, g
+
+    y0, f0, g0 = run(p)
+    for name, bad in (("x", math.inf), ("B", math.nan), ("C", -math.inf), ("d_y", math.nan), ("dt", math.nan)):
+        q = {k: v.clone() for k, v in p.items()}
+        q[name][70 + 200] = bad
+        q[name][:3] = q[name][431:] = math.nan      # rows of no sequence
+        y, f, g = run(q)
+        whole = [slice(3, 70), slice(400, 431)]
+        for s in whole + [slice(70, 70 + 192)]:
+            assert torch.equal(y[s], y0[s]), (name, s)
+        for s in whole:
+            for k in ("d_x", "d_dt", "d_B", "d_C"):
+                assert torch.equal(g[k][s], g0[k][s]), (name, k, s)
+        for row in (0, 2):
+            assert torch.equal(f[row], f0[row]) and torch.equal(g["d_initial_state"][row], g0["d_initial_state"][row])
+        if name not in ("d_y", "C"):
+            assert not bool(torch.isfinite(f[1]).all()), name
+
+
 def test_runs_are_bitwise_the_same():
     p = to(scan_inputs(7, (2, 700), 2, 4, 64, 1, 64, "bf16", "bf16"), DEV)
     kw = dict(initial_state=p["state"], **_kw(p, True))
