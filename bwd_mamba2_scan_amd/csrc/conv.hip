@@ -646,6 +646,11 @@ int mamba2_conv_step(int type, int batch, int channels, int taps, int silu, mamb
   if ((st = check_rows(y, q, channels, e)) != MAMBA2_SCAN_OK) return st;
   if (!aligned_to(weight, 4) || !aligned_to(bias, 4) || !aligned_to(state, e) || !aligned_to(new_state, e))
     return MAMBA2_SCAN_EALIGN;
+  const long long row = static_cast<long long>(channels) * static_cast<long long>(e), tail = batch * (taps - 1) * row;
+  const Region mem[] = {token_region(y, batch, channels, e), region(new_state, tail), token_region(x, batch, channels, e),
+                        region(weight, 4LL * channels * taps), region(bias, 4LL * channels),
+                        region(state != new_state ? state : nullptr, tail)};
+  if (!apart(mem, 2, 6)) return MAMBA2_SCAN_EOVERLAP;
   const bool vec = channels % (16 / static_cast<int>(e)) == 0 && rows_vec(x, e) && rows_vec(y, e) &&
                    state_vec(state) && state_vec(new_state);
   ConvArgs a = {};

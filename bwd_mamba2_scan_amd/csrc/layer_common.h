@@ -168,6 +168,39 @@ inline bool rows_vec(const mamba2_rows& r, size_t elem) {
   return aligned_to(r.data, 16) && r.row_stride % n == 0 && r.batch_stride % n == 0;
 }
 
+// The memory of a tensor: rows of `width` bytes, `stride` bytes apart (0: one row).
+struct Region {
+  uintptr_t lo, hi;
+  long long stride, width;
+};
+inline Region region(const void* p, long long bytes) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return p == nullptr ? Region{0, 0, 0, 0} : Region{lo, lo + bytes, 0, bytes};
+}
+inline Region token_region(const mamba2_rows& r, int batch, long long width, size_t elem) {
+  const long long bytes = width * static_cast<long long>(elem);
+  if (batch == 1) return region(r.data, bytes);
+  const long long stride = r.batch_stride * static_cast<long long>(elem);
+  Region v = region(r.data, (batch - 1) * stride + bytes);
+  v.stride = stride;
+  v.width = bytes;
+  return v;
+}
+// Slices of one wide row-major tensor interleave without overlapping.
+inline bool overlap(const Region& a, const Region& b) {
+  if (a.hi <= b.lo || b.hi <= a.lo) return false;
+  if (a.stride == 0 || a.stride != b.stride) return true;
+  const long long d = static_cast<long long>(b.lo - a.lo) % a.stride, gap = d < 0 ? d + a.stride : d;
+  return a.width > gap || gap + b.width > a.stride;
+}
+// Of the first n regions, the outputs, none may overlap another one or an input.
+inline bool apart(const Region* v, int n, int count) {
+  for (int i = 0; i < n; ++i)
+    for (int k = i + 1; k < count; ++k)
+      if (overlap(v[i], v[k])) return false;
+  return true;
+}
+
 inline int launch_status() { return hipGetLastError() == hipSuccess ? MAMBA2_SCAN_OK : MAMBA2_SCAN_EHIP; }
 
 }  // namespace layer

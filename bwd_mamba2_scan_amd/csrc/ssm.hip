@@ -483,6 +483,12 @@ int mamba2_ssm_step(int batch, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows dt,
   if (!aligned_to(A, 4) || !aligned_to(D, 4) || !aligned_to(dt_bias, 4) || !aligned_to(state, 16) ||
       !aligned_to(new_state, 16))
     return MAMBA2_SCAN_EALIGN;
+  const long long all = 4LL * batch * xw * d.states, vec = 4LL * d.heads;
+  const Region mem[] = {token_region(y, batch, xw, e), region(new_state, all), token_region(x, batch, xw, e),
+                        token_region(dt, batch, d.heads, type_size(d.dt_type)), token_region(B, batch, bw, e),
+                        token_region(C, batch, bw, e), region(A, vec), region(D, vec), region(dt_bias, vec),
+                        region(state != new_state ? state : nullptr, all)};
+  if (!apart(mem, 2, 10)) return MAMBA2_SCAN_EOVERLAP;
   StepArgs sa = {};
   SsmArgs& a = sa.a;
   a.x = x;

@@ -22,6 +22,7 @@ import math
 import struct
 
 _F32, _BF16 = 0, 1
+_EOVERLAP = -8
 
 _c_int, _c_size, _c_vp, _c_ll = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_longlong
 
@@ -229,13 +230,6 @@ def _apart(outs, ins):
                 raise ValueError(f"{n} overlaps {m}")
 
 
-def _other(new_state, state):
-    """new_state where it is not the state's own memory, which moves on in place."""
-    if new_state is None or (new_state.data_ptr() == state.data_ptr() and new_state.shape == state.shape):
-        return None
-    return new_state
-
-
 def _interleaved(t, o):
     def window(v):  # row strides in bytes, outermost first, and the bytes of a row's window
         sizes, strides = list(v.shape), list(v.stride())
@@ -268,13 +262,13 @@ def _new_rows(t, name, lead, inner, like, dev):
     return t, Rows(t.data_ptr(), width * lead[-1], width)
 
 
-def _new_dense(t, name, shape, dtype, dev, wanted=True):
-    """(a contiguous output or None, its address): the given tensor, or a new one where it is wanted."""
+def _new_dense(t, name, shape, like, dev, wanted=True):
+    """(a contiguous output of a tensor's type or None, its address): the given tensor, or a new one where it is wanted."""
     if t is not None:
-        return t, _dense(t, name, shape, dtype, dev)
+        return t, _dense(t, name, shape, like.dtype, dev)
     if not wanted:
         return None, None
-    t = torch.empty(shape, dtype=dtype, device=dev)
+    t = like.new_empty(shape)
     return t, t.data_ptr()
 
 
@@ -308,8 +302,7 @@ def conv_fwd(x, weight, bias=None, *, silu=True, initial_state=None, offsets=Non
            (("x", x), ("weight", weight), ("bias", bias), ("initial_state", initial_state)))
     with _On(dev, stream) as s:
         y, ry = _new_rows(y, "y", lead, (channels,), x, dev)
-        final_state, s1 = _new_dense(final_state, "final_state", (batch, taps - 1, channels), x.dtype, dev,
-                                     want_final_state)
+        final_state, s1 = _new_dense(final_state, "final_state", (batch, taps - 1, channels), x, dev, want_final_state)
         st = lib.mamba2_conv_fwd(typ, seqs, channels, taps, bool(silu), rx, w, b, s0, ry, s1, s)
     _raise(st, "mamba2_conv_fwd")
     return y, final_state
@@ -336,24 +329,24 @@ def conv_bwd(x, weight, d_y, bias=None, *, silu=True, initial_state=None, d_fina
     with _On(dev, stream) as s:
         get = res.get
         res["d_x"], rx1 = _new_rows(get("d_x"), "d_x", lead, (channels,), x, dev)
-        res["d_weight"], w1 = _new_dense(get("d_weight"), "d_weight", (channels, taps), torch.float32, dev)
-        res["d_bias"], b1 = (_new_dense(get("d_bias"), "d_bias", (channels,), torch.float32, dev)
+        res["d_weight"], w1 = _new_dense(get("d_weight"), "d_weight", (channels, taps), weight, dev)
+        res["d_bias"], b1 = (_new_dense(get("d_bias"), "d_bias", (channels,), weight, dev)
                              if bias is not None else (None, None))
-        res["d_initial_state"], s1 = (_new_dense(get("d_initial_state"), "d_initial_state", tail, x.dtype, dev)
+        res["d_initial_state"], s1 = (_new_dense(get("d_initial_state"), "d_initial_state", tail, x, dev)
                                       if initial_state is not None else (None, None))
-        workspace, nbytes = _workspace(workspace, lib.mamba2_conv_bwd_workspace_bytes(seqs, channels, taps), dev)
+        workspace, nbytes = _workspace(workspace, lib.mamba2_conv_bwd_workspace_bytes(seqs, channels, taps), x, dev)
         st = lib.mamba2_conv_bwd(typ, seqs, channels, taps, bool(silu), rx, w, b, s0, rg, sf, rx1, w1, b1, s1,
                                  _ptr(workspace), nbytes, s)
     _raise(st, "mamba2_conv_bwd")
     return res
 
 
-def _workspace(workspace, need, dev):
-    """The given workspace or a new one; (tensor or None, bytes)."""
+def _workspace(workspace, need, like, dev):
+    """The given workspace or a new one of a tensor's type; (tensor or None, bytes)."""
     if workspace is None:
         if need == 0:
             return None, 0
-        workspace = torch.empty(-(-need // 4), dtype=torch.float32, device=dev)
+        return like.new_empty(-(-need // like.element_size())), need
     _gpu(workspace, "workspace", dev)
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
@@ -373,13 +366,12 @@ def conv_step(x, weight, state, bias=None, *, silu=True, new_state=None, y=None,
     if s0 is None:
         raise TypeError("state must be a torch.Tensor")
     b = _dense(bias, "bias", (channels,), torch.float32, dev)
-    if y is not None or new_state is not None:
-        _apart((("y", y), ("new_state", _other(new_state, state))),
-               (("x", x), ("weight", weight), ("bias", bias), ("state", state)))
     s1 = s0 if new_state is None else _dense(new_state, "new_state", tail, x.dtype, dev)
     with _On(dev, stream) as s:
         y, ry = _new_rows(y, "y", (batch,), (channels,), x, dev)
         st = lib.mamba2_conv_step(typ, batch, channels, taps, bool(silu), rx, w, b, s0, _token(ry), s1, s)
+    if st == _EOVERLAP:
+        raise ValueError("y or new_state overlaps another tensor of the call")
     _raise(st, "mamba2_conv_step")
     return y
 
@@ -428,8 +420,8 @@ def ssm_fwd(x, dt, A, B, C, *, D=None, dt_bias=None, softplus=True, initial_stat
             ("initial_state", initial_state)))
     with _On(dev, stream) as s:
         y, py = _new_rows(y, "y", lead, (d.heads, d.width), x, dev)
-        final_state, s1 = _new_dense(final_state, "final_state", shape, torch.float32, dev, want_final_state)
-        workspace, nbytes = _workspace(workspace, lib.mamba2_ssm_fwd_workspace_bytes(seqs, d), dev)
+        final_state, s1 = _new_dense(final_state, "final_state", shape, A, dev, want_final_state)
+        workspace, nbytes = _workspace(workspace, lib.mamba2_ssm_fwd_workspace_bytes(seqs, d), A, dev)
         st = lib.mamba2_ssm_fwd(seqs, d, px, pdt, pA, pB, pC, pD, pbias, s0, py, s1, _ptr(workspace), nbytes, s)
     _raise(st, "mamba2_ssm_fwd")
     return y, final_state
@@ -463,8 +455,8 @@ def ssm_bwd(x, dt, A, B, C, d_y, *, D=None, dt_bias=None, softplus=True, initial
             if given is None:
                 res[name] = ptr[name] = None
             else:
-                res[name], ptr[name] = _new_dense(res.get(name), name, size, f32, dev)
-        workspace, nbytes = _workspace(workspace, lib.mamba2_ssm_bwd_workspace_bytes(seqs, d), dev)
+                res[name], ptr[name] = _new_dense(res.get(name), name, size, A, dev)
+        workspace, nbytes = _workspace(workspace, lib.mamba2_ssm_bwd_workspace_bytes(seqs, d), A, dev)
         st = lib.mamba2_ssm_bwd(seqs, d, px, pdt, pA, pB, pC, pD, pbias, s0, pg, sf, ptr["d_x"], ptr["d_dt"],
                                 ptr["d_A"], ptr["d_B"], ptr["d_C"], ptr["d_D"], ptr["d_dt_bias"],
                                 ptr["d_initial_state"], _ptr(workspace), nbytes, s)
@@ -488,22 +480,21 @@ def ssm_step(x, dt, A, B, C, state, *, D=None, dt_bias=None, softplus=True, new_
     s0 = _dense(state, "state", shape, torch.float32, dev)
     if s0 is None:
         raise TypeError("state must be a torch.Tensor")
-    if y is not None or new_state is not None:
-        _apart((("y", y), ("new_state", _other(new_state, state))),
-               (("x", x), ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("dt_bias", dt_bias), ("state", state)))
     s1 = s0 if new_state is None else _dense(new_state, "new_state", shape, torch.float32, dev)
     with _On(dev, stream) as s:
         y, py = _new_rows(y, "y", (batch,), (d.heads, d.width), x, dev)
         for r in (px, pdt, pB, pC, py):
             _token(r)
         st = lib.mamba2_ssm_step(batch, d, px, pdt, pA, pB, pC, pD, pbias, s0, py, s1, s)
+    if st == _EOVERLAP:
+        raise ValueError("y or new_state overlaps another tensor of the call")
     _raise(st, "mamba2_ssm_step")
     return y
 
 
 # ----------------------------------------------------------------- gradients
 def _grad_table(grads, out):
-    """(the mamba2_grad table as bytes, its length, the device)"""
+    """(the mamba2_grad table as bytes, its length, the first gradient)"""
     if torch is None:
         _load()
     grads = list(grads)
@@ -533,7 +524,7 @@ def _grad_table(grads, out):
         if o.dtype is not g.dtype or o.shape != g.shape or not o.is_contiguous():
             raise ValueError(f"out[{i}] must be contiguous, of the gradient's type and shape")
         fields += (p, o.data_ptr(), g.numel(), typ)
-    return struct.pack("=" + "QQqq" * len(grads), *fields), len(grads), grads[0].device
+    return struct.pack("=" + "QQqq" * len(grads), *fields), len(grads), grads[0]
 
 
 def grad_norm(grads, *, norm=None, workspace=None, stream=None):
@@ -553,14 +544,16 @@ def clip_grads(grads, max_norm, *, out=None, norm=None, workspace=None, stream=N
 
 
 def _grads(grads, max_norm, out, norm, workspace, stream):
-    table, count, dev = _grad_table(grads, out)
+    table, count, first = _grad_table(grads, out)
+    dev = first.device
     with _On(dev, stream) as s:
         if norm is None:
-            norm = torch.empty((), dtype=torch.float32, device=dev)
-        _gpu(norm, "norm", dev)
-        if norm.dtype != torch.float32 or norm.numel() != 1:
-            raise ValueError("norm must be one float32")
-        workspace, nbytes = _workspace(workspace, lib.mamba2_grad_workspace_bytes(table, count), dev)
+            norm = first.new_empty((), dtype=torch.float32)
+        else:
+            _gpu(norm, "norm", dev)
+            if norm.dtype != torch.float32 or norm.numel() != 1:
+                raise ValueError("norm must be one float32")
+        workspace, nbytes = _workspace(workspace, lib.mamba2_grad_workspace_bytes(table, count), first, dev)
         if max_norm is None:
             st = lib.mamba2_grad_norm(table, count, norm.data_ptr(), _ptr(workspace), nbytes, s)
         else:

@@ -106,6 +106,7 @@ int mamba2_conv_bwd(int type, mamba2_seqs seqs, int channels, int taps, int silu
  * One token of each of `batch` sequences: x and y [batch][channels] (their
  * batch_stride; row_stride is not used), state [batch][taps - 1][channels].
  * new_state gets the state moved on by the token; it may be `state` itself.
+ * Any other overlap is refused (MAMBA2_SCAN_EOVERLAP).
  */
 int mamba2_conv_step(int type, int batch, int channels, int taps, int silu,
                      mamba2_rows x, const float* weight, const float* bias,
@@ -179,7 +180,7 @@ int mamba2_ssm_bwd(mamba2_seqs seqs, mamba2_ssm_dims dims, mamba2_rows x,
 /*
  * One token of each of `batch` sequences: the tensors of the scan without a
  * token axis (batch_stride; row_stride is not used).  new_state may be
- * `state` itself.
+ * `state` itself; any other overlap is refused (MAMBA2_SCAN_EOVERLAP).
  */
 int mamba2_ssm_step(int batch, mamba2_ssm_dims dims, mamba2_rows x,
                     mamba2_rows dt, const float* A, mamba2_rows B,

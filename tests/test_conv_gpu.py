@@ -195,7 +195,7 @@ def test_refusals_of_the_binding():
     with pytest.raises(ValueError, match="overlaps"):
         m2.conv_step(p["x"][:, 0], p["weight"], p["state"], y=p["state"][:, 0])
     flat = p["weight"].view(-1).view(torch.bfloat16)[:32].view(2, 16)
-    with pytest.raises(ValueError, match="y overlaps weight"):
+    with pytest.raises(ValueError, match="overlaps"):
         m2.conv_step(p["x"][:, 0].contiguous(), p["weight"], p["state"], y=flat)
     one, two = p["state"].clone(), p["state"].clone()       # the state's own memory under another name
     m2.conv_step(p["x"][:, 0], p["weight"], one)

@@ -94,6 +94,18 @@ def test_conv_step_refuses(L):
     assert call(state=None) == m2.ENULL and call(new=None) == m2.ENULL and call(x=Rows(None, 16, 0)) == m2.ENULL
     assert call(batch=0) == m2.EBADDIM and call(batch=70000) == m2.EBADDIM and call(x=Rows(P, 15, 0)) == m2.EBADDIM
     assert call(typ=7) == m2.EUNSUPPORTED and call(state=P + 2) == m2.EALIGN
+    far = [P + (i << 20) for i in range(8)]
+
+    def at(x=Rows(far[0], 16, 0), w=far[1], bias=far[2], state=far[3], y=Rows(far[4], 16, 0), new=far[5], batch=2):
+        return L.mamba2_conv_step(0, batch, 16, 3, 1, x, w, bias, state, y, new, None)
+
+    # x, y [2][16], weight [16][3], bias [16], states [2][2][16], all fp32
+    for bad in (dict(y=Rows(far[0], 16, 0)), dict(y=Rows(far[0] + 124, 16, 0)), dict(y=Rows(far[1] + 188, 16, 0)),
+                dict(y=Rows(far[2] + 60, 16, 0)), dict(y=Rows(far[3] + 252, 16, 0)), dict(y=Rows(far[5] + 252, 16, 0)),
+                dict(new=far[3] + 4), dict(new=far[3] - 252), dict(new=far[0] + 124), dict(new=far[1]), dict(new=far[2]),
+                dict(state=far[0], new=far[0]), dict(x=Rows(far[0], 64, 0), y=Rows(far[0] + 60, 64, 0)),
+                dict(x=Rows(far[0], 64, 0), y=Rows(far[0] - 60, 64, 0)), dict(x=Rows(far[0], 64, 0), y=Rows(far[0] + 200, 64, 0))):
+        assert at(**bad) == EOVERLAP, bad
 
 
 # -------------------------------------------------------------------- scan
@@ -163,6 +175,18 @@ def test_ssm_step_refuses(L):
     assert call(x=Rows(P, 63, 0)) == m2.EBADDIM and call(batch=0) == m2.EBADDIM
     assert call(state=P + 8) == m2.EALIGN and call(x=Rows(P + 1, 64, 0)) == m2.EALIGN
     assert call(dims=_dims(width=9)) == m2.EUNSUPPORTED
+    far = [P + (i << 20) for i in range(10)]
+
+    def at(i=None, p=0):
+        """The call with tensor i at p.  bf16: x, y [2][4][16], dt [2][4], B, C [2][2][24]; fp32: A, D, dt_bias [4], states [2][4][24][16]"""
+        q = [p if k == i else v for k, v in enumerate(far)]
+        return L.mamba2_ssm_step(2, _dims(), Rows(q[0], 64, 0), Rows(q[1], 4, 0), q[2], Rows(q[3], 48, 0),
+                                 Rows(q[4], 48, 0), q[5], q[6], q[7], Rows(q[8], 64, 0), q[9], None)
+
+    for i, n in ((0, 256), (1, 16), (2, 16), (3, 192), (4, 192), (5, 16), (6, 16), (7, 12288)):
+        assert at(8, far[i]) == EOVERLAP and at(8, far[i] + (n - 1) // 16 * 16) == EOVERLAP, i
+        assert at(9, far[i] + (16 if i == 7 else 0)) == EOVERLAP, i
+    assert at(8, far[9] + 12272) == EOVERLAP
 
 
 # --------------------------------------------------------------- gradients
