@@ -506,20 +506,20 @@ def _grad_table(grads, out):
     _gpu(grads[0], "grads[0]")
     index = grads[0].get_device()
     fields = []
-    for i, g in enumerate(grads):
-        if not isinstance(g, torch.Tensor) or g.get_device() != index:
+    Tensor, types = torch.Tensor, _TYPES
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        if not isinstance(g, Tensor) or g.get_device() != index:
             _gpu(g, f"grads[{i}]", grads[0].device)
-        typ = _TYPES.get(g.dtype)
+        typ = types.get(g.dtype)
         if typ is None:
             _type(g, f"grads[{i}]")
         if not g.is_contiguous():
             raise ValueError(f"grads[{i}] must be contiguous")
         p = g.data_ptr()
-        o = outs[i]
         if o is g:
             fields += (p, p, g.numel(), typ)
             continue
-        if not isinstance(o, torch.Tensor) or o.get_device() != index:
+        if not isinstance(o, Tensor) or o.get_device() != index:
             _gpu(o, f"out[{i}]", grads[0].device)
         if o.dtype is not g.dtype or o.shape != g.shape or not o.is_contiguous():
             raise ValueError(f"out[{i}] must be contiguous, of the gradient's type and shape")

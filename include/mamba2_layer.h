@@ -210,8 +210,8 @@ int mamba2_grad_norm(const mamba2_grad* grads, int count, float* norm,
 
 /*
  * *norm as above, and out = grad * min(1, max_norm / (norm + 1e-6)) for every
- * tensor.  max_norm >= 0 (infinity clips nothing).  A NaN among the gradients
- * makes every output NaN; an infinite one makes the factor 0.  The tensors
+ * tensor.  max_norm >= 0 (infinity clips nothing but a NaN).  A NaN among the
+ * gradients makes every output NaN; an infinite one makes the factor 0.  The tensors
  * may not overlap one another, norm or the workspace; out overlaps grad only
  * by being it (MAMBA2_SCAN_EOVERLAP otherwise).
  */

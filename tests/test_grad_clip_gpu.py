@@ -21,7 +21,7 @@ def _grads(seed, sizes, scale=1.0):
 
 
 SIZES = [[1], [0, 5, 0], [4096] * 3, [1, 2, 3, 4, 5, 7, 8, 9, 15, 17, 8191, 8192, 8193, 100003], [3] * 250, [0, 0],
-         [3_000_000, 11]]
+         [3_000_000, 11], [5] * 16, [6] * 17, [100] * 97]
 
 
 @pytest.mark.parametrize("sizes", SIZES, ids=lambda s: f"{len(s)}x{max(s)}")
@@ -82,6 +82,8 @@ def test_infinities_and_nan():
     d = [torch.tensor([3.0, math.inf], device=DEV)]
     m2.clip_grads(d, math.inf)
     assert float(d[0][0]) == 3.0 and math.isinf(float(d[0][1]))
+    d = [torch.tensor([3.0, math.nan], device=DEV)]
+    assert math.isnan(float(m2.clip_grads(d, math.inf))) and bool(torch.isnan(d[0]).all())
 
 
 def test_refusals_of_the_binding():
