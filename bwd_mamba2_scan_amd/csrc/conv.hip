@@ -7,14 +7,14 @@
 //
 // A few operations per element against two (forward) or three (backward)
 // streamed tensors: bound by HBM, the backward nearly as much by arithmetic.
-// A lane owns 16 bytes of channels and walks a run of tokens with the last
-// W - 1 inputs (and W pre-activation gradients) in registers, so x and d_y are
-// read once but for the W - 1 tokens where runs meet.  The next tokens' loads
-// are in flight while the last ones are computed.
+// A lane owns 16 bytes of channels (8 in the backward with bf16) and walks a
+// run of tokens with the last W - 1 inputs (and W pre-activation gradients) in
+// registers, so x and d_y are read once but for the W - 1 tokens where runs
+// meet.  The next tokens' loads are in flight while the last ones are computed.
 // At 4 x 4096 tokens of 4352 bf16 channels, 4 taps: forward 55 us, 285 MB at
-// 5.2 TB/s, what a large copy reaches; backward 114 us, 428 MB at 3.8 TB/s: its
-// loop is 290 vector instructions a token and wave, 16 of them exponentials and
-// reciprocals, or 88 us of the vector units.
+// 5.2 TB/s, what a large copy reaches; backward 94 us, 428 MB at 4.6 TB/s, the
+// vector units busy nearly as long: some 35 instructions an element, among them
+// an exponential and a reciprocal.
 #include "layer_common.h"
 
 namespace {
@@ -102,6 +102,14 @@ struct Raw<float, 1> {
   __device__ __forceinline__ float get(int) const { return v; }
 };
 template <>
+struct Raw<bf16, 4> {
+  v4bf v;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, int lane_off, int row_off) {
+    v = __builtin_bit_cast(v4bf, __builtin_amdgcn_raw_buffer_load_b64(rs, lane_off, row_off, 0));
+  }
+  __device__ __forceinline__ float get(int i) const { return static_cast<float>(v[i]); }
+};
+template <>
 struct Raw<bf16, 1> {
   unsigned short v;
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, int lane_off, int row_off) {
@@ -128,6 +136,12 @@ __device__ __forceinline__ void put(__amdgpu_buffer_rsrc_t rs, int lane_off, int
     const T t = static_cast<T>(v[0]);
     if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, t), rs, off, 0, 0);
     else __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(t), rs, off, 0, 0);
+  } else if constexpr (V != Vec<T>::n) {
+    v4bf r;
+#pragma unroll
+    for (int i = 0; i < V; ++i) r[i] = static_cast<T>(v[i]);
+    typedef int v2i __attribute__((ext_vector_type(2)));
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2i, r), rs, off, 0, 0);
   } else {
     typename Vec<T>::type r;
 #pragma unroll
@@ -241,7 +255,7 @@ __device__ __forceinline__ void pre_grad(const float (&w)[W][V], const float (&b
 // read.  W - 1 tokens behind the run are loaded and differentiated again, 3 in
 // 32.
 template <class T, int V, int W, bool SILU>
-__global__ __launch_bounds__(kLanes * kBwdWaves, 2) void conv_bwd_kernel(ConvArgs a) {
+__global__ __launch_bounds__(kLanes * kBwdWaves, sizeof(T) == 2 ? 4 : 2) void conv_bwd_kernel(ConvArgs a) {
   __shared__ float lds[kBwdWaves][kLanes * V];
   const int lane = threadIdx.x % kLanes;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
@@ -467,11 +481,16 @@ __global__ __launch_bounds__(kLanes) void conv_step_kernel(ConvArgs a) {
 // --------------------------------------------------------------------- host
 enum Which { kFwd, kBwd, kStep };
 
+// Channels of a backward lane.  The windows, weights and sums of eight take 254
+// registers, two waves on a SIMD; four with 8-byte accesses take 128, four waves:
+// 94 us against 113 (4 x 4096 tokens of 4352 channels).
+constexpr int bwd_vec(int v) { return v > 4 ? 4 : v; }
+
 template <class T, int V, int W, bool SILU>
 void launch(Which which, const ConvArgs& a, dim3 grid, hipStream_t s) {
   switch (which) {
     case kFwd: conv_fwd_kernel<T, V, W, SILU><<<grid, kLanes, 0, s>>>(a); break;
-    case kBwd: conv_bwd_kernel<T, V, W, SILU><<<grid, kLanes * kBwdWaves, 0, s>>>(a); break;
+    case kBwd: conv_bwd_kernel<T, bwd_vec(V), W, SILU><<<grid, kLanes * kBwdWaves, 0, s>>>(a); break;
     case kStep: conv_step_kernel<T, V, W, SILU><<<grid, kLanes, 0, s>>>(a); break;
   }
 }
@@ -518,18 +537,18 @@ long long total_rows(const mamba2_seqs& q) {
 
 // Tokens per run: enough waves to fill the chip first, then longer runs, which
 // re-read fewer meeting tokens.  Measured at 4 x 4096 tokens of 4352 channels:
-// forward runs of 64 tokens 55 us, of 32 60 us; backward runs of 32 115 us, of
-// 64 123 us, of 8 217 us (more partial sums).
+// forward runs of 64 tokens 55 us, of 32 60 us; backward runs of 36 94 us, of 32
+// 96 us; of 8 twice that (more partial sums).
 int run_tokens(const mamba2_seqs& q, int channels, int waves_per_cu, int most) {
   const long long tokens = total_rows(q) * ((channels + 511) / 512);
   const long long r = (tokens / (kCUs * waves_per_cu) + kAhead - 1) / kAhead * kAhead;
   return static_cast<int>(r < kLeastRun ? kLeastRun : r > most ? most : r);
 }
 int fwd_run(const mamba2_seqs& q, int channels) { return run_tokens(q, channels, 8, 64); }
-int bwd_run(const mamba2_seqs& q, int channels) { return run_tokens(q, channels, 16, 32); }
+int bwd_run(const mamba2_seqs& q, int channels) { return run_tokens(q, channels, 16, 64); }
 
-int cblocks_of(int type, bool vec, int channels) {
-  const int per = kLanes * (vec ? (type == MAMBA2_BF16 ? 8 : 4) : 1);
+int cblocks_of(Which which, int type, bool vec, int channels) {
+  const int v = vec ? (type == MAMBA2_BF16 ? 8 : 4) : 1, per = kLanes * (which == kBwd ? bwd_vec(v) : v);
   return (channels + per - 1) / per;
 }
 
@@ -557,7 +576,7 @@ int mamba2_conv_fwd(int type, mamba2_seqs q, int channels, int taps, int silu, m
   a.channels = channels;
   a.run = fwd_run(q, channels);
   a.units = static_cast<int>(unit_count(q, a.run));
-  a.cblocks = cblocks_of(type, vec, channels);
+  a.cblocks = cblocks_of(kFwd, type, vec, channels);
   a.x = x;
   a.y = y;
   a.weight = weight;
@@ -609,7 +628,7 @@ int mamba2_conv_bwd(int type, mamba2_seqs q, int channels, int taps, int silu, m
   a.channels = channels;
   a.run = bwd_run(q, channels);
   a.units = static_cast<int>(unit_count(q, a.run * kBwdWaves));
-  a.cblocks = cblocks_of(type, vec, channels);
+  a.cblocks = cblocks_of(kBwd, type, vec, channels);
   a.x = x;
   a.d_y = d_y;
   a.d_x = d_x;
@@ -655,7 +674,7 @@ int mamba2_conv_step(int type, int batch, int channels, int taps, int silu, mamb
                    state_vec(state) && state_vec(new_state);
   ConvArgs a = {};
   a.channels = channels;
-  a.cblocks = cblocks_of(type, vec, channels);
+  a.cblocks = cblocks_of(kStep, type, vec, channels);
   a.x = x;
   a.y = y;
   a.weight = weight;

@@ -16,6 +16,7 @@ typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 typedef unsigned int v2u __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16;
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr int kCUs = 256;
@@ -41,7 +42,10 @@ __device__ __forceinline__ void load_vec(const T* p, float (&v)[V]) {
     const typename Vec<T>::type r = *reinterpret_cast<const typename Vec<T>::type*>(p);
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = static_cast<float>(r[i]);
-  } else {
+  } else if constexpr (sizeof(T) == 2 && V == 4) {
+    const v4bf r = *reinterpret_cast<const v4bf*>(p);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = static_cast<float>(r[i]);  } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = static_cast<float>(p[i]);
   }

@@ -65,7 +65,6 @@ __device__ __forceinline__ void mma(v4f& acc, const Frag<float>& a, const Frag<f
 }
 
 typedef short v4s __attribute__((ext_vector_type(4)));
-typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
 
 // LDS row stride of `n` columns: 16 bytes of padding spread neighbouring rows
 // over the banks and keep them 16-byte aligned.
