@@ -14,6 +14,8 @@ Token-major tensors are [batch, length, ...] or, with `offsets`, packed as
 their inner dimensions need be contiguous, so slices of a wider projection go
 in as they are.  Work runs on `stream` (default: the current stream of the
 tensors' device); outputs and workspaces that a call allocates belong to it.
+Tensors that another stream made or will reuse are the caller's to order
+(Stream.wait_stream, Tensor.record_stream), as with any kernel.
 """
 from __future__ import annotations
 
