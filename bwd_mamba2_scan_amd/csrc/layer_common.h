@@ -45,7 +45,8 @@ __device__ __forceinline__ void load_vec(const T* p, float (&v)[V]) {
   } else if constexpr (sizeof(T) == 2 && V == 4) {
     const v4bf r = *reinterpret_cast<const v4bf*>(p);
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = static_cast<float>(r[i]);  } else {
+    for (int i = 0; i < V; ++i) v[i] = static_cast<float>(r[i]);
+  } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = static_cast<float>(p[i]);
   }
@@ -154,6 +155,15 @@ inline int check_seqs(const mamba2_seqs& q) {
   if (rows + q.batch > 2147483647LL - 65536) return MAMBA2_SCAN_EBADDIM;
   if (!aligned_to(q.offsets, 4)) return MAMBA2_SCAN_EALIGN;
   return MAMBA2_SCAN_OK;
+}
+
+// A tensor with the strides that its addresses need: a single row's stride and a
+// single sequence's (or packed rows') may be anything, and the kernels form the
+// addresses of rows behind the last, which have to lie behind the tensor's end.
+inline mamba2_rows used_strides(mamba2_rows r, const mamba2_seqs& q, long long width) {
+  if (q.length <= 1) r.row_stride = width;
+  if (q.offsets != nullptr || q.batch == 1) r.batch_stride = 0;
+  return r;
 }
 
 // A token-major tensor of `width` elements per row.

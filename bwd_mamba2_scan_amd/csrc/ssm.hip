@@ -417,6 +417,11 @@ int mamba2_ssm_fwd(mamba2_seqs q, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows 
   const size_t e = type_size(d.type);
   const long long xw = static_cast<long long>(d.heads) * d.width, bw = static_cast<long long>(d.groups) * d.states;
   if (A == nullptr) return MAMBA2_SCAN_ENULL;
+  x = used_strides(x, q, xw);
+  y = used_strides(y, q, xw);
+  B = used_strides(B, q, bw);
+  C = used_strides(C, q, bw);
+  dt = used_strides(dt, q, d.heads);
   if ((st = check_vec_rows(x, q, xw, e)) != MAMBA2_SCAN_OK || (st = check_vec_rows(B, q, bw, e)) != MAMBA2_SCAN_OK ||
       (st = check_vec_rows(C, q, bw, e)) != MAMBA2_SCAN_OK || (st = check_vec_rows(y, q, xw, e)) != MAMBA2_SCAN_OK ||
       (st = check_step_rows(dt, q, d)) != MAMBA2_SCAN_OK)

@@ -23,6 +23,8 @@
 // Nothing is obtained as a difference of larger sums.
 #include "ssm_common.h"
 
+#include <initializer_list>
+
 namespace {
 
 using namespace ssm;
@@ -751,12 +753,16 @@ int mamba2_ssm_bwd(mamba2_seqs q, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows 
   const size_t e = type_size(d.type);
   const long long xw = static_cast<long long>(d.heads) * d.width, bw = static_cast<long long>(d.groups) * d.states;
   if (A == nullptr || d_A == nullptr || workspace == nullptr) return MAMBA2_SCAN_ENULL;
-  const mamba2_rows* wide[4] = {&x, &d_y, &d_x, nullptr};
-  for (int i = 0; wide[i] != nullptr; ++i)
-    if ((st = check_vec_rows(*wide[i], q, xw, e)) != MAMBA2_SCAN_OK) return st;
-  const mamba2_rows* shared[5] = {&B, &C, &d_B, &d_C, nullptr};
-  for (int i = 0; shared[i] != nullptr; ++i)
-    if ((st = check_vec_rows(*shared[i], q, bw, e)) != MAMBA2_SCAN_OK) return st;
+  for (mamba2_rows* r : {&x, &d_y, &d_x}) {
+    *r = used_strides(*r, q, xw);
+    if ((st = check_vec_rows(*r, q, xw, e)) != MAMBA2_SCAN_OK) return st;
+  }
+  for (mamba2_rows* r : {&B, &C, &d_B, &d_C}) {
+    *r = used_strides(*r, q, bw);
+    if ((st = check_vec_rows(*r, q, bw, e)) != MAMBA2_SCAN_OK) return st;
+  }
+  dt = used_strides(dt, q, d.heads);
+  d_dt = used_strides(d_dt, q, d.heads);
   if ((st = check_step_rows(dt, q, d)) != MAMBA2_SCAN_OK || (st = check_step_rows(d_dt, q, d)) != MAMBA2_SCAN_OK)
     return st;
   if (workspace_bytes < c.p.total * sizeof(float)) return MAMBA2_SCAN_ESIZE;

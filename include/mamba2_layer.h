@@ -61,7 +61,9 @@ typedef struct {
  * A token-major tensor: element e of token t of sequence s is at
  * data + s * batch_stride + t * row_stride + e, strides in elements (with
  * offsets: row r at data + r * row_stride).  So a tensor may be a slice of a
- * wider one.  Strides are not negative, and rows do not overlap.
+ * wider one.  Strides are not negative, and rows do not overlap.  Where there
+ * is one row, or one sequence (or offsets), row_stride or batch_stride is not
+ * used and may be anything.
  */
 typedef struct {
   void* data;
