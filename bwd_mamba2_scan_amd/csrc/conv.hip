@@ -564,6 +564,8 @@ int mamba2_conv_fwd(int type, mamba2_seqs q, int channels, int taps, int silu, m
   if (st != MAMBA2_SCAN_OK) return st;
   const size_t e = type_size(type);
   if (weight == nullptr) return MAMBA2_SCAN_ENULL;
+  x = used_strides(x, q, channels);
+  y = used_strides(y, q, channels);
   if ((st = check_rows(x, q, channels, e)) != MAMBA2_SCAN_OK) return st;
   if ((st = check_rows(y, q, channels, e)) != MAMBA2_SCAN_OK) return st;
   if (!aligned_to(weight, 4) || !aligned_to(bias, 4) || !aligned_to(initial_state, e) || !aligned_to(final_state, e))
@@ -607,6 +609,9 @@ int mamba2_conv_bwd(int type, mamba2_seqs q, int channels, int taps, int silu, m
   const bool sums = d_weight != nullptr || d_bias != nullptr;
   if (weight == nullptr) return MAMBA2_SCAN_ENULL;
   if (d_x.data == nullptr && !sums && d_initial_state == nullptr) return MAMBA2_SCAN_ENULL;
+  x = used_strides(x, q, channels);
+  d_y = used_strides(d_y, q, channels);
+  d_x = used_strides(d_x, q, channels);
   if ((st = check_rows(x, q, channels, e)) != MAMBA2_SCAN_OK) return st;
   if ((st = check_rows(d_y, q, channels, e)) != MAMBA2_SCAN_OK) return st;
   if (d_x.data != nullptr && (st = check_rows(d_x, q, channels, e)) != MAMBA2_SCAN_OK) return st;

@@ -8,7 +8,7 @@ import torch
 
 import bwd_mamba2_scan_amd as m2
 from bwd_mamba2_scan_amd.layer import Rows, Seqs, SsmDims
-from tests.selective import TYPES, scan_inputs, to
+from tests.selective import TYPES, gen, scan_inputs, to
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -96,3 +96,45 @@ def test_through_the_binding():
         assert torch.equal(y, y0) and torch.equal(f, f0)
         for k, v in g0.items():
             assert torch.equal(g[k], v), (stride, k)
+
+
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+@pytest.mark.parametrize("packed", [False, True])
+def test_convolution(typ, packed):
+    batch, C, W = 1 if packed else 2, 40, 4
+    g = gen(7)
+    r = lambda *s: torch.randn(*s, generator=g).to(DEV)
+    t = TYPES[typ]
+    x, d_y, tail, d_final = r(batch, C).to(t), r(batch, C).to(t), r(batch, W - 1, C).to(t), r(batch, W - 1, C).to(t)
+    weight, bias = r(C, W), r(C)
+    code = {"f32": 0, "bf16": 1}[typ]
+    q, off = _seqs(packed, batch)
+    L = m2.lib()
+    ws = torch.empty(L.mamba2_conv_bwd_workspace_bytes(q, C, W) // 4, device=DEV)
+
+    def run(stride):
+        rows = lambda v: Rows(_p(v), v.shape[1], C if stride is None else stride)
+        y, d_x = (torch.full((batch, 3 * C), MARK, dtype=t, device=DEV) for _ in range(2))
+        final, first = torch.empty_like(tail), torch.empty_like(tail)
+        dw, db = torch.empty_like(weight), torch.empty_like(bias)
+        _call(L.mamba2_conv_fwd, code, q, C, W, 1, rows(x), _p(weight), _p(bias), _p(tail), rows(y), _p(final))
+        _call(L.mamba2_conv_bwd, code, q, C, W, 1, rows(x), _p(weight), _p(bias), _p(tail), rows(d_y), _p(d_final), rows(d_x),
+              _p(dw), _p(db), _p(first), _p(ws), ws.numel() * 4)
+        return dict(y=y, d_x=d_x, final=final, first=first, dw=dw, db=db)
+
+    want = run(None)
+    for k in ("y", "d_x"):
+        assert bool((want[k][:, C:] == MARK).all()) and not bool((want[k][:, :C] == MARK).any()), k
+    for stride in STRIDES:
+        print("convolution of one token", typ, packed, stride, flush=True)
+        got = run(stride)
+        for k in want:
+            assert torch.equal(got[k], want[k]), (stride, k)
+
+
+def test_convolution_of_a_slice():
+    """One token out of a time-major tensor: its row stride passes the limit of the strides that are used."""
+    wide = torch.randn(1, 600, 8000, generator=gen(8)).bfloat16().to(DEV)
+    x = wide[..., :16].transpose(0, 1)          # [600, 1, 16], row stride 4.8 million
+    weight = torch.randn(16, 4, generator=gen(9)).to(DEV)
+    assert torch.equal(m2.conv_fwd(x, weight)[0], m2.conv_fwd(x.contiguous(), weight)[0])
