@@ -243,7 +243,7 @@ __global__ __launch_bounds__(kStepThreads) void ssm_step_kernel(StepArgs sa) {
   const float raw = a.dt_bf16 ? static_cast<float>(static_cast<const bf16*>(a.dt.data)[di])
                               : static_cast<const float*>(a.dt.data)[di];
   const float d = step_of(a, raw, a.bias != nullptr ? a.bias[h] : 0.0f);
-  const float decay = exp2_of(static_cast<double>(d) * static_cast<double>(a.A[h]) * 1.4426950408889634074);
+  const float decay = exp2_of(log_decay(d, a.A[h]));
   const T* xp = static_cast<const T*>(a.x.data) + seq * a.x.batch_stride + h * a.width + 4 * q;
   float x[4], xd[4];
 #pragma unroll

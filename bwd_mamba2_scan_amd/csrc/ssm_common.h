@@ -383,13 +383,20 @@ struct DecaysOf {
 };
 typedef DecaysOf<false> Decays;
 
-// One wave; lane t has token t.  A token whose decay underflows any fp32
-// (2^-1100) is held there, so that later differences keep their bits.
+// log2 of a token's decay.  One that underflows any fp32 (2^-1100) is held there,
+// so that later differences keep their bits.  A step of 0 decays nothing even
+// where A is infinite; a NaN of either stays one.
+__device__ __forceinline__ double log_decay(float d, float A) {
+  const double l = static_cast<double>(d) * static_cast<double>(A) * 1.4426950408889634074;
+  if (d == 0.0f && A == A) return 0.0;
+  return l < -1100.0 ? -1100.0 : l;
+}
+
+// One wave; lane t has token t.
 template <bool LEFT>
 __device__ __forceinline__ void make_decays(DecaysOf<LEFT>& dc, float d, float A) {
   const int t = threadIdx.x & 63;
-  const double l = fmax(static_cast<double>(d) * static_cast<double>(A) * 1.4426950408889634074, -1100.0);
-  const double c = scan64(l);
+  const double c = scan64(log_decay(d, A));
   const long cbits = __builtin_bit_cast(long, c);
   const double end = __builtin_bit_cast(
       double, (static_cast<long>(__builtin_amdgcn_readlane(static_cast<int>(cbits >> 32), 63)) << 32) |
