@@ -201,7 +201,7 @@ __global__ __launch_bounds__(NW * 64, 2) void ssm_summary_kernel(SsmArgs a, Walk
   walk<T, NB, NW, false>(a, w, s);
 }
 
-__global__ __launch_bounds__(256) void ssm_carry_kernel(SsmArgs a, Walk w) { carry(a, w, blockIdx.z); }
+__global__ __launch_bounds__(256) void ssm_carry_kernel(SsmArgs a, Walk w) { carry(a, w, blockIdx.z, blockIdx.x); }
 
 // ------------------------------------------------------------- single token
 // A work-group per sequence and head; a thread holds four neighbouring

@@ -61,7 +61,7 @@ __global__ __launch_bounds__(NW * 64, 2) void ssm_walk_summary_kernel(SsmArgs a,
   walk<T, NB, NW, false>(a, ws.w[blockIdx.y], s);
 }
 __global__ __launch_bounds__(256) void ssm_walk_carry_kernel(SsmArgs a, Walks ws) {
-  carry(a, ws.w[blockIdx.z & 1], blockIdx.z >> 1);
+  carry(a, ws.w[blockIdx.x & 1], blockIdx.z, blockIdx.x >> 1);
 }
 
 constexpr int kBwdThreads = 512;
@@ -702,7 +702,7 @@ int launch_bwd(const Call& c) {
     if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
     if (!a.fold) {
       const unsigned quads = static_cast<unsigned>((a.states * a.width + 1023) / 1024);
-      ssm_walk_carry_kernel<<<dim3(quads, a.heads, 2 * a.q.batch), 256, 0, c.s>>>(a, c.w);
+      ssm_walk_carry_kernel<<<dim3(2 * quads, a.heads, a.q.batch), 256, 0, c.s>>>(a, c.w);
       if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
     }
   }
@@ -771,7 +771,7 @@ int mamba2_ssm_bwd(mamba2_seqs q, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows 
       !aligned_to(d_A, 4) || !aligned_to(d_D, 4) || !aligned_to(d_dt_bias, 4))
     return MAMBA2_SCAN_EALIGN;
   if (static_cast<long long>(c.p.units) * d.heads * c.p.slices > 2147483647LL ||
-      static_cast<long long>(c.p.steps) * d.groups * c.p.splits > 2147483647LL || q.batch > 32767)
+      static_cast<long long>(c.p.steps) * d.groups * c.p.splits > 2147483647LL)
     return MAMBA2_SCAN_EBADDIM;
 
   SsmArgs& a = c.ba.a;

@@ -683,9 +683,9 @@ __device__ __forceinline__ void walk(const SsmArgs& a, const Walk& w, WalkLds<T,
 // 8 us for 43 segments of 24 heads of 64 x 64, the chain's length (18 MB).
 // Carry: turns the segments' own contributions into the state each segment
 // starts from.  One thread per four elements of a sequence's head.
-__device__ __forceinline__ void carry(const SsmArgs& a, const Walk& w, int seq) {
+__device__ __forceinline__ void carry(const SsmArgs& a, const Walk& w, int seq, int block) {
   const long head = static_cast<long>(a.states) * a.width;
-  const long e = (static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x) * 4;
+  const long e = (static_cast<long>(block) * blockDim.x + threadIdx.x) * 4;
   if (e >= head) return;
   const int h = blockIdx.y;
   long row0;

@@ -105,8 +105,8 @@ int mamba2_conv_bwd(int type, mamba2_seqs seqs, int channels, int taps, int silu
                     size_t workspace_bytes, void* stream);
 
 /*
- * One token of each of `batch` sequences: x and y [batch][channels] (their
- * batch_stride; row_stride is not used), state [batch][taps - 1][channels].
+ * One token of each of `batch` <= 65535 sequences: x and y [batch][channels]
+ * (their batch_stride; row_stride is not used), state [batch][taps - 1][channels].
  * new_state gets the state moved on by the token; it may be `state` itself.
  * Any other overlap is refused (MAMBA2_SCAN_EOVERLAP).
  */
@@ -128,8 +128,9 @@ int mamba2_conv_step(int type, int batch, int channels, int taps, int silu,
  * after the last token, and initial_state itself for an empty sequence.
  * A token whose d_t is 0 (dt = -inf under softplus) leaves the state as it
  * was; so a padded batch marks its padding, x, B and C there being finite.
- *   1 <= groups, heads a multiple of groups; width and states multiples of 8,
- *   8 .. 128.  x, B, C, y and the states are 16-byte aligned, with row and
+ *   1 <= groups, heads a multiple of groups, at most 65535, as batch is;
+ *   width and states multiples of 8, 8 .. 128.  x, B, C, y and the states are
+ *   16-byte aligned, with row and
  *   batch strides that are multiples of 8 elements; dt has any stride.  Row
  *   strides are at most 2^29 / 65 elements.
  *   A value of x, B, C, dt or d_y that is not finite may reach every token of
