@@ -587,7 +587,7 @@ int mamba2_conv_fwd(int type, mamba2_seqs q, int channels, int taps, int silu, m
   a.final_state = final_state;
   const long long blocks = (static_cast<long long>(a.units) + (final_state != nullptr ? q.batch : 0)) * a.cblocks;
   if (blocks == 0) return MAMBA2_SCAN_OK;
-  if (blocks > 2147483647LL) return MAMBA2_SCAN_EBADDIM;
+  if (!grid_ok(blocks, kLanes)) return MAMBA2_SCAN_EBADDIM;
   launch_conv(kFwd, type, vec, taps, silu, a, dim3(static_cast<unsigned>(blocks)), static_cast<hipStream_t>(stream));
   return launch_status();
 }
@@ -644,7 +644,7 @@ int mamba2_conv_bwd(int type, mamba2_seqs q, int channels, int taps, int silu, m
   a.d_initial = d_initial_state;
   a.partial = sums ? static_cast<float*>(workspace) : nullptr;
   const long long blocks = (static_cast<long long>(a.units) + (d_initial_state != nullptr ? q.batch : 0)) * a.cblocks;
-  if (blocks > 2147483647LL) return MAMBA2_SCAN_EBADDIM;
+  if (!grid_ok(blocks, kLanes * kBwdWaves)) return MAMBA2_SCAN_EBADDIM;
   if (blocks > 0) {
     launch_conv(kBwd, type, vec, taps, silu, a, dim3(static_cast<unsigned>(blocks)), s);
     if ((st = launch_status()) != MAMBA2_SCAN_OK) return st;

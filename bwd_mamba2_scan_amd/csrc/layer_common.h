@@ -215,6 +215,9 @@ inline bool apart(const Region* v, int n, int count) {
   return true;
 }
 
+// A launch counts its threads in 32 bits.
+inline bool grid_ok(long long blocks, int threads) { return blocks <= 0xffffffffLL / threads; }
+
 inline int launch_status() { return hipGetLastError() == hipSuccess ? MAMBA2_SCAN_OK : MAMBA2_SCAN_EHIP; }
 
 }  // namespace layer

@@ -383,6 +383,15 @@ int fold_segments(const mamba2_seqs& q, int seg) {
   return units_of(q.length, seg) <= 8 * (q.offsets != nullptr ? min(q.batch, 3) : 1);
 }
 
+// check_dims, and that the passes over the segments can be launched.
+int check_scan(const mamba2_seqs& q, const mamba2_ssm_dims& d) {
+  const int st = check_dims(q, d);
+  if (st != MAMBA2_SCAN_OK) return st;
+  const int nw = waves_of(d.width), slices = (d.width + nw * 16 - 1) / (nw * 16);
+  const long long units = unit_count(q, segment_tokens(q, d));
+  return grid_ok(units * d.heads * slices, nw * 64) ? MAMBA2_SCAN_OK : MAMBA2_SCAN_EBADDIM;
+}
+
 }  // namespace ssm
 
 extern "C" {
@@ -402,7 +411,7 @@ const char* mamba2_layer_strerror(int status) {
 }
 
 size_t mamba2_ssm_fwd_workspace_bytes(mamba2_seqs q, mamba2_ssm_dims d) {
-  if (check_dims(q, d) != MAMBA2_SCAN_OK) return 0;
+  if (check_scan(q, d) != MAMBA2_SCAN_OK) return 0;
   const int seg = segment_tokens(q, d);
   if (q.length <= seg) return 0;
   const size_t n = static_cast<size_t>(unit_count(q, seg)) * d.heads * (static_cast<size_t>(d.states) * d.width + 1);
@@ -412,7 +421,7 @@ size_t mamba2_ssm_fwd_workspace_bytes(mamba2_seqs q, mamba2_ssm_dims d) {
 int mamba2_ssm_fwd(mamba2_seqs q, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows dt, const float* A, mamba2_rows B,
                    mamba2_rows C, const float* D, const float* dt_bias, const float* initial_state, mamba2_rows y,
                    float* final_state, void* workspace, size_t workspace_bytes, void* stream) {
-  int st = check_dims(q, d);
+  int st = check_scan(q, d);
   if (st != MAMBA2_SCAN_OK) return st;
   const size_t e = type_size(d.type);
   const long long xw = static_cast<long long>(d.heads) * d.width, bw = static_cast<long long>(d.groups) * d.states;
@@ -465,10 +474,8 @@ int mamba2_ssm_fwd(mamba2_seqs q, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows 
   w.first = initial_state;
   w.seg_state = static_cast<float*>(workspace);
   w.seg_decay = need > 0 ? w.seg_state + static_cast<size_t>(a.units) * d.heads * d.states * d.width : nullptr;
-  const long long blocks = static_cast<long long>(a.units) * a.heads * a.slices;
-  if (blocks > 2147483647LL) return MAMBA2_SCAN_EBADDIM;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const unsigned n = static_cast<unsigned>(blocks);
+  const unsigned n = static_cast<unsigned>(a.units) * a.heads * a.slices;
   return d.type == MAMBA2_BF16 ? launch_fwd_states<bf16>(a, w, need > 0, n, nw, s)
                                : launch_fwd_states<float>(a, w, need > 0, n, nw, s);
 }

@@ -659,7 +659,7 @@ struct Plan {
 size_t pad4(size_t n) { return (n + 3) / 4 * 4; }
 
 int make_plan(const mamba2_seqs& q, const mamba2_ssm_dims& d, Plan* p) {
-  const int st = check_dims(q, d);
+  const int st = check_scan(q, d);
   if (st != MAMBA2_SCAN_OK) return st;
   const size_t head = static_cast<size_t>(d.states) * d.width;
   p->nw = waves_of(d.width);
@@ -676,6 +676,7 @@ int make_plan(const mamba2_seqs& q, const mamba2_ssm_dims& d, Plan* p) {
   if (splits > ratio) splits = ratio;
   p->run = static_cast<int>((ratio + splits - 1) / splits);
   p->splits = (ratio + p->run - 1) / p->run;
+  if (!grid_ok(static_cast<long long>(p->steps) * d.groups * p->splits, kBwdThreads)) return MAMBA2_SCAN_EBADDIM;
   p->keep = static_cast<size_t>(p->steps) * d.heads * kept_size(d.width, d.states);
   p->seg_state = p->segments ? pad4(static_cast<size_t>(p->units) * d.heads * head) : 0;
   p->seg_decay = p->segments ? pad4(static_cast<size_t>(p->units) * d.heads) : 0;
@@ -770,9 +771,6 @@ int mamba2_ssm_bwd(mamba2_seqs q, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows 
       !aligned_to(d_final_state, 16) || !aligned_to(d_initial_state, 16) || !aligned_to(workspace, 16) ||
       !aligned_to(d_A, 4) || !aligned_to(d_D, 4) || !aligned_to(d_dt_bias, 4))
     return MAMBA2_SCAN_EALIGN;
-  if (static_cast<long long>(c.p.units) * d.heads * c.p.slices > 2147483647LL ||
-      static_cast<long long>(c.p.steps) * d.groups * c.p.splits > 2147483647LL)
-    return MAMBA2_SCAN_EBADDIM;
 
   SsmArgs& a = c.ba.a;
   a.q = q;

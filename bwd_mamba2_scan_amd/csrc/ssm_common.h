@@ -723,6 +723,7 @@ __device__ __forceinline__ void carry(const SsmArgs& a, const Walk& w, int seq, 
 
 // Host side, in ssm.hip.
 int check_dims(const mamba2_seqs& q, const mamba2_ssm_dims& d);
+int check_scan(const mamba2_seqs& q, const mamba2_ssm_dims& d);
 int check_vec_rows(const mamba2_rows& r, const mamba2_seqs& q, long long width, size_t elem);
 int check_step_rows(const mamba2_rows& r, const mamba2_seqs& q, const mamba2_ssm_dims& d);
 int waves_of(int width);

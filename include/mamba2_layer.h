@@ -16,6 +16,11 @@
  *     bitwise reproducible: no atomics, every sum in a fixed order.
  *   - An output may not overlap an input or another output, except where a
  *     call says so.
+ *   - Calls whose launch would have 2^32 threads or more are refused
+ *     (MAMBA2_SCAN_EBADDIM).  The convolution has 64 (backward: 256) for every 8
+ *     to 64 tokens of a sequence and 64 channels (wide accesses: 256 or 512),
+ *     the scan up to 256 for every sequence and head and its backward 512 for
+ *     every 64 tokens of a sequence and group.
  *   - Calls on different streams, and replays of different captured graphs,
  *     may run concurrently if their outputs and workspaces do not overlap.
  *   - A call may be captured into a graph; the addresses it was given, the

@@ -1,0 +1,41 @@
+"""Limits of the selective layer's calls (CPU): every call below is refused before anything is launched."""
+from __future__ import annotations
+
+import pytest
+
+import bwd_mamba2_scan_amd as m2
+from bwd_mamba2_scan_amd.layer import Rows, Seqs, SsmDims
+
+P, MUCH = 0x100000, 1 << 62
+
+
+@pytest.fixture(scope="module")
+def L():
+    return m2.lib()
+
+
+def test_convolutions_of_too_many_threads(L):
+    # 2^27 sequences of one token: a work-group of 64 (256) threads each
+    q, r = Seqs(1 << 27, 1, None), Rows(P, 8, 8)
+    assert L.mamba2_conv_fwd(1, q, 8, 4, 1, r, P, None, None, r, None, None) == m2.EBADDIM
+    q = Seqs(1 << 25, 1, None)
+    assert L.mamba2_conv_bwd(1, q, 8, 4, 1, r, P, None, None, r, None, r, P, None, None, P, MUCH, None) == m2.EBADDIM
+    # 2^30 tokens of 1024 channels one at a time, their rows not aligned
+    q, r = Seqs(1, 1 << 30, None), Rows(P + 4, 0, 1025)
+    assert L.mamba2_conv_fwd(0, q, 1024, 4, 1, r, P, None, None, r, None, None) == m2.EBADDIM
+
+
+def test_scans_of_too_many_threads(L):
+    def call(q, d, bwd):
+        r, s, t = Rows(P, d.heads * d.width, 0), Rows(P, d.groups * d.states, 0), Rows(P, d.heads, 0)
+        head = (q, d, r, t, P, s, s, None, None, None, r)
+        if bwd:
+            return L.mamba2_ssm_bwd(*head, None, r, t, P, s, s, None, None, None, P, MUCH, None)
+        return L.mamba2_ssm_fwd(*head, None, P, MUCH, None)
+
+    q, d = Seqs(65535, 1, None), SsmDims(0, 0, 1100, 8, 1, 8, 1)            # one wave per sequence and head
+    assert call(q, d, False) == m2.EBADDIM == call(q, d, True)
+    assert L.mamba2_ssm_bwd_workspace_bytes(q, d) == 0 == L.mamba2_ssm_fwd_workspace_bytes(q, d)
+    d = SsmDims(0, 0, 200, 8, 200, 8, 1)                                     # 512 threads per step and group
+    assert call(q, d, True) == m2.EBADDIM and L.mamba2_ssm_bwd_workspace_bytes(q, d) == 0
+    assert L.mamba2_ssm_bwd_workspace_bytes(q, SsmDims(0, 0, 100, 8, 100, 8, 1)) > 0
