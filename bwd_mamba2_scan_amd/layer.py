@@ -25,6 +25,7 @@ import struct
 
 _F32, _BF16 = 0, 1
 _EOVERLAP = -8
+_MAX_INT = 2 ** 31 - 1
 
 _c_int, _c_size, _c_vp, _c_ll = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_longlong
 
@@ -183,12 +184,19 @@ def _token(rows):
     return rows
 
 
+def _sizes(*sizes):
+    """Refuses sizes that the C ABI's ints do not hold (ctypes would cut them off)."""
+    if max(sizes) > _MAX_INT:
+        raise ValueError(f"a dimension of {max(sizes)} is too large (at most {_MAX_INT})")
+
+
 def _seqs(x, offsets, inner_dims, dev):
     """(mamba2_seqs, the leading shape, the number of sequences)"""
     if offsets is None:
         if x.dim() != 2 + inner_dims:
             raise ValueError(f"x must have {2 + inner_dims} dimensions (got {x.dim()}); packed rows need offsets")
         batch, length = x.shape[:2]
+        _sizes(batch, length)
         return Seqs(batch, length, None), (batch, length), batch
     if x.dim() != 1 + inner_dims:
         raise ValueError(f"with offsets x must have {1 + inner_dims} dimensions (got {x.dim()})")
@@ -196,6 +204,7 @@ def _seqs(x, offsets, inner_dims, dev):
     if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous int32 vector of at least two elements")
     batch = offsets.numel() - 1
+    _sizes(batch, x.shape[0])
     return Seqs(batch, x.shape[0], offsets.data_ptr()), (x.shape[0],), batch
 
 
@@ -280,6 +289,7 @@ def _conv_dims(x, weight, dev):
     if weight.dim() != 2:
         raise ValueError("weight must be [channels, taps]")
     channels, taps = weight.shape
+    _sizes(channels, taps)
     w = _dense(weight, "weight", (channels, taps), torch.float32, dev)
     return channels, taps, w
 
@@ -362,6 +372,7 @@ def conv_step(x, weight, state, bias=None, *, silu=True, new_state=None, y=None,
     dev, typ = _start(x)
     channels, taps, w = _conv_dims(x, weight, dev)
     batch = x.shape[0]
+    _sizes(batch)
     rx = _token(_rows(x, "x", (batch,), (channels,), x.dtype, dev))
     tail = (batch, taps - 1, channels)
     s0 = _dense(state, "state", tail, x.dtype, dev)
@@ -384,7 +395,10 @@ def _ssm_dims(typ, x, dt, B, softplus):
     _gpu(B, "B")
     if B.dim() != x.dim():
         raise ValueError("B and C must be [..., groups, states] beside x [..., heads, width]")
-    return SsmDims(typ, _type(dt, "dt"), *x.shape[-2:], *B.shape[-2:], bool(softplus))
+    heads, width = x.shape[-2:]
+    groups, states = B.shape[-2:]
+    _sizes(heads, width, groups, states)
+    return SsmDims(typ, _type(dt, "dt"), heads, width, groups, states, bool(softplus))
 
 
 def _ssm_inputs(x, dt, A, B, C, D, dt_bias, lead, d, dev):
@@ -476,6 +490,7 @@ def ssm_step(x, dt, A, B, C, state, *, D=None, dt_bias=None, softplus=True, new_
     if x.dim() != 3:
         raise ValueError("x must be [batch, heads, width]")
     batch = x.shape[0]
+    _sizes(batch)
     d = _ssm_dims(typ, x, dt, B, softplus)
     px, pdt, pA, pB, pC, pD, pbias = _ssm_inputs(x, dt, A, B, C, D, dt_bias, (batch,), d, dev)
     shape = (batch, d.heads, d.states, d.width)

@@ -2,8 +2,10 @@
 from __future__ import annotations
 
 import pytest
+import torch
 
 import bwd_mamba2_scan_amd as m2
+from bwd_mamba2_scan_amd import layer
 from bwd_mamba2_scan_amd.layer import Rows, Seqs, SsmDims
 
 P, MUCH = 0x100000, 1 << 62
@@ -39,3 +41,24 @@ def test_scans_of_too_many_threads(L):
     d = SsmDims(0, 0, 200, 8, 200, 8, 1)                                     # 512 threads per step and group
     assert call(q, d, True) == m2.EBADDIM and L.mamba2_ssm_bwd_workspace_bytes(q, d) == 0
     assert L.mamba2_ssm_bwd_workspace_bytes(q, SsmDims(0, 0, 100, 8, 100, 8, 1)) > 0
+
+
+@pytest.mark.parametrize("shape", [(1, (1 << 32) + 8, 8), ((1 << 32) + 1, 4, 8), (1, 1 << 31, 1)])
+def test_sizes_beyond_an_int_are_not_cut_off(shape):
+    layer._load()
+    with pytest.raises(ValueError, match="too large"):
+        layer._seqs(torch.empty(shape, device="meta"), None, 1, torch.device("meta"))
+    with pytest.raises(ValueError, match="too large"):
+        layer._ssm_dims(0, *_Sizes.of((2, 8), ((1 << 32) + 1, 8)), True)
+    with pytest.raises(ValueError, match="too large"):
+        layer._ssm_dims(0, *_Sizes.of(((1 << 32) + 2, 8), (1, 8)), True)
+
+
+class _Sizes(torch.Tensor):
+    """A tensor without memory that passes for one on a GPU."""
+    is_cuda = True
+
+    @classmethod
+    def of(cls, x, B):
+        make = lambda *s: torch.empty(s, device="meta").as_subclass(cls)
+        return make(1, 4, *x), make(1, 4, x[0]), make(1, 4, *B)
