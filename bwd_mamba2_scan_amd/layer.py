@@ -98,11 +98,11 @@ class _On:
 
     def __enter__(self):
         index = self._dev.index
+        if self._stream is not None and self._stream.device != self._dev:  # before any guard: none is left behind
+            raise ValueError(f"stream is on {self._stream.device}, the tensors on {self._dev}")
         if torch._C._cuda_getDevice() != index:
             self._push(torch.cuda.device(index))
         if self._stream is not None:
-            if self._stream.device != self._dev:
-                raise ValueError(f"stream is on {self._stream.device}, the tensors on {self._dev}")
             self._push(torch.cuda.stream(self._stream))
         return torch._C._cuda_getCurrentRawStream(index)
 

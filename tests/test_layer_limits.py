@@ -62,3 +62,28 @@ class _Sizes(torch.Tensor):
     def of(cls, x, B):
         make = lambda *s: torch.empty(s, device="meta").as_subclass(cls)
         return make(1, 4, *x), make(1, 4, x[0]), make(1, 4, *B)
+
+
+def test_a_refused_stream_leaves_the_current_device(monkeypatch):
+    """Tensors on a device that is not the current one, a stream of a third: refused, and the device stays."""
+    import types
+
+    current = [0]
+
+    class Guard:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    fake = types.SimpleNamespace(cuda=types.SimpleNamespace(device=Guard),
+                                 _C=types.SimpleNamespace(_cuda_getDevice=lambda: current[0]))
+    monkeypatch.setattr(layer, "torch", fake)
+    with pytest.raises(ValueError, match="stream is on"):
+        with layer._On(torch.device("cuda:1"), types.SimpleNamespace(device=torch.device("cuda:2"))):
+            pass
+    assert current[0] == 0
