@@ -258,6 +258,17 @@ def _interleaved(t, o):
     return wt <= gap and gap + wo <= row
 
 
+def _given(out, **inputs):
+    """The tensors of `out`: gradients of required inputs (True) or of inputs that were given."""
+    res = dict(out or {})
+    for name, t in res.items():
+        if name not in inputs:
+            raise ValueError(f"out holds {name!r}; the gradients are {', '.join(inputs)}")
+        if t is not None and inputs[name] is None:
+            raise ValueError(f"out holds {name}, but no {name[2:]} was given")
+    return res
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -323,7 +334,7 @@ def conv_fwd(x, weight, bias=None, *, silu=True, initial_state=None, offsets=Non
 def conv_bwd(x, weight, d_y, bias=None, *, silu=True, initial_state=None, d_final_state=None, offsets=None, out=None,
              workspace=None, stream=None):
     """Gradients of conv_fwd for dL/dy = d_y (and dL/dfinal_state): dict with d_x, d_weight, d_bias (None without
-    bias) and d_initial_state (None without initial_state).  `out` may hold some of these tensors.
+    bias) and d_initial_state (None without initial_state).  `out` may hold some of these tensors, no others.
     """
     dev, typ = _start(x)
     seqs, lead, batch = _seqs(x, offsets, 1, dev)
@@ -334,7 +345,7 @@ def conv_bwd(x, weight, d_y, bias=None, *, silu=True, initial_state=None, d_fina
     tail = (batch, taps - 1, channels)
     s0 = _dense(initial_state, "initial_state", tail, x.dtype, dev)
     sf = _dense(d_final_state, "d_final_state", tail, x.dtype, dev)
-    res = dict(out or {})
+    res = _given(out, d_x=True, d_weight=True, d_bias=bias, d_initial_state=initial_state)
     _apart(tuple(res.items()) + (("workspace", workspace),),
            (("x", x), ("weight", weight), ("bias", bias), ("d_y", d_y), ("initial_state", initial_state),
             ("d_final_state", d_final_state)))
@@ -446,7 +457,7 @@ def ssm_fwd(x, dt, A, B, C, *, D=None, dt_bias=None, softplus=True, initial_stat
 def ssm_bwd(x, dt, A, B, C, d_y, *, D=None, dt_bias=None, softplus=True, initial_state=None, d_final_state=None,
             offsets=None, out=None, workspace=None, stream=None):
     """Gradients of ssm_fwd for dL/dy = d_y (and dL/dfinal_state): dict with d_x, d_dt, d_A, d_B, d_C, and d_D,
-    d_dt_bias, d_initial_state (each None where the forward had no such input).  `out` may hold some of them.
+    d_dt_bias, d_initial_state (each None where the forward had no such input).  `out` may hold some of them, no others.
     """
     dev, typ = _start(x)
     f32 = torch.float32
@@ -458,7 +469,8 @@ def ssm_bwd(x, dt, A, B, C, d_y, *, D=None, dt_bias=None, softplus=True, initial
     pg = _rows(d_y, "d_y", lead, inner, x.dtype, dev)
     s0 = _dense(initial_state, "initial_state", shape, f32, dev)
     sf = _dense(d_final_state, "d_final_state", shape, f32, dev)
-    res = dict(out or {})
+    res = _given(out, d_x=True, d_dt=True, d_A=True, d_B=True, d_C=True, d_D=D, d_dt_bias=dt_bias,
+                 d_initial_state=initial_state)
     _apart(tuple(res.items()) + (("workspace", workspace),),
            (("x", x), ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("dt_bias", dt_bias), ("d_y", d_y),
             ("initial_state", initial_state), ("d_final_state", d_final_state)))
