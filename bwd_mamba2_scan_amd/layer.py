@@ -322,7 +322,7 @@ def conv_fwd(x, weight, bias=None, *, silu=True, initial_state=None, offsets=Non
     b = _dense(bias, "bias", (channels,), torch.float32, dev)
     s0 = _dense(initial_state, "initial_state", (batch, taps - 1, channels), x.dtype, dev)
     _apart((("y", y), ("final_state", final_state)),
-           (("x", x), ("weight", weight), ("bias", bias), ("initial_state", initial_state)))
+           (("x", x), ("weight", weight), ("bias", bias), ("initial_state", initial_state), ("offsets", offsets)))
     with _On(dev, stream) as s:
         y, ry = _new_rows(y, "y", lead, (channels,), x, dev)
         final_state, s1 = _new_dense(final_state, "final_state", (batch, taps - 1, channels), x, dev, want_final_state)
@@ -348,7 +348,7 @@ def conv_bwd(x, weight, d_y, bias=None, *, silu=True, initial_state=None, d_fina
     res = _given(out, d_x=True, d_weight=True, d_bias=bias, d_initial_state=initial_state)
     _apart(tuple(res.items()) + (("workspace", workspace),),
            (("x", x), ("weight", weight), ("bias", bias), ("d_y", d_y), ("initial_state", initial_state),
-            ("d_final_state", d_final_state)))
+            ("d_final_state", d_final_state), ("offsets", offsets)))
     with _On(dev, stream) as s:
         get = res.get
         res["d_x"], rx1 = _new_rows(get("d_x"), "d_x", lead, (channels,), x, dev)
@@ -444,7 +444,7 @@ def ssm_fwd(x, dt, A, B, C, *, D=None, dt_bias=None, softplus=True, initial_stat
     s0 = _dense(initial_state, "initial_state", shape, torch.float32, dev)
     _apart((("y", y), ("final_state", final_state), ("workspace", workspace)),
            (("x", x), ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("dt_bias", dt_bias),
-            ("initial_state", initial_state)))
+            ("initial_state", initial_state), ("offsets", offsets)))
     with _On(dev, stream) as s:
         y, py = _new_rows(y, "y", lead, (d.heads, d.width), x, dev)
         final_state, s1 = _new_dense(final_state, "final_state", shape, A, dev, want_final_state)
@@ -473,7 +473,7 @@ def ssm_bwd(x, dt, A, B, C, d_y, *, D=None, dt_bias=None, softplus=True, initial
                  d_initial_state=initial_state)
     _apart(tuple(res.items()) + (("workspace", workspace),),
            (("x", x), ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("dt_bias", dt_bias), ("d_y", d_y),
-            ("initial_state", initial_state), ("d_final_state", d_final_state)))
+            ("initial_state", initial_state), ("d_final_state", d_final_state), ("offsets", offsets)))
     with _On(dev, stream) as s:
         ptr = {}
         for name, size, like in (("d_x", inner, x), ("d_dt", vec, dt), ("d_B", shared, x), ("d_C", shared, x)):

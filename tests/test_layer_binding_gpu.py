@@ -33,3 +33,23 @@ def test_gradients_that_there_are_not():
             m2.ssm_bwd(*args, out={name: torch.empty_like(p[t])})
     g = m2.ssm_bwd(*args, D=p["D"], out=dict(d_D=torch.empty_like(p["D"])))
     assert g["d_dt_bias"] is None and g["d_D"] is not None
+
+
+def test_outputs_over_the_offsets():
+    x, w, d_y, _, _ = _conv(1)
+    p = to(scan_inputs(2, (9,), 1, 1, 8, 1, 8, "f32", "f32"), DEV)
+    args = [p[k] for k in ("x", "dt", "A", "B", "C")]
+    both = torch.zeros(1 << 16, device=DEV)
+    offsets = both.view(torch.int32)[:2]
+    offsets.copy_(torch.tensor([0, 9]))
+    over = lambda *s: both[:torch.Size(s).numel()].view(s)
+    for call in (lambda: m2.conv_fwd(x[0], w, offsets=offsets, y=over(9, 16)),
+                 lambda: m2.conv_fwd(x[0], w, offsets=offsets, final_state=over(1, 3, 16)),
+                 lambda: m2.conv_bwd(x[0], w, d_y[0], offsets=offsets, workspace=both),
+                 lambda: m2.conv_bwd(x[0], w, d_y[0], offsets=offsets, out=dict(d_weight=over(16, 4))),
+                 lambda: m2.ssm_fwd(*args, offsets=offsets, y=over(9, 1, 8)),
+                 lambda: m2.ssm_bwd(*args, p["d_y"], offsets=offsets, out=dict(d_B=over(9, 1, 8))),
+                 lambda: m2.ssm_bwd(*args, p["d_y"], offsets=offsets, workspace=both)):
+        with pytest.raises(ValueError, match="overlaps offsets"):
+            call()
+    assert offsets.tolist() == [0, 9] and not bool(both[2:].any())
