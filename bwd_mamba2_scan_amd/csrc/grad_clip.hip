@@ -205,6 +205,18 @@ struct Span {
   uintptr_t lo, hi;
 };
 
+// Does the norm or the workspace overlap the other or a gradient?  (Gradients
+// that are only read may overlap.)
+int check_norm_apart(const mamba2_grad* g, int count, const float* norm, const void* workspace, size_t workspace_bytes) {
+  const Region r = region(norm, sizeof(float)), w = region(workspace, static_cast<long long>(workspace_bytes));
+  bool apart = !overlap(r, w);
+  for (int i = 0; i < count; ++i) {
+    const Region v = region(g[i].grad, g[i].numel * static_cast<long long>(type_size(g[i].type)));
+    apart = apart && (g[i].numel == 0 || (!overlap(v, r) && !overlap(v, w)));
+  }
+  return apart ? MAMBA2_SCAN_OK : MAMBA2_SCAN_EOVERLAP;
+}
+
 // Does any gradient or output overlap another?  The second pass writes while
 // the first one's other tensors are still to be scaled, so each must be apart.
 int check_apart(const mamba2_grad* g, int count, const float* norm, const void* workspace, size_t workspace_bytes) {
@@ -306,6 +318,7 @@ int mamba2_grad_norm(const mamba2_grad* grads, int count, float* norm, void* wor
   Sizes sz;
   int st = check_call(grads, count, false, norm, workspace, workspace_bytes, &sz);
   if (st != MAMBA2_SCAN_OK) return st;
+  if ((st = check_norm_apart(grads, count, norm, workspace, workspace_bytes)) != MAMBA2_SCAN_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   st = count <= kFew ? run_squares<kFew>(grads, count, sz, workspace, s) : run_squares<kTable>(grads, count, sz, workspace, s);
   if (st != MAMBA2_SCAN_OK) return st;

@@ -214,7 +214,8 @@ typedef struct {
 /* Bytes of the workspace of both calls; 0 for tables that are refused. */
 size_t mamba2_grad_workspace_bytes(const mamba2_grad* grads, int count);
 
-/* *norm = sqrt(sum of squares of every element), fp32. */
+/* *norm = sqrt(sum of squares of every element), fp32.  The gradients may
+ * overlap one another, but not norm or the workspace (MAMBA2_SCAN_EOVERLAP). */
 int mamba2_grad_norm(const mamba2_grad* grads, int count, float* norm,
                      void* workspace, size_t workspace_bytes, void* stream);
 

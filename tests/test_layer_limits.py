@@ -1,6 +1,8 @@
 """Limits of the selective layer's calls (CPU): every call below is refused before anything is launched."""
 from __future__ import annotations
 
+import ctypes
+
 import pytest
 import torch
 
@@ -87,3 +89,19 @@ def test_a_refused_stream_leaves_the_current_device(monkeypatch):
         with layer._On(torch.device("cuda:1"), types.SimpleNamespace(device=torch.device("cuda:2"))):
             pass
     assert current[0] == 0
+
+
+class Grad(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_longlong), ("type", ctypes.c_int)]
+
+
+def test_norm_and_workspace_over_a_gradient(L):
+    t = (Grad * 3)(Grad(P, None, 100, 0), Grad(None, None, 0, 0), Grad(P + 4096, None, 8, 1))     # 400 and 16 bytes
+    need = L.mamba2_grad_workspace_bytes(t, 3)
+    call = lambda norm, ws, n=need: L.mamba2_grad_norm(t, 3, norm, ws, n, None)
+    far = P + (1 << 20)
+    for norm in (P, P + 396, P + 4096, P + 4108):
+        assert call(norm, far) == -8, norm - P
+    for ws, n in ((P, need), (P + 384, need), (P - need + 16, need), (P + 4096, need), (P - 4096, 4112), (P - 64, 8192)):
+        assert call(far, ws, n) == -8, ws - P
+    assert call(far, far) == -8 == call(far + need - 4, far)
