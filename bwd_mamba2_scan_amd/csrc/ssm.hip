@@ -72,7 +72,8 @@ __global__ __launch_bounds__(NW * 64, sizeof(T) == 2 ? 2 : NB == 4 ? 1 : 2) void
   const T* bp = seq_ptr<const T>(a.B, u.seq, u.row0, packed) + h / a.ratio * a.states;
   const T* cp = seq_ptr<const T>(a.C, u.seq, u.row0, packed) + h / a.ratio * a.states;
   T* yp = seq_ptr<T>(a.y, u.seq, u.row0, packed) + h * a.width + p0;
-  const float A = a.A[h], bias = a.bias != nullptr ? a.bias[h] : 0.0f, D = a.D != nullptr ? a.D[h] : 0.0f;
+  const double rate = decay_rate(a.A[h]);
+  const float bias = a.bias != nullptr ? a.bias[h] : 0.0f, D = a.D != nullptr ? a.D[h] : 0.0f;
 
   State<NB, true> st;
   st.init(a.width, p0, wave);
@@ -98,7 +99,7 @@ __global__ __launch_bounds__(NW * 64, sizeof(T) == 2 ? 2 : NB == 4 ? 1 : 2) void
   float raw = 0.0f;
   const auto fetch_raw = [&](int t) { raw = load_raw(a, step_rsrc(a, u, packed, t, min(end - t, kTok)), h); };
   const auto prepare = [&](Decays& dc, int t) {
-    make_decays(dc, lane < end - t ? step_of(a, raw, bias) : 0.0f, A);
+    make_decays(dc, lane < end - t ? step_of(a, raw, bias) : 0.0f, rate);
   };
   if (u.t0 < end) {
     fetch(u.t0);
@@ -243,7 +244,7 @@ __global__ __launch_bounds__(kStepThreads) void ssm_step_kernel(StepArgs sa) {
   const float raw = a.dt_bf16 ? static_cast<float>(static_cast<const bf16*>(a.dt.data)[di])
                               : static_cast<const float*>(a.dt.data)[di];
   const float d = step_of(a, raw, a.bias != nullptr ? a.bias[h] : 0.0f);
-  const float decay = exp2_of(log_decay(d, a.A[h]));
+  const float decay = exp2_of(log_decay(d, decay_rate(a.A[h])));
   const T* xp = static_cast<const T*>(a.x.data) + seq * a.x.batch_stride + h * a.width + 4 * q;
   float x[4], xd[4];
 #pragma unroll

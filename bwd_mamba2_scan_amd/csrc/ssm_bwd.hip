@@ -272,7 +272,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
   const auto prepare = [&](int h, int k) {
     const int lane = lane_anew();
     const float bias = a.bias != nullptr ? a.bias[h] : 0.0f;
-    make_decays(s.dc[k], lane < rows ? step_of(a, raw, bias) : 0.0f, a.A[h]);
+    make_decays(s.dc[k], lane < rows ? step_of(a, raw, bias) : 0.0f, decay_rate(a.A[h]));
     s.slope[k][lane] = a.softplus ? __builtin_amdgcn_rcpf(1.0f + expf(-(raw + bias))) : 1.0f;
   };
   // The step sizes' gradients of a head whose sums are complete: a token per lane.

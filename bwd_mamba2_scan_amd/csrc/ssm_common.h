@@ -383,20 +383,24 @@ struct DecaysOf {
 };
 typedef DecaysOf<false> Decays;
 
+// log2(e) A, finite, so that a step of 0 decays nothing even where A is infinite;
+// a NaN stays one.
+__device__ __forceinline__ double decay_rate(float A) {
+  const double r = static_cast<double>(A) * 1.4426950408889634074;
+  return A == A ? fmin(fmax(r, -1e300), 1e300) : r;
+}
 // log2 of a token's decay.  One that underflows any fp32 (2^-1100) is held there,
-// so that later differences keep their bits.  A step of 0 decays nothing even
-// where A is infinite; a NaN of either stays one.
-__device__ __forceinline__ double log_decay(float d, float A) {
-  const double l = static_cast<double>(d) * static_cast<double>(A) * 1.4426950408889634074;
-  if (d == 0.0f && A == A) return 0.0;
+// so that later differences keep their bits; a NaN stays one.
+__device__ __forceinline__ double log_decay(float d, double rate) {
+  const double l = static_cast<double>(d) * rate;
   return l < -1100.0 ? -1100.0 : l;
 }
 
 // One wave; lane t has token t.
 template <bool LEFT>
-__device__ __forceinline__ void make_decays(DecaysOf<LEFT>& dc, float d, float A) {
+__device__ __forceinline__ void make_decays(DecaysOf<LEFT>& dc, float d, double rate) {
   const int t = threadIdx.x & 63;
-  const double c = scan64(log_decay(d, A));
+  const double c = scan64(log_decay(d, rate));
   const long cbits = __builtin_bit_cast(long, c);
   const double end = __builtin_bit_cast(
       double, (static_cast<long>(__builtin_amdgcn_readlane(static_cast<int>(cbits >> 32), 63)) << 32) |
@@ -598,7 +602,8 @@ __device__ __forceinline__ void walk(const SsmArgs& a, const Walk& w, WalkLds<T,
   const long head = static_cast<long>(a.states) * a.width;
   const T* vp = seq_ptr<const T>(w.v, u.seq, u.row0, packed) + h * a.width + p0;
   const T* mp = seq_ptr<const T>(w.m, u.seq, u.row0, packed) + h / a.ratio * a.states;
-  const float A = a.A[h], bias = a.bias != nullptr ? a.bias[h] : 0.0f;
+  const double rate = decay_rate(a.A[h]);
+  const float bias = a.bias != nullptr ? a.bias[h] : 0.0f;
   const long at = static_cast<long>(unit) * a.heads + h;
   const long of_seq = (static_cast<long>(u.seq) * a.heads + h) * head;
   State<NB, false> st;
@@ -628,7 +633,7 @@ __device__ __forceinline__ void walk(const SsmArgs& a, const Walk& w, WalkLds<T,
   float raw = 0.0f;
   const auto fetch_raw = [&](int t) { raw = load_raw(a, step_rsrc(a, u, packed, t, min(end - t, kTok)), h); };
   const auto prepare = [&](Decays& dc, int t) {
-    make_decays(dc, lane < end - t ? step_of(a, raw, bias) : 0.0f, A);
+    make_decays(dc, lane < end - t ? step_of(a, raw, bias) : 0.0f, rate);
   };
   if (steps > 0) {
     fetch(token(0));
