@@ -46,8 +46,8 @@ def _run(cmd: list[str], verbose: bool) -> None:
     out = "\n".join(ln for ln in proc.stdout.splitlines() if noise not in ln)
     if proc.returncode != 0:
         raise RuntimeError(f"hipcc failed ({proc.returncode}):\n{out}")
-    if out.strip() and verbose:
-        print(out, flush=True)
+    if out.strip():  # warnings
+        print(out, file=sys.stderr, flush=True)
 
 
 def build(verbose: bool = False) -> str:

@@ -49,7 +49,7 @@ struct FwdLds {
 };
 
 template <class T, int NB, int NW>
-__global__ __launch_bounds__(NW * 64, sizeof(T) == 2 ? 2 : NB == 4 ? 1 : 2) void ssm_fwd_kernel(SsmArgs a, Walk w) {
+__global__ __launch_bounds__(NW * 64, simd_waves(sizeof(FwdLds<T, NB, NW>), NW)) void ssm_fwd_kernel(SsmArgs a, Walk w) {
   typedef FwdLds<T, NB, NW> L;
   __shared__ L s;
   constexpr int kThreads = NW * 64;
@@ -197,7 +197,7 @@ __global__ __launch_bounds__(NW * 64, sizeof(T) == 2 ? 2 : NB == 4 ? 1 : 2) void
 // Summary pass of the segments; see walk().  43 us where the forward takes 87:
 // it reads x and B (52 MB) and has no scores to compute.
 template <class T, int NB, int NW>
-__global__ __launch_bounds__(NW * 64, 2) void ssm_summary_kernel(SsmArgs a, Walk w) {
+__global__ __launch_bounds__(NW * 64, simd_waves(sizeof(WalkLds<T, NB, NW>), NW)) void ssm_summary_kernel(SsmArgs a, Walk w) {
   __shared__ WalkLds<T, NB, NW> s;
   walk<T, NB, NW, false>(a, w, s);
 }

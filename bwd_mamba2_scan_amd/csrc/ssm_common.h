@@ -553,6 +553,10 @@ struct WalkLds {
   alignas(16) Decays dc[2];
 };
 
+// Waves on a SIMD that registers are allotted for: two, unless LDS holds no more
+// than one for each of a CU's four.
+constexpr int simd_waves(size_t lds, int nw) { return 160 * 1024 / lds * nw > 4 ? 2 : 1; }
+
 // The state a segment starts from: the sequence's first one, brought through
 // the segments before it (in the pass's direction), whose own contributions
 // lie in the place of the segment behind each.  With few segments every one
