@@ -151,18 +151,8 @@ struct StateTile {
     for (int i = 0; i < kN; ++i) {
       const int t = wave_id() + i * kWaves;
       if (kAll % kWaves != 0 && t >= kAll) continue;
-      T* p = &st[0][L::State::at(t % kTiles * 16 + (lane & 15), t / kTiles * 16 + 4 * (lane >> 4))];
-      v4f r = v[i];
-#pragma unroll
-      for (int z = 0; z < L::kTerms; ++z) {
-        if constexpr (L::kTerms > 1) {
-          const unsigned a = pack_bf16(r[0], r[1]), b = pack_bf16(r[2], r[3]);
-          *reinterpret_cast<v2u*>(p + z * L::State::kSize) = v2u{a, b};
-          r = v4f{r[0] - low_of(a), r[1] - high_of(a), r[2] - low_of(b), r[3] - high_of(b)};
-        } else {
-          quad_put(p, r);
-        }
-      }
+      quad_put_parts<L::kTerms>(&st[0][L::State::at(t % kTiles * 16 + (lane & 15), t / kTiles * 16 + 4 * (lane >> 4))],
+                                L::State::kSize, v[i]);
     }
   }
 };

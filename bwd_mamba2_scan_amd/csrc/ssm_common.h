@@ -271,6 +271,22 @@ __device__ __forceinline__ void quad_put(bf16* p, v4f v) {
   *reinterpret_cast<v2u*>(p) = v2u{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
 }
 
+// The parts of split_of, one `plane` elements behind the other.
+template <int TERMS>
+__device__ __forceinline__ void quad_put_parts(bf16* p, int plane, v4f v) {
+#pragma unroll
+  for (int t = 0; t < TERMS; ++t) {
+    const unsigned a = pack_bf16(v[0], v[1]), b = pack_bf16(v[2], v[3]);
+    *reinterpret_cast<v2u*>(p + t * plane) = v2u{a, b};
+    v = v4f{v[0] - low_of(a), v[1] - high_of(a), v[2] - low_of(b), v[3] - high_of(b)};
+  }
+}
+template <int TERMS>
+__device__ __forceinline__ void quad_put_parts(float* p, int, v4f v) {
+  static_assert(TERMS == 1, "fp32 is whole in one part");
+  quad_put(p, v);
+}
+
 // ------------------------------------------------------------------ decays
 // v + the lane's DPP neighbour, where the DPP control reaches one (else v).
 template <int CTRL, int ROWS>

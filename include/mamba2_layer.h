@@ -28,7 +28,8 @@
  *
  * Types: activations are fp32 or bf16 (MAMBA2_F32, MAMBA2_BF16); weights,
  * their gradients and the scan's states are fp32.  bf16 is storage: products
- * accumulate in fp32.
+ * accumulate in fp32, and an operand that the call itself computes goes into
+ * them with 16 bits or more.
  */
 #ifndef MAMBA2_LAYER_H
 #define MAMBA2_LAYER_H

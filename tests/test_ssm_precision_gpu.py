@@ -1,0 +1,54 @@
+"""bf16 scans give what the formulas give, rounded once: no term loses more than 2^-16 on its way.  On an MI355X.
+
+The bound of a result is half a step of bf16 at that very value (not the most
+that a value's binade allows), beside the roundings of fp32 sums and 2^-16 for
+each operand that goes into a product in two bf16 parts.  The inputs have both
+signs, so the terms cancel and what they lose shows.
+"""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import bwd_mamba2_scan_amd as m2
+from oracle import selective_oracle as orc
+from tests.selective import TINY, U, scan_inputs, scan_roundings, to
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+TWO = 2.0 ** -16    # what an operand in two parts leaves out
+
+# (batch, L, H, P, G, N)
+CASES = [(2, 200, 7, 64, 1, 128), (1, 130, 4, 24, 2, 40), (1, 720, 2, 128, 1, 64), (2, 100, 3, 16, 1, 16)]
+
+
+def _half_step(v):
+    """Half the distance of bf16 numbers at |v|."""
+    return torch.exp2(torch.floor(torch.log2(v.abs().clamp_min(2.0 ** -126))) - 8)
+
+
+def _within(got, want, size, n, parts, what):
+    off = (n + 1.02 * parts * TWO) * size + TINY
+    over = (got.cpu().double() - want).abs() - off - _half_step(want.abs() + off)
+    assert float(over.max()) <= 0, (what, float(over.max()), int((over > 0).sum()), over.numel())
+
+
+def _run(case):
+    batch, L, H, P, G, N = case
+    p = scan_inputs(sum(case), (batch, L), batch, H, P, G, N, "bf16", "f32")
+    d = to(p, DEV)
+    args = tuple(d[k] for k in ("x", "dt", "A", "B", "C"))
+    kw = dict(D=d["D"], dt_bias=d["dt_bias"], initial_state=d["state"])
+    n = scan_roundings(L, P, N) * U
+    for row in range(batch):
+        cpu = tuple(p[k][row] if k in ("x", "dt", "B", "C") else p[k] for k in ("x", "dt", "A", "B", "C", "D", "dt_bias"))
+        yield d, args, kw, n, row, cpu + (True, p["state"][row]), (p["d_y"][row], p["d_final"][row])
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
+def test_forward(case):
+    print("precision of y", case, flush=True)
+    for d, args, kw, n, row, cpu, _ in _run(case):
+        y, _ = m2.ssm_fwd(*args, **kw)
+        # the scores, or the state, in two parts
+        _within(y[row], orc.scan(*cpu)[0], orc.scan(*cpu, absolute=True)[0], n, 1, "y")
