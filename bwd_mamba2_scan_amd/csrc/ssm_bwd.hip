@@ -95,7 +95,9 @@ struct BwdLds {
   static constexpr int kN = NB * 32;
   static constexpr int kP = PT * 16 < 32 ? 32 : PT * 16;  // a product over the columns takes 32 at a time
   static constexpr int kTerms = sizeof(T) == 2 ? 3 : 1;
-  static constexpr int kQ = sizeof(T) == 2 ? 2 : 1;  // parts of Q: with one, its rounding shows in d_B and d_C (2.4e-3 against 1.7e-3)
+  // Parts of P and Q: with one, Q's rounding shows in d_B and d_C (2.4e-3 against
+  // 1.7e-3) and P's in d_x (1.89e-3 against 1.66e-3, d_x's own rounding).
+  static constexpr int kParts = sizeof(T) == 2 ? 2 : 1;
   static constexpr int kRows = sizeof(T) == 2 || kN < 64 ? kN : 64;  // state rows staged at a time
   // b and c are read by rows and, in fours of neighbouring ones, by columns:
   // 32 bytes of padding put four rows of 128 bf16 into different banks
@@ -416,21 +418,24 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
             if (g == 0) sum.direct[mine] = slice == 0 ? direct : sum.direct[mine] + direct;
             skip = sum64(skip);
             if (lane == 0) sum.skip[wave] = slice == 0 ? skip : sum.skip[wave] + skip;
-            // P goes in with 8 bits, as d_x comes out: one term among the three of d_x.
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               if (2 * k + 1 < wave) continue;
-              const Frag<T> pf = split_tiles<T, 1>(pw[2 * k], pw[2 * k + 1]).f[0];
-              const auto qf = split_tiles<T, L::kQ>(qw[2 * k], qw[2 * k + 1]);
+              const auto pf = split_tiles<T, L::kParts>(pw[2 * k], pw[2 * k + 1]);
+              const auto qf = split_tiles<T, L::kParts>(qw[2 * k], qw[2 * k + 1]);
 #pragma unroll
-              for (int p = 0; p < kPt; ++p) mma(dx[p], frag_col_result(s.dy, L::ldp, k * 32, p * 16, ln), pf);
+              for (int p = 0; p < kPt; ++p) {
+                const Frag<T> yf = frag_col_result(s.dy, L::ldp, k * 32, p * 16, ln);
+#pragma unroll
+                for (int z = 0; z < L::kParts; ++z) mma(dx[p], yf, pf.f[z]);
+              }
 #pragma unroll
               for (int n0 = 0; n0 < 2 * NB; n0 += kBatch) {
                 Frag<T> cf[kBatch];
 #pragma unroll
                 for (int n = 0; n < kBatch; ++n) cf[n] = frag_col_result(s.c, L::ldn, k * 32, (n0 + n) * 16, ln);
 #pragma unroll
-                for (int z = 0; z < L::kQ; ++z)
+                for (int z = 0; z < L::kParts; ++z)
 #pragma unroll
                   for (int n = 0; n < kBatch; ++n) mma(acc[n0 + n], cf[n], qf.f[z]);
               }
@@ -503,14 +508,14 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               if (2 * k > wave) continue;
-              const auto qf = split_tiles<T, L::kQ>(qw[2 * k], qw[2 * k + 1]);
+              const auto qf = split_tiles<T, L::kParts>(qw[2 * k], qw[2 * k + 1]);
 #pragma unroll
               for (int n0 = 0; n0 < 2 * NB; n0 += kBatch) {
                 Frag<T> cf[kBatch];
 #pragma unroll
                 for (int n = 0; n < kBatch; ++n) cf[n] = frag_col_result(s.b, L::ldn, k * 32, (n0 + n) * 16, ln);
 #pragma unroll
-                for (int z = 0; z < L::kQ; ++z)
+                for (int z = 0; z < L::kParts; ++z)
 #pragma unroll
                   for (int n = 0; n < kBatch; ++n) mma(acc[n0 + n], cf[n], qf.f[z]);
               }

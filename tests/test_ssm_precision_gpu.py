@@ -52,3 +52,16 @@ def test_forward(case):
         y, _ = m2.ssm_fwd(*args, **kw)
         # the scores, or the state, in two parts
         _within(y[row], orc.scan(*cpu)[0], orc.scan(*cpu, absolute=True)[0], n, 1, "y")
+
+
+def _backward(case, name, parts):
+    print(f"precision of {name}", case, flush=True)
+    for d, args, kw, n, row, cpu, ups in _run(case):
+        g = m2.ssm_bwd(*args, d["d_y"], d_final_state=d["d_final"], **kw)
+        _within(g[name][row], orc.scan_grads(*cpu, *ups)[name], orc.scan_grads(*cpu, *ups, absolute=True)[name], n, parts,
+                name)
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
+def test_d_x(case):
+    _backward(case, "d_x", 1)       # P
