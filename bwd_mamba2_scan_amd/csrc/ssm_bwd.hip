@@ -95,8 +95,9 @@ struct BwdLds {
   static constexpr int kN = NB * 32;
   static constexpr int kP = PT * 16 < 32 ? 32 : PT * 16;  // a product over the columns takes 32 at a time
   static constexpr int kTerms = sizeof(T) == 2 ? 3 : 1;
-  // Parts of P and Q: with one, Q's rounding shows in d_B and d_C (2.4e-3 against
-  // 1.7e-3) and P's in d_x (1.89e-3 against 1.66e-3, d_x's own rounding).
+  // Parts of P and Q, and of the gradient's state in d_B: with one, Q's rounding
+  // shows in d_B and d_C (2.4e-3 against 1.66e-3, their own rounding), P's in d_x
+  // (1.89e-3), the state's in d_B (1.71e-3).
   static constexpr int kParts = sizeof(T) == 2 ? 2 : 1;
   static constexpr int kRows = sizeof(T) == 2 || kN < 64 ? kN : 64;  // state rows staged at a time
   // b and c are read by rows and, in fours of neighbouring ones, by columns:
@@ -475,7 +476,9 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
 #pragma unroll
             for (int k = 0; k < kKp; ++k)
 #pragma unroll
-              for (int n = 0; n < kSide; ++n) mma(o[n], L::State::by_row(s.st[1][0], (n0 + n) * 16, k * 32, ln), xf[k]);
+              for (int z = 0; z < L::kParts; ++z)
+#pragma unroll
+                for (int n = 0; n < kSide; ++n) mma(o[n], L::State::by_row(s.st[1][z], (n0 + n) * 16, k * 32, ln), xf[k]);
 #pragma unroll
             for (int n = 0; n < kSide; ++n)
 #pragma unroll

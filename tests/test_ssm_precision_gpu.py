@@ -65,3 +65,9 @@ def _backward(case, name, parts):
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
 def test_d_x(case):
     _backward(case, "d_x", 1)       # P
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
+def test_d_B_and_d_C(case):
+    _backward(case, "d_B", 1)       # Q, or the gradient's state
+    _backward(case, "d_C", 1)       # Q
