@@ -52,8 +52,10 @@ struct FwdLds {
   alignas(16) Decays dc[2];
 };
 
+// Up to 64 states three waves fit a SIMD (24 heads of 64, 64 states, 32768 tokens:
+// 127 us a call, with two waves 160); of 128 states three would spill.
 template <class T, int NB, int NW>
-__global__ __launch_bounds__(NW * 64, simd_waves(sizeof(FwdLds<T, NB, NW>), NW)) void ssm_fwd_kernel(SsmArgs a, Walk w) {
+__global__ __launch_bounds__(NW * 64, simd_waves(sizeof(FwdLds<T, NB, NW>), NW, NB < 4 ? 3 : 2)) void ssm_fwd_kernel(SsmArgs a, Walk w) {
   typedef FwdLds<T, NB, NW> L;
   __shared__ L s;
   constexpr int kThreads = NW * 64;
@@ -204,7 +206,7 @@ __global__ __launch_bounds__(NW * 64, simd_waves(sizeof(FwdLds<T, NB, NW>), NW))
 // Summary pass of the segments; see walk().  43 us where the forward takes 87:
 // it reads x and B (52 MB) and has no scores to compute.
 template <class T, int NB, int NW>
-__global__ __launch_bounds__(NW * 64, simd_waves(sizeof(WalkLds<T, NB, NW>), NW)) void ssm_summary_kernel(SsmArgs a, Walk w) {
+__global__ __launch_bounds__(NW * 64, simd_waves(sizeof(WalkLds<T, NB, NW>), NW, 2)) void ssm_summary_kernel(SsmArgs a, Walk w) {
   __shared__ WalkLds<T, NB, NW> s;
   walk<T, NB, NW, false>(a, w, s);
 }

@@ -51,12 +51,12 @@ struct Walks {  // forward, reverse: side by side in one launch
 };
 
 template <class T, int NB, int NW>
-__global__ __launch_bounds__(NW * 64, simd_waves(sizeof(WalkLds<T, NB, NW>), NW)) void ssm_walk_kernel(SsmArgs a, Walks ws) {
+__global__ __launch_bounds__(NW * 64, simd_waves(sizeof(WalkLds<T, NB, NW>), NW, 2)) void ssm_walk_kernel(SsmArgs a, Walks ws) {
   __shared__ WalkLds<T, NB, NW> s;
   walk<T, NB, NW, true>(a, ws.w[blockIdx.y], s);
 }
 template <class T, int NB, int NW>
-__global__ __launch_bounds__(NW * 64, simd_waves(sizeof(WalkLds<T, NB, NW>), NW)) void ssm_walk_summary_kernel(SsmArgs a, Walks ws) {
+__global__ __launch_bounds__(NW * 64, simd_waves(sizeof(WalkLds<T, NB, NW>), NW, 2)) void ssm_walk_summary_kernel(SsmArgs a, Walks ws) {
   __shared__ WalkLds<T, NB, NW> s;
   walk<T, NB, NW, false>(a, ws.w[blockIdx.y], s);
 }

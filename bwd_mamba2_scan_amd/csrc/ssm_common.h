@@ -517,12 +517,13 @@ struct State {
   }
   // S = total S + M^T (coef_s v_s); vf holds v.  With bf16 the scaled v goes
   // in whole, in three parts: M is exact, so the state keeps fp32's precision.
+  // A step's products are added up by themselves: on top of the state, each
+  // would round, or drop bits, at the state's size.
   template <class T>
   __device__ __forceinline__ void advance(float total, const float* coef, const T* m, int ldn,
                                           const Frag<T> (&vf)[2]) {
     const int g = (threadIdx.x & 63) >> 4;
-#pragma unroll
-    for (int n = 0; n < 2 * NB; ++n) st[n] *= total;
+    Split<T, kExact<T>> parts[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       float v[8];
@@ -530,11 +531,17 @@ struct State {
       const v4f c0 = c[0], c1 = c[1];
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = frag_get(vf[k], j) * (j < 4 ? c0[j & 3] : c1[j & 3]);
-      const auto parts = split_of<T, kExact<T>>(v);
-      // four tiles at a time: a product waits for the last one on the same tile
-      constexpr int kTiles = 2 * NB < 4 ? 2 * NB : 4;
+      parts[k] = split_of<T, kExact<T>>(v);
+    }
+    // four tiles at a time: a product waits for the last one on the same tile
+    constexpr int kTiles = 2 * NB < 4 ? 2 * NB : 4;
 #pragma unroll
-      for (int n = 0; n < 2 * NB; n += kTiles) {
+    for (int n = 0; n < 2 * NB; n += kTiles) {
+      v4f add[kTiles];
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) add[i] = v4f{0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
         Frag<T> mf[kTiles];
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) mf[i] = frag_col(m, ldn, k * 32, (n + i) * 16);
@@ -542,9 +549,11 @@ struct State {
         for (int z = 0; z < kExact<T>; ++z)
 #pragma unroll
           for (int i = 0; i < kTiles; ++i) {
-            if constexpr (COLS) mma(st[n + i], mf[i], parts.f[z]); else mma(st[n + i], parts.f[z], mf[i]);
+            if constexpr (COLS) mma(add[i], mf[i], parts[k].f[z]); else mma(add[i], parts[k].f[z], mf[i]);
           }
       }
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) st[n + i] = st[n + i] * total + add[i];
     }
   }
 };
@@ -569,9 +578,12 @@ struct WalkLds {
   alignas(16) Decays dc[2];
 };
 
-// Waves on a SIMD that registers are allotted for: two, unless LDS holds no more
-// than one for each of a CU's four.
-constexpr int simd_waves(size_t lds, int nw) { return 160 * 1024 / lds * nw > 4 ? 2 : 1; }
+// Waves on a SIMD that registers are allotted for: as many as LDS holds of a CU's
+// four, up to `most`.
+constexpr int simd_waves(size_t lds, int nw, int most) {
+  const int n = (160 * 1024 / static_cast<int>(lds) * nw + 3) / 4;
+  return n < most ? n : most;
+}
 
 // The state a segment starts from: the sequence's first one, brought through
 // the segments before it (in the pass's direction), whose own contributions

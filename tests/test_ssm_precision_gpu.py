@@ -71,3 +71,20 @@ def test_d_x(case):
 def test_d_B_and_d_C(case):
     _backward(case, "d_B", 1)       # Q, or the gradient's state
     _backward(case, "d_C", 1)       # Q
+
+
+@pytest.mark.parametrize("typ,tiny", [("f32", 2.0 ** -27), ("bf16", 1.875 * 2.0 ** -30)])
+def test_small_terms_are_not_lost_in_a_large_state(typ, tiny):
+    """A state of 1 that keeps, and terms that are below its half step alone but not 64 of them together: one rounding a
+    step (2^-24) is all that the state may be off by, in the scan and in its gradient's reverse recurrence."""
+    L, steps, H, P, N = 640, 10, 2, 16, 24
+    t = torch.float32 if typ == "f32" else torch.bfloat16
+    print("small terms", typ, flush=True)
+    full = lambda v, *s, dtype=t: torch.full(s, v, dtype=dtype, device=DEV)
+    x, one, dt = full(tiny, 1, L, H, P), full(1.0, 1, L, 1, N), full(1.0, 1, L, H)
+    A, state = full(0.0, H, dtype=torch.float32), full(1.0, 1, H, N, P, dtype=torch.float32)
+    _, final = m2.ssm_fwd(x, dt, A, one, one, softplus=False, initial_state=state, want_final_state=True)
+    g = m2.ssm_bwd(x, dt, A, one, one, x, softplus=False, initial_state=state, d_final_state=state)
+    want = 1.0 + L * tiny
+    for name, got in (("final", final), ("d_initial_state", g["d_initial_state"])):
+        assert float((got.double() - want).abs().max()) <= 1.01 * steps * U, name
