@@ -365,21 +365,28 @@ int waves_of(int width) { return width <= 16 ? 1 : width <= 32 ? 2 : 4; }
 // Tokens per segment.  A work-group walks its tokens one step after another,
 // so short of one or two rounds of work-groups the tokens are cut into
 // segments.  Each costs a second reading of x and B and a state, and all of
-// them two launches, so no more than needed, and none where a few steps do.
+// them one launch or two, so no more than needed, and none where a few steps do:
+// four in the forward (8 heads of 64, 128 states, bf16: 4 steps 17.5 us, cut 18.7;
+// 6 steps 23.5, cut 19.6; 10 steps 35.7, cut 21.6), ten in the backward, where the
+// walk is a part of the time (8 steps 47.6 us, cut 47.8; 10 steps 51.9, cut 50.3;
+// 16 heads of 128: 67.5, cut 70.4; 13 steps, 24 heads, 64 states: 59.9, cut 58.2).
+// The lengths of packed sequences are not known here: up to ten steps of rows
+// are taken to be shared out evenly (10 of 64 tokens: 9.9 us, cut 12.1).
 // A CU holds two work-groups with up to 128 states (LDS) and three with up to 64
 // (registers); one work-group more than the rounds hold costs a round (24 heads,
 // 64 states: 1032 work-groups 109 us, 768 89 us).  Packed sequences' ends add units
 // by themselves: half as many segments again, for their unequal lengths, took
 // 0.93 to 1.28 times as long over seven mixes of 1 to 32 prompts.
-int segment_tokens(const mamba2_seqs& q, const mamba2_ssm_dims& d) {
-  constexpr int kFewSteps = 10;
+int segment_tokens(const mamba2_seqs& q, const mamba2_ssm_dims& d, bool bwd) {
+  constexpr int kFewSteps = 4, kFewStepsBwd = 10;
   const bool packed = q.offsets != nullptr;
   const long work = static_cast<long>(kCUs) * (d.states > 64 ? 2 : 3);
   const long slices = (d.width + waves_of(d.width) * 16 - 1) / (waves_of(d.width) * 16);
   const long lanes = static_cast<long>(d.heads) * slices * (packed ? 1 : q.batch);
   const long want = work / lanes > 1 ? work / lanes : 1;  // segments, over all rows of a packed call
   long seg = (q.length + want - 1) / want;
-  if (q.length <= kFewSteps * kTok) seg = q.length;
+  const long few = (bwd ? kFewStepsBwd : packed ? min(static_cast<long>(kFewSteps) * q.batch, 10L) : kFewSteps) * kTok;
+  if (q.length <= few) seg = q.length;
   seg = (seg + kTok - 1) / kTok * kTok;
   return static_cast<int>(seg < 2 * kTok ? 2 * kTok : seg);
 }
@@ -394,11 +401,11 @@ int fold_segments(const mamba2_seqs& q, int seg) {
 }
 
 // check_dims, and that the passes over the segments can be launched.
-int check_scan(const mamba2_seqs& q, const mamba2_ssm_dims& d) {
+int check_scan(const mamba2_seqs& q, const mamba2_ssm_dims& d, bool bwd) {
   const int st = check_dims(q, d);
   if (st != MAMBA2_SCAN_OK) return st;
   const int nw = waves_of(d.width), slices = (d.width + nw * 16 - 1) / (nw * 16);
-  const long long units = unit_count(q, segment_tokens(q, d));
+  const long long units = unit_count(q, segment_tokens(q, d, bwd));
   return grid_ok(units * d.heads * slices, nw * 64) ? MAMBA2_SCAN_OK : MAMBA2_SCAN_EBADDIM;
 }
 
@@ -421,8 +428,8 @@ const char* mamba2_layer_strerror(int status) {
 }
 
 size_t mamba2_ssm_fwd_workspace_bytes(mamba2_seqs q, mamba2_ssm_dims d) {
-  if (check_scan(q, d) != MAMBA2_SCAN_OK) return 0;
-  const int seg = segment_tokens(q, d);
+  if (check_scan(q, d, false) != MAMBA2_SCAN_OK) return 0;
+  const int seg = segment_tokens(q, d, false);
   if (q.length <= seg) return 0;
   const size_t n = static_cast<size_t>(unit_count(q, seg)) * d.heads * (static_cast<size_t>(d.states) * d.width + 1);
   return (n * sizeof(float) + 15) / 16 * 16;
@@ -431,7 +438,7 @@ size_t mamba2_ssm_fwd_workspace_bytes(mamba2_seqs q, mamba2_ssm_dims d) {
 int mamba2_ssm_fwd(mamba2_seqs q, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows dt, const float* A, mamba2_rows B,
                    mamba2_rows C, const float* D, const float* dt_bias, const float* initial_state, mamba2_rows y,
                    float* final_state, void* workspace, size_t workspace_bytes, void* stream) {
-  int st = check_scan(q, d);
+  int st = check_scan(q, d, false);
   if (st != MAMBA2_SCAN_OK) return st;
   const size_t e = type_size(d.type);
   const long long xw = static_cast<long long>(d.heads) * d.width, bw = static_cast<long long>(d.groups) * d.states;
@@ -475,7 +482,7 @@ int mamba2_ssm_fwd(mamba2_seqs q, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows 
   a.dt_bf16 = d.dt_type == MAMBA2_BF16;
   const int nw = waves_of(d.width);
   a.slices = (d.width + nw * 16 - 1) / (nw * 16);
-  a.seg = segment_tokens(q, d);
+  a.seg = segment_tokens(q, d, false);
   a.units = static_cast<int>(unit_count(q, a.seg));
   a.fold = fold_segments(q, a.seg);
   Walk w = {};

@@ -657,12 +657,12 @@ struct Plan {
 size_t pad4(size_t n) { return (n + 3) / 4 * 4; }
 
 int make_plan(const mamba2_seqs& q, const mamba2_ssm_dims& d, Plan* p) {
-  const int st = check_scan(q, d);
+  const int st = check_scan(q, d, true);
   if (st != MAMBA2_SCAN_OK) return st;
   const size_t head = static_cast<size_t>(d.states) * d.width;
   p->nw = waves_of(d.width);
   p->slices = (d.width + p->nw * 16 - 1) / (p->nw * 16);
-  p->seg = segment_tokens(q, d);
+  p->seg = segment_tokens(q, d, true);
   p->units = static_cast<int>(unit_count(q, p->seg));
   p->steps = static_cast<int>(unit_count(q, kTok));
   p->segments = q.length > p->seg;

@@ -760,11 +760,11 @@ __device__ __forceinline__ void carry(const SsmArgs& a, const Walk& w, int seq, 
 
 // Host side, in ssm.hip.
 int check_dims(const mamba2_seqs& q, const mamba2_ssm_dims& d);
-int check_scan(const mamba2_seqs& q, const mamba2_ssm_dims& d);
+int check_scan(const mamba2_seqs& q, const mamba2_ssm_dims& d, bool bwd);
 int check_vec_rows(const mamba2_rows& r, const mamba2_seqs& q, long long width, size_t elem);
 int check_step_rows(const mamba2_rows& r, const mamba2_seqs& q, const mamba2_ssm_dims& d);
 int waves_of(int width);
-int segment_tokens(const mamba2_seqs& q, const mamba2_ssm_dims& d);
+int segment_tokens(const mamba2_seqs& q, const mamba2_ssm_dims& d, bool bwd);
 int fold_segments(const mamba2_seqs& q, int seg);
 
 }  // namespace ssm

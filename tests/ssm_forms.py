@@ -18,12 +18,13 @@ def _units_of(length, run):
     return max(1, _ceil(length, run))
 
 
-def plan(length, batch, packed, H, P, G, N):
+def plan(length, batch, packed, H, P, G, N, bwd=True):
     """length: tokens of a sequence, or all rows of a packed call."""
     waves = 1 if P <= 16 else 2 if P <= 32 else 4
     slices = _ceil(P, 16 * waves)
     want = max(1, CUS * (2 if N > 64 else 3) // (H * slices * (1 if packed else batch)))
-    seg = length if length <= 10 * STEP else _ceil(length, want)
+    few = STEP * (10 if bwd else min(4 * batch, 10) if packed else 4)
+    seg = length if length <= few else _ceil(length, want)
     seg = max(2 * STEP, _ceil(seg, STEP) * STEP)
     units = lambda run: length // run + batch if packed else _units_of(length, run) * batch
     steps, ratio = units(STEP), H // G
@@ -35,10 +36,10 @@ def plan(length, batch, packed, H, P, G, N):
 
 def workspaces(length, batch, packed, H, P, G, N):
     """Bytes of the forward's and the backward's workspace."""
-    p = plan(length, batch, packed, H, P, G, N)
+    p, f = (plan(length, batch, packed, H, P, G, N, bwd) for bwd in (True, False))
     pad4 = lambda n: _ceil(n, 4) * 4
     states = p["units"] * H * N * P
-    fwd = _ceil((states + p["units"] * H) * 4, 16) * 16 if p["segments"] else 0
+    fwd = _ceil(f["units"] * H * (N * P + 1) * 4, 16) * 16 if f["segments"] else 0
     keep = p["steps"] * H * _ceil(P, 16) * _ceil(N, 16) * 256
     rows = length * (1 if packed else batch)
     part_bc = pad4(p["splits"] * rows * G * N) if p["splits"] > 1 else 0

@@ -77,7 +77,7 @@ def test_d_B_and_d_C(case):
 def test_small_terms_are_not_lost_in_a_large_state(typ, tiny):
     """A state of 1 that keeps, and terms that are below its half step alone but not 64 of them together: one rounding a
     step (2^-24) is all that the state may be off by, in the scan and in its gradient's reverse recurrence."""
-    L, steps, H, P, N = 640, 10, 2, 16, 24
+    L, steps, H, P, N = 640, 10, 800, 16, 24        # more heads than work-groups at a time: not cut into segments
     t = torch.float32 if typ == "f32" else torch.bfloat16
     print("small terms", typ, flush=True)
     full = lambda v, *s, dtype=t: torch.full(s, v, dtype=dtype, device=DEV)
