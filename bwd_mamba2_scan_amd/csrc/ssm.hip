@@ -85,7 +85,8 @@ __global__ __launch_bounds__(NW * 64, simd_waves(sizeof(FwdLds<T, NB, NW>), NW, 
   st.init(a.width, p0, wave);
   start_state(st, a, w, u, unit, h);
   // tiles above the diagonal that a 32-wide product step touches stay zero
-  for (int i = tid; i < L::kParts * kTok * L::ldw; i += kThreads) s.w[0][i] = static_cast<T>(0.0f);
+  constexpr int kQuads = sizeof(s.w) / sizeof(v4u);
+  for (int i = tid; i < kQuads; i += kThreads) reinterpret_cast<v4u*>(s.w[0])[i] = v4u{0, 0, 0, 0};
 
   const int end = min(u.t0 + a.seg, u.len);
   Tile<T, kTok, L::kN, kThreads> tb, tc;
