@@ -393,12 +393,16 @@ int segment_tokens(const mamba2_seqs& q, const mamba2_ssm_dims& d, bool bwd) {
 }
 
 // Few segments add up the states before them themselves: i of them read
-// i (i - 1) / 2 states where the carry pass reads and writes 2 (i - 1) in a
-// launch of its own (4 segments: 3 us more in the pass behind, 7 us less before
-// it).  How a packed call's rows are shared out is not known here; with
-// several sequences each is taken to have a part of them.
-int fold_segments(const mamba2_seqs& q, int seg) {
-  return units_of(q.length, seg) <= 8 * (q.offsets != nullptr ? min(q.batch, 3) : 1);
+// i (i - 1) / 2 states where the carry pass reads and writes 2 (i - 1) in a launch
+// of its own.  Forwards of 256 tokens a segment that fill the chip, us, added up
+// and carried: 128 states 4 segments 49.8 and 50.7, 6 segments 50.2 and 48.2, 16
+// segments 58 and 50; 64 states 46.3 and 48.0, 46.5 and 46.1, 51.8 and 48.6.
+// How a packed call's rows are shared out is not known here; with several
+// sequences each is taken to have a part of them (128 states, forwards, 3 alike
+// with 12 segments 60.8 and 63.8, 6 with 16 segments 61.5 and 67.3; 3 of which one
+// has nine tenths, 12 segments: 73 and 65).
+int fold_segments(const mamba2_seqs& q, const mamba2_ssm_dims& d, int seg) {
+  return units_of(q.length, seg) <= (d.states > 64 ? 4 : 6) * (q.offsets != nullptr ? min(q.batch, 4) : 1);
 }
 
 // check_dims, and that the passes over the segments can be launched.
@@ -485,7 +489,7 @@ int mamba2_ssm_fwd(mamba2_seqs q, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows 
   a.slices = (d.width + nw * 16 - 1) / (nw * 16);
   a.seg = segment_tokens(q, d, false);
   a.units = static_cast<int>(unit_count(q, a.seg));
-  a.fold = fold_segments(q, a.seg);
+  a.fold = fold_segments(q, d, a.seg);
   Walk w = {};
   w.v = x;
   w.m = B;

@@ -788,7 +788,7 @@ int mamba2_ssm_bwd(mamba2_seqs q, mamba2_ssm_dims d, mamba2_rows x, mamba2_rows 
   a.slices = c.p.slices;
   a.seg = c.p.seg;
   a.units = c.p.units;
-  a.fold = fold_segments(q, a.seg);
+  a.fold = fold_segments(q, d, a.seg);
 
   float* w = static_cast<float*>(workspace);
   const auto take = [&w](size_t n) {

@@ -765,6 +765,6 @@ int check_vec_rows(const mamba2_rows& r, const mamba2_seqs& q, long long width, 
 int check_step_rows(const mamba2_rows& r, const mamba2_seqs& q, const mamba2_ssm_dims& d);
 int waves_of(int width);
 int segment_tokens(const mamba2_seqs& q, const mamba2_ssm_dims& d, bool bwd);
-int fold_segments(const mamba2_seqs& q, int seg);
+int fold_segments(const mamba2_seqs& q, const mamba2_ssm_dims& d, int seg);
 
 }  // namespace ssm

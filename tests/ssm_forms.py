@@ -31,7 +31,7 @@ def plan(length, batch, packed, H, P, G, N, bwd=True):
     run = _ceil(ratio, min(ratio, _ceil(2 * CUS, steps * G)))
     return dict(waves=waves, slices=slices, seg=seg, units=units(seg), steps=steps, ratio=ratio, run=run,
                 splits=_ceil(ratio, run), segments=length > seg,
-                fold=_units_of(length, seg) <= 8 * (min(batch, 3) if packed else 1))
+                fold=_units_of(length, seg) <= (4 if N > 64 else 6) * (min(batch, 4) if packed else 1))
 
 
 def workspaces(length, batch, packed, H, P, G, N):
@@ -72,8 +72,13 @@ SEGMENTS = [
     ([0, 100, 2900, 2900, 3400], 2, 24, 2, 40, "f32", "f32"),   # packed, a carry over 22 segments
     ([5, 2905, 3300, 3301], 4, 64, 1, 72, "bf16", "bf16"),
     ([0, 1390], 2, 32, 1, 32, "bf16", "f32"),                   # one packed sequence
-    ([0, 2990, 2990, 3000], 2, 40, 1, 24, "f32", "f32"),        # packed, folded over 24 segments
+    ([0, 2990, 2990, 3000], 2, 40, 1, 24, "f32", "f32"),        # one long sequence among three
     ([0, 900, 1990], 3, 16, 3, 88, "bf16", "bf16"),
+    # from here on the segments add up the states before them
+    ([0, 2290, 2290, 2300], 2, 40, 1, 24, "f32", "f32"),        # 18 in one sequence
+    ([9, 700, 1020], 3, 64, 1, 96, "bf16", "bf16"),
+    ((2, 760), 4, 24, 2, 48, "bf16", "f32"),                    # six
+    ((1, 700), 3, 72, 1, 16, "f32", "f32"),
 ]
 
 
