@@ -253,7 +253,7 @@ __device__ __forceinline__ void pre_grad(const float (&w)[W][V], const float (&b
 // channel and tap; the blocks behind the units compute d_initial_state.  The
 // pre-activation is recomputed from x: a saved one would be another tensor to
 // read.  W - 1 tokens behind the run are loaded and differentiated again, 3 in
-// 32.
+// 36 at the size above.
 template <class T, int V, int W, bool SILU>
 __global__ __launch_bounds__(kLanes * kBwdWaves, sizeof(T) == 2 ? 4 : 2) void conv_bwd_kernel(ConvArgs a) {
   __shared__ float lds[kBwdWaves][kLanes * V];
