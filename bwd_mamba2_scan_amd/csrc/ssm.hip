@@ -367,19 +367,21 @@ int waves_of(int width) { return width <= 16 ? 1 : width <= 32 ? 2 : 4; }
 // so short of one or two rounds of work-groups the tokens are cut into
 // segments.  Each costs a second reading of x and B and a state, and all of
 // them one launch or two, so no more than needed, and none where a few steps do:
-// four in the forward (8 heads of 64, 128 states, bf16: 4 steps 17.5 us, cut 18.7;
-// 6 steps 23.5, cut 19.6; 10 steps 35.7, cut 21.6), ten in the backward, where the
-// walk is a part of the time (8 steps 47.6 us, cut 47.8; 10 steps 51.9, cut 50.3;
-// 16 heads of 128: 67.5, cut 70.4; 13 steps, 24 heads, 64 states: 59.9, cut 58.2).
-// The lengths of packed sequences are not known here: up to ten steps of rows
-// are taken to be shared out evenly (10 of 64 tokens: 9.9 us, cut 12.1).
+// six in the forward (8 heads of 64, 128 states, bf16, GPU time: 4 steps 17.5 us,
+// cut 18.7; 6 steps 22.6, cut 19.5; 10 steps 35.7, cut 21.6; but a launch more
+// costs the host 4 us: 6 steps and their backward, called from Python, 56 us, cut
+// 60, 7 steps 62, cut 60), ten in the backward, where the walk is a part of the
+// time (8 steps 47.6 us, cut 47.8; 10 steps 51.9, cut 50.3; 16 heads of 128: 67.5,
+// cut 70.4; 13 steps, 24 heads, 64 states: 59.9, cut 58.2).  The lengths of packed
+// sequences are not known here: up to ten steps of rows are taken to be shared out
+// evenly (10 of 64 tokens: 9.9 us, cut 12.1).
 // A CU holds two work-groups with up to 128 states (LDS) and three with up to 64
 // (registers); one work-group more than the rounds hold costs a round (24 heads,
 // 64 states: 1032 work-groups 109 us, 768 89 us).  Packed sequences' ends add units
 // by themselves: half as many segments again, for their unequal lengths, took
 // 0.93 to 1.28 times as long over seven mixes of 1 to 32 prompts.
 int segment_tokens(const mamba2_seqs& q, const mamba2_ssm_dims& d, bool bwd) {
-  constexpr int kFewSteps = 4, kFewStepsBwd = 10;
+  constexpr int kFewSteps = 6, kFewStepsBwd = 10;
   const bool packed = q.offsets != nullptr;
   const long work = static_cast<long>(kCUs) * (d.states > 64 ? 2 : 3);
   const long slices = (d.width + waves_of(d.width) * 16 - 1) / (waves_of(d.width) * 16);

@@ -23,7 +23,7 @@ def plan(length, batch, packed, H, P, G, N, bwd=True):
     waves = 1 if P <= 16 else 2 if P <= 32 else 4
     slices = _ceil(P, 16 * waves)
     want = max(1, CUS * (2 if N > 64 else 3) // (H * slices * (1 if packed else batch)))
-    few = STEP * (10 if bwd else min(4 * batch, 10) if packed else 4)
+    few = STEP * (10 if bwd else min(6 * batch, 10) if packed else 6)
     seg = length if length <= few else _ceil(length, want)
     seg = max(2 * STEP, _ceil(seg, STEP) * STEP)
     units = lambda run: length // run + batch if packed else _units_of(length, run) * batch

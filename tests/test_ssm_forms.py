@@ -11,7 +11,7 @@ from tests.ssm_forms import HEADS, SEGMENTS, plan, sizes, workspaces
 def test_rules_are_the_librarys():
     L = m2.lib()
     for length, batch, packed, (H, G), P, N in itertools.product(
-            (0, 1, 64, 65, 256, 257, 512, 513, 640, 641, 1400, 5000, 100000), (1, 2, 3, 7, 40, 520), (False, True),
+            (0, 1, 64, 65, 256, 257, 384, 385, 640, 641, 1400, 5000, 100000), (1, 2, 3, 7, 40, 520), (False, True),
             ((1, 1), (3, 1), (12, 2), (32, 1), (24, 8)), (8, 32, 72, 128), (8, 64, 72, 128)):
         q, d = Seqs(batch, length, 0x1000 if packed else None), SsmDims(1, 1, H, P, G, N, 1)
         args = length, batch, packed, H, P, G, N
