@@ -11,8 +11,8 @@
 // run of tokens with the last W - 1 inputs (and W pre-activation gradients) in
 // registers, so x and d_y are read once but for the W - 1 tokens where runs
 // meet.  The next tokens' loads are in flight while the last ones are computed.
-// At 4 x 4096 tokens of 4352 bf16 channels, 4 taps: forward 55 us, 285 MB at
-// 5.2 TB/s, what a large copy reaches; backward 94 us, 428 MB at 4.6 TB/s, the
+// At 4 x 4096 tokens of 4352 bf16 channels, 4 taps: forward 56 us, 285 MB at
+// 5.1 TB/s, what a large copy reaches; backward 95 us, 428 MB at 4.5 TB/s, the
 // vector units busy nearly as long: some 35 instructions an element, among them
 // an exponential and a reciprocal.
 #include "layer_common.h"
@@ -425,7 +425,7 @@ __global__ __launch_bounds__(kLanes * kBwdWaves, sizeof(T) == 2 ? 4 : 2) void co
   }
 }
 
-// 4.5 us for 128 units of 4352 channels and 5 sums each (11 MB), most of it the
+// 5.9 us for 116 units of 4352 channels and 5 sums each (10 MB), most of it the
 // launch.  Sums the units' partials of one (tap or bias, channel) in a fixed order:
 // lanes over channels, four waves over the units.
 __global__ __launch_bounds__(256) void conv_reduce_kernel(const float* partial, int units, int channels, int taps,

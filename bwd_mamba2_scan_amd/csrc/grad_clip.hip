@@ -8,8 +8,8 @@
 // Two launches per table of tensors: each block sums the squares of its piece
 // of one tensor into one partial; each block of the second launch adds up all
 // partials itself, in a fixed order, instead of waiting for a third launch.
-// 60 tensors of 617 MB in all: squares 97 us (6.3 TB/s: the last call's tail is in
-// the cache), scaling 226 us (5.4 TB/s); a large copy reaches 5.1.  Small calls
+// 60 tensors of 617 MB in all: squares 102 us (6.0 TB/s: the last call's tail is in
+// the cache), scaling 230 us (5.4 TB/s); a large copy reaches 5.1.  Small calls
 // take two launches' time, 4 and 5 us.
 // The number of blocks is held near kBlocks so that those partials stay few.
 // The second pass walks the pieces backwards: what the first pass read last

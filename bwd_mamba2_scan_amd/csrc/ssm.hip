@@ -18,10 +18,11 @@
 // the states so found.  Few segments carry by themselves (start_state).
 //
 // Measured at 4 x 4096 tokens, 32 heads of 64 columns, one group of 128 states,
-// bf16: summary 43 us, forward 87 us.  The bytes (164 MB) would take 32 us and
-// the products 17 us at this card's rates; what bounds both kernels is LDS,
-// whose pipes are busy 60 % of the forward's time, and the two barriers of a
-// step, which two work-groups on a CU hide for each other (matrix cores: 24 %).
+// bf16: summary 46 us, forward 100 us.  The forward's bytes (165 MB) would take
+// 32 us at a large copy's rate and its products keep the matrix cores busy 29 % of
+// the time; what bounds both kernels is LDS, whose pipes are busy 62 % of the
+// forward's time, and the barriers of a step, which two work-groups on a CU hide
+// for each other.
 #include "ssm_common.h"
 
 namespace {
@@ -204,8 +205,8 @@ __global__ __launch_bounds__(NW * 64, simd_waves(sizeof(FwdLds<T, NB, NW>), NW, 
     st.save(a.final_state + of_seq, a.width, a.states);
 }
 
-// Summary pass of the segments; see walk().  43 us where the forward takes 87:
-// it reads x and B (52 MB) and has no scores to compute.
+// Summary pass of the segments; see walk().  46 us where the forward takes 100:
+// it reads x and B (54 MB) and has no scores to compute.
 template <class T, int NB, int NW>
 __global__ __launch_bounds__(NW * 64, simd_waves(sizeof(WalkLds<T, NB, NW>), NW, 2)) void ssm_summary_kernel(SsmArgs a, Walk w) {
   __shared__ WalkLds<T, NB, NW> s;
@@ -219,7 +220,7 @@ __global__ __launch_bounds__(256) void ssm_carry_kernel(SsmArgs a, Walk w) { car
 // columns and walks the state's rows, so a row is read and written as 16-byte
 // accesses and y needs no sum across the lanes of a row.  Bound by HBM, the
 // fp32 state read and written once: 256 sequences of 32 heads, 128 x 64, 539 MB
-// in 97 us, 5.6 TB/s.  Two sequences of 24 heads take 4 us, a launch's time.
+// in 98 us, 5.5 TB/s.  Two sequences of 24 heads take 4 us, a launch's time.
 constexpr int kStepThreads = 256;
 
 struct StepArgs {

@@ -44,8 +44,8 @@ struct BwdArgs {
   int run;                 // heads per run
 };
 
-// The walk is bound by HBM: it writes the kept states, 537 MB, and reads 187 MB in
-// 125 us, 5.8 TB/s.  Its summaries take 58 us.
+// The walk is bound by HBM: it writes the kept states, 537 MB, and reads 179 MB in
+// 126 us, 5.7 TB/s.  Its summaries take 63 us.
 struct Walks {  // forward, reverse: side by side in one launch
   Walk w[2];
 };
@@ -125,8 +125,8 @@ struct BwdLds {
 // Rows of a [states][width] fp32 matrix slice in registers, then LDS, where a
 // bf16 product finds them whole, in three parts.  d_x and d_C would do with
 // two, but d_A and d_dt_bias, fp32 sums of terms of both signs, show the third:
-// 2e-7 of them against 7e-7, and 1.5e-6 over short sequences (for 40 of 287 us
-// at 4 x 4096 tokens, 32 heads of 64 columns, 128 states).
+// 2e-7 of them against 7e-7, and 1.5e-6 over short sequences (for 40 us at
+// 4 x 4096 tokens, 32 heads of 64 columns, 128 states).
 template <class T, int NB, int PT>
 struct StateTile {
   typedef BwdLds<T, NB, PT> L;
@@ -182,10 +182,10 @@ __device__ __forceinline__ void put_quad(Rsrc rs, int row_off, int c, int cols, 
   Quad<T>::store(rs, c < cols ? static_cast<unsigned>((row_off + c) * static_cast<int>(sizeof(T))) : kOutside, v);
 }
 
-// At 4 x 4096 tokens, 32 heads of 64 columns, 128 states, bf16: 287 us for 681 MB
-// read (the kept states 537 MB, in fp32) and 102 MB written.  The products would
-// take 73 us and the bytes 154 us; LDS is busy 43 % of the time, the matrix
-// cores 15 %, and half of the waves' time is waiting: for a head's states, which
+// At 4 x 4096 tokens, 32 heads of 64 columns, 128 states, bf16: 317 us (301 at
+// best) for 681 MB read (the kept states 537 MB, in fp32) and 103 MB written.  The
+// bytes would take 154 us; LDS is busy 43 % of the time, the matrix cores 16 %,
+// and half of the waves' time is waiting: for a head's states, which
 // are loaded one head ahead (the registers hold no more), and at the two barriers
 // of a head.  The staging alone, without the products, takes 188 us.
 // Eight waves: the first four own 16 rows each of d_x and d_B (rows s), the
@@ -595,7 +595,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(BwdArgs ba) {
     put_quad<T>(rs, mine * static_cast<int>(out.row_stride), n * 16 + 4 * g, a.states, acc[n]);
 }
 
-// 11 us at the size above (33 MB).  What is left to add up, in a fixed order: the first blocks take a step's
+// 12 us at the size above (35 MB read).  What is left to add up, in a fixed order: the first blocks take a step's
 // rows of d_B and d_C each (over the runs of heads, where there are several),
 // the last ones a head's d_A, d_D and d_dt_bias (over the steps).
 template <class T>

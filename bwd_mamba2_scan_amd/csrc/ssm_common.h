@@ -717,7 +717,7 @@ __device__ __forceinline__ void walk(const SsmArgs& a, const Walk& w, WalkLds<T,
   }
 }
 
-// 8 us for 43 segments of 24 heads of 64 x 64, the chain's length (18 MB).
+// 8 us for 32 segments of 24 heads of 64 x 64, the chain's length (24 MB).
 // Carry: turns the segments' own contributions into the state each segment
 // starts from.  One thread per four elements of a sequence's head.
 __device__ __forceinline__ void carry(const SsmArgs& a, const Walk& w, int seq, int block) {

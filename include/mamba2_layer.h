@@ -136,12 +136,12 @@ int mamba2_conv_step(int type, int batch, int channels, int taps, int silu,
  * was; so a padded batch marks its padding, x, B and C there being finite.
  *   1 <= groups, heads a multiple of groups, at most 65535, as batch is;
  *   width and states multiples of 8, 8 .. 128.  x, B, C, y and the states are
- *   16-byte aligned, with row and
- *   batch strides that are multiples of 8 elements; dt has any stride.  Row
- *   strides are at most 2^29 / 65 elements.
+ *   16-byte aligned, with row and batch strides that are multiples of 8
+ *   elements; dt has any stride.  Row strides are at most 2^29 / 65 elements.
  *   A value of x, B, C, dt or d_y that is not finite may reach every token of
  * its own sequence from the start of its step of 64 tokens on (gradients: up
- * to the end of it and before), but no other sequence.  A NaN in A (D, dt_bias)
+ * to the end of it and before), but no other sequence; an infinity may come out
+ * as a NaN.  A NaN in A (D, dt_bias)
  * reaches every token of its head (groups share d_B and d_C).  A = -inf: every
  * token but those whose d_t is 0 forgets the state.
  *   A <= 0 is meant; growing states (A > 0) are computed as long as the decay
