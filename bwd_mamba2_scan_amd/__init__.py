@@ -25,7 +25,8 @@ import ctypes
 import os
 import re
 
-from . import layer
+from . import delta, layer
+from .delta import delta_fwd, delta_step  # noqa: F401
 from .layer import clip_grads, conv_bwd, conv_fwd, conv_step, grad_norm, ssm_bwd, ssm_fwd, ssm_step  # noqa: F401
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -95,7 +96,7 @@ def lib():
                 f"{LIB_PATH} is missing: build it with `python -m bwd_mamba2_scan_amd.build` "
                 "(there is no fallback implementation)")
         handle = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in (*_SIGNATURES.items(), *layer.SIGNATURES.items()):
+        for name, (res, args) in (*_SIGNATURES.items(), *layer.SIGNATURES.items(), *delta.SIGNATURES.items()):
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args

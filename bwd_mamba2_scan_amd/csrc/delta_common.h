@@ -1,0 +1,146 @@
+// Shared by the gated delta rule's kernels: the call's arguments, the matrices
+// of a step, and the walk of a state over the tokens.
+//
+// The rule is computed in steps of 64 tokens.  With c_t the sum of log2(e) g
+// over the step up to t, S the state before the step, E_ij = 2^(c_i - c_j) and
+//   T_ij = beta_i E_ij k_i.k_j  (j < i),   M = (1 + T)^-1,
+//   P_ij = scale E_ij q_i.k_j   (j <= i),
+// the step's corrections U [64][width] solve a triangular system,
+//   U     = M (beta (V - 2^c K S))
+//   Y     = scale 2^c Q S + P U
+//   S_end = 2^c_end S + K^T (2^(c_end - c) U)
+// so everything but M is a matrix product, and the columns of V, U, Y and S do
+// not meet: they are what the work is split over.
+#pragma once
+
+#include "mamba2_delta.h"
+#include "ssm_common.h"
+
+namespace delta {
+
+using namespace ssm;
+
+// A 64 x 64 lower triangular matrix as the left operand of a product: six
+// 16 x 32 pieces (tile row i, k-step s: s = 0 for i < 2, both for i >= 2) in
+// result order, lane by lane.
+constexpr int kPieces = 6;
+constexpr int kPiece = 512;  // elements
+__host__ __device__ constexpr int piece_of(int i, int s) { return i < 2 ? i : 2 * i - 2 + s; }
+// The transpose's pieces: both k-steps for i < 2, s = 1 for i >= 2.
+__host__ __device__ constexpr int piece_of_t(int i, int s) { return i < 2 ? 2 * i + s : i + 2; }
+
+template <class T>
+constexpr int kTwo = sizeof(T) == 2 ? 2 : 1;  // parts that hold 16 bits of a value
+
+// What the walks need of a step's gates.  64 floats each; behind the last token
+// from = to = those of the last one, beta = 0.
+struct Coef {
+  float from[kTok];  // 2^c_t
+  float to[kTok];    // 2^(c_end - c_t)
+  float beta[kTok];
+  float total;       // 2^c_end
+  float pad[3];
+};
+
+struct DeltaArgs {
+  mamba2_seqs seqs;
+  mamba2_rows q, k, v, g, beta, y;
+  const float* initial;    // [batch][heads][states][width]
+  float* final_state;
+  float scale;
+  int heads, width, ratio, states;
+  int slices;              // work-groups per head: slices of its width
+  int gate_bf16;
+  int seg;                 // tokens per segment (a multiple of kTok)
+  void* m;                 // [steps][heads][kExact][kPieces][kPiece]: M
+  void* p;                 // [steps][heads][kTwo][kPieces][kPiece]: P
+  Coef* coef;              // [steps][heads]
+};
+
+// Number of the step that starts at token t of a sequence.
+__device__ __forceinline__ long step_at(const mamba2_seqs& q, int seq, int t) {
+  return static_cast<long>(unit_base(q, seq, kTok)) + t / kTok;
+}
+
+template <class T>
+__device__ __forceinline__ float load_elem(Rsrc rs, unsigned off) {
+  if constexpr (sizeof(T) == 2)
+    return __builtin_bit_cast(float, static_cast<unsigned>(static_cast<unsigned short>(
+                                         __builtin_amdgcn_raw_buffer_load_b16(rs, off, 0, 0))) << 16);
+  else
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0));
+}
+template <class T>
+__device__ __forceinline__ void store_elem(Rsrc rs, unsigned off, float v) {
+  if constexpr (sizeof(T) == 2)
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, static_cast<bf16>(v)), rs, off, 0, 0);
+  else
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, v), rs, off, 0, 0);
+}
+
+// Lane t's gate of token t of a step with `rows` tokens; 0 behind the last.
+__device__ __forceinline__ float load_gate(const mamba2_rows& r, int is_bf16, const Unit& u, bool packed, int t,
+                                           int rows, int h, int heads) {
+  const unsigned e = static_cast<unsigned>((threadIdx.x & 63) * static_cast<int>(r.row_stride) + h);
+  if (is_bf16)
+    return load_elem<bf16>(rows_rsrc(seq_ptr<const bf16>(r, u.seq, u.row0, packed) + t * r.row_stride, r.row_stride,
+                                     rows, heads), e * 2);
+  return load_elem<float>(rows_rsrc(seq_ptr<const float>(r, u.seq, u.row0, packed) + t * r.row_stride, r.row_stride,
+                                    rows, heads), e * 4);
+}
+
+// log2 of a token's decay.  One that underflows any fp32 is held at 2^-1100, so
+// that later differences keep their bits; a NaN stays one.
+__device__ __forceinline__ double gate_log(float g) {
+  const double l = static_cast<double>(g) * 1.4426950408889634074;
+  return l < -1100.0 ? -1100.0 : l;
+}
+
+// Eight elements of a piece as its lane holds them.
+template <class T>
+__device__ __forceinline__ Frag<T> piece_get(const T* p, int lane) {
+  if constexpr (sizeof(T) == 2) {
+    return {*reinterpret_cast<const v8bf*>(p + lane * 8)};
+  } else {
+    const v4f* r = reinterpret_cast<const v4f*>(p + lane * 8);
+    return {{r[0], r[1]}};
+  }
+}
+template <class T>
+__device__ __forceinline__ void piece_put(T* p, int lane, const Frag<T>& f) {
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<v8bf*>(p + lane * 8) = f.v;
+  } else {
+    v4f* r = reinterpret_cast<v4f*>(p + lane * 8);
+    r[0] = f.v[0];
+    r[1] = f.v[1];
+  }
+}
+
+// acc += a b for operands in parts, small products first; what is dropped is
+// below 2^-24 (three parts each), 2^-16 (two) of the product.
+template <class T, int A, int B>
+__device__ __forceinline__ void mma_parts(v4f& acc, const Frag<T> (&a)[A], const Frag<T> (&b)[B]) {
+  constexpr int kMost = A > B ? A : B;
+#pragma unroll
+  for (int n = kMost - 1; n >= 0; --n)
+#pragma unroll
+    for (int i = 0; i <= n; ++i)
+      if (i < A && n - i < B) mma(acc, a[i], b[n - i]);
+}
+
+// Four values of rows 4 g .. of tile i, of an array by token.
+__device__ __forceinline__ v4f rows_of(const float* p, int i, int g) {
+  return *reinterpret_cast<const v4f*>(p + 16 * i + 4 * g);
+}
+
+// Two stacked results as an operand over their rows.
+template <class T, int TERMS>
+__device__ __forceinline__ Split<T, TERMS> split_pair(v4f a, v4f b) {
+  const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  return split_of<T, TERMS>(v);
+}
+
+int check_delta(const mamba2_seqs& q, const mamba2_delta_dims& d);
+
+}  // namespace delta

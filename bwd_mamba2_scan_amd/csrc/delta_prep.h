@@ -1,0 +1,188 @@
+// The matrices of the gated delta rule's steps: M = (1 + T)^-1 and P, for one
+// step of one head, as the left operands that the walks read.
+#pragma once
+
+#include "delta_common.h"
+
+namespace delta {
+
+constexpr int kPrepWaves = 4;
+constexpr int kSq = kTok + 4;  // row stride of a 64 x 64 fp32 matrix in LDS
+
+template <class T, int NB>
+struct PrepLds {
+  static constexpr int ldn = stride_of<T>(NB * 32);
+  union {
+    struct {
+      T k[kTok * ldn];
+      T q[kTok * ldn];
+    } in;
+    struct {
+      float t[kTok * kSq];
+      float p[kTok * kSq];
+    } sq;
+  };
+  alignas(16) float m[kTok * kSq];
+  alignas(16) Coef coef;
+  float hi[kTok], lo[kTok];  // c_t in two floats
+};
+
+// acc += A B over 16: A row-major at a, B in the order of a result: register r
+// holds row 4 g + r.
+__device__ __forceinline__ void mul16(v4f& acc, const float* a, const v4f& b, int l15, int g) {
+  const v4f x = *reinterpret_cast<const v4f*>(a + l15 * kSq + 4 * g);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[r], b[r], acc, 0, 0, 0);
+}
+__device__ __forceinline__ v4f block_get(const float* a, int l15, int g) {
+  v4f v;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) v[r] = a[(4 * g + r) * kSq + l15];
+  return v;
+}
+__device__ __forceinline__ void block_put(float* a, v4f v, int l15, int g) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) a[(4 * g + r) * kSq + l15] = v[r];
+}
+
+// The inverse of 1 + t (t strictly lower, 64 x 64) into m, by all four waves:
+// each inverts a 16 x 16 block of the diagonal row by row, a lane a column;
+// then the blocks below the diagonal by halves,
+//   [[A, 0], [B, C]]^-1 = [[A^-1, 0], [-C^-1 B A^-1, C^-1]].
+// fp32 products throughout: the inverse's entries multiply every correction.
+__device__ __forceinline__ void invert(float* m, const float* t, int wave, int lane) {
+  const int l15 = lane & 15, g = lane >> 4;
+  const auto at = [](int i, int j) { return 16 * i * kSq + 16 * j; };
+  {
+    const float* d = t + at(wave, wave);
+    float col[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s = i == l15 ? 1.0f : 0.0f;
+#pragma unroll
+      for (int j = 0; j < i; ++j) s = fmaf(-d[i * kSq + j], col[j], s);
+      col[i] = s;
+    }
+    if (g == 0) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) m[at(wave, wave) + i * kSq + l15] = col[i];
+    }
+    if (wave < 2) block_put(m + at(2 * wave, 2 * wave + 1), v4f{0, 0, 0, 0}, l15, g);
+  }
+  __syncthreads();
+  if (wave < 2) {
+    const int i = 2 * wave;
+    v4f x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
+    mul16(x, t + at(i + 1, i), block_get(m + at(i, i), l15, g), l15, g);
+    mul16(y, m + at(i + 1, i + 1), x, l15, g);
+    block_put(m + at(i + 1, i), -y, l15, g);
+  }
+  __syncthreads();
+  const int rb = wave >> 1, cb = wave & 1;  // a block of the lower left quarter each
+  v4f y = {0, 0, 0, 0};
+  for (int r = 0; r <= rb; ++r) {
+    v4f x = {0, 0, 0, 0};
+    for (int j = cb; j < 2; ++j) mul16(x, t + at(2 + r, j), block_get(m + at(j, cb), l15, g), l15, g);
+    mul16(y, m + at(2 + rb, 2 + r), x, l15, g);
+  }
+  block_put(m + at(2 + rb, cb), -y, l15, g);
+  __syncthreads();
+}
+
+// Writes the pieces of a 64 x 64 matrix (transposed: of its transpose) in PARTS
+// parts, a wave's share of them.
+template <class T, int PARTS, bool TRANSPOSED>
+__device__ __forceinline__ void put_pieces(T* out, const float* m, int wave, int lane) {
+  const int l15 = lane & 15, g = lane >> 4;
+  for (int n = wave; n < kPieces; n += kPrepWaves) {
+    int i, s;  // the piece's tile row and k-step
+    if (TRANSPOSED) {
+      i = n < 4 ? n >> 1 : n - 2;
+      s = n < 4 ? n & 1 : 1;
+    } else {
+      i = n < 2 ? n : (n + 2) >> 1;
+      s = n < 2 ? 0 : n & 1;
+    }
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int row = 16 * i + l15, k = 32 * s + (j >> 2) * 16 + 4 * g + (j & 3);
+      v[j] = TRANSPOSED ? m[k * kSq + row] : m[row * kSq + k];
+    }
+    const Split<T, PARTS> f = split_of<T, PARTS>(v);
+#pragma unroll
+    for (int z = 0; z < PARTS; ++z) piece_put(out + (z * kPieces + n) * kPiece, lane, f.f[z]);
+  }
+}
+
+// One step of one head: leaves T in s.sq.t, P (without scale where SCALE is
+// false) in s.sq.p, M in s.m and the gates in s.coef, for all waves.
+template <class T, int NB>
+__device__ __forceinline__ void make_step(PrepLds<T, NB>& s, const DeltaArgs& a, const Unit& u, int h, bool packed) {
+  typedef PrepLds<T, NB> L;
+  constexpr int kThreads = kPrepWaves * 64;
+  const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
+  const int rows = min(u.len - u.t0, kTok);
+  const int j = h / a.ratio * a.states;
+  Tile<T, kTok, NB * 32, kThreads> tk, tq;
+  tk.init(a.k.row_stride, a.states, tid);
+  tq.init(a.q.row_stride, a.states, tid);
+  tk.load(rows_rsrc(seq_ptr<const T>(a.k, u.seq, u.row0, packed) + u.t0 * a.k.row_stride + j, a.k.row_stride, rows,
+                    a.states));
+  tq.load(rows_rsrc(seq_ptr<const T>(a.q, u.seq, u.row0, packed) + u.t0 * a.q.row_stride + j, a.q.row_stride, rows,
+                    a.states));
+  if (wave == kPrepWaves - 1) {
+    const double c = scan64(gate_log(load_gate(a.g, a.gate_bf16, u, packed, u.t0, rows, h, a.heads)));
+    const long bits = __builtin_bit_cast(long, c);
+    const double end = __builtin_bit_cast(
+        double, (static_cast<long>(__builtin_amdgcn_readlane(static_cast<int>(bits >> 32), 63)) << 32) |
+                    static_cast<unsigned>(__builtin_amdgcn_readlane(static_cast<int>(bits), 63)));
+    s.hi[lane] = static_cast<float>(c);
+    s.lo[lane] = static_cast<float>(c - static_cast<float>(c));
+    s.coef.from[lane] = exp2_of(c);
+    s.coef.to[lane] = exp2_of(end - c);
+    s.coef.beta[lane] = load_gate(a.beta, a.gate_bf16, u, packed, u.t0, rows, h, a.heads);
+    if (lane == 0) s.coef.total = exp2_of(end);
+  }
+  tk.store(s.in.k, L::ldn, tid);
+  tq.store(s.in.q, L::ldn, tid);
+  __syncthreads();
+  // a wave's sixteen rows of both products, up to the diagonal
+  v4f kk[4], qk[4];
+  Frag<T> kf[NB], qf[NB];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    kf[n] = frag_row(s.in.k, L::ldn, wave * 16, n * 32);
+    qf[n] = frag_row(s.in.q, L::ldn, wave * 16, n * 32);
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    kk[c] = qk[c] = v4f{0, 0, 0, 0};
+    if (c <= wave) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const Frag<T> b = frag_row(s.in.k, L::ldn, c * 16, n * 32);
+        mma(kk[c], kf[n], b);
+        mma(qk[c], qf[n], b);
+      }
+    }
+  }
+  __syncthreads();  // k and q give way to T and P
+  const v4f hi = rows_of(s.hi, wave, g), lo = rows_of(s.lo, wave, g), beta = rows_of(s.coef.beta, wave, g);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int col = c * 16 + l15;
+    const float ch = s.hi[col], cl = s.lo[col];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = wave * 16 + 4 * g + r;
+      const float e = exp2_of((hi[r] - ch) + (lo[r] - cl));
+      s.sq.t[row * kSq + col] = col < row ? beta[r] * (e * kk[c][r]) : 0.0f;
+      s.sq.p[row * kSq + col] = col <= row ? a.scale * (e * qk[c][r]) : 0.0f;
+    }
+  }
+  __syncthreads();
+  invert(s.m, s.sq.t, wave, lane);
+}
+
+}  // namespace delta

@@ -1,0 +1,131 @@
+"""Python binding of the gated delta rule and of the group norm beside it (include/mamba2_delta.h).
+
+    delta_fwd(q, k, v, g, beta)                -> (y, final_state)
+    delta_bwd(q, k, v, g, beta, d_y)           -> dict(d_q, d_k, d_v, d_g, d_beta[, d_initial_state])
+    delta_step(q, k, v, g, beta, state)        -> y; the state moves on in place
+    group_norm_fwd(x, weight, bias, groups=)   -> y
+    group_norm_bwd(x, d_y, weight, bias, ...)  -> dict(d_x[, d_weight, d_bias, d_gate])
+
+Tensors, packed sequences (`offsets`), streams, outputs and workspaces are as in
+the selective layer's calls (module `layer`).
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import layer as _l
+from .layer import (_EOVERLAP, Rows, Seqs, _apart, _c_int, _c_size, _c_vp, _dense, _given, _gpu, _new_dense, _new_rows,
+                    _On, _ptr, _raise, _rows, _seqs, _sizes, _start, _token, _type, _workspace)
+
+
+class DeltaDims(ctypes.Structure):
+    """mamba2_delta_dims"""
+    _fields_ = [(n, _c_int) for n in ("type", "gate_type", "heads", "width", "groups", "states")] + [
+        ("scale", ctypes.c_float)]
+
+
+class NormDims(ctypes.Structure):
+    """mamba2_norm_dims"""
+    _fields_ = [(n, _c_int) for n in ("type", "groups", "width", "form", "centered", "shared")] + [
+        ("eps", ctypes.c_float)]
+
+
+PLAIN, SILU, GATED, GATE_FIRST = 0, 1, 2, 3  # MAMBA2_NORM_*
+
+SIGNATURES = {
+    "mamba2_delta_fwd_workspace_bytes": (_c_size, [Seqs, DeltaDims]),
+    "mamba2_delta_fwd": (_c_int, [Seqs, DeltaDims, Rows, Rows, Rows, Rows, Rows, _c_vp, Rows, _c_vp, _c_vp, _c_size,
+                                  _c_vp]),
+    "mamba2_delta_step": (_c_int, [_c_int, DeltaDims, Rows, Rows, Rows, Rows, Rows, _c_vp, Rows, _c_vp, _c_vp]),
+}
+
+
+# ---------------------------------------------------------------- delta rule
+def _delta_dims(typ, q, v, g, scale):
+    _gpu(q, "q")
+    _gpu(g, "g")
+    if q.dim() != v.dim():
+        raise ValueError("q and k must be [..., groups, states] beside v [..., heads, width]")
+    heads, width = v.shape[-2:]
+    groups, states = q.shape[-2:]
+    _sizes(heads, width, groups, states)
+    scale = states ** -0.5 if scale is None and states > 0 else float(scale or 0.0)
+    return DeltaDims(typ, _type(g, "g"), heads, width, groups, states, scale)
+
+
+def _delta_inputs(q, k, v, g, beta, lead, d, dev):
+    shared, vec = (d.groups, d.states), (d.heads,)
+    return (_rows(q, "q", lead, shared, v.dtype, dev), _rows(k, "k", lead, shared, v.dtype, dev),
+            _rows(v, "v", lead, (d.heads, d.width), v.dtype, dev), _rows(g, "g", lead, vec, g.dtype, dev),
+            _rows(beta, "beta", lead, vec, g.dtype, dev))
+
+
+def delta_fwd(q, k, v, g, beta, *, scale=None, initial_state=None, offsets=None, want_final_state=False, y=None,
+              final_state=None, workspace=None, stream=None):
+    """Gated delta rule: S' = e^g_t S_{t-1}, S_t = S' + k_t (beta_t (v_t - S'^T k_t))^T, y_t = scale S_t^T q_t.
+
+    q, k [batch, length, groups, states], v [batch, length, heads, width],
+    g, beta [batch, length, heads] (with offsets: no batch axis), float32 or
+    bfloat16 (q, k, v alike, g and beta alike); heads / groups neighbouring
+    heads share a q and k.  g holds log decays (<= 0); scale defaults to
+    states ** -0.5.  initial_state [batch, heads, states, width] float32
+    (default: zeros).  Returns (y, the final state, or None unless
+    want_final_state or final_state is given).
+    """
+    dev, typ = _start(v, "v")
+    f32 = _l.torch.float32
+    seqs, lead, batch = _seqs(v, offsets, 2, dev, "v")
+    d = _delta_dims(typ, q, v, g, scale)
+    pq, pk, pv, pg, pb = _delta_inputs(q, k, v, g, beta, lead, d, dev)
+    shape = (batch, d.heads, d.states, d.width)
+    s0 = _dense(initial_state, "initial_state", shape, f32, dev)
+    _apart((("y", y), ("final_state", final_state), ("workspace", workspace)),
+           (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("initial_state", initial_state),
+            ("offsets", offsets)))
+    with _On(dev, stream) as s:
+        y, py = _new_rows(y, "y", lead, (d.heads, d.width), v, dev)
+        final_state, s1 = _new_state(final_state, "final_state", shape, v, dev, want_final_state)
+        workspace, nbytes = _workspace(workspace, _l.lib.mamba2_delta_fwd_workspace_bytes(seqs, d), v, dev)
+        st = _l.lib.mamba2_delta_fwd(seqs, d, pq, pk, pv, pg, pb, s0, py, s1, _ptr(workspace), nbytes, s)
+    _raise(st, "mamba2_delta_fwd")
+    return y, final_state
+
+
+def _new_state(t, name, shape, like, dev, wanted=True):
+    """_new_dense for a float32 tensor beside inputs of any type."""
+    if t is not None:
+        return t, _dense(t, name, shape, _l.torch.float32, dev)
+    if not wanted:
+        return None, None
+    t = like.new_empty(shape, dtype=_l.torch.float32)
+    return t, t.data_ptr()
+
+
+def delta_step(q, k, v, g, beta, state, *, scale=None, new_state=None, y=None, stream=None):
+    """One token of each sequence: q, k [batch, groups, states], v [batch, heads, width], g, beta [batch, heads] -> y.
+
+    state [batch, heads, states, width] float32 moves on in place, or into
+    new_state where that is given.
+    """
+    dev, typ = _start(v, "v")
+    if v.dim() != 3:
+        raise ValueError("v must be [batch, heads, width]")
+    f32 = _l.torch.float32
+    batch = v.shape[0]
+    _sizes(batch)
+    d = _delta_dims(typ, q, v, g, scale)
+    rows = _delta_inputs(q, k, v, g, beta, (batch,), d, dev)
+    shape = (batch, d.heads, d.states, d.width)
+    s0 = _dense(state, "state", shape, f32, dev)
+    if s0 is None:
+        raise TypeError("state must be a torch.Tensor")
+    s1 = s0 if new_state is None else _dense(new_state, "new_state", shape, f32, dev)
+    with _On(dev, stream) as s:
+        y, py = _new_rows(y, "y", (batch,), (d.heads, d.width), v, dev)
+        for r in (*rows, py):
+            _token(r)
+        st = _l.lib.mamba2_delta_step(batch, d, *rows, s0, py, s1, s)
+    if st == _EOVERLAP:
+        raise ValueError("y or new_state overlaps another tensor of the call")
+    _raise(st, "mamba2_delta_step")
+    return y

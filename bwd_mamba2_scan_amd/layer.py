@@ -116,12 +116,12 @@ class _On:
         return False
 
 
-def _start(x):
+def _start(x, name="x"):
     """(device, element type code) of a call's first tensor."""
     if torch is None:
         _load()
-    _gpu(x, "x")
-    return x.device, _type(x, "x")
+    _gpu(x, name)
+    return x.device, _type(x, name)
 
 
 def _type(t, name):
@@ -190,16 +190,16 @@ def _sizes(*sizes):
         raise ValueError(f"a dimension of {max(sizes)} is too large (at most {_MAX_INT})")
 
 
-def _seqs(x, offsets, inner_dims, dev):
+def _seqs(x, offsets, inner_dims, dev, name="x"):
     """(mamba2_seqs, the leading shape, the number of sequences)"""
     if offsets is None:
         if x.dim() != 2 + inner_dims:
-            raise ValueError(f"x must have {2 + inner_dims} dimensions (got {x.dim()}); packed rows need offsets")
+            raise ValueError(f"{name} must have {2 + inner_dims} dimensions (got {x.dim()}); packed rows need offsets")
         batch, length = x.shape[:2]
         _sizes(batch, length)
         return Seqs(batch, length, None), (batch, length), batch
     if x.dim() != 1 + inner_dims:
-        raise ValueError(f"with offsets x must have {1 + inner_dims} dimensions (got {x.dim()})")
+        raise ValueError(f"with offsets {name} must have {1 + inner_dims} dimensions (got {x.dim()})")
     _gpu(offsets, "offsets", dev)
     if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous int32 vector of at least two elements")
