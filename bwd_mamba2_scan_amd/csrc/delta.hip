@@ -9,6 +9,7 @@
 // step's left operands (K, Q, M, P) through LDS.
 #include "delta_common.h"
 #include "delta_prep.h"
+#include "delta_walk.h"
 
 namespace {
 
@@ -30,173 +31,10 @@ __global__ __launch_bounds__(kPrepWaves * 64) void delta_prep_kernel(DeltaArgs a
     reinterpret_cast<v4f*>(a.coef + at)[threadIdx.x] = reinterpret_cast<const v4f*>(&s.coef)[threadIdx.x];
 }
 
-constexpr int kWaves = 4;  // of a walk: 64 columns
-
-// Contiguous memory to LDS, in 16-byte vectors by THREADS threads.
-template <int BYTES, int THREADS>
-struct Flat {
-  static constexpr int kAll = BYTES / 16, kN = (kAll + THREADS - 1) / THREADS;
-  v4u v[kN];
-  __device__ __forceinline__ void load(const void* p, int tid) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int e = min(tid + i * THREADS, kAll - 1);
-      v[i] = static_cast<const v4u*>(p)[e];
-    }
-  }
-  __device__ __forceinline__ void store(void* lds, int tid) const {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int e = tid + i * THREADS;
-      if (kAll % THREADS == 0 || e < kAll) static_cast<v4u*>(lds)[e] = v[i];
-    }
-  }
-};
-
-template <class T, int NB>
-struct FwdLds {
-  static constexpr int ldn = stride_of<T>(NB * 32);
-  alignas(16) T k[kTok * ldn];
-  alignas(16) T q[kTok * ldn];
-  alignas(16) T m[kExact<T> * kPieces * kPiece];
-  alignas(16) T p[kTwo<T> * kPieces * kPiece];
-  alignas(16) Coef coef;
-};
-
 template <class T, int NB>
 __global__ __launch_bounds__(kWaves * 64, 1) void delta_fwd_kernel(DeltaArgs a) {
-  typedef FwdLds<T, NB> L;
-  __shared__ L s;
-  constexpr int kThreads = kWaves * 64;
-  constexpr int kM = kExact<T> * kPieces * kPiece, kP = kTwo<T> * kPieces * kPiece;
-  const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
-  const int work = xcd_contiguous(blockIdx.x, gridDim.x);
-  const int per = a.heads * a.slices;
-  const int unit = work / per, h = work % per / a.slices, slice = work % a.slices;
-  const Unit u = locate(a.seqs, unit, a.seg);
-  if (!u.live) return;
-  const bool packed = a.seqs.offsets != nullptr;
-  const int p0 = slice * kThreads / 4;
-  const int col = p0 + wave * 16 + l15;
-  const long of_seq = (static_cast<long>(u.seq) * a.heads + h) * (static_cast<long>(a.states) * a.width);
-  const T* kp = seq_ptr<const T>(a.k, u.seq, u.row0, packed) + h / a.ratio * a.states;
-  const T* qp = seq_ptr<const T>(a.q, u.seq, u.row0, packed) + h / a.ratio * a.states;
-  const T* vp = seq_ptr<const T>(a.v, u.seq, u.row0, packed) + h * a.width;
-  T* yp = seq_ptr<T>(a.y, u.seq, u.row0, packed) + h * a.width;
-
-  State<NB, true> st;
-  st.init(a.width, p0, wave);
-  st.load(a.initial == nullptr ? nullptr : a.initial + of_seq, a.width, a.states);
-
-  const int end = u.len;
-  Tile<T, kTok, NB * 32, kThreads> tk, tq;
-  tk.init(a.k.row_stride, a.states, tid);
-  tq.init(a.q.row_stride, a.states, tid);
-  Flat<kM * sizeof(T), kThreads> tm;
-  Flat<kP * sizeof(T), kThreads> tp;
-  Flat<sizeof(Coef), kThreads> tc;
-  float v[4][4];
-  const unsigned v_off = col < a.width ? static_cast<unsigned>((4 * g * static_cast<int>(a.v.row_stride) + col) * sizeof(T)) : kOutside;
-  const unsigned y_off = col < a.width ? static_cast<unsigned>((4 * g * static_cast<int>(a.y.row_stride) + col) * sizeof(T)) : kOutside;
-  const int v_row = static_cast<int>(a.v.row_stride * sizeof(T)), y_row = static_cast<int>(a.y.row_stride * sizeof(T));
-  const auto fetch = [&](int t) {
-    const int rows = min(end - t, kTok);
-    const long at = step_at(a.seqs, u.seq, t) * a.heads + h;
-    tk.load(rows_rsrc(kp + t * a.k.row_stride, a.k.row_stride, rows, a.states));
-    tq.load(rows_rsrc(qp + t * a.q.row_stride, a.q.row_stride, rows, a.states));
-    tm.load(static_cast<const T*>(a.m) + at * kM, tid);
-    tp.load(static_cast<const T*>(a.p) + at * kP, tid);
-    tc.load(a.coef + at, tid);
-    const Rsrc rv = rows_rsrc(vp + t * a.v.row_stride, a.v.row_stride, rows, a.width);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) v[i][r] = load_elem<T>(rv, v_off + (16 * i + r) * v_row);
-  };
-  if (u.t0 < end) fetch(u.t0);
-  for (int t = u.t0; t < end; t += kTok) {
-    __syncthreads();
-    tk.store(s.k, L::ldn, tid);
-    tq.store(s.q, L::ldn, tid);
-    tm.store(s.m, tid);
-    tp.store(s.p, tid);
-    tc.store(&s.coef, tid);
-    v4f x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = v4f{v[i][0], v[i][1], v[i][2], v[i][3]};
-    __syncthreads();
-    if (t + kTok < end) fetch(t + kTok);
-
-    // K S and Q S
-    v4f ks[4], qs[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ks[i] = qs[i] = v4f{0, 0, 0, 0};
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      const Split<T, kExact<T>> sp = split_pair<T, kExact<T>>(st.st[2 * n], st.st[2 * n + 1]);
-      Frag<T> two[kTwo<T>];
-#pragma unroll
-      for (int z = 0; z < kTwo<T>; ++z) two[z] = sp.f[z];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const Frag<T> kf[1] = {frag_row_result(s.k, L::ldn, 16 * i, 32 * n)};
-        const Frag<T> qf[1] = {frag_row_result(s.q, L::ldn, 16 * i, 32 * n)};
-        mma_parts<T>(ks[i], kf, sp.f);
-        mma_parts<T>(qs[i], qf, two);
-      }
-    }
-    // beta (V - 2^c K S), then U = M that
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = rows_of(s.coef.beta, i, g) * (x[i] - rows_of(s.coef.from, i, g) * ks[i]);
-    const Split<T, kExact<T>> xs[2] = {split_pair<T, kExact<T>>(x[0], x[1]), split_pair<T, kExact<T>>(x[2], x[3])};
-    v4f w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[i] = v4f{0, 0, 0, 0};
-#pragma unroll
-      for (int n = 0; n <= i / 2; ++n) {
-        Frag<T> mf[kExact<T>];
-#pragma unroll
-        for (int z = 0; z < kExact<T>; ++z) mf[z] = piece_get(s.m + (z * kPieces + piece_of(i, n)) * kPiece, lane);
-        mma_parts<T>(w[i], mf, xs[n].f);
-      }
-    }
-    // Y = scale 2^c Q S + P U
-    {
-      const Split<T, kTwo<T>> us[2] = {split_pair<T, kTwo<T>>(w[0], w[1]), split_pair<T, kTwo<T>>(w[2], w[3])};
-      const Rsrc ry = rows_rsrc(yp + t * a.y.row_stride, a.y.row_stride, min(end - t, kTok), a.width);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v4f y = qs[i] * rows_of(s.coef.from, i, g) * a.scale;
-#pragma unroll
-        for (int n = 0; n <= i / 2; ++n) {
-          Frag<T> pf[kTwo<T>];
-#pragma unroll
-          for (int z = 0; z < kTwo<T>; ++z) pf[z] = piece_get(s.p + (z * kPieces + piece_of(i, n)) * kPiece, lane);
-          mma_parts<T>(y, pf, us[n].f);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) store_elem<T>(ry, y_off + (16 * i + r) * y_row, y[r]);
-      }
-    }
-    // S = 2^c_end S + K^T (2^(c_end - c) U); a step's products are added up by
-    // themselves: on top of the state, each would round at the state's size
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = w[i] * rows_of(s.coef.to, i, g);
-    const Split<T, kExact<T>> us[2] = {split_pair<T, kExact<T>>(w[0], w[1]), split_pair<T, kExact<T>>(w[2], w[3])};
-    const float total = s.coef.total;
-#pragma unroll
-    for (int n = 0; n < 2 * NB; ++n) {
-      v4f add = {0, 0, 0, 0};
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const Frag<T> kf[1] = {frag_col_result(s.k, L::ldn, 32 * j, 16 * n)};
-        mma_parts<T>(add, kf, us[j].f);
-      }
-      st.st[n] = st.st[n] * total + add;
-    }
-  }
-  if (a.final_state != nullptr) st.save(a.final_state + of_seq, a.width, a.states);
+  __shared__ FwdLds<T, NB, false> s;
+  walk_forward<T, NB, false>(a, s);
 }
 
 // ------------------------------------------------------------ single tokens
@@ -313,14 +151,45 @@ size_t p_bytes(int type) { return (type == MAMBA2_BF16 ? 2 * 2 : 4) * kPieces * 
 
 namespace delta {
 
+namespace {
+mamba2_ssm_dims scan_dims(const mamba2_delta_dims& d) {
+  return {d.type, d.gate_type, d.heads, d.width, d.groups, d.states, 0};
+}
+}  // namespace
+
 int check_delta(const mamba2_seqs& q, const mamba2_delta_dims& d) {
-  const mamba2_ssm_dims like = {d.type, d.gate_type, d.heads, d.width, d.groups, d.states, 0};
-  const int st = check_dims(q, like);
+  const int st = check_dims(q, scan_dims(d));
   if (st != MAMBA2_SCAN_OK) return st;
   if (!(d.scale - d.scale == 0.0f)) return MAMBA2_SCAN_EBADDIM;
-  // a step's work-group of four waves for every step and head, and for every sequence, head and 64 columns
-  const long long most = steps_of(q) > 2LL * q.batch ? steps_of(q) : 2LL * q.batch;
-  return grid_ok(most * d.heads, kPrepWaves * 64) ? MAMBA2_SCAN_OK : MAMBA2_SCAN_EBADDIM;
+  // the largest launches: up to 512 threads for every step and head, and 256 for every
+  // sequence (packed: one more), head and 64 columns
+  const long long most = steps_of(q) > q.batch + 1LL ? steps_of(q) : q.batch + 1LL;
+  return grid_ok(most * d.heads, 512) ? MAMBA2_SCAN_OK : MAMBA2_SCAN_EBADDIM;
+}
+int check_keys(mamba2_rows* r, const mamba2_seqs& q, const mamba2_delta_dims& d) {
+  const long long n = static_cast<long long>(d.groups) * d.states;
+  *r = used_strides(*r, q, n);
+  return check_vec_rows(*r, q, n, type_size(d.type));
+}
+int check_values(mamba2_rows* r, const mamba2_seqs& q, const mamba2_delta_dims& d) {
+  const long long n = static_cast<long long>(d.heads) * d.width;
+  *r = used_strides(*r, q, n);
+  return check_vec_rows(*r, q, n, type_size(d.type));
+}
+int check_gates(mamba2_rows* r, const mamba2_seqs& q, const mamba2_delta_dims& d) {
+  *r = used_strides(*r, q, d.heads);
+  return check_step_rows(*r, q, scan_dims(d));
+}
+void set_dims(DeltaArgs* a, const mamba2_seqs& q, const mamba2_delta_dims& d) {
+  a->seqs = q;
+  a->scale = d.scale;
+  a->heads = d.heads;
+  a->width = d.width;
+  a->ratio = d.heads / d.groups;
+  a->states = d.states;
+  a->slices = (d.width + kWaves * 16 - 1) / (kWaves * 16);
+  a->gate_bf16 = d.gate_type == MAMBA2_BF16;
+  a->seg = q.length > kTok ? (q.length + kTok - 1) / kTok * kTok : kTok;
 }
 
 }  // namespace delta
@@ -337,38 +206,25 @@ int mamba2_delta_fwd(mamba2_seqs seqs, mamba2_delta_dims d, mamba2_rows q, mamba
                      size_t workspace_bytes, void* stream) {
   int st = check_delta(seqs, d);
   if (st != MAMBA2_SCAN_OK) return st;
-  const size_t e = type_size(d.type);
-  const long long vw = static_cast<long long>(d.heads) * d.width, kw = static_cast<long long>(d.groups) * d.states;
-  const mamba2_ssm_dims like = {d.type, d.gate_type, d.heads, d.width, d.groups, d.states, 0};
   DeltaArgs a = {};
-  a.seqs = seqs;
-  a.q = used_strides(q, seqs, kw);
-  a.k = used_strides(k, seqs, kw);
-  a.v = used_strides(v, seqs, vw);
-  a.y = used_strides(y, seqs, vw);
-  a.g = used_strides(g, seqs, d.heads);
-  a.beta = used_strides(beta, seqs, d.heads);
-  if ((st = check_vec_rows(a.q, seqs, kw, e)) != MAMBA2_SCAN_OK || (st = check_vec_rows(a.k, seqs, kw, e)) != MAMBA2_SCAN_OK ||
-      (st = check_vec_rows(a.v, seqs, vw, e)) != MAMBA2_SCAN_OK || (st = check_vec_rows(a.y, seqs, vw, e)) != MAMBA2_SCAN_OK ||
-      (st = check_step_rows(a.g, seqs, like)) != MAMBA2_SCAN_OK || (st = check_step_rows(a.beta, seqs, like)) != MAMBA2_SCAN_OK)
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.g = g;
+  a.beta = beta;
+  a.y = y;
+  if ((st = check_keys(&a.q, seqs, d)) != MAMBA2_SCAN_OK || (st = check_keys(&a.k, seqs, d)) != MAMBA2_SCAN_OK ||
+      (st = check_values(&a.v, seqs, d)) != MAMBA2_SCAN_OK || (st = check_values(&a.y, seqs, d)) != MAMBA2_SCAN_OK ||
+      (st = check_gates(&a.g, seqs, d)) != MAMBA2_SCAN_OK || (st = check_gates(&a.beta, seqs, d)) != MAMBA2_SCAN_OK)
     return st;
   if (!aligned_to(initial_state, 16) || !aligned_to(final_state, 16)) return MAMBA2_SCAN_EALIGN;
-  const size_t need = mamba2_delta_fwd_workspace_bytes(seqs, d);
   if (workspace == nullptr) return MAMBA2_SCAN_ENULL;
-  if (workspace_bytes < need) return MAMBA2_SCAN_ESIZE;
+  if (workspace_bytes < mamba2_delta_fwd_workspace_bytes(seqs, d)) return MAMBA2_SCAN_ESIZE;
   if (!aligned_to(workspace, 16)) return MAMBA2_SCAN_EALIGN;
   if (seqs.length == 0 && final_state == nullptr) return MAMBA2_SCAN_OK;
   a.initial = initial_state;
   a.final_state = final_state;
-  a.scale = d.scale;
-  a.heads = d.heads;
-  a.width = d.width;
-  a.ratio = d.heads / d.groups;
-  a.states = d.states;
-  a.slices = (d.width + kWaves * 16 - 1) / (kWaves * 16);
-  a.gate_bf16 = d.gate_type == MAMBA2_BF16;
-  a.seg = (seqs.length + kTok - 1) / kTok * kTok;
-  if (a.seg == 0) a.seg = kTok;
+  set_dims(&a, seqs, d);
   const long cells = steps_of(seqs) * d.heads;
   char* at = static_cast<char*>(workspace);
   a.m = at;
@@ -388,11 +244,10 @@ int mamba2_delta_step(int batch, mamba2_delta_dims d, mamba2_rows q, mamba2_rows
   if (state == nullptr || new_state == nullptr) return MAMBA2_SCAN_ENULL;
   const size_t e = type_size(d.type), eg = type_size(d.gate_type);
   const long long vw = static_cast<long long>(d.heads) * d.width, kw = static_cast<long long>(d.groups) * d.states;
-  const mamba2_ssm_dims like = {d.type, d.gate_type, d.heads, d.width, d.groups, d.states, 0};
   q.row_stride = k.row_stride = v.row_stride = g.row_stride = beta.row_stride = y.row_stride = 0;
-  if ((st = check_vec_rows(q, seqs, kw, e)) != MAMBA2_SCAN_OK || (st = check_vec_rows(k, seqs, kw, e)) != MAMBA2_SCAN_OK ||
-      (st = check_vec_rows(v, seqs, vw, e)) != MAMBA2_SCAN_OK || (st = check_vec_rows(y, seqs, vw, e)) != MAMBA2_SCAN_OK ||
-      (st = check_step_rows(g, seqs, like)) != MAMBA2_SCAN_OK || (st = check_step_rows(beta, seqs, like)) != MAMBA2_SCAN_OK)
+  if ((st = check_keys(&q, seqs, d)) != MAMBA2_SCAN_OK || (st = check_keys(&k, seqs, d)) != MAMBA2_SCAN_OK ||
+      (st = check_values(&v, seqs, d)) != MAMBA2_SCAN_OK || (st = check_values(&y, seqs, d)) != MAMBA2_SCAN_OK ||
+      (st = check_gates(&g, seqs, d)) != MAMBA2_SCAN_OK || (st = check_gates(&beta, seqs, d)) != MAMBA2_SCAN_OK)
     return st;
   if (!aligned_to(state, 16) || !aligned_to(new_state, 16)) return MAMBA2_SCAN_EALIGN;
   const long long states = static_cast<long long>(batch) * d.heads * d.states * d.width * 4;

@@ -55,6 +55,16 @@ struct DeltaArgs {
   void* m;                 // [steps][heads][kExact][kPieces][kPiece]: M
   void* p;                 // [steps][heads][kTwo][kPieces][kPiece]: P
   Coef* coef;              // [steps][heads]
+  // the backward's
+  mamba2_rows d_y, d_q, d_k, d_v, d_g, d_beta;
+  const float* d_final;
+  float* d_initial;
+  void* mt;                // as m: the transpose of M
+  void* pt;                // as m: the transpose of P
+  float* keep;             // [steps][heads][states][width]: the state each step starts from
+  float* d_keep;           // the same: the gradient of the state each step ends with
+  float* u;                // [steps][heads][kTok][width]: U
+  float* d_r;              // the same: the gradient of beta (V - 2^c K S)
 };
 
 // Number of the step that starts at token t of a sequence.
@@ -141,6 +151,12 @@ __device__ __forceinline__ Split<T, TERMS> split_pair(v4f a, v4f b) {
   return split_of<T, TERMS>(v);
 }
 
+// Host side, in delta.hip.  check_keys, check_values, check_gates: a tensor of
+// the call, whose unused strides they replace.
 int check_delta(const mamba2_seqs& q, const mamba2_delta_dims& d);
+int check_keys(mamba2_rows* r, const mamba2_seqs& q, const mamba2_delta_dims& d);
+int check_values(mamba2_rows* r, const mamba2_seqs& q, const mamba2_delta_dims& d);
+int check_gates(mamba2_rows* r, const mamba2_seqs& q, const mamba2_delta_dims& d);
+void set_dims(DeltaArgs* a, const mamba2_seqs& q, const mamba2_delta_dims& d);
 
 }  // namespace delta

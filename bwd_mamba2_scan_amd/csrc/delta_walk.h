@@ -1,0 +1,343 @@
+// The walks of the gated delta rule's states over the tokens.
+#pragma once
+
+#include "delta_common.h"
+
+namespace delta {
+
+constexpr int kWaves = 4;  // of a walk: 64 columns
+
+// Contiguous memory to LDS, in 16-byte vectors by THREADS threads.
+template <int BYTES, int THREADS>
+struct Flat {
+  static constexpr int kAll = BYTES / 16, kN = (kAll + THREADS - 1) / THREADS;
+  v4u v[kN];
+  __device__ __forceinline__ void load(const void* p, int tid) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int e = min(tid + i * THREADS, kAll - 1);
+      v[i] = static_cast<const v4u*>(p)[e];
+    }
+  }
+  __device__ __forceinline__ void store(void* lds, int tid) const {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int e = tid + i * THREADS;
+      if (kAll % THREADS == 0 || e < kAll) static_cast<v4u*>(lds)[e] = v[i];
+    }
+  }
+};
+
+// A wave's 64 x 16 result into [kTok][width] floats.
+__device__ __forceinline__ void save_rows(float* p, int width, int col, int g, const v4f (&w)[4]) {
+  const Rsrc rs = make_rsrc(p, static_cast<unsigned>(kTok * width * 4));
+  const unsigned off = col < width ? static_cast<unsigned>((4 * g * width + col) * 4) : kOutside;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) store_elem<float>(rs, off + (16 * i + r) * width * 4, w[i][r]);
+}
+
+template <class T, int NB, bool KEEP>
+struct FwdLds {
+  static constexpr int ldn = stride_of<T>(NB * 32);
+  alignas(16) T k[kTok * ldn];
+  alignas(16) T m[kExact<T> * kPieces * kPiece];
+  alignas(16) Coef coef;
+  alignas(16) T q[KEEP ? 8 : kTok * ldn];
+  alignas(16) T p[KEEP ? 8 : kTwo<T> * kPieces * kPiece];
+};
+
+// The walk of a head's 64 columns.  KEEP false: writes y.  KEEP true (for the
+// backward): writes each step's starting state and its U instead.
+template <class T, int NB, bool KEEP>
+__device__ __forceinline__ void walk_forward(const DeltaArgs& a, FwdLds<T, NB, KEEP>& s) {
+  typedef FwdLds<T, NB, KEEP> L;
+  constexpr int kThreads = kWaves * 64;
+  constexpr int kM = kExact<T> * kPieces * kPiece, kP = kTwo<T> * kPieces * kPiece;
+  const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
+  const int work = xcd_contiguous(blockIdx.x, gridDim.x);
+  const int per = a.heads * a.slices;
+  const int unit = work / per, h = work % per / a.slices, slice = work % a.slices;
+  const Unit u = locate(a.seqs, unit, a.seg);
+  if (!u.live) return;
+  const bool packed = a.seqs.offsets != nullptr;
+  const int p0 = slice * kThreads / 4;
+  const int col = p0 + wave * 16 + l15;
+  const long of_seq = (static_cast<long>(u.seq) * a.heads + h) * (static_cast<long>(a.states) * a.width);
+  const T* kp = seq_ptr<const T>(a.k, u.seq, u.row0, packed) + h / a.ratio * a.states;
+  const T* qp = seq_ptr<const T>(a.q, u.seq, u.row0, packed) + h / a.ratio * a.states;
+  const T* vp = seq_ptr<const T>(a.v, u.seq, u.row0, packed) + h * a.width;
+  T* yp = seq_ptr<T>(a.y, u.seq, u.row0, packed) + h * a.width;
+
+  State<NB, true> st;
+  st.init(a.width, p0, wave);
+  st.load(a.initial == nullptr ? nullptr : a.initial + of_seq, a.width, a.states);
+
+  const int end = u.len;
+  Tile<T, kTok, NB * 32, kThreads> tk, tq;
+  tk.init(a.k.row_stride, a.states, tid);
+  tq.init(a.q.row_stride, a.states, tid);
+  Flat<kM * sizeof(T), kThreads> tm;
+  Flat<kP * sizeof(T), kThreads> tp;
+  Flat<sizeof(Coef), kThreads> tc;
+  float v[4][4];
+  const unsigned v_off = col < a.width ? static_cast<unsigned>((4 * g * static_cast<int>(a.v.row_stride) + col) * sizeof(T)) : kOutside;
+  const unsigned y_off = col < a.width ? static_cast<unsigned>((4 * g * static_cast<int>(a.y.row_stride) + col) * sizeof(T)) : kOutside;
+  const int v_row = static_cast<int>(a.v.row_stride * sizeof(T)), y_row = static_cast<int>(a.y.row_stride * sizeof(T));
+  const auto fetch = [&](int t) {
+    const int rows = min(end - t, kTok);
+    const long at = step_at(a.seqs, u.seq, t) * a.heads + h;
+    tk.load(rows_rsrc(kp + t * a.k.row_stride, a.k.row_stride, rows, a.states));
+    if (!KEEP) tq.load(rows_rsrc(qp + t * a.q.row_stride, a.q.row_stride, rows, a.states));
+    tm.load(static_cast<const T*>(a.m) + at * kM, tid);
+    if (!KEEP) tp.load(static_cast<const T*>(a.p) + at * kP, tid);
+    tc.load(a.coef + at, tid);
+    const Rsrc rv = rows_rsrc(vp + t * a.v.row_stride, a.v.row_stride, rows, a.width);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[i][r] = load_elem<T>(rv, v_off + (16 * i + r) * v_row);
+  };
+  if (u.t0 < end) fetch(u.t0);
+  for (int t = u.t0; t < end; t += kTok) {
+    __syncthreads();
+    tk.store(s.k, L::ldn, tid);
+    if (!KEEP) tq.store(s.q, L::ldn, tid);
+    tm.store(s.m, tid);
+    if (!KEEP) tp.store(s.p, tid);
+    tc.store(&s.coef, tid);
+    v4f x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = v4f{v[i][0], v[i][1], v[i][2], v[i][3]};
+    __syncthreads();
+    if (t + kTok < end) fetch(t + kTok);
+
+    const long cell = step_at(a.seqs, u.seq, t) * a.heads + h;
+    if (KEEP) st.save(a.keep + cell * (static_cast<long>(a.states) * a.width), a.width, a.states);
+    // K S and Q S
+    v4f ks[4], qs[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ks[i] = qs[i] = v4f{0, 0, 0, 0};
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const Split<T, kExact<T>> sp = split_pair<T, kExact<T>>(st.st[2 * n], st.st[2 * n + 1]);
+      Frag<T> two[kTwo<T>];
+#pragma unroll
+      for (int z = 0; z < kTwo<T>; ++z) two[z] = sp.f[z];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const Frag<T> kf[1] = {frag_row_result(s.k, L::ldn, 16 * i, 32 * n)};
+        mma_parts<T>(ks[i], kf, sp.f);
+        if (!KEEP) {
+          const Frag<T> qf[1] = {frag_row_result(s.q, L::ldn, 16 * i, 32 * n)};
+          mma_parts<T>(qs[i], qf, two);
+        }
+      }
+    }
+    // beta (V - 2^c K S), then U = M that
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = rows_of(s.coef.beta, i, g) * (x[i] - rows_of(s.coef.from, i, g) * ks[i]);
+    const Split<T, kExact<T>> xs[2] = {split_pair<T, kExact<T>>(x[0], x[1]), split_pair<T, kExact<T>>(x[2], x[3])};
+    v4f w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = v4f{0, 0, 0, 0};
+#pragma unroll
+      for (int n = 0; n <= i / 2; ++n) {
+        Frag<T> mf[kExact<T>];
+#pragma unroll
+        for (int z = 0; z < kExact<T>; ++z) mf[z] = piece_get(s.m + (z * kPieces + piece_of(i, n)) * kPiece, lane);
+        mma_parts<T>(w[i], mf, xs[n].f);
+      }
+    }
+    if (KEEP) {
+      save_rows(a.u + cell * (kTok * static_cast<long>(a.width)), a.width, col, g, w);
+    } else {  // Y = scale 2^c Q S + P U
+      const Split<T, kTwo<T>> us[2] = {split_pair<T, kTwo<T>>(w[0], w[1]), split_pair<T, kTwo<T>>(w[2], w[3])};
+      const Rsrc ry = rows_rsrc(yp + t * a.y.row_stride, a.y.row_stride, min(end - t, kTok), a.width);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v4f y = qs[i] * rows_of(s.coef.from, i, g) * a.scale;
+#pragma unroll
+        for (int n = 0; n <= i / 2; ++n) {
+          Frag<T> pf[kTwo<T>];
+#pragma unroll
+          for (int z = 0; z < kTwo<T>; ++z) pf[z] = piece_get(s.p + (z * kPieces + piece_of(i, n)) * kPiece, lane);
+          mma_parts<T>(y, pf, us[n].f);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) store_elem<T>(ry, y_off + (16 * i + r) * y_row, y[r]);
+      }
+    }
+    // S = 2^c_end S + K^T (2^(c_end - c) U); a step's products are added up by
+    // themselves: on top of the state, each would round at the state's size
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = w[i] * rows_of(s.coef.to, i, g);
+    const Split<T, kExact<T>> us[2] = {split_pair<T, kExact<T>>(w[0], w[1]), split_pair<T, kExact<T>>(w[2], w[3])};
+    const float total = s.coef.total;
+#pragma unroll
+    for (int n = 0; n < 2 * NB; ++n) {
+      v4f add = {0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const Frag<T> kf[1] = {frag_col_result(s.k, L::ldn, 32 * j, 16 * n)};
+        mma_parts<T>(add, kf, us[j].f);
+      }
+      st.st[n] = st.st[n] * total + add;
+    }
+  }
+  if (!KEEP && a.final_state != nullptr) st.save(a.final_state + of_seq, a.width, a.states);
+}
+
+template <class T, int NB>
+struct RevLds {
+  static constexpr int ldn = stride_of<T>(NB * 32);
+  alignas(16) T k[kTok * ldn];
+  alignas(16) T q[kTok * ldn];
+  alignas(16) T mt[kExact<T> * kPieces * kPiece];
+  alignas(16) T pt[kExact<T> * kPieces * kPiece];
+  alignas(16) Coef coef;
+};
+
+// The walk of the state's gradient D, from the last step to the first:
+//   dU = P^T dY + 2^(c_end - c) K D,   dR = M^T dU,   dV = beta dR
+//   D  = 2^c_end D + scale Q^T (2^c dY) - K^T (beta 2^c dR)
+// It leaves every step's D (of the state the step ends with) and dR.
+template <class T, int NB>
+__device__ __forceinline__ void walk_reverse(const DeltaArgs& a, RevLds<T, NB>& s) {
+  typedef RevLds<T, NB> L;
+  constexpr int kThreads = kWaves * 64;
+  constexpr int kM = kExact<T> * kPieces * kPiece;
+  const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
+  const int work = xcd_contiguous(blockIdx.x, gridDim.x);
+  const int per = a.heads * a.slices;
+  const int unit = work / per, h = work % per / a.slices, slice = work % a.slices;
+  const Unit u = locate(a.seqs, unit, a.seg);
+  if (!u.live) return;
+  const bool packed = a.seqs.offsets != nullptr;
+  const int p0 = slice * kThreads / 4;
+  const int col = p0 + wave * 16 + l15;
+  const long head = static_cast<long>(a.states) * a.width;
+  const long of_seq = (static_cast<long>(u.seq) * a.heads + h) * head;
+  const T* kp = seq_ptr<const T>(a.k, u.seq, u.row0, packed) + h / a.ratio * a.states;
+  const T* qp = seq_ptr<const T>(a.q, u.seq, u.row0, packed) + h / a.ratio * a.states;
+  const T* yp = seq_ptr<const T>(a.d_y, u.seq, u.row0, packed) + h * a.width;
+  T* vp = seq_ptr<T>(a.d_v, u.seq, u.row0, packed) + h * a.width;
+
+  State<NB, true> st;
+  st.init(a.width, p0, wave);
+  st.load(a.d_final == nullptr ? nullptr : a.d_final + of_seq, a.width, a.states);
+
+  const int end = u.len;
+  Tile<T, kTok, NB * 32, kThreads> tk, tq;
+  tk.init(a.k.row_stride, a.states, tid);
+  tq.init(a.q.row_stride, a.states, tid);
+  Flat<kM * sizeof(T), kThreads> tm, tp;
+  Flat<sizeof(Coef), kThreads> tc;
+  float y[4][4];
+  const unsigned y_off = col < a.width ? static_cast<unsigned>((4 * g * static_cast<int>(a.d_y.row_stride) + col) * sizeof(T)) : kOutside;
+  const unsigned v_off = col < a.width ? static_cast<unsigned>((4 * g * static_cast<int>(a.d_v.row_stride) + col) * sizeof(T)) : kOutside;
+  const int y_row = static_cast<int>(a.d_y.row_stride * sizeof(T)), v_row = static_cast<int>(a.d_v.row_stride * sizeof(T));
+  const auto fetch = [&](int t) {
+    const int rows = min(end - t, kTok);
+    const long at = step_at(a.seqs, u.seq, t) * a.heads + h;
+    tk.load(rows_rsrc(kp + t * a.k.row_stride, a.k.row_stride, rows, a.states));
+    tq.load(rows_rsrc(qp + t * a.q.row_stride, a.q.row_stride, rows, a.states));
+    tm.load(static_cast<const T*>(a.mt) + at * kM, tid);
+    tp.load(static_cast<const T*>(a.pt) + at * kM, tid);
+    tc.load(a.coef + at, tid);
+    const Rsrc ry = rows_rsrc(yp + t * a.d_y.row_stride, a.d_y.row_stride, rows, a.width);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) y[i][r] = load_elem<T>(ry, y_off + (16 * i + r) * y_row);
+  };
+  const int last = end > u.t0 ? u.t0 + (end - 1 - u.t0) / kTok * kTok : u.t0 - kTok;
+  if (last >= u.t0) fetch(last);
+  for (int t = last; t >= u.t0; t -= kTok) {
+    __syncthreads();
+    tk.store(s.k, L::ldn, tid);
+    tq.store(s.q, L::ldn, tid);
+    tm.store(s.mt, tid);
+    tp.store(s.pt, tid);
+    tc.store(&s.coef, tid);
+    v4f dy[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dy[i] = v4f{y[i][0], y[i][1], y[i][2], y[i][3]};
+    __syncthreads();
+    if (t > u.t0) fetch(t - kTok);
+
+    const long cell = step_at(a.seqs, u.seq, t) * a.heads + h;
+    st.save(a.d_keep + cell * head, a.width, a.states);
+    // dU
+    v4f w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = v4f{0, 0, 0, 0};
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const Split<T, kExact<T>> sp = split_pair<T, kExact<T>>(st.st[2 * n], st.st[2 * n + 1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const Frag<T> kf[1] = {frag_row_result(s.k, L::ldn, 16 * i, 32 * n)};
+        mma_parts<T>(w[i], kf, sp.f);
+      }
+    }
+    const Split<T, 1> ys[2] = {split_pair<T, 1>(dy[0], dy[1]), split_pair<T, 1>(dy[2], dy[3])};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = w[i] * rows_of(s.coef.to, i, g);
+#pragma unroll
+      for (int n = i / 2; n < 2; ++n) {
+        Frag<T> pf[kExact<T>];
+#pragma unroll
+        for (int z = 0; z < kExact<T>; ++z) pf[z] = piece_get(s.pt + (z * kPieces + piece_of_t(i, n)) * kPiece, lane);
+        mma_parts<T>(w[i], pf, ys[n].f);
+      }
+    }
+    // dR
+    const Split<T, kExact<T>> us[2] = {split_pair<T, kExact<T>>(w[0], w[1]), split_pair<T, kExact<T>>(w[2], w[3])};
+    v4f dr[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      dr[i] = v4f{0, 0, 0, 0};
+#pragma unroll
+      for (int n = i / 2; n < 2; ++n) {
+        Frag<T> mf[kExact<T>];
+#pragma unroll
+        for (int z = 0; z < kExact<T>; ++z) mf[z] = piece_get(s.mt + (z * kPieces + piece_of_t(i, n)) * kPiece, lane);
+        mma_parts<T>(dr[i], mf, us[n].f);
+      }
+    }
+    save_rows(a.d_r + cell * (kTok * static_cast<long>(a.width)), a.width, col, g, dr);
+    const Rsrc rv = rows_rsrc(vp + t * a.d_v.row_stride, a.d_v.row_stride, min(end - t, kTok), a.width);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const v4f from = rows_of(s.coef.from, i, g);
+      dr[i] = dr[i] * rows_of(s.coef.beta, i, g);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) store_elem<T>(rv, v_off + (16 * i + r) * v_row, dr[i][r]);
+      dr[i] = -from * dr[i];
+      dy[i] = a.scale * (from * dy[i]);
+    }
+    // D
+    const Split<T, kExact<T>> rs[2] = {split_pair<T, kExact<T>>(dr[0], dr[1]), split_pair<T, kExact<T>>(dr[2], dr[3])};
+    const Split<T, kExact<T>> ss[2] = {split_pair<T, kExact<T>>(dy[0], dy[1]), split_pair<T, kExact<T>>(dy[2], dy[3])};
+    const float total = s.coef.total;
+#pragma unroll
+    for (int n = 0; n < 2 * NB; ++n) {
+      v4f add = {0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const Frag<T> kf[1] = {frag_col_result(s.k, L::ldn, 32 * j, 16 * n)};
+        const Frag<T> qf[1] = {frag_col_result(s.q, L::ldn, 32 * j, 16 * n)};
+        mma_parts<T>(add, kf, rs[j].f);
+        mma_parts<T>(add, qf, ss[j].f);
+      }
+      st.st[n] = st.st[n] * total + add;
+    }
+  }
+  if (a.d_initial != nullptr) st.save(a.d_initial + of_seq, a.width, a.states);
+}
+
+}  // namespace delta

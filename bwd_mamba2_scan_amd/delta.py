@@ -36,6 +36,9 @@ SIGNATURES = {
     "mamba2_delta_fwd_workspace_bytes": (_c_size, [Seqs, DeltaDims]),
     "mamba2_delta_fwd": (_c_int, [Seqs, DeltaDims, Rows, Rows, Rows, Rows, Rows, _c_vp, Rows, _c_vp, _c_vp, _c_size,
                                   _c_vp]),
+    "mamba2_delta_bwd_workspace_bytes": (_c_size, [Seqs, DeltaDims]),
+    "mamba2_delta_bwd": (_c_int, [Seqs, DeltaDims, Rows, Rows, Rows, Rows, Rows, _c_vp, Rows, _c_vp, Rows, Rows, Rows,
+                                  Rows, Rows, _c_vp, _c_vp, _c_size, _c_vp]),
     "mamba2_delta_step": (_c_int, [_c_int, DeltaDims, Rows, Rows, Rows, Rows, Rows, _c_vp, Rows, _c_vp, _c_vp]),
 }
 
@@ -99,6 +102,39 @@ def _new_state(t, name, shape, like, dev, wanted=True):
         return None, None
     t = like.new_empty(shape, dtype=_l.torch.float32)
     return t, t.data_ptr()
+
+
+def delta_bwd(q, k, v, g, beta, d_y, *, scale=None, initial_state=None, d_final_state=None, offsets=None, out=None,
+              workspace=None, stream=None):
+    """Gradients of delta_fwd for dL/dy = d_y (and dL/dfinal_state): dict with d_q, d_k, d_v, d_g, d_beta and
+    d_initial_state (None where the forward had none).  `out` may hold some of them, no others.
+    """
+    dev, typ = _start(v, "v")
+    f32 = _l.torch.float32
+    seqs, lead, batch = _seqs(v, offsets, 2, dev, "v")
+    d = _delta_dims(typ, q, v, g, scale)
+    pq, pk, pv, pg, pb = _delta_inputs(q, k, v, g, beta, lead, d, dev)
+    inner, shared, vec = (d.heads, d.width), (d.groups, d.states), (d.heads,)
+    shape = (batch, d.heads, d.states, d.width)
+    py = _rows(d_y, "d_y", lead, inner, v.dtype, dev)
+    s0 = _dense(initial_state, "initial_state", shape, f32, dev)
+    sf = _dense(d_final_state, "d_final_state", shape, f32, dev)
+    res = _given(out, d_q=True, d_k=True, d_v=True, d_g=True, d_beta=True, d_initial_state=initial_state)
+    _apart(tuple(res.items()) + (("workspace", workspace),),
+           (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("d_y", d_y), ("initial_state", initial_state),
+            ("d_final_state", d_final_state), ("offsets", offsets)))
+    with _On(dev, stream) as s:
+        ptr = []
+        for name, size, like in (("d_q", shared, v), ("d_k", shared, v), ("d_v", inner, v), ("d_g", vec, g),
+                                 ("d_beta", vec, g)):
+            res[name], p = _new_rows(res.get(name), name, lead, size, like, dev)
+            ptr.append(p)
+        res["d_initial_state"], s1 = _new_state(res.get("d_initial_state"), "d_initial_state", shape, v, dev,
+                                                initial_state is not None)
+        workspace, nbytes = _workspace(workspace, _l.lib.mamba2_delta_bwd_workspace_bytes(seqs, d), v, dev)
+        st = _l.lib.mamba2_delta_bwd(seqs, d, pq, pk, pv, pg, pb, s0, py, sf, *ptr, s1, _ptr(workspace), nbytes, s)
+    _raise(st, "mamba2_delta_bwd")
+    return res
 
 
 def delta_step(q, k, v, g, beta, state, *, scale=None, new_state=None, y=None, stream=None):
