@@ -26,7 +26,7 @@ import os
 import re
 
 from . import delta, layer
-from .delta import delta_bwd, delta_fwd, delta_step  # noqa: F401
+from .delta import delta_bwd, delta_fwd, delta_step, group_norm_bwd, group_norm_fwd  # noqa: F401
 from .layer import clip_grads, conv_bwd, conv_fwd, conv_step, grad_norm, ssm_bwd, ssm_fwd, ssm_step  # noqa: F401
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))

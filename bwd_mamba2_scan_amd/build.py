@@ -13,7 +13,8 @@ import tempfile
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
-SOURCES = ("mamba2_scan.hip", "conv.hip", "grad_clip.hip", "ssm.hip", "ssm_bwd.hip", "delta.hip", "delta_bwd.hip")
+SOURCES = ("mamba2_scan.hip", "conv.hip", "grad_clip.hip", "ssm.hip", "ssm_bwd.hip", "delta.hip", "delta_bwd.hip",
+           "norm.hip")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libmamba2scan.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)

@@ -33,6 +33,10 @@ class NormDims(ctypes.Structure):
 PLAIN, SILU, GATED, GATE_FIRST = 0, 1, 2, 3  # MAMBA2_NORM_*
 
 SIGNATURES = {
+    "mamba2_norm_fwd": (_c_int, [Seqs, NormDims, Rows, _c_vp, _c_vp, Rows, Rows, _c_vp]),
+    "mamba2_norm_bwd_workspace_bytes": (_c_size, [Seqs, NormDims]),
+    "mamba2_norm_bwd": (_c_int, [Seqs, NormDims, Rows, _c_vp, _c_vp, Rows, Rows, Rows, _c_vp, _c_vp, Rows, _c_vp,
+                                 _c_size, _c_vp]),
     "mamba2_delta_fwd_workspace_bytes": (_c_size, [Seqs, DeltaDims]),
     "mamba2_delta_fwd": (_c_int, [Seqs, DeltaDims, Rows, Rows, Rows, Rows, Rows, _c_vp, Rows, _c_vp, _c_vp, _c_size,
                                   _c_vp]),
@@ -165,3 +169,98 @@ def delta_step(q, k, v, g, beta, state, *, scale=None, new_state=None, y=None, s
         raise ValueError("y or new_state overlaps another tensor of the call")
     _raise(st, "mamba2_delta_step")
     return y
+
+
+# ---------------------------------------------------------------- group norm
+_NONE = Rows(None, 0, 0)
+
+
+def _norm(x, weight, bias, groups, gate, gate_first, silu, centered, eps, offsets):
+    """A call's device, dims, sequences, leading shape, channels and parameters."""
+    dev, typ = _start(x)
+    if offsets is None and x.dim() == 2:  # rows of one sequence
+        channels = x.shape[1]
+        _sizes(*x.shape)
+        seqs, lead = Seqs(1, x.shape[0], None), (x.shape[0],)
+    else:
+        seqs, lead, _ = _seqs(x, offsets, 1, dev)
+        channels = x.shape[-1]
+        _sizes(channels)
+    groups = int(groups)
+    if groups < 1 or channels % groups:
+        raise ValueError(f"{channels} channels do not divide into {groups} groups")
+    if gate is None:
+        if gate_first:
+            raise ValueError("gate_first needs a gate")
+        form = SILU if silu else PLAIN
+    else:
+        if silu:
+            raise ValueError("silu is the activation of a norm without a gate")
+        form = GATE_FIRST if gate_first else GATED
+    width = channels // groups
+    w = b = None
+    shape = (channels,)
+    if weight is not None:
+        _gpu(weight, "weight", dev)
+        if groups > 1 and weight.shape == (width,):
+            shape = (width,)
+        w = _dense(weight, "weight", shape, _l.torch.float32, dev)
+    if bias is not None:
+        if weight is None:
+            raise ValueError("a bias needs a weight")
+        b = _dense(bias, "bias", shape, _l.torch.float32, dev)
+    d = NormDims(typ, groups, width, form, bool(centered), shape != (channels,), eps)
+    z = _NONE if gate is None else _rows(gate, "gate", lead, (channels,), x.dtype, dev)
+    return dev, d, seqs, lead, channels, shape, w, b, z
+
+
+def group_norm_fwd(x, weight=None, bias=None, *, groups=1, gate=None, gate_first=False, silu=False, centered=False,
+                   eps=1e-5, offsets=None, y=None, stream=None):
+    """Group norm with an activation, channels last: for every token and group of channels
+
+        n = (h - mean) / sqrt(mean((h - mean)^2) + eps),  o = n weight + bias
+
+    x [batch, length, channels], [rows, channels], or packed rows with offsets,
+    float32 or bfloat16.  mean is the group's with centered, 0 without.  h is
+    x and the result o, silu(o) with silu, o silu(gate) with a gate; with
+    gate_first h is x silu(gate) instead.  gate has x's type and shape; weight
+    and bias are float32, [channels], or [channels / groups] for every group.
+    Rows outside the sequences that offsets names are neither read nor written.
+    """
+    dev, d, seqs, lead, channels, _, w, b, z = _norm(x, weight, bias, groups, gate, gate_first, silu, centered, eps,
+                                                     offsets)
+    rx = _rows(x, "x", lead, (channels,), x.dtype, dev)
+    if y is not None:
+        _apart((("y", y),), (("x", x), ("weight", weight), ("bias", bias), ("gate", gate), ("offsets", offsets)))
+    with _On(dev, stream) as s:
+        y, ry = _new_rows(y, "y", lead, (channels,), x, dev)
+        st = _l.lib.mamba2_norm_fwd(seqs, d, rx, w, b, z, ry, s)
+    _raise(st, "mamba2_norm_fwd")
+    return y
+
+
+def group_norm_bwd(x, d_y, weight=None, bias=None, *, groups=1, gate=None, gate_first=False, silu=False,
+                   centered=False, eps=1e-5, offsets=None, out=None, workspace=None, stream=None):
+    """Gradients of group_norm_fwd for dL/dy = d_y: dict with d_x, d_weight, d_bias and d_gate (None where the forward
+    had no such input).  `out` may hold some of them, no others.
+    """
+    dev, d, seqs, lead, channels, shape, w, b, z = _norm(x, weight, bias, groups, gate, gate_first, silu, centered,
+                                                         eps, offsets)
+    rx = _rows(x, "x", lead, (channels,), x.dtype, dev)
+    rg = _rows(d_y, "d_y", lead, (channels,), x.dtype, dev)
+    res = _given(out, d_x=True, d_weight=weight, d_bias=bias, d_gate=gate)
+    _apart(tuple(res.items()) + (("workspace", workspace),),
+           (("x", x), ("weight", weight), ("bias", bias), ("gate", gate), ("d_y", d_y), ("offsets", offsets)))
+    with _On(dev, stream) as s:
+        get = res.get
+        res["d_x"], r1 = _new_rows(get("d_x"), "d_x", lead, (channels,), x, dev)
+        res["d_weight"], w1 = (_new_dense(get("d_weight"), "d_weight", shape, weight, dev)
+                               if weight is not None else (None, None))
+        res["d_bias"], b1 = _new_dense(get("d_bias"), "d_bias", shape, bias, dev) if bias is not None else (None, None)
+        res["d_gate"], z1 = (_new_rows(get("d_gate"), "d_gate", lead, (channels,), x, dev)
+                             if gate is not None else (None, _NONE))
+        need = 0 if weight is None else _l.lib.mamba2_norm_bwd_workspace_bytes(seqs, d)
+        workspace, nbytes = _workspace(workspace, need, x, dev)
+        st = _l.lib.mamba2_norm_bwd(seqs, d, rx, w, b, z, rg, r1, w1, b1, z1, _ptr(workspace), nbytes, s)
+    _raise(st, "mamba2_norm_bwd")
+    return res
