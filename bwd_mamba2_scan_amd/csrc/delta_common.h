@@ -67,18 +67,29 @@ struct DeltaArgs {
   float* d_r;              // the same: the gradient of beta (V - 2^c K S)
 };
 
-// Number of the step that starts at token t of a sequence.
-__device__ __forceinline__ long step_at(const mamba2_seqs& q, int seq, int t) {
-  return static_cast<long>(unit_base(q, seq, kTok)) + t / kTok;
-}
 
+// An element as it was loaded, and its value.  Values are formed where they are
+// used: forming one waits for its load.
+template <class T>
+struct Raw {
+  int v;
+};
+template <>
+struct Raw<bf16> {
+  short v;
+};
+template <class T>
+__device__ __forceinline__ Raw<T> load_raw_elem(Rsrc rs, unsigned off) {
+  if constexpr (sizeof(T) == 2) return {static_cast<short>(__builtin_amdgcn_raw_buffer_load_b16(rs, off, 0, 0))};
+  else return {static_cast<int>(__builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0))};
+}
+__device__ __forceinline__ float value_of(Raw<bf16> r) {
+  return __uint_as_float(static_cast<unsigned>(static_cast<unsigned short>(r.v)) << 16);
+}
+__device__ __forceinline__ float value_of(Raw<float> r) { return __int_as_float(r.v); }
 template <class T>
 __device__ __forceinline__ float load_elem(Rsrc rs, unsigned off) {
-  if constexpr (sizeof(T) == 2)
-    return __builtin_bit_cast(float, static_cast<unsigned>(static_cast<unsigned short>(
-                                         __builtin_amdgcn_raw_buffer_load_b16(rs, off, 0, 0))) << 16);
-  else
-    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0));
+  return value_of(load_raw_elem<T>(rs, off));
 }
 template <class T>
 __device__ __forceinline__ void store_elem(Rsrc rs, unsigned off, float v) {
@@ -138,6 +149,45 @@ __device__ __forceinline__ void mma_parts(v4f& acc, const Frag<T> (&a)[A], const
     for (int i = 0; i <= n; ++i)
       if (i < A && n - i < B) mma(acc, a[i], b[n - i]);
 }
+
+// acc += A b for a 64 x 64 lower triangular A in pieces and a b of 64 rows, in
+// parts, small products first; neighbouring products are on different tiles, as
+// one waits for the last one on its own.  TRANSPOSED: acc += (A b)^T.
+template <class T, int A, int B, bool TRANSPOSED = false>
+__device__ __forceinline__ void mma_lower(v4f (&acc)[4], const Frag<T> (&a)[A][kPieces], const Split<T, B> (&b)[2]) {
+  constexpr int kMost = A > B ? A : B;
+#pragma unroll
+  for (int n = kMost - 1; n >= 0; --n)
+#pragma unroll
+    for (int z = 0; z <= n; ++z)
+      if (z < A && n - z < B) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int i = 2 * s; i < 4; ++i) {
+            if (TRANSPOSED) mma(acc[i], b[s].f[n - z], a[z][piece_of(i, s)]);
+            else mma(acc[i], a[z][piece_of(i, s)], b[s].f[n - z]);
+          }
+      }
+}
+// The same for an upper triangular A (a transpose's pieces).
+template <class T, int A, int B>
+__device__ __forceinline__ void mma_upper(v4f (&acc)[4], const Frag<T> (&a)[A][kPieces], const Split<T, B> (&b)[2]) {
+  constexpr int kMost = A > B ? A : B;
+#pragma unroll
+  for (int n = kMost - 1; n >= 0; --n)
+#pragma unroll
+    for (int z = 0; z <= n; ++z)
+      if (z < A && n - z < B) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int i = 0; i < 2 * s + 2; ++i) mma(acc[i], a[z][piece_of_t(i, s)], b[s].f[n - z]);
+      }
+}
+
+// Reads of LDS stay on their side of this; everything else may be moved over it.
+__device__ __forceinline__ void keep_reads_here() { __builtin_amdgcn_sched_barrier(0x7f); }
 
 // Four values of rows 4 g .. of tile i, of an array by token.
 __device__ __forceinline__ v4f rows_of(const float* p, int i, int g) {

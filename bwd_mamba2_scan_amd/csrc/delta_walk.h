@@ -38,12 +38,29 @@ __device__ __forceinline__ void save_rows(float* p, int width, int col, int g, c
     for (int r = 0; r < 4; ++r) store_elem<float>(rs, off + (16 * i + r) * width * 4, w[i][r]);
 }
 
+constexpr int kCols = kWaves * 16;
+
+// Four rows 4 g .. of column l15 of tile i of an LDS tile of tokens.
+__device__ __forceinline__ v4f tile_col(const bf16* p, int ld, int i, int col, int lane) {
+  const v4s r = read_tr(p + (16 * i + 4 * (lane >> 4) + ((lane & 15) >> 2)) * ld + col + 4 * (lane & 3));
+  v4f v;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(static_cast<unsigned>(static_cast<unsigned short>(r[j])) << 16);
+  return v;
+}
+__device__ __forceinline__ v4f tile_col(const float* p, int ld, int i, int col, int lane) {
+  const float* r = p + (16 * i + 4 * (lane >> 4)) * ld + col + (lane & 15);
+  return v4f{r[0], r[ld], r[2 * ld], r[3 * ld]};
+}
+
 template <class T, int NB, bool KEEP>
 struct FwdLds {
   static constexpr int ldn = stride_of<T>(NB * 32);
+  static constexpr int ldv = stride_of<T>(kCols);
   alignas(16) T k[kTok * ldn];
   alignas(16) T m[kExact<T> * kPieces * kPiece];
   alignas(16) Coef coef;
+  alignas(16) T v[kTok * ldv];
   alignas(16) T q[KEEP ? 8 : kTok * ldn];
   alignas(16) T p[KEEP ? 8 : kTwo<T> * kPieces * kPiece];
 };
@@ -67,7 +84,7 @@ __device__ __forceinline__ void walk_forward(const DeltaArgs& a, FwdLds<T, NB, K
   const long of_seq = (static_cast<long>(u.seq) * a.heads + h) * (static_cast<long>(a.states) * a.width);
   const T* kp = seq_ptr<const T>(a.k, u.seq, u.row0, packed) + h / a.ratio * a.states;
   const T* qp = seq_ptr<const T>(a.q, u.seq, u.row0, packed) + h / a.ratio * a.states;
-  const T* vp = seq_ptr<const T>(a.v, u.seq, u.row0, packed) + h * a.width;
+  const T* vp = seq_ptr<const T>(a.v, u.seq, u.row0, packed) + h * a.width + p0;
   T* yp = seq_ptr<T>(a.y, u.seq, u.row0, packed) + h * a.width;
 
   State<NB, true> st;
@@ -75,29 +92,28 @@ __device__ __forceinline__ void walk_forward(const DeltaArgs& a, FwdLds<T, NB, K
   st.load(a.initial == nullptr ? nullptr : a.initial + of_seq, a.width, a.states);
 
   const int end = u.len;
+  const long cell0 = static_cast<long>(unit_base(a.seqs, u.seq, kTok)) * a.heads + h;  // of the sequence's first step
   Tile<T, kTok, NB * 32, kThreads> tk, tq;
   tk.init(a.k.row_stride, a.states, tid);
   tq.init(a.q.row_stride, a.states, tid);
   Flat<kM * sizeof(T), kThreads> tm;
   Flat<kP * sizeof(T), kThreads> tp;
   Flat<sizeof(Coef), kThreads> tc;
-  float v[4][4];
-  const unsigned v_off = col < a.width ? static_cast<unsigned>((4 * g * static_cast<int>(a.v.row_stride) + col) * sizeof(T)) : kOutside;
-  const unsigned y_off = col < a.width ? static_cast<unsigned>((4 * g * static_cast<int>(a.y.row_stride) + col) * sizeof(T)) : kOutside;
-  const int v_row = static_cast<int>(a.v.row_stride * sizeof(T)), y_row = static_cast<int>(a.y.row_stride * sizeof(T));
+  Tile<T, kTok, kCols, kThreads> tv;
+  tv.init(a.v.row_stride, min(a.width - p0, kCols), tid);
+  // y^T: this lane's token of each tile, four columns
+  const int quad = p0 + wave * 16 + 4 * g;
+  const unsigned y_off = quad < a.width ? static_cast<unsigned>((l15 * static_cast<int>(a.y.row_stride) + quad) * sizeof(T)) : kOutside;
+  const int y16 = static_cast<int>(16 * a.y.row_stride * sizeof(T));
   const auto fetch = [&](int t) {
     const int rows = min(end - t, kTok);
-    const long at = step_at(a.seqs, u.seq, t) * a.heads + h;
+    const long at = cell0 + static_cast<long>(t / kTok) * a.heads;
     tk.load(rows_rsrc(kp + t * a.k.row_stride, a.k.row_stride, rows, a.states));
     if (!KEEP) tq.load(rows_rsrc(qp + t * a.q.row_stride, a.q.row_stride, rows, a.states));
     tm.load(static_cast<const T*>(a.m) + at * kM, tid);
     if (!KEEP) tp.load(static_cast<const T*>(a.p) + at * kP, tid);
     tc.load(a.coef + at, tid);
-    const Rsrc rv = rows_rsrc(vp + t * a.v.row_stride, a.v.row_stride, rows, a.width);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) v[i][r] = load_elem<T>(rv, v_off + (16 * i + r) * v_row);
+    tv.load(rows_rsrc(vp + t * a.v.row_stride, a.v.row_stride, rows, min(a.width - p0, kCols)));
   };
   if (u.t0 < end) fetch(u.t0);
   for (int t = u.t0; t < end; t += kTok) {
@@ -107,84 +123,121 @@ __device__ __forceinline__ void walk_forward(const DeltaArgs& a, FwdLds<T, NB, K
     tm.store(s.m, tid);
     if (!KEEP) tp.store(s.p, tid);
     tc.store(&s.coef, tid);
-    v4f x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = v4f{v[i][0], v[i][1], v[i][2], v[i][3]};
+    tv.store(s.v, L::ldv, tid);
     __syncthreads();
     if (t + kTok < end) fetch(t + kTok);
 
-    const long cell = step_at(a.seqs, u.seq, t) * a.heads + h;
+    const long cell = cell0 + static_cast<long>(t / kTok) * a.heads;
     if (KEEP) st.save(a.keep + cell * (static_cast<long>(a.states) * a.width), a.width, a.states);
-    // K S and Q S
+    // K S and (Q S)^T.  The operands of a part are read from LDS while the part
+    // before it is multiplied: one wave a SIMD hides no latency by itself.
+    constexpr int kBuf = NB > 1 ? 2 : 1;
+    Frag<T> kf[kBuf][4], qf[kBuf][4];
+    Frag<T> mf[kExact<T>][kPieces];
+    const auto read_rows = [&](int n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        kf[n % kBuf][i] = frag_row_result(s.k, L::ldn, 16 * i, 32 * n);
+        if (!KEEP) qf[n % kBuf][i] = frag_row_result(s.q, L::ldn, 16 * i, 32 * n);
+      }
+    };
     v4f ks[4], qs[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) ks[i] = qs[i] = v4f{0, 0, 0, 0};
+    read_rows(0);
+    v4f from[4], beta[4], to[4], x[4];
+    float mine[4];  // scale 2^c of this lane's token of each tile
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
+      if (n + 1 < NB) {
+        read_rows(n + 1);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          beta[i] = rows_of(s.coef.beta, i, g);
+          from[i] = rows_of(s.coef.from, i, g);
+          x[i] = tile_col(s.v, L::ldv, i, wave * 16, lane);
+        }
+#pragma unroll
+        for (int z = 0; z < kExact<T>; ++z)
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) mf[z][i] = piece_get(s.m + (z * kPieces + i) * kPiece, lane);
+      }
+      keep_reads_here();
       const Split<T, kExact<T>> sp = split_pair<T, kExact<T>>(st.st[2 * n], st.st[2 * n + 1]);
-      Frag<T> two[kTwo<T>];
 #pragma unroll
-      for (int z = 0; z < kTwo<T>; ++z) two[z] = sp.f[z];
+      for (int z = kExact<T> - 1; z >= 0; --z) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const Frag<T> kf[1] = {frag_row_result(s.k, L::ldn, 16 * i, 32 * n)};
-        mma_parts<T>(ks[i], kf, sp.f);
-        if (!KEEP) {
-          const Frag<T> qf[1] = {frag_row_result(s.q, L::ldn, 16 * i, 32 * n)};
-          mma_parts<T>(qs[i], qf, two);
+        for (int i = 0; i < 4; ++i) mma(ks[i], kf[n % kBuf][i], sp.f[z]);
+        if (!KEEP && z < kTwo<T>) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mma(qs[i], sp.f[z], qf[n % kBuf][i]);
         }
       }
     }
     // beta (V - 2^c K S), then U = M that
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = rows_of(s.coef.beta, i, g) * (x[i] - rows_of(s.coef.from, i, g) * ks[i]);
+    for (int i = 0; i < 4; ++i) x[i] = beta[i] * (x[i] - from[i] * ks[i]);
     const Split<T, kExact<T>> xs[2] = {split_pair<T, kExact<T>>(x[0], x[1]), split_pair<T, kExact<T>>(x[2], x[3])};
-    v4f w[4];
+    Frag<T> pf[kTwo<T>][kPieces];
+    if (!KEEP) {
+#pragma unroll
+      for (int z = 0; z < kTwo<T>; ++z)
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) pf[z][i] = piece_get(s.p + (z * kPieces + i) * kPiece, lane);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w[i] = v4f{0, 0, 0, 0};
-#pragma unroll
-      for (int n = 0; n <= i / 2; ++n) {
-        Frag<T> mf[kExact<T>];
-#pragma unroll
-        for (int z = 0; z < kExact<T>; ++z) mf[z] = piece_get(s.m + (z * kPieces + piece_of(i, n)) * kPiece, lane);
-        mma_parts<T>(w[i], mf, xs[n].f);
-      }
+      to[i] = rows_of(s.coef.to, i, g);
+      if (!KEEP) mine[i] = a.scale * s.coef.from[16 * i + l15];
     }
+    keep_reads_here();
+    v4f w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = v4f{0, 0, 0, 0};
+    mma_lower<T, kExact<T>, kExact<T>>(w, mf, xs);
+    // the left operands of the state's products, four tiles at a time
+    constexpr int kTiles = 2 * NB < 4 ? 2 * NB : 4;
+    Frag<T> cf[2][kTiles];
+    const auto read_cols = [&](int n) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) cf[j][i] = frag_col_result(s.k, L::ldn, 32 * j, 16 * (n + i));
+    };
+    read_cols(0);
+    keep_reads_here();
     if (KEEP) {
       save_rows(a.u + cell * (kTok * static_cast<long>(a.width)), a.width, col, g, w);
-    } else {  // Y = scale 2^c Q S + P U
+    } else {  // Y^T = (scale 2^c Q S)^T + U^T P^T
       const Split<T, kTwo<T>> us[2] = {split_pair<T, kTwo<T>>(w[0], w[1]), split_pair<T, kTwo<T>>(w[2], w[3])};
       const Rsrc ry = rows_rsrc(yp + t * a.y.row_stride, a.y.row_stride, min(end - t, kTok), a.width);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v4f y = qs[i] * rows_of(s.coef.from, i, g) * a.scale;
+      for (int i = 0; i < 4; ++i) qs[i] = qs[i] * mine[i];
+      mma_lower<T, kTwo<T>, kTwo<T>, true>(qs, pf, us);
 #pragma unroll
-        for (int n = 0; n <= i / 2; ++n) {
-          Frag<T> pf[kTwo<T>];
-#pragma unroll
-          for (int z = 0; z < kTwo<T>; ++z) pf[z] = piece_get(s.p + (z * kPieces + piece_of(i, n)) * kPiece, lane);
-          mma_parts<T>(y, pf, us[n].f);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) store_elem<T>(ry, y_off + (16 * i + r) * y_row, y[r]);
-      }
+      for (int i = 0; i < 4; ++i) Quad<T>::store(ry, y_off + i * y16, qs[i]);
     }
     // S = 2^c_end S + K^T (2^(c_end - c) U); a step's products are added up by
     // themselves: on top of the state, each would round at the state's size
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = w[i] * rows_of(s.coef.to, i, g);
+    for (int i = 0; i < 4; ++i) w[i] = w[i] * to[i];
     const Split<T, kExact<T>> us[2] = {split_pair<T, kExact<T>>(w[0], w[1]), split_pair<T, kExact<T>>(w[2], w[3])};
     const float total = s.coef.total;
 #pragma unroll
-    for (int n = 0; n < 2 * NB; ++n) {
-      v4f add = {0, 0, 0, 0};
+    for (int n = 0; n < 2 * NB; n += kTiles) {
+      v4f add[kTiles];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const Frag<T> kf[1] = {frag_col_result(s.k, L::ldn, 32 * j, 16 * n)};
-        mma_parts<T>(add, kf, us[j].f);
-      }
-      st.st[n] = st.st[n] * total + add;
+      for (int i = 0; i < kTiles; ++i) add[i] = v4f{0, 0, 0, 0};
+#pragma unroll
+      for (int z = kExact<T> - 1; z >= 0; --z)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i) mma(add[i], cf[j][i], us[j].f[z]);
+      if (n + kTiles < 2 * NB) read_cols(n + kTiles);
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) st.st[n + i] = st.st[n + i] * total + add[i];
     }
   }
   if (!KEEP && a.final_state != nullptr) st.save(a.final_state + of_seq, a.width, a.states);
@@ -197,7 +250,9 @@ struct RevLds {
   alignas(16) T q[kTok * ldn];
   alignas(16) T mt[kExact<T> * kPieces * kPiece];
   alignas(16) T pt[kExact<T> * kPieces * kPiece];
+  alignas(16) T y[kTok * stride_of<T>(kCols)];
   alignas(16) Coef coef;
+  static constexpr int ldv = stride_of<T>(kCols);
 };
 
 // The walk of the state's gradient D, from the last step to the first:
@@ -222,7 +277,7 @@ __device__ __forceinline__ void walk_reverse(const DeltaArgs& a, RevLds<T, NB>& 
   const long of_seq = (static_cast<long>(u.seq) * a.heads + h) * head;
   const T* kp = seq_ptr<const T>(a.k, u.seq, u.row0, packed) + h / a.ratio * a.states;
   const T* qp = seq_ptr<const T>(a.q, u.seq, u.row0, packed) + h / a.ratio * a.states;
-  const T* yp = seq_ptr<const T>(a.d_y, u.seq, u.row0, packed) + h * a.width;
+  const T* yp = seq_ptr<const T>(a.d_y, u.seq, u.row0, packed) + h * a.width + p0;
   T* vp = seq_ptr<T>(a.d_v, u.seq, u.row0, packed) + h * a.width;
 
   State<NB, true> st;
@@ -230,28 +285,25 @@ __device__ __forceinline__ void walk_reverse(const DeltaArgs& a, RevLds<T, NB>& 
   st.load(a.d_final == nullptr ? nullptr : a.d_final + of_seq, a.width, a.states);
 
   const int end = u.len;
+  const long cell0 = static_cast<long>(unit_base(a.seqs, u.seq, kTok)) * a.heads + h;  // of the sequence's first step
   Tile<T, kTok, NB * 32, kThreads> tk, tq;
   tk.init(a.k.row_stride, a.states, tid);
   tq.init(a.q.row_stride, a.states, tid);
   Flat<kM * sizeof(T), kThreads> tm, tp;
   Flat<sizeof(Coef), kThreads> tc;
-  float y[4][4];
-  const unsigned y_off = col < a.width ? static_cast<unsigned>((4 * g * static_cast<int>(a.d_y.row_stride) + col) * sizeof(T)) : kOutside;
+  Tile<T, kTok, kCols, kThreads> ty;
+  ty.init(a.d_y.row_stride, min(a.width - p0, kCols), tid);
   const unsigned v_off = col < a.width ? static_cast<unsigned>((4 * g * static_cast<int>(a.d_v.row_stride) + col) * sizeof(T)) : kOutside;
-  const int y_row = static_cast<int>(a.d_y.row_stride * sizeof(T)), v_row = static_cast<int>(a.d_v.row_stride * sizeof(T));
+  const int v_row = static_cast<int>(a.d_v.row_stride * sizeof(T));
   const auto fetch = [&](int t) {
     const int rows = min(end - t, kTok);
-    const long at = step_at(a.seqs, u.seq, t) * a.heads + h;
+    const long at = cell0 + static_cast<long>(t / kTok) * a.heads;
     tk.load(rows_rsrc(kp + t * a.k.row_stride, a.k.row_stride, rows, a.states));
     tq.load(rows_rsrc(qp + t * a.q.row_stride, a.q.row_stride, rows, a.states));
     tm.load(static_cast<const T*>(a.mt) + at * kM, tid);
     tp.load(static_cast<const T*>(a.pt) + at * kM, tid);
     tc.load(a.coef + at, tid);
-    const Rsrc ry = rows_rsrc(yp + t * a.d_y.row_stride, a.d_y.row_stride, rows, a.width);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) y[i][r] = load_elem<T>(ry, y_off + (16 * i + r) * y_row);
+    ty.load(rows_rsrc(yp + t * a.d_y.row_stride, a.d_y.row_stride, rows, min(a.width - p0, kCols)));
   };
   const int last = end > u.t0 ? u.t0 + (end - 1 - u.t0) / kTok * kTok : u.t0 - kTok;
   if (last >= u.t0) fetch(last);
@@ -262,79 +314,111 @@ __device__ __forceinline__ void walk_reverse(const DeltaArgs& a, RevLds<T, NB>& 
     tm.store(s.mt, tid);
     tp.store(s.pt, tid);
     tc.store(&s.coef, tid);
-    v4f dy[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) dy[i] = v4f{y[i][0], y[i][1], y[i][2], y[i][3]};
+    ty.store(s.y, L::ldv, tid);
     __syncthreads();
     if (t > u.t0) fetch(t - kTok);
 
-    const long cell = step_at(a.seqs, u.seq, t) * a.heads + h;
+    const long cell = cell0 + static_cast<long>(t / kTok) * a.heads;
     st.save(a.d_keep + cell * head, a.width, a.states);
     // dU
-    v4f w[4];
+    constexpr int kBuf = NB > 1 ? 2 : 1;
+    Frag<T> kf[kBuf][4];
+    Frag<T> mf[kExact<T>][kPieces];
+    const auto read_rows = [&](int n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) kf[n % kBuf][i] = frag_row_result(s.k, L::ldn, 16 * i, 32 * n);
+    };
+    const auto read_pieces = [&](const T* p) {
+#pragma unroll
+      for (int z = 0; z < kExact<T>; ++z)
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) mf[z][i] = piece_get(p + (z * kPieces + i) * kPiece, lane);
+    };
+    v4f w[4], to[4], from[4], beta[4], dy[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = v4f{0, 0, 0, 0};
+    read_rows(0);
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
+      if (n + 1 < NB) {
+        read_rows(n + 1);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          to[i] = rows_of(s.coef.to, i, g);
+          dy[i] = tile_col(s.y, L::ldv, i, wave * 16, lane);
+        }
+        read_pieces(s.pt);
+      }
+      keep_reads_here();
       const Split<T, kExact<T>> sp = split_pair<T, kExact<T>>(st.st[2 * n], st.st[2 * n + 1]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const Frag<T> kf[1] = {frag_row_result(s.k, L::ldn, 16 * i, 32 * n)};
-        mma_parts<T>(w[i], kf, sp.f);
-      }
+      for (int z = kExact<T> - 1; z >= 0; --z)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mma(w[i], kf[n % kBuf][i], sp.f[z]);
     }
     const Split<T, 1> ys[2] = {split_pair<T, 1>(dy[0], dy[1]), split_pair<T, 1>(dy[2], dy[3])};
 #pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = w[i] * to[i];
+    mma_upper<T, kExact<T>, 1>(w, mf, ys);
+    keep_reads_here();
+    read_pieces(s.mt);
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w[i] = w[i] * rows_of(s.coef.to, i, g);
-#pragma unroll
-      for (int n = i / 2; n < 2; ++n) {
-        Frag<T> pf[kExact<T>];
-#pragma unroll
-        for (int z = 0; z < kExact<T>; ++z) pf[z] = piece_get(s.pt + (z * kPieces + piece_of_t(i, n)) * kPiece, lane);
-        mma_parts<T>(w[i], pf, ys[n].f);
-      }
+      from[i] = rows_of(s.coef.from, i, g);
+      beta[i] = rows_of(s.coef.beta, i, g);
     }
+    keep_reads_here();
     // dR
     const Split<T, kExact<T>> us[2] = {split_pair<T, kExact<T>>(w[0], w[1]), split_pair<T, kExact<T>>(w[2], w[3])};
     v4f dr[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      dr[i] = v4f{0, 0, 0, 0};
+    for (int i = 0; i < 4; ++i) dr[i] = v4f{0, 0, 0, 0};
+    mma_upper<T, kExact<T>, kExact<T>>(dr, mf, us);
+    constexpr int kTiles = 2 * NB < 4 ? 2 * NB : 4;
+    Frag<T> cf[2][kTiles], df[2][kTiles];
+    const auto read_cols = [&](int n) {
 #pragma unroll
-      for (int n = i / 2; n < 2; ++n) {
-        Frag<T> mf[kExact<T>];
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int z = 0; z < kExact<T>; ++z) mf[z] = piece_get(s.mt + (z * kPieces + piece_of_t(i, n)) * kPiece, lane);
-        mma_parts<T>(dr[i], mf, us[n].f);
-      }
-    }
+        for (int i = 0; i < kTiles; ++i) {
+          df[j][i] = frag_col_result(s.q, L::ldn, 32 * j, 16 * (n + i));
+          cf[j][i] = frag_col_result(s.k, L::ldn, 32 * j, 16 * (n + i));
+        }
+    };
+    read_cols(0);
+    keep_reads_here();
     save_rows(a.d_r + cell * (kTok * static_cast<long>(a.width)), a.width, col, g, dr);
     const Rsrc rv = rows_rsrc(vp + t * a.d_v.row_stride, a.d_v.row_stride, min(end - t, kTok), a.width);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const v4f from = rows_of(s.coef.from, i, g);
-      dr[i] = dr[i] * rows_of(s.coef.beta, i, g);
+      dr[i] = dr[i] * beta[i];
 #pragma unroll
       for (int r = 0; r < 4; ++r) store_elem<T>(rv, v_off + (16 * i + r) * v_row, dr[i][r]);
-      dr[i] = -from * dr[i];
-      dy[i] = a.scale * (from * dy[i]);
+      dr[i] = -from[i] * dr[i];
+      dy[i] = a.scale * (from[i] * dy[i]);
     }
     // D
     const Split<T, kExact<T>> rs[2] = {split_pair<T, kExact<T>>(dr[0], dr[1]), split_pair<T, kExact<T>>(dr[2], dr[3])};
     const Split<T, kExact<T>> ss[2] = {split_pair<T, kExact<T>>(dy[0], dy[1]), split_pair<T, kExact<T>>(dy[2], dy[3])};
     const float total = s.coef.total;
 #pragma unroll
-    for (int n = 0; n < 2 * NB; ++n) {
-      v4f add = {0, 0, 0, 0};
+    for (int n = 0; n < 2 * NB; n += kTiles) {
+      v4f add[kTiles];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const Frag<T> kf[1] = {frag_col_result(s.k, L::ldn, 32 * j, 16 * n)};
-        const Frag<T> qf[1] = {frag_col_result(s.q, L::ldn, 32 * j, 16 * n)};
-        mma_parts<T>(add, kf, rs[j].f);
-        mma_parts<T>(add, qf, ss[j].f);
-      }
-      st.st[n] = st.st[n] * total + add;
+      for (int i = 0; i < kTiles; ++i) add[i] = v4f{0, 0, 0, 0};
+#pragma unroll
+      for (int z = kExact<T> - 1; z >= 0; --z)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i) mma(add[i], df[j][i], ss[j].f[z]);
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i) mma(add[i], cf[j][i], rs[j].f[z]);
+        }
+      if (n + kTiles < 2 * NB) read_cols(n + kTiles);
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) st.st[n + i] = st.st[n + i] * total + add[i];
     }
   }
   if (a.d_initial != nullptr) st.save(a.d_initial + of_seq, a.width, a.states);

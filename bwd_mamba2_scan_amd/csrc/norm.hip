@@ -29,7 +29,8 @@ struct NormArgs {
   mamba2_rows x, gate, y, d_y, d_x, d_gate;
   const float* weight;
   const float* bias;
-  float* partial;        // [slices][2][n]: the weights' gradients, then the biases'
+  float* partial;        // [slices][2][n]: the weights' gradients, then the biases'; a slice for each run of rows
+                         // (shared: for each block)
   int groups, width, shared, centered;
   int lanes;             // L: lanes of a group
   int across;            // neighbouring groups of a block
@@ -228,6 +229,8 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void norm_fwd_kernel(NormArgs a)
 template <class T, int V, int R, int FORM, bool WIDE>
 __global__ __launch_bounds__(WIDE ? 1024 : 256) void norm_bwd_kernel(NormArgs a) {
   __shared__ float part[32];
+  constexpr int kSums = 2 * R * V;  // sums that a thread holds
+  __shared__ float sums[WIDE ? 1 : 256][kSums + 1];
   constexpr bool kGate = FORM == MAMBA2_NORM_GATED || FORM == MAMBA2_NORM_GATE_FIRST;
   const int column = blockIdx.x % a.columns, chunk = blockIdx.x / a.columns;
   const Place w = place_of<V>(a, column);
@@ -243,8 +246,7 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void norm_bwd_kernel(NormArgs a)
   for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int j = 0; j < V; ++j) d_w[i][j] = d_b[i][j] = 0.0f;
-  if (!WIDE && !w.live) return;
-  for (long row = row0 + w.row; row < end; row += w.step) {
+  for (long row = row0 + w.row; row < end && w.live; row += w.step) {
     float h[R][V], z[R][V], x[R][V], d[R][V];
     load_row<T, V, R>(row_ptr<const T>(a.x, a, row), w, a, h);
     if constexpr (kGate) load_row<T, V, R>(row_ptr<const T>(a.gate, a, row), w, a, z);
@@ -308,31 +310,51 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void norm_bwd_kernel(NormArgs a)
     }
   }
   if (a.partial == nullptr) return;
-  // A slice for every row that the block works on at a time, and, with shared
-  // parameters, for every group.
-  const long rows_at = static_cast<long>(chunk) * w.step + w.row;
-  const long slice = a.shared ? (rows_at * a.columns + column) * a.across + w.group : rows_at;
-  float* p = a.partial + slice * 2 * a.n + (a.shared ? w.in_group : w.channel);
+  if constexpr (WIDE) {
+    float* p = a.partial + (a.shared ? static_cast<long>(chunk) * a.columns + column : chunk) * 2 * a.n +
+               (a.shared ? w.in_group : w.channel);
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (w.live && w.in_group + i * a.lanes * V < a.width) {
-        p[i * a.lanes * V + j] = d_w[i][j];
-        p[a.n + i * a.lanes * V + j] = d_b[i][j];
+      for (int j = 0; j < V; ++j)
+        if (w.in_group + i * a.lanes * V < a.width) {
+          p[i * a.lanes * V + j] = d_w[i][j];
+          p[a.n + i * a.lanes * V + j] = d_b[i][j];
+        }
+  } else {
+    // the block's items with the same parameters: those of a group, or with shared
+    // parameters all
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        sums[threadIdx.x][i * V + j] = d_w[i][j];
+        sums[threadIdx.x][R * V + i * V + j] = d_b[i][j];
       }
+    __syncthreads();
+    const int keys = a.shared ? 1 : a.across, items = 256 / a.lanes;
+    float* p = a.partial + (a.shared ? static_cast<long>(chunk) * a.columns + column : chunk) * 2 * a.n;
+    for (int o = threadIdx.x; o < keys * kSums * a.lanes; o += 256) {
+      const int lane = o % a.lanes, e = o / a.lanes % kSums, key = o / a.lanes / kSums;
+      const int v = e < R * V ? e : e - R * V;
+      const int in_group = (v / V * a.lanes + lane) * V + v % V, group = column * a.across + key;
+      if (in_group >= a.width || group >= a.groups) continue;
+      float s = 0.0f;
+      for (int i = key; i < items; i += keys) s += sums[i * a.lanes + lane][e];
+      p[(e < R * V ? 0 : a.n) + (a.shared ? 0 : group * a.width) + in_group] = s;
+    }
+  }
 }
 
 // Sums [slices][2][n] over the slices: 32 columns a block, 32 runs of slices, in a
-// fixed order.  Slices of groups that do not exist (shared parameters, the last
-// column of blocks) are not written and not read.
+// fixed order.
 constexpr int kSumCols = 32, kSumRuns = 32;
 struct SumArgs {
   const float* partial;
   float* d_weight;
   float* d_bias;
   long slices;
-  int n, per, live;  // of `per` neighbouring slices the first `live` exist
+  int n;
 };
 __global__ __launch_bounds__(kSumCols * kSumRuns) void norm_sum_kernel(SumArgs a) {
   __shared__ float part[kSumRuns][kSumCols + 1];
@@ -340,8 +362,7 @@ __global__ __launch_bounds__(kSumCols * kSumRuns) void norm_sum_kernel(SumArgs a
   const long col = static_cast<long>(blockIdx.x) * kSumCols + c;  // of 2 n
   float s = 0.0f;
   if (col < 2 * a.n)
-    for (long i = run; i < a.slices; i += kSumRuns)
-      if (i % a.per < a.live) s += a.partial[i * 2 * a.n + col];
+    for (long i = run; i < a.slices; i += kSumRuns) s += a.partial[i * 2 * a.n + col];
   part[run][c] = s;
   __syncthreads();
   if (run == 0 && col < 2 * a.n) {
@@ -396,7 +417,7 @@ Shape shape_of(const mamba2_seqs& q, const mamba2_norm_dims& d, bool vec, bool b
   if (run < at_once) run = at_once;
   s.run = static_cast<int>(run);
   s.chunks = static_cast<long>((rows + run - 1) / run);
-  s.slices = s.chunks * at_once * (d.shared ? s.columns * s.across : 1);
+  s.slices = s.chunks * (d.shared ? s.columns : 1);
   return s;
 }
 
@@ -568,8 +589,7 @@ int mamba2_norm_bwd(mamba2_seqs seqs, mamba2_norm_dims d, mamba2_rows x, const f
     if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
   }
   if (sums) {
-    const int per = d.shared ? s.columns * s.across : 1, live = d.shared ? d.groups : 1;
-    const SumArgs sa = {a.partial, d_weight, d_bias, s.slices, a.n, per, live};
+    const SumArgs sa = {a.partial, d_weight, d_bias, s.slices, a.n};
     norm_sum_kernel<<<(2 * a.n + kSumCols - 1) / kSumCols, kSumCols * kSumRuns, 0, hs>>>(sa);
   }
   return launch_status();
