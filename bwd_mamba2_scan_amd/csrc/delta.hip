@@ -8,6 +8,7 @@
 // without leaving its lane, so waves meet only where they share the loads of a
 // step's left operands (K, Q, M, P) through LDS.
 #include "delta_common.h"
+#include "delta_pair.h"
 #include "delta_prep.h"
 #include "delta_walk.h"
 
@@ -32,9 +33,14 @@ __global__ __launch_bounds__(kPrepWaves * 64) void delta_prep_kernel(DeltaArgs a
 }
 
 template <class T, int NB>
-__global__ __launch_bounds__(kWaves * 64, 1) void delta_fwd_kernel(DeltaArgs a) {
-  __shared__ FwdLds<T, NB, false> s;
-  walk_forward<T, NB, false>(a, s);
+__global__ __launch_bounds__(walk_threads<T>) void delta_fwd_kernel(DeltaArgs a) {
+  if constexpr (sizeof(T) == 2) {
+    __shared__ PairFwdLds<NB, false> s;
+    pair_forward<NB, false>(a, s);
+  } else {
+    __shared__ FwdLds<T, NB, false> s;
+    walk_forward<T, NB, false>(a, s);
+  }
 }
 
 // ------------------------------------------------------------ single tokens
@@ -133,7 +139,7 @@ int launch_fwd(const DeltaArgs& a, unsigned steps, unsigned blocks, hipStream_t 
     delta_prep_kernel<T, NB><<<steps, kPrepWaves * 64, 0, s>>>(a);
     if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
   }
-  delta_fwd_kernel<T, NB><<<blocks, kWaves * 64, 0, s>>>(a);
+  delta_fwd_kernel<T, NB><<<blocks, walk_threads<T>, 0, s>>>(a);
   return launch_status();
 }
 template <class T>

@@ -18,6 +18,7 @@
 // every step (delta_grads_kernel), whose work-group takes the heads of a group
 // one after another and adds up the shared q's and k's gradients in registers.
 #include "delta_common.h"
+#include "delta_pair.h"
 #include "delta_prep.h"
 #include "delta_walk.h"
 
@@ -44,15 +45,25 @@ __global__ __launch_bounds__(kPrepWaves * 64) void delta_bwd_prep_kernel(DeltaAr
 }
 
 template <class T, int NB>
-__global__ __launch_bounds__(kWaves * 64, 1) void delta_keep_kernel(DeltaArgs a) {
-  __shared__ FwdLds<T, NB, true> s;
-  walk_forward<T, NB, true>(a, s);
+__global__ __launch_bounds__(walk_threads<T>) void delta_keep_kernel(DeltaArgs a) {
+  if constexpr (sizeof(T) == 2) {
+    __shared__ PairFwdLds<NB, true> s;
+    pair_forward<NB, true>(a, s);
+  } else {
+    __shared__ FwdLds<T, NB, true> s;
+    walk_forward<T, NB, true>(a, s);
+  }
 }
 
 template <class T, int NB>
-__global__ __launch_bounds__(kWaves * 64, 1) void delta_reverse_kernel(DeltaArgs a) {
-  __shared__ RevLds<T, NB> s;
-  walk_reverse<T, NB>(a, s);
+__global__ __launch_bounds__(walk_threads<T>) void delta_reverse_kernel(DeltaArgs a) {
+  if constexpr (sizeof(T) == 2) {
+    __shared__ PairRevLds<NB> s;
+    pair_reverse<NB>(a, s);
+  } else {
+    __shared__ RevLds<T, NB> s;
+    walk_reverse<T, NB>(a, s);
+  }
 }
 
 // ------------------------------------------------------- a step's gradients
@@ -417,10 +428,10 @@ int launch_bwd(const DeltaArgs& a, unsigned steps, unsigned blocks, hipStream_t 
   if (steps > 0) {
     delta_bwd_prep_kernel<T, NB><<<steps, kPrepWaves * 64, 0, s>>>(a);
     if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
-    delta_keep_kernel<T, NB><<<blocks, kWaves * 64, 0, s>>>(a);
+    delta_keep_kernel<T, NB><<<blocks, walk_threads<T>, 0, s>>>(a);
     if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
   }
-  delta_reverse_kernel<T, NB><<<blocks, kWaves * 64, 0, s>>>(a);
+  delta_reverse_kernel<T, NB><<<blocks, walk_threads<T>, 0, s>>>(a);
   if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
   if (steps > 0) delta_grads_kernel<T, NB><<<steps / a.ratio, kGradWaves<NB> * 64, 0, s>>>(a);
   return launch_status();
