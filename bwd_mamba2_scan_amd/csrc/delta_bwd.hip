@@ -67,17 +67,22 @@ __global__ __launch_bounds__(walk_threads<T>) void delta_reverse_kernel(DeltaArg
 }
 
 // ------------------------------------------------------- a step's gradients
-constexpr int kPart = 64;   // columns of a head that are staged at a time
+template <class T>
+constexpr int kPart = sizeof(T) == 2 ? 128 : 64;  // columns of a head that LDS holds at a time
 
+// Eight waves share a step's 2 NB tiles of 16 states by four tiles of 16 tokens:
+// two by two of them a wave (NB = 2: one by two, NB = 1: one).
+constexpr int kGradWaves = 8;
 template <int NB>
-constexpr int kGradWaves = NB < 2 ? 4 : 2 * NB;  // 16 rows of the states each
+constexpr int kGradStates = NB < 4 ? 1 : 2;
+template <int NB>
+constexpr int kGradTokens = NB < 2 ? 1 : 2;
 
 template <class T, int NB>
 struct GradLds {
   static constexpr int ldn = stride_of<T>(NB * 32);
-  static constexpr int ldv = stride_of<T>(kPart);
+  static constexpr int ldv = stride_of<T>(kPart<T>);
   static constexpr int ldm = stride_of<T>(kTok);
-  static constexpr int kW = kGradWaves<NB>;
   alignas(16) T k[kTok * ldn];
   alignas(16) T q[kTok * ldn];
   union {
@@ -88,40 +93,43 @@ struct GradLds {
     } in;
     struct {
       T pm[kTwo<T>][kTok * ldm];   // Pm
-      T xm[kTwo<T>][kTok * ldm];   // Xm + Xm^T
+      T xm[kTwo<T>][kTok * ldm];   // Xm
       float z[kTok * kSq];         // Z
     } sq;
   };
   alignas(16) Coef coef;
   float c_hi[kTok], c_lo[kTok];
-  float qs[kW][kTok], ks[kW][kTok], kd[kW][kTok];  // a wave's states of A_i's two terms, without their factors, and F_j's
+  static constexpr int kAcross = 2 * NB / kGradStates<NB>;
+  float qs[kAcross][kTok], ks[kAcross][kTok], kd[kAcross][kTok];  // some states' part of A_i's two terms, without their factors, and F_j's
   float rv[kTok];                                  // dR_i.V_i
   float bt[4][kTok];                               // a column tile's part of sum_j dT_ij E_ij k_i.k_j
-  float sd[kW];                                    // a wave's part of <S, D>
+  float sd[kAcross];                               // some states' part of <S, D>
   float a_i[kTok], f_j[kTok];
 };
 
-// Eight floats of a row of the kept state, columns c ..; zero outside.
-__device__ __forceinline__ void load8(Rsrc rs, unsigned off, float (&v)[8]) {
-  const v4f a = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
-  const v4f b = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, off + 16, 0, 0));
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[j] = a[j];
-    v[j + 4] = b[j];
-  }
+// The thread's number, as a value that the compiler knows nothing of: what is
+// computed from it is computed where it is used, and not kept in registers over
+// the whole loop (143 of them spilled).
+__device__ __forceinline__ int thread_here() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
 }
 
-// Eight values of T from global memory as floats; zero outside.
-template <class T>
-__device__ __forceinline__ void load8_as(Rsrc rs, unsigned off, float (&v)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    const v8bf a = __builtin_bit_cast(v8bf, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
+// acc[n][i] += a[n] b[i] in parts, small products first, over all tiles in turn.
+template <class T, int N, int I, int B>
+__device__ __forceinline__ void mma_grid(v4f (&acc)[N][I], const Split<T, kExact<T>> (&a)[N], const Frag<T> (&b)[I][B]) {
+  constexpr int kMost = kExact<T>;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = static_cast<float>(a[j]);
-  } else {
-    load8(rs, off, v);
-  }
+  for (int m = kMost - 1; m >= 0; --m)
+#pragma unroll
+    for (int z = 0; z <= m; ++z)
+      if (m - z < B) {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int i = 0; i < I; ++i) mma(acc[n][i], a[n].f[z], b[i][m - z]);
+      }
 }
 
 // Eight values to an LDS row in PARTS parts, `plane` elements apart.
@@ -140,21 +148,32 @@ __device__ __forceinline__ void put8(T* p, int plane, const float (&v)[8]) {
   }
 }
 
-template <class T, int PARTS>
-__device__ __forceinline__ void put1(T* p, int plane, float v) {
+// Eight values of T as they were loaded.
+template <class T>
+struct Eight {
+  v4i v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(Rsrc rs, unsigned off) {
 #pragma unroll
-  for (int z = 0; z < PARTS; ++z) {
-    const T t = static_cast<T>(v);
-    p[z * plane] = t;
-    v -= static_cast<float>(t);
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, off + 16 * i, 0, 0);
   }
-}
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    if constexpr (sizeof(T) == 2) {
+      const v8bf b = __builtin_bit_cast(v8bf, v[0]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = static_cast<float>(b[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = __builtin_bit_cast(v4f, v[j >> 2])[j & 3];
+    }
+  }
+};
 
 template <class T, int NB>
-__global__ __launch_bounds__(kGradWaves<NB> * 64) void delta_grads_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs a) {
   typedef GradLds<T, NB> L;
   __shared__ L s;
-  constexpr int kW = kGradWaves<NB>, kThreads = kW * 64;
+  constexpr int kW = kGradWaves, kThreads = kW * 64;
+  constexpr int kN = kGradStates<NB>, kI = kGradTokens<NB>;
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
   const int work = xcd_contiguous(blockIdx.x, gridDim.x);
   const int groups = a.heads / a.ratio;
@@ -164,6 +183,66 @@ __global__ __launch_bounds__(kGradWaves<NB> * 64) void delta_grads_kernel(DeltaA
   const bool packed = a.seqs.offsets != nullptr;
   const int rows = min(u.len - u.t0, kTok);
   const long head = static_cast<long>(a.states) * a.width, slab = kTok * static_cast<long>(a.width);
+  constexpr int kAcross = 2 * NB / kN;             // waves side by side over the states
+  const int s0 = wave % kAcross * kN;              // this wave's tiles of states
+  const int i0 = wave / kAcross * kI;              // and of tokens
+
+  // A part of a head's columns on their way to LDS: a thread has eight columns of
+  // every 32 of one row, of dR and V (the first 256 threads) or of U and dY.
+  constexpr int kEights = kPart<T> / 32;
+  Eight<float> flat[kEights];
+  Eight<T> token[kEights];
+  const bool second = __builtin_amdgcn_readfirstlane(tid >= 256);
+  const long my_stride = second ? a.d_y.row_stride : a.v.row_stride;
+  const T* my_p = second ? seq_ptr<const T>(a.d_y, u.seq, u.row0, packed) + u.t0 * a.d_y.row_stride
+                         : seq_ptr<const T>(a.v, u.seq, u.row0, packed) + u.t0 * a.v.row_stride;
+  const auto fetch = [&](int h, int c0) {
+    const long cell = static_cast<long>(step) * a.heads + h;
+    const Rsrc rf = make_rsrc((second ? a.u : a.d_r) + cell * slab, static_cast<unsigned>(slab * 4));
+    const Rsrc rt = rows_rsrc(my_p + h * a.width, my_stride, rows, a.width);
+    const int t = thread_here(), row = (t & 255) >> 2, col = c0 + (t & 3) * 8;
+    const unsigned off = static_cast<unsigned>(row * a.width + col) * 4;
+    const unsigned tok = static_cast<unsigned>(row * static_cast<int>(my_stride) + col) * sizeof(T);
+#pragma unroll
+    for (int i = 0; i < kEights; ++i) {
+      const bool in = col + 32 * i < a.width;
+      flat[i].load(rf, in ? off + 128 * i : kOutside);
+      token[i].load(rt, in ? tok + 32 * sizeof(T) * i : kOutside);
+    }
+  };
+  float rv = 0.0f;
+  const auto put = [&] {
+    const int here = thread_here(), at0 = ((here & 255) >> 2) * L::ldv + (here & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < kEights; ++i) {
+      const int at = at0 + 32 * i;
+      float f[8], t[8];
+      flat[i].get(f);
+      token[i].get(t);
+      put8<T, kExact<T>>((second ? s.in.u[0] : s.in.r[0]) + at, kTok * L::ldv, f);
+      if (second) {
+        put8<T, 1>(s.in.y + at, 0, t);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) rv = fmaf(f[j], t[j], rv);
+      }
+    }
+  };
+  // This lane's rows of a kept state, columns 8 g .. of 32; rows and columns outside are zero.
+  const auto load_state = [&](Eight<float> (&e)[kN], const float* kept, long cell, int c0) {
+    const Rsrc rs = make_rsrc(kept + cell * head, static_cast<unsigned>(head * 4));
+    const int t = thread_here() & 63, c = c0 + 8 * (t >> 4);
+    const unsigned off = c < a.width ? static_cast<unsigned>(((16 * s0 + (t & 15)) * a.width + c) * 4) : kOutside;
+#pragma unroll
+    for (int n = 0; n < kN; ++n) e[n].load(rs, off + 64 * n * a.width);
+  };
+  float g_raw = 0.0f;
+  v4f coef_raw = {0, 0, 0, 0};
+  const auto fetch_gates = [&](int h) {
+    if (wave == kW - 1) g_raw = load_gate(a.g, a.gate_bf16, u, packed, u.t0, rows, h, a.heads);
+    else if (tid < static_cast<int>(sizeof(Coef) / 16))
+      coef_raw = reinterpret_cast<const v4f*>(a.coef + static_cast<long>(step) * a.heads + h)[tid];
+  };
   {
     Tile<T, kTok, NB * 32, kThreads> tk, tq;
     tk.init(a.k.row_stride, a.states, tid);
@@ -171,140 +250,166 @@ __global__ __launch_bounds__(kGradWaves<NB> * 64) void delta_grads_kernel(DeltaA
     const int j = group * a.states;
     tk.load(rows_rsrc(seq_ptr<const T>(a.k, u.seq, u.row0, packed) + u.t0 * a.k.row_stride + j, a.k.row_stride, rows, a.states));
     tq.load(rows_rsrc(seq_ptr<const T>(a.q, u.seq, u.row0, packed) + u.t0 * a.q.row_stride + j, a.q.row_stride, rows, a.states));
+    fetch_gates(group * a.ratio);
+    fetch(group * a.ratio, 0);
     tk.store(s.k, L::ldn, tid);
     tq.store(s.q, L::ldn, tid);
   }
-  const bool states = wave < 2 * NB;   // has a tile of the states
-  const int n0 = 16 * wave;            // its first
-  v4f dq[4], dk[4];
+  constexpr int kMine = 2;  // a wave's share of the ten score tiles
+  // the gradients of q and k, transposed: token l15 of a tile, states 4 g .. of another
+  v4f dq[kN][kI], dk[kN][kI];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) dq[i] = dk[i] = v4f{0, 0, 0, 0};
-
+  for (int n = 0; n < kN; ++n)
+#pragma unroll
+    for (int i = 0; i < kI; ++i) dq[n][i] = dk[n][i] = v4f{0, 0, 0, 0};
   for (int hh = 0; hh < a.ratio; ++hh) {
     const int h = group * a.ratio + hh;
-    const long cell = static_cast<long>(step) * a.heads + h;
+    const int tid = thread_here(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
     __syncthreads();  // the last head's matrices are read
     if (wave == kW - 1) {
-      const double c = scan64(gate_log(load_gate(a.g, a.gate_bf16, u, packed, u.t0, rows, h, a.heads)));
+      const double c = scan64(gate_log(g_raw));
       s.c_hi[lane] = static_cast<float>(c);
       s.c_lo[lane] = static_cast<float>(c - static_cast<float>(c));
     } else if (tid < static_cast<int>(sizeof(Coef) / 16)) {
-      reinterpret_cast<v4f*>(&s.coef)[tid] = reinterpret_cast<const v4f*>(a.coef + cell)[tid];
+      reinterpret_cast<v4f*>(&s.coef)[tid] = coef_raw;
     }
-    if (tid < kTok) s.rv[tid] = 0.0f;
-
-    // products over the columns
-    v4f ys[4], rs[4], ud[4];  // dY S^T, dR S^T, U D^T: 64 tokens by this wave's states
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ys[i] = rs[i] = ud[i] = v4f{0, 0, 0, 0};
-    constexpr int kMine = (10 + kW - 1) / kW;
-    v4f dp[kMine], dt[kMine];  // this wave's tiles of dP and -dT
+    rv = 0.0f;
+    const long cell = static_cast<long>(step) * a.heads + h;
+    float sd = 0.0f, sq[kI] = {}, sk[kI] = {}, sf[kI] = {};
+    v4f dp[kMine], dt[kMine];  // this wave's tiles of dP^T and -dT^T
 #pragma unroll
     for (int i = 0; i < kMine; ++i) dp[i] = dt[i] = v4f{0, 0, 0, 0};
-    float sd = 0.0f;
-    const Rsrc rS = make_rsrc(a.keep + cell * head, static_cast<unsigned>(head * 4));
-    const Rsrc rD = make_rsrc(a.d_keep + cell * head, static_cast<unsigned>(head * 4));
-    const Rsrc rU = make_rsrc(a.u + cell * slab, static_cast<unsigned>(slab * 4));
-    const Rsrc rR = make_rsrc(a.d_r + cell * slab, static_cast<unsigned>(slab * 4));
-    const Rsrc rY = rows_rsrc(seq_ptr<const T>(a.d_y, u.seq, u.row0, packed) + u.t0 * a.d_y.row_stride + h * a.width,
-                              a.d_y.row_stride, rows, a.width);
-    const Rsrc rV = rows_rsrc(seq_ptr<const T>(a.v, u.seq, u.row0, packed) + u.t0 * a.v.row_stride + h * a.width,
-                              a.v.row_stride, rows, a.width);
-    for (int c0 = 0; c0 < a.width; c0 += kPart) {
-      __syncthreads();
-      for (int e = tid; e < kTok * kPart / 8; e += kThreads) {
-        const int row = e >> 3, c = c0 + (e & 7) * 8;
-        const bool in = c < a.width;
-        float y[8], v[8], r[8], w[8];
-        load8_as<T>(rY, in ? static_cast<unsigned>((row * static_cast<int>(a.d_y.row_stride) + c) * sizeof(T)) : kOutside, y);
-        load8_as<T>(rV, in ? static_cast<unsigned>((row * static_cast<int>(a.v.row_stride) + c) * sizeof(T)) : kOutside, v);
-        load8(rR, in ? static_cast<unsigned>((row * a.width + c) * 4) : kOutside, r);
-        load8(rU, in ? static_cast<unsigned>((row * a.width + c) * 4) : kOutside, w);
-        const int at = row * L::ldv + (e & 7) * 8;
-        put8<T, 1>(s.in.y + at, 0, y);
-        put8<T, kExact<T>>(s.in.r[0] + at, kTok * L::ldv, r);
-        put8<T, kExact<T>>(s.in.u[0] + at, kTok * L::ldv, w);
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fmaf(r[j], v[j], sum);
-        sum += __shfl_xor(sum, 1);
-        sum += __shfl_xor(sum, 2);
-        sum += __shfl_xor(sum, 4);
-        if ((e & 7) == 0) s.rv[row] += sum;
+    constexpr bool kWhole = kPart<T> >= kMaxDim;  // LDS holds every head's columns at once
+    for (int c0 = 0; c0 < (kWhole ? 1 : a.width); c0 += kPart<T>) {
+      if (!kWhole && c0 > 0) {
+        __syncthreads();
+        fetch(h, c0);
       }
+      const int behind = min(a.width - c0, kPart<T>);
+      Eight<float> raw[kN], other[kN];
+      load_state(raw, a.keep, cell, c0);
+      put();
       __syncthreads();
+      {  // products over the columns with S, transposed: S dY^T, S dR^T; and the score tiles
+        v4f ys[kN][kI], rs[kN][kI];
 #pragma unroll
-      for (int ks = 0; ks < kPart / 32; ++ks) {
-        if (c0 + ks * 32 >= a.width) break;
-        if (states) {
-          // the lane's row of the states, eight columns; rows and columns outside are zero
-          float f[8], d[8];
-          const int c = c0 + ks * 32 + 8 * g;
-          const unsigned off = c < a.width ? static_cast<unsigned>(((n0 + l15) * a.width + c) * 4) : kOutside;
-          load8(rS, off, f);
-          load8(rD, off, d);
+        for (int n = 0; n < kN; ++n)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) sd = fmaf(f[j], d[j], sd);
-          const Split<T, kExact<T>> fs = split_of<T, kExact<T>>(f), ds = split_of<T, kExact<T>>(d);
+          for (int i = 0; i < kI; ++i) ys[n][i] = rs[n][i] = v4f{0, 0, 0, 0};
+        for (int c = 0; c < behind; c += 32) {
+          Frag<T> yf[kI][1], rf[kI][kExact<T>];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const Frag<T> yf[1] = {frag_row(s.in.y, L::ldv, 16 * i, 32 * ks)};
-            Frag<T> rf[kExact<T>], uf[kExact<T>];
+          for (int i = 0; i < kI; ++i) {
+            yf[i][0] = frag_row(s.in.y, L::ldv, 16 * (i0 + i), c, lane);
 #pragma unroll
-            for (int z = 0; z < kExact<T>; ++z) {
-              rf[z] = frag_row(s.in.r[z], L::ldv, 16 * i, 32 * ks);
-              uf[z] = frag_row(s.in.u[z], L::ldv, 16 * i, 32 * ks);
+            for (int z = 0; z < kExact<T>; ++z) rf[i][z] = frag_row(s.in.r[z], L::ldv, 16 * (i0 + i), c, lane);
+          }
+          keep_reads_here();
+          Split<T, kExact<T>> part[kN];
+#pragma unroll
+          for (int n = 0; n < kN; ++n) {
+            float f[8];
+            raw[n].get(f);
+            part[n] = split_of<T, kExact<T>>(f);
+          }
+          load_state(raw, a.keep, cell, c0 + c + 32);
+          mma_grid<T>(ys, part, yf);
+          mma_grid<T>(rs, part, rf);
+#pragma unroll
+          for (int n = 0; n < kMine; ++n) {
+            const int tile = wave + n * kW;
+            if (tile < 10) {
+              const int ti = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, tj = tile - ti * (ti + 1) / 2;
+              Frag<T> uf[kExact<T>];
+              yf[0][0] = frag_row(s.in.y, L::ldv, 16 * ti, c, lane);
+#pragma unroll
+              for (int z = 0; z < kExact<T>; ++z) {
+                rf[0][z] = frag_row(s.in.r[z], L::ldv, 16 * ti, c, lane);
+                uf[z] = frag_row(s.in.u[z], L::ldv, 16 * tj, c, lane);
+              }
+              mma_parts<T>(dp[n], uf, yf[0]);
+              mma_parts<T>(dt[n], uf, rf[0]);
             }
-            mma_parts<T>(ys[i], yf, fs.f);
-            mma_parts<T>(rs[i], rf, fs.f);
-            mma_parts<T>(ud[i], uf, ds.f);
           }
         }
+        load_state(raw, a.d_keep, cell, c0);
+        load_state(other, a.keep, cell, c0);  // a second time, from the cache, for <S, D>
 #pragma unroll
-        for (int n = 0; n < kMine; ++n) {
-          const int tile = wave + n * kW;
-          if (tile < 10) {
-            const int ti = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, tj = tile - ti * (ti + 1) / 2;
-            const Frag<T> yf[1] = {frag_row(s.in.y, L::ldv, 16 * ti, 32 * ks)};
-            Frag<T> rf[kExact<T>], uf[kExact<T>];
+        for (int i = 0; i < kI; ++i) {
+          const int t = 16 * (i0 + i) + l15;
+          const float from = s.coef.from[t], beta = s.coef.beta[t];
 #pragma unroll
-            for (int z = 0; z < kExact<T>; ++z) {
-              rf[z] = frag_row(s.in.r[z], L::ldv, 16 * ti, 32 * ks);
-              uf[z] = frag_row(s.in.u[z], L::ldv, 16 * tj, 32 * ks);
-            }
-            mma_parts<T>(dp[n], yf, uf);
-            mma_parts<T>(dt[n], rf, uf);
+          for (int n = 0; n < kN; ++n) {
+            const int at = t * L::ldn + 16 * (s0 + n) + 4 * g;
+            const v4f pq = quad_get(s.q + at) * ys[n][i], pk = quad_get(s.k + at) * rs[n][i];
+            sq[i] += (pq[0] + pq[1]) + (pq[2] + pq[3]);
+            sk[i] += (pk[0] + pk[1]) + (pk[2] + pk[3]);
+            dq[n][i] += (a.scale * from) * ys[n][i];
+            dk[n][i] -= (beta * from) * rs[n][i];
+          }
+        }
+      }
+      {  // with D: D U^T
+        v4f ud[kN][kI];
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+          for (int i = 0; i < kI; ++i) ud[n][i] = v4f{0, 0, 0, 0};
+        for (int c = 0; c < behind; c += 32) {
+          Frag<T> uf[kI][kExact<T>];
+#pragma unroll
+          for (int i = 0; i < kI; ++i)
+#pragma unroll
+            for (int z = 0; z < kExact<T>; ++z) uf[i][z] = frag_row(s.in.u[z], L::ldv, 16 * (i0 + i), c, lane);
+          keep_reads_here();
+          Split<T, kExact<T>> part[kN];
+#pragma unroll
+          for (int n = 0; n < kN; ++n) {
+            float d[8], f[8];
+            raw[n].get(d);
+            other[n].get(f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sd = fmaf(f[j], d[j], sd);
+            part[n] = split_of<T, kExact<T>>(d);
+          }
+          load_state(raw, a.d_keep, cell, c0 + c + 32);
+          load_state(other, a.keep, cell, c0 + c + 32);
+          mma_grid<T>(ud, part, uf);
+        }
+#pragma unroll
+        for (int i = 0; i < kI; ++i) {
+          const int t = 16 * (i0 + i) + l15;
+          const float to = s.coef.to[t];
+#pragma unroll
+          for (int n = 0; n < kN; ++n) {
+            const v4f pd = quad_get(s.k + t * L::ldn + 16 * (s0 + n) + 4 * g) * ud[n][i];
+            sf[i] += (pd[0] + pd[1]) + (pd[2] + pd[3]);
+            dk[n][i] += to * ud[n][i];
           }
         }
       }
     }
-    __syncthreads();  // the columns' tiles give way to the matrices
+    rv += __shfl_xor(rv, 1);
+    rv += __shfl_xor(rv, 2);
+    if (!second && (tid & 3) == 0) s.rv[tid >> 2] = rv;
+    __syncthreads();  // the columns give way to the matrices
+    // the next head's; behind the last one, its own again
+    const int next = hh + 1 < a.ratio ? h + 1 : h;
+    fetch_gates(next);
 
-    // what the states give: the shared gradients, and the sums over the states
     sd = sum64(sd);
-    if (lane == 0) s.sd[wave] = sd;
+    if (lane == 0 && i0 == 0) s.sd[s0 / kN] = sd;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const v4f from = rows_of(s.coef.from, i, g), to = rows_of(s.coef.to, i, g), beta = rows_of(s.coef.beta, i, g);
-      v4f sq, sk, sf;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * i + 4 * g + r;
-        const float qe = states ? static_cast<float>(s.q[row * L::ldn + n0 + l15]) : 0.0f;
-        const float ke = states ? static_cast<float>(s.k[row * L::ldn + n0 + l15]) : 0.0f;
-        sq[r] = sum16(qe * ys[i][r]);
-        sk[r] = sum16(ke * rs[i][r]);
-        sf[r] = sum16(ke * ud[i][r]);
+    for (int i = 0; i < kI; ++i) {
+      const int t = 16 * (i0 + i) + l15;
+      const float tq = sum_groups(sq[i]), tk = sum_groups(sk[i]), tf = sum_groups(sf[i]);
+      if (g == 0) {
+        s.qs[s0 / kN][t] = tq;
+        s.ks[s0 / kN][t] = tk;
+        s.kd[s0 / kN][t] = tf;
       }
-      if (l15 == 0) {
-        *reinterpret_cast<v4f*>(&s.qs[wave][16 * i + 4 * g]) = sq;
-        *reinterpret_cast<v4f*>(&s.ks[wave][16 * i + 4 * g]) = sk;
-        *reinterpret_cast<v4f*>(&s.kd[wave][16 * i + 4 * g]) = sf;
-      }
-      dq[i] += a.scale * (from * ys[i]);
-      dk[i] += to * ud[i] - beta * (from * rs[i]);
     }
-    // the matrices of the step
+    // the matrices of the step: this lane's row of a tile, columns 4 g ..
 #pragma unroll
     for (int n = 0; n < kMine; ++n) {
       const int tile = wave + n * kW;
@@ -313,70 +418,91 @@ __global__ __launch_bounds__(kGradWaves<NB> * 64) void delta_grads_kernel(DeltaA
         v4f kk = {0, 0, 0, 0}, qk = {0, 0, 0, 0};
 #pragma unroll
         for (int m = 0; m < NB; ++m) {
-          const Frag<T> b = frag_row(s.k, L::ldn, 16 * tj, 32 * m);
-          mma(kk, frag_row(s.k, L::ldn, 16 * ti, 32 * m), b);
-          mma(qk, frag_row(s.q, L::ldn, 16 * ti, 32 * m), b);
+          const Frag<T> b = frag_row(s.k, L::ldn, 16 * tj, 32 * m, lane);
+          mma(kk, b, frag_row(s.k, L::ldn, 16 * ti, 32 * m, lane));
+          mma(qk, b, frag_row(s.q, L::ldn, 16 * ti, 32 * m, lane));
         }
-        const int col = 16 * tj + l15;
-        const float ch = s.c_hi[col], cl = s.c_lo[col];
-        v4f bt;
+        const int row = 16 * ti + l15, col = 16 * tj + 4 * g;
+        const float ch = s.c_hi[row], cl = s.c_lo[row], beta = s.coef.beta[row];
+        const v4f hi = rows_of(s.c_hi, tj, g), lo = rows_of(s.c_lo, tj, g);
+        v4f pm, et;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int row = 16 * ti + 4 * g + r;
-          const float e = exp2_of((s.c_hi[row] - ch) + (s.c_lo[row] - cl));
-          const float pm = col <= row ? a.scale * (e * dp[n][r]) : 0.0f;
-          const float et = col < row ? -e * dt[n][r] : 0.0f;
-          const float xm = s.coef.beta[row] * et;
-          put1<T, kTwo<T>>(&s.sq.pm[0][row * L::ldm + col], kTok * L::ldm, pm);
-          // the symmetric sum, each element written once (the diagonal of Xm is zero)
-          if (ti != tj || col <= row) put1<T, kTwo<T>>(&s.sq.xm[0][row * L::ldm + col], kTok * L::ldm, xm);
-          if (ti != tj || col < row) put1<T, kTwo<T>>(&s.sq.xm[0][col * L::ldm + row], kTok * L::ldm, xm);
-          s.sq.z[row * kSq + col] = pm * qk[r] + xm * kk[r];
-          bt[r] = sum16(et * kk[r]);
+          const float e = exp2_of((ch - hi[r]) + (cl - lo[r]));
+          pm[r] = col + r <= row ? a.scale * (e * dp[n][r]) : 0.0f;
+          et[r] = col + r < row ? -e * dt[n][r] : 0.0f;
         }
-        if (l15 == 0) *reinterpret_cast<v4f*>(&s.bt[tj][16 * ti + 4 * g]) = bt;
+        const v4f xm = beta * et, ek = et * kk;
+        quad_put_parts<kTwo<T>>(&s.sq.pm[0][row * L::ldm + col], kTok * L::ldm, pm);
+        quad_put_parts<kTwo<T>>(&s.sq.xm[0][row * L::ldm + col], kTok * L::ldm, xm);
+        quad_put(&s.sq.z[row * kSq + col], pm * qk + xm * kk);
+        const float bt = sum_groups((ek[0] + ek[1]) + (ek[2] + ek[3]));
+        if (g == 0) s.bt[tj][row] = bt;
       }
     }
-    // Pm is zero above the diagonal where a product of 32 columns reaches
-    for (int e = tid; e < 2 * 16 * 16; e += kThreads) {
-      const int b = e >> 8, row = 32 * b + (e >> 4 & 15), col = 32 * b + 16 + (e & 15);
-      put1<T, kTwo<T>>(&s.sq.pm[0][row * L::ldm + col], kTok * L::ldm, 0.0f);
+    // zeros above the diagonal where a product of 32 columns reaches
+    if (tid < 128) {
+      const int z = tid >> 6, row = 32 * z + (tid >> 2 & 15), col = 32 * z + 16 + 4 * (tid & 3);
+      quad_put_parts<kTwo<T>>(&s.sq.pm[0][row * L::ldm + col], kTok * L::ldm, v4f{0, 0, 0, 0});
+      quad_put_parts<kTwo<T>>(&s.sq.xm[0][row * L::ldm + col], kTok * L::ldm, v4f{0, 0, 0, 0});
     }
     __syncthreads();
-    if (states) {
+    // dQ^T += K^T Pm^T, dK^T += Q^T Pm + K^T (Xm + Xm^T)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const Frag<T> kf[1] = {frag_col(s.k, L::ldn, 32 * j, n0)}, qf[1] = {frag_col(s.q, L::ldn, 32 * j, n0)};
+    for (int j = 0; j < 2; ++j) {
+      Frag<T> kf[kN][1], qf[kN][1];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          Frag<T> pf[kTwo<T>], tf[kTwo<T>], xf[kTwo<T>];
+      for (int n = 0; n < kN; ++n) {
+        kf[n][0] = frag_col(s.k, L::ldn, 32 * j, 16 * (s0 + n), lane);
+        qf[n][0] = frag_col(s.q, L::ldn, 32 * j, 16 * (s0 + n), lane);
+      }
+#pragma unroll
+      for (int m = 0; m < kI; ++m) {
+        const int i = i0 + m;
+        Frag<T> pf[kTwo<T>], xf[kTwo<T>];
+        if (j <= i / 2) {
 #pragma unroll
           for (int z = 0; z < kTwo<T>; ++z) {
-            xf[z] = frag_row(s.sq.xm[z], L::ldm, 16 * i, 32 * j);
-            if (j <= i / 2) pf[z] = frag_row(s.sq.pm[z], L::ldm, 16 * i, 32 * j);
-            if (j >= i / 2) tf[z] = frag_col(s.sq.pm[z], L::ldm, 32 * j, 16 * i);
+            pf[z] = frag_row(s.sq.pm[z], L::ldm, 16 * i, 32 * j, lane);
+            xf[z] = frag_row(s.sq.xm[z], L::ldm, 16 * i, 32 * j, lane);
           }
-          mma_parts<T>(dk[i], xf, kf);
-          if (j <= i / 2) mma_parts<T>(dq[i], pf, kf);
-          if (j >= i / 2) mma_parts<T>(dk[i], tf, qf);
+#pragma unroll
+          for (int n = 0; n < kN; ++n) {
+            mma_parts<T>(dq[n][m], kf[n], pf);
+            mma_parts<T>(dk[n][m], kf[n], xf);
+          }
+        }
+        if (j >= i / 2) {
+#pragma unroll
+          for (int z = 0; z < kTwo<T>; ++z) {
+            pf[z] = frag_col(s.sq.pm[z], L::ldm, 32 * j, 16 * i, lane);
+            xf[z] = frag_col(s.sq.xm[z], L::ldm, 32 * j, 16 * i, lane);
+          }
+#pragma unroll
+          for (int n = 0; n < kN; ++n) {
+            mma_parts<T>(dk[n][m], qf[n], pf);
+            mma_parts<T>(dk[n][m], kf[n], xf);
+          }
         }
       }
     }
+    keep_all_here();
+    fetch(next, 0);  // no earlier: the matrices' products need the registers
     // the gates' gradients: A_i and F_j first
     if (tid < kTok) {
-      float sq = 0.0f, sk = 0.0f, sf = 0.0f;
+      float tq = 0.0f, tk = 0.0f, tf = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 2 * NB; ++w) {
-        sq += s.qs[w][tid];
-        sk += s.ks[w][tid];
-        sf += s.kd[w][tid];
+      for (int w = 0; w < kAcross; ++w) {
+        tq += s.qs[w][tid];
+        tk += s.ks[w][tid];
+        tf += s.kd[w][tid];
       }
       const float from = s.coef.from[tid], beta = s.coef.beta[tid];
-      s.a_i[tid] = a.scale * (from * sq) - beta * (from * sk);
-      s.f_j[tid] = s.coef.to[tid] * sf;
+      s.a_i[tid] = a.scale * (from * tq) - beta * (from * tk);
+      s.f_j[tid] = s.coef.to[tid] * tf;
       float bt = 0.0f;
       for (int c = 0; c <= tid / 16; ++c) bt += s.bt[c][tid];
-      const float db = s.rv[tid] - from * sk + bt;
+      const float db = s.rv[tid] - from * tk + bt;
       if (tid < rows) {
         const long e = static_cast<long>(u.t0 + tid) * a.d_beta.row_stride + h;
         if (a.gate_bf16) seq_ptr<bf16>(a.d_beta, u.seq, u.row0, packed)[e] = static_cast<bf16>(db);
@@ -387,39 +513,51 @@ __global__ __launch_bounds__(kGradWaves<NB> * 64) void delta_grads_kernel(DeltaA
     {
       float ends = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 2 * NB; ++w) ends += s.sd[w];
+      for (int w = 0; w < kAcross; ++w) ends += s.sd[w];
       ends *= s.coef.total;
       constexpr int kEach = kTok / kW;  // tokens of a wave
       const int first = wave * kEach;
       float z = 0.0f;                   // lane j: sum of Z_ij over i >= t
-      for (int i = kTok - 1; i >= first + kEach; --i) z += lane <= i ? s.sq.z[i * kSq + lane] : 0.0f;
-      for (int t = first + kEach - 1; t >= first; --t) {
-        z += lane <= t ? s.sq.z[t * kSq + lane] : 0.0f;
-        const float part = (lane < t ? z + s.f_j[lane] : 0.0f) + (lane >= t ? s.a_i[lane] : 0.0f);
-        const float dg = sum64(part) + ends;
-        if (lane == 0 && t < rows) {
-          const long e = static_cast<long>(u.t0 + t) * a.d_g.row_stride + h;
-          if (a.gate_bf16) seq_ptr<bf16>(a.d_g, u.seq, u.row0, packed)[e] = static_cast<bf16>(dg);
-          else seq_ptr<float>(a.d_g, u.seq, u.row0, packed)[e] = dg;
+      for (int i = kTok - 8; i >= first + kEach; i -= 8) {
+        float zs[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) zs[e] = s.sq.z[(i + e) * kSq + lane];
+#pragma unroll
+        for (int e = 7; e >= 0; --e) z += lane <= i + e ? zs[e] : 0.0f;
+      }
+      const float fj = s.f_j[lane], ai = s.a_i[lane];
+      float zs[kEach], dg[kEach];
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) zs[e] = s.sq.z[(first + e) * kSq + lane];
+#pragma unroll
+      for (int e = kEach - 1; e >= 0; --e) {
+        const int t = first + e;
+        z += lane <= t ? zs[e] : 0.0f;
+        dg[e] = sum64((lane < t ? z + fj : 0.0f) + (lane >= t ? ai : 0.0f)) + ends;
+      }
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const int t = first + e;
+        if (lane == e && t < rows) {
+          const long at = static_cast<long>(u.t0 + t) * a.d_g.row_stride + h;
+          if (a.gate_bf16) seq_ptr<bf16>(a.d_g, u.seq, u.row0, packed)[at] = static_cast<bf16>(dg[e]);
+          else seq_ptr<float>(a.d_g, u.seq, u.row0, packed)[at] = dg[e];
         }
       }
     }
   }
-  if (states) {
-    const Rsrc rq = rows_rsrc(seq_ptr<const T>(a.d_q, u.seq, u.row0, packed) + u.t0 * a.d_q.row_stride + group * a.states,
-                              a.d_q.row_stride, rows, a.states);
-    const Rsrc rk = rows_rsrc(seq_ptr<const T>(a.d_k, u.seq, u.row0, packed) + u.t0 * a.d_k.row_stride + group * a.states,
-                              a.d_k.row_stride, rows, a.states);
-    const int col = n0 + l15;
+  const Rsrc rq = rows_rsrc(seq_ptr<const T>(a.d_q, u.seq, u.row0, packed) + u.t0 * a.d_q.row_stride + group * a.states,
+                            a.d_q.row_stride, rows, a.states);
+  const Rsrc rk = rows_rsrc(seq_ptr<const T>(a.d_k, u.seq, u.row0, packed) + u.t0 * a.d_k.row_stride + group * a.states,
+                            a.d_k.row_stride, rows, a.states);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+  for (int n = 0; n < kN; ++n)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * i + 4 * g + r;
-        store_elem<T>(rq, col < a.states ? static_cast<unsigned>((row * static_cast<int>(a.d_q.row_stride) + col) * sizeof(T)) : kOutside, dq[i][r]);
-        store_elem<T>(rk, col < a.states ? static_cast<unsigned>((row * static_cast<int>(a.d_k.row_stride) + col) * sizeof(T)) : kOutside, dk[i][r]);
-      }
-  }
+    for (int i = 0; i < kI; ++i) {
+      const int row = 16 * (i0 + i) + l15, col = 16 * (s0 + n) + 4 * g;
+      Quad<T>::store(rq, col < a.states ? static_cast<unsigned>((row * static_cast<int>(a.d_q.row_stride) + col) * sizeof(T)) : kOutside, dq[n][i]);
+      Quad<T>::store(rk, col < a.states ? static_cast<unsigned>((row * static_cast<int>(a.d_k.row_stride) + col) * sizeof(T)) : kOutside, dk[n][i]);
+    }
 }
 
 // ---------------------------------------------------------------- host side
@@ -433,7 +571,7 @@ int launch_bwd(const DeltaArgs& a, unsigned steps, unsigned blocks, hipStream_t 
   }
   delta_reverse_kernel<T, NB><<<blocks, walk_threads<T>, 0, s>>>(a);
   if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
-  if (steps > 0) delta_grads_kernel<T, NB><<<steps / a.ratio, kGradWaves<NB> * 64, 0, s>>>(a);
+  if (steps > 0) delta_grads_kernel<T, NB><<<steps / a.ratio, kGradWaves * 64, 0, s>>>(a);
   return launch_status();
 }
 template <class T>

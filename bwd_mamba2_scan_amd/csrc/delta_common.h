@@ -188,6 +188,8 @@ __device__ __forceinline__ void mma_upper(v4f (&acc)[4], const Frag<T> (&a)[A][k
 
 // Reads of LDS stay on their side of this; everything else may be moved over it.
 __device__ __forceinline__ void keep_reads_here() { __builtin_amdgcn_sched_barrier(0x7f); }
+// Nothing is moved over this.
+__device__ __forceinline__ void keep_all_here() { __builtin_amdgcn_sched_barrier(0); }
 
 // Four values of rows 4 g .. of tile i, of an array by token.
 __device__ __forceinline__ v4f rows_of(const float* p, int i, int g) {
