@@ -286,17 +286,23 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
         fetch(h, c0);
       }
       const int behind = min(a.width - c0, kPart<T>);
-      Eight<float> raw[kN], other[kN];
-      load_state(raw, a.keep, cell, c0);
+      // S, then D: all of a part's columns are on their way before they are needed
+      Eight<float> raw[kEights][kN];
+#pragma unroll
+      for (int e = 0; e < kEights; ++e) load_state(raw[e], a.keep, cell, c0 + 32 * e);
       put();
       __syncthreads();
+      Eight<float> other[kN];
       {  // products over the columns with S, transposed: S dY^T, S dR^T; and the score tiles
         v4f ys[kN][kI], rs[kN][kI];
 #pragma unroll
         for (int n = 0; n < kN; ++n)
 #pragma unroll
           for (int i = 0; i < kI; ++i) ys[n][i] = rs[n][i] = v4f{0, 0, 0, 0};
-        for (int c = 0; c < behind; c += 32) {
+#pragma unroll
+        for (int e = 0; e < kEights; ++e) {
+          const int c = 32 * e;
+          if (c >= behind) break;
           Frag<T> yf[kI][1], rf[kI][kExact<T>];
 #pragma unroll
           for (int i = 0; i < kI; ++i) {
@@ -309,10 +315,10 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
 #pragma unroll
           for (int n = 0; n < kN; ++n) {
             float f[8];
-            raw[n].get(f);
+            raw[e][n].get(f);
             part[n] = split_of<T, kExact<T>>(f);
           }
-          load_state(raw, a.keep, cell, c0 + c + 32);
+          load_state(raw[e], a.d_keep, cell, c0 + c);
           mma_grid<T>(ys, part, yf);
           mma_grid<T>(rs, part, rf);
 #pragma unroll
@@ -332,7 +338,6 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
             }
           }
         }
-        load_state(raw, a.d_keep, cell, c0);
         load_state(other, a.keep, cell, c0);  // a second time, from the cache, for <S, D>
 #pragma unroll
         for (int i = 0; i < kI; ++i) {
@@ -355,7 +360,10 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
         for (int n = 0; n < kN; ++n)
 #pragma unroll
           for (int i = 0; i < kI; ++i) ud[n][i] = v4f{0, 0, 0, 0};
-        for (int c = 0; c < behind; c += 32) {
+#pragma unroll
+        for (int e = 0; e < kEights; ++e) {
+          const int c = 32 * e;
+          if (c >= behind) break;
           Frag<T> uf[kI][kExact<T>];
 #pragma unroll
           for (int i = 0; i < kI; ++i)
@@ -366,14 +374,13 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
 #pragma unroll
           for (int n = 0; n < kN; ++n) {
             float d[8], f[8];
-            raw[n].get(d);
+            raw[e][n].get(d);
             other[n].get(f);
 #pragma unroll
             for (int j = 0; j < 8; ++j) sd = fmaf(f[j], d[j], sd);
             part[n] = split_of<T, kExact<T>>(d);
           }
-          load_state(raw, a.d_keep, cell, c0 + c + 32);
-          load_state(other, a.keep, cell, c0 + c + 32);
+          if (e + 1 < kEights) load_state(other, a.keep, cell, c0 + c + 32);
           mma_grid<T>(ud, part, uf);
         }
 #pragma unroll
