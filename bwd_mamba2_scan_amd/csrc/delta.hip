@@ -35,11 +35,74 @@ __global__ __launch_bounds__(kPrepWaves * 64) void delta_prep_kernel(DeltaArgs a
 template <class T, int NB>
 __global__ __launch_bounds__(walk_threads<T>) void delta_fwd_kernel(DeltaArgs a) {
   if constexpr (sizeof(T) == 2) {
-    __shared__ PairFwdLds<NB, false> s;
-    pair_forward<NB, false>(a, s);
+    __shared__ PairFwdLds<NB, kResults> s;
+    pair_forward<NB, kResults>(a, s);
   } else {
-    __shared__ FwdLds<T, NB, false> s;
-    walk_forward<T, NB, false>(a, s);
+    __shared__ FwdLds<T, NB, kResults> s;
+    walk_forward<T, NB, kResults>(a, s);
+  }
+}
+
+template <class T, int NB>
+__global__ __launch_bounds__(walk_threads<T>) void delta_summary_kernel(DeltaArgs a) {
+  if constexpr (sizeof(T) == 2) {
+    __shared__ PairFwdLds<NB, kSummary> s;
+    pair_forward<NB, kSummary>(a, s);
+  } else {
+    __shared__ FwdLds<T, NB, kSummary> s;
+    walk_forward<T, NB, kSummary>(a, s);
+  }
+}
+
+// Turns the segments' own contributions into the states they start from, one
+// segment of a sequence after the other: S = Phi S + own.  REVERSE: the gradients
+// they end with, by the transposed Phi, from the last.  A wave has 16 columns.
+template <int NB, bool REVERSE>
+__global__ __launch_bounds__(kWaves * 64) void delta_carry_kernel(DeltaArgs a) {
+  const int lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
+  const int h = blockIdx.y, seq = blockIdx.z;
+  long row0;
+  int len;
+  seq_rows(a.seqs, seq, &row0, &len);
+  const int n = units_of(len, a.seg);
+  if (n < 2) return;
+  const long base = unit_base(a.seqs, seq, a.seg);
+  const long head = static_cast<long>(a.states) * a.width;
+  const float* first = REVERSE ? a.d_final : a.initial;
+  float* places = REVERSE ? a.seg_grad : a.seg_state;
+  State<NB, true> st, own;
+  st.init(a.width, blockIdx.x * kCols, wave_id());
+  own.off = st.off;
+  st.load(first == nullptr ? nullptr : first + (static_cast<long>(seq) * a.heads + h) * head, a.width, a.states);
+  for (int i = 1; i < n; ++i) {
+    const long at = base + (REVERSE ? n - 1 - i : i), by = REVERSE ? at + 1 : at - 1;
+    own.load(places + (at * a.heads + h) * head, a.width, a.states);
+    const Rsrc rs = make_rsrc(a.seg_trans + (by * a.heads + h) * a.states * a.states,
+                              static_cast<unsigned>(a.states * a.states * 4));
+#pragma unroll
+    for (int m = 0; m < 2 * NB; ++m) {
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        // row (REVERSE: column) 16 m + l15 of Phi, in result order; outside it is zero
+        const int row = 16 * m + l15, c = 32 * k + 4 * g;
+        Frag<float> f;
+        if (REVERSE) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            f.v[j >> 2][j & 3] = load_elem<float>(
+                rs, row < a.states ? static_cast<unsigned>(((c + (j >> 2) * 16 + (j & 3)) * a.states + row) * 4) : kOutside);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            f.v[j] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(
+                rs, c + 16 * j < a.states ? static_cast<unsigned>((row * a.states + c + 16 * j) * 4) : kOutside, 0, 0));
+        }
+        mma(own.st[m], f, split_pair<float, 1>(st.st[2 * k], st.st[2 * k + 1]).f[0]);
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < 2 * NB; ++m) st.st[m] = own.st[m];
+    st.save(places + (at * a.heads + h) * head, a.width, a.states);
   }
 }
 
@@ -134,19 +197,36 @@ __global__ __launch_bounds__(kStepThreads) void delta_step_kernel(StepArgs a) {
 
 // ---------------------------------------------------------------- host side
 template <class T, int NB>
-int launch_fwd(const DeltaArgs& a, unsigned steps, unsigned blocks, hipStream_t s) {
-  if (steps > 0) {
-    delta_prep_kernel<T, NB><<<steps, kPrepWaves * 64, 0, s>>>(a);
-    if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
-  }
-  delta_fwd_kernel<T, NB><<<blocks, walk_threads<T>, 0, s>>>(a);
+int launch_summary(const DeltaArgs& a, hipStream_t s) {
+  const int slices = a.slices + (a.states + kCols - 1) / kCols;
+  delta_summary_kernel<T, NB><<<static_cast<unsigned>(a.units) * a.heads * slices, walk_threads<T>, 0, s>>>(a);
+  if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
+  delta_carry_kernel<NB, false><<<dim3(a.slices, a.heads, a.seqs.batch), kWaves * 64, 0, s>>>(a);
   return launch_status();
 }
 template <class T>
-int launch_fwd_states(const DeltaArgs& a, unsigned steps, unsigned blocks, hipStream_t s) {
-  if (a.states <= 32) return launch_fwd<T, 1>(a, steps, blocks, s);
-  if (a.states <= 64) return launch_fwd<T, 2>(a, steps, blocks, s);
-  return launch_fwd<T, 4>(a, steps, blocks, s);
+int launch_summary_states(const DeltaArgs& a, hipStream_t s) {
+  if (a.states <= 32) return launch_summary<T, 1>(a, s);
+  if (a.states <= 64) return launch_summary<T, 2>(a, s);
+  return launch_summary<T, 4>(a, s);
+}
+
+template <class T, int NB>
+int launch_fwd(const DeltaArgs& a, unsigned steps, int type, hipStream_t s) {
+  if (steps > 0) {
+    delta_prep_kernel<T, NB><<<steps, kPrepWaves * 64, 0, s>>>(a);
+    if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
+    const int st = start_segments(a, type, s);
+    if (st != MAMBA2_SCAN_OK) return st;
+  }
+  delta_fwd_kernel<T, NB><<<walk_blocks(a), walk_threads<T>, 0, s>>>(a);
+  return launch_status();
+}
+template <class T>
+int launch_fwd_states(const DeltaArgs& a, unsigned steps, int type, hipStream_t s) {
+  if (a.states <= 32) return launch_fwd<T, 1>(a, steps, type, s);
+  if (a.states <= 64) return launch_fwd<T, 2>(a, steps, type, s);
+  return launch_fwd<T, 4>(a, steps, type, s);
 }
 
 long steps_of(const mamba2_seqs& q) { return unit_count(q, kTok); }
@@ -167,10 +247,13 @@ int check_delta(const mamba2_seqs& q, const mamba2_delta_dims& d) {
   const int st = check_dims(q, scan_dims(d));
   if (st != MAMBA2_SCAN_OK) return st;
   if (!(d.scale - d.scale == 0.0f)) return MAMBA2_SCAN_EBADDIM;
-  // the largest launches: up to 512 threads for every step and head, and 256 for every
-  // sequence (packed: one more), head and 64 columns
-  const long long most = steps_of(q) > q.batch + 1LL ? steps_of(q) : q.batch + 1LL;
-  return grid_ok(most * d.heads, 512) ? MAMBA2_SCAN_OK : MAMBA2_SCAN_EBADDIM;
+  // the largest launches: 512 threads for every step and head, and for every segment,
+  // head and 64 columns, in summaries of the values and of the state
+  for (const bool bwd : {false, true}) {
+    const long long units = unit_count(q, segment_tokens(q, d, bwd)) * ((d.width + kCols - 1) / kCols + (d.states + kCols - 1) / kCols);
+    if (!grid_ok(units * d.heads, 512)) return MAMBA2_SCAN_EBADDIM;
+  }
+  return grid_ok(static_cast<long long>(steps_of(q)) * d.heads, 512) ? MAMBA2_SCAN_OK : MAMBA2_SCAN_EBADDIM;
 }
 int check_keys(mamba2_rows* r, const mamba2_seqs& q, const mamba2_delta_dims& d) {
   const long long n = static_cast<long long>(d.groups) * d.states;
@@ -186,7 +269,66 @@ int check_gates(mamba2_rows* r, const mamba2_seqs& q, const mamba2_delta_dims& d
   *r = used_strides(*r, q, d.heads);
   return check_step_rows(*r, q, scan_dims(d));
 }
-void set_dims(DeltaArgs* a, const mamba2_seqs& q, const mamba2_delta_dims& d) {
+// Tokens per segment.  A head's columns are walked by work-groups of which a CU
+// holds one; with fewer of them than CUs the tokens are cut into segments.  That
+// costs the summary, a walk of the state's columns beside the values', and the
+// carry, whose segments follow one another.  In units of a walk's step: XXX
+int segment_tokens(const mamba2_seqs& q, const mamba2_delta_dims& d, bool bwd) {
+  const bool packed = q.offsets != nullptr;
+  // how a packed call's rows are shared out is not known here
+  const long seqs = packed ? (q.batch < 4 ? q.batch : 4) : q.batch;
+  const long steps = ((packed ? q.length / seqs : q.length) + kTok - 1) / kTok;
+  const long slices = (d.width + kCols - 1) / kCols, more = (d.states + kCols - 1) / kCols;
+  const long lanes = seqs * d.heads * slices, summary = seqs * d.heads * (slices + more);
+  const auto rounds = [](long n) { return static_cast<float>((n + kCUs - 1) / kCUs); };
+  const float carry = (d.states > 64 ? 1.5f : 0.7f) * (bwd ? 2 : 1), fixed = bwd ? 8.0f : 4.0f;
+  float best = 0.0f;
+  long cut = 1;
+  if (lanes < kCUs) {
+    for (long n = 1; n <= 64 && n <= steps; ++n) {
+      const float s = static_cast<float>((steps + n - 1) / n);
+      float cost = rounds(lanes * n) * s * (bwd ? 2.2f : 1.0f);
+      if (n > 1) cost += rounds(summary * n) * s * 0.7f + (bwd ? rounds(lanes * n) * s : 0.0f) + n * carry + fixed;
+      if (n == 1 || cost < best) {
+        best = cost;
+        cut = n;
+      }
+    }
+  }
+  const long rows = packed ? q.length / seqs : q.length;
+  long seg = cut > 1 ? (rows + cut - 1) / cut : q.length;
+  seg = (seg + kTok - 1) / kTok * kTok;
+  return static_cast<int>(seg < kTok ? kTok : seg);
+}
+
+int start_segments(const DeltaArgs& a, int type, hipStream_t s) {
+  if (a.seqs.length <= a.seg) return MAMBA2_SCAN_OK;
+  return type == MAMBA2_BF16 ? launch_summary_states<bf16>(a, s) : launch_summary_states<float>(a, s);
+}
+int carry_gradients(const DeltaArgs& a, hipStream_t s) {
+  const dim3 grid(a.slices, a.heads, a.seqs.batch);
+  if (a.states <= 32) delta_carry_kernel<1, true><<<grid, kWaves * 64, 0, s>>>(a);
+  else if (a.states <= 64) delta_carry_kernel<2, true><<<grid, kWaves * 64, 0, s>>>(a);
+  else delta_carry_kernel<4, true><<<grid, kWaves * 64, 0, s>>>(a);
+  return launch_status();
+}
+unsigned walk_blocks(const DeltaArgs& a) { return static_cast<unsigned>(a.units) * a.heads * a.slices; }
+
+size_t segment_bytes(const mamba2_seqs& q, const mamba2_delta_dims& d, bool bwd) {
+  const int seg = segment_tokens(q, d, bwd);
+  if (q.length <= seg) return 0;
+  const size_t head = static_cast<size_t>(d.states) * ((bwd ? 2 : 1) * d.width + d.states);
+  return static_cast<size_t>(unit_count(q, seg)) * d.heads * head * sizeof(float);
+}
+void set_segments(DeltaArgs* a, char* at, bool bwd) {
+  if (a->seqs.length <= a->seg) return;
+  const long cells = static_cast<long>(a->units) * a->heads, head = static_cast<long>(a->states) * a->width;
+  a->seg_state = reinterpret_cast<float*>(at);
+  a->seg_trans = a->seg_state + cells * head;
+  if (bwd) a->seg_grad = a->seg_trans + cells * a->states * a->states;
+}
+
+void set_dims(DeltaArgs* a, const mamba2_seqs& q, const mamba2_delta_dims& d, bool bwd) {
   a->seqs = q;
   a->scale = d.scale;
   a->heads = d.heads;
@@ -195,7 +337,8 @@ void set_dims(DeltaArgs* a, const mamba2_seqs& q, const mamba2_delta_dims& d) {
   a->states = d.states;
   a->slices = (d.width + kWaves * 16 - 1) / (kWaves * 16);
   a->gate_bf16 = d.gate_type == MAMBA2_BF16;
-  a->seg = q.length > kTok ? (q.length + kTok - 1) / kTok * kTok : kTok;
+  a->seg = segment_tokens(q, d, bwd);
+  a->units = static_cast<int>(unit_count(q, a->seg));
 }
 
 }  // namespace delta
@@ -204,7 +347,8 @@ extern "C" {
 
 size_t mamba2_delta_fwd_workspace_bytes(mamba2_seqs seqs, mamba2_delta_dims d) {
   if (check_delta(seqs, d) != MAMBA2_SCAN_OK) return 0;
-  return static_cast<size_t>(steps_of(seqs)) * d.heads * (m_bytes(d.type) + p_bytes(d.type) + sizeof(Coef));
+  return static_cast<size_t>(steps_of(seqs)) * d.heads * (m_bytes(d.type) + p_bytes(d.type) + sizeof(Coef)) +
+         segment_bytes(seqs, d, false);
 }
 
 int mamba2_delta_fwd(mamba2_seqs seqs, mamba2_delta_dims d, mamba2_rows q, mamba2_rows k, mamba2_rows v, mamba2_rows g,
@@ -230,16 +374,16 @@ int mamba2_delta_fwd(mamba2_seqs seqs, mamba2_delta_dims d, mamba2_rows q, mamba
   if (seqs.length == 0 && final_state == nullptr) return MAMBA2_SCAN_OK;
   a.initial = initial_state;
   a.final_state = final_state;
-  set_dims(&a, seqs, d);
+  set_dims(&a, seqs, d, false);
   const long cells = steps_of(seqs) * d.heads;
   char* at = static_cast<char*>(workspace);
   a.m = at;
   a.p = at + cells * m_bytes(d.type);
   a.coef = reinterpret_cast<Coef*>(at + cells * (m_bytes(d.type) + p_bytes(d.type)));
   const unsigned steps = seqs.length == 0 ? 0 : static_cast<unsigned>(cells);
-  const unsigned blocks = static_cast<unsigned>(unit_count(seqs, a.seg) * d.heads * a.slices);
+  set_segments(&a, reinterpret_cast<char*>(a.coef + cells), false);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return d.type == MAMBA2_BF16 ? launch_fwd_states<bf16>(a, steps, blocks, s) : launch_fwd_states<float>(a, steps, blocks, s);
+  return d.type == MAMBA2_BF16 ? launch_fwd_states<bf16>(a, steps, d.type, s) : launch_fwd_states<float>(a, steps, d.type, s);
 }
 
 int mamba2_delta_step(int batch, mamba2_delta_dims d, mamba2_rows q, mamba2_rows k, mamba2_rows v, mamba2_rows g,

@@ -47,22 +47,22 @@ __global__ __launch_bounds__(kPrepWaves * 64) void delta_bwd_prep_kernel(DeltaAr
 template <class T, int NB>
 __global__ __launch_bounds__(walk_threads<T>) void delta_keep_kernel(DeltaArgs a) {
   if constexpr (sizeof(T) == 2) {
-    __shared__ PairFwdLds<NB, true> s;
-    pair_forward<NB, true>(a, s);
+    __shared__ PairFwdLds<NB, kKept> s;
+    pair_forward<NB, kKept>(a, s);
   } else {
-    __shared__ FwdLds<T, NB, true> s;
-    walk_forward<T, NB, true>(a, s);
+    __shared__ FwdLds<T, NB, kKept> s;
+    walk_forward<T, NB, kKept>(a, s);
   }
 }
 
-template <class T, int NB>
+template <class T, int NB, bool SUMMARY>
 __global__ __launch_bounds__(walk_threads<T>) void delta_reverse_kernel(DeltaArgs a) {
   if constexpr (sizeof(T) == 2) {
     __shared__ PairRevLds<NB> s;
-    pair_reverse<NB>(a, s);
+    pair_reverse<NB, SUMMARY>(a, s);
   } else {
     __shared__ RevLds<T, NB> s;
-    walk_reverse<T, NB>(a, s);
+    walk_reverse<T, NB, SUMMARY>(a, s);
   }
 }
 
@@ -569,23 +569,30 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
 
 // ---------------------------------------------------------------- host side
 template <class T, int NB>
-int launch_bwd(const DeltaArgs& a, unsigned steps, unsigned blocks, hipStream_t s) {
+int launch_bwd(const DeltaArgs& a, unsigned steps, int type, hipStream_t s) {
   if (steps > 0) {
     delta_bwd_prep_kernel<T, NB><<<steps, kPrepWaves * 64, 0, s>>>(a);
     if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
-    delta_keep_kernel<T, NB><<<blocks, walk_threads<T>, 0, s>>>(a);
+    int st = start_segments(a, type, s);
+    if (st != MAMBA2_SCAN_OK) return st;
+    delta_keep_kernel<T, NB><<<walk_blocks(a), walk_threads<T>, 0, s>>>(a);
     if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
+    if (a.seg_grad != nullptr) {
+      delta_reverse_kernel<T, NB, true><<<walk_blocks(a), walk_threads<T>, 0, s>>>(a);
+      if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
+      if ((st = carry_gradients(a, s)) != MAMBA2_SCAN_OK) return st;
+    }
   }
-  delta_reverse_kernel<T, NB><<<blocks, walk_threads<T>, 0, s>>>(a);
+  delta_reverse_kernel<T, NB, false><<<walk_blocks(a), walk_threads<T>, 0, s>>>(a);
   if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
   if (steps > 0) delta_grads_kernel<T, NB><<<steps / a.ratio, kGradWaves * 64, 0, s>>>(a);
   return launch_status();
 }
 template <class T>
-int launch_bwd_states(const DeltaArgs& a, unsigned steps, unsigned blocks, hipStream_t s) {
-  if (a.states <= 32) return launch_bwd<T, 1>(a, steps, blocks, s);
-  if (a.states <= 64) return launch_bwd<T, 2>(a, steps, blocks, s);
-  return launch_bwd<T, 4>(a, steps, blocks, s);
+int launch_bwd_states(const DeltaArgs& a, unsigned steps, int type, hipStream_t s) {
+  if (a.states <= 32) return launch_bwd<T, 1>(a, steps, type, s);
+  if (a.states <= 64) return launch_bwd<T, 2>(a, steps, type, s);
+  return launch_bwd<T, 4>(a, steps, type, s);
 }
 
 // The workspace's parts: bytes for each step of each head.
@@ -607,7 +614,7 @@ extern "C" {
 
 size_t mamba2_delta_bwd_workspace_bytes(mamba2_seqs seqs, mamba2_delta_dims d) {
   if (check_delta(seqs, d) != MAMBA2_SCAN_OK) return 0;
-  return static_cast<size_t>(unit_count(seqs, kTok)) * d.heads * bwd_cell(d).all;
+  return static_cast<size_t>(unit_count(seqs, kTok)) * d.heads * bwd_cell(d).all + segment_bytes(seqs, d, true);
 }
 
 int mamba2_delta_bwd(mamba2_seqs seqs, mamba2_delta_dims d, mamba2_rows q, mamba2_rows k, mamba2_rows v, mamba2_rows g,
@@ -646,7 +653,7 @@ int mamba2_delta_bwd(mamba2_seqs seqs, mamba2_delta_dims d, mamba2_rows q, mamba
   a.initial = initial_state;
   a.d_final = d_final_state;
   a.d_initial = d_initial_state;
-  set_dims(&a, seqs, d);
+  set_dims(&a, seqs, d, true);
   const long cells = static_cast<long>(unit_count(seqs, kTok)) * d.heads;
   const BwdCell c = bwd_cell(d);
   char* at = static_cast<char*>(workspace);
@@ -664,9 +671,9 @@ int mamba2_delta_bwd(mamba2_seqs seqs, mamba2_delta_dims d, mamba2_rows q, mamba
   a.d_r = reinterpret_cast<float*>(take(c.rows));
   a.coef = reinterpret_cast<Coef*>(take(sizeof(Coef)));
   const unsigned steps = seqs.length == 0 ? 0 : static_cast<unsigned>(cells);
-  const unsigned blocks = static_cast<unsigned>(unit_count(seqs, a.seg) * d.heads * a.slices);
+  set_segments(&a, at, true);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return d.type == MAMBA2_BF16 ? launch_bwd_states<bf16>(a, steps, blocks, s) : launch_bwd_states<float>(a, steps, blocks, s);
+  return d.type == MAMBA2_BF16 ? launch_bwd_states<bf16>(a, steps, d.type, s) : launch_bwd_states<float>(a, steps, d.type, s);
 }
 
 }  // extern "C"

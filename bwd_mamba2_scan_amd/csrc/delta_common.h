@@ -52,6 +52,10 @@ struct DeltaArgs {
   int slices;              // work-groups per head: slices of its width
   int gate_bf16;
   int seg;                 // tokens per segment (a multiple of kTok)
+  int units;               // segments of the call
+  float* seg_state;        // [units][heads][states][width]: the state a segment starts from
+  float* seg_trans;        // [units][heads][states][states]: what a segment makes of it
+  float* seg_grad;         // [units][heads][states][width]: the gradient of the state a segment ends with
   void* m;                 // [steps][heads][kExact][kPieces][kPiece]: M
   void* p;                 // [steps][heads][kTwo][kPieces][kPiece]: P
   Coef* coef;              // [steps][heads]
@@ -78,6 +82,24 @@ template <>
 struct Raw<bf16> {
   short v;
 };
+// What a walk over a segment is for: the results, each step's starting state and U
+// (for the backward), or a summary for the segments behind: with columns of V
+// the segment's own contribution to the state, and with columns of the unit
+// matrix in place of the state and no V what it makes of the state before it.
+enum Walked { kResults, kKept, kSummary };
+
+// A walk's place in the call.  Every XCD gets all sequences of some heads, whose
+// unequal lengths would else leave some XCDs with more (the walk of nine prompts
+// 256 us with neighbouring sequences on an XCD, XXX).
+struct WalkWork {
+  int unit, h, slice;
+};
+__device__ __forceinline__ WalkWork walk_work(const DeltaArgs& a, int slices) {
+  const int i = xcd_contiguous(blockIdx.x, gridDim.x);
+  const int hs = i / a.units;
+  return {i - hs * a.units, hs / slices, hs % slices};
+}
+
 template <class T>
 __device__ __forceinline__ Raw<T> load_raw_elem(Rsrc rs, unsigned off) {
   if constexpr (sizeof(T) == 2) return {static_cast<short>(__builtin_amdgcn_raw_buffer_load_b16(rs, off, 0, 0))};
@@ -209,6 +231,14 @@ int check_delta(const mamba2_seqs& q, const mamba2_delta_dims& d);
 int check_keys(mamba2_rows* r, const mamba2_seqs& q, const mamba2_delta_dims& d);
 int check_values(mamba2_rows* r, const mamba2_seqs& q, const mamba2_delta_dims& d);
 int check_gates(mamba2_rows* r, const mamba2_seqs& q, const mamba2_delta_dims& d);
-void set_dims(DeltaArgs* a, const mamba2_seqs& q, const mamba2_delta_dims& d);
+int segment_tokens(const mamba2_seqs& q, const mamba2_delta_dims& d, bool bwd);
+size_t segment_bytes(const mamba2_seqs& q, const mamba2_delta_dims& d, bool bwd);
+void set_dims(DeltaArgs* a, const mamba2_seqs& q, const mamba2_delta_dims& d, bool bwd);
+void set_segments(DeltaArgs* a, char* at, bool bwd);  // the segments' part of the workspace
+// The states that the segments start from, where there are several; for the
+// backward also their transitions, with which carry_gradients finishes the gradients.
+int start_segments(const DeltaArgs& a, int type, hipStream_t s);
+int carry_gradients(const DeltaArgs& a, hipStream_t s);
+unsigned walk_blocks(const DeltaArgs& a);
 
 }  // namespace delta

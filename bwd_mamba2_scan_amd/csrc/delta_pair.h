@@ -61,7 +61,7 @@ __device__ __forceinline__ void read_pieces(Frag<bf16> (&f)[3][kPieces], const b
 }
 
 
-template <int NB, bool KEEP>
+template <int NB, Walked MODE>
 struct PairFwdLds {
   static constexpr int ldn = stride_of<bf16>(NB * 32);
   static constexpr int ldv = stride_of<bf16>(kCols);
@@ -81,23 +81,20 @@ struct PairFwdLds {
 };
 
 // As walk_forward.
-template <int NB, bool KEEP>
-__device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, KEEP>& s) {
-  typedef PairFwdLds<NB, KEEP> L;
+template <int NB, Walked MODE>
+__device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, MODE>& s) {
+  typedef PairFwdLds<NB, MODE> L;
   constexpr int kM = 3 * kPieces * kPiece, kP = 2 * kPieces * kPiece;
   const int wave = wave_id(), lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
   const int strip = wave & (kWaves - 1);
-  const int work = xcd_contiguous(blockIdx.x, gridDim.x);
-  const int per = a.heads * a.slices;
-  const int unit = work / per, h = work % per / a.slices, slice = work % a.slices;
-  const Unit u = locate(a.seqs, unit, a.seg);
-  if (!u.live) return;
+  const Columns cl = columns_of<MODE>(a);
+  const Unit u = locate(a.seqs, cl.unit, a.seg);
+  if (!u.live || !wanted<MODE>(a, cl, u)) return;
+  const int h = cl.h, p0 = cl.p0;
   const bool packed = a.seqs.offsets != nullptr;
-  const int p0 = slice * kCols;
   const long head = static_cast<long>(a.states) * a.width;
-  const long of_seq = (static_cast<long>(u.seq) * a.heads + h) * head;
   const long cell0 = static_cast<long>(unit_base(a.seqs, u.seq, kTok)) * a.heads + h;  // of the sequence's first step
-  const int end = u.len;
+  const int end = min(u.t0 + a.seg, u.len);
 
   if (wave >= kWaves) {  // a helper
     const int tid = threadIdx.x - kHelpers;
@@ -110,7 +107,7 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
     Flat<kM * sizeof(bf16), kHelpers> tm;
     Flat<sizeof(Coef), kHelpers> tc;
     Frag<bf16> pf[2][kPieces];
-    const int cols = min(a.width - p0, kCols);
+    const int cols = cl.cols;
     tk.init(a.k.row_stride, a.states, tid);
     tq.init(a.q.row_stride, a.states, tid);
     tv.init(a.v.row_stride, cols, tid);
@@ -124,14 +121,14 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
       tm.load(static_cast<const bf16*>(a.m) + at * kM, tid);
       tc.load(a.coef + at, tid);
       tv.load(rows_rsrc(vp + t * a.v.row_stride, a.v.row_stride, rows, cols));
-      if (!KEEP) tq.load(rows_rsrc(qp + t * a.q.row_stride, a.q.row_stride, rows, a.states));
+      if (MODE == kResults) tq.load(rows_rsrc(qp + t * a.q.row_stride, a.q.row_stride, rows, a.states));
     };
     const auto put = [&](int b) {
       tk.store(s.step[b].k, L::ldn, tid);
       tm.store(s.step[b].m, tid);
       tc.store(&s.step[b].coef, tid);
       tv.store(s.v[b], L::ldv, tid);
-      if (!KEEP) tq.store(s.out.q, L::ldn, tid);
+      if (MODE == kResults) tq.store(s.out.q, L::ldn, tid);
     };
     const auto fetch_p = [&](int t) {
       const bf16* p = static_cast<const bf16*>(a.p) + (cell0 + static_cast<long>(t / kTok) * a.heads) * kP;
@@ -142,7 +139,7 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
     };
     if (u.t0 < end) {
       fetch(u.t0);
-      if (!KEEP) fetch_p(u.t0);
+      if (MODE == kResults) fetch_p(u.t0);
       put(0);
     }
     int b = 0;
@@ -152,10 +149,14 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
       // waits for these loads wait for what is issued after them, too
       const int next = t + kTok < end ? t + kTok : t;
       fetch(next);
+      if (MODE == kSummary) {
+        put(b ^ 1);
+        continue;
+      }
       __syncthreads();  // the state is in LDS
       const long cell = cell0 + static_cast<long>(t / kTok) * a.heads;
       v4f y[4];
-      if (KEEP) {
+      if (MODE == kKept) {
         swap_save<2 * NB>(a.keep + cell * head, a.states, a.width, p0 + strip * 16, s.keep.s[strip], lane);
       } else {  // (Q S)^T
 #pragma unroll
@@ -175,7 +176,7 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
         for (int i = 0; i < 4; ++i) y[i] = y[i] * (a.scale * s.step[b].coef.from[16 * i + l15]);
       }
       __syncthreads();  // U is in LDS
-      if (KEEP) {
+      if (MODE == kKept) {
         swap_save<4>(a.u + cell * (kTok * static_cast<long>(a.width)), kTok, a.width, p0 + strip * 16, s.keep.u[strip], lane);
       } else {
         Split<bf16, 2> us[2];
@@ -195,8 +196,7 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
   }
 
   State<NB, true> st;
-  st.init(a.width, p0, strip);
-  st.load(a.initial == nullptr ? nullptr : a.initial + of_seq, a.width, a.states);
+  first_state<MODE>(st, a, cl, u, strip);
   int b = 0;
   for (int t = u.t0; t < end; t += kTok, b ^= 1) {
     __syncthreads();
@@ -207,7 +207,7 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
       for (int i = 0; i < 4; ++i) kf[n & 1][i] = frag_row_result(p.k, L::ldn, 16 * i, 32 * n);
     };
     read_rows(0);
-    if (KEEP) {
+    if (MODE == kKept) {
 #pragma unroll
       for (int n = 0; n < 2 * NB; ++n) swap_put(s.keep.s[strip] + n * kSwapTile, lane, st.st[n]);
     }
@@ -226,7 +226,7 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
       }
       keep_reads_here();
       const Split<bf16, 3> sp = split_pair<bf16, 3>(st.st[2 * n], st.st[2 * n + 1]);
-      if (!KEEP) {
+      if (MODE == kResults) {
         piece_put(s.out.s[strip][n][0], lane, sp.f[0]);
         piece_put(s.out.s[strip][n][1], lane, sp.f[1]);
       }
@@ -235,7 +235,7 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) mma(ks[i], kf[n & 1][i], sp.f[z]);
     }
-    __syncthreads();
+    if (MODE != kSummary) __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = rows_of(p.coef.beta, i, g) * (x[i] - rows_of(p.coef.from, i, g) * ks[i]);
     const Split<bf16, 3> xs[2] = {split_pair<bf16, 3>(x[0], x[1]), split_pair<bf16, 3>(x[2], x[3])};
@@ -257,10 +257,10 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
     read_cols(0);
     const float total = p.coef.total;
     keep_reads_here();
-    if (KEEP) {
+    if (MODE == kKept) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) swap_put(s.keep.u[strip] + i * kSwapTile, lane, w[i]);
-    } else {
+    } else if (MODE == kResults) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const Split<bf16, 2> us = split_pair<bf16, 2>(w[2 * j], w[2 * j + 1]);
@@ -268,7 +268,7 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
         piece_put(s.out.u[strip][j][1], lane, us.f[1]);
       }
     }
-    __syncthreads();
+    if (MODE != kSummary) __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = w[i] * to[i];
     const Split<bf16, 3> us[2] = {split_pair<bf16, 3>(w[0], w[1]), split_pair<bf16, 3>(w[2], w[3])};
@@ -288,7 +288,7 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
       for (int i = 0; i < kTiles; ++i) st.st[n + i] = st.st[n + i] * total + add[i];
     }
   }
-  if (!KEEP && a.final_state != nullptr) st.save(a.final_state + of_seq, a.width, a.states);
+  last_state<MODE>(st, a, cl, u);
 }
 
 template <int NB>
@@ -305,24 +305,22 @@ struct PairRevLds {
 
 // As walk_reverse.  LDS holds one step here: the helpers keep the next one in
 // registers until the walkers are done with this one's operands.
-template <int NB>
+template <int NB, bool SUMMARY>
 __device__ __forceinline__ void pair_reverse(const DeltaArgs& a, PairRevLds<NB>& s) {
   typedef PairRevLds<NB> L;
   constexpr int kM = 3 * kPieces * kPiece;
   constexpr int kTiles = 2 * NB < 4 ? 2 * NB : 4;
   const int wave = wave_id(), lane = threadIdx.x & 63, g = lane >> 4;
   const int strip = wave & (kWaves - 1);
-  const int work = xcd_contiguous(blockIdx.x, gridDim.x);
-  const int per = a.heads * a.slices;
-  const int unit = work / per, h = work % per / a.slices, slice = work % a.slices;
-  const Unit u = locate(a.seqs, unit, a.seg);
-  if (!u.live) return;
+  const WalkWork wk = walk_work(a, a.slices);
+  const Unit u = locate(a.seqs, wk.unit, a.seg);
+  if (!u.live || (SUMMARY && u.index == 0)) return;
+  const int h = wk.h, slice = wk.slice;
   const bool packed = a.seqs.offsets != nullptr;
   const int p0 = slice * kCols;
   const long head = static_cast<long>(a.states) * a.width, slab = kTok * static_cast<long>(a.width);
-  const long of_seq = (static_cast<long>(u.seq) * a.heads + h) * head;
   const long cell0 = static_cast<long>(unit_base(a.seqs, u.seq, kTok)) * a.heads + h;
-  const int end = u.len;
+  const int end = min(u.t0 + a.seg, u.len);
   const int last = end > u.t0 ? u.t0 + (end - 1 - u.t0) / kTok * kTok : u.t0 - kTok;
   const Coef& coef = s.step.coef;
 
@@ -397,10 +395,11 @@ __device__ __forceinline__ void pair_reverse(const DeltaArgs& a, PairRevLds<NB>&
       }
       __syncthreads();  // D and dR are in LDS
       const long cell = cell0 + static_cast<long>(t / kTok) * a.heads;
-      swap_save<2 * NB>(a.d_keep + cell * head, a.states, a.width, p0 + strip * 16, s.d[strip], lane);
+      if (!SUMMARY) swap_save<2 * NB>(a.d_keep + cell * head, a.states, a.width, p0 + strip * 16, s.d[strip], lane);
 #pragma unroll
       for (int n = 0; n < 2 * NB; ++n) swap_put(s.d[strip] + n * kSwapTile, lane, add[n]);
       __syncthreads();  // the walkers are done with the operands but for what was put last
+      if (SUMMARY) continue;
       swap_save<4>(a.d_r + cell * slab, kTok, a.width, p0 + strip * 16, s.r[strip], lane);
       const Rsrc rv = rows_rsrc(vp + t * a.d_v.row_stride, a.d_v.row_stride, min(end - t, kTok), a.width);
 #pragma unroll
@@ -412,7 +411,7 @@ __device__ __forceinline__ void pair_reverse(const DeltaArgs& a, PairRevLds<NB>&
 
   State<NB, true> st;
   st.init(a.width, p0, strip);
-  st.load(a.d_final == nullptr ? nullptr : a.d_final + of_seq, a.width, a.states);
+  first_gradient<SUMMARY>(st, a, wk, u);
   for (int t = last; t >= u.t0; t -= kTok) {
     __syncthreads();
     const PairStep<NB>& p = s.step;
@@ -423,7 +422,8 @@ __device__ __forceinline__ void pair_reverse(const DeltaArgs& a, PairRevLds<NB>&
     };
     read_rows(0);
 #pragma unroll
-    for (int n = 0; n < 2 * NB; ++n) swap_put(s.d[strip] + n * kSwapTile, lane, st.st[n]);
+    for (int n = 0; n < 2 * NB; ++n)
+      if (!SUMMARY) swap_put(s.d[strip] + n * kSwapTile, lane, st.st[n]);
     v4f w[4], dy[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = v4f{0, 0, 0, 0};
@@ -473,7 +473,8 @@ __device__ __forceinline__ void pair_reverse(const DeltaArgs& a, PairRevLds<NB>&
     read_cols(0);
     keep_reads_here();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) swap_put(s.r[strip] + i * kSwapTile, lane, dr[i]);
+    for (int i = 0; i < 4; ++i)
+      if (!SUMMARY) swap_put(s.r[strip] + i * kSwapTile, lane, dr[i]);
     __syncthreads();
     // D = 2^c_end D - K^T (beta 2^c dR) + what the helper has
 #pragma unroll
@@ -497,7 +498,7 @@ __device__ __forceinline__ void pair_reverse(const DeltaArgs& a, PairRevLds<NB>&
     for (int n = 0; n < 2 * NB; ++n)
       st.st[n] = st.st[n] * total + (add[n] + swap_get(s.d[strip] + n * kSwapTile, lane));
   }
-  if (a.d_initial != nullptr) st.save(a.d_initial + of_seq, a.width, a.states);
+  last_gradient<SUMMARY>(st, a, wk, u);
 }
 
 }  // namespace delta

@@ -53,7 +53,60 @@ __device__ __forceinline__ v4f tile_col(const float* p, int ld, int i, int col, 
   return v4f{r[0], r[ld], r[2 * ld], r[3 * ld]};
 }
 
-template <class T, int NB, bool KEEP>
+// A walk's columns: of the head's values, or in a summary behind those of the
+// state itself.
+struct Columns {
+  int unit, h, p0, width, cols;  // cols: of V
+  bool trans;
+};
+template <Walked MODE>
+__device__ __forceinline__ Columns columns_of(const DeltaArgs& a) {
+  const int ks = MODE == kSummary ? (a.states + kCols - 1) / kCols : 0;
+  const WalkWork w = walk_work(a, a.slices + ks);
+  const bool trans = MODE == kSummary && w.slice >= a.slices;
+  const int p0 = (trans ? w.slice - a.slices : w.slice) * kCols;
+  return {w.unit, w.h, p0, trans ? a.states : a.width, trans ? 0 : min(a.width - p0, kCols), trans};
+}
+__device__ __forceinline__ bool last_unit(const DeltaArgs& a, const Unit& u) {
+  return u.t0 + static_cast<long>(a.seg) >= u.len;
+}
+// A summary is of use to a segment behind, and in the backward, where the gradient
+// passes through the transposed transitions, of a segment before.
+template <Walked MODE>
+__device__ __forceinline__ bool wanted(const DeltaArgs& a, const Columns& c, const Unit& u) {
+  if (MODE != kSummary) return true;
+  const bool last = last_unit(a, u);
+  if (c.trans) return last ? a.seg_grad != nullptr && u.index > 0 : true;
+  return !last;
+}
+template <Walked MODE, int NB>
+__device__ __forceinline__ void first_state(State<NB, true>& st, const DeltaArgs& a, const Columns& c, const Unit& u, int strip) {
+  const long head = static_cast<long>(a.states) * a.width;
+  st.init(c.width, c.p0, strip);
+  if (MODE == kSummary) {
+    const int lane = threadIdx.x & 63, col = c.p0 + strip * 16 + (lane & 15), row = 4 * (lane >> 4);
+#pragma unroll
+    for (int n = 0; n < 2 * NB; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) st.st[n][i] = c.trans && 16 * n + row + i == col ? 1.0f : 0.0f;
+  } else if (u.index > 0) {
+    st.load(a.seg_state + (static_cast<long>(c.unit) * a.heads + c.h) * head, a.width, a.states);
+  } else {
+    st.load(a.initial == nullptr ? nullptr : a.initial + (static_cast<long>(u.seq) * a.heads + c.h) * head, a.width, a.states);
+  }
+}
+template <Walked MODE, int NB>
+__device__ __forceinline__ void last_state(const State<NB, true>& st, const DeltaArgs& a, const Columns& c, const Unit& u) {
+  const long at = static_cast<long>(c.unit) * a.heads + c.h;
+  if (MODE == kSummary) {
+    if (c.trans) st.save(a.seg_trans + at * a.states * a.states, a.states, a.states);
+    else st.save(a.seg_state + (at + a.heads) * a.states * a.width, a.width, a.states);  // the next one's place
+  } else if (MODE == kResults && a.final_state != nullptr && last_unit(a, u)) {
+    st.save(a.final_state + (static_cast<long>(u.seq) * a.heads + c.h) * a.states * a.width, a.width, a.states);
+  }
+}
+
+template <class T, int NB, Walked MODE>
 struct FwdLds {
   static constexpr int ldn = stride_of<T>(NB * 32);
   static constexpr int ldv = stride_of<T>(kCols);
@@ -61,37 +114,32 @@ struct FwdLds {
   alignas(16) T m[kExact<T> * kPieces * kPiece];
   alignas(16) Coef coef;
   alignas(16) T v[kTok * ldv];
-  alignas(16) T q[KEEP ? 8 : kTok * ldn];
-  alignas(16) T p[KEEP ? 8 : kTwo<T> * kPieces * kPiece];
+  alignas(16) T q[MODE != kResults ? 8 : kTok * ldn];
+  alignas(16) T p[MODE != kResults ? 8 : kTwo<T> * kPieces * kPiece];
 };
 
-// The walk of a head's 64 columns.  KEEP false: writes y.  KEEP true (for the
-// backward): writes each step's starting state and its U instead.
-template <class T, int NB, bool KEEP>
-__device__ __forceinline__ void walk_forward(const DeltaArgs& a, FwdLds<T, NB, KEEP>& s) {
-  typedef FwdLds<T, NB, KEEP> L;
+// The walk of 64 columns of a head over a segment.
+template <class T, int NB, Walked MODE>
+__device__ __forceinline__ void walk_forward(const DeltaArgs& a, FwdLds<T, NB, MODE>& s) {
+  typedef FwdLds<T, NB, MODE> L;
   constexpr int kThreads = kWaves * 64;
   constexpr int kM = kExact<T> * kPieces * kPiece, kP = kTwo<T> * kPieces * kPiece;
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
-  const int work = xcd_contiguous(blockIdx.x, gridDim.x);
-  const int per = a.heads * a.slices;
-  const int unit = work / per, h = work % per / a.slices, slice = work % a.slices;
-  const Unit u = locate(a.seqs, unit, a.seg);
-  if (!u.live) return;
+  const Columns cl = columns_of<MODE>(a);
+  const Unit u = locate(a.seqs, cl.unit, a.seg);
+  if (!u.live || !wanted<MODE>(a, cl, u)) return;
+  const int h = cl.h, p0 = cl.p0;
   const bool packed = a.seqs.offsets != nullptr;
-  const int p0 = slice * kThreads / 4;
   const int col = p0 + wave * 16 + l15;
-  const long of_seq = (static_cast<long>(u.seq) * a.heads + h) * (static_cast<long>(a.states) * a.width);
   const T* kp = seq_ptr<const T>(a.k, u.seq, u.row0, packed) + h / a.ratio * a.states;
   const T* qp = seq_ptr<const T>(a.q, u.seq, u.row0, packed) + h / a.ratio * a.states;
   const T* vp = seq_ptr<const T>(a.v, u.seq, u.row0, packed) + h * a.width + p0;
   T* yp = seq_ptr<T>(a.y, u.seq, u.row0, packed) + h * a.width;
 
   State<NB, true> st;
-  st.init(a.width, p0, wave);
-  st.load(a.initial == nullptr ? nullptr : a.initial + of_seq, a.width, a.states);
+  first_state<MODE>(st, a, cl, u, wave);
 
-  const int end = u.len;
+  const int end = min(u.t0 + a.seg, u.len);
   const long cell0 = static_cast<long>(unit_base(a.seqs, u.seq, kTok)) * a.heads + h;  // of the sequence's first step
   Tile<T, kTok, NB * 32, kThreads> tk, tq;
   tk.init(a.k.row_stride, a.states, tid);
@@ -100,7 +148,7 @@ __device__ __forceinline__ void walk_forward(const DeltaArgs& a, FwdLds<T, NB, K
   Flat<kP * sizeof(T), kThreads> tp;
   Flat<sizeof(Coef), kThreads> tc;
   Tile<T, kTok, kCols, kThreads> tv;
-  tv.init(a.v.row_stride, min(a.width - p0, kCols), tid);
+  tv.init(a.v.row_stride, cl.cols, tid);
   // y^T: this lane's token of each tile, four columns
   const int quad = p0 + wave * 16 + 4 * g;
   const unsigned y_off = quad < a.width ? static_cast<unsigned>((l15 * static_cast<int>(a.y.row_stride) + quad) * sizeof(T)) : kOutside;
@@ -109,26 +157,26 @@ __device__ __forceinline__ void walk_forward(const DeltaArgs& a, FwdLds<T, NB, K
     const int rows = min(end - t, kTok);
     const long at = cell0 + static_cast<long>(t / kTok) * a.heads;
     tk.load(rows_rsrc(kp + t * a.k.row_stride, a.k.row_stride, rows, a.states));
-    if (!KEEP) tq.load(rows_rsrc(qp + t * a.q.row_stride, a.q.row_stride, rows, a.states));
+    if (MODE == kResults) tq.load(rows_rsrc(qp + t * a.q.row_stride, a.q.row_stride, rows, a.states));
     tm.load(static_cast<const T*>(a.m) + at * kM, tid);
-    if (!KEEP) tp.load(static_cast<const T*>(a.p) + at * kP, tid);
+    if (MODE == kResults) tp.load(static_cast<const T*>(a.p) + at * kP, tid);
     tc.load(a.coef + at, tid);
-    tv.load(rows_rsrc(vp + t * a.v.row_stride, a.v.row_stride, rows, min(a.width - p0, kCols)));
+    tv.load(rows_rsrc(vp + t * a.v.row_stride, a.v.row_stride, rows, cl.cols));
   };
   if (u.t0 < end) fetch(u.t0);
   for (int t = u.t0; t < end; t += kTok) {
     __syncthreads();
     tk.store(s.k, L::ldn, tid);
-    if (!KEEP) tq.store(s.q, L::ldn, tid);
+    if (MODE == kResults) tq.store(s.q, L::ldn, tid);
     tm.store(s.m, tid);
-    if (!KEEP) tp.store(s.p, tid);
+    if (MODE == kResults) tp.store(s.p, tid);
     tc.store(&s.coef, tid);
     tv.store(s.v, L::ldv, tid);
     __syncthreads();
     if (t + kTok < end) fetch(t + kTok);
 
     const long cell = cell0 + static_cast<long>(t / kTok) * a.heads;
-    if (KEEP) st.save(a.keep + cell * (static_cast<long>(a.states) * a.width), a.width, a.states);
+    if (MODE == kKept) st.save(a.keep + cell * (static_cast<long>(a.states) * a.width), a.width, a.states);
     // K S and (Q S)^T.  The operands of a part are read from LDS while the part
     // before it is multiplied: one wave a SIMD hides no latency by itself.
     constexpr int kBuf = NB > 1 ? 2 : 1;
@@ -138,7 +186,7 @@ __device__ __forceinline__ void walk_forward(const DeltaArgs& a, FwdLds<T, NB, K
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         kf[n % kBuf][i] = frag_row_result(s.k, L::ldn, 16 * i, 32 * n);
-        if (!KEEP) qf[n % kBuf][i] = frag_row_result(s.q, L::ldn, 16 * i, 32 * n);
+        if (MODE == kResults) qf[n % kBuf][i] = frag_row_result(s.q, L::ldn, 16 * i, 32 * n);
       }
     };
     v4f ks[4], qs[4];
@@ -169,7 +217,7 @@ __device__ __forceinline__ void walk_forward(const DeltaArgs& a, FwdLds<T, NB, K
       for (int z = kExact<T> - 1; z >= 0; --z) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) mma(ks[i], kf[n % kBuf][i], sp.f[z]);
-        if (!KEEP && z < kTwo<T>) {
+        if (MODE == kResults && z < kTwo<T>) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) mma(qs[i], sp.f[z], qf[n % kBuf][i]);
         }
@@ -180,7 +228,7 @@ __device__ __forceinline__ void walk_forward(const DeltaArgs& a, FwdLds<T, NB, K
     for (int i = 0; i < 4; ++i) x[i] = beta[i] * (x[i] - from[i] * ks[i]);
     const Split<T, kExact<T>> xs[2] = {split_pair<T, kExact<T>>(x[0], x[1]), split_pair<T, kExact<T>>(x[2], x[3])};
     Frag<T> pf[kTwo<T>][kPieces];
-    if (!KEEP) {
+    if (MODE == kResults) {
 #pragma unroll
       for (int z = 0; z < kTwo<T>; ++z)
 #pragma unroll
@@ -189,7 +237,7 @@ __device__ __forceinline__ void walk_forward(const DeltaArgs& a, FwdLds<T, NB, K
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       to[i] = rows_of(s.coef.to, i, g);
-      if (!KEEP) mine[i] = a.scale * s.coef.from[16 * i + l15];
+      if (MODE == kResults) mine[i] = a.scale * s.coef.from[16 * i + l15];
     }
     keep_reads_here();
     v4f w[4];
@@ -207,9 +255,9 @@ __device__ __forceinline__ void walk_forward(const DeltaArgs& a, FwdLds<T, NB, K
     };
     read_cols(0);
     keep_reads_here();
-    if (KEEP) {
+    if (MODE == kKept) {
       save_rows(a.u + cell * (kTok * static_cast<long>(a.width)), a.width, col, g, w);
-    } else {  // Y^T = (scale 2^c Q S)^T + U^T P^T
+    } else if (MODE == kResults) {  // Y^T = (scale 2^c Q S)^T + U^T P^T
       const Split<T, kTwo<T>> us[2] = {split_pair<T, kTwo<T>>(w[0], w[1]), split_pair<T, kTwo<T>>(w[2], w[3])};
       const Rsrc ry = rows_rsrc(yp + t * a.y.row_stride, a.y.row_stride, min(end - t, kTok), a.width);
 #pragma unroll
@@ -240,7 +288,7 @@ __device__ __forceinline__ void walk_forward(const DeltaArgs& a, FwdLds<T, NB, K
       for (int i = 0; i < kTiles; ++i) st.st[n + i] = st.st[n + i] * total + add[i];
     }
   }
-  if (!KEEP && a.final_state != nullptr) st.save(a.final_state + of_seq, a.width, a.states);
+  last_state<MODE>(st, a, cl, u);
 }
 
 template <class T, int NB>
@@ -255,26 +303,42 @@ struct RevLds {
   static constexpr int ldv = stride_of<T>(kCols);
 };
 
+// The gradient of the state that a segment ends with, and what its walk leaves.
+template <bool SUMMARY, int NB>
+__device__ __forceinline__ void first_gradient(State<NB, true>& st, const DeltaArgs& a, const WalkWork& w, const Unit& u) {
+  const long head = static_cast<long>(a.states) * a.width;
+  if (SUMMARY) st.zero();
+  else if (!last_unit(a, u)) st.load(a.seg_grad + (static_cast<long>(w.unit) * a.heads + w.h) * head, a.width, a.states);
+  else st.load(a.d_final == nullptr ? nullptr : a.d_final + (static_cast<long>(u.seq) * a.heads + w.h) * head, a.width, a.states);
+}
+template <bool SUMMARY, int NB>
+__device__ __forceinline__ void last_gradient(const State<NB, true>& st, const DeltaArgs& a, const WalkWork& w, const Unit& u) {
+  const long head = static_cast<long>(a.states) * a.width;
+  if (SUMMARY)  // the place of the segment before
+    st.save(a.seg_grad + (static_cast<long>(w.unit - 1) * a.heads + w.h) * head, a.width, a.states);
+  else if (a.d_initial != nullptr && u.index == 0)
+    st.save(a.d_initial + (static_cast<long>(u.seq) * a.heads + w.h) * head, a.width, a.states);
+}
+
 // The walk of the state's gradient D, from the last step to the first:
 //   dU = P^T dY + 2^(c_end - c) K D,   dR = M^T dU,   dV = beta dR
 //   D  = 2^c_end D + scale Q^T (2^c dY) - K^T (beta 2^c dR)
-// It leaves every step's D (of the state the step ends with) and dR.
-template <class T, int NB>
+// It leaves every step's D (of the state the step ends with) and dR; SUMMARY: only
+// the segment's own contribution to the gradient before it.
+template <class T, int NB, bool SUMMARY>
 __device__ __forceinline__ void walk_reverse(const DeltaArgs& a, RevLds<T, NB>& s) {
   typedef RevLds<T, NB> L;
   constexpr int kThreads = kWaves * 64;
   constexpr int kM = kExact<T> * kPieces * kPiece;
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
-  const int work = xcd_contiguous(blockIdx.x, gridDim.x);
-  const int per = a.heads * a.slices;
-  const int unit = work / per, h = work % per / a.slices, slice = work % a.slices;
-  const Unit u = locate(a.seqs, unit, a.seg);
-  if (!u.live) return;
+  const WalkWork wk = walk_work(a, a.slices);
+  const Unit u = locate(a.seqs, wk.unit, a.seg);
+  if (!u.live || (SUMMARY && u.index == 0)) return;
+  const int h = wk.h, slice = wk.slice;
   const bool packed = a.seqs.offsets != nullptr;
   const int p0 = slice * kThreads / 4;
   const int col = p0 + wave * 16 + l15;
   const long head = static_cast<long>(a.states) * a.width;
-  const long of_seq = (static_cast<long>(u.seq) * a.heads + h) * head;
   const T* kp = seq_ptr<const T>(a.k, u.seq, u.row0, packed) + h / a.ratio * a.states;
   const T* qp = seq_ptr<const T>(a.q, u.seq, u.row0, packed) + h / a.ratio * a.states;
   const T* yp = seq_ptr<const T>(a.d_y, u.seq, u.row0, packed) + h * a.width + p0;
@@ -282,9 +346,9 @@ __device__ __forceinline__ void walk_reverse(const DeltaArgs& a, RevLds<T, NB>& 
 
   State<NB, true> st;
   st.init(a.width, p0, wave);
-  st.load(a.d_final == nullptr ? nullptr : a.d_final + of_seq, a.width, a.states);
+  first_gradient<SUMMARY>(st, a, wk, u);
 
-  const int end = u.len;
+  const int end = min(u.t0 + a.seg, u.len);
   const long cell0 = static_cast<long>(unit_base(a.seqs, u.seq, kTok)) * a.heads + h;  // of the sequence's first step
   Tile<T, kTok, NB * 32, kThreads> tk, tq;
   tk.init(a.k.row_stride, a.states, tid);
@@ -319,7 +383,7 @@ __device__ __forceinline__ void walk_reverse(const DeltaArgs& a, RevLds<T, NB>& 
     if (t > u.t0) fetch(t - kTok);
 
     const long cell = cell0 + static_cast<long>(t / kTok) * a.heads;
-    st.save(a.d_keep + cell * head, a.width, a.states);
+    if (!SUMMARY) st.save(a.d_keep + cell * head, a.width, a.states);
     // dU
     constexpr int kBuf = NB > 1 ? 2 : 1;
     Frag<T> kf[kBuf][4];
@@ -388,13 +452,14 @@ __device__ __forceinline__ void walk_reverse(const DeltaArgs& a, RevLds<T, NB>& 
     };
     read_cols(0);
     keep_reads_here();
-    save_rows(a.d_r + cell * (kTok * static_cast<long>(a.width)), a.width, col, g, dr);
+    if (!SUMMARY) save_rows(a.d_r + cell * (kTok * static_cast<long>(a.width)), a.width, col, g, dr);
     const Rsrc rv = rows_rsrc(vp + t * a.d_v.row_stride, a.d_v.row_stride, min(end - t, kTok), a.width);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       dr[i] = dr[i] * beta[i];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) store_elem<T>(rv, v_off + (16 * i + r) * v_row, dr[i][r]);
+      for (int r = 0; r < 4; ++r)
+        if (!SUMMARY) store_elem<T>(rv, v_off + (16 * i + r) * v_row, dr[i][r]);
       dr[i] = -from[i] * dr[i];
       dy[i] = a.scale * (from[i] * dy[i]);
     }
@@ -421,7 +486,7 @@ __device__ __forceinline__ void walk_reverse(const DeltaArgs& a, RevLds<T, NB>& 
       for (int i = 0; i < kTiles; ++i) st.st[n + i] = st.st[n + i] * total + add[i];
     }
   }
-  if (a.d_initial != nullptr) st.save(a.d_initial + of_seq, a.width, a.states);
+  last_gradient<SUMMARY>(st, a, wk, u);
 }
 
 }  // namespace delta
