@@ -24,10 +24,9 @@ __global__ __launch_bounds__(kPrepWaves * 64) void delta_prep_kernel(DeltaArgs a
   const int step = work / a.heads, h = work % a.heads;
   const Unit u = locate(a.seqs, step, kTok);
   if (!u.live || u.t0 >= u.len) return;
-  make_step<T, NB>(s, a, u, h, a.seqs.offsets != nullptr);
   const long at = static_cast<long>(step) * a.heads + h;
-  put_pieces<T, kExact<T>, false>(static_cast<T*>(a.m) + at * kExact<T> * kPieces * kPiece, s.m, wave, lane);
-  put_pieces<T, kTwo<T>, false>(static_cast<T*>(a.p) + at * kTwo<T> * kPieces * kPiece, s.sq.p, wave, lane);
+  make_step<T, NB, false>(s, a, u, h, a.seqs.offsets != nullptr, static_cast<T*>(a.p) + at * kTwo<T> * kPieces * kPiece);
+  put_pieces<T, kExact<T>, false>(static_cast<T*>(a.m) + at * kExact<T> * kPieces * kPiece, s.sq.m, wave, lane);
   if (threadIdx.x < sizeof(Coef) / 16)
     reinterpret_cast<v4f*>(a.coef + at)[threadIdx.x] = reinterpret_cast<const v4f*>(&s.coef)[threadIdx.x];
 }

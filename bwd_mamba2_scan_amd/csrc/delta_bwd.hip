@@ -34,12 +34,11 @@ __global__ __launch_bounds__(kPrepWaves * 64) void delta_bwd_prep_kernel(DeltaAr
   const int step = work / a.heads, h = work % a.heads;
   const Unit u = locate(a.seqs, step, kTok);
   if (!u.live || u.t0 >= u.len) return;
-  make_step<T, NB>(s, a, u, h, a.seqs.offsets != nullptr);
   const long at = static_cast<long>(step) * a.heads + h;
   constexpr int kM = kExact<T> * kPieces * kPiece;
-  put_pieces<T, kExact<T>, false>(static_cast<T*>(a.m) + at * kM, s.m, wave, lane);
-  put_pieces<T, kExact<T>, true>(static_cast<T*>(a.mt) + at * kM, s.m, wave, lane);
-  put_pieces<T, kExact<T>, true>(static_cast<T*>(a.pt) + at * kM, s.sq.p, wave, lane);
+  make_step<T, NB, true>(s, a, u, h, a.seqs.offsets != nullptr, static_cast<T*>(a.pt) + at * kM);
+  put_pieces<T, kExact<T>, false>(static_cast<T*>(a.m) + at * kM, s.sq.m, wave, lane);
+  put_pieces<T, kExact<T>, true>(static_cast<T*>(a.mt) + at * kM, s.sq.m, wave, lane);
   if (threadIdx.x < sizeof(Coef) / 16)
     reinterpret_cast<v4f*>(a.coef + at)[threadIdx.x] = reinterpret_cast<const v4f*>(&s.coef)[threadIdx.x];
 }

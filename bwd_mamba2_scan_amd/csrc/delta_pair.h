@@ -88,6 +88,7 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
   const int wave = wave_id(), lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
   const int strip = wave & (kWaves - 1);
   const Columns cl = columns_of<MODE>(a);
+  if (cl.unit < 0) return;
   const Unit u = locate(a.seqs, cl.unit, a.seg);
   if (!u.live || !wanted<MODE>(a, cl, u)) return;
   const int h = cl.h, p0 = cl.p0;
@@ -313,6 +314,7 @@ __device__ __forceinline__ void pair_reverse(const DeltaArgs& a, PairRevLds<NB>&
   const int wave = wave_id(), lane = threadIdx.x & 63, g = lane >> 4;
   const int strip = wave & (kWaves - 1);
   const WalkWork wk = walk_work(a, a.slices);
+  if (wk.unit < 0) return;
   const Unit u = locate(a.seqs, wk.unit, a.seg);
   if (!u.live || (SUMMARY && u.index == 0)) return;
   const int h = wk.h, slice = wk.slice;

@@ -19,10 +19,9 @@ struct PrepLds {
     } in;
     struct {
       float t[kTok * kSq];
-      float p[kTok * kSq];
+      float m[kTok * kSq];
     } sq;
   };
-  alignas(16) float m[kTok * kSq];
   alignas(16) Coef coef;
   float hi[kTok], lo[kTok];  // c_t in two floats
 };
@@ -115,12 +114,18 @@ __device__ __forceinline__ void put_pieces(T* out, const float* m, int wave, int
   }
 }
 
-// One step of one head: leaves T in s.sq.t, P (without scale where SCALE is
-// false) in s.sq.p, M in s.m and the gates in s.coef, for all waves.
-template <class T, int NB>
-__device__ __forceinline__ void make_step(PrepLds<T, NB>& s, const DeltaArgs& a, const Unit& u, int h, bool packed) {
+// One step of one head: leaves M in s.sq.m and the gates in s.coef, for all waves,
+// and writes P's pieces (BWD: those of its transpose).
+//
+// A product's result that has a matrix's row in a lane and 4 g .. of its columns is
+// a piece of that matrix as it lies in the registers: so K Q^T gives P's pieces and
+// Q K^T those of P^T, without a way through LDS.
+template <class T, int NB, bool BWD>
+__device__ __forceinline__ void make_step(PrepLds<T, NB>& s, const DeltaArgs& a, const Unit& u, int h, bool packed,
+                                          T* pieces) {
   typedef PrepLds<T, NB> L;
   constexpr int kThreads = kPrepWaves * 64;
+  constexpr int kParts = BWD ? kExact<T> : kTwo<T>;
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
   const int rows = min(u.len - u.t0, kTok);
   const int j = h / a.ratio * a.states;
@@ -147,42 +152,59 @@ __device__ __forceinline__ void make_step(PrepLds<T, NB>& s, const DeltaArgs& a,
   tk.store(s.in.k, L::ldn, tid);
   tq.store(s.in.q, L::ldn, tid);
   __syncthreads();
-  // a wave's sixteen rows of both products, up to the diagonal
-  v4f kk[4], qk[4];
-  Frag<T> kf[NB], qf[NB];
+  // a wave's sixteen rows of K K^T up to the diagonal, transposed: row l15, columns 4 g ..
+  v4f kk[4], pq[4];
+  Frag<T> kf[NB], of[NB];  // of: this wave's rows of Q; BWD: of K, for P's columns
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
     kf[n] = frag_row(s.in.k, L::ldn, wave * 16, n * 32);
-    qf[n] = frag_row(s.in.q, L::ldn, wave * 16, n * 32);
+    of[n] = BWD ? kf[n] : frag_row(s.in.q, L::ldn, wave * 16, n * 32);
   }
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    kk[c] = qk[c] = v4f{0, 0, 0, 0};
-    if (c <= wave) {
+    kk[c] = pq[c] = v4f{0, 0, 0, 0};
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
+    for (int n = 0; n < NB; ++n) {
+      if (c <= wave) {
         const Frag<T> b = frag_row(s.in.k, L::ldn, c * 16, n * 32);
-        mma(kk[c], kf[n], b);
-        mma(qk[c], qf[n], b);
+        mma(kk[c], b, kf[n]);
+        if (!BWD) mma(pq[c], b, of[n]);
       }
+      if (BWD && c >= wave) mma(pq[c], frag_row(s.in.q, L::ldn, c * 16, n * 32), of[n]);
     }
   }
-  __syncthreads();  // k and q give way to T and P
-  const v4f hi = rows_of(s.hi, wave, g), lo = rows_of(s.lo, wave, g), beta = rows_of(s.coef.beta, wave, g);
+  __syncthreads();  // k and q give way to T and M
+  const int mine = wave * 16 + l15;
+  const float ch = s.hi[mine], cl = s.lo[mine], beta = s.coef.beta[mine];
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const int col = c * 16 + l15;
-    const float ch = s.hi[col], cl = s.lo[col];
+    const v4f hi = rows_of(s.hi, c, g), lo = rows_of(s.lo, c, g);
+    v4f t;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int row = wave * 16 + 4 * g + r;
-      const float e = exp2_of((hi[r] - ch) + (lo[r] - cl));
-      s.sq.t[row * kSq + col] = col < row ? beta[r] * (e * kk[c][r]) : 0.0f;
-      s.sq.p[row * kSq + col] = col <= row ? a.scale * (e * qk[c][r]) : 0.0f;
+      const int other = c * 16 + 4 * g + r;
+      const float d = (ch - hi[r]) + (cl - lo[r]);  // c_mine - c_other
+      const float e = exp2_of(BWD && c > wave ? -d : d);
+      t[r] = other < mine ? beta * (e * kk[c][r]) : 0.0f;
+      if (BWD) {
+        const float w = c == wave ? exp2_of(-d) : e;
+        pq[c][r] = other >= mine ? a.scale * (w * pq[c][r]) : 0.0f;
+      } else {
+        pq[c][r] = other <= mine ? a.scale * (e * pq[c][r]) : 0.0f;
+      }
     }
+    if (c <= wave) *reinterpret_cast<v4f*>(&s.sq.t[mine * kSq + c * 16 + 4 * g]) = t;
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (BWD ? k < wave / 2 : k > wave / 2) continue;
+    const Split<T, kParts> f = split_pair<T, kParts>(pq[2 * k], pq[2 * k + 1]);
+    const int n = BWD ? piece_of_t(wave, k) : piece_of(wave, k);
+#pragma unroll
+    for (int z = 0; z < kParts; ++z) piece_put(pieces + (z * kPieces + n) * kPiece, lane, f.f[z]);
   }
   __syncthreads();
-  invert(s.m, s.sq.t, wave, lane);
+  invert(s.sq.m, s.sq.t, wave, lane);
 }
 
 }  // namespace delta

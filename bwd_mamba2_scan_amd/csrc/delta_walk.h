@@ -126,6 +126,7 @@ __device__ __forceinline__ void walk_forward(const DeltaArgs& a, FwdLds<T, NB, M
   constexpr int kM = kExact<T> * kPieces * kPiece, kP = kTwo<T> * kPieces * kPiece;
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
   const Columns cl = columns_of<MODE>(a);
+  if (cl.unit < 0) return;
   const Unit u = locate(a.seqs, cl.unit, a.seg);
   if (!u.live || !wanted<MODE>(a, cl, u)) return;
   const int h = cl.h, p0 = cl.p0;
@@ -332,6 +333,7 @@ __device__ __forceinline__ void walk_reverse(const DeltaArgs& a, RevLds<T, NB>& 
   constexpr int kM = kExact<T> * kPieces * kPiece;
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
   const WalkWork wk = walk_work(a, a.slices);
+  if (wk.unit < 0) return;
   const Unit u = locate(a.seqs, wk.unit, a.seg);
   if (!u.live || (SUMMARY && u.index == 0)) return;
   const int h = wk.h, slice = wk.slice;
