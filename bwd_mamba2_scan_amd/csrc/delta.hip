@@ -26,7 +26,7 @@ __global__ __launch_bounds__(kPrepWaves * 64) void delta_prep_kernel(DeltaArgs a
   if (!u.live || u.t0 >= u.len) return;
   const long at = static_cast<long>(step) * a.heads + h;
   make_step<T, NB, false>(s, a, u, h, a.seqs.offsets != nullptr, static_cast<T*>(a.p) + at * kTwo<T> * kPieces * kPiece);
-  put_pieces<T, kExact<T>, false>(static_cast<T*>(a.m) + at * kExact<T> * kPieces * kPiece, s.sq.m, wave, lane);
+  put_pieces<false>(a.m + at * kPieces * kPiece, s.sq.m, wave, lane);
   if (threadIdx.x < sizeof(Coef) / 16)
     reinterpret_cast<v4f*>(a.coef + at)[threadIdx.x] = reinterpret_cast<const v4f*>(&s.coef)[threadIdx.x];
 }
@@ -229,7 +229,7 @@ int launch_fwd_states(const DeltaArgs& a, unsigned steps, int type, hipStream_t 
 }
 
 long steps_of(const mamba2_seqs& q) { return unit_count(q, kTok); }
-size_t m_bytes(int type) { return (type == MAMBA2_BF16 ? 3 * 2 : 4) * kPieces * kPiece; }
+constexpr size_t kMBytes = kPieces * kPiece * sizeof(float);
 size_t p_bytes(int type) { return (type == MAMBA2_BF16 ? 2 * 2 : 4) * kPieces * kPiece; }
 
 }  // namespace
@@ -346,7 +346,7 @@ extern "C" {
 
 size_t mamba2_delta_fwd_workspace_bytes(mamba2_seqs seqs, mamba2_delta_dims d) {
   if (check_delta(seqs, d) != MAMBA2_SCAN_OK) return 0;
-  return static_cast<size_t>(steps_of(seqs)) * d.heads * (m_bytes(d.type) + p_bytes(d.type) + sizeof(Coef)) +
+  return static_cast<size_t>(steps_of(seqs)) * d.heads * (kMBytes + p_bytes(d.type) + sizeof(Coef)) +
          segment_bytes(seqs, d, false);
 }
 
@@ -376,9 +376,9 @@ int mamba2_delta_fwd(mamba2_seqs seqs, mamba2_delta_dims d, mamba2_rows q, mamba
   set_dims(&a, seqs, d, false);
   const long cells = steps_of(seqs) * d.heads;
   char* at = static_cast<char*>(workspace);
-  a.m = at;
-  a.p = at + cells * m_bytes(d.type);
-  a.coef = reinterpret_cast<Coef*>(at + cells * (m_bytes(d.type) + p_bytes(d.type)));
+  a.m = reinterpret_cast<float*>(at);
+  a.p = at + cells * kMBytes;
+  a.coef = reinterpret_cast<Coef*>(at + cells * (kMBytes + p_bytes(d.type)));
   const unsigned steps = seqs.length == 0 ? 0 : static_cast<unsigned>(cells);
   set_segments(&a, reinterpret_cast<char*>(a.coef + cells), false);
   hipStream_t s = static_cast<hipStream_t>(stream);

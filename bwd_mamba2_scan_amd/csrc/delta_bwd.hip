@@ -35,10 +35,10 @@ __global__ __launch_bounds__(kPrepWaves * 64) void delta_bwd_prep_kernel(DeltaAr
   const Unit u = locate(a.seqs, step, kTok);
   if (!u.live || u.t0 >= u.len) return;
   const long at = static_cast<long>(step) * a.heads + h;
-  constexpr int kM = kExact<T> * kPieces * kPiece;
-  make_step<T, NB, true>(s, a, u, h, a.seqs.offsets != nullptr, static_cast<T*>(a.pt) + at * kM);
-  put_pieces<T, kExact<T>, false>(static_cast<T*>(a.m) + at * kM, s.sq.m, wave, lane);
-  put_pieces<T, kExact<T>, true>(static_cast<T*>(a.mt) + at * kM, s.sq.m, wave, lane);
+  constexpr int kM = kPieces * kPiece;
+  make_step<T, NB, true>(s, a, u, h, a.seqs.offsets != nullptr, a.pt + at * kM);
+  put_pieces<false>(a.m + at * kM, s.sq.m, wave, lane);
+  put_pieces<true>(a.mt + at * kM, s.sq.m, wave, lane);
   if (threadIdx.x < sizeof(Coef) / 16)
     reinterpret_cast<v4f*>(a.coef + at)[threadIdx.x] = reinterpret_cast<const v4f*>(&s.coef)[threadIdx.x];
 }
@@ -600,7 +600,7 @@ struct BwdCell {
 };
 BwdCell bwd_cell(const mamba2_delta_dims& d) {
   BwdCell c;
-  c.m = (d.type == MAMBA2_BF16 ? 3 * 2 : 4) * kPieces * kPiece;
+  c.m = kPieces * kPiece * sizeof(float);
   c.state = static_cast<size_t>(d.states) * d.width * 4;
   c.rows = static_cast<size_t>(kTok) * d.width * 4;
   c.all = 3 * c.m + 2 * c.state + 2 * c.rows + sizeof(Coef);
@@ -661,9 +661,9 @@ int mamba2_delta_bwd(mamba2_seqs seqs, mamba2_delta_dims d, mamba2_rows q, mamba
     at += cells * bytes;
     return p;
   };
-  a.m = take(c.m);
-  a.mt = take(c.m);
-  a.pt = take(c.m);
+  a.m = reinterpret_cast<float*>(take(c.m));
+  a.mt = reinterpret_cast<float*>(take(c.m));
+  a.pt = reinterpret_cast<float*>(take(c.m));
   a.keep = reinterpret_cast<float*>(take(c.state));
   a.d_keep = reinterpret_cast<float*>(take(c.state));
   a.u = reinterpret_cast<float*>(take(c.rows));

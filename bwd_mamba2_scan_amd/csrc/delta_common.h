@@ -56,15 +56,15 @@ struct DeltaArgs {
   float* seg_state;        // [units][heads][states][width]: the state a segment starts from
   float* seg_trans;        // [units][heads][states][states]: what a segment makes of it
   float* seg_grad;         // [units][heads][states][width]: the gradient of the state a segment ends with
-  void* m;                 // [steps][heads][kExact][kPieces][kPiece]: M
+  float* m;                // [steps][heads][kPieces][kPiece]: M
   void* p;                 // [steps][heads][kTwo][kPieces][kPiece]: P
   Coef* coef;              // [steps][heads]
   // the backward's
   mamba2_rows d_y, d_q, d_k, d_v, d_g, d_beta;
   const float* d_final;
   float* d_initial;
-  void* mt;                // as m: the transpose of M
-  void* pt;                // as m: the transpose of P
+  float* mt;               // as m: the transpose of M
+  float* pt;               // as m: the transpose of P
   float* keep;             // [steps][heads][states][width]: the state each step starts from
   float* d_keep;           // the same: the gradient of the state each step ends with
   float* u;                // [steps][heads][kTok][width]: U

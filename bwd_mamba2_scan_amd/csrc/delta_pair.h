@@ -44,6 +44,21 @@ __device__ __forceinline__ void swap_save(float* out, int rows, int width, int c
                                            off + n * 64 * width, 0, 0);
 }
 
+// A matrix's fp32 pieces on their way to LDS, where they lie in three bf16 parts that
+// add up to them.  In memory they would be half as long again.
+struct Pieces {
+  static constexpr int kN = kPieces * kPiece / 4 / kHelpers;
+  v4f v[kN];
+  __device__ __forceinline__ void load(const float* p, long cell, int tid) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = reinterpret_cast<const v4f*>(p + cell * kPieces * kPiece)[tid + i * kHelpers];
+  }
+  __device__ __forceinline__ void store(bf16* lds, int tid) const {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) quad_put_parts<3>(lds + 4 * (tid + i * kHelpers), kPieces * kPiece, v[i]);
+  }
+};
+
 // What the walkers read of a step.
 template <int NB>
 struct PairStep {
@@ -84,7 +99,7 @@ struct PairFwdLds {
 template <int NB, Walked MODE>
 __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, MODE>& s) {
   typedef PairFwdLds<NB, MODE> L;
-  constexpr int kM = 3 * kPieces * kPiece, kP = 2 * kPieces * kPiece;
+  constexpr int kP = 2 * kPieces * kPiece;
   const int wave = wave_id(), lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
   const int strip = wave & (kWaves - 1);
   const Columns cl = columns_of<MODE>(a);
@@ -105,7 +120,7 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
     bf16* yp = seq_ptr<bf16>(a.y, u.seq, u.row0, packed) + h * a.width;
     Tile<bf16, kTok, NB * 32, kHelpers> tk, tq;
     Tile<bf16, kTok, kCols, kHelpers> tv;
-    Flat<kM * sizeof(bf16), kHelpers> tm;
+    Pieces tm;
     Flat<sizeof(Coef), kHelpers> tc;
     Frag<bf16> pf[2][kPieces];
     const int cols = cl.cols;
@@ -119,7 +134,7 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
       const int rows = min(end - t, kTok);
       const long at = cell0 + static_cast<long>(t / kTok) * a.heads;
       tk.load(rows_rsrc(kp + t * a.k.row_stride, a.k.row_stride, rows, a.states));
-      tm.load(static_cast<const bf16*>(a.m) + at * kM, tid);
+      tm.load(a.m, at, tid);
       tc.load(a.coef + at, tid);
       tv.load(rows_rsrc(vp + t * a.v.row_stride, a.v.row_stride, rows, cols));
       if (MODE == kResults) tq.load(rows_rsrc(qp + t * a.q.row_stride, a.q.row_stride, rows, a.states));
@@ -309,7 +324,6 @@ struct PairRevLds {
 template <int NB, bool SUMMARY>
 __device__ __forceinline__ void pair_reverse(const DeltaArgs& a, PairRevLds<NB>& s) {
   typedef PairRevLds<NB> L;
-  constexpr int kM = 3 * kPieces * kPiece;
   constexpr int kTiles = 2 * NB < 4 ? 2 * NB : 4;
   const int wave = wave_id(), lane = threadIdx.x & 63, g = lane >> 4;
   const int strip = wave & (kWaves - 1);
@@ -334,7 +348,7 @@ __device__ __forceinline__ void pair_reverse(const DeltaArgs& a, PairRevLds<NB>&
     bf16* vp = seq_ptr<bf16>(a.d_v, u.seq, u.row0, packed) + h * a.width;
     Tile<bf16, kTok, NB * 32, kHelpers> tk, tq;
     Tile<bf16, kTok, kCols, kHelpers> ty;
-    Flat<kM * sizeof(bf16), kHelpers> tm, tp;
+    Pieces tm, tp;
     Flat<sizeof(Coef), kHelpers> tc;
     const int cols = min(a.width - p0, kCols);
     tk.init(a.k.row_stride, a.states, tid);
@@ -350,8 +364,8 @@ __device__ __forceinline__ void pair_reverse(const DeltaArgs& a, PairRevLds<NB>&
       tk.load(rows_rsrc(kp + t * a.k.row_stride, a.k.row_stride, rows, a.states));
       tq.load(rows_rsrc(qp + t * a.q.row_stride, a.q.row_stride, rows, a.states));
       ty.load(rows_rsrc(yp + t * a.d_y.row_stride, a.d_y.row_stride, rows, cols));
-      tm.load(static_cast<const bf16*>(a.mt) + at * kM, tid);
-      tp.load(static_cast<const bf16*>(a.pt) + at * kM, tid);
+      tm.load(a.mt, at, tid);
+      tp.load(a.pt, at, tid);
       tc.load(a.coef + at, tid);
     };
     const auto put = [&] {

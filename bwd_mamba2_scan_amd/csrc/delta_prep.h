@@ -88,10 +88,10 @@ __device__ __forceinline__ void invert(float* m, const float* t, int wave, int l
   __syncthreads();
 }
 
-// Writes the pieces of a 64 x 64 matrix (transposed: of its transpose) in PARTS
-// parts, a wave's share of them.
-template <class T, int PARTS, bool TRANSPOSED>
-__device__ __forceinline__ void put_pieces(T* out, const float* m, int wave, int lane) {
+// Writes the pieces of a 64 x 64 matrix (transposed: of its transpose) in fp32, a
+// wave's share of them.
+template <bool TRANSPOSED>
+__device__ __forceinline__ void put_pieces(float* out, const float* m, int wave, int lane) {
   const int l15 = lane & 15, g = lane >> 4;
   for (int n = wave; n < kPieces; n += kPrepWaves) {
     int i, s;  // the piece's tile row and k-step
@@ -102,17 +102,25 @@ __device__ __forceinline__ void put_pieces(T* out, const float* m, int wave, int
       i = n < 2 ? n : (n + 2) >> 1;
       s = n < 2 ? 0 : n & 1;
     }
-    float v[8];
+    Frag<float> f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int row = 16 * i + l15, k = 32 * s + (j >> 2) * 16 + 4 * g + (j & 3);
-      v[j] = TRANSPOSED ? m[k * kSq + row] : m[row * kSq + k];
+      f.v[j >> 2][j & 3] = TRANSPOSED ? m[k * kSq + row] : m[row * kSq + k];
     }
-    const Split<T, PARTS> f = split_of<T, PARTS>(v);
-#pragma unroll
-    for (int z = 0; z < PARTS; ++z) piece_put(out + (z * kPieces + n) * kPiece, lane, f.f[z]);
+    piece_put(out + n * kPiece, lane, f);
   }
 }
+
+// P's pieces: two parts of T, as the forward multiplies them; the backward's in fp32.
+template <class T, bool BWD>
+struct PiecesOf {
+  typedef T type;
+};
+template <class T>
+struct PiecesOf<T, true> {
+  typedef float type;
+};
 
 // One step of one head: leaves M in s.sq.m and the gates in s.coef, for all waves,
 // and writes P's pieces (BWD: those of its transpose).
@@ -122,10 +130,11 @@ __device__ __forceinline__ void put_pieces(T* out, const float* m, int wave, int
 // Q K^T those of P^T, without a way through LDS.
 template <class T, int NB, bool BWD>
 __device__ __forceinline__ void make_step(PrepLds<T, NB>& s, const DeltaArgs& a, const Unit& u, int h, bool packed,
-                                          T* pieces) {
+                                          typename PiecesOf<T, BWD>::type* pieces) {
   typedef PrepLds<T, NB> L;
+  typedef typename PiecesOf<T, BWD>::type P;
   constexpr int kThreads = kPrepWaves * 64;
-  constexpr int kParts = BWD ? kExact<T> : kTwo<T>;
+  constexpr int kParts = kTwo<P>;
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
   const int rows = min(u.len - u.t0, kTok);
   const int j = h / a.ratio * a.states;
@@ -198,7 +207,7 @@ __device__ __forceinline__ void make_step(PrepLds<T, NB>& s, const DeltaArgs& a,
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     if (BWD ? k < wave / 2 : k > wave / 2) continue;
-    const Split<T, kParts> f = split_pair<T, kParts>(pq[2 * k], pq[2 * k + 1]);
+    const Split<P, kParts> f = split_pair<P, kParts>(pq[2 * k], pq[2 * k + 1]);
     const int n = BWD ? piece_of_t(wave, k) : piece_of(wave, k);
 #pragma unroll
     for (int z = 0; z < kParts; ++z) piece_put(pieces + (z * kPieces + n) * kPiece, lane, f.f[z]);

@@ -159,7 +159,7 @@ __device__ __forceinline__ void walk_forward(const DeltaArgs& a, FwdLds<T, NB, M
     const long at = cell0 + static_cast<long>(t / kTok) * a.heads;
     tk.load(rows_rsrc(kp + t * a.k.row_stride, a.k.row_stride, rows, a.states));
     if (MODE == kResults) tq.load(rows_rsrc(qp + t * a.q.row_stride, a.q.row_stride, rows, a.states));
-    tm.load(static_cast<const T*>(a.m) + at * kM, tid);
+    tm.load(a.m + at * kPieces * kPiece, tid);
     if (MODE == kResults) tp.load(static_cast<const T*>(a.p) + at * kP, tid);
     tc.load(a.coef + at, tid);
     tv.load(rows_rsrc(vp + t * a.v.row_stride, a.v.row_stride, rows, cl.cols));
@@ -366,8 +366,8 @@ __device__ __forceinline__ void walk_reverse(const DeltaArgs& a, RevLds<T, NB>& 
     const long at = cell0 + static_cast<long>(t / kTok) * a.heads;
     tk.load(rows_rsrc(kp + t * a.k.row_stride, a.k.row_stride, rows, a.states));
     tq.load(rows_rsrc(qp + t * a.q.row_stride, a.q.row_stride, rows, a.states));
-    tm.load(static_cast<const T*>(a.mt) + at * kM, tid);
-    tp.load(static_cast<const T*>(a.pt) + at * kM, tid);
+    tm.load(a.mt + at * kPieces * kPiece, tid);
+    tp.load(a.pt + at * kPieces * kPiece, tid);
     tc.load(a.coef + at, tid);
     ty.load(rows_rsrc(yp + t * a.d_y.row_stride, a.d_y.row_stride, rows, min(a.width - p0, kCols)));
   };
