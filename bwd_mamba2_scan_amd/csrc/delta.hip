@@ -1,8 +1,8 @@
 // Gated delta rule for gfx950: the forward over prompts and the single-token
 // form.  The mathematics of a step is in delta_common.h.
 //
-// delta_prep_kernel: one work-group per step and head writes the step's M and P
-// as operands.  delta_fwd_kernel: a wave owns 16 columns of a head's state, S
+// delta_prep_kernel: one work-group per step and group of heads writes the step's M
+// and P as operands.  delta_fwd_kernel: a wave owns 16 columns of a head's state, S
 // [states][16], in registers in fp32 as a matrix result, and walks the tokens
 // in steps of 64; every product's result is the next one's right operand
 // without leaving its lane, so waves meet only where they share the loads of a
@@ -20,15 +20,12 @@ template <class T, int NB>
 __global__ __launch_bounds__(kPrepWaves * 64) void delta_prep_kernel(DeltaArgs a) {
   __shared__ PrepLds<T, NB> s;
   const int wave = wave_id(), lane = threadIdx.x & 63;
-  const int work = xcd_contiguous(blockIdx.x, gridDim.x);
-  const int step = work / a.heads, h = work % a.heads;
-  const Unit u = locate(a.seqs, step, kTok);
+  const PrepWork w = prep_work(a);
+  const Unit u = locate(a.seqs, w.step, kTok);
   if (!u.live || u.t0 >= u.len) return;
-  const long at = static_cast<long>(step) * a.heads + h;
-  make_step<T, NB, false>(s, a, u, h, a.seqs.offsets != nullptr, static_cast<T*>(a.p) + at * kTwo<T> * kPieces * kPiece);
-  put_pieces<false>(a.m + at * kPieces * kPiece, s.sq.m, wave, lane);
-  if (threadIdx.x < sizeof(Coef) / 16)
-    reinterpret_cast<v4f*>(a.coef + at)[threadIdx.x] = reinterpret_cast<const v4f*>(&s.coef)[threadIdx.x];
+  make_steps<T, NB, false>(s, a, u, w.step, w.first, w.heads, static_cast<T*>(a.p), [&](long cell) {
+    put_pieces<false>(a.m + cell * kPieces * kPiece, s.sq.m, wave, lane);
+  });
 }
 
 template <class T, int NB>
@@ -213,7 +210,7 @@ int launch_summary_states(const DeltaArgs& a, hipStream_t s) {
 template <class T, int NB>
 int launch_fwd(const DeltaArgs& a, unsigned steps, int type, hipStream_t s) {
   if (steps > 0) {
-    delta_prep_kernel<T, NB><<<steps, kPrepWaves * 64, 0, s>>>(a);
+    delta_prep_kernel<T, NB><<<prep_blocks(a, steps), kPrepWaves * 64, 0, s>>>(a);
     if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
     const int st = start_segments(a, type, s);
     if (st != MAMBA2_SCAN_OK) return st;
@@ -336,6 +333,10 @@ void set_dims(DeltaArgs* a, const mamba2_seqs& q, const mamba2_delta_dims& d, bo
   a->states = d.states;
   a->slices = (d.width + kWaves * 16 - 1) / (kWaves * 16);
   a->gate_bf16 = d.gate_type == MAMBA2_BF16;
+  // the matrices: heads that share a q and k one after the other, once the chip (three
+  // work-groups on a CU) is full
+  const long full = steps_of(q) * d.heads / (3 * kCUs);
+  a->prep_heads = full < 1 ? 1 : full < a->ratio ? static_cast<int>(full) : a->ratio;
   a->seg = segment_tokens(q, d, bwd);
   a->units = static_cast<int>(unit_count(q, a->seg));
 }

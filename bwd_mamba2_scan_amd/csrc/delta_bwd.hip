@@ -30,17 +30,13 @@ template <class T, int NB>
 __global__ __launch_bounds__(kPrepWaves * 64) void delta_bwd_prep_kernel(DeltaArgs a) {
   __shared__ PrepLds<T, NB> s;
   const int wave = wave_id(), lane = threadIdx.x & 63;
-  const int work = xcd_contiguous(blockIdx.x, gridDim.x);
-  const int step = work / a.heads, h = work % a.heads;
-  const Unit u = locate(a.seqs, step, kTok);
+  const PrepWork w = prep_work(a);
+  const Unit u = locate(a.seqs, w.step, kTok);
   if (!u.live || u.t0 >= u.len) return;
-  const long at = static_cast<long>(step) * a.heads + h;
-  constexpr int kM = kPieces * kPiece;
-  make_step<T, NB, true>(s, a, u, h, a.seqs.offsets != nullptr, a.pt + at * kM);
-  put_pieces<false>(a.m + at * kM, s.sq.m, wave, lane);
-  put_pieces<true>(a.mt + at * kM, s.sq.m, wave, lane);
-  if (threadIdx.x < sizeof(Coef) / 16)
-    reinterpret_cast<v4f*>(a.coef + at)[threadIdx.x] = reinterpret_cast<const v4f*>(&s.coef)[threadIdx.x];
+  make_steps<T, NB, true>(s, a, u, w.step, w.first, w.heads, a.pt, [&](long cell) {
+    put_pieces<false>(a.m + cell * kPieces * kPiece, s.sq.m, wave, lane);
+    put_pieces<true>(a.mt + cell * kPieces * kPiece, s.sq.m, wave, lane);
+  });
 }
 
 template <class T, int NB>
@@ -570,7 +566,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
 template <class T, int NB>
 int launch_bwd(const DeltaArgs& a, unsigned steps, int type, hipStream_t s) {
   if (steps > 0) {
-    delta_bwd_prep_kernel<T, NB><<<steps, kPrepWaves * 64, 0, s>>>(a);
+    delta_bwd_prep_kernel<T, NB><<<prep_blocks(a, steps), kPrepWaves * 64, 0, s>>>(a);
     if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
     int st = start_segments(a, type, s);
     if (st != MAMBA2_SCAN_OK) return st;

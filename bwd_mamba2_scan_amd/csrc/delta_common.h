@@ -50,6 +50,7 @@ struct DeltaArgs {
   float scale;
   int heads, width, ratio, states;
   int slices;              // work-groups per head: slices of its width
+  int prep_heads;          // heads of a group that one work-group makes the matrices of
   int gate_bf16;
   int seg;                 // tokens per segment (a multiple of kTok)
   int units;               // segments of the call

@@ -22,8 +22,7 @@ struct PrepLds {
       float m[kTok * kSq];
     } sq;
   };
-  alignas(16) Coef coef;
-  float hi[kTok], lo[kTok];  // c_t in two floats
+  alignas(16) float hi[kTok], lo[kTok], beta[kTok];  // c_t in two floats
 };
 
 // acc += A B over 16: A row-major at a, B in the order of a result: register r
@@ -122,98 +121,133 @@ struct PiecesOf<T, true> {
   typedef float type;
 };
 
-// One step of one head: leaves M in s.sq.m and the gates in s.coef, for all waves,
-// and writes P's pieces (BWD: those of its transpose).
+// Work-groups per step: each has up to prep_heads heads of one group.
+__host__ __device__ inline int prep_parts(const DeltaArgs& a) { return (a.ratio + a.prep_heads - 1) / a.prep_heads; }
+inline unsigned prep_blocks(const DeltaArgs& a, unsigned cells) {
+  return cells / a.heads * (a.heads / a.ratio) * prep_parts(a);
+}
+struct PrepWork {
+  int step, first, heads;
+};
+__device__ __forceinline__ PrepWork prep_work(const DeltaArgs& a) {
+  const int work = xcd_contiguous(blockIdx.x, gridDim.x), parts = prep_parts(a);
+  const int per = a.heads / a.ratio * parts, step = work / per, at = work % per;
+  const int part = at % parts, skip = part * a.prep_heads;
+  return {step, at / parts * a.ratio + skip, min(a.prep_heads, a.ratio - skip)};
+}
+
+// One step of `heads` heads of a group, one after the other, the products of their
+// shared q and k formed once: writes P's pieces (BWD: those of its transpose) and
+// the gates, and calls done(cell) with M in s.sq.m.
 //
 // A product's result that has a matrix's row in a lane and 4 g .. of its columns is
 // a piece of that matrix as it lies in the registers: so K Q^T gives P's pieces and
 // Q K^T those of P^T, without a way through LDS.
-template <class T, int NB, bool BWD>
-__device__ __forceinline__ void make_step(PrepLds<T, NB>& s, const DeltaArgs& a, const Unit& u, int h, bool packed,
-                                          typename PiecesOf<T, BWD>::type* pieces) {
+template <class T, int NB, bool BWD, class Done>
+__device__ __forceinline__ void make_steps(PrepLds<T, NB>& s, const DeltaArgs& a, const Unit& u, int step, int first, int heads,
+                                           typename PiecesOf<T, BWD>::type* pieces, Done done) {
   typedef PrepLds<T, NB> L;
   typedef typename PiecesOf<T, BWD>::type P;
   constexpr int kThreads = kPrepWaves * 64;
   constexpr int kParts = kTwo<P>;
+  const bool packed = a.seqs.offsets != nullptr;
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
   const int rows = min(u.len - u.t0, kTok);
-  const int j = h / a.ratio * a.states;
-  Tile<T, kTok, NB * 32, kThreads> tk, tq;
-  tk.init(a.k.row_stride, a.states, tid);
-  tq.init(a.q.row_stride, a.states, tid);
-  tk.load(rows_rsrc(seq_ptr<const T>(a.k, u.seq, u.row0, packed) + u.t0 * a.k.row_stride + j, a.k.row_stride, rows,
-                    a.states));
-  tq.load(rows_rsrc(seq_ptr<const T>(a.q, u.seq, u.row0, packed) + u.t0 * a.q.row_stride + j, a.q.row_stride, rows,
-                    a.states));
-  if (wave == kPrepWaves - 1) {
-    const double c = scan64(gate_log(load_gate(a.g, a.gate_bf16, u, packed, u.t0, rows, h, a.heads)));
-    const long bits = __builtin_bit_cast(long, c);
-    const double end = __builtin_bit_cast(
-        double, (static_cast<long>(__builtin_amdgcn_readlane(static_cast<int>(bits >> 32), 63)) << 32) |
-                    static_cast<unsigned>(__builtin_amdgcn_readlane(static_cast<int>(bits), 63)));
-    s.hi[lane] = static_cast<float>(c);
-    s.lo[lane] = static_cast<float>(c - static_cast<float>(c));
-    s.coef.from[lane] = exp2_of(c);
-    s.coef.to[lane] = exp2_of(end - c);
-    s.coef.beta[lane] = load_gate(a.beta, a.gate_bf16, u, packed, u.t0, rows, h, a.heads);
-    if (lane == 0) s.coef.total = exp2_of(end);
-  }
-  tk.store(s.in.k, L::ldn, tid);
-  tq.store(s.in.q, L::ldn, tid);
-  __syncthreads();
+  const int j = first / a.ratio * a.states;
+  float g_raw = 0.0f, beta_raw = 0.0f;
+  const auto fetch_gates = [&](int h) {
+    if (wave != kPrepWaves - 1) return;
+    g_raw = load_gate(a.g, a.gate_bf16, u, packed, u.t0, rows, h, a.heads);
+    beta_raw = load_gate(a.beta, a.gate_bf16, u, packed, u.t0, rows, h, a.heads);
+  };
+  fetch_gates(first);
   // a wave's sixteen rows of K K^T up to the diagonal, transposed: row l15, columns 4 g ..
-  v4f kk[4], pq[4];
-  Frag<T> kf[NB], of[NB];  // of: this wave's rows of Q; BWD: of K, for P's columns
-#pragma unroll
-  for (int n = 0; n < NB; ++n) {
-    kf[n] = frag_row(s.in.k, L::ldn, wave * 16, n * 32);
-    of[n] = BWD ? kf[n] : frag_row(s.in.q, L::ldn, wave * 16, n * 32);
-  }
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    kk[c] = pq[c] = v4f{0, 0, 0, 0};
+  v4f kk[4], qk[4];
+  {
+    Tile<T, kTok, NB * 32, kThreads> tk, tq;
+    tk.init(a.k.row_stride, a.states, tid);
+    tq.init(a.q.row_stride, a.states, tid);
+    tk.load(rows_rsrc(seq_ptr<const T>(a.k, u.seq, u.row0, packed) + u.t0 * a.k.row_stride + j, a.k.row_stride, rows,
+                      a.states));
+    tq.load(rows_rsrc(seq_ptr<const T>(a.q, u.seq, u.row0, packed) + u.t0 * a.q.row_stride + j, a.q.row_stride, rows,
+                      a.states));
+    tk.store(s.in.k, L::ldn, tid);
+    tq.store(s.in.q, L::ldn, tid);
+    __syncthreads();
+    Frag<T> kf[NB], of[NB];  // of: this wave's rows of Q; BWD: of K, for P's columns
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-      if (c <= wave) {
-        const Frag<T> b = frag_row(s.in.k, L::ldn, c * 16, n * 32);
-        mma(kk[c], b, kf[n]);
-        if (!BWD) mma(pq[c], b, of[n]);
+      kf[n] = frag_row(s.in.k, L::ldn, wave * 16, n * 32);
+      of[n] = BWD ? kf[n] : frag_row(s.in.q, L::ldn, wave * 16, n * 32);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      kk[c] = qk[c] = v4f{0, 0, 0, 0};
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        if (c <= wave) {
+          const Frag<T> b = frag_row(s.in.k, L::ldn, c * 16, n * 32);
+          mma(kk[c], b, kf[n]);
+          if (!BWD) mma(qk[c], b, of[n]);
+        }
+        if (BWD && c >= wave) mma(qk[c], frag_row(s.in.q, L::ldn, c * 16, n * 32), of[n]);
       }
-      if (BWD && c >= wave) mma(pq[c], frag_row(s.in.q, L::ldn, c * 16, n * 32), of[n]);
     }
   }
-  __syncthreads();  // k and q give way to T and M
   const int mine = wave * 16 + l15;
-  const float ch = s.hi[mine], cl = s.lo[mine], beta = s.coef.beta[mine];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const v4f hi = rows_of(s.hi, c, g), lo = rows_of(s.lo, c, g);
-    v4f t;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int other = c * 16 + 4 * g + r;
-      const float d = (ch - hi[r]) + (cl - lo[r]);  // c_mine - c_other
-      const float e = exp2_of(BWD && c > wave ? -d : d);
-      t[r] = other < mine ? beta * (e * kk[c][r]) : 0.0f;
-      if (BWD) {
-        const float w = c == wave ? exp2_of(-d) : e;
-        pq[c][r] = other >= mine ? a.scale * (w * pq[c][r]) : 0.0f;
-      } else {
-        pq[c][r] = other <= mine ? a.scale * (e * pq[c][r]) : 0.0f;
-      }
+  for (int h = first; h < first + heads; ++h) {
+    const long cell = static_cast<long>(step) * a.heads + h;
+    __syncthreads();  // k and q, or the last head's matrices, give way to T and M
+    if (wave == kPrepWaves - 1) {
+      const double c = scan64(gate_log(g_raw));
+      const long bits = __builtin_bit_cast(long, c);
+      const double end = __builtin_bit_cast(
+          double, (static_cast<long>(__builtin_amdgcn_readlane(static_cast<int>(bits >> 32), 63)) << 32) |
+                      static_cast<unsigned>(__builtin_amdgcn_readlane(static_cast<int>(bits), 63)));
+      s.hi[lane] = static_cast<float>(c);
+      s.lo[lane] = static_cast<float>(c - static_cast<float>(c));
+      s.beta[lane] = beta_raw;
+      Coef& coef = a.coef[cell];
+      coef.from[lane] = exp2_of(c);
+      coef.to[lane] = exp2_of(end - c);
+      coef.beta[lane] = beta_raw;
+      if (lane == 0) coef.total = exp2_of(end);
+      fetch_gates(h + 1 < first + heads ? h + 1 : h);
     }
-    if (c <= wave) *reinterpret_cast<v4f*>(&s.sq.t[mine * kSq + c * 16 + 4 * g]) = t;
-  }
+    __syncthreads();
+    const float ch = s.hi[mine], cl = s.lo[mine], beta = s.beta[mine];
+    v4f pq[4];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (BWD ? k < wave / 2 : k > wave / 2) continue;
-    const Split<P, kParts> f = split_pair<P, kParts>(pq[2 * k], pq[2 * k + 1]);
-    const int n = BWD ? piece_of_t(wave, k) : piece_of(wave, k);
+    for (int c = 0; c < 4; ++c) {
+      const v4f hi = rows_of(s.hi, c, g), lo = rows_of(s.lo, c, g);
+      v4f t;
 #pragma unroll
-    for (int z = 0; z < kParts; ++z) piece_put(pieces + (z * kPieces + n) * kPiece, lane, f.f[z]);
+      for (int r = 0; r < 4; ++r) {
+        const int other = c * 16 + 4 * g + r;
+        const float d = (ch - hi[r]) + (cl - lo[r]);  // c_mine - c_other
+        const float e = exp2_of(BWD && c > wave ? -d : d);
+        t[r] = other < mine ? beta * (e * kk[c][r]) : 0.0f;
+        if (BWD) {
+          const float w = c == wave ? exp2_of(-d) : e;
+          pq[c][r] = other >= mine ? a.scale * (w * qk[c][r]) : 0.0f;
+        } else {
+          pq[c][r] = other <= mine ? a.scale * (e * qk[c][r]) : 0.0f;
+        }
+      }
+      if (c <= wave) *reinterpret_cast<v4f*>(&s.sq.t[mine * kSq + c * 16 + 4 * g]) = t;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (BWD ? k < wave / 2 : k > wave / 2) continue;
+      const Split<P, kParts> f = split_pair<P, kParts>(pq[2 * k], pq[2 * k + 1]);
+      const int n = BWD ? piece_of_t(wave, k) : piece_of(wave, k);
+#pragma unroll
+      for (int z = 0; z < kParts; ++z) piece_put(pieces + ((cell * kParts + z) * kPieces + n) * kPiece, lane, f.f[z]);
+    }
+    __syncthreads();
+    invert(s.sq.m, s.sq.t, wave, lane);
+    done(cell);
   }
-  __syncthreads();
-  invert(s.sq.m, s.sq.t, wave, lane);
 }
 
 }  // namespace delta
