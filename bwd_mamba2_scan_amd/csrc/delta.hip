@@ -17,7 +17,7 @@ namespace {
 using namespace delta;
 
 template <class T, int NB>
-__global__ __launch_bounds__(kPrepWaves * 64) void delta_prep_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(kPrepWaves * 64, NB < 4 || sizeof(T) == 2 ? 4 : 2) void delta_prep_kernel(DeltaArgs a) {
   __shared__ PrepLds<T, NB> s;
   const int wave = wave_id(), lane = threadIdx.x & 63;
   const PrepWork w = prep_work(a);
