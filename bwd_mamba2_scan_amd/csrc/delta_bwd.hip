@@ -163,6 +163,13 @@ struct Eight {
   }
 };
 
+// A group's heads are split over several work-groups where there are few steps;
+// their parts of the shared gradients then meet in delta_sum_kernel.  3 x 333
+// tokens, 10 heads of 24 x 40 in 2 groups, fp32: 54 us with all five heads of a
+// group in one work-group, 16 and 6 us with one each.
+__host__ __device__ inline int grad_parts(const DeltaArgs& a) { return (a.ratio + a.grad_heads - 1) / a.grad_heads; }
+__host__ __device__ inline long grad_part_at(const DeltaArgs& a, long i) { return i * 2 * kTok * a.states; }
+
 template <class T, int NB>
 __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs a) {
   typedef GradLds<T, NB> L;
@@ -171,8 +178,9 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
   constexpr int kN = kGradStates<NB>, kI = kGradTokens<NB>;
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
   const int work = xcd_contiguous(blockIdx.x, gridDim.x);
-  const int groups = a.heads / a.ratio;
-  const int step = work / groups, group = work % groups;
+  const int groups = a.heads / a.ratio, parts = grad_parts(a);
+  const int step = work / (groups * parts), at = work % (groups * parts), group = at / parts, part = at % parts;
+  const int first = group * a.ratio + part * a.grad_heads, behind_h = min(first + a.grad_heads, (group + 1) * a.ratio);
   const Unit u = locate(a.seqs, step, kTok);
   if (!u.live || u.t0 >= u.len) return;
   const bool packed = a.seqs.offsets != nullptr;
@@ -245,8 +253,8 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
     const int j = group * a.states;
     tk.load(rows_rsrc(seq_ptr<const T>(a.k, u.seq, u.row0, packed) + u.t0 * a.k.row_stride + j, a.k.row_stride, rows, a.states));
     tq.load(rows_rsrc(seq_ptr<const T>(a.q, u.seq, u.row0, packed) + u.t0 * a.q.row_stride + j, a.q.row_stride, rows, a.states));
-    fetch_gates(group * a.ratio);
-    fetch(group * a.ratio, 0);
+    fetch_gates(first);
+    fetch(first, 0);
     tk.store(s.k, L::ldn, tid);
     tq.store(s.q, L::ldn, tid);
   }
@@ -257,8 +265,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
   for (int n = 0; n < kN; ++n)
 #pragma unroll
     for (int i = 0; i < kI; ++i) dq[n][i] = dk[n][i] = v4f{0, 0, 0, 0};
-  for (int hh = 0; hh < a.ratio; ++hh) {
-    const int h = group * a.ratio + hh;
+  for (int h = first; h < behind_h; ++h) {
     const int tid = thread_here(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
     __syncthreads();  // the last head's matrices are read
     if (wave == kW - 1) {
@@ -396,7 +403,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
     if (!second && (tid & 3) == 0) s.rv[tid >> 2] = rv;
     __syncthreads();  // the columns give way to the matrices
     // the next head's; behind the last one, its own again
-    const int next = hh + 1 < a.ratio ? h + 1 : h;
+    const int next = h + 1 < behind_h ? h + 1 : h;
     fetch_gates(next);
 
     sd = sum64(sd);
@@ -548,6 +555,21 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
       }
     }
   }
+  if (parts > 1) {  // added up by delta_sum_kernel
+    float* p = a.grad_part + grad_part_at(a, (static_cast<long>(step) * groups + group) * parts + part);
+    const unsigned bytes = static_cast<unsigned>(kTok * a.states * 4);
+    const Rsrc rq = make_rsrc(p, bytes), rk = make_rsrc(p + kTok * a.states, bytes);
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int i = 0; i < kI; ++i) {
+        const int row = 16 * (i0 + i) + l15, col = 16 * (s0 + n) + 4 * g;
+        const unsigned off = col < a.states ? static_cast<unsigned>((row * a.states + col) * 4) : kOutside;
+        Quad<float>::store(rq, off, dq[n][i]);
+        Quad<float>::store(rk, off, dk[n][i]);
+      }
+    return;
+  }
   const Rsrc rq = rows_rsrc(seq_ptr<const T>(a.d_q, u.seq, u.row0, packed) + u.t0 * a.d_q.row_stride + group * a.states,
                             a.d_q.row_stride, rows, a.states);
   const Rsrc rk = rows_rsrc(seq_ptr<const T>(a.d_k, u.seq, u.row0, packed) + u.t0 * a.d_k.row_stride + group * a.states,
@@ -560,6 +582,27 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
       Quad<T>::store(rq, col < a.states ? static_cast<unsigned>((row * static_cast<int>(a.d_q.row_stride) + col) * sizeof(T)) : kOutside, dq[n][i]);
       Quad<T>::store(rk, col < a.states ? static_cast<unsigned>((row * static_cast<int>(a.d_k.row_stride) + col) * sizeof(T)) : kOutside, dk[n][i]);
     }
+}
+
+// Adds up the parts of a step's and group's shared gradients, in order.
+template <class T>
+__global__ __launch_bounds__(256) void delta_sum_kernel(DeltaArgs a) {
+  const int groups = a.heads / a.ratio, parts = grad_parts(a);
+  const int step = blockIdx.x / groups, group = blockIdx.x % groups;
+  const Unit u = locate(a.seqs, step, kTok);
+  if (!u.live || u.t0 >= u.len) return;
+  const bool packed = a.seqs.offsets != nullptr;
+  const int rows = min(u.len - u.t0, kTok), quads = a.states / 4;
+  const float* p = a.grad_part + grad_part_at(a, static_cast<long>(blockIdx.x) * parts);
+  for (int e = threadIdx.x; e < 2 * rows * quads; e += 256) {
+    const int which = e >= rows * quads, i = e - which * rows * quads, row = i / quads, col = i % quads * 4;
+    const float* src = p + (which * kTok + row) * a.states + col;
+    v4f sum = *reinterpret_cast<const v4f*>(src);
+    for (int n = 1; n < parts; ++n) sum += *reinterpret_cast<const v4f*>(src + grad_part_at(a, n));
+    const mamba2_rows& out = which ? a.d_k : a.d_q;
+    T* dst = seq_ptr<T>(out, u.seq, u.row0, packed) + (u.t0 + row) * out.row_stride + group * a.states + col;
+    quad_put(dst, sum);
+  }
 }
 
 // ---------------------------------------------------------------- host side
@@ -580,7 +623,12 @@ int launch_bwd(const DeltaArgs& a, unsigned steps, int type, hipStream_t s) {
   }
   delta_reverse_kernel<T, NB, false><<<walk_blocks(a), walk_threads<T>, 0, s>>>(a);
   if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
-  if (steps > 0) delta_grads_kernel<T, NB><<<steps / a.ratio, kGradWaves * 64, 0, s>>>(a);
+  if (steps > 0) {
+    const unsigned shared = steps / a.ratio;
+    delta_grads_kernel<T, NB><<<shared * grad_parts(a), kGradWaves * 64, 0, s>>>(a);
+    if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
+    if (grad_parts(a) > 1) delta_sum_kernel<T><<<shared, 256, 0, s>>>(a);
+  }
   return launch_status();
 }
 template <class T>
@@ -588,6 +636,18 @@ int launch_bwd_states(const DeltaArgs& a, unsigned steps, int type, hipStream_t 
   if (a.states <= 32) return launch_bwd<T, 1>(a, steps, type, s);
   if (a.states <= 64) return launch_bwd<T, 2>(a, steps, type, s);
   return launch_bwd<T, 4>(a, steps, type, s);
+}
+
+// Heads of a group that one work-group takes: all of them, unless that leaves CUs
+// without one (there is one on a CU).
+int grad_heads(const mamba2_seqs& q, const mamba2_delta_dims& d) {
+  const long ratio = d.heads / d.groups, cells = static_cast<long>(unit_count(q, kTok)) * d.heads, each = cells / kCUs;
+  return static_cast<int>(each < 1 ? 1 : each < ratio ? each : ratio);
+}
+size_t grad_part_bytes(const mamba2_seqs& q, const mamba2_delta_dims& d) {
+  const int ratio = d.heads / d.groups, each = grad_heads(q, d), parts = (ratio + each - 1) / each;
+  if (parts == 1) return 0;
+  return static_cast<size_t>(unit_count(q, kTok)) * d.groups * parts * 2 * kTok * d.states * sizeof(float);
 }
 
 // The workspace's parts: bytes for each step of each head.
@@ -609,7 +669,8 @@ extern "C" {
 
 size_t mamba2_delta_bwd_workspace_bytes(mamba2_seqs seqs, mamba2_delta_dims d) {
   if (check_delta(seqs, d) != MAMBA2_SCAN_OK) return 0;
-  return static_cast<size_t>(unit_count(seqs, kTok)) * d.heads * bwd_cell(d).all + segment_bytes(seqs, d, true);
+  return static_cast<size_t>(unit_count(seqs, kTok)) * d.heads * bwd_cell(d).all + grad_part_bytes(seqs, d) +
+         segment_bytes(seqs, d, true);
 }
 
 int mamba2_delta_bwd(mamba2_seqs seqs, mamba2_delta_dims d, mamba2_rows q, mamba2_rows k, mamba2_rows v, mamba2_rows g,
@@ -666,7 +727,9 @@ int mamba2_delta_bwd(mamba2_seqs seqs, mamba2_delta_dims d, mamba2_rows q, mamba
   a.d_r = reinterpret_cast<float*>(take(c.rows));
   a.coef = reinterpret_cast<Coef*>(take(sizeof(Coef)));
   const unsigned steps = seqs.length == 0 ? 0 : static_cast<unsigned>(cells);
-  set_segments(&a, at, true);
+  a.grad_heads = grad_heads(seqs, d);
+  a.grad_part = reinterpret_cast<float*>(at);
+  set_segments(&a, at + grad_part_bytes(seqs, d), true);
   hipStream_t s = static_cast<hipStream_t>(stream);
   return d.type == MAMBA2_BF16 ? launch_bwd_states<bf16>(a, steps, d.type, s) : launch_bwd_states<float>(a, steps, d.type, s);
 }

@@ -70,6 +70,8 @@ struct DeltaArgs {
   float* d_keep;           // the same: the gradient of the state each step ends with
   float* u;                // [steps][heads][kTok][width]: U
   float* d_r;              // the same: the gradient of beta (V - 2^c K S)
+  int grad_heads;          // heads of a group that one work-group takes the gradients of
+  float* grad_part;        // [steps][groups][parts][2][kTok][states]: their parts of d_q and d_k
 };
 
 
@@ -111,7 +113,7 @@ __device__ __forceinline__ int longest_unit(const DeltaArgs& a, int r) {
 // Every XCD gets all sequences of some heads, whose unequal lengths would else
 // leave some XCDs with more, and the longest of them first: nine prompts of 1 to
 // 2048 tokens, 32 heads of 128 x 128: with neighbouring sequences on an XCD 257 us,
-// all of them 174 us, the longest first XXX us.
+// all of them 174 us, the longest first 132 us.
 __device__ __forceinline__ WalkWork walk_work(const DeltaArgs& a, int slices) {
   const int per = a.heads * slices;
   const bool sorted = a.seqs.offsets != nullptr && a.seqs.batch > 1 && a.seqs.batch <= 64 && a.seg >= a.seqs.length;
