@@ -52,10 +52,16 @@ __global__ __launch_bounds__(walk_threads<T>) void delta_summary_kernel(DeltaArg
 
 // Turns the segments' own contributions into the states they start from, one
 // segment of a sequence after the other: S = Phi S + own.  REVERSE: the gradients
-// they end with, by the transposed Phi, from the last.  A wave has 16 columns.
+// they end with, by the transposed Phi, from the last.  fp32 products throughout.
+//
+// A work-group has 16 columns, a wave 16 rows of them; the segments follow one
+// another, so a wave's rows of the next one's Phi are loaded while this one is
+// multiplied, and the waves meet once a segment, in LDS.  With a wave for all rows
+// of 16 columns, 128 states took 13 us a segment, with this 1.
 template <int NB, bool REVERSE>
-__global__ __launch_bounds__(kWaves * 64) void delta_carry_kernel(DeltaArgs a) {
-  const int lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
+__global__ __launch_bounds__(2 * NB * 64) void delta_carry_kernel(DeltaArgs a) {
+  __shared__ v4f state[2][2 * NB][64];
+  const int wave = wave_id(), lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
   const int h = blockIdx.y, seq = blockIdx.z;
   long row0;
   int len;
@@ -63,42 +69,54 @@ __global__ __launch_bounds__(kWaves * 64) void delta_carry_kernel(DeltaArgs a) {
   const int n = units_of(len, a.seg);
   if (n < 2) return;
   const long base = unit_base(a.seqs, seq, a.seg);
-  const long head = static_cast<long>(a.states) * a.width;
+  const long head = static_cast<long>(a.states) * a.width, square = static_cast<long>(a.states) * a.states;
   const float* first = REVERSE ? a.d_final : a.initial;
+  const float* phi = REVERSE ? a.seg_trans_t : a.seg_trans;
   float* places = REVERSE ? a.seg_grad : a.seg_state;
-  State<NB, true> st, own;
-  st.init(a.width, blockIdx.x * kCols, wave_id());
-  own.off = st.off;
-  st.load(first == nullptr ? nullptr : first + (static_cast<long>(seq) * a.heads + h) * head, a.width, a.states);
-  for (int i = 1; i < n; ++i) {
+  // this lane's part of the wave's tile: column l15, rows 4 g ..
+  const int col = blockIdx.x * 16 + l15, row = wave * 16 + 4 * g;
+  const unsigned off = col < a.width ? static_cast<unsigned>((row * a.width + col) * 4) : kOutside;
+  const unsigned bytes = static_cast<unsigned>(head * 4);
+  const auto load = [&](const float* p) {
+    const Rsrc rs = make_rsrc(p, bytes);
+    v4f v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = load_elem<float>(rs, off + i * 4 * a.width);
+    return v;
+  };
+  Frag<float> f[NB];
+  v4f own;
+  const auto fetch = [&](int i) {  // the place that segment step i fills, and the Phi it takes
     const long at = base + (REVERSE ? n - 1 - i : i), by = REVERSE ? at + 1 : at - 1;
-    own.load(places + (at * a.heads + h) * head, a.width, a.states);
-    const Rsrc rs = make_rsrc(a.seg_trans + (by * a.heads + h) * a.states * a.states,
-                              static_cast<unsigned>(a.states * a.states * 4));
+    own = load(places + (at * a.heads + h) * head);
+    const Rsrc rs = make_rsrc(phi + (by * a.heads + h) * square, static_cast<unsigned>(square * 4));
+    const int r = wave * 16 + l15;  // rows behind the states are outside
 #pragma unroll
-    for (int m = 0; m < 2 * NB; ++m) {
+    for (int k = 0; k < NB; ++k)
 #pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        // row (REVERSE: column) 16 m + l15 of Phi, in result order; outside it is zero
-        const int row = 16 * m + l15, c = 32 * k + 4 * g;
-        Frag<float> f;
-        if (REVERSE) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            f.v[j >> 2][j & 3] = load_elem<float>(
-                rs, row < a.states ? static_cast<unsigned>(((c + (j >> 2) * 16 + (j & 3)) * a.states + row) * 4) : kOutside);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            f.v[j] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(
-                rs, c + 16 * j < a.states ? static_cast<unsigned>((row * a.states + c + 16 * j) * 4) : kOutside, 0, 0));
-        }
-        mma(own.st[m], f, split_pair<float, 1>(st.st[2 * k], st.st[2 * k + 1]).f[0]);
+      for (int j = 0; j < 2; ++j) {
+        const int c = 32 * k + 16 * j + 4 * g;
+        f[k].v[j] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(
+            rs, c < a.states ? static_cast<unsigned>((r * a.states + c) * 4) : kOutside, 0, 0));
       }
-    }
+  };
+  fetch(1);
+  v4f mine = {0, 0, 0, 0};
+  if (first != nullptr) mine = load(first + (static_cast<long>(seq) * a.heads + h) * head);
+  for (int i = 1; i < n; ++i) {
+    v4f (&s)[2 * NB][64] = state[i & 1];
+    s[wave][lane] = mine;
+    __syncthreads();
+    mine = own;
+    Frag<float> now[NB];
 #pragma unroll
-    for (int m = 0; m < 2 * NB; ++m) st.st[m] = own.st[m];
-    st.save(places + (at * a.heads + h) * head, a.width, a.states);
+    for (int k = 0; k < NB; ++k) now[k] = f[k];
+    if (i + 1 < n) fetch(i + 1);
+#pragma unroll
+    for (int k = 0; k < NB; ++k) mma(mine, now[k], split_pair<float, 1>(s[2 * k][lane], s[2 * k + 1][lane]).f[0]);
+    const Rsrc rs = make_rsrc(places + ((base + (REVERSE ? n - 1 - i : i)) * a.heads + h) * head, bytes);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) store_elem<float>(rs, off + j * 4 * a.width, mine[j]);
   }
 }
 
@@ -197,7 +215,7 @@ int launch_summary(const DeltaArgs& a, hipStream_t s) {
   const int slices = a.slices + (a.states + kCols - 1) / kCols;
   delta_summary_kernel<T, NB><<<static_cast<unsigned>(a.units) * a.heads * slices, walk_threads<T>, 0, s>>>(a);
   if (launch_status() != MAMBA2_SCAN_OK) return MAMBA2_SCAN_EHIP;
-  delta_carry_kernel<NB, false><<<dim3(a.slices, a.heads, a.seqs.batch), kWaves * 64, 0, s>>>(a);
+  delta_carry_kernel<NB, false><<<dim3((a.width + 15) / 16, a.heads, a.seqs.batch), 2 * NB * 64, 0, s>>>(a);
   return launch_status();
 }
 template <class T>
@@ -267,8 +285,16 @@ int check_gates(mamba2_rows* r, const mamba2_seqs& q, const mamba2_delta_dims& d
 }
 // Tokens per segment.  A head's columns are walked by work-groups of which a CU
 // holds one; with fewer of them than CUs the tokens are cut into segments.  That
-// costs the summary, a walk of the state's columns beside the values', and the
-// carry, whose segments follow one another.  In units of a walk's step: XXX
+// costs the summary, a walk of the state's columns beside the values' that is 0.7
+// of one with results, and the carry, whose segments follow one another (0.3 of a
+// step each); two steps pass before a walk's first.  The fewest such steps are
+// taken, rounds of work-groups counted whole.  Forward, us a call, bf16, one sequence:
+//                                       whole   cut by the rule   best of the cuts tried
+//   32768 tokens, 24 heads of 64 x 64   1558    467 (10)          467 (10)
+//   8192 tokens, 8 heads of 128 x 128    466    139 (16)          139 (16)
+//   4096 tokens, 32 heads of 128 x 128   249    180 (4)           180 (4)
+//   1024 tokens, 8 heads of 128 x 128     71     56 (8)            56 (4 to 12)
+// and forward and backward, 4096 tokens, 8 heads of 128 x 128: 732, 343 (16), 324 (8).
 int segment_tokens(const mamba2_seqs& q, const mamba2_delta_dims& d, bool bwd) {
   const bool packed = q.offsets != nullptr;
   // how a packed call's rows are shared out is not known here
@@ -277,14 +303,16 @@ int segment_tokens(const mamba2_seqs& q, const mamba2_delta_dims& d, bool bwd) {
   const long slices = (d.width + kCols - 1) / kCols, more = (d.states + kCols - 1) / kCols;
   const long lanes = seqs * d.heads * slices, summary = seqs * d.heads * (slices + more);
   const auto rounds = [](long n) { return static_cast<float>((n + kCUs - 1) / kCUs); };
-  const float carry = (d.states > 64 ? 1.5f : 0.7f) * (bwd ? 2 : 1), fixed = bwd ? 8.0f : 4.0f;
   float best = 0.0f;
   long cut = 1;
   if (lanes < kCUs) {
     for (long n = 1; n <= 64 && n <= steps; ++n) {
-      const float s = static_cast<float>((steps + n - 1) / n);
-      float cost = rounds(lanes * n) * s * (bwd ? 2.2f : 1.0f);
-      if (n > 1) cost += rounds(summary * n) * s * 0.7f + (bwd ? rounds(lanes * n) * s : 0.0f) + n * carry + fixed;
+      const float walk = static_cast<float>((steps + n - 1) / n + 2);
+      float cost = rounds(lanes * n) * walk * (bwd ? 2.35f : 1.0f);
+      if (n > 1) {
+        cost += rounds(summary * n) * walk * 0.7f + 0.3f * n + 2.0f;
+        if (bwd) cost += rounds(lanes * n) * walk * 1.1f + 0.3f * n + 2.0f;
+      }
       if (n == 1 || cost < best) {
         best = cost;
         cut = n;
@@ -302,10 +330,10 @@ int start_segments(const DeltaArgs& a, int type, hipStream_t s) {
   return type == MAMBA2_BF16 ? launch_summary_states<bf16>(a, s) : launch_summary_states<float>(a, s);
 }
 int carry_gradients(const DeltaArgs& a, hipStream_t s) {
-  const dim3 grid(a.slices, a.heads, a.seqs.batch);
-  if (a.states <= 32) delta_carry_kernel<1, true><<<grid, kWaves * 64, 0, s>>>(a);
-  else if (a.states <= 64) delta_carry_kernel<2, true><<<grid, kWaves * 64, 0, s>>>(a);
-  else delta_carry_kernel<4, true><<<grid, kWaves * 64, 0, s>>>(a);
+  const dim3 grid((a.width + 15) / 16, a.heads, a.seqs.batch);
+  if (a.states <= 32) delta_carry_kernel<1, true><<<grid, 128, 0, s>>>(a);
+  else if (a.states <= 64) delta_carry_kernel<2, true><<<grid, 256, 0, s>>>(a);
+  else delta_carry_kernel<4, true><<<grid, 512, 0, s>>>(a);
   return launch_status();
 }
 unsigned walk_blocks(const DeltaArgs& a) { return static_cast<unsigned>(a.units) * a.heads * a.slices; }
@@ -313,7 +341,7 @@ unsigned walk_blocks(const DeltaArgs& a) { return static_cast<unsigned>(a.units)
 size_t segment_bytes(const mamba2_seqs& q, const mamba2_delta_dims& d, bool bwd) {
   const int seg = segment_tokens(q, d, bwd);
   if (q.length <= seg) return 0;
-  const size_t head = static_cast<size_t>(d.states) * ((bwd ? 2 : 1) * d.width + d.states);
+  const size_t head = (bwd ? 2 : 1) * static_cast<size_t>(d.states) * (d.width + d.states);
   return static_cast<size_t>(unit_count(q, seg)) * d.heads * head * sizeof(float);
 }
 void set_segments(DeltaArgs* a, char* at, bool bwd) {
@@ -321,7 +349,9 @@ void set_segments(DeltaArgs* a, char* at, bool bwd) {
   const long cells = static_cast<long>(a->units) * a->heads, head = static_cast<long>(a->states) * a->width;
   a->seg_state = reinterpret_cast<float*>(at);
   a->seg_trans = a->seg_state + cells * head;
-  if (bwd) a->seg_grad = a->seg_trans + cells * a->states * a->states;
+  if (!bwd) return;
+  a->seg_trans_t = a->seg_trans + cells * a->states * a->states;
+  a->seg_grad = a->seg_trans_t + cells * a->states * a->states;
 }
 
 void set_dims(DeltaArgs* a, const mamba2_seqs& q, const mamba2_delta_dims& d, bool bwd) {

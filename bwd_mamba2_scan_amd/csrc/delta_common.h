@@ -56,6 +56,7 @@ struct DeltaArgs {
   int units;               // segments of the call
   float* seg_state;        // [units][heads][states][width]: the state a segment starts from
   float* seg_trans;        // [units][heads][states][states]: what a segment makes of it
+  float* seg_trans_t;      // the same, transposed (the backward)
   float* seg_grad;         // [units][heads][states][width]: the gradient of the state a segment ends with
   float* m;                // [steps][heads][kPieces][kPiece]: M
   void* p;                 // [steps][heads][kTwo][kPieces][kPiece]: P

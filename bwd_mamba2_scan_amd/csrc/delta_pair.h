@@ -304,7 +304,7 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
       for (int i = 0; i < kTiles; ++i) st.st[n + i] = st.st[n + i] * total + add[i];
     }
   }
-  last_state<MODE>(st, a, cl, u);
+  last_state<MODE>(st, a, cl, u, strip);
 }
 
 template <int NB>

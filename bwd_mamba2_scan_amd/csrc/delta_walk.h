@@ -96,11 +96,20 @@ __device__ __forceinline__ void first_state(State<NB, true>& st, const DeltaArgs
   }
 }
 template <Walked MODE, int NB>
-__device__ __forceinline__ void last_state(const State<NB, true>& st, const DeltaArgs& a, const Columns& c, const Unit& u) {
+__device__ __forceinline__ void last_state(const State<NB, true>& st, const DeltaArgs& a, const Columns& c, const Unit& u, int strip) {
   const long at = static_cast<long>(c.unit) * a.heads + c.h;
   if (MODE == kSummary) {
-    if (c.trans) st.save(a.seg_trans + at * a.states * a.states, a.states, a.states);
-    else st.save(a.seg_state + (at + a.heads) * a.states * a.width, a.width, a.states);  // the next one's place
+    if (c.trans) {
+      const long square = static_cast<long>(a.states) * a.states;
+      st.save(a.seg_trans + at * square, a.states, a.states);
+      if (a.seg_trans_t != nullptr) {  // its transpose: this lane's column is a row, 4 g .. of each tile
+        const int lane = threadIdx.x & 63, row = c.p0 + strip * 16 + (lane & 15), col = 4 * (lane >> 4);
+        const Rsrc rs = make_rsrc(a.seg_trans_t + at * square, static_cast<unsigned>(square * 4));
+#pragma unroll
+        for (int n = 0; n < 2 * NB; ++n)
+          Quad<float>::store(rs, row < a.states && 16 * n + col < a.states ? static_cast<unsigned>((row * a.states + 16 * n + col) * 4) : kOutside, st.st[n]);
+      }
+    } else st.save(a.seg_state + (at + a.heads) * a.states * a.width, a.width, a.states);  // the next one's place
   } else if (MODE == kResults && a.final_state != nullptr && last_unit(a, u)) {
     st.save(a.final_state + (static_cast<long>(u.seq) * a.heads + c.h) * a.states * a.width, a.width, a.states);
   }
@@ -289,7 +298,7 @@ __device__ __forceinline__ void walk_forward(const DeltaArgs& a, FwdLds<T, NB, M
       for (int i = 0; i < kTiles; ++i) st.st[n + i] = st.st[n + i] * total + add[i];
     }
   }
-  last_state<MODE>(st, a, cl, u);
+  last_state<MODE>(st, a, cl, u, wave);
 }
 
 template <class T, int NB>
