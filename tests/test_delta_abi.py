@@ -86,8 +86,8 @@ def test_rule_workspaces(L):
         assert need > 0 and need % 16 == 0
         assert _rule(L, n=need - 1, bwd=bwd) == m2.ESIZE
         assert f(q, _dims(width=7)) == 0 and f(Seqs(0, 70, None), d) == 0
-        # one long sequence is cut into segments, whose states take room
-        assert f(Seqs(1, 65536, None), d) > 1024 * (need // 4)
+        # one long sequence is cut into segments, whose states take room; as many tokens in many sequences are not
+        assert f(Seqs(1, 65536, None), d) > f(Seqs(256, 256, None), d)
         # more tokens, or the same in more sequences, never need less
         sizes = [f(Seqs(1, n, P), d) for n in (0, 1, 64, 65)]
         assert sizes == sorted(sizes) and sizes[0] > 0
