@@ -66,18 +66,15 @@ template <class T>
 constexpr int kPart = sizeof(T) == 2 ? 128 : 64;  // columns of a head that LDS holds at a time
 
 // Eight waves share a step's 2 NB tiles of 16 states by four tiles of 16 tokens:
-// two by two of them a wave (NB = 2: one by two, NB = 1: one).
+// one by NB of them a wave.
 constexpr int kGradWaves = 8;
-template <int NB>
-constexpr int kGradStates = NB < 4 ? 1 : 2;
-template <int NB>
-constexpr int kGradTokens = NB < 2 ? 1 : 2;
 
 template <class T, int NB>
 struct GradLds {
   static constexpr int ldn = stride_of<T>(NB * 32);
   static constexpr int ldv = stride_of<T>(kPart<T>);
   static constexpr int ldm = stride_of<T>(kTok);
+  static constexpr int kAcross = 2 * NB;
   alignas(16) T k[kTok * ldn];
   alignas(16) T q[kTok * ldn];
   union {
@@ -90,12 +87,11 @@ struct GradLds {
       T pm[kTwo<T>][kTok * ldm];   // Pm
       T xm[kTwo<T>][kTok * ldm];   // Xm
       float z[kTok * kSq];         // Z
+      float qs[kAcross][kTok], ks[kAcross][kTok], kd[kAcross][kTok];  // some states' part of A_i's two terms, without their factors, and F_j's
     } sq;
   };
   alignas(16) Coef coef;
   float c_hi[kTok], c_lo[kTok];
-  static constexpr int kAcross = 2 * NB / kGradStates<NB>;
-  float qs[kAcross][kTok], ks[kAcross][kTok], kd[kAcross][kTok];  // some states' part of A_i's two terms, without their factors, and F_j's
   float rv[kTok];                                  // dR_i.V_i
   float bt[4][kTok];                               // a column tile's part of sum_j dT_ij E_ij k_i.k_j
   float sd[kAcross];                               // some states' part of <S, D>
@@ -111,9 +107,9 @@ __device__ __forceinline__ int thread_here() {
   return t;
 }
 
-// acc[n][i] += a[n] b[i] in parts, small products first, over all tiles in turn.
-template <class T, int N, int I, int B>
-__device__ __forceinline__ void mma_grid(v4f (&acc)[N][I], const Split<T, kExact<T>> (&a)[N], const Frag<T> (&b)[I][B]) {
+// acc[i + j] += a b[j] in parts, small products first, over all tiles in turn.
+template <class T, int I, int J, int B>
+__device__ __forceinline__ void mma_row(v4f (&acc)[I], int i, const Split<T, kExact<T>>& a, const Frag<T> (&b)[J][B]) {
   constexpr int kMost = kExact<T>;
 #pragma unroll
   for (int m = kMost - 1; m >= 0; --m)
@@ -121,9 +117,7 @@ __device__ __forceinline__ void mma_grid(v4f (&acc)[N][I], const Split<T, kExact
     for (int z = 0; z <= m; ++z)
       if (m - z < B) {
 #pragma unroll
-        for (int n = 0; n < N; ++n)
-#pragma unroll
-          for (int i = 0; i < I; ++i) mma(acc[n][i], a[n].f[z], b[i][m - z]);
+        for (int j = 0; j < J; ++j) mma(acc[i + j], a.f[z], b[j][m - z]);
       }
 }
 
@@ -161,7 +155,30 @@ struct Eight {
       for (int j = 0; j < 8; ++j) f[j] = __builtin_bit_cast(v4f, v[j >> 2])[j & 3];
     }
   }
+  __device__ __forceinline__ void put(T* p) const {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) reinterpret_cast<v4i*>(p)[i] = v[i];
+  }
 };
+
+// The sums of I values over the four lanes with the same l & 15: value
+// g / (4 / I) in the lanes of group g.  Where a lane has several values, they
+// share the swaps.
+template <int I>
+__device__ __forceinline__ float sums_of_groups(const float (&v)[I]) {
+  if constexpr (I == 1) {
+    return sum_groups(v[0]);
+  } else {
+    float half[I / 2];
+#pragma unroll
+    for (int i = 0; i < I / 2; ++i) {
+      const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[i + I / 2]), false, false);
+      half[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(half[0]), __float_as_uint(half[I / 2 - 1]), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+}
 
 // A group's heads are split over several work-groups where there are few steps;
 // their parts of the shared gradients then meet in delta_sum_kernel.  3 x 333
@@ -175,7 +192,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
   typedef GradLds<T, NB> L;
   __shared__ L s;
   constexpr int kW = kGradWaves, kThreads = kW * 64;
-  constexpr int kN = kGradStates<NB>, kI = kGradTokens<NB>;
+  constexpr int kI = NB, kJ = NB < 2 ? 1 : 2;      // a wave's tiles of tokens, and those of them at a time
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
   const int work = xcd_contiguous(blockIdx.x, gridDim.x);
   const int groups = a.heads / a.ratio, parts = grad_parts(a);
@@ -186,9 +203,9 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
   const bool packed = a.seqs.offsets != nullptr;
   const int rows = min(u.len - u.t0, kTok);
   const long head = static_cast<long>(a.states) * a.width, slab = kTok * static_cast<long>(a.width);
-  constexpr int kAcross = 2 * NB / kN;             // waves side by side over the states
-  const int s0 = wave % kAcross * kN;              // this wave's tiles of states
-  const int i0 = wave / kAcross * kI;              // and of tokens
+  constexpr int kAcross = 2 * NB;                  // waves side by side over the states
+  const int s0 = wave % kAcross;                   // this wave's tile of states
+  const int i0 = wave / kAcross * kI;              // and the first of tokens
 
   // A part of a head's columns on their way to LDS: a thread has eight columns of
   // every 32 of one row, of dR and V (the first 256 threads) or of U and dY.
@@ -219,25 +236,24 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
 #pragma unroll
     for (int i = 0; i < kEights; ++i) {
       const int at = at0 + 32 * i;
-      float f[8], t[8];
+      float f[8];
       flat[i].get(f);
-      token[i].get(t);
       put8<T, kExact<T>>((second ? s.in.u[0] : s.in.r[0]) + at, kTok * L::ldv, f);
       if (second) {
-        put8<T, 1>(s.in.y + at, 0, t);
+        token[i].put(s.in.y + at);
       } else {
+        float t[8];
+        token[i].get(t);
 #pragma unroll
         for (int j = 0; j < 8; ++j) rv = fmaf(f[j], t[j], rv);
       }
     }
   };
   // This lane's rows of a kept state, columns 8 g .. of 32; rows and columns outside are zero.
-  const auto load_state = [&](Eight<float> (&e)[kN], const float* kept, long cell, int c0) {
+  const auto load_state = [&](Eight<float>& e, const float* kept, long cell, int c0) {
     const Rsrc rs = make_rsrc(kept + cell * head, static_cast<unsigned>(head * 4));
     const int t = thread_here() & 63, c = c0 + 8 * (t >> 4);
-    const unsigned off = c < a.width ? static_cast<unsigned>(((16 * s0 + (t & 15)) * a.width + c) * 4) : kOutside;
-#pragma unroll
-    for (int n = 0; n < kN; ++n) e[n].load(rs, off + 64 * n * a.width);
+    e.load(rs, c < a.width ? static_cast<unsigned>(((16 * s0 + (t & 15)) * a.width + c) * 4) : kOutside);
   };
   float g_raw = 0.0f;
   v4f coef_raw = {0, 0, 0, 0};
@@ -258,13 +274,21 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
     tk.store(s.k, L::ldn, tid);
     tq.store(s.q, L::ldn, tid);
   }
-  constexpr int kMine = 2;  // a wave's share of the ten score tiles
+  // A wave's share of the ten score tiles (row ti, column tj <= ti): of the rows
+  // that it has products of.
+  constexpr int kMine = 2;
+  int mine[kMine], row_of[kMine], col_of[kMine];
+#pragma unroll
+  for (int n = 0; n < kMine; ++n) {
+    const int at = i0 * (i0 + 1) / 2 + s0 + n * kAcross;
+    mine[n] = at < (i0 + kI) * (i0 + kI + 1) / 2;
+    row_of[n] = at < 1 ? 0 : at < 3 ? 1 : at < 6 ? 2 : 3;
+    col_of[n] = at - row_of[n] * (row_of[n] + 1) / 2;
+  }
   // the gradients of q and k, transposed: token l15 of a tile, states 4 g .. of another
-  v4f dq[kN][kI], dk[kN][kI];
+  v4f dq[kI], dk[kI];
 #pragma unroll
-  for (int n = 0; n < kN; ++n)
-#pragma unroll
-    for (int i = 0; i < kI; ++i) dq[n][i] = dk[n][i] = v4f{0, 0, 0, 0};
+  for (int i = 0; i < kI; ++i) dq[i] = dk[i] = v4f{0, 0, 0, 0};
   for (int h = first; h < behind_h; ++h) {
     const int tid = thread_here(), lane = tid & 63, l15 = lane & 15, g = lane >> 4;
     __syncthreads();  // the last head's matrices are read
@@ -288,113 +312,92 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
         fetch(h, c0);
       }
       const int behind = min(a.width - c0, kPart<T>);
-      // S, then D: all of a part's columns are on their way before they are needed
-      Eight<float> raw[kEights][kN];
+      // all of a part's columns of S and D are on their way before they are needed
+      Eight<float> state[kEights], grad[kEights];
 #pragma unroll
-      for (int e = 0; e < kEights; ++e) load_state(raw[e], a.keep, cell, c0 + 32 * e);
+      for (int e = 0; e < kEights; ++e) load_state(state[e], a.keep, cell, c0 + 32 * e);
+#pragma unroll
+      for (int e = 0; e < kEights; ++e) load_state(grad[e], a.d_keep, cell, c0 + 32 * e);
       put();
       __syncthreads();
-      Eight<float> other[kN];
       {  // products over the columns with S, transposed: S dY^T, S dR^T; and the score tiles
-        v4f ys[kN][kI], rs[kN][kI];
+        v4f ys[kI], rs[kI];
 #pragma unroll
-        for (int n = 0; n < kN; ++n)
-#pragma unroll
-          for (int i = 0; i < kI; ++i) ys[n][i] = rs[n][i] = v4f{0, 0, 0, 0};
+        for (int i = 0; i < kI; ++i) ys[i] = rs[i] = v4f{0, 0, 0, 0};
 #pragma unroll
         for (int e = 0; e < kEights; ++e) {
           const int c = 32 * e;
           if (c >= behind) break;
-          Frag<T> yf[kI][1], rf[kI][kExact<T>];
+          float f[8];
+          state[e].get(f);
+          const Split<T, kExact<T>> part = split_of<T, kExact<T>>(f);
 #pragma unroll
-          for (int i = 0; i < kI; ++i) {
-            yf[i][0] = frag_row(s.in.y, L::ldv, 16 * (i0 + i), c, lane);
+          for (int i = 0; i < kI; i += kJ) {
+            Frag<T> yf[kJ][1], rf[kJ][kExact<T>];
 #pragma unroll
-            for (int z = 0; z < kExact<T>; ++z) rf[i][z] = frag_row(s.in.r[z], L::ldv, 16 * (i0 + i), c, lane);
-          }
-          keep_reads_here();
-          Split<T, kExact<T>> part[kN];
+            for (int j = 0; j < kJ; ++j) {
+              yf[j][0] = frag_row(s.in.y, L::ldv, 16 * (i0 + i + j), c, lane);
 #pragma unroll
-          for (int n = 0; n < kN; ++n) {
-            float f[8];
-            raw[e][n].get(f);
-            part[n] = split_of<T, kExact<T>>(f);
-          }
-          load_state(raw[e], a.d_keep, cell, c0 + c);
-          mma_grid<T>(ys, part, yf);
-          mma_grid<T>(rs, part, rf);
-#pragma unroll
-          for (int n = 0; n < kMine; ++n) {
-            const int tile = wave + n * kW;
-            if (tile < 10) {
-              const int ti = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, tj = tile - ti * (ti + 1) / 2;
-              Frag<T> uf[kExact<T>];
-              yf[0][0] = frag_row(s.in.y, L::ldv, 16 * ti, c, lane);
-#pragma unroll
-              for (int z = 0; z < kExact<T>; ++z) {
-                rf[0][z] = frag_row(s.in.r[z], L::ldv, 16 * ti, c, lane);
-                uf[z] = frag_row(s.in.u[z], L::ldv, 16 * tj, c, lane);
-              }
-              mma_parts<T>(dp[n], uf, yf[0]);
-              mma_parts<T>(dt[n], uf, rf[0]);
+              for (int z = 0; z < kExact<T>; ++z) rf[j][z] = frag_row(s.in.r[z], L::ldv, 16 * (i0 + i + j), c, lane);
             }
+            keep_reads_here();
+            mma_row<T>(ys, i, part, yf);
+            mma_row<T>(rs, i, part, rf);
+#pragma unroll
+            for (int n = 0; n < kMine; ++n)
+#pragma unroll
+              for (int j = 0; j < kJ; ++j)
+                if (mine[n] && row_of[n] == i0 + i + j) {
+                  Frag<T> uf[kExact<T>];
+#pragma unroll
+                  for (int z = 0; z < kExact<T>; ++z) uf[z] = frag_row(s.in.u[z], L::ldv, 16 * col_of[n], c, lane);
+                  mma_parts<T>(dp[n], uf, yf[j]);
+                  mma_parts<T>(dt[n], uf, rf[j]);
+                }
           }
         }
-        load_state(other, a.keep, cell, c0);  // a second time, from the cache, for <S, D>
 #pragma unroll
         for (int i = 0; i < kI; ++i) {
-          const int t = 16 * (i0 + i) + l15;
+          const int t = 16 * (i0 + i) + l15, at = t * L::ldn + 16 * s0 + 4 * g;
           const float from = s.coef.from[t], beta = s.coef.beta[t];
-#pragma unroll
-          for (int n = 0; n < kN; ++n) {
-            const int at = t * L::ldn + 16 * (s0 + n) + 4 * g;
-            const v4f pq = quad_get(s.q + at) * ys[n][i], pk = quad_get(s.k + at) * rs[n][i];
-            sq[i] += (pq[0] + pq[1]) + (pq[2] + pq[3]);
-            sk[i] += (pk[0] + pk[1]) + (pk[2] + pk[3]);
-            dq[n][i] += (a.scale * from) * ys[n][i];
-            dk[n][i] -= (beta * from) * rs[n][i];
-          }
+          const v4f pq = quad_get(s.q + at) * ys[i], pk = quad_get(s.k + at) * rs[i];
+          sq[i] += (pq[0] + pq[1]) + (pq[2] + pq[3]);
+          sk[i] += (pk[0] + pk[1]) + (pk[2] + pk[3]);
+          dq[i] += (a.scale * from) * ys[i];
+          dk[i] -= (beta * from) * rs[i];
         }
       }
       {  // with D: D U^T
-        v4f ud[kN][kI];
+        v4f ud[kI];
 #pragma unroll
-        for (int n = 0; n < kN; ++n)
-#pragma unroll
-          for (int i = 0; i < kI; ++i) ud[n][i] = v4f{0, 0, 0, 0};
+        for (int i = 0; i < kI; ++i) ud[i] = v4f{0, 0, 0, 0};
 #pragma unroll
         for (int e = 0; e < kEights; ++e) {
           const int c = 32 * e;
           if (c >= behind) break;
-          Frag<T> uf[kI][kExact<T>];
+          float d[8], f[8];
+          grad[e].get(d);
+          state[e].get(f);
 #pragma unroll
-          for (int i = 0; i < kI; ++i)
+          for (int j = 0; j < 8; ++j) sd = fmaf(f[j], d[j], sd);
+          const Split<T, kExact<T>> part = split_of<T, kExact<T>>(d);
 #pragma unroll
-            for (int z = 0; z < kExact<T>; ++z) uf[i][z] = frag_row(s.in.u[z], L::ldv, 16 * (i0 + i), c, lane);
-          keep_reads_here();
-          Split<T, kExact<T>> part[kN];
+          for (int i = 0; i < kI; i += kJ) {
+            Frag<T> uf[kJ][kExact<T>];
 #pragma unroll
-          for (int n = 0; n < kN; ++n) {
-            float d[8], f[8];
-            raw[e][n].get(d);
-            other[n].get(f);
+            for (int j = 0; j < kJ; ++j)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sd = fmaf(f[j], d[j], sd);
-            part[n] = split_of<T, kExact<T>>(d);
+              for (int z = 0; z < kExact<T>; ++z) uf[j][z] = frag_row(s.in.u[z], L::ldv, 16 * (i0 + i + j), c, lane);
+            keep_reads_here();
+            mma_row<T>(ud, i, part, uf);
           }
-          if (e + 1 < kEights) load_state(other, a.keep, cell, c0 + c + 32);
-          mma_grid<T>(ud, part, uf);
         }
 #pragma unroll
         for (int i = 0; i < kI; ++i) {
           const int t = 16 * (i0 + i) + l15;
-          const float to = s.coef.to[t];
-#pragma unroll
-          for (int n = 0; n < kN; ++n) {
-            const v4f pd = quad_get(s.k + t * L::ldn + 16 * (s0 + n) + 4 * g) * ud[n][i];
-            sf[i] += (pd[0] + pd[1]) + (pd[2] + pd[3]);
-            dk[n][i] += to * ud[n][i];
-          }
+          const v4f pd = quad_get(s.k + t * L::ldn + 16 * s0 + 4 * g) * ud[i];
+          sf[i] += (pd[0] + pd[1]) + (pd[2] + pd[3]);
+          dk[i] += s.coef.to[t] * ud[i];
         }
       }
     }
@@ -407,23 +410,21 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
     fetch_gates(next);
 
     sd = sum64(sd);
-    if (lane == 0 && i0 == 0) s.sd[s0 / kN] = sd;
-#pragma unroll
-    for (int i = 0; i < kI; ++i) {
-      const int t = 16 * (i0 + i) + l15;
-      const float tq = sum_groups(sq[i]), tk = sum_groups(sk[i]), tf = sum_groups(sf[i]);
-      if (g == 0) {
-        s.qs[s0 / kN][t] = tq;
-        s.ks[s0 / kN][t] = tk;
-        s.kd[s0 / kN][t] = tf;
+    if (lane == 0 && i0 == 0) s.sd[s0] = sd;
+    {
+      const float tq = sums_of_groups(sq), tk = sums_of_groups(sk), tf = sums_of_groups(sf);
+      const int t = 16 * (i0 + g * kI / 4) + l15;
+      if (g * kI % 4 == 0) {
+        s.sq.qs[s0][t] = tq;
+        s.sq.ks[s0][t] = tk;
+        s.sq.kd[s0][t] = tf;
       }
     }
     // the matrices of the step: this lane's row of a tile, columns 4 g ..
 #pragma unroll
     for (int n = 0; n < kMine; ++n) {
-      const int tile = wave + n * kW;
-      if (tile < 10) {
-        const int ti = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, tj = tile - ti * (ti + 1) / 2;
+      if (mine[n]) {
+        const int ti = row_of[n], tj = col_of[n];
         v4f kk = {0, 0, 0, 0}, qk = {0, 0, 0, 0};
 #pragma unroll
         for (int m = 0; m < NB; ++m) {
@@ -459,12 +460,8 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
     // dQ^T += K^T Pm^T, dK^T += Q^T Pm + K^T (Xm + Xm^T)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      Frag<T> kf[kN][1], qf[kN][1];
-#pragma unroll
-      for (int n = 0; n < kN; ++n) {
-        kf[n][0] = frag_col(s.k, L::ldn, 32 * j, 16 * (s0 + n), lane);
-        qf[n][0] = frag_col(s.q, L::ldn, 32 * j, 16 * (s0 + n), lane);
-      }
+      const Frag<T> kf[1] = {frag_col(s.k, L::ldn, 32 * j, 16 * s0, lane)};
+      const Frag<T> qf[1] = {frag_col(s.q, L::ldn, 32 * j, 16 * s0, lane)};
 #pragma unroll
       for (int m = 0; m < kI; ++m) {
         const int i = i0 + m;
@@ -475,11 +472,8 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
             pf[z] = frag_row(s.sq.pm[z], L::ldm, 16 * i, 32 * j, lane);
             xf[z] = frag_row(s.sq.xm[z], L::ldm, 16 * i, 32 * j, lane);
           }
-#pragma unroll
-          for (int n = 0; n < kN; ++n) {
-            mma_parts<T>(dq[n][m], kf[n], pf);
-            mma_parts<T>(dk[n][m], kf[n], xf);
-          }
+          mma_parts<T>(dq[m], kf, pf);
+          mma_parts<T>(dk[m], kf, xf);
         }
         if (j >= i / 2) {
 #pragma unroll
@@ -487,72 +481,68 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
             pf[z] = frag_col(s.sq.pm[z], L::ldm, 32 * j, 16 * i, lane);
             xf[z] = frag_col(s.sq.xm[z], L::ldm, 32 * j, 16 * i, lane);
           }
-#pragma unroll
-          for (int n = 0; n < kN; ++n) {
-            mma_parts<T>(dk[n][m], qf[n], pf);
-            mma_parts<T>(dk[n][m], kf[n], xf);
-          }
+          mma_parts<T>(dk[m], qf, pf);
+          mma_parts<T>(dk[m], kf, xf);
         }
       }
     }
     keep_all_here();
     fetch(next, 0);  // no earlier: the matrices' products need the registers
-    // the gates' gradients: A_i and F_j first
-    if (tid < kTok) {
+    // the gates' gradients: A_i and F_j by the wave with the fewest Z to add up
+    if (wave == kW - 1) {
       float tq = 0.0f, tk = 0.0f, tf = 0.0f;
 #pragma unroll
       for (int w = 0; w < kAcross; ++w) {
-        tq += s.qs[w][tid];
-        tk += s.ks[w][tid];
-        tf += s.kd[w][tid];
+        tq += s.sq.qs[w][lane];
+        tk += s.sq.ks[w][lane];
+        tf += s.sq.kd[w][lane];
       }
-      const float from = s.coef.from[tid], beta = s.coef.beta[tid];
-      s.a_i[tid] = a.scale * (from * tq) - beta * (from * tk);
-      s.f_j[tid] = s.coef.to[tid] * tf;
+      const float from = s.coef.from[lane], beta = s.coef.beta[lane];
+      s.a_i[lane] = a.scale * (from * tq) - beta * (from * tk);
+      s.f_j[lane] = s.coef.to[lane] * tf;
       float bt = 0.0f;
-      for (int c = 0; c <= tid / 16; ++c) bt += s.bt[c][tid];
-      const float db = s.rv[tid] - from * tk + bt;
-      if (tid < rows) {
-        const long e = static_cast<long>(u.t0 + tid) * a.d_beta.row_stride + h;
+      for (int c = 0; c <= lane / 16; ++c) bt += s.bt[c][lane];
+      const float db = s.rv[lane] - from * tk + bt;
+      if (lane < rows) {
+        const long e = static_cast<long>(u.t0 + lane) * a.d_beta.row_stride + h;
         if (a.gate_bf16) seq_ptr<bf16>(a.d_beta, u.seq, u.row0, packed)[e] = static_cast<bf16>(db);
         else seq_ptr<float>(a.d_beta, u.seq, u.row0, packed)[e] = db;
       }
     }
+    constexpr int kEach = kTok / kW;  // tokens of a wave
+    static_assert(kEach == 8, "two values of each group");
+    const int t0 = wave * kEach;
+    float z = 0.0f;                   // lane j: sum of Z_ij over i >= t
+    for (int i = kTok - 8; i >= t0 + kEach; i -= 8) {
+      float zs[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) zs[e] = s.sq.z[(i + e) * kSq + lane];
+#pragma unroll
+      for (int e = 7; e >= 0; --e) z += lane <= i + e ? zs[e] : 0.0f;
+    }
+    float zs[kEach], dg[2][4];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) zs[e] = s.sq.z[(t0 + e) * kSq + lane];
     __syncthreads();
-    {
-      float ends = 0.0f;
+    float ends = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kAcross; ++w) ends += s.sd[w];
-      ends *= s.coef.total;
-      constexpr int kEach = kTok / kW;  // tokens of a wave
-      const int first = wave * kEach;
-      float z = 0.0f;                   // lane j: sum of Z_ij over i >= t
-      for (int i = kTok - 8; i >= first + kEach; i -= 8) {
-        float zs[8];
+    for (int w = 0; w < kAcross; ++w) ends += s.sd[w];
+    ends *= s.coef.total;
+    const float fj = s.f_j[lane], ai = s.a_i[lane];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) zs[e] = s.sq.z[(i + e) * kSq + lane];
-#pragma unroll
-        for (int e = 7; e >= 0; --e) z += lane <= i + e ? zs[e] : 0.0f;
-      }
-      const float fj = s.f_j[lane], ai = s.a_i[lane];
-      float zs[kEach], dg[kEach];
-#pragma unroll
-      for (int e = 0; e < kEach; ++e) zs[e] = s.sq.z[(first + e) * kSq + lane];
-#pragma unroll
-      for (int e = kEach - 1; e >= 0; --e) {
-        const int t = first + e;
-        z += lane <= t ? zs[e] : 0.0f;
-        dg[e] = sum64((lane < t ? z + fj : 0.0f) + (lane >= t ? ai : 0.0f)) + ends;
-      }
-#pragma unroll
-      for (int e = 0; e < kEach; ++e) {
-        const int t = first + e;
-        if (lane == e && t < rows) {
-          const long at = static_cast<long>(u.t0 + t) * a.d_g.row_stride + h;
-          if (a.gate_bf16) seq_ptr<bf16>(a.d_g, u.seq, u.row0, packed)[at] = static_cast<bf16>(dg[e]);
-          else seq_ptr<float>(a.d_g, u.seq, u.row0, packed)[at] = dg[e];
-        }
-      }
+    for (int e = kEach - 1; e >= 0; --e) {
+      const int t = t0 + e;
+      z += lane <= t ? zs[e] : 0.0f;
+      dg[e >> 2][e & 3] = (lane < t ? z + fj : 0.0f) + (lane >= t ? ai : 0.0f);
+    }
+    // token 4 n + g of the wave's in the lanes n of group g
+    const float low = sum16(sums_of_groups(dg[0])), high = sum16(sums_of_groups(dg[1]));
+    const float sum = (l15 == 0 ? low : high) + ends;
+    const int t = t0 + 4 * l15 + g;
+    if (l15 < 2 && t < rows) {
+      const long at = static_cast<long>(u.t0 + t) * a.d_g.row_stride + h;
+      if (a.gate_bf16) seq_ptr<bf16>(a.d_g, u.seq, u.row0, packed)[at] = static_cast<bf16>(sum);
+      else seq_ptr<float>(a.d_g, u.seq, u.row0, packed)[at] = sum;
     }
   }
   if (parts > 1) {  // added up by delta_sum_kernel
@@ -560,14 +550,12 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
     const unsigned bytes = static_cast<unsigned>(kTok * a.states * 4);
     const Rsrc rq = make_rsrc(p, bytes), rk = make_rsrc(p + kTok * a.states, bytes);
 #pragma unroll
-    for (int n = 0; n < kN; ++n)
-#pragma unroll
-      for (int i = 0; i < kI; ++i) {
-        const int row = 16 * (i0 + i) + l15, col = 16 * (s0 + n) + 4 * g;
-        const unsigned off = col < a.states ? static_cast<unsigned>((row * a.states + col) * 4) : kOutside;
-        Quad<float>::store(rq, off, dq[n][i]);
-        Quad<float>::store(rk, off, dk[n][i]);
-      }
+    for (int i = 0; i < kI; ++i) {
+      const int row = 16 * (i0 + i) + l15, col = 16 * s0 + 4 * g;
+      const unsigned off = col < a.states ? static_cast<unsigned>((row * a.states + col) * 4) : kOutside;
+      Quad<float>::store(rq, off, dq[i]);
+      Quad<float>::store(rk, off, dk[i]);
+    }
     return;
   }
   const Rsrc rq = rows_rsrc(seq_ptr<const T>(a.d_q, u.seq, u.row0, packed) + u.t0 * a.d_q.row_stride + group * a.states,
@@ -575,13 +563,11 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
   const Rsrc rk = rows_rsrc(seq_ptr<const T>(a.d_k, u.seq, u.row0, packed) + u.t0 * a.d_k.row_stride + group * a.states,
                             a.d_k.row_stride, rows, a.states);
 #pragma unroll
-  for (int n = 0; n < kN; ++n)
-#pragma unroll
-    for (int i = 0; i < kI; ++i) {
-      const int row = 16 * (i0 + i) + l15, col = 16 * (s0 + n) + 4 * g;
-      Quad<T>::store(rq, col < a.states ? static_cast<unsigned>((row * static_cast<int>(a.d_q.row_stride) + col) * sizeof(T)) : kOutside, dq[n][i]);
-      Quad<T>::store(rk, col < a.states ? static_cast<unsigned>((row * static_cast<int>(a.d_k.row_stride) + col) * sizeof(T)) : kOutside, dk[n][i]);
-    }
+  for (int i = 0; i < kI; ++i) {
+    const int row = 16 * (i0 + i) + l15, col = 16 * s0 + 4 * g;
+    Quad<T>::store(rq, col < a.states ? static_cast<unsigned>((row * static_cast<int>(a.d_q.row_stride) + col) * sizeof(T)) : kOutside, dq[i]);
+    Quad<T>::store(rk, col < a.states ? static_cast<unsigned>((row * static_cast<int>(a.d_k.row_stride) + col) * sizeof(T)) : kOutside, dk[i]);
+  }
 }
 
 // Adds up the parts of a step's and group's shared gradients, in order.
