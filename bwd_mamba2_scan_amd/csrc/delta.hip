@@ -305,7 +305,9 @@ int segment_tokens(const mamba2_seqs& q, const mamba2_delta_dims& d, bool bwd) {
   const auto rounds = [](long n) { return static_cast<float>((n + kCUs - 1) / kCUs); };
   float best = 0.0f;
   long cut = 1;
-  if (lanes < kCUs) {
+  // A packed call of many sequences is not cut, though one of them may be long: each
+  // has a place for a segment's state and transition, and the carry its work-groups.
+  if (lanes < kCUs && q.batch * d.heads * slices < 16 * kCUs) {
     for (long n = 1; n <= 64 && n <= steps; ++n) {
       const float walk = static_cast<float>((steps + n - 1) / n + 2);
       float cost = rounds(lanes * n) * walk * (bwd ? 2.35f : 1.0f);

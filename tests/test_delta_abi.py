@@ -88,6 +88,11 @@ def test_rule_workspaces(L):
         assert f(q, _dims(width=7)) == 0 and f(Seqs(0, 70, None), d) == 0
         # one long sequence is cut into segments, whose states take room; as many tokens in many sequences are not
         assert f(Seqs(1, 65536, None), d) > f(Seqs(256, 256, None), d)
+        # few packed sequences are cut, many are not, and have no states of segments
+        one, few, many = (f(Seqs(n, 65536, P), _dims(heads=1, groups=1)) for n in (1, 16, 65535))
+        cell = (one - f(Seqs(1, 128, P), _dims(heads=1, groups=1))) / 1022  # of a step, with its share of the segments
+        assert one > f(Seqs(256, 256, None), _dims(heads=1, groups=1)) and few > one
+        assert many <= cell * (1024 + 65535)
         # more tokens, or the same in more sequences, never need less
         sizes = [f(Seqs(1, n, P), d) for n in (0, 1, 64, 65)]
         assert sizes == sorted(sizes) and sizes[0] > 0

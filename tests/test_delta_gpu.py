@@ -117,6 +117,38 @@ def test_packed(lengths, heads, typ):
 
 
 @pytest.mark.parametrize("typ", ["f32", "bf16"])
+def test_many_sequences(typ):
+    """More packed sequences than a wave has lanes, and one tensor as both q and k."""
+    lengths = [13 * i % 97 for i in range(70)]
+    ends = [0]
+    for v in lengths:
+        ends.append(ends[-1] + v)
+    p = dr.inputs(17, (ends[-1],), 70, 2, 24, 1, 32, typ, "f32")
+    d = dr.to(p, DEV)
+    p["q"], d["q"] = p["k"], d["k"]
+    got = _run(d, offsets=torch.tensor(ends, dtype=torch.int32, device=DEV))
+    for i in (0, 1, 33, 65, 69):
+        _check(p, 32 ** -0.5, got, i, lengths[i], span=(ends[i], ends[i + 1]))
+
+
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+@pytest.mark.parametrize("shape,cut", [((2, 70, 2, 24, 1, 40), None), ((1, 1250, 2, 64, 1, 128), None),
+                                       ((1, 1000, 4, 40, 4, 24), [0, 1, 66, 66, 900, 1000])])
+def test_workspaces_of_any_content(shape, cut, typ):
+    """What a workspace held before the call reaches no result."""
+    B, L, H, V, G, K = shape
+    n = B if cut is None else len(cut) - 1
+    d = dr.to(dr.inputs(18, (L,) if cut else (B, L), n, H, V, G, K, typ, "f32"), DEV)
+    off = None if cut is None else torch.tensor(cut, dtype=torch.int32, device=DEV)
+    want = _run(d, offsets=off)
+    spaces = [torch.full((1 << 26,), math.nan, device=DEV), torch.full((1 << 26,), 3e38, device=DEV)]
+    for space in spaces:
+        got = _run(d, offsets=off, workspace=space)
+        for name in want:
+            assert torch.equal(got[name], want[name]), name
+
+
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
 def test_slices(typ):
     """Tensors that are slices of wider ones, gates with any stride, outputs given: bitwise the contiguous result."""
     B, L, H, V, G, K = 2, 90, 4, 24, 2, 16
