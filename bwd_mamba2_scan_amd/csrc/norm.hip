@@ -11,6 +11,11 @@
 // (a power of two up to 64, or the whole block) of R vectors; a thread keeps its
 // channels from row to row, so weights are loaded once and the weights' gradients
 // add up in registers.
+//
+// 16384 tokens, 32 groups of 128 channels, bf16, gated, a weight for all groups:
+// forward 80 us, 0.40 GB, 5.0 TB/s; backward 137 us, 0.67 GB, 4.9 TB/s, and 11 us for
+// the sums over its blocks.  3063 tokens, 8 groups of 97 channels, fp32, element by
+// element: forward 9.7 us, backward 16.4 and 6.3.
 #include "layer_common.h"
 #include "mamba2_delta.h"
 #include "ssm_common.h"

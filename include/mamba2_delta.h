@@ -34,7 +34,8 @@ extern "C" {
  *   width and states multiples of 8, 8 .. 128.  q, k, v, y and the states are
  *   16-byte aligned, with row and batch strides that are multiples of 8
  *   elements; g and beta have any stride.  Row strides are at most 2^29 / 65
- *   elements.
+ *   elements.  A call has 512 threads for every step of 64 tokens and head, and
+ *   for every sequence (a cut one: segment), head, 64 columns and 64 states.
  *   A value that is not finite may reach every token of its own sequence and
  * head (q, k: group) from the start of its step of 64 tokens on (gradients: up
  * to the end of it and before), but no other sequence; an infinity may come
@@ -97,7 +98,8 @@ int mamba2_delta_step(int batch, mamba2_delta_dims dims, mamba2_rows q,
  *   y = o                        (MAMBA2_NORM_SILU: silu(o),
  *                                 MAMBA2_NORM_GATED: o silu(gate))
  * with mean the group's mean (centered), or 0.  silu(v) = v / (1 + e^-v).
- * The statistics are of one token's channels: no token sees another.
+ * The statistics are of one token's channels: no token sees another.  They are
+ * formed in fp32: the sum of a group's (h - mean)^2 stays within its range.
  *   weight, bias: fp32, [channels], or [width] for all groups (shared), or
  *   NULL (1, 0); a bias needs a weight.
  *   1 <= groups <= 65535, 1 <= width <= 16384, channels <= 2^22; eps > 0.
