@@ -18,6 +18,9 @@ The selective layer (include/mamba2_layer.h; module `layer`):
     conv_fwd, conv_bwd, conv_step  -- short causal depthwise convolution with SiLU
     ssm_fwd, ssm_bwd, ssm_step     -- selective state space scan
     grad_norm, clip_grads          -- global gradient norm over many tensors, and clipping
+and beside it (include/mamba2_delta.h; module `delta`):
+    delta_fwd, delta_bwd, delta_step -- gated delta rule
+    group_norm_fwd, group_norm_bwd   -- group norm of a token's channels, with SiLU or a gate
 """
 from __future__ import annotations
 

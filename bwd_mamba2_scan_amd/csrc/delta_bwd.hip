@@ -226,10 +226,11 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
   const long my_stride = second ? a.d_y.row_stride : a.v.row_stride;
   const T* my_p = second ? seq_ptr<const T>(a.d_y, u.seq, u.row0, packed) + u.t0 * a.d_y.row_stride
                          : seq_ptr<const T>(a.v, u.seq, u.row0, packed) + u.t0 * a.v.row_stride;
-  const auto fetch = [&](int h, int c0) {
+  const auto fetch = [&](int h, int c0) {  // behind the last head nothing, by the same loads
     const long cell = static_cast<long>(step) * a.heads + h;
-    const Rsrc rf = make_rsrc((second ? a.u : a.d_r) + cell * slab, static_cast<unsigned>(slab * 4));
-    const Rsrc rt = rows_rsrc(my_p + h * a.width, my_stride, rows, a.width);
+    const bool any = h < behind_h;
+    const Rsrc rf = make_rsrc((second ? a.u : a.d_r) + cell * slab, any ? static_cast<unsigned>(slab * 4) : 0);
+    const Rsrc rt = rows_rsrc(my_p + h * a.width, my_stride, any ? rows : 0, a.width);
     const int t = thread_here(), row = (t & 255) >> 2, col = c0 + (t & 3) * 8;
     const unsigned off = static_cast<unsigned>(row * a.width + col) * 4;
     const unsigned tok = static_cast<unsigned>(row * static_cast<int>(my_stride) + col) * sizeof(T);
@@ -415,9 +416,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
     rv += __shfl_xor(rv, 2);
     if (!second && (tid & 3) == 0) s.rv[tid >> 2] = rv;
     __syncthreads();  // the columns give way to the matrices
-    // the next head's; behind the last one, its own again
-    const int next = h + 1 < behind_h ? h + 1 : h;
-    fetch_gates(next);
+    fetch_gates(h + 1 < behind_h ? h + 1 : h);  // the next head's
 
     sd = sum64(sd);
     if (lane == 0 && i0 == 0) s.sd[s0] = sd;
@@ -497,7 +496,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
       }
     }
     keep_all_here();
-    fetch(next, 0);  // no earlier: the matrices' products need the registers
+    fetch(h + 1, 0);  // no earlier: the matrices' products need the registers
     // the gates' gradients: A_i and F_j by the wave with the fewest Z to add up
     if (wave == kW - 1) {
       float tq = 0.0f, tk = 0.0f, tf = 0.0f;
