@@ -155,6 +155,11 @@ struct Eight {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, off + 16 * i, 0, 0);
   }
+  __device__ __forceinline__ void load_kept(Rsrc rs, unsigned off) {  // of what the walks keep
+    static_assert(sizeof(T) == 4, "in fp32");
+#pragma unroll
+    for (int i = 0; i < 2; ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, off + 1024 * i, 0, 0);
+  }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     if constexpr (sizeof(T) == 2) {
       const v8bf b = __builtin_bit_cast(v8bf, v[0]);
@@ -212,13 +217,13 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
   if (!u.live || u.t0 >= u.len) return;
   const bool packed = a.seqs.offsets != nullptr;
   const int rows = min(u.len - u.t0, kTok);
-  const long head = static_cast<long>(a.states) * a.width, slab = kTok * static_cast<long>(a.width);
+  const long bytes = kept_bytes(a.states, a.width), slab = kept_bytes(kTok, a.width);
   constexpr int kAcross = 2 * NB;                  // waves side by side over the states
   const int s0 = wave % kAcross;                   // this wave's tile of states
   const int i0 = wave / kAcross * kI;              // and the first of tokens
 
   // A part of a head's columns on their way to LDS: a thread has eight columns of
-  // every 32 of one row, of dR and V (the first 256 threads) or of U and dY.
+  // every 32 of one row, of dR and V (the first four waves) or of U and dY.
   constexpr int kEights = kPart<T> / 32;
   Eight<float> flat[kEights];
   Eight<T> token[kEights];
@@ -229,21 +234,21 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
   const auto fetch = [&](int h, int c0) {  // behind the last head nothing, by the same loads
     const long cell = static_cast<long>(step) * a.heads + h;
     const bool any = h < behind_h;
-    const Rsrc rf = make_rsrc((second ? a.u : a.d_r) + cell * slab, any ? static_cast<unsigned>(slab * 4) : 0);
+    const Rsrc rf = make_rsrc((second ? a.u : a.d_r) + cell * (slab / 4), any ? static_cast<unsigned>(slab) : 0);
     const Rsrc rt = rows_rsrc(my_p + h * a.width, my_stride, any ? rows : 0, a.width);
-    const int t = thread_here(), row = (t & 255) >> 2, col = c0 + (t & 3) * 8;
-    const unsigned off = static_cast<unsigned>(row * a.width + col) * 4;
+    const int t = thread_here() & 255, row = (t >> 6) * 16 + (t & 15), col = c0 + 8 * (t >> 4 & 3);
+    const unsigned off = static_cast<unsigned>((t >> 6) * kept_strip(a.width) + kept_at(0, c0) + 16 * (t & 63));
     const unsigned tok = static_cast<unsigned>(row * static_cast<int>(my_stride) + col) * sizeof(T);
 #pragma unroll
     for (int i = 0; i < kEights; ++i) {
       const bool in = col + 32 * i < a.width;
-      flat[i].load(rf, in ? off + 128 * i : kOutside);
+      flat[i].load_kept(rf, in ? off + 2048 * i : kOutside);
       token[i].load(rt, in ? tok + 32 * sizeof(T) * i : kOutside);
     }
   };
   float rv = 0.0f;
   const auto put = [&] {
-    const int here = thread_here(), at0 = ((here & 255) >> 2) * L::ldv + (here & 3) * 8;
+    const int t = thread_here() & 255, at0 = ((t >> 6) * 16 + (t & 15)) * L::ldv + 8 * (t >> 4 & 3);
 #pragma unroll
     for (int i = 0; i < kEights; ++i) {
       const int at = at0 + 32 * i;
@@ -262,9 +267,11 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
   };
   // This lane's rows of a kept state, columns 8 g .. of 32; rows and columns outside are zero.
   const auto load_state = [&](Eight<float>& e, const float* kept, long cell, int c0) {
-    const Rsrc rs = make_rsrc(kept + cell * head, static_cast<unsigned>(head * 4));
-    const int t = thread_here() & 63, c = c0 + 8 * (t >> 4);
-    e.load(rs, c < a.width ? static_cast<unsigned>(((16 * s0 + (t & 15)) * a.width + c) * 4) : kOutside);
+    const Rsrc rs = make_rsrc(kept + cell * (bytes / 4), static_cast<unsigned>(bytes));
+    const int t = thread_here() & 63;
+    const bool in = 16 * s0 + (t & 15) < a.states && c0 + 8 * (t >> 4) < a.width;
+    const unsigned off = in ? static_cast<unsigned>(s0 * kept_strip(a.width) + kept_at(0, c0) + 16 * t) : kOutside;
+    e.load_kept(rs, off);
   };
   float g_raw = 0.0f;
   v4f coef_raw = {0, 0, 0, 0};
@@ -412,9 +419,8 @@ __global__ __launch_bounds__(kGradWaves * 64) void delta_grads_kernel(DeltaArgs 
         }
       }
     }
-    rv += __shfl_xor(rv, 1);
-    rv += __shfl_xor(rv, 2);
-    if (!second && (tid & 3) == 0) s.rv[tid >> 2] = rv;
+    rv = sum_groups(rv);
+    if (!second && g == 0) s.rv[wave * 16 + l15] = rv;
     __syncthreads();  // the columns give way to the matrices
     fetch_gates(h + 1 < behind_h ? h + 1 : h);  // the next head's
 
@@ -652,8 +658,8 @@ struct BwdCell {
 BwdCell bwd_cell(const mamba2_delta_dims& d) {
   BwdCell c;
   c.m = kPieces * kPiece * sizeof(float);
-  c.state = static_cast<size_t>(d.states) * d.width * 4;
-  c.rows = static_cast<size_t>(kTok) * d.width * 4;
+  c.state = static_cast<size_t>(kept_bytes(d.states, d.width));
+  c.rows = static_cast<size_t>(kept_bytes(kTok, d.width));
   c.all = 3 * c.m + 2 * c.state + 2 * c.rows + sizeof(Coef);
   return c;
 }

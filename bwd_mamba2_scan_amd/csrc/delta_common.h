@@ -67,14 +67,23 @@ struct DeltaArgs {
   float* d_initial;
   float* mt;               // as m: the transpose of M
   float* pt;               // as m: the transpose of P
-  float* keep;             // [steps][heads][states][width]: the state each step starts from
+  float* keep;             // [steps][heads], kept_bytes each: the state each step starts from
   float* d_keep;           // the same: the gradient of the state each step ends with
-  float* u;                // [steps][heads][kTok][width]: U
-  float* d_r;              // the same: the gradient of beta (V - 2^c K S)
+  float* u;                // the same for kTok rows: U
+  float* d_r;              // and the gradient of beta (V - 2^c K S)
   int grad_heads;          // heads of a group that one work-group takes the gradients of
   float* grad_part;        // [steps][groups][parts][2][kTok][states]: their parts of d_q and d_k
 };
 
+// What the walks keep lies as delta_grads_kernel reads it, a kilobyte at a time: tiles of
+// 16 rows by 32 columns, of which lane l has row l & 15 and columns 8 (l >> 4) .., four
+// columns of all lanes and then the other four.  Bytes of 16 rows, of all of them, and of
+// an element from its 16 rows' start.
+__host__ __device__ inline int kept_strip(int width) { return (width + 31) / 32 * 2048; }
+__host__ __device__ inline long kept_bytes(int rows, int width) { return static_cast<long>((rows + 15) / 16) * kept_strip(width); }
+__device__ __forceinline__ int kept_at(int row, int col) {
+  return (col >> 5) * 2048 + (col >> 2 & 1) * 1024 + (col >> 3 & 3) * 256 + row * 16 + (col & 3) * 4;
+}
 
 // An element as it was loaded, and its value.  Values are formed where they are
 // used: forming one waits for its load.

@@ -32,16 +32,15 @@ __device__ __forceinline__ v4f swap_row(const float* p, int lane) {
   const int row = lane >> 2, at = 4 * (17 * (row >> 2) + 4 * (lane & 3)) + (row & 3);
   return v4f{p[at], p[at + 4], p[at + 8], p[at + 12]};
 }
-// Tiles of a wave's 16 columns to rows of `width` floats, row lane / 4 of each tile.
+// The tiles of a wave's 16 columns of `rows` rows, kept.
 template <int TILES>
-__device__ __forceinline__ void swap_save(float* out, int rows, int width, int col0, const float* p, int lane) {
-  const Rsrc rs = make_rsrc(out, static_cast<unsigned>(rows * width * 4));
-  const int c = col0 + 4 * (lane & 3);
-  const unsigned off = c < width ? static_cast<unsigned>(((lane >> 2) * width + c) * 4) : kOutside;
+__device__ __forceinline__ void swap_keep(float* out, int rows, int width, int col0, const float* p, int lane) {
+  const Rsrc rs = make_rsrc(out, static_cast<unsigned>(kept_bytes(rows, width)));
+  const int c = col0 + 4 * (lane & 3), strip = kept_strip(width);
+  const unsigned off = c < width ? static_cast<unsigned>(kept_at(lane >> 2, c)) : kOutside;
 #pragma unroll
   for (int n = 0; n < TILES; ++n)
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, swap_row(p + n * kSwapTile, lane)), rs,
-                                           off + n * 64 * width, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, swap_row(p + n * kSwapTile, lane)), rs, off + n * strip, 0, 0);
 }
 
 // A matrix's fp32 pieces on their way to LDS, where they lie in three bf16 parts that
@@ -108,7 +107,7 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
   if (!u.live || !wanted<MODE>(a, cl, u)) return;
   const int h = cl.h, p0 = cl.p0;
   const bool packed = a.seqs.offsets != nullptr;
-  const long head = static_cast<long>(a.states) * a.width;
+  const long kept = kept_bytes(a.states, a.width) / 4, slab = kept_bytes(kTok, a.width) / 4;
   const long cell0 = static_cast<long>(unit_base(a.seqs, u.seq, kTok)) * a.heads + h;  // of the sequence's first step
   const int end = min(u.t0 + a.seg, u.len);
 
@@ -173,7 +172,7 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
       const long cell = cell0 + static_cast<long>(t / kTok) * a.heads;
       v4f y[4];
       if (MODE == kKept) {
-        swap_save<2 * NB>(a.keep + cell * head, a.states, a.width, p0 + strip * 16, s.keep.s[strip], lane);
+        swap_keep<2 * NB>(a.keep + cell * kept, a.states, a.width, p0 + strip * 16, s.keep.s[strip], lane);
       } else {  // (Q S)^T
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] = v4f{0, 0, 0, 0};
@@ -193,7 +192,7 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
       }
       __syncthreads();  // U is in LDS
       if (MODE == kKept) {
-        swap_save<4>(a.u + cell * (kTok * static_cast<long>(a.width)), kTok, a.width, p0 + strip * 16, s.keep.u[strip], lane);
+        swap_keep<4>(a.u + cell * slab, kTok, a.width, p0 + strip * 16, s.keep.u[strip], lane);
       } else {
         Split<bf16, 2> us[2];
 #pragma unroll
@@ -334,7 +333,7 @@ __device__ __forceinline__ void pair_reverse(const DeltaArgs& a, PairRevLds<NB>&
   const int h = wk.h, slice = wk.slice;
   const bool packed = a.seqs.offsets != nullptr;
   const int p0 = slice * kCols;
-  const long head = static_cast<long>(a.states) * a.width, slab = kTok * static_cast<long>(a.width);
+  const long kept = kept_bytes(a.states, a.width) / 4, slab = kept_bytes(kTok, a.width) / 4;
   const long cell0 = static_cast<long>(unit_base(a.seqs, u.seq, kTok)) * a.heads + h;
   const int end = min(u.t0 + a.seg, u.len);
   const int last = end > u.t0 ? u.t0 + (end - 1 - u.t0) / kTok * kTok : u.t0 - kTok;
@@ -411,12 +410,12 @@ __device__ __forceinline__ void pair_reverse(const DeltaArgs& a, PairRevLds<NB>&
       }
       __syncthreads();  // D and dR are in LDS
       const long cell = cell0 + static_cast<long>(t / kTok) * a.heads;
-      if (!SUMMARY) swap_save<2 * NB>(a.d_keep + cell * head, a.states, a.width, p0 + strip * 16, s.d[strip], lane);
+      if (!SUMMARY) swap_keep<2 * NB>(a.d_keep + cell * kept, a.states, a.width, p0 + strip * 16, s.d[strip], lane);
 #pragma unroll
       for (int n = 0; n < 2 * NB; ++n) swap_put(s.d[strip] + n * kSwapTile, lane, add[n]);
       __syncthreads();  // the walkers are done with the operands but for what was put last
       if (SUMMARY) continue;
-      swap_save<4>(a.d_r + cell * slab, kTok, a.width, p0 + strip * 16, s.r[strip], lane);
+      swap_keep<4>(a.d_r + cell * slab, kTok, a.width, p0 + strip * 16, s.r[strip], lane);
       const Rsrc rv = rows_rsrc(vp + t * a.d_v.row_stride, a.d_v.row_stride, min(end - t, kTok), a.width);
 #pragma unroll
       for (int i = 0; i < 4; ++i)

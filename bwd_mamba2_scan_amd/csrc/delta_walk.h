@@ -28,17 +28,19 @@ struct Flat {
   }
 };
 
-// A wave's 64 x 16 result into [kTok][width] floats.
-__device__ __forceinline__ void save_rows(float* p, int width, int col, int g, const v4f (&w)[4]) {
-  const Rsrc rs = make_rsrc(p, static_cast<unsigned>(kTok * width * 4));
-  const unsigned off = col < width ? static_cast<unsigned>((4 * g * width + col) * 4) : kOutside;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) store_elem<float>(rs, off + (16 * i + r) * width * 4, w[i][r]);
-}
-
 constexpr int kCols = kWaves * 16;
+
+// A wave's columns of `rows` rows, kept.
+template <int N>
+__device__ __forceinline__ void save_kept(float* p, int rows, int width, int col, int g, const v4f (&w)[N]) {
+  const Rsrc rs = make_rsrc(p, static_cast<unsigned>(kept_bytes(rows, width)));
+  const int strip = kept_strip(width);
+  const unsigned off = col < width ? static_cast<unsigned>(kept_at(4 * g, col)) : kOutside;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) store_elem<float>(rs, off + n * strip + 16 * i, w[n][i]);
+}
 
 // Four rows 4 g .. of column l15 of tile i of an LDS tile of tokens.
 __device__ __forceinline__ v4f tile_col(const bf16* p, int ld, int i, int col, int lane) {
@@ -186,7 +188,7 @@ __device__ __forceinline__ void walk_forward(const DeltaArgs& a, FwdLds<T, NB, M
     if (t + kTok < end) fetch(t + kTok);
 
     const long cell = cell0 + static_cast<long>(t / kTok) * a.heads;
-    if (MODE == kKept) st.save(a.keep + cell * (static_cast<long>(a.states) * a.width), a.width, a.states);
+    if (MODE == kKept) save_kept(a.keep + cell * (kept_bytes(a.states, a.width) / 4), a.states, a.width, col, g, st.st);
     // K S and (Q S)^T.  The operands of a part are read from LDS while the part
     // before it is multiplied: one wave a SIMD hides no latency by itself.
     constexpr int kBuf = NB > 1 ? 2 : 1;
@@ -266,7 +268,7 @@ __device__ __forceinline__ void walk_forward(const DeltaArgs& a, FwdLds<T, NB, M
     read_cols(0);
     keep_reads_here();
     if (MODE == kKept) {
-      save_rows(a.u + cell * (kTok * static_cast<long>(a.width)), a.width, col, g, w);
+      save_kept(a.u + cell * (kept_bytes(kTok, a.width) / 4), kTok, a.width, col, g, w);
     } else if (MODE == kResults) {  // Y^T = (scale 2^c Q S)^T + U^T P^T
       const Split<T, kTwo<T>> us[2] = {split_pair<T, kTwo<T>>(w[0], w[1]), split_pair<T, kTwo<T>>(w[2], w[3])};
       const Rsrc ry = rows_rsrc(yp + t * a.y.row_stride, a.y.row_stride, min(end - t, kTok), a.width);
@@ -349,7 +351,6 @@ __device__ __forceinline__ void walk_reverse(const DeltaArgs& a, RevLds<T, NB>& 
   const bool packed = a.seqs.offsets != nullptr;
   const int p0 = slice * kThreads / 4;
   const int col = p0 + wave * 16 + l15;
-  const long head = static_cast<long>(a.states) * a.width;
   const T* kp = seq_ptr<const T>(a.k, u.seq, u.row0, packed) + h / a.ratio * a.states;
   const T* qp = seq_ptr<const T>(a.q, u.seq, u.row0, packed) + h / a.ratio * a.states;
   const T* yp = seq_ptr<const T>(a.d_y, u.seq, u.row0, packed) + h * a.width + p0;
@@ -394,7 +395,7 @@ __device__ __forceinline__ void walk_reverse(const DeltaArgs& a, RevLds<T, NB>& 
     if (t > u.t0) fetch(t - kTok);
 
     const long cell = cell0 + static_cast<long>(t / kTok) * a.heads;
-    if (!SUMMARY) st.save(a.d_keep + cell * head, a.width, a.states);
+    if (!SUMMARY) save_kept(a.d_keep + cell * (kept_bytes(a.states, a.width) / 4), a.states, a.width, col, g, st.st);
     // dU
     constexpr int kBuf = NB > 1 ? 2 : 1;
     Frag<T> kf[kBuf][4];
@@ -463,7 +464,7 @@ __device__ __forceinline__ void walk_reverse(const DeltaArgs& a, RevLds<T, NB>& 
     };
     read_cols(0);
     keep_reads_here();
-    if (!SUMMARY) save_rows(a.d_r + cell * (kTok * static_cast<long>(a.width)), a.width, col, g, dr);
+    if (!SUMMARY) save_kept(a.d_r + cell * (kept_bytes(kTok, a.width) / 4), kTok, a.width, col, g, dr);
     const Rsrc rv = rows_rsrc(vp + t * a.d_v.row_stride, a.d_v.row_stride, min(end - t, kTok), a.width);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
