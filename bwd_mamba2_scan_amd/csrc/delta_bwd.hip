@@ -72,11 +72,13 @@ constexpr int kPart = sizeof(T) == 2 ? 128 : 64;  // columns of a head that LDS 
 
 // Eight waves share a step's 2 NB tiles of 16 states by four tiles of 16 tokens:
 // one by NB of them a wave, so that each state is loaded and split once.
-// 716 us, 1.6 GB of states and rows read; with two by two tiles a wave 750.  LDS holds
-// one work-group on a CU, whose phases take turns: of its cycles the vector pipes are
-// busy for 34%, the matrix pipes for 24%, LDS for 36%, and HBM could have moved the
-// bytes in 310 us.  Sixteen waves, and work-groups that stay for several steps and
-// load the next one's operands ahead, spilled registers: 960 and 747 us.
+// 680 us, 2.0 GB read; with two by two tiles a wave 750, and 690 with what is kept in
+// rows.  LDS holds one work-group on a CU, whose phases take turns: of its cycles the
+// vector pipes are busy for 36%, the matrix pipes for 24%, LDS for 36%, and HBM could
+// have moved the bytes in 420 us.  Sixteen waves, and work-groups that stay for several
+// steps and load the next one's operands ahead, spilled registers: 960 and 747 us; the
+// next head's states loaded ahead with its rows took 713 (S) and 761 us (S and D), as
+// the loads are issued in order and those needed first wait behind them.
 constexpr int kGradWaves = 8;
 
 template <class T, int NB>

@@ -13,9 +13,9 @@
 // add up in registers.
 //
 // 16384 tokens, 32 groups of 128 channels, bf16, gated, a weight for all groups:
-// forward 80 us, 0.40 GB, 5.0 TB/s; backward 137 us, 0.67 GB, 4.9 TB/s, and 11 us for
+// forward 80 us, 0.40 GB, 5.0 TB/s; backward 138 us, 0.67 GB, 4.9 TB/s, and 5 us for
 // the sums over its blocks.  3063 tokens, 8 groups of 97 channels, fp32, element by
-// element: forward 9.7 us, backward 16.4 and 6.3.
+// element: forward 10 us, backward 16 and 5.
 #include "layer_common.h"
 #include "mamba2_delta.h"
 #include "ssm_common.h"
@@ -352,8 +352,9 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void norm_bwd_kernel(NormArgs a)
 }
 
 // Sums [slices][2][n] over the slices: 32 columns a block, 32 runs of slices, in a
-// fixed order.
-constexpr int kSumCols = 32, kSumRuns = 32;
+// fixed order.  Latency bounds it, so kSumAhead loads are on their way at a time:
+// 1024 slices of 256 columns 4.9 us, one load after the other 11.7.
+constexpr int kSumCols = 32, kSumRuns = 32, kSumAhead = 8;
 struct SumArgs {
   const float* partial;
   float* d_weight;
@@ -366,8 +367,17 @@ __global__ __launch_bounds__(kSumCols * kSumRuns) void norm_sum_kernel(SumArgs a
   const int c = threadIdx.x % kSumCols, run = threadIdx.x / kSumCols;
   const long col = static_cast<long>(blockIdx.x) * kSumCols + c;  // of 2 n
   float s = 0.0f;
-  if (col < 2 * a.n)
-    for (long i = run; i < a.slices; i += kSumRuns) s += a.partial[i * 2 * a.n + col];
+  if (col < 2 * a.n) {
+    long i = run;
+    for (; i + (kSumAhead - 1) * kSumRuns < a.slices; i += kSumAhead * kSumRuns) {
+      float v[kSumAhead];
+#pragma unroll
+      for (int j = 0; j < kSumAhead; ++j) v[j] = a.partial[(i + j * kSumRuns) * 2 * a.n + col];
+#pragma unroll
+      for (int j = 0; j < kSumAhead; ++j) s += v[j];
+    }
+    for (; i < a.slices; i += kSumRuns) s += a.partial[i * 2 * a.n + col];
+  }
   part[run][c] = s;
   __syncthreads();
   if (run == 0 && col < 2 * a.n) {
