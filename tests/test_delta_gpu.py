@@ -345,3 +345,54 @@ def test_far_apart_sequences():
     out = big.as_strided((2, L, H, V), (far, H * V, V, 1))
     m2.delta_fwd(*_args(d), initial_state=d["state"], y=out)
     assert torch.equal(out, want["y"])
+
+
+def test_rows_far_apart():
+    """Rows of the largest stride: a sequence's last ones are more than 2^31 elements behind its first."""
+    H, V, G, K, L = 2, 16, 1, 16, 300
+    d = dr.to(dr.inputs(19, (1, L), 1, H, V, G, K, "bf16", "f32"), DEV)
+    want = _run(d)
+    stride = (1 << 29) // 65
+    big = torch.empty((L - 1) * stride + 4 * H * V, dtype=torch.bfloat16, device=DEV)
+    at = lambda i: big.as_strided((1, L, H, V), (L * stride, stride, V, 1), i * H * V)
+    s = dict(d, v=at(0).copy_(d["v"]), d_y=at(1).copy_(d["d_y"]))
+    y, final = m2.delta_fwd(*_args(s), initial_state=s["state"], want_final_state=True, y=at(2))
+    assert torch.equal(y, want["y"]) and torch.equal(final, want["final"])
+    g = m2.delta_bwd(*_args(s), s["d_y"], initial_state=s["state"], d_final_state=s["d_final"], out=dict(d_v=at(3)))
+    for n in ("d_q", "d_k", "d_v", "d_g", "d_beta"):
+        assert torch.equal(g[n], want[n]), n
+
+
+def test_states_beyond_32_bits():
+    """More than 2^31 elements of state: the last sequences' are what they are by themselves."""
+    B, H, V, G, K = 1050, 128, 128, 16, 128
+    d = dr.to(dr.inputs(20, (2, 1), 2, H, V, G, K, "bf16", "f32"), DEV)
+    many = {n: d[n].repeat(B // 2, 1, 1, 1) if d[n].dim() == 4 else d[n].repeat(B // 2, 1, 1) for n in NAMES}
+    state = torch.zeros(B, H, K, V, device=DEV)
+    assert state.numel() > 1 << 31
+    state[-2:] = d["state"]
+    y, final = m2.delta_fwd(*_args(d), initial_state=d["state"], want_final_state=True)
+    got, ends = m2.delta_fwd(*_args(many), initial_state=state, want_final_state=True)
+    assert torch.equal(got[-2:], y) and torch.equal(ends[-2:], final)
+    del ends
+    new = d["state"].clone()
+    y = m2.delta_step(*(d[n][:, 0] for n in NAMES), new)
+    got = m2.delta_step(*(many[n][:, 0] for n in NAMES), state)
+    assert torch.equal(got[-2:], y) and torch.equal(state[-2:], new)
+
+
+def test_gates_of_another_type():
+    """bf16 gates beside fp32 values."""
+    B, L, H, V, G, K = 2, 65, 4, 72, 2, 40
+    p = dr.inputs(21, (B, L), B, H, V, G, K, "f32", "bf16")
+    got = _run(dr.to(p, DEV))
+    assert got["d_g"].dtype == got["d_beta"].dtype == torch.bfloat16
+    for i in range(B):
+        _check(p, K ** -0.5, got, i, "gates")
+    s = {n: p[n][:, 0] for n in NAMES}
+    new = p["state"].to(DEV)
+    y = m2.delta_step(*(s[n].to(DEV) for n in NAMES), new)
+    for i in range(B):
+        one = dict({n: p[n][i, :1] for n in NAMES}, d_y=p["d_y"][i, :1], state=p["state"][i], d_final=None)
+        b = dr.bounds(one, K ** -0.5)
+        within(y[i], b["y"][0][0], b["y"][1][0], (i, "y"))

@@ -158,3 +158,20 @@ def test_reproducible_and_refusals():
         m2.group_norm_fwd(x.half(), groups=6)
     with pytest.raises(m2.Mamba2ScanError):
         m2.group_norm_fwd(x, groups=6, eps=0.0)
+
+
+def test_rows_far_apart():
+    """The last rows are more than 2^31 elements behind the first."""
+    rows, stride = 300, (1 << 23) + 8
+    p = gn.inputs(9, (rows,), 4, 16, "bf16", "gated", "group", True)
+    d = _to(p)
+    kw = gn.keywords(4, "gated", True)
+    want = _run(d, **kw)
+    big = torch.empty((rows - 1) * stride + 5 * 64, dtype=torch.bfloat16, device=DEV)
+    at = lambda i: big.as_strided((rows, 64), (stride, 1), 64 * i)
+    s = {n: at(i).copy_(d[n]) for i, n in enumerate(("x", "gate", "d_y"))}
+    y = m2.group_norm_fwd(s["x"], d["weight"], d["bias"], gate=s["gate"], y=at(3), **kw)
+    assert torch.equal(y, want["y"])
+    g = m2.group_norm_bwd(s["x"], s["d_y"], d["weight"], d["bias"], gate=s["gate"], out=dict(d_x=at(4)), **kw)
+    for n in ("d_x", "d_gate", "d_weight", "d_bias"):
+        assert torch.equal(g[n], want[n]), n
