@@ -49,7 +49,7 @@ __global__ __launch_bounds__(walk_threads<T>) void delta_fwd_kernel(DeltaArgs a)
 }
 
 // What segments make of the states before them: a step costs 0.7 of delta_fwd_kernel's.
-// One sequence of 32768 tokens, 24 heads of 64 x 64, ten segments: 204 us, beside 180
+// One sequence of 32768 tokens, 24 heads of 64 x 64, ten segments: 190 us, beside 180
 // of the walk itself and 12 of the carry.
 template <class T, int NB>
 __global__ __launch_bounds__(walk_threads<T>) void delta_summary_kernel(DeltaArgs a) {
