@@ -33,9 +33,9 @@ __global__ __launch_bounds__(kPrepWaves * 64, NB < 4 || sizeof(T) == 2 ? 4 : 2) 
   });
 }
 
-// A chain of steps, with LDS as the busiest pipe: 4 x 4096 tokens, 32 heads of 128 x
-// 128, bf16, a work-group on every CU: 280 us, 4.4 a step, LDS busy for 45% of it and
-// the matrix pipes for 31%.  fp32 (simple walks, 3 x 333 tokens, 10 heads of 24 x 40):
+// A chain of steps: 4 x 4096 tokens, 32 heads of 128 x 128, bf16, a work-group on every
+// CU: 275 us, 4.3 a step, LDS busy for 48% of it, the vector pipes for 38%, the matrix
+// pipes for 33%.  fp32 (simple walks, 3 x 333 tokens, 10 heads of 24 x 40):
 // 28 us, 4.7 a step.
 template <class T, int NB>
 __global__ __launch_bounds__(walk_threads<T>) void delta_fwd_kernel(DeltaArgs a) {

@@ -54,7 +54,8 @@ __global__ __launch_bounds__(walk_threads<T>) void delta_keep_kernel(DeltaArgs a
 }
 
 // 402 us, 6.3 a step: two triangular products on its chain, and LDS has room for one
-// step's operands only.  The matrix pipes are busy for 34% of it, LDS for 40%.
+// step's operands only.  LDS is busy for 40% of it, the vector pipes for 31%, the matrix
+// pipes for 24%.  With all but K put into LDS before the walkers are done, the same.
 template <class T, int NB, bool SUMMARY>
 __global__ __launch_bounds__(walk_threads<T>) void delta_reverse_kernel(DeltaArgs a) {
   if constexpr (sizeof(T) == 2) {

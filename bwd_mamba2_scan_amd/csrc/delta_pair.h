@@ -208,7 +208,10 @@ __device__ __forceinline__ void pair_forward(const DeltaArgs& a, PairFwdLds<NB, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) Quad<bf16>::store(ry, y_off + i * y16, y[i]);
       }
-      put(b ^ 1);  // no earlier: beside the walkers' first product it took longer (275 to 294 us)
+      // Here, where walkers have little to do: put beside their first product, a step
+      // ahead, the walk of delta_fwd_kernel's figures took 294 us for 275, and with P U
+      // and the results there 289.
+      put(b ^ 1);
     }
     return;
   }
