@@ -13,7 +13,7 @@
 // add up in registers.
 //
 // 16384 tokens, 32 groups of 128 channels, bf16, gated, a weight for all groups:
-// forward 80 us, 0.40 GB, 5.0 TB/s; backward 138 us, 0.67 GB, 4.9 TB/s, and 5 us for
+// forward 76 us, 0.40 GB, 5.3 TB/s; backward 128 us, 0.67 GB, 5.2 TB/s, and 5 us for
 // the sums over its blocks.  3063 tokens, 8 groups of 97 channels, fp32, element by
 // element: forward 10 us, backward 16 and 5.
 #include "layer_common.h"
@@ -134,23 +134,40 @@ __device__ __forceinline__ void rows_range(const NormArgs& a, int* first, int* b
   }
 }
 
-template <class T, int V, int R>
-__device__ __forceinline__ void load_row(const T* p, const Place& w, const NormArgs& a, float (&v)[R][V]) {
+// V neighbouring elements as they were loaded.
+template <class T, int V>
+struct Piece {
+  typename Vec<T>::type v;
+  __device__ __forceinline__ void load(const T* p) { v = *reinterpret_cast<const typename Vec<T>::type*>(p); }
+  __device__ __forceinline__ float operator[](int j) const { return static_cast<float>(v[j]); }
+};
+template <class T>
+struct Piece<T, 1> {
+  T v;
+  __device__ __forceinline__ void load(const T* p) { v = *p; }
+  __device__ __forceinline__ float operator[](int) const { return static_cast<float>(v); }
+};
+// A thread's pieces of a row.  AHEAD: one that its group does not have is the group's
+// first one, so that all are loaded, none behind a branch, which would make a wait for
+// these loads a wait for what is issued after them, too.  Else it is 0.
+template <class T, int V, int R, bool AHEAD>
+struct Pieces {
+  Piece<T, V> p[R];
+  __device__ __forceinline__ void load(const mamba2_rows& r, const NormArgs& a, const Place& w, int row) {
+    const T* base = row_ptr<const T>(r, a, row);
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    if (w.in_group + i * a.lanes * V < a.width) {
-      load_vec<T, V>(p + w.channel + i * a.lanes * V, v[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[i][j] = 0.0f;
+    for (int i = 0; i < R; ++i) {
+      const bool in = w.in_group + i * a.lanes * V < a.width;
+      const int at = w.channel + i * a.lanes * V;
+      if (AHEAD) p[i].load(base + (in ? at : w.channel - w.in_group));
+      else if (in) p[i].load(base + at);
+      else p[i] = {};
     }
   }
-}
-template <class T, int V, int R>
-__device__ __forceinline__ void store_row(T* p, const Place& w, const NormArgs& a, const float (&v)[R][V]) {
-#pragma unroll
-  for (int i = 0; i < R; ++i)
-    if (w.in_group + i * a.lanes * V < a.width) store_vec<T, V>(p + w.channel + i * a.lanes * V, v[i]);
+};
+template <class T, int V>
+__device__ __forceinline__ void store_piece(T* p, const Place& w, const NormArgs& a, int i, const float (&v)[V]) {
+  if (w.in_group + i * a.lanes * V < a.width) store_vec<T, V>(p + w.channel + i * a.lanes * V, v);
 }
 // A parameter's values of a thread's channels.
 template <int V, int R>
@@ -192,6 +209,29 @@ __device__ __forceinline__ float normalise(float (&h)[R][V], const Place& w, con
   return r;
 }
 
+// A block's rows, the call's `first` .. `behind` - 1.
+__device__ __forceinline__ long rows_of_block(const NormArgs& a, int chunk, int* end) {
+  int first, behind;
+  rows_range(a, &first, &behind);
+  const long row0 = static_cast<long>(first) + static_cast<long>(chunk) * a.run;
+  *end = static_cast<int>(min(row0 + a.run, static_cast<long>(behind)));
+  return row0;
+}
+
+// The next row is loaded while one is worked on, where a thread has the registers and
+// whole vectors: 16384 rows of 4096 channels, bf16, gated, backward 171 us without, 154
+// with it; 65536 rows of 1024, 204 and 145; 16384 tokens of 32 groups of 128, 137 and 128.
+// Groups of 97, element by element, lose by it (the last row is loaded twice).
+// Nor do wide blocks' forwards of whole vectors gain, of which more are on a CU (8192
+// rows of 8192, gated: 87 us without, 96 with it; by elements, 16384 of 4096, 316 and 136).
+template <class T, int V, int R, bool WIDE, bool BWD>
+constexpr bool kAhead = !WIDE ? V > 1 : BWD ? R * V * static_cast<int>(sizeof(T)) <= 16 : V == 1 && R < 16;
+// The backward of a block of 1024 threads reads its parameters again for each row where
+// it has two vectors of bf16 or four of fp32 (4096 rows of 12288, bf16, gated: 418 us
+// with them held, which spills, 276).
+template <int V, int R, bool WIDE>
+constexpr bool kHold = !WIDE || V == 1 || R * V <= 8;
+
 template <class T, int V, int R, int FORM, bool WIDE>
 __global__ __launch_bounds__(WIDE ? 1024 : 256) void norm_fwd_kernel(NormArgs a) {
   __shared__ float part[32];
@@ -199,35 +239,45 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void norm_fwd_kernel(NormArgs a)
   const int column = blockIdx.x % a.columns, chunk = blockIdx.x / a.columns;
   const Place w = place_of<V>(a, column);
   GroupSum<WIDE> sum{a.lanes, part, 0};
-  int first, behind;
-  rows_range(a, &first, &behind);
-  const long row0 = static_cast<long>(first) + static_cast<long>(chunk) * a.run;
-  const int end = static_cast<int>(min(row0 + a.run, static_cast<long>(behind)));
+  int end;
+  long row = rows_of_block(a, chunk, &end) + w.row;
   float weight[R][V], bias[R][V];
   load_parameter<V, R>(a.weight, w, a, 1.0f, weight);
   load_parameter<V, R>(a.bias, w, a, 0.0f, bias);
-  if (!WIDE && !w.live) return;  // a wide block has one group
-  for (long row = row0 + w.row; row < end; row += w.step) {
-    float h[R][V], z[R][V];
-    load_row<T, V, R>(row_ptr<const T>(a.x, a, row), w, a, h);
-    if constexpr (kGate) load_row<T, V, R>(row_ptr<const T>(a.gate, a, row), w, a, z);
-    if constexpr (FORM == MAMBA2_NORM_GATE_FIRST) {
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) h[i][j] *= z[i][j] * sigmoid_of(z[i][j]);
-    }
-    normalise<V, R>(h, w, a, sum);
+  if (!w.live || row >= end) return;  // a wide block has one group and one row at a time
+  constexpr bool kNext = kAhead<T, V, R, WIDE, false>;
+  Pieces<T, V, R, kNext> x, gate;
+  const auto fetch = [&](long r) {
+    x.load(a.x, a, w, r);
+    if constexpr (kGate) gate.load(a.gate, a, w, r);
+  };
+  if constexpr (kNext) fetch(row);
+  for (; row < end; row += w.step) {
+    if constexpr (!kNext) fetch(row);
+    const Pieces<T, V, R, kNext> hx = x, hz = gate;
+    if constexpr (kNext) fetch(row + w.step < end ? row + w.step : row);  // the last one again
+    float h[R][V];
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int j = 0; j < V; ++j) {
+        float v = hx.p[i][j];
+        if constexpr (FORM == MAMBA2_NORM_GATE_FIRST) v *= hz.p[i][j] * sigmoid_of(hz.p[i][j]);
+        h[i][j] = !kNext || w.in_group + i * a.lanes * V < a.width ? v : 0.0f;
+      }
+    normalise<V, R>(h, w, a, sum);
+    T* y = row_ptr<T>(a.y, a, row);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
         float o = fmaf(h[i][j], weight[i][j], bias[i][j]);
         if constexpr (FORM == MAMBA2_NORM_SILU) o *= sigmoid_of(o);
-        if constexpr (FORM == MAMBA2_NORM_GATED) o *= z[i][j] * sigmoid_of(z[i][j]);
+        if constexpr (FORM == MAMBA2_NORM_GATED) o *= hz.p[i][j] * sigmoid_of(hz.p[i][j]);
         h[i][j] = o;
       }
-    store_row<T, V, R>(row_ptr<T>(a.y, a, row), w, a, h);
+      store_piece<T, V>(y, w, a, i, h[i]);
+    }
   }
 }
 
@@ -240,78 +290,93 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void norm_bwd_kernel(NormArgs a)
   const int column = blockIdx.x % a.columns, chunk = blockIdx.x / a.columns;
   const Place w = place_of<V>(a, column);
   GroupSum<WIDE> sum{a.lanes, part, 0};
-  int first, behind;
-  rows_range(a, &first, &behind);
-  const long row0 = static_cast<long>(first) + static_cast<long>(chunk) * a.run;
-  const int end = static_cast<int>(min(row0 + a.run, static_cast<long>(behind)));
+  int end;
+  long row = rows_of_block(a, chunk, &end) + w.row;
   float weight[R][V], bias[R][V], d_w[R][V], d_b[R][V];
-  load_parameter<V, R>(a.weight, w, a, 1.0f, weight);
-  load_parameter<V, R>(a.bias, w, a, 0.0f, bias);
+  const auto parameters = [&] {
+    load_parameter<V, R>(a.weight, w, a, 1.0f, weight);
+    if constexpr (FORM == MAMBA2_NORM_SILU || FORM == MAMBA2_NORM_GATED) load_parameter<V, R>(a.bias, w, a, 0.0f, bias);
+  };
+  if constexpr (kHold<V, R, WIDE>) parameters();
 #pragma unroll
   for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int j = 0; j < V; ++j) d_w[i][j] = d_b[i][j] = 0.0f;
-  for (long row = row0 + w.row; row < end && w.live; row += w.step) {
-    float h[R][V], z[R][V], x[R][V], d[R][V];
-    load_row<T, V, R>(row_ptr<const T>(a.x, a, row), w, a, h);
-    if constexpr (kGate) load_row<T, V, R>(row_ptr<const T>(a.gate, a, row), w, a, z);
-    load_row<T, V, R>(row_ptr<const T>(a.d_y, a, row), w, a, d);
-    float s[R][V];  // sigmoid of the gate
-    if constexpr (kGate) {
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) s[i][j] = sigmoid_of(z[i][j]);
-    }
-    if constexpr (FORM == MAMBA2_NORM_GATE_FIRST) {
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          x[i][j] = h[i][j];
-          h[i][j] *= z[i][j] * s[i][j];
-        }
-    }
-    const float r = normalise<V, R>(h, w, a, sum);
-    float dn = 0.0f, dnn = 0.0f;
-    float dz[R][V];
+  constexpr bool kNext = kAhead<T, V, R, WIDE, true>;
+  Pieces<T, V, R, kNext> x, gate, d_y;
+  const auto fetch = [&](long r) {
+    x.load(a.x, a, w, r);
+    if constexpr (kGate) gate.load(a.gate, a, w, r);
+    d_y.load(a.d_y, a, w, r);
+  };
+  const bool any = w.live && row < end;
+  if (kNext && any) fetch(row);
+  for (; any && row < end; row += w.step) {
+    if constexpr (!kNext) fetch(row);
+    const Pieces<T, V, R, kNext> hx = x, hz = gate, hd = d_y;
+    if constexpr (kNext) fetch(row + w.step < end ? row + w.step : row);
+    float h[R][V], d[R][V];
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int j = 0; j < V; ++j) {
+        float v = hx.p[i][j];
+        if constexpr (FORM == MAMBA2_NORM_GATE_FIRST) v *= hz.p[i][j] * sigmoid_of(hz.p[i][j]);
+        h[i][j] = !kNext || w.in_group + i * a.lanes * V < a.width ? v : 0.0f;
+      }
+    const float r = normalise<V, R>(h, w, a, sum);
+    if constexpr (!kHold<V, R, WIDE>) parameters();
+    T* const d_x = row_ptr<T>(a.d_x, a, row);
+    T* const d_gate = kGate ? row_ptr<T>(a.d_gate, a, row) : nullptr;
+    const bool put_x = a.d_x.data != nullptr, put_gate = a.d_gate.data != nullptr;
+    float dn = 0.0f, dnn = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const bool in = !kNext || w.in_group + i * a.lanes * V < a.width;  // else 0 was loaded
+      float dz[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
         const float n = h[i][j];
+        float e = in ? hd.p[i][j] : 0.0f;
         if constexpr (FORM == MAMBA2_NORM_SILU) {
           const float o = fmaf(n, weight[i][j], bias[i][j]), so = sigmoid_of(o);
-          d[i][j] *= so * fmaf(o, 1.0f - so, 1.0f);
+          e *= so * fmaf(o, 1.0f - so, 1.0f);
         }
         if constexpr (FORM == MAMBA2_NORM_GATED) {
-          const float o = fmaf(n, weight[i][j], bias[i][j]), g = s[i][j];
-          dz[i][j] = d[i][j] * o * (g * fmaf(z[i][j], 1.0f - g, 1.0f));
-          d[i][j] *= z[i][j] * g;
+          const float z = in ? hz.p[i][j] : 0.0f, g = sigmoid_of(z), o = fmaf(n, weight[i][j], bias[i][j]);
+          dz[j] = e * o * (g * fmaf(z, 1.0f - g, 1.0f));
+          e *= z * g;
         }
-        d_w[i][j] = fmaf(d[i][j], n, d_w[i][j]);
-        d_b[i][j] += d[i][j];
-        d[i][j] *= weight[i][j];
-        dn += d[i][j];
-        dnn = fmaf(d[i][j], n, dnn);
+        d_w[i][j] = fmaf(e, n, d_w[i][j]);
+        d_b[i][j] += e;
+        e *= weight[i][j];
+        dn += e;
+        dnn = fmaf(e, n, dnn);
+        d[i][j] = e;
       }
+      if constexpr (FORM == MAMBA2_NORM_GATED) {
+        if (put_gate) store_piece<T, V>(d_gate, w, a, i, dz);
+      }
+    }
     dnn = sum(dnn) * a.inv_width;
     dn = a.centered ? sum(dn) * a.inv_width : 0.0f;
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int i = 0; i < R; ++i) {
+      float dz[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         float dh = r * (fmaf(-h[i][j], dnn, d[i][j]) - dn);
         if constexpr (FORM == MAMBA2_NORM_GATE_FIRST) {
-          const float g = s[i][j];
-          dz[i][j] = dh * x[i][j] * (g * fmaf(z[i][j], 1.0f - g, 1.0f));
-          dh *= z[i][j] * g;
+          const float z = hz.p[i][j], g = sigmoid_of(z);
+          dz[j] = dh * hx.p[i][j] * (g * fmaf(z, 1.0f - g, 1.0f));
+          dh *= z * g;
         }
         d[i][j] = dh;
       }
-    if (a.d_x.data != nullptr) store_row<T, V, R>(row_ptr<T>(a.d_x, a, row), w, a, d);
-    if constexpr (kGate) {
-      if (a.d_gate.data != nullptr) store_row<T, V, R>(row_ptr<T>(a.d_gate, a, row), w, a, dz);
+      if (put_x) store_piece<T, V>(d_x, w, a, i, d[i]);
+      if constexpr (FORM == MAMBA2_NORM_GATE_FIRST) {
+        if (put_gate) store_piece<T, V>(d_gate, w, a, i, dz);
+      }
     }
   }
   if (a.partial == nullptr) return;
