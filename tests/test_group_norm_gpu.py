@@ -175,3 +175,38 @@ def test_rows_far_apart():
     g = m2.group_norm_bwd(s["x"], s["d_y"], d["weight"], d["bias"], gate=s["gate"], out=dict(d_x=at(4)), **kw)
     for n in ("d_x", "d_gate", "d_weight", "d_bias"):
         assert torch.equal(g[n], want[n]), n
+
+
+@pytest.mark.parametrize("form", ["plain", "gated", "gate_first"])
+@pytest.mark.parametrize("groups,width,typ", [(8, 128, "bf16"), (1, 4096, "bf16"), (1, 12288, "bf16"), (3, 97, "f32"),
+                                              (1, 8192, "f32"), (1, 5001, "bf16")])
+def test_many_rows(groups, width, typ, form):
+    """A thread's rows one after another: bitwise the same rows in calls of few, and sums over all of them."""
+    rows, few = 9000, 700
+    g = torch.Generator(DEV).manual_seed(rows + width)
+    dtype = torch.bfloat16 if typ == "bf16" else torch.float32
+    x, d_y, z = (torch.randn(rows, groups * width, generator=g, device=DEV).to(dtype) for _ in range(3))
+    w = 1 + 0.5 * torch.rand(groups * width, generator=g, device=DEV)
+    kw = gn.keywords(groups, form, False)
+    gate = {} if form == "plain" else dict(gate=z)
+    y = m2.group_norm_fwd(x, w, **gate, **kw)
+    got = m2.group_norm_bwd(x, d_y, w, **gate, **kw)
+    for at in (0, 4111, rows - few):
+        s = slice(at, at + few)
+        part = {k: v[s] for k, v in gate.items()}
+        assert torch.equal(m2.group_norm_fwd(x[s], w, **part, **kw), y[s])
+        want = m2.group_norm_bwd(x[s], d_y[s], w, **part, **kw)
+        assert torch.equal(want["d_x"], got["d_x"][s])
+        if gate:
+            assert torch.equal(want["d_gate"], got["d_gate"][s])
+    # d_weight's terms, in 64 bits; up to 16 roundings in a term, and under 112 additions one behind the other
+    h, e = x.double(), d_y.double()
+    silu = z.double() * torch.sigmoid(z.double())
+    if form == "gated":
+        e *= silu
+    elif form == "gate_first":
+        h *= silu
+    r = (h.unflatten(-1, (groups, width)).square().mean(-1, keepdim=True) + kw["eps"]).rsqrt()
+    terms = e * (h.unflatten(-1, (groups, width)) * r).flatten(-2)
+    error = (got["d_weight"].double() - terms.sum(0)).abs()
+    assert bool((error <= 128 * 2.0 ** -24 * terms.abs().sum(0)).all())
