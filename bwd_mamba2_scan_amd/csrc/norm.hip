@@ -46,13 +46,15 @@ struct NormArgs {
   float eps, inv_width;
 };
 
-// 1 / (1 + e^-v), to fp32's last bits; the exponent's product in two terms.
+// 1 / (1 + e^-v), to fp32's last bits; the exponent's product in two terms.  The
+// second one's share is added where 2^p is finite: from 2^128 on it is infinite, and
+// infinity times a negative rest would make a NaN of a sigmoid that is 0.
 __device__ __forceinline__ float sigmoid_of(float v) {
   constexpr float kLog2e = 1.4426950408889634f;
   const float p = -v * kLog2e;
   const float rest = fmaf(-v, 1.925963033500e-8f, fmaf(-v, kLog2e, -p));
   float t = __builtin_amdgcn_exp2f(p);
-  t = fabsf(p) < 150.0f ? fmaf(t, 0.69314718056f * rest, t) : t;  // beyond, t is 0 or infinite
+  t = fabsf(p) < 128.0f ? fmaf(t, 0.69314718056f * rest, t) : t;
   return __builtin_amdgcn_rcpf(1.0f + t);
 }
 
