@@ -644,7 +644,8 @@ int mamba2_norm_bwd(mamba2_seqs seqs, mamba2_norm_dims d, mamba2_rows x, const f
     return st;
   if ((bias != nullptr && weight == nullptr) || (d_weight != nullptr && weight == nullptr) ||
       (d_bias != nullptr && bias == nullptr) ||
-      (d_x.data == nullptr && d_weight == nullptr && d_bias == nullptr && (!gated(d) || d_gate.data == nullptr)))
+      (seqs.length > 0 && d_x.data == nullptr && d_weight == nullptr && d_bias == nullptr &&
+       (!gated(d) || d_gate.data == nullptr)))  // a tensor of no rows may have no address
     return MAMBA2_SCAN_ENULL;
   if (!gated(d) && d_gate.data != nullptr) return MAMBA2_SCAN_EUNSUPPORTED;
   if (!aligned_to(weight, 4) || !aligned_to(bias, 4) || !aligned_to(d_weight, 4) || !aligned_to(d_bias, 4))
@@ -655,6 +656,7 @@ int mamba2_norm_bwd(mamba2_seqs seqs, mamba2_norm_dims d, mamba2_rows x, const f
     if (workspace_bytes < mamba2_norm_bwd_workspace_bytes(seqs, d)) return MAMBA2_SCAN_ESIZE;
     if (!aligned_to(workspace, 16)) return MAMBA2_SCAN_EALIGN;
   }
+  if (seqs.length == 0 && !sums) return MAMBA2_SCAN_OK;
   const Shape s = shape_of(seqs, d, t.vec, true);
   hipStream_t hs = static_cast<hipStream_t>(stream);
   NormArgs a = args_of(seqs, d, s, t.flat);

@@ -134,8 +134,8 @@ size_t mamba2_norm_bwd_workspace_bytes(mamba2_seqs seqs, mamba2_norm_dims dims);
 /*
  * Gradients for given dL/dy: d_x, d_gate (their data may be NULL; d_gate only
  * with a gate), d_weight, d_bias (NULL, or given with the parameter), not all
- * NULL.  The statistics are recomputed from x.  workspace: 16-byte aligned,
- * needed when d_weight or d_bias is.
+ * NULL unless there are no rows.  The statistics are recomputed from x.
+ * workspace: 16-byte aligned, needed when d_weight or d_bias is.
  */
 int mamba2_norm_bwd(mamba2_seqs seqs, mamba2_norm_dims dims, mamba2_rows x,
                     const float* weight, const float* bias, mamba2_rows gate,
