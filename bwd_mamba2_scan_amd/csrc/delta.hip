@@ -22,7 +22,7 @@ using namespace delta;
 // 0.2 GB written (2.4 TB/s), the matrix pipes busy for 15% of it.  With three work-groups
 // on a CU 89 us; with every head's products of q and k formed anew 97.
 template <class T, int NB>
-__global__ __launch_bounds__(kPrepWaves * 64, NB < 4 || sizeof(T) == 2 ? 4 : 2) void delta_prep_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(kPrepWaves * 64, prep_per_cu(sizeof(T), NB * 32)) void delta_prep_kernel(DeltaArgs a) {
   __shared__ PrepLds<T, NB> s;
   const int wave = wave_id(), lane = threadIdx.x & 63;
   const PrepWork w = prep_work(a);
@@ -378,9 +378,10 @@ void set_dims(DeltaArgs* a, const mamba2_seqs& q, const mamba2_delta_dims& d, bo
   a->states = d.states;
   a->slices = (d.width + kWaves * 16 - 1) / (kWaves * 16);
   a->gate_bf16 = d.gate_type == MAMBA2_BF16;
-  // the matrices: heads that share a q and k one after the other, once the chip (three
-  // work-groups on a CU) is full
-  const long full = steps_of(q) * d.heads / (3 * kCUs);
+  // the matrices: heads that share a q and k one after the other, once the chip is full.
+  // Counted for 4, 3 and 2 work-groups on a CU, us: 2 x 4096 tokens, 32 heads of 64
+  // states in 4 groups, bf16, 29, 33, 36; fp32 with 128 states 56, 61, 45.
+  const long full = steps_of(q) * d.heads / (prep_per_cu(type_size(d.type), d.states) * kCUs);
   a->prep_heads = full < 1 ? 1 : full < a->ratio ? static_cast<int>(full) : a->ratio;
   a->seg = segment_tokens(q, d, bwd);
   a->units = static_cast<int>(unit_count(q, a->seg));

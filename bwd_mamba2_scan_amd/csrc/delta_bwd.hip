@@ -29,7 +29,7 @@ using namespace delta;
 // Times here: 4 x 4096 tokens, 16 groups of two heads of 128 x 128, bf16.  98 us, as
 // delta_prep_kernel, with 0.3 GB written.
 template <class T, int NB>
-__global__ __launch_bounds__(kPrepWaves * 64, NB < 4 || sizeof(T) == 2 ? 4 : 2) void delta_bwd_prep_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(kPrepWaves * 64, prep_per_cu(sizeof(T), NB * 32)) void delta_bwd_prep_kernel(DeltaArgs a) {
   __shared__ PrepLds<T, NB> s;
   const int wave = wave_id(), lane = threadIdx.x & 63;
   const PrepWork w = prep_work(a);
