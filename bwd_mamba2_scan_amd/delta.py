@@ -74,8 +74,9 @@ def delta_fwd(q, k, v, g, beta, *, scale=None, initial_state=None, offsets=None,
     q, k [batch, length, groups, states], v [batch, length, heads, width],
     g, beta [batch, length, heads] (with offsets: no batch axis), float32 or
     bfloat16 (q, k, v alike, g and beta alike); heads / groups neighbouring
-    heads share a q and k.  g holds log decays (<= 0); scale defaults to
-    states ** -0.5.  initial_state [batch, heads, states, width] float32
+    heads share a q and k.  g holds log decays (<= 0), and beta |k|^2 <= 2 is
+    meant: keys of length one, say (group_norm_fwd makes them); scale defaults
+    to states ** -0.5.  initial_state [batch, heads, states, width] float32
     (default: zeros).  Returns (y, the final state, or None unless
     want_final_state or final_state is given).
     """
@@ -225,6 +226,8 @@ def group_norm_fwd(x, weight=None, bias=None, *, groups=1, gate=None, gate_first
     x and the result o, silu(o) with silu, o silu(gate) with a gate; with
     gate_first h is x silu(gate) instead.  gate has x's type and shape; weight
     and bias are float32, [channels], or [channels / groups] for every group.
+    A weight of (channels / groups) ** -0.5 makes a group's length one: x /
+    sqrt(sum x^2 + eps channels / groups), as queries and keys have.
     Rows outside the sequences that offsets names are neither read nor written.
     """
     dev, d, seqs, lead, channels, _, w, b, z = _norm(x, weight, bias, groups, gate, gate_first, silu, centered, eps,

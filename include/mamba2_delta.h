@@ -27,9 +27,10 @@ extern "C" {
  * A token whose g and beta are 0 leaves the state as it was; so a padded batch
  * marks its padding, q, k and v there being finite.  g = -inf forgets the state
  * before the token.
- *   g <= 0 is meant, and beta |k|^2 <= 2, beyond which the recurrence itself
- *   grows; growing states are computed as long as e^(sum of g) over 64 tokens,
- *   and what the rule makes of the keys within them, stay finite.
+ *   g <= 0 is meant, and beta |k|^2 <= 2 (keys of length one, say: the group norm
+ *   with a weight of width^-1/2), beyond which the recurrence itself grows; growing
+ *   states are computed as long as e^(sum of g) over 64 tokens, and what the rule
+ *   makes of the keys within them, stay finite.
  *   1 <= groups, heads a multiple of groups, at most 65535, as batch is;
  *   width and states multiples of 8, 8 .. 128.  q, k, v, y and the states are
  *   16-byte aligned, with row and batch strides that are multiples of 8
