@@ -151,7 +151,9 @@ struct Piece<T, 1> {
 };
 // A thread's pieces of a row.  AHEAD: one that its group does not have is the group's
 // first one, so that all are loaded, none behind a branch, which would make a wait for
-// these loads a wait for what is issued after them, too.  Else it is 0.
+// these loads a wait for what is issued after them, too.  Else it is 0, and the offsets
+// are formed where they are used: formed before the branch, all are kept over the rows
+// (2048 rows of 16384 elements, fp32, backward: 213 us, 138 so).
 template <class T, int V, int R, bool AHEAD>
 struct Pieces {
   Piece<T, V> p[R];
@@ -160,9 +162,8 @@ struct Pieces {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const bool in = w.in_group + i * a.lanes * V < a.width;
-      const int at = w.channel + i * a.lanes * V;
-      if (AHEAD) p[i].load(base + (in ? at : w.channel - w.in_group));
-      else if (in) p[i].load(base + at);
+      if (AHEAD) p[i].load(base + (in ? w.channel + i * a.lanes * V : w.channel - w.in_group));
+      else if (in) p[i].load(base + w.channel + i * a.lanes * V);
       else p[i] = {};
     }
   }
