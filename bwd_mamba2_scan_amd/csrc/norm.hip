@@ -229,6 +229,11 @@ __device__ __forceinline__ long rows_of_block(const NormArgs& a, int chunk, int*
 // rows of 8192, gated: 87 us without, 96 with it; by elements, 16384 of 4096, 316 and 136).
 template <class T, int V, int R, bool WIDE, bool BWD>
 constexpr bool kAhead = !WIDE ? V > 1 : BWD ? R * V * static_cast<int>(sizeof(T)) <= 16 : V == 1 && R < 16;
+// The gate's gradients are stored at once, before the group's sums, which frees their
+// registers.  Groups taken by elements in a wave have those and lose by it (65536 rows
+// of 8 groups of 97, bf16: 490 us, 424 behind the sums).
+template <int V, bool WIDE>
+constexpr bool kGateAtOnce = WIDE || V > 1;
 // The backward of a block of 1024 threads reads its parameters again for each row where
 // it has two vectors of bf16 or four of fp32 (4096 rows of 12288, bf16, gated: 418 us
 // with them held, which spills, 276).
@@ -333,10 +338,10 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void norm_bwd_kernel(NormArgs a)
     T* const d_gate = kGate ? row_ptr<T>(a.d_gate, a, row) : nullptr;
     const bool put_x = a.d_x.data != nullptr, put_gate = a.d_gate.data != nullptr;
     float dn = 0.0f, dnn = 0.0f;
+    float dz[R][V];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const bool in = !kNext || w.in_group + i * a.lanes * V < a.width;  // else 0 was loaded
-      float dz[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float n = h[i][j];
@@ -347,7 +352,7 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void norm_bwd_kernel(NormArgs a)
         }
         if constexpr (FORM == MAMBA2_NORM_GATED) {
           const float z = in ? hz.p[i][j] : 0.0f, g = sigmoid_of(z), o = fmaf(n, weight[i][j], bias[i][j]);
-          dz[j] = e * o * (g * fmaf(z, 1.0f - g, 1.0f));
+          dz[i][j] = e * o * (g * fmaf(z, 1.0f - g, 1.0f));
           e *= z * g;
         }
         d_w[i][j] = fmaf(e, n, d_w[i][j]);
@@ -357,28 +362,27 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void norm_bwd_kernel(NormArgs a)
         dnn = fmaf(e, n, dnn);
         d[i][j] = e;
       }
-      if constexpr (FORM == MAMBA2_NORM_GATED) {
-        if (put_gate) store_piece<T, V>(d_gate, w, a, i, dz);
+      if constexpr (FORM == MAMBA2_NORM_GATED && kGateAtOnce<V, WIDE>) {
+        if (put_gate) store_piece<T, V>(d_gate, w, a, i, dz[i]);
       }
     }
     dnn = sum(dnn) * a.inv_width;
     dn = a.centered ? sum(dn) * a.inv_width : 0.0f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      float dz[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         float dh = r * (fmaf(-h[i][j], dnn, d[i][j]) - dn);
         if constexpr (FORM == MAMBA2_NORM_GATE_FIRST) {
           const float z = hz.p[i][j], g = sigmoid_of(z);
-          dz[j] = dh * hx.p[i][j] * (g * fmaf(z, 1.0f - g, 1.0f));
+          dz[i][j] = dh * hx.p[i][j] * (g * fmaf(z, 1.0f - g, 1.0f));
           dh *= z * g;
         }
         d[i][j] = dh;
       }
       if (put_x) store_piece<T, V>(d_x, w, a, i, d[i]);
-      if constexpr (FORM == MAMBA2_NORM_GATE_FIRST) {
-        if (put_gate) store_piece<T, V>(d_gate, w, a, i, dz);
+      if constexpr (FORM == MAMBA2_NORM_GATE_FIRST || (FORM == MAMBA2_NORM_GATED && !kGateAtOnce<V, WIDE>)) {
+        if (put_gate) store_piece<T, V>(d_gate, w, a, i, dz[i]);
       }
     }
   }
