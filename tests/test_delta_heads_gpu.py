@@ -41,3 +41,26 @@ def test_packed(typ):
     got = _run(dr.to(p, DEV), offsets=torch.tensor(ends, dtype=torch.int32, device=DEV))
     for i in (0, 1, 3, 17, 39):
         _check(p, K ** -0.5, got, i, lengths[i], span=(ends[i], ends[i + 1]))
+
+
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [40, 72])
+def test_values_that_are_not_finite(K, typ):
+    """A head's reach no other head that its work-group takes."""
+    B, L, H, G, V = 40, 200, 20, 2, 16
+    d = dr.to(dr.inputs(K, (B, L), B, H, V, G, K, typ, "f32"), DEV)
+    want = _run(d)
+    for name, at in (("v", (1, 70, 3, 5)), ("beta", (1, 70, 3)), ("g", (1, 70, 3)), ("state", (1, 3, 2, 2)), ("d_y", (1, 70, 3, 5))):
+        bad = dict(d)
+        bad[name] = d[name].clone()
+        bad[name][at] = float("nan")
+        got = _run(bad)
+        for n in ("y", "final", "d_v", "d_g", "d_beta", "d_state"):
+            x, y = got[n], want[n]
+            axis = 1 if n in ("final", "d_state") else 2
+            others = [h for h in range(H) if h != 3]
+            keep = torch.tensor(others, device=DEV)
+            assert torch.equal(x.index_select(axis, keep), y.index_select(axis, keep)), (name, n)
+            assert torch.equal(x[0], y[0]) and torch.equal(x[2:], y[2:]), (name, n)
+        for n in ("d_q", "d_k"):
+            assert torch.equal(got[n][:, :, 1], want[n][:, :, 1]) and torch.equal(got[n][0], want[n][0]), (name, n)
