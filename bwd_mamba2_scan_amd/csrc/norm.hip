@@ -221,22 +221,24 @@ __device__ __forceinline__ long rows_of_block(const NormArgs& a, int chunk, int*
   return row0;
 }
 
-// The next row is loaded while one is worked on, where a thread has the registers and
-// whole vectors: 16384 rows of 4096 channels, bf16, gated, backward 171 us without, 154
-// with it; 65536 rows of 1024, 204 and 145; 16384 tokens of 32 groups of 128, 137 and 128.
-// Groups of 97, element by element, lose by it (the last row is loaded twice).
-// Nor do wide blocks' forwards of whole vectors gain, of which more are on a CU (8192
-// rows of 8192, gated: 87 us without, 96 with it; by elements, 16384 of 4096, 316 and 136).
+// The next row is loaded while one is worked on, where a thread has the registers.
+// Backward, gated, bf16: 16384 rows of 4096 channels 164 us without, 155 with it; 65536
+// of 1024, 152 and 146; 65536 of 8 groups of 97, element by element, 425 and 205 (3063 of
+// them 24 and 23, plain 19 and 21: the last row is loaded twice).  fp32 elements are left
+// out: 3063 rows of 8 groups of 97, plain, 19 and 21; 32768 of them 94 and 81.  Nor do
+// wide blocks' forwards of whole vectors gain, of which more are on a CU (8192 rows of
+// 8192, gated: 84 us without, 97 with it; by elements, 16384 of 4096, 315 and 136).
 template <class T, int V, int R, bool WIDE, bool BWD>
-constexpr bool kAhead = !WIDE ? V > 1 : BWD ? R * V * static_cast<int>(sizeof(T)) <= 16 : V == 1 && R < 16;
+constexpr bool kAhead = !WIDE ? V > 1 || sizeof(T) == 2 : BWD ? R * V * static_cast<int>(sizeof(T)) <= 16 : V == 1 && R < 16;
 // The gate's gradients are stored at once, before the group's sums, which frees their
 // registers.  Groups taken by elements in a wave have those and lose by it (65536 rows
-// of 8 groups of 97, bf16: 490 us, 424 behind the sums).
+// of 8 groups of 97, bf16: 220 us, 205 behind the sums).
 template <int V, bool WIDE>
 constexpr bool kGateAtOnce = WIDE || V > 1;
 // The backward of a block of 1024 threads reads its parameters again for each row where
-// it has two vectors of bf16 or four of fp32 (4096 rows of 12288, bf16, gated: 418 us
-// with them held, which spills, 276).
+// it has two vectors of bf16 or four of fp32: held, it spills.  4096 rows of 12288, bf16,
+// held and not: gate first 372 and 322 us, 512 rows 93 and 81; fp32, SiLU 196 and 187;
+// the other side is the gate behind, 242 and 268.
 template <int V, int R, bool WIDE>
 constexpr bool kHold = !WIDE || V == 1 || R * V <= 8;
 

@@ -9,6 +9,7 @@ import torch
 import bwd_mamba2_scan_amd as m2
 from oracle import delta_oracle as orc
 from tests import group_norm as gn
+from tests import test_group_norm_gpu as base
 from tests.rounded import within
 
 pytestmark = pytest.mark.gpu
@@ -67,3 +68,10 @@ def test_arguments_of_silu(typ, groups, width):
     p["weight"] = 0.01 * p["weight"]
     p["bias"] = torch.cat([v, torch.zeros(max(0, groups * width - len(v)))])[:groups * width].contiguous()
     _check(p, groups, "silu", (typ, groups, width))
+
+
+@pytest.mark.parametrize("form", ["plain", "gated", "gate_first"])
+@pytest.mark.parametrize("groups,width,typ", [(8, 97, "bf16"), (5, 3, "bf16"), (64, 1, "bf16"), (7, 120, "f32"), (1, 127, "bf16")])
+def test_many_rows_by_elements(groups, width, typ, form):
+    """Groups of a wave that fill no vector, a thread's rows one after another."""
+    base.test_many_rows(groups, width, typ, form)
