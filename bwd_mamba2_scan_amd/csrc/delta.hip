@@ -303,11 +303,11 @@ int check_gates(mamba2_rows* r, const mamba2_seqs& q, const mamba2_delta_dims& d
 // step each); two steps pass before a walk's first.  The fewest such steps are
 // taken, rounds of work-groups counted whole.  Forward, us a call, bf16, one sequence:
 //                                       whole   cut by the rule   best of the cuts tried
-//   32768 tokens, 24 heads of 64 x 64   1558    467 (10)          467 (10)
-//   8192 tokens, 8 heads of 128 x 128    466    139 (16)          139 (16)
-//   4096 tokens, 32 heads of 128 x 128   249    180 (4)           180 (4)
-//   1024 tokens, 8 heads of 128 x 128     71     56 (8)            56 (4 to 12)
-// and forward and backward, 4096 tokens, 8 heads of 128 x 128: 732, 343 (16), 324 (8).
+//   32768 tokens, 24 heads of 64 x 64   1557    434 (10)          434 (10)
+//   8192 tokens, 8 heads of 128 x 128    463    132 (16)          132 (16)
+//   4096 tokens, 32 heads of 128 x 128   247    174 (4)           174 (4)
+//   1024 tokens, 8 heads of 128 x 128     68     52 (8)            52 (4 to 12)
+// and forward and backward, 4096 tokens, 8 heads of 128 x 128: 742, 328 (16), 308 (8).
 int segment_tokens(const mamba2_seqs& q, const mamba2_delta_dims& d, bool bwd) {
   const bool packed = q.offsets != nullptr;
   // how a packed call's rows are shared out is not known here
