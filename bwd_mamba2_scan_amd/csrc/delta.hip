@@ -18,9 +18,9 @@ using namespace delta;
 
 // A work-group's time is mostly its chain: 16 rows of substitution, one behind the
 // other, and the barriers between the inverse's halves; four work-groups on a CU hide
-// one another's.  4 x 4096 tokens, 16 groups of two heads, 128 states, bf16: 84 us,
-// 0.2 GB written (2.4 TB/s), the matrix pipes busy for 15% of it.  With three work-groups
-// on a CU 89 us; with every head's products of q and k formed anew 97.
+// one another's.  4 x 4096 tokens, 16 groups of two heads, 128 states, bf16: 79 us,
+// 0.2 GB written (2.6 TB/s), the matrix pipes busy for 15% of it.  With every head's
+// products of q and k formed anew 91 us.
 template <class T, int NB>
 __global__ __launch_bounds__(kPrepWaves * 64, prep_per_cu(sizeof(T), NB * 32)) void delta_prep_kernel(DeltaArgs a) {
   __shared__ PrepLds<T, NB> s;
@@ -34,7 +34,7 @@ __global__ __launch_bounds__(kPrepWaves * 64, prep_per_cu(sizeof(T), NB * 32)) v
 }
 
 // A chain of steps: 4 x 4096 tokens, 32 heads of 128 x 128, bf16, a work-group on every
-// CU: 275 us, 4.3 a step, LDS busy for 48% of it, the vector pipes for 38%, the matrix
+// CU: 278 us, 4.3 a step, LDS busy for 48% of it, the vector pipes for 38%, the matrix
 // pipes for 33%.  fp32 (simple walks, 3 x 333 tokens, 10 heads of 24 x 40):
 // 28 us, 4.7 a step.
 template <class T, int NB>
@@ -49,7 +49,7 @@ __global__ __launch_bounds__(walk_threads<T>) void delta_fwd_kernel(DeltaArgs a)
 }
 
 // What segments make of the states before them: a step costs 0.7 of delta_fwd_kernel's.
-// One sequence of 32768 tokens, 24 heads of 64 x 64, ten segments: 190 us, beside 180
+// One sequence of 32768 tokens, 24 heads of 64 x 64, ten segments: 192 us, beside 182
 // of the walk itself and 12 of the carry.
 template <class T, int NB>
 __global__ __launch_bounds__(walk_threads<T>) void delta_summary_kernel(DeltaArgs a) {

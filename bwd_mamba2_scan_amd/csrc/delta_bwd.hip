@@ -26,7 +26,7 @@ namespace {
 
 using namespace delta;
 
-// Times here: 4 x 4096 tokens, 16 groups of two heads of 128 x 128, bf16.  98 us, as
+// Times here: 4 x 4096 tokens, 16 groups of two heads of 128 x 128, bf16.  96 us, as
 // delta_prep_kernel, with 0.3 GB written.
 template <class T, int NB>
 __global__ __launch_bounds__(kPrepWaves * 64, prep_per_cu(sizeof(T), NB * 32)) void delta_bwd_prep_kernel(DeltaArgs a) {
@@ -41,7 +41,7 @@ __global__ __launch_bounds__(kPrepWaves * 64, prep_per_cu(sizeof(T), NB * 32)) v
   });
 }
 
-// 237 us, 3.7 a step; 0.8 GB written (3.4 TB/s).
+// 234 us, 3.7 a step; 0.8 GB written (3.4 TB/s).
 template <class T, int NB>
 __global__ __launch_bounds__(walk_threads<T>) void delta_keep_kernel(DeltaArgs a) {
   if constexpr (sizeof(T) == 2) {
@@ -73,7 +73,7 @@ constexpr int kPart = sizeof(T) == 2 ? 128 : 64;  // columns of a head that LDS 
 
 // Eight waves share a step's 2 NB tiles of 16 states by four tiles of 16 tokens:
 // one by NB of them a wave, so that each state is loaded and split once.
-// 680 us, 2.0 GB read; with two by two tiles a wave 750, and 690 with what is kept in
+// 674 us, 2.0 GB read; with two by two tiles a wave 750, and 690 with what is kept in
 // rows.  LDS holds one work-group on a CU, whose phases take turns: of its cycles the
 // vector pipes are busy for 36%, the matrix pipes for 24%, LDS for 36%, and HBM could
 // have moved the bytes in 420 us.  Sixteen waves, and work-groups that stay for several
