@@ -7,8 +7,8 @@
 namespace delta {
 
 constexpr int kPrepWaves = 4;
-// Work-groups of the matrices' kernels that a CU holds: by their registers, and for
-// fp32 with over 64 states by their LDS.
+// Work-groups of the matrices' kernels that a CU's LDS holds: of 35 KB each, fp32 with
+// over 64 states 68.
 __host__ __device__ constexpr int prep_per_cu(size_t elem, int states) { return elem == 2 || states <= 64 ? 4 : 2; }
 constexpr int kSq = kTok + 4;  // row stride of a 64 x 64 fp32 matrix in LDS
 
